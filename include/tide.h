@@ -478,6 +478,125 @@ TIDE_API tide_status_t tide_layout_set_test_stall(tide_layout_t layout, int64_t 
 TIDE_API tide_status_t tide_layout_check_tiles(tide_layout_t layout, tide_op_t op, const int64_t* rows,
                                                int64_t count, int64_t* first_bad);
 
+/*
+ * The feed-forward unit: what runs on an FSDP unit's parameters between
+ * their placement and the reduce-scatter of their gradients.  The weights
+ * are read where tide_ag_place puts them (bf16, [ffn, hidden], contiguous)
+ * and the weight gradients are written as the reduce-scatter reads them
+ * (bf16, same shape, contiguous).
+ *
+ * Conventions, besides those above:
+ *  - Matrices are row-major.  Arguments ld* are row strides in elements, at
+ *    least the row's width.  Rows whose stride and width are multiples of
+ *    8 elements (16 for 8-bit operands) start on 16 bytes and run the
+ *    tensor-core kernels; any other width or stride runs plain tiled
+ *    kernels, right but many times slower.
+ *  - Sums are fp32; a result is rounded to bf16 once, to nearest even.
+ *  - Every buffer is the caller's, 16-byte aligned (TIDE_ERR_MISALIGNED) and
+ *    in memory of the handle's device; outputs must not overlap inputs or
+ *    each other.  A pointer to a matrix without elements may be NULL.
+ *  - Sizes are 0 .. 2^31 - 1 each, and any matrix has at most 2^38 elements.
+ *  - A compute handle may be used from several host threads and streams; it
+ *    keeps nothing between calls but its device's properties and an error
+ *    word.  Its first call binds it to the current device and cannot be
+ *    captured into a CUDA graph; later calls can.
+ *  - Results do not depend on timing: no call sums in an order that changes.
+ */
+typedef struct tide_compute_s* tide_compute_t;
+
+/* Gate activation: x sigmoid(x), or the tanh form of GELU. */
+typedef enum { TIDE_ACT_SILU = 0, TIDE_ACT_GELU = 1 } tide_activation_t;
+
+/* Create a handle (host-only; no CUDA call is made) / free it (work that
+ * uses it must have completed; NULL does nothing). */
+TIDE_API tide_status_t tide_compute_create(tide_compute_t* out);
+TIDE_API void tide_compute_destroy(tide_compute_t compute);
+
+/*
+ * 8-bit blocks: a matrix [rows, cols] held as e4m3 codes (one byte each,
+ * contiguous) and one fp32 scale for each block of block_rows x 128
+ * (block_rows = 1: activations; 128: weights), [ceil(rows / block_rows),
+ * ceil(cols / 128)].  The scale is the smallest power of two, at least
+ * 2^-126, that brings the block's largest finite magnitude to 448 or below
+ * (1 for a block of zeros), so the codes' rounding (to nearest even) is the
+ * only one and code * scale is exact in bf16 down to its smallest normal
+ * value.  Infinities and NaN become NaN codes and do not enter the scale.
+ *
+ * tide_fp8_store: bf16 -> blocks.  tide_fp8_restore: blocks -> bf16; it takes
+ * any fp32 scales.
+ */
+TIDE_API tide_status_t tide_fp8_store(tide_compute_t compute, int64_t rows, int64_t cols, const uint16_t* src,
+                                      int64_t ld_src, uint8_t* codes, float* scales, int32_t block_rows,
+                                      cudaStream_t stream);
+TIDE_API tide_status_t tide_fp8_restore(tide_compute_t compute, int64_t rows, int64_t cols, const uint8_t* codes,
+                                        const float* scales, int32_t block_rows, uint16_t* dst, int64_t ld_dst,
+                                        cudaStream_t stream);
+
+/*
+ * Product of two matrices held in 8-bit blocks:
+ *   out[i, j] = bf16( sum_b a_scales[i, b] * b_scales[j / 128, b] *
+ *                     sum_{k in block b} a[i, k] * b[j, k] ).
+ *   a    [m, k] codes, a_scales [m, ceil(k / 128)]             (block_rows = 1)
+ *   b    [n, k] codes, b_scales [ceil(n / 128), ceil(k / 128)] (block_rows = 128)
+ *   out  [m, n] bf16, row stride ld_out
+ * Scales may be any fp32 values.
+ */
+TIDE_API tide_status_t tide_fp8_matmul(tide_compute_t compute, int64_t m, int64_t n, int64_t k, const uint8_t* a,
+                                       const float* a_scales, const uint8_t* b, const float* b_scales,
+                                       uint16_t* out, int64_t ld_out, cudaStream_t stream);
+
+/*
+ * A gated block's activations in 8-bit blocks (block_rows = 1), kept from
+ * the forward pass for the backward pass.  gate / up: the pre-activations
+ * x Wg^T and x Wu^T, [tokens, ffn]; x: the input, [tokens, hidden], or NULL
+ * (both pointers) to leave the input as it is.
+ */
+typedef struct {
+  uint8_t* gate_codes;
+  float* gate_scales;
+  uint8_t* up_codes;
+  float* up_scales;
+  uint8_t* x_codes;
+  float* x_scales;
+} tide_gated_checkpoint_t;
+
+/*
+ * Gated feed-forward projections:
+ *   h = act(x Wg^T) * (x Wu^T)
+ *   x [tokens, hidden], w_gate and w_up [ffn, hidden], h [tokens, ffn], bf16.
+ * With `checkpoint` (NULL: none) the call also writes the blocks it points to.
+ */
+TIDE_API tide_status_t tide_gated_forward(tide_compute_t compute, int64_t tokens, int64_t hidden, int64_t ffn,
+                                          tide_activation_t act, const uint16_t* x, int64_t ld_x,
+                                          const uint16_t* w_gate, const uint16_t* w_up, uint16_t* h, int64_t ld_h,
+                                          const tide_gated_checkpoint_t* checkpoint, cudaStream_t stream);
+
+/* Bytes of the workspace tide_gated_backward needs for these sizes: the
+ * gradients of the two pre-activations, [tokens, ffn] bf16 each, the restored
+ * input, and partial sums of split products. */
+TIDE_API tide_status_t tide_gated_workspace(int64_t tokens, int64_t hidden, int64_t ffn, int64_t* bytes);
+
+/*
+ * Backward pass of the gated block.  With g = x Wg^T, u = x Wu^T:
+ *   dG = dh * u * act'(g),  dU = dh * act(g)   (rounded to bf16 for the products below)
+ *   dx = dG Wg + dU Wu,  dw_gate = dG^T x,  dw_up = dU^T x.
+ * Without a checkpoint g and u are recomputed from x.  With one they are read
+ * from its codes; where its x_codes are set the restored input takes x's place
+ * and x may be NULL.
+ *   dx               [tokens, hidden], or NULL: not computed
+ *   dw_gate, dw_up   [ffn, hidden], or both NULL: not computed
+ *   h                NULL, or [tokens, ffn]: receives act(g) * u again, for
+ *                    the next projection's weight gradient
+ *   workspace        at least tide_gated_workspace bytes, 16-byte aligned
+ */
+TIDE_API tide_status_t tide_gated_backward(tide_compute_t compute, int64_t tokens, int64_t hidden, int64_t ffn,
+                                           tide_activation_t act, const uint16_t* dh, int64_t ld_dh,
+                                           const uint16_t* x, int64_t ld_x, const uint16_t* w_gate,
+                                           const uint16_t* w_up, const tide_gated_checkpoint_t* checkpoint,
+                                           uint16_t* dx, int64_t ld_dx, uint16_t* dw_gate, uint16_t* dw_up,
+                                           uint16_t* h, int64_t ld_h, void* workspace, int64_t workspace_bytes,
+                                           cudaStream_t stream);
+
 /* "release", or "debug: device range checks" for the library built with
  * TIDE_DEBUG=1 (libtide_debug.so). */
 TIDE_API const char* tide_build_info(void);

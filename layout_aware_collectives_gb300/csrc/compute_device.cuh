@@ -1,0 +1,99 @@
+// Device helpers shared by the feed-forward unit's kernels: bf16 and e4m3
+// conversions, the block scale, and the gate activations.
+#pragma once
+
+#include <math_constants.h>
+#include <stdint.h>
+
+#include "compute_internal.h"
+
+namespace tide {
+
+__device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+__device__ __forceinline__ float bf16_value(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+
+// Two floats to packed bf16, to nearest even: `lo` in the low half.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint16_t to_bf16(float v) { return (uint16_t)pack_bf16(v, 0.0f); }
+
+// The largest finite magnitude e4m3 holds is 448 = 1.75 * 2^8.  The block
+// scale is the smallest power of two >= 2^-126 that brings `amax`, the
+// block's largest finite magnitude, to 448 or below; 1 for a block of zeros.
+// Being a power of two it rounds nothing: a value's only rounding is e4m3's
+// own, and code * scale is exact in bf16 (4 significant bits; below 2^-126
+// it may round as any bf16 subnormal does).
+__device__ __forceinline__ uint32_t scale_exponent(float amax) {
+  const uint32_t b = __float_as_uint(amax);
+  if (b == 0) return 127;
+  const int e = (int)(b >> 23) - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return (uint32_t)(e < 1 ? 1 : e);
+}
+__device__ __forceinline__ float exponent_value(uint32_t e) { return __uint_as_float(e << 23); }
+// 1 / 2^(e - 127), exact: e is within [1, 247].
+__device__ __forceinline__ float exponent_inverse(uint32_t e) { return __uint_as_float((254u - e) << 23); }
+
+// |v| where v is finite, else 0.
+__device__ __forceinline__ float finite_abs(float v) {
+  const float a = fabsf(v);
+  return a < CUDART_INF_F ? a : 0.0f;  // false for infinities and NaN
+}
+
+// Two scaled values to e4m3, to nearest even, infinities and NaN to NaN.
+__device__ __forceinline__ uint16_t pack_e4m3(float lo, float hi) {
+  lo = fabsf(lo) < CUDART_INF_F ? lo : CUDART_NAN_F;
+  hi = fabsf(hi) < CUDART_INF_F ? hi : CUDART_NAN_F;
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float d) {
+  return (uint32_t)pack_e4m3(a, b) | ((uint32_t)pack_e4m3(c, d) << 16);
+}
+
+// Two e4m3 codes to float (exact: every e4m3 value is an f16 value).
+__device__ __forceinline__ float2 e4m3_values(uint16_t v) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(v));
+  float2 f;
+  asm("{ .reg .f16 l, h; mov.b32 {l, h}, %2; cvt.f32.f16 %0, l; cvt.f32.f16 %1, h; }"
+      : "=f"(f.x), "=f"(f.y)
+      : "r"(h));
+  return f;
+}
+
+// The tanh form of GELU is g * sigmoid(2 z), z = sqrt(2/pi) (g + 0.044715 g^3),
+// since 0.5 (1 + tanh z) = sigmoid(2 z).  Past |g| = 64 the sigmoid is 0 or 1
+// in 32 bits; the clamp keeps the cube and the square there finite.
+__device__ __forceinline__ float gelu_clamp(float g) { return fminf(fmaxf(g, -64.0f), 64.0f); }
+__device__ __forceinline__ float gelu_sigmoid(float c) {
+  const float z = 0.7978845608028654f * (c + 0.044715f * c * c * c);
+  return __fdividef(1.0f, 1.0f + __expf(-2.0f * z));
+}
+
+// Gate activations, in 32 bits.  expf's argument may overflow to infinity,
+// which gives the sigmoid's limit 0.
+template <int ACT>
+__device__ __forceinline__ float activation(float g) {
+  if (ACT == TIDE_ACT_SILU) return __fdividef(g, 1.0f + __expf(-g));
+  return g * gelu_sigmoid(gelu_clamp(g));
+}
+
+// act(g) and its derivative.
+template <int ACT>
+__device__ __forceinline__ float2 activation_grad(float g) {
+  if (ACT == TIDE_ACT_SILU) {
+    const float s = __fdividef(1.0f, 1.0f + __expf(-g));
+    return make_float2(g * s, s * (1.0f + g * (1.0f - s)));
+  }
+  const float c = gelu_clamp(g);
+  const float s = gelu_sigmoid(c);
+  const float dz = 0.7978845608028654f * (1.0f + 3.0f * 0.044715f * c * c);
+  return make_float2(g * s, s + 2.0f * g * s * (1.0f - s) * dz);
+}
+
+}  // namespace tide

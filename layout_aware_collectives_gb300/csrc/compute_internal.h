@@ -1,0 +1,85 @@
+// Internal interface between the feed-forward unit's C ABI (compute_api.cpp)
+// and its kernels (fp8_blocks.cu, gated_simple.cu).
+#pragma once
+
+#include <cuda_runtime_api.h>
+#include <stdint.h>
+
+#include <mutex>
+
+#include "tide.h"
+#include "tide_internal.h"
+
+namespace tide {
+
+constexpr int kBlock = 128;  // columns (and, for weights, rows) that share one scale
+
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// A bf16 matrix [rows, cols] beside its 8-bit blocks.  ld is the bf16
+// matrix's row stride in elements; codes are contiguous.
+struct Fp8Args {
+  int64_t rows, cols, ld;
+  uint16_t* bf16;  // read by the store, written by the restore
+  uint8_t* codes;
+  float* scales;  // [ceil(rows / block_rows), ceil(cols / 128)]
+  int block_rows;  // 1 or 128
+};
+
+// One call of the gated block, forward or backward.  Null pointers leave an
+// output out.
+struct GatedArgs {
+  int64_t tokens, hidden, ffn;
+  int act;
+  const uint16_t* x;
+  int64_t ldx;
+  const uint16_t* wg;
+  const uint16_t* wu;
+  uint16_t* h;
+  int64_t ldh;
+  uint8_t* g8;  // checkpoint of the two pre-activations
+  float* gs;
+  uint8_t* u8;
+  float* us;
+  // backward
+  const uint16_t* dh;
+  int64_t lddh;
+  uint16_t* dx;
+  int64_t lddx;
+  uint16_t* dwg;
+  uint16_t* dwu;
+  uint16_t* dg;  // [tokens, ffn] each, workspace
+  uint16_t* du;
+};
+
+struct MatmulArgs {
+  int64_t m, n, k;
+  const uint8_t* a;
+  const float* sa;
+  const uint8_t* b;
+  const float* sb;
+  uint16_t* out;
+  int64_t ldo;
+};
+
+// Bytes <-> blocks (fp8_blocks.cu).
+cudaError_t launch_fp8_store(const Fp8Args& a, cudaStream_t stream);
+cudaError_t launch_fp8_restore(const Fp8Args& a, cudaStream_t stream);
+
+// dG, dU (and h) from the checkpoint's codes (fp8_blocks.cu).
+cudaError_t launch_gated_grad_stored(const GatedArgs& a, cudaStream_t stream);
+
+// Plain tiled kernels for every size and stride (gated_simple.cu).
+cudaError_t launch_gated_forward_simple(const GatedArgs& a, cudaStream_t stream);
+cudaError_t launch_gated_grad_simple(const GatedArgs& a, cudaStream_t stream);
+cudaError_t launch_gated_dx_simple(const GatedArgs& a, cudaStream_t stream);
+cudaError_t launch_gated_dw_simple(const GatedArgs& a, cudaStream_t stream);
+cudaError_t launch_fp8_matmul_simple(const MatmulArgs& a, cudaStream_t stream);
+
+}  // namespace tide
+
+struct tide_compute_s {
+  int device = -1;  // bound by the first call
+  int num_sms = 0;
+  std::mutex mu;
+};

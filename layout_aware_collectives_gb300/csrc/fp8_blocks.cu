@@ -1,0 +1,319 @@
+// The 8-bit block format of activations and weights: store, restore, and the
+// gated block's gradients from stored pre-activations.
+//
+// Every kernel here is one pass over its data, bound by HBM.
+#include "compute_device.cuh"
+
+namespace tide {
+namespace {
+
+constexpr int kThreads = 256;
+
+// ------------------------------------------------------------------ store
+
+// One scale for each 1 x 128: half a warp takes a block, 8 columns (16
+// bytes) a lane, so the block's maximum is four shuffles and nothing is read
+// twice.  U blocks are loaded before the first is reduced.
+template <int U>
+__global__ void __launch_bounds__(kThreads) store_rows_kernel(Fp8Args a, int64_t blocks_per_row, int64_t blocks) {
+  const int lane = threadIdx.x & 15;
+  const int64_t group = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 4;
+  uint4 v[U];
+  int64_t row[U], col[U];
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    const int64_t blk = group + (int64_t)i * gridDim.x * (kThreads / 16);
+    row[i] = blk < blocks ? blk / blocks_per_row : -1;
+    col[i] = (blk - row[i] * blocks_per_row) * kBlock + lane * 8;
+    v[i] = make_uint4(0, 0, 0, 0);
+    if (row[i] >= 0 && col[i] < a.cols) v[i] = __ldcs((const uint4*)(a.bf16 + row[i] * a.ld + col[i]));
+  }
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+    float f[8], amax = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      f[2 * j] = bf16_lo(w[j]);
+      f[2 * j + 1] = bf16_hi(w[j]);
+      amax = fmaxf(amax, fmaxf(finite_abs(f[2 * j]), finite_abs(f[2 * j + 1])));
+    }
+#pragma unroll
+    for (int d = 8; d; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+    const uint32_t e = scale_exponent(amax);
+    const float inv = exponent_inverse(e);
+    if (row[i] < 0) continue;
+    if (col[i] < a.cols) {
+      const uint2 c = make_uint2(pack_e4m3x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv),
+                                 pack_e4m3x4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv));
+      *(uint2*)(a.codes + row[i] * a.cols + col[i]) = c;
+    }
+    if (lane == 0) a.scales[row[i] * blocks_per_row + col[i] / kBlock] = exponent_value(e);
+  }
+}
+
+// The same for rows whose stride or width is no multiple of 8: a warp takes
+// a block, 4 single columns a lane, 32 apart.
+template <int U>
+__global__ void __launch_bounds__(kThreads) store_rows_any_kernel(Fp8Args a, int64_t blocks_per_row, int64_t blocks) {
+  const int lane = threadIdx.x & 31;
+  const int64_t warp = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5;
+  uint16_t v[U][4];
+  int64_t row[U], col[U];
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    const int64_t blk = warp + (int64_t)i * gridDim.x * (kThreads / 32);
+    row[i] = blk < blocks ? blk / blocks_per_row : -1;
+    col[i] = (blk - row[i] * blocks_per_row) * kBlock + lane;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[i][j] = 0;
+      if (row[i] >= 0 && col[i] + 32 * j < a.cols) v[i][j] = a.bf16[row[i] * a.ld + col[i] + 32 * j];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    float amax = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) amax = fmaxf(amax, finite_abs(bf16_value(v[i][j])));
+#pragma unroll
+    for (int d = 16; d; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+    const uint32_t e = scale_exponent(amax);
+    const float inv = exponent_inverse(e);
+    if (row[i] < 0) continue;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (col[i] + 32 * j < a.cols)
+        a.codes[row[i] * a.cols + col[i] + 32 * j] = (uint8_t)pack_e4m3(bf16_value(v[i][j]) * inv, 0.0f);
+    if (lane == 0) a.scales[row[i] * blocks_per_row + col[i] / kBlock] = exponent_value(e);
+  }
+}
+
+// One scale for each 128 x 128: a CTA holds the whole block in registers
+// (VEC: 8 16-byte vectors a thread; else 64 single columns), so it is read
+// once.
+template <bool VEC>
+__global__ void __launch_bounds__(kThreads) store_square_kernel(Fp8Args a, int64_t blocks_per_row) {
+  constexpr int kPerLoad = VEC ? 8 : 1;
+  constexpr int kLanes = kBlock / kPerLoad;        // threads across a row
+  constexpr int kRows = kThreads / kLanes;         // rows a pass
+  constexpr int kPasses = kBlock / kRows;
+  const int64_t br = blockIdx.x / blocks_per_row, bc = blockIdx.x - br * blocks_per_row;
+  const int64_t col = bc * kBlock + (threadIdx.x % kLanes) * kPerLoad;
+  const int64_t row0 = br * kBlock + threadIdx.x / kLanes;
+  uint32_t v[kPasses][VEC ? 4 : 1];
+  float amax = 0.0f;
+#pragma unroll
+  for (int p = 0; p < kPasses; ++p) {
+    const int64_t row = row0 + p * kRows;
+    const bool in = row < a.rows && col < a.cols;
+    if constexpr (VEC) {
+      uint4 q = make_uint4(0, 0, 0, 0);
+      if (in) q = __ldcs((const uint4*)(a.bf16 + row * a.ld + col));
+      v[p][0] = q.x, v[p][1] = q.y, v[p][2] = q.z, v[p][3] = q.w;
+    } else {
+      v[p][0] = in ? a.bf16[row * a.ld + col] : 0;
+    }
+  }
+#pragma unroll
+  for (int p = 0; p < kPasses; ++p)
+#pragma unroll
+    for (int j = 0; j < (VEC ? 4 : 1); ++j)
+      amax = fmaxf(amax, fmaxf(finite_abs(bf16_lo(v[p][j])), finite_abs(bf16_hi(v[p][j]))));
+#pragma unroll
+  for (int d = 16; d; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+  __shared__ float part[kThreads / 32];
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = amax;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) amax = fmaxf(amax, part[w]);
+  const uint32_t e = scale_exponent(amax);
+  const float inv = exponent_inverse(e);
+#pragma unroll
+  for (int p = 0; p < kPasses; ++p) {
+    const int64_t row = row0 + p * kRows;
+    if (row >= a.rows || col >= a.cols) continue;
+    if constexpr (VEC) {
+      uint32_t c[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        c[j] = pack_e4m3x4(bf16_lo(v[p][2 * j]) * inv, bf16_hi(v[p][2 * j]) * inv, bf16_lo(v[p][2 * j + 1]) * inv,
+                           bf16_hi(v[p][2 * j + 1]) * inv);
+      *(uint2*)(a.codes + row * a.cols + col) = make_uint2(c[0], c[1]);
+    } else {
+      a.codes[row * a.cols + col] = (uint8_t)pack_e4m3(bf16_lo(v[p][0]) * inv, 0.0f);
+    }
+  }
+  if (threadIdx.x == 0) a.scales[blockIdx.x] = exponent_value(e);
+}
+
+// ---------------------------------------------------------------- restore
+
+__device__ __forceinline__ float scale_at(const Fp8Args& a, int64_t blocks_per_row, int64_t row, int64_t col) {
+  return a.scales[(a.block_rows == 1 ? row : row / kBlock) * blocks_per_row + col / kBlock];
+}
+
+// Contiguous on both sides: the matrix is one run of elements, taken 8 at a
+// time (8 bytes of codes, 16 of bf16) whatever the width; a group of 8 that
+// passes a block's or a row's end looks its scales up one by one.
+template <int U>
+__global__ void __launch_bounds__(kThreads) restore_flat_kernel(Fp8Args a, int64_t blocks_per_row, int64_t numel) {
+  uint2 c[U];
+  int64_t at[U];
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    at[i] = (((int64_t)blockIdx.x * U + i) * kThreads + threadIdx.x) * 8;
+    c[i] = make_uint2(0, 0);
+    if (at[i] + 8 <= numel) c[i] = __ldcs((const uint2*)(a.codes + at[i]));
+  }
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    if (at[i] >= numel) continue;
+    int64_t row = at[i] / a.cols, col = at[i] - row * a.cols;
+    if (at[i] + 8 > numel) {
+      for (int64_t e = at[i]; e < numel; ++e) {
+        a.bf16[e] = to_bf16(e4m3_values(a.codes[e]).x * scale_at(a, blocks_per_row, row, col));
+        if (++col == a.cols) ++row, col = 0;
+      }
+      continue;
+    }
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t w = j < 2 ? c[i].x : c[i].y;
+      const float2 t = e4m3_values((uint16_t)(w >> (16 * (j & 1))));
+      f[2 * j] = t.x;
+      f[2 * j + 1] = t.y;
+    }
+    if (col + 8 <= a.cols && (col & (kBlock - 1)) <= kBlock - 8) {
+      const float s = scale_at(a, blocks_per_row, row, col);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] *= s;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        f[j] *= scale_at(a, blocks_per_row, row, col);
+        if (++col == a.cols) ++row, col = 0;
+      }
+    }
+    __stcs((uint4*)(a.bf16 + at[i]), make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
+                                               pack_bf16(f[6], f[7])));
+  }
+}
+
+// Strided destination rows: one element a thread and step.
+__global__ void __launch_bounds__(kThreads) restore_any_kernel(Fp8Args a, int64_t blocks_per_row, int64_t numel) {
+  for (int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x; e < numel; e += (int64_t)gridDim.x * kThreads) {
+    const int64_t row = e / a.cols, col = e - row * a.cols;
+    a.bf16[row * a.ld + col] = to_bf16(e4m3_values(a.codes[e]).x * scale_at(a, blocks_per_row, row, col));
+  }
+}
+
+// ------------------------------------------------- gradients from the codes
+
+// dU = dh act(g), dG = dh u act'(g) and, where asked, h = act(g) u, with g
+// and u read from their codes: 4 bytes in and 4 (6) out an element, so the
+// pre-activations are never spelled out in memory.  V = 8 columns a thread
+// where rows allow 16-byte accesses, else 1.
+template <int ACT, int V>
+__global__ void __launch_bounds__(kThreads) grad_stored_kernel(GatedArgs a, int64_t groups_per_row, int64_t groups) {
+  const int64_t nb = (a.ffn + kBlock - 1) / kBlock;
+  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (i >= groups) return;
+  const int64_t row = i / groups_per_row, col = (i - row * groups_per_row) * V;
+  const int64_t at = row * a.ffn + col, sat = row * nb + col / kBlock;
+  const float sg = a.gs[sat], su = a.us[sat];
+  float g[V], u[V], d[V], dg[V], du[V], h[V];
+  if constexpr (V == 8) {
+    const uint2 cg = __ldcs((const uint2*)(a.g8 + at)), cu = __ldcs((const uint2*)(a.u8 + at));
+    const uint4 cd = __ldcs((const uint4*)(a.dh + row * a.lddh + col));
+    const uint32_t w[4] = {cd.x, cd.y, cd.z, cd.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 tg = e4m3_values((uint16_t)((j < 2 ? cg.x : cg.y) >> (16 * (j & 1))));
+      const float2 tu = e4m3_values((uint16_t)((j < 2 ? cu.x : cu.y) >> (16 * (j & 1))));
+      g[2 * j] = tg.x, g[2 * j + 1] = tg.y;
+      u[2 * j] = tu.x, u[2 * j + 1] = tu.y;
+      d[2 * j] = bf16_lo(w[j]), d[2 * j + 1] = bf16_hi(w[j]);
+    }
+  } else {
+    g[0] = e4m3_values(a.g8[at]).x;
+    u[0] = e4m3_values(a.u8[at]).x;
+    d[0] = bf16_value(a.dh[row * a.lddh + col]);
+  }
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const float gv = g[j] * sg, uv = u[j] * su;
+    const float2 t = activation_grad<ACT>(gv);
+    du[j] = d[j] * t.x;
+    dg[j] = d[j] * uv * t.y;
+    h[j] = t.x * uv;
+  }
+  if constexpr (V == 8) {
+    *(uint4*)(a.dg + at) = make_uint4(pack_bf16(dg[0], dg[1]), pack_bf16(dg[2], dg[3]), pack_bf16(dg[4], dg[5]),
+                                      pack_bf16(dg[6], dg[7]));
+    *(uint4*)(a.du + at) = make_uint4(pack_bf16(du[0], du[1]), pack_bf16(du[2], du[3]), pack_bf16(du[4], du[5]),
+                                      pack_bf16(du[6], du[7]));
+    if (a.h)
+      *(uint4*)(a.h + row * a.ldh + col) = make_uint4(pack_bf16(h[0], h[1]), pack_bf16(h[2], h[3]),
+                                                      pack_bf16(h[4], h[5]), pack_bf16(h[6], h[7]));
+  } else {
+    a.dg[at] = to_bf16(dg[0]);
+    a.du[at] = to_bf16(du[0]);
+    if (a.h) a.h[row * a.ldh + col] = to_bf16(h[0]);
+  }
+}
+
+template <int ACT>
+cudaError_t grad_stored(const GatedArgs& a, cudaStream_t stream) {
+  const bool vec = a.ffn % 8 == 0 && a.lddh % 8 == 0 && (!a.h || a.ldh % 8 == 0);
+  const int64_t per_row = vec ? a.ffn / 8 : a.ffn, groups = per_row * a.tokens;
+  const unsigned grid = (unsigned)ceil_div(groups, kThreads);
+  if (vec)
+    grad_stored_kernel<ACT, 8><<<grid, kThreads, 0, stream>>>(a, per_row, groups);
+  else
+    grad_stored_kernel<ACT, 1><<<grid, kThreads, 0, stream>>>(a, per_row, groups);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_fp8_store(const Fp8Args& a, cudaStream_t stream) {
+  const int64_t per_row = ceil_div(a.cols, kBlock);
+  const bool vec = a.cols % 8 == 0 && a.ld % 8 == 0;
+  if (a.block_rows == 1) {
+    const int64_t blocks = per_row * a.rows;
+    const int64_t per_cta = (vec ? kThreads / 16 : kThreads / 32) * 4;
+    const unsigned grid = (unsigned)ceil_div(blocks, per_cta);
+    if (vec)
+      store_rows_kernel<4><<<grid, kThreads, 0, stream>>>(a, per_row, blocks);
+    else
+      store_rows_any_kernel<4><<<grid, kThreads, 0, stream>>>(a, per_row, blocks);
+  } else {
+    const unsigned grid = (unsigned)(per_row * ceil_div(a.rows, kBlock));
+    if (vec)
+      store_square_kernel<true><<<grid, kThreads, 0, stream>>>(a, per_row);
+    else
+      store_square_kernel<false><<<grid, kThreads, 0, stream>>>(a, per_row);
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_fp8_restore(const Fp8Args& a, cudaStream_t stream) {
+  const int64_t per_row = ceil_div(a.cols, kBlock), numel = a.rows * a.cols;
+  if (a.ld == a.cols) {
+    constexpr int kUnroll = 4;
+    restore_flat_kernel<kUnroll><<<(unsigned)ceil_div(numel, (int64_t)kThreads * 8 * kUnroll), kThreads, 0, stream>>>(
+        a, per_row, numel);
+  } else {
+    const int64_t grid = ceil_div(numel, kThreads);
+    restore_any_kernel<<<(unsigned)(grid < 65536 ? grid : 65536), kThreads, 0, stream>>>(a, per_row, numel);
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_gated_grad_stored(const GatedArgs& a, cudaStream_t stream) {
+  return a.act == TIDE_ACT_SILU ? grad_stored<TIDE_ACT_SILU>(a, stream) : grad_stored<TIDE_ACT_GELU>(a, stream);
+}
+
+}  // namespace tide

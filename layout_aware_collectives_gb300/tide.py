@@ -42,6 +42,9 @@ TIDE_OP_PACK = 2
 TIDE_OP_STAGE = 3
 TIDE_OP_STAGED_RS = 4
 
+TIDE_ACT_SILU = 0
+TIDE_ACT_GELU = 1
+
 TIDE_MAX_RANKS = 4096
 TIDE_IPC_HANDLE_BYTES = 64
 TIDE_NOALLOC_SCRATCH_BYTES = 4 << 20
@@ -93,6 +96,16 @@ _sig("tide_ipc_export", _st, _vp, _vp, ctypes.POINTER(ctypes.c_uint64))
 _sig("tide_ipc_open", _st, _vp, ctypes.POINTER(_vp))
 _sig("tide_ipc_close", _st, _vp)
 _sig("tide_layout_check_tiles", _st, _vp, ctypes.c_int, _vp, ctypes.c_int64, _i64p)
+_i64 = ctypes.c_int64
+_sig("tide_compute_create", _st, ctypes.POINTER(_vp))
+_sig("tide_compute_destroy", None, _vp)
+_sig("tide_fp8_store", _st, _vp, _i64, _i64, _vp, _i64, _vp, _vp, ctypes.c_int32, _vp)
+_sig("tide_fp8_restore", _st, _vp, _i64, _i64, _vp, _vp, ctypes.c_int32, _vp, _i64, _vp)
+_sig("tide_fp8_matmul", _st, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _vp)
+_sig("tide_gated_forward", _st, _vp, _i64, _i64, _i64, ctypes.c_int, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _vp)
+_sig("tide_gated_workspace", _st, _i64, _i64, _i64, _i64p)
+_sig("tide_gated_backward", _st, _vp, _i64, _i64, _i64, ctypes.c_int, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i64,
+     _vp, _vp, _vp, _i64, _vp, _i64, _vp)
 _sig("tide_build_info", ctypes.c_char_p)
 _sig("tide_status_string", ctypes.c_char_p, _st)
 _sig("tide_last_error", ctypes.c_char_p)
@@ -351,6 +364,79 @@ def tide_ag_place_ranks(layout, gathered, params, stream=None) -> None:
     """gathered: N rank-major bf16 buffers (block k read from buffer k); params: P pointers."""
     g, t = _table(gathered), _table(params)
     _check(_lib.tide_ag_place_ranks(layout, _tptr(g), _tptr(t), _stream(stream)), "tide_ag_place_ranks")
+
+
+class GatedCheckpointStruct(ctypes.Structure):
+    """tide_gated_checkpoint_t."""
+
+    _fields_ = [(n, ctypes.c_void_p)
+                for n in ("gate_codes", "gate_scales", "up_codes", "up_scales", "x_codes", "x_scales")]
+
+
+_ACTIVATIONS = {"silu": TIDE_ACT_SILU, "gelu": TIDE_ACT_GELU}
+
+
+def _activation(a) -> int:
+    if isinstance(a, str):
+        if a not in _ACTIVATIONS:
+            raise ValueError(f"activation {a!r}: one of {sorted(_ACTIVATIONS)}")
+        return _ACTIVATIONS[a]
+    return int(a)
+
+
+def tide_compute_create() -> int:
+    """Handle of the feed-forward operators."""
+    out = ctypes.c_void_p(0)
+    _check(_lib.tide_compute_create(ctypes.byref(out)), "tide_compute_create")
+    return out.value
+
+
+def tide_compute_destroy(compute: int) -> None:
+    _lib.tide_compute_destroy(compute)
+
+
+def tide_fp8_store(compute, rows, cols, src, ld_src, codes, scales, block_rows, stream=None) -> None:
+    """bf16 [rows, cols] to e4m3 codes and one power-of-two scale per block_rows x 128."""
+    _check(_lib.tide_fp8_store(compute, rows, cols, _addr(src), ld_src, _addr(codes), _addr(scales), block_rows,
+                               _stream(stream)), "tide_fp8_store")
+
+
+def tide_fp8_restore(compute, rows, cols, codes, scales, block_rows, dst, ld_dst, stream=None) -> None:
+    """The blocks' values as bf16."""
+    _check(_lib.tide_fp8_restore(compute, rows, cols, _addr(codes), _addr(scales), block_rows, _addr(dst), ld_dst,
+                                 _stream(stream)), "tide_fp8_restore")
+
+
+def tide_fp8_matmul(compute, m, n, k, a, a_scales, b, b_scales, out, ld_out, stream=None) -> None:
+    """out [m, n] = a [m, k] b [n, k]^T, a in 1 x 128 blocks and b in 128 x 128."""
+    _check(_lib.tide_fp8_matmul(compute, m, n, k, _addr(a), _addr(a_scales), _addr(b), _addr(b_scales), _addr(out),
+                                ld_out, _stream(stream)), "tide_fp8_matmul")
+
+
+def _checkpoint(c):
+    return 0 if c is None else ctypes.addressof(c.struct)
+
+
+def tide_gated_forward(compute, tokens, hidden, ffn, act, x, ld_x, w_gate, w_up, h, ld_h, checkpoint=None,
+                       stream=None) -> None:
+    """h = act(x w_gate^T) * (x w_up^T); a checkpoint's buffers are written too."""
+    _check(_lib.tide_gated_forward(compute, tokens, hidden, ffn, _activation(act), _addr(x), ld_x, _addr(w_gate),
+                                   _addr(w_up), _addr(h), ld_h, _checkpoint(checkpoint), _stream(stream)),
+           "tide_gated_forward")
+
+
+def gated_workspace_bytes(tokens: int, hidden: int, ffn: int) -> int:
+    """Bytes of tide_gated_backward's workspace."""
+    return _q64("tide_gated_workspace", tokens, hidden, ffn)
+
+
+def tide_gated_backward(compute, tokens, hidden, ffn, act, dh, ld_dh, x, ld_x, w_gate, w_up, checkpoint, dx, ld_dx,
+                        dw_gate, dw_up, h, ld_h, workspace, workspace_bytes, stream=None) -> None:
+    """dx, dw_gate, dw_up (and h) from dh; see include/tide.h."""
+    _check(_lib.tide_gated_backward(compute, tokens, hidden, ffn, _activation(act), _addr(dh), ld_dh, _addr(x), ld_x,
+                                    _addr(w_gate), _addr(w_up), _checkpoint(checkpoint), _addr(dx), ld_dx,
+                                    _addr(dw_gate), _addr(dw_up), _addr(h), ld_h, _addr(workspace), workspace_bytes,
+                                    _stream(stream)), "tide_gated_backward")
 
 
 def exported_symbols():

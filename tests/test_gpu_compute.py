@@ -1,0 +1,425 @@
+"""Feed-forward operators on the GPU against their 64-bit definitions.
+
+Bounds come from the formats (see ffn_reference); outputs are framed by guard
+elements that must stay as they were."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import ffn_reference as ref  # noqa: E402
+import layout_aware_collectives_gb300 as tide  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+GUARD = 64
+
+
+@pytest.fixture(scope="module")
+def compute():
+    with tide.Compute() as c:
+        yield c
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def randn(g, *shape, scale=1.0):
+    return (torch.randn(*shape, generator=g, device="cuda") * scale).bfloat16()
+
+
+class Guarded:
+    """An output of `rows` rows of `cols` elements, `ld` apart, in a buffer
+    filled with a value that nothing may overwrite around it."""
+
+    def __init__(self, rows, cols, ld=None, dtype=torch.bfloat16):
+        self.rows, self.cols, self.ld = rows, cols, cols if ld is None else ld
+        self.fill = 0x5A
+        n = GUARD + max(0, rows - 1) * self.ld + cols + GUARD
+        size = torch.empty(0, dtype=dtype).element_size()
+        self.bytes = torch.full((n * size,), self.fill, dtype=torch.uint8, device="cuda")
+        self.all = self.bytes.view(dtype)
+        self.size = size
+        self.t = self.all[GUARD:GUARD + max(0, rows - 1) * self.ld + cols]
+        self.view = torch.as_strided(self.all, (rows, cols), (self.ld, 1), GUARD)
+
+    def data_ptr(self):
+        return self.t.data_ptr()
+
+    def intact(self):
+        at = torch.arange(self.all.numel(), device="cuda") - GUARD
+        mine = (at >= 0) & (at < (self.rows - 1) * self.ld + self.cols) & (at.remainder(self.ld) < self.cols)
+        rest = self.bytes.view(-1, self.size)[~mine]
+        return bool((rest == self.fill).all())
+
+
+def strided(t, ld):
+    """A copy of t with rows ld apart."""
+    buf = torch.full((t.shape[0], ld), math.nan, dtype=t.dtype, device=t.device)
+    buf[:, :t.shape[1]] = t
+    return buf
+
+
+def close(got, want, bound):
+    got, want = got.double(), want.double()
+    assert got.shape == want.shape
+    bad = ~((got - want).abs() <= bound)
+    assert not bad.any(), f"{int(bad.sum())} of {bad.numel()} outside; worst {float((got - want).abs().sub(bound)[bad].max())}"
+
+
+# ------------------------------------------------------------------- blocks
+
+BLOCK_SHAPES = [(1, 1), (1, 128), (3, 129), (5, 250), (37, 768), (130, 136), (257, 1000), (128, 128), (64, 2049)]
+
+
+def awkward(g, rows, cols):
+    """Values over the whole range: zeros, subnormals, the largest, infinities, NaN, exact block limits."""
+    v = torch.randn(rows, cols, generator=g, device="cuda") * torch.exp2(
+        torch.randint(-120, 120, (rows, 1), generator=g, device="cuda").float())
+    flat = v.view(-1)
+    for i, s in enumerate((0.0, math.inf, -math.inf, math.nan, 448.0, 449.0, 464.0, 3.3e38, 1e-40, -0.0, 2.0 ** -133)):
+        flat[torch.randint(0, flat.numel(), (max(1, flat.numel() // 97),), generator=g, device="cuda")] = s
+    if rows > 2:
+        v[1] = 0
+        v[2, : cols // 2] = 1e-39
+    return v.bfloat16()
+
+
+def same_codes(got, want):
+    a, b = got.float(), want.float()
+    assert torch.equal(torch.isnan(a), torch.isnan(b))
+    a, b = torch.nan_to_num(a), torch.nan_to_num(b)
+    assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("block_rows", [1, 128])
+@pytest.mark.parametrize("rows,cols", BLOCK_SHAPES)
+@pytest.mark.parametrize("pad", [0, 3, 8])
+def test_store(compute, rows, cols, block_rows, pad):
+    g = gen(rows * 1000 + cols)
+    for v in (randn(g, rows, cols), awkward(g, rows, cols)):
+        codes = Guarded(rows, cols, dtype=torch.float8_e4m3fn)
+        scales = Guarded(-(-rows // block_rows), -(-cols // 128), dtype=torch.float32)
+        compute.fp8_store(rows, cols, strided(v, cols + pad) if pad else v, codes, scales, block_rows=block_rows,
+                          ld_src=cols + pad)
+        want_codes, want_scales = ref.blocks_store(v.float().cpu(), block_rows)
+        assert torch.equal(scales.view.cpu(), want_scales)
+        same_codes(codes.view.cpu(), want_codes)
+        assert codes.intact() and scales.intact()
+
+
+@pytest.mark.parametrize("block_rows", [1, 128])
+@pytest.mark.parametrize("rows,cols", BLOCK_SHAPES)
+@pytest.mark.parametrize("pad", [0, 3, 8])
+def test_restore(compute, rows, cols, block_rows, pad):
+    g = gen(rows * 1000 + cols + 1)
+    codes = torch.randint(0, 256, (rows, cols), generator=g, device="cuda", dtype=torch.uint8)
+    # any scale, not powers of two alone
+    scales = torch.randn(-(-rows // block_rows), -(-cols // 128), generator=g, device="cuda").exp()
+    dst = Guarded(rows, cols, cols + pad)
+    compute.fp8_restore(rows, cols, codes, scales, dst, block_rows=block_rows, ld_dst=cols + pad)
+    want = ref.blocks_value(codes.view(torch.float8_e4m3fn), scales, block_rows).float().bfloat16()
+    assert torch.equal(torch.isnan(dst.view), torch.isnan(want))
+    assert torch.equal(torch.nan_to_num(dst.view), torch.nan_to_num(want))
+    assert dst.intact()
+
+
+# ------------------------------------------------------------------ products
+
+MATMUL_SHAPES = [(1, 128, 128), (1, 8, 16), (2, 264, 400), (3, 1, 1), (7, 130, 129), (37, 768, 2048), (129, 264, 1040),
+                 (250, 704, 256), (300, 520, 144), (33, 100, 300), (513, 1024, 4096)]
+
+
+def fp8(g, rows, cols, block_rows, scale=1.0):
+    v = torch.randn(rows, cols, generator=g, device="cuda") * scale
+    codes = (v * 64).clamp(-448, 448).to(torch.float8_e4m3fn)
+    scales = torch.randn(-(-rows // block_rows), -(-cols // 128), generator=g, device="cuda").exp()
+    return codes, scales
+
+
+@pytest.mark.parametrize("m,n,k", MATMUL_SHAPES)
+@pytest.mark.parametrize("pad", [0, 1, 8])
+def test_matmul(compute, m, n, k, pad):
+    g = gen(m + n + k)
+    (a, sa), (b, sb) = fp8(g, m, k, 1), fp8(g, n, k, 128)
+    out = Guarded(m, n, n + pad)
+    compute.fp8_matmul(m, n, k, a, sa, b, sb, out, ld_out=n + pad)
+    close(out.view, *ref.matmul(a, sa, b, sb))
+    assert out.intact()
+
+
+def test_matmul_empty_sum(compute):
+    out = Guarded(5, 16, 24)
+    compute.fp8_matmul(5, 16, 0, 0, 0, 0, 0, out, ld_out=24)
+    assert (out.view == 0).all() and out.intact()
+
+
+def test_matmul_nan_stays_in_its_row_and_column(compute):
+    g = gen(5)
+    (a, sa), (b, sb) = fp8(g, 140, 512, 1), fp8(g, 264, 512, 128)
+    a.view(torch.uint8)[3, 200] = 0x7F
+    b.view(torch.uint8)[129, 17] = 0xFF
+    out = Guarded(140, 264)
+    compute.fp8_matmul(140, 264, 512, a, sa, b, sb, out)
+    nan = torch.zeros(140, 264, dtype=torch.bool, device="cuda")
+    nan[3], nan[:, 129] = True, True
+    assert torch.equal(torch.isnan(out.view), nan)
+
+
+# --------------------------------------------------------------------- gated
+
+# tokens, hidden, ffn: one token, single columns, ragged and unaligned sizes,
+# several tiles each way
+GATED_SHAPES = [(1, 256, 704), (1, 8, 8), (3, 1, 1), (5, 250, 130), (16, 128, 128), (17, 264, 136), (37, 2048, 768),
+                (129, 72, 1000), (250, 256, 704), (300, 1032, 264), (513, 512, 1408)]
+
+
+def checkpoint(tokens, hidden, ffn, with_x):
+    c = {n: Guarded(tokens, ffn, dtype=torch.float8_e4m3fn) for n in ("g8", "u8")}
+    c |= {n: Guarded(tokens, -(-ffn // 128), dtype=torch.float32) for n in ("gs", "us")}
+    if with_x:
+        c["x8"] = Guarded(tokens, hidden, dtype=torch.float8_e4m3fn)
+        c["xs"] = Guarded(tokens, -(-hidden // 128), dtype=torch.float32)
+    return c, tide.GatedCheckpoint(c["g8"], c["gs"], c["u8"], c["us"], c.get("x8"), c.get("xs"))
+
+
+def weights(g, hidden, ffn):
+    return randn(g, ffn, hidden, scale=hidden ** -0.5), randn(g, ffn, hidden, scale=hidden ** -0.5)
+
+
+def close_to_stored(codes, scales, want, err):
+    """Stored values are within e4m3's rounding (half a step: 2^-4 of the value,
+    2^-10 of the scale below its normal range) of values within `err` of want,
+    and each scale is the power of two its block's maximum asks for."""
+    got = ref.blocks_value(codes, scales, 1)
+    j = torch.arange(codes.shape[1], device="cuda") // 128
+    close(got, want, err + 2.0 ** -4 * (want.abs() + err) + 2.0 ** -10 * scales.double()[:, j])
+    for b in range(scales.shape[1]):
+        top = want[:, b * 128:(b + 1) * 128].abs().amax(1)
+        off = err[:, b * 128:(b + 1) * 128].amax(1)
+        s = scales[:, b].double()
+        assert (torch.frexp(scales[:, b])[0] == 0.5).all()
+        assert ((top - off <= 448 * s) & ((top + off > 224 * s) | (s <= 2.0 ** -126) | (top == 0))).all()
+
+
+@pytest.mark.parametrize("tokens,hidden,ffn", GATED_SHAPES)
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+@pytest.mark.parametrize("keep", ["none", "pre", "all"])
+def test_gated_forward(compute, tokens, hidden, ffn, kind, keep):
+    g = gen(tokens + hidden + ffn)
+    x, (wg, wu) = randn(g, tokens, hidden), weights(g, hidden, ffn)
+    h = Guarded(tokens, ffn)
+    bufs, ck = checkpoint(tokens, hidden, ffn, keep == "all") if keep != "none" else ({}, None)
+    compute.gated_forward(tokens, hidden, ffn, x, wg, wu, h, activation=kind, checkpoint=ck)
+    want, gg, uu = ref.gated_forward(x, wg, wu, kind)
+    bh, eg, eu = ref.gated_forward_bound(x, wg, wu, kind)
+    close(h.view, want, bh)
+    assert h.intact() and all(b.intact() for b in bufs.values())
+    if ck:
+        close_to_stored(bufs["g8"].view, bufs["gs"].view, gg, eg)
+        close_to_stored(bufs["u8"].view, bufs["us"].view, uu, eu)
+    if keep == "all":
+        codes, scales = ref.blocks_store(x.float().cpu(), 1)
+        assert torch.equal(bufs["xs"].view.cpu(), scales)
+        same_codes(bufs["x8"].view.cpu(), codes)
+
+
+@pytest.mark.parametrize("pad_x,pad_h", [(8, 16), (1, 0), (0, 3)])
+@pytest.mark.parametrize("tokens", [1, 40, 200])
+def test_gated_forward_strided(compute, pad_x, pad_h, tokens):
+    hidden, ffn = 264, 392
+    g = gen(tokens + pad_x)
+    x, (wg, wu) = randn(g, tokens, hidden), weights(g, hidden, ffn)
+    h = Guarded(tokens, ffn, ffn + pad_h)
+    compute.gated_forward(tokens, hidden, ffn, strided(x, hidden + pad_x), wg, wu, h, ld_x=hidden + pad_x, ld_h=ffn + pad_h)
+    close(h.view, ref.gated_forward(x, wg, wu, "silu")[0], ref.gated_forward_bound(x, wg, wu, "silu")[0])
+    assert h.intact()
+
+
+def run_backward(compute, tokens, hidden, ffn, kind, dh, x, wg, wu, ck=None, h=None, pad=0, **kw):
+    dx, dwg, dwu = Guarded(tokens, hidden, hidden + pad), Guarded(ffn, hidden), Guarded(ffn, hidden)
+    ws = torch.full((tide.gated_workspace_bytes(tokens, hidden, ffn) + 256,), 0xFF, dtype=torch.uint8, device="cuda")
+    compute.gated_backward(tokens, hidden, ffn, dh, x, wg, wu, dx, dwg, dwu, ws, activation=kind, checkpoint=ck, h=h,
+                           workspace_bytes=ws.numel() - 256, ld_dx=hidden + pad, **kw)
+    assert dx.intact() and dwg.intact() and dwu.intact()
+    assert (ws[-256:] == 0xFF).all()
+    return dx.view, dwg.view, dwu.view
+
+
+@pytest.mark.parametrize("tokens,hidden,ffn", GATED_SHAPES)
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+@pytest.mark.parametrize("with_h", [False, True])
+def test_gated_backward_recomputed(compute, tokens, hidden, ffn, kind, with_h):
+    g = gen(tokens + hidden + ffn + 1)
+    x, (wg, wu), dh = randn(g, tokens, hidden), weights(g, hidden, ffn), randn(g, tokens, ffn)
+    h = Guarded(tokens, ffn) if with_h else None
+    got = run_backward(compute, tokens, hidden, ffn, kind, dh, x, wg, wu, h=h)
+    want_h, gg, uu = ref.gated_forward(x, wg, wu, kind)
+    bh, eg, eu = ref.gated_forward_bound(x, wg, wu, kind)
+    want = ref.gated_backward_from(dh, gg, uu, x, wg, wu, kind)
+    for a, b, e in zip(got, want, ref.gated_backward_bound(dh, gg, uu, x, wg, wu, kind, eg, eu)):
+        close(a, b, e)
+    if with_h:
+        close(h.view, want_h, bh)
+        assert h.intact()
+
+
+@pytest.mark.parametrize("tokens,hidden,ffn", GATED_SHAPES)
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+@pytest.mark.parametrize("x8", [False, True])
+def test_gated_backward_from_checkpoint(compute, tokens, hidden, ffn, kind, x8):
+    g = gen(tokens + hidden + ffn + 2)
+    (wg, wu), dh = weights(g, hidden, ffn), randn(g, tokens, ffn)
+    x = randn(g, tokens, hidden)
+    g8, gs = ref.blocks_store(torch.randn(tokens, ffn, generator=g, device="cuda") * 3, 1)
+    u8, us = ref.blocks_store(torch.randn(tokens, ffn, generator=g, device="cuda"), 1)
+    xs = ref.blocks_store(x.float(), 1) if x8 else (None, None)
+    h = Guarded(tokens, ffn)
+    got = run_backward(compute, tokens, hidden, ffn, kind, dh, None if x8 else x, wg, wu,
+                       tide.GatedCheckpoint(g8, gs, u8, us, *xs), h=h)
+    xv = ref.blocks_value(*xs, 1) if x8 else x.double()
+    gg, uu = ref.blocks_value(g8, gs, 1), ref.blocks_value(u8, us, 1)
+    want = ref.gated_backward_from(dh, gg, uu, xv, wg, wu, kind)
+    for a, b, e in zip(got, want, ref.gated_backward_bound(dh, gg, uu, xv, wg, wu, kind)):
+        close(a, b, e)
+    arith = ref.arithmetic(gg, kind)
+    close(h.view, want[3], want[3].abs() * (arith + ref.U_BF16 * (1 + arith)) + uu.abs() * ref.flushed(gg) + ref.TINY)
+    assert h.intact()
+
+
+@pytest.mark.parametrize("pad", [8, 3])
+def test_gated_backward_strided_and_partial(compute, pad):
+    tokens, hidden, ffn = 130, 136, 264
+    g = gen(pad)
+    x, (wg, wu), dh = randn(g, tokens, hidden), weights(g, hidden, ffn), randn(g, tokens, ffn)
+    _, gg, uu = ref.gated_forward(x, wg, wu, "silu")
+    _, eg, eu = ref.gated_forward_bound(x, wg, wu, "silu")
+    want = ref.gated_backward_from(dh, gg, uu, x, wg, wu, "silu")
+    bounds = ref.gated_backward_bound(dh, gg, uu, x, wg, wu, "silu", eg, eu)
+    got = run_backward(compute, tokens, hidden, ffn, "silu", strided(dh, ffn + pad), strided(x, hidden + pad), wg, wu,
+                       pad=pad, ld_dh=ffn + pad, ld_x=hidden + pad)
+    for a, b, e in zip(got, want, bounds):
+        close(a, b, e)
+    ws = torch.empty(tide.gated_workspace_bytes(tokens, hidden, ffn), dtype=torch.uint8, device="cuda")
+    dx, dwg, dwu = Guarded(tokens, hidden), Guarded(ffn, hidden), Guarded(ffn, hidden)
+    compute.gated_backward(tokens, hidden, ffn, dh, x, wg, wu, dx, None, None, ws)
+    close(dx.view, want[0], bounds[0])
+    compute.gated_backward(tokens, hidden, ffn, dh, x, wg, wu, None, dwg, dwu, ws)
+    close(dwg.view, want[1], bounds[1])
+    close(dwu.view, want[2], bounds[2])
+
+
+def test_no_tokens_give_zero_gradients(compute):
+    hidden, ffn = 64, 128
+    wg = wu = torch.zeros(ffn, hidden, dtype=torch.bfloat16, device="cuda")
+    dwg, dwu = Guarded(ffn, hidden), Guarded(ffn, hidden)
+    compute.gated_backward(0, hidden, ffn, 0, 0, wg, wu, 0, dwg, dwu, 0, workspace_bytes=0)
+    assert (dwg.view == 0).all() and (dwu.view == 0).all() and dwg.intact() and dwu.intact()
+
+
+def test_nan_and_infinity_stay_in_their_token(compute):
+    """A token that holds NaN or infinities spoils its own row of h only, and
+    its checkpoint shows them as NaN."""
+    tokens, hidden, ffn = 150, 256, 264
+    g = gen(9)
+    x, (wg, wu) = randn(g, tokens, hidden), weights(g, hidden, ffn)
+    clean = Guarded(tokens, ffn)
+    compute.gated_forward(tokens, hidden, ffn, x, wg, wu, clean)
+    x[3, 7], x[140, 255] = math.nan, math.inf
+    h = Guarded(tokens, ffn)
+    bufs, ck = checkpoint(tokens, hidden, ffn, True)
+    compute.gated_forward(tokens, hidden, ffn, x, wg, wu, h, checkpoint=ck)
+    rows = torch.ones(tokens, dtype=torch.bool, device="cuda")
+    rows[[3, 140]] = False
+    assert torch.equal(h.view[rows], clean.view[rows])
+    assert torch.isnan(h.view[3]).all() and not torch.isfinite(h.view[140]).any()
+    for n in ("g8", "u8"):
+        bad = torch.isnan(bufs[n].view.float())
+        assert not bad[rows].any() and bad[3].all() and bad[140].all()
+    assert torch.equal(torch.isnan(bufs["x8"].view.float()), ~torch.isfinite(x))
+
+
+@pytest.mark.parametrize("value", [0.0, 30.0, 90.0, 1e4, 1e18])
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+def test_saturated_gates(compute, value, kind):
+    """Gates far out on both sides keep their limits, forward and backward."""
+    tokens, hidden, ffn = 5, 8, 128
+    x = torch.zeros(tokens, hidden, dtype=torch.bfloat16, device="cuda")
+    x[:, 0], x[:, 1] = 1.0, 1.0
+    wg = torch.zeros(ffn, hidden, dtype=torch.bfloat16, device="cuda")
+    wg[::2, 0], wg[1::2, 0] = value, -value
+    wu = torch.zeros_like(wg)
+    wu[:, 1] = 0.5
+    dh = torch.ones(tokens, ffn, dtype=torch.bfloat16, device="cuda")
+    h = Guarded(tokens, ffn)
+    compute.gated_forward(tokens, hidden, ffn, x, wg, wu, h, activation=kind)
+    want, gg, uu = ref.gated_forward(x, wg, wu, kind)
+    close(h.view, want, ref.gated_forward_bound(x, wg, wu, kind)[0])
+    got = run_backward(compute, tokens, hidden, ffn, kind, dh, x, wg, wu)
+    bounds = ref.gated_backward_bound(dh, gg, uu, x, wg, wu, kind)
+    for a, b, e in zip(got, ref.gated_backward_from(dh, gg, uu, x, wg, wu, kind), bounds):
+        close(a, b, e)
+
+
+def test_streams_and_capture(compute):
+    """Calls follow their own stream, and replay from a CUDA graph."""
+    tokens, hidden, ffn = 64, 256, 704
+    g = gen(4)
+    (wg, wu), dh = weights(g, hidden, ffn), randn(g, tokens, ffn)
+    x = torch.zeros(tokens, hidden, dtype=torch.bfloat16, device="cuda")
+    h, dx, dwg, dwu = (torch.empty(*s, dtype=torch.bfloat16, device="cuda")
+                       for s in ((tokens, ffn), (tokens, hidden), (ffn, hidden), (ffn, hidden)))
+    ws = torch.empty(tide.gated_workspace_bytes(tokens, hidden, ffn), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+
+    def step():
+        compute.gated_forward(tokens, hidden, ffn, x, wg, wu, h, stream=torch.cuda.current_stream())
+        compute.gated_backward(tokens, hidden, ffn, dh, x, wg, wu, dx, dwg, dwu, ws, stream=torch.cuda.current_stream())
+
+    def check():
+        want, gg, uu = ref.gated_forward(x, wg, wu, "silu")
+        bh, eg, eu = ref.gated_forward_bound(x, wg, wu, "silu")
+        close(h, want, bh)
+        for a, b, e in zip((dx, dwg, dwu), ref.gated_backward_from(dh, gg, uu, x, wg, wu, "silu"),
+                           ref.gated_backward_bound(dh, gg, uu, x, wg, wu, "silu", eg, eu)):
+            close(a, b, e)
+
+    with torch.cuda.stream(s):
+        x.copy_(randn(gen(7), tokens, hidden))
+        step()
+    s.synchronize()
+    check()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        step()
+    for seed in (11, 12):
+        x.copy_(randn(gen(seed), tokens, hidden))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        check()
+
+
+def test_first_call_is_not_captured():
+    with tide.Compute() as c:
+        src = torch.zeros(4, 128, dtype=torch.bfloat16, device="cuda")
+        codes, scales = torch.empty(4, 128, dtype=torch.uint8, device="cuda"), torch.empty(4, 1, device="cuda")
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            with pytest.raises(tide.TideError) as e:
+                c.fp8_store(4, 128, src, codes, scales, stream=torch.cuda.current_stream())
+        assert e.value.status == tide.TIDE_ERR_UNSUPPORTED
+
+
+def test_same_results_every_time(compute):
+    tokens, hidden, ffn = 90, 520, 1032
+    g = gen(21)
+    x, (wg, wu), dh = randn(g, tokens, hidden), weights(g, hidden, ffn), randn(g, tokens, ffn)
+    first = [t.clone() for t in run_backward(compute, tokens, hidden, ffn, "silu", dh, x, wg, wu)]
+    for _ in range(5):
+        for a, b in zip(first, run_backward(compute, tokens, hidden, ffn, "silu", dh, x, wg, wu)):
+            assert torch.equal(a, b)
