@@ -492,8 +492,8 @@ TIDE_API tide_status_t tide_layout_check_tiles(tide_layout_t layout, tide_op_t o
  *    tensor-core kernels; any other width or stride runs plain tiled
  *    kernels, right but many times slower.
  *  - Sums are fp32; a result is rounded to bf16 once, to nearest even.
- *  - Every buffer is the caller's, 16-byte aligned (TIDE_ERR_MISALIGNED) and
- *    in memory of the handle's device; outputs must not overlap inputs or
+ *  - Every buffer is the caller's, 16-byte aligned (scales: 4-byte;
+ *    TIDE_ERR_MISALIGNED otherwise) and in memory of the handle's device; outputs must not overlap inputs or
  *    each other.  A pointer to a matrix without elements may be NULL.
  *  - Sizes are 0 .. 2^31 - 1 each, and any matrix has at most 2^38 elements.
  *  - A compute handle may be used from several host threads and streams; it
@@ -511,6 +511,17 @@ typedef enum { TIDE_ACT_SILU = 0, TIDE_ACT_GELU = 1 } tide_activation_t;
  * uses it must have completed; NULL does nothing). */
 TIDE_API tide_status_t tide_compute_create(tide_compute_t* out);
 TIDE_API void tide_compute_destroy(tide_compute_t compute);
+
+/* Synchronises the device, then reads and clears the handle's error word:
+ * TIDE_ERR_TIMEOUT if, since the last check, a bounded wait inside one of its
+ * tensor-core kernels ran out (that call's outputs are incomplete), else
+ * TIDE_OK.  The wait bound is 2 s. */
+TIDE_API tide_status_t tide_compute_check_device(tide_compute_t compute);
+
+/* Test hook for the bounded waits, as tide_layout_set_test_stall: with ns > 0
+ * every following tensor-core launch waits, bounded by ns nanoseconds, on a
+ * barrier nothing arrives on, reports it and computes nothing. */
+TIDE_API tide_status_t tide_compute_set_test_stall(tide_compute_t compute, int64_t ns);
 
 /*
  * 8-bit blocks: a matrix [rows, cols] held as e4m3 codes (one byte each,

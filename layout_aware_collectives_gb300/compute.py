@@ -50,6 +50,12 @@ class Compute:
                                hidden if ld_dx is None else ld_dx, dw_gate, dw_up, h, ffn if ld_h is None else ld_h,
                                workspace, workspace_bytes, stream)
 
+    def check_device(self) -> None:
+        _t.tide_compute_check_device(self.handle)
+
+    def set_test_stall(self, ns: int) -> None:
+        _t.tide_compute_set_test_stall(self.handle, ns)
+
     # -------- lifetime
     def close(self) -> None:
         if getattr(self, "handle", None):

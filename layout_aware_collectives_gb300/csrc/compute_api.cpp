@@ -43,7 +43,10 @@ tide_status_t check_matrix(const void* p, int64_t rows, int64_t cols, int64_t ld
 
 tide_status_t check_blocks(const void* codes, const void* scales, int64_t rows, int64_t cols, const char* what) {
   TIDE_TRY(check_buffer(codes, rows * cols, (std::string(what) + " codes").c_str()));
-  return check_buffer(scales, rows * cols, (std::string(what) + " scales").c_str());
+  if (rows * cols == 0) return TIDE_OK;
+  if (!scales) return invalid(std::string(what) + " scales is NULL");
+  if ((uintptr_t)scales & 3u) return set_error(TIDE_ERR_MISALIGNED, std::string(what) + " scales is not 4-byte aligned");
+  return TIDE_OK;
 }
 
 bool capturing(cudaStream_t stream) {
@@ -72,8 +75,25 @@ tide_status_t bind(tide_compute_s* c, cudaStream_t stream) {
                      "the handle's first call sets it up on the device and cannot be captured; make one call before");
   e = cudaDeviceGetAttribute(&c->num_sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute(MultiProcessorCount)");
+  c->pairs = gated_tc_pairs();
+  if (c->pairs < 1) {
+    cudaGetLastError();
+    return set_error(TIDE_ERR_CUDA, "the device holds no pair of tensor-core CTAs");
+  }
+  if (!c->err) {
+    e = cudaHostAlloc((void**)&c->err, sizeof(int), cudaHostAllocMapped);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaHostAlloc(error word)");
+    *c->err = 0;
+    e = cudaHostGetDevicePointer((void**)&c->d_err, c->err, 0);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaHostGetDevicePointer(error word)");
+  }
   c->device = dev;
   return TIDE_OK;
+}
+
+TcLaunch launch_of(tide_compute_s* c) {
+  std::lock_guard<std::mutex> g(c->mu);
+  return TcLaunch{c->pairs, c->num_sms, c->d_err, (uint64_t)c->test_stall_ns};
 }
 
 tide_status_t launched(cudaError_t e, const char* what) { return e == cudaSuccess ? TIDE_OK : cuda_fail(e, what); }
@@ -119,7 +139,30 @@ tide_status_t tide_compute_create(tide_compute_t* out) {
   return *out ? TIDE_OK : set_error(TIDE_ERR_OUT_OF_MEMORY, "host allocation failed");
 }
 
-void tide_compute_destroy(tide_compute_t c) { delete c; }
+void tide_compute_destroy(tide_compute_t c) {
+  if (!c) return;
+  if (c->err && cudaFreeHost(c->err) != cudaSuccess) cudaGetLastError();
+  delete c;
+}
+
+tide_status_t tide_compute_check_device(tide_compute_t c) {
+  if (!c) return invalid("compute is NULL");
+  std::lock_guard<std::mutex> g(c->mu);
+  if (c->device < 0) return TIDE_OK;  // nothing launched yet
+  const cudaError_t e = cudaDeviceSynchronize();
+  if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize");
+  volatile int* err = c->err;
+  if (*err == 0) return TIDE_OK;
+  *err = 0;
+  return set_error(TIDE_ERR_TIMEOUT, "a bounded wait in a tensor-core kernel ran out; its outputs are incomplete");
+}
+
+tide_status_t tide_compute_set_test_stall(tide_compute_t c, int64_t ns) {
+  if (!c || ns < 0) return invalid("NULL handle or negative time");
+  std::lock_guard<std::mutex> g(c->mu);
+  c->test_stall_ns = ns;
+  return TIDE_OK;
+}
 
 tide_status_t tide_fp8_store(tide_compute_t c, int64_t rows, int64_t cols, const uint16_t* src, int64_t ld_src,
                              uint8_t* codes, float* scales, int32_t block_rows, cudaStream_t stream) {
@@ -164,6 +207,8 @@ tide_status_t tide_fp8_matmul(tide_compute_t c, int64_t m, int64_t n, int64_t k,
   if (k == 0)  // an empty sum
     return launched(cudaMemset2DAsync(out, ld_out * 2, 0, n * 2, m, stream), "tide_fp8_matmul");
   const MatmulArgs args{m, n, k, a, a_scales, b, b_scales, out, ld_out};
+  if (k % 16 == 0 && n % 8 == 0 && ld_out % 8 == 0)
+    return launched(launch_fp8_matmul_tc(args, launch_of(c), stream), "tide_fp8_matmul");
   return launched(launch_fp8_matmul_simple(args, stream), "tide_fp8_matmul");
 }
 
@@ -188,6 +233,8 @@ tide_status_t tide_gated_forward(tide_compute_t c, int64_t tokens, int64_t hidde
     TIDE_TRY(launched(launch_fp8_store(s, stream), "tide_gated_forward"));
   }
   if (ffn == 0) return TIDE_OK;
+  if (gated_tc_takes(a) && ld_x % 8 == 0 && ld_h % 8 == 0)
+    return launched(launch_gated_forward_tc(a, launch_of(c), stream), "tide_gated_forward");
   return launched(launch_gated_forward_simple(a, stream), "tide_gated_forward");
 }
 
@@ -245,9 +292,16 @@ tide_status_t tide_gated_backward(tide_compute_t c, int64_t tokens, int64_t hidd
   }
   a.dg = (uint16_t*)((char*)workspace + w.dg);
   a.du = (uint16_t*)((char*)workspace + w.du);
-  TIDE_TRY(launched(ck ? launch_gated_grad_stored(a, stream) : launch_gated_grad_simple(a, stream), what));
+  const TcLaunch l = launch_of(c);
+  const bool tc = gated_tc_takes(a);
+  if (ck)
+    TIDE_TRY(launched(launch_gated_grad_stored(a, stream), what));
+  else if (tc && ld_x % 8 == 0 && ld_dh % 8 == 0 && (!h || ld_h % 8 == 0))
+    TIDE_TRY(launched(launch_gated_grad_tc(a, l, stream), what));
+  else
+    TIDE_TRY(launched(launch_gated_grad_simple(a, stream), what));
   if (hidden == 0) return TIDE_OK;
-  if (dx) TIDE_TRY(launched(launch_gated_dx_simple(a, stream), what));
+  if (dx) TIDE_TRY(launched(tc && ld_dx % 8 == 0 ? launch_gated_dx_tc(a, l, stream) : launch_gated_dx_simple(a, stream), what));
   if (!dw_gate) return TIDE_OK;
   if (x8) {
     uint16_t* xr = (uint16_t*)((char*)workspace + w.x);
@@ -255,7 +309,7 @@ tide_status_t tide_gated_backward(tide_compute_t c, int64_t tokens, int64_t hidd
     TIDE_TRY(launched(launch_fp8_restore(r, stream), what));
     a.x = xr, a.ldx = hidden;
   }
-  return launched(launch_gated_dw_simple(a, stream), what);
+  return launched(tc && a.ldx % 8 == 0 ? launch_gated_dw_tc(a, l, stream) : launch_gated_dw_simple(a, stream), what);
 }
 
 }  // extern "C"

@@ -76,10 +76,37 @@ cudaError_t launch_gated_dx_simple(const GatedArgs& a, cudaStream_t stream);
 cudaError_t launch_gated_dw_simple(const GatedArgs& a, cudaStream_t stream);
 cudaError_t launch_fp8_matmul_simple(const MatmulArgs& a, cudaStream_t stream);
 
+// What a tensor-core launch takes from its handle.
+struct TcLaunch {
+  int pairs;  // pairs of CTAs the device holds at one time
+  int sms;
+  int* err;   // the handle's error word
+  uint64_t stall_ns;  // test: a wait that must run out
+};
+
+// Tensor-core kernels of the gated block (gated_tc.cu).  They take matrices
+// whose rows start on 16 bytes.
+int gated_tc_pairs();
+bool gated_tc_takes(const GatedArgs& a);
+cudaError_t launch_gated_forward_tc(const GatedArgs& a, const TcLaunch& l, cudaStream_t stream);
+cudaError_t launch_gated_grad_tc(const GatedArgs& a, const TcLaunch& l, cudaStream_t stream);
+cudaError_t launch_gated_dx_tc(const GatedArgs& a, const TcLaunch& l, cudaStream_t stream);
+cudaError_t launch_gated_dw_tc(const GatedArgs& a, const TcLaunch& l, cudaStream_t stream);
+
+// Tensor-core product of 8-bit blocks (fp8_tc.cu): k a multiple of 16, n and
+// the output's stride of 8.
+cudaError_t launch_fp8_matmul_tc(const MatmulArgs& a, const TcLaunch& l, cudaStream_t stream);
+
 }  // namespace tide
 
 struct tide_compute_s {
   int device = -1;  // bound by the first call
   int num_sms = 0;
+  int pairs = 0;
+  // Error word: pinned host memory that a kernel writes when a bounded wait
+  // runs out, so that nothing has to be zeroed on a stream.
+  int* err = nullptr;
+  int* d_err = nullptr;
+  int64_t test_stall_ns = 0;
   std::mutex mu;
 };

@@ -1,0 +1,232 @@
+// Product of two matrices held in 8-bit blocks, on the tensor cores.
+//
+//   out[i, j] = sum_b sa[i, b] sb[j / 128, b] sum_{k in b} a[i, k] b[j, k]
+//
+// A block is 128 steps of the contraction: one pipeline stage.  Its codes'
+// product is summed by the tensor cores into one of two TMEM accumulators;
+// from there 8 warps add it, times sa sb, to fp32 sums in registers (one
+// fused multiply-add each, a row's scale being a thread's), while the tensor
+// cores sum the next block into the other.  So scales need not be powers of
+// two, and the sum across blocks is fp32's own.
+//
+// A pair of CTAs works on a 256 x 256 tile, each with 128 rows of A and 128
+// of B as in the gated block's kernel.  One block of it is 512 cycles of the
+// tensor cores at their 8-bit rate, against 256 of TMEM reads and 256 of
+// multiply-adds (the latter halved by the two-wide form).
+#include "compute_device.cuh"
+#include "tc_device.cuh"
+#include "tc_host.h"
+
+namespace tide {
+namespace {
+
+using namespace tc;
+
+constexpr int kStages = 6;
+constexpr int kHalf = 128;
+constexpr uint32_t kOperand = kHalf * kBlock;  // bytes of either operand in one stage
+constexpr uint32_t kStage = 2 * kOperand;
+constexpr int kSumWarps = 8;
+constexpr int kThreads = 128 + 32 * kSumWarps;
+constexpr int kBoxes = 2;
+constexpr size_t kSmem = 1024 + kStages * kStage + kSumWarps * kBoxes * kBox;
+
+struct Params {
+  CUtensorMap a, b, out;
+  const float *sa, *sb;
+  int rows, cols;
+  int tiles_m, tiles_n, tiles;
+  int blocks;  // of the contraction
+  int* err;
+  uint64_t limit_ns, stall_ns;
+};
+
+// (x, y) += (a, b) * s.
+__device__ __forceinline__ void fma2(float& x, float& y, uint32_t a, uint32_t b, float s) {
+  asm("{ .reg .b64 c, v, w; mov.b64 c, {%0, %1}; mov.b64 v, {%2, %3}; mov.b64 w, {%4, %4};\n"
+      "fma.rn.f32x2 c, v, w, c; mov.b64 {%0, %1}, c; }"
+      : "+f"(x), "+f"(y)
+      : "r"(a), "r"(b), "f"(s));
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) fp8_tc_kernel(const __grid_constant__ Params p) {
+  constexpr uint32_t kInstr = instr_desc(0, 0, 0, 256, 256);
+  extern __shared__ uint8_t raw[];
+  __shared__ uint64_t bars[2 * kStages + 5];
+  __shared__ uint32_t tmem_at;
+  __shared__ int stop;
+
+  const uint32_t smem = (smem_addr(raw) + 1023u) & ~1023u;
+  const uint32_t bar0 = smem_addr(bars);
+  const auto full = [&](int s) { return bar0 + 8u * s; };
+  const auto empty = [&](int s) { return bar0 + 8u * (kStages + s); };
+  const auto sums_full = [&](int b) { return bar0 + 8u * (2 * kStages + b); };
+  const auto sums_empty = [&](int b) { return bar0 + 8u * (2 * kStages + 2 + b); };
+  const uint32_t spare = bar0 + 8u * (2 * kStages + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const Watch watch{&stop, p.err, p.limit_ns};
+
+  if (threadIdx.x == 0) {
+    stop = 0;
+    for (int s = 0; s < kStages; ++s) bar_init(full(s), 1), bar_init(empty(s), 1);
+    for (int b = 0; b < 2; ++b) bar_init(sums_full(b), 1), bar_init(sums_empty(b), 2 * kSumWarps);
+    bar_init(spare, 1);
+    bar_init_fence();
+    prefetch_map(&p.a), prefetch_map(&p.b), prefetch_map(&p.out);
+  }
+  if (warp == 2) tmem_alloc<2>(smem_addr(&tmem_at), 512);
+  fence_before();
+  __syncthreads();
+  cluster_sync();
+  fence_after();
+  const uint32_t tmem = tmem_at;
+
+  if (p.stall_ns) {  // test: a wait on a barrier nothing arrives on runs out
+    if (threadIdx.x == 0) bar_wait(spare, 0, Watch{&stop, p.err, p.stall_ns});
+  } else if (warp < 4) {
+    // 384 threads start with 168 registers each (64,512); this warpgroup goes
+    // down to 56 and the two that hold sums go up to 216: 62,464.
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == 0 && lane == 0) {
+      int j = 0;  // stages filled so far
+      bool go = true;
+      for (int t = pair; t < p.tiles && go; t += pairs) {
+        const TileAt at = tile_at(p.tiles_m, p.tiles_n, t);
+        for (int k = 0; k < p.blocks; ++k, ++j) {
+          const int s = j % kStages;
+          if (j >= kStages && !bar_wait(empty(s), (j / kStages + 1) & 1, watch)) {
+            go = false;
+            break;
+          }
+          if (rank == 0) bar_expect(full(s), 2 * kStage);
+          const uint32_t bar = peer_addr(full(s), 0);
+          const uint32_t a = smem + s * kStage;
+          load_box<true>(a, &p.a, k * kBlock, (at.m * 2 + rank) * kHalf, bar);
+          load_box<true>(a + kOperand, &p.b, k * kBlock, (at.n * 2 + rank) * kHalf, bar);
+        }
+      }
+      // the MMAs' last arrivals reach this CTA while it is still there
+      for (int i = max(0, j - kStages); i < j && go; ++i) go = bar_wait(empty(i % kStages), (i / kStages) & 1, watch);
+      // after a wait that ran out: both CTAs' copies in flight, with a limit
+      // again; the peer's memory stays until the cluster's last barrier
+      if (!go && rank == 0) {
+        int never = 0;
+        for (int i = max(0, j - kStages); i < j; ++i)
+          bar_wait(full(i % kStages), (i / kStages) & 1, Watch{&never, p.err, p.limit_ns / 16});
+      }
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+      int j = 0;  // blocks so far
+      bool go = true;
+      for (int t = pair; t < p.tiles && go; t += pairs) {
+        for (int k = 0; k < p.blocks; ++k, ++j) {
+          const int s = j % kStages, b = j & 1;
+          if ((j >= 2 && !bar_wait(sums_empty(b), (j / 2 + 1) & 1, watch)) || !bar_wait(full(s), (j / kStages) & 1, watch)) {
+            go = false;
+            break;
+          }
+          fence_after();
+          const uint32_t a = smem + s * kStage;
+          const uint64_t da = operand_desc(a, 16), db = operand_desc(a + kOperand, 16);
+#pragma unroll
+          for (int q = 0; q < kBlock / 32; ++q) mma<2, true>(tmem + b * 256, da + q * 2, db + q * 2, kInstr, q > 0);
+          mma_commit<2>(empty(s));
+          mma_commit<2>(sums_full(b));
+        }
+      }
+      if (!go) {  // the MMAs in flight, with a limit
+        int never = 0;
+        mma_commit<2>(spare);
+        bar_wait(spare, 0, Watch{&never, p.err, p.limit_ns / 16});
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    const int w = warp - 4, half = w >> 2;
+    const uint32_t lanes = (uint32_t)(w & 3) * 32;
+    Outbox<kBoxes> out{smem + kStages * kStage + w * kBoxes * kBox, 0, lane};
+    const uint32_t taddr = tmem + (lanes << 16) + half * kHalf;
+    int j = 0;
+    bool go = true;
+    for (int t = pair; t < p.tiles && go; t += pairs) {
+      const TileAt at = tile_at(p.tiles_m, p.tiles_n, t);
+      const int row0 = (at.m * 2 + rank) * kHalf + lanes, row = row0 + lane;
+      const int col0 = (at.n * 2 + half) * kHalf;
+      // rows and columns past the end take any scale that is there: their
+      // codes are zeros, or they are not written
+      const float* sa = p.sa + (int64_t)min(row, p.rows - 1) * p.blocks;
+      const float* sb = p.sb + (int64_t)(min(col0, p.cols - 1) / kBlock) * p.blocks;
+      float sum[kHalf];
+#pragma unroll
+      for (int i = 0; i < kHalf; ++i) sum[i] = 0.0f;
+      float next = __ldg(sa) * __ldg(sb);
+      for (int k = 0; k < p.blocks; ++k, ++j) {
+        const int b = j & 1;
+        const float s = next;
+        if (k + 1 < p.blocks) next = __ldg(sa + k + 1) * __ldg(sb + k + 1);
+        if (!bar_wait_warp(sums_full(b), (j / 2) & 1, watch)) {
+          go = false;
+          break;
+        }
+        fence_after();
+#pragma unroll
+        for (int c = 0; c < kHalf / 64; ++c) {
+          uint32_t v[32], x[32];
+          tmem_read32x2(taddr + b * 256 + c * 64, taddr + b * 256 + c * 64 + 32, v, x);
+          if (c == kHalf / 64 - 1) {
+            fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive_peer(peer_addr(sums_empty(b), 0));
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            fma2(sum[c * 64 + 2 * i], sum[c * 64 + 2 * i + 1], v[2 * i], v[2 * i + 1], s);
+            fma2(sum[c * 64 + 32 + 2 * i], sum[c * 64 + 33 + 2 * i], x[2 * i], x[2 * i + 1], s);
+          }
+        }
+      }
+      if (!go) break;
+#pragma unroll
+      for (int c = 0; c < kHalf / 32; ++c) {
+        const int col = col0 + c * 32;
+        if (row0 < p.rows && col < p.cols) {
+          uint32_t o[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[i] = pack_bf16(sum[c * 32 + 2 * i], sum[c * 32 + 2 * i + 1]);
+          out.put(&p.out, o, col, row0);
+        }
+      }
+    }
+    if (lane == 0) stores_done();
+  }
+  __syncthreads();
+  cluster_sync();
+  if (warp == 2) tmem_free<2>(tmem, 512);
+}
+
+}  // namespace
+
+cudaError_t launch_fp8_matmul_tc(const MatmulArgs& a, const TcLaunch& l, cudaStream_t stream) {
+  static const cudaError_t ready =
+      cudaFuncSetAttribute(fp8_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  if (ready != cudaSuccess) return ready;
+  Params p{};
+  p.sa = a.sa, p.sb = a.sb;
+  p.rows = (int)a.m, p.cols = (int)a.n;
+  p.tiles_m = (int)ceil_div(a.m, 2 * kHalf), p.tiles_n = (int)ceil_div(a.n, 2 * kHalf);
+  p.tiles = p.tiles_m * p.tiles_n;
+  p.blocks = (int)ceil_div(a.k, kBlock);
+  p.err = l.err;
+  p.limit_ns = TIDE_BULK_TIMEOUT_NS;
+  p.stall_ns = l.stall_ns;
+  if (!make_map(&p.a, a.a, 1, a.k, a.m, a.k, kBlock, kHalf, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_map(&p.b, a.b, 1, a.k, a.n, a.k, kBlock, kHalf, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_map(&p.out, a.out, 2, a.n, a.m, a.ldo, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
+    return cudaErrorInvalidValue;
+  const int pairs = p.tiles < l.pairs ? p.tiles : l.pairs;
+  fp8_tc_kernel<<<2 * pairs, kThreads, kSmem, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace tide

@@ -1,0 +1,273 @@
+// Device helpers of the tensor-core kernels: mbarriers with bounded waits,
+// tensor-map copies, and the 5th-generation tensor-core instructions with
+// their shared-memory and instruction descriptors.
+#pragma once
+
+#include <cuda.h>
+#include <stdint.h>
+
+namespace tide {
+namespace tc {
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+
+// Address in CTA `rank`'s shared memory of what has this address here.
+__device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// ---------------------------------------------------------------- mbarriers
+
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_init_fence() { asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory"); }
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// Arrives on a barrier of another CTA of the cluster (a peer_addr).
+__device__ __forceinline__ void bar_arrive_peer(uint32_t peer_bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(peer_bar) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; selp.b32 %0, 1, 0, p; }"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+__device__ __forceinline__ uint64_t now_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+
+// What a wait that runs out does: the handle's error word is set and every
+// role of this CTA leaves its loop.
+struct Watch {
+  volatile int* stop;   // shared
+  int* err;             // host-visible
+  uint64_t limit_ns;
+};
+
+__device__ __forceinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, const Watch& w) {
+  const uint64_t t0 = now_ns();
+  while (!bar_try(bar, parity)) {
+    if (*w.stop) return false;
+    if (now_ns() - t0 > w.limit_ns) {
+      *w.stop = 1;
+      *(volatile int*)w.err = kDevErrTimeout;
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, const Watch& w) {
+  return bar_try(bar, parity) || bar_wait_slow(bar, parity, w);
+}
+// The same for a whole warp, which leaves together.
+__device__ __forceinline__ bool bar_wait_warp(uint32_t bar, uint32_t parity, const Watch& w) {
+  return __all_sync(0xffffffffu, bar_wait(bar, parity, w));
+}
+
+// ------------------------------------------------------- tensor-map copies
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
+}
+
+// A box of a 2-D tensor into this CTA's shared memory.  PAIR: `bar` may be
+// the pair's leader's barrier (a peer_addr).
+template <bool PAIR>
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* m, int x, int y, uint32_t bar) {
+  if constexpr (PAIR)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+        "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(m), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(m), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+// A box of shared memory to a 2-D tensor, clipped at its end.
+__device__ __forceinline__ void store_box(const CUtensorMap* m, int x, int y, uint32_t src) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(m), "r"(x),
+               "r"(y), "r"(src)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void stores_read() {  // all but the last N groups have been read from shared memory
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+__device__ __forceinline__ void async_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// ------------------------------------------------------------ tensor cores
+
+template <int GROUP>
+__device__ __forceinline__ void tmem_alloc(uint32_t dst, uint32_t columns) {
+  if constexpr (GROUP == 2)
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(columns) : "memory");
+  else
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(columns) : "memory");
+}
+template <int GROUP>
+__device__ __forceinline__ void tmem_free(uint32_t base, uint32_t columns) {
+  if constexpr (GROUP == 2) {
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(columns));
+  } else {
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(columns));
+  }
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// Shared-memory descriptor of an operand tile with 128-byte swizzle (8 rows
+// of 128 bytes repeat).  K-major: a row is 64 (bf16) or 128 (8-bit) steps of
+// the contraction, SBO = 1024 steps 8 rows on.  MN-major: a row is 64 rows or
+// columns of the operand, SBO steps 8 of the contraction on and LBO 64 rows
+// or columns on.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, uint32_t lbo) {
+  constexpr uint32_t kSbo = 1024;
+  return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(kSbo >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+// Instruction descriptor: fp32 sums, A and B of type `ab` (bf16: 1 in
+// kind::f16; e4m3: 0 in kind::f8f6f4), majors 1 = MN.
+constexpr uint32_t instr_desc(uint32_t ab, uint32_t a_mn, uint32_t b_mn, uint32_t m, uint32_t n) {
+  return (1u << 4) | (ab << 7) | (ab << 10) | (a_mn << 15) | (b_mn << 16) | ((n >> 3) << 17) | ((m >> 4) << 24);
+}
+
+// D (+)= A B for one step of the contraction (32 bytes of it).
+template <int GROUP, bool FP8>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  const uint32_t p = add ? 1u : 0u;
+#define TIDE_MMA(group, kind)                                                                               \
+  asm volatile("{ .reg .pred p; setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::" group ".kind::" kind       \
+               " [%0], %1, %2, %3, p; }" ::"r"(d),                                                          \
+               "l"(a), "l"(b), "r"(idesc), "r"(p)                                                           \
+               : "memory")
+  if constexpr (GROUP == 2 && FP8) TIDE_MMA("2", "f8f6f4");
+  if constexpr (GROUP == 2 && !FP8) TIDE_MMA("2", "f16");
+  if constexpr (GROUP == 1 && FP8) TIDE_MMA("1", "f8f6f4");
+  if constexpr (GROUP == 1 && !FP8) TIDE_MMA("1", "f16");
+#undef TIDE_MMA
+}
+
+// Arrives on `bar` (at this address in both CTAs of a pair) once the MMAs
+// issued so far have completed.
+template <int GROUP>
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+  if constexpr (GROUP == 2)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+  else
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+#define TIDE_R8(v, i) "=r"(v[i]), "=r"(v[i + 1]), "=r"(v[i + 2]), "=r"(v[i + 3]), "=r"(v[i + 4]), "=r"(v[i + 5]), \
+                      "=r"(v[i + 6]), "=r"(v[i + 7])
+#define TIDE_R32(v) TIDE_R8(v, 0), TIDE_R8(v, 8), TIDE_R8(v, 16), TIDE_R8(v, 24)
+
+// 32 columns of this warp's 32 TMEM lanes, one lane a thread; waits for them.
+__device__ __forceinline__ void tmem_read32(uint32_t addr, uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : TIDE_R32(v)
+      : "r"(addr)
+      : "memory");
+}
+// The same for two runs of 32 columns.
+__device__ __forceinline__ void tmem_read32x2(uint32_t a0, uint32_t a1, uint32_t (&v)[32], uint32_t (&w)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%64];\n"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,"
+      "%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%65];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : TIDE_R32(v), TIDE_R32(w)
+      : "r"(a0), "r"(a1)
+      : "memory");
+}
+
+struct TileAt {
+  int z, m, n;  // which of several products; tile indices
+};
+
+// Tiles in bands of 16 down the rows, so that the tiles at work at one time
+// share their operands in L2.
+__device__ __forceinline__ TileAt tile_at(int tiles_m, int tiles_n, int t) {
+  constexpr int kBand = 16;
+  const int per = tiles_m * tiles_n;
+  TileAt r;
+  r.z = t / per;
+  t -= r.z * per;
+  const int band = t / (kBand * tiles_n), first = band * kBand;
+  const int high = min(kBand, tiles_m - first);
+  t -= first * tiles_n;
+  r.n = t / high;
+  r.m = first + t - r.n * high;
+  return r;
+}
+
+__device__ __forceinline__ float as_f(uint32_t v) { return __uint_as_float(v); }
+
+// Results on their way out: 32 x 32 boxes of one warp, a ring of BOXES.
+constexpr uint32_t kBox = 32 * 32 * 2;  // 32 rows of 32 bf16
+
+template <int BOXES>
+struct Outbox {
+  uint32_t base;
+  int next;
+  int lane;
+
+  __device__ __forceinline__ void put(const CUtensorMap* map, const uint32_t (&p)[16], int col, int row) {
+    if (lane == 0) stores_read<BOXES - 1>();
+    __syncwarp();
+    const uint32_t box = base + (uint32_t)(next % BOXES) * kBox;
+    ++next;
+    // 64-byte swizzle: 16-byte piece c of row r lies at piece c ^ (r / 2 % 4)
+    const uint32_t row_at = box + lane * 64, turn = (lane >> 1) & 3;
+#pragma unroll
+    for (uint32_t c = 0; c < 4; ++c)
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row_at + ((c ^ turn) << 4)), "r"(p[4 * c]),
+                   "r"(p[4 * c + 1]), "r"(p[4 * c + 2]), "r"(p[4 * c + 3])
+                   : "memory");
+    async_fence();
+    __syncwarp();
+    if (lane == 0) store_box(map, col, row, box);
+  }
+};
+
+}  // namespace tc
+}  // namespace tide

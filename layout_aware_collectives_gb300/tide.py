@@ -99,6 +99,8 @@ _sig("tide_layout_check_tiles", _st, _vp, ctypes.c_int, _vp, ctypes.c_int64, _i6
 _i64 = ctypes.c_int64
 _sig("tide_compute_create", _st, ctypes.POINTER(_vp))
 _sig("tide_compute_destroy", None, _vp)
+_sig("tide_compute_check_device", _st, _vp)
+_sig("tide_compute_set_test_stall", _st, _vp, _i64)
 _sig("tide_fp8_store", _st, _vp, _i64, _i64, _vp, _i64, _vp, _vp, ctypes.c_int32, _vp)
 _sig("tide_fp8_restore", _st, _vp, _i64, _i64, _vp, _vp, ctypes.c_int32, _vp, _i64, _vp)
 _sig("tide_fp8_matmul", _st, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _vp)
@@ -393,6 +395,15 @@ def tide_compute_create() -> int:
 
 def tide_compute_destroy(compute: int) -> None:
     _lib.tide_compute_destroy(compute)
+
+
+def tide_compute_check_device(compute) -> None:
+    """Raises TideError(TIDE_ERR_TIMEOUT) if a bounded device wait ran out."""
+    _check(_lib.tide_compute_check_device(compute), "tide_compute_check_device")
+
+
+def tide_compute_set_test_stall(compute, ns: int) -> None:
+    _check(_lib.tide_compute_set_test_stall(compute, ns), "tide_compute_set_test_stall")
 
 
 def tide_fp8_store(compute, rows, cols, src, ld_src, codes, scales, block_rows, stream=None) -> None:

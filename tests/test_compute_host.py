@@ -37,7 +37,7 @@ def test_store_and_restore_refuse(compute):
         refused(BAD, f, 4, 128, A, A, 0)
         refused(MIS, f, 4, 128, A + 2, A, A)
         refused(MIS, f, 4, 128, A, A + 1, A)
-        refused(MIS, f, 4, 128, A, A, A + 4)
+        refused(MIS, f, 4, 128, A, A, A + 2)
         f(0, 128, 0, 0, 0)  # nothing to do, no device touched
         f(4, 0, 0, 0, 0)
     refused(BAD, compute.fp8_store, 4, 128, A, A, A, ld_src=127)
@@ -47,7 +47,7 @@ def test_store_and_restore_refuse(compute):
 def test_matmul_refuses(compute):
     ok = [4, 8, 128, A, A, A, A, A]
     for i, v, st in ((0, -1, BAD), (1, 1 << 31, BAD), (2, -5, BAD), (3, 0, BAD), (4, 0, BAD), (5, A + 8, MIS),
-                     (6, A + 4, MIS), (7, A + 2, MIS), (7, 0, BAD)):
+                     (6, A + 1, MIS), (7, A + 2, MIS), (7, 0, BAD)):
         bad = list(ok)
         bad[i] = v
         refused(st, compute.fp8_matmul, *bad)

@@ -423,3 +423,25 @@ def test_same_results_every_time(compute):
     for _ in range(5):
         for a, b in zip(first, run_backward(compute, tokens, hidden, ffn, "silu", dh, x, wg, wu)):
             assert torch.equal(a, b)
+
+
+def test_wait_that_runs_out_is_reported():
+    tokens, hidden, ffn = 300, 256, 704
+    g = gen(30)
+    x, (wg, wu), dh = randn(g, tokens, hidden), weights(g, hidden, ffn), randn(g, tokens, ffn)
+    h = Guarded(tokens, ffn)
+    with tide.Compute() as c:
+        c.check_device()
+        c.set_test_stall(1_000_000)
+        for call in (lambda: c.gated_forward(tokens, hidden, ffn, x, wg, wu, h),
+                     lambda: run_backward(c, tokens, hidden, ffn, "silu", dh, x, wg, wu)):
+            call()
+            with pytest.raises(tide.TideError) as e:
+                c.check_device()
+            assert e.value.status == tide.TIDE_ERR_TIMEOUT
+            c.check_device()  # cleared
+        c.set_test_stall(0)
+        c.gated_forward(tokens, hidden, ffn, x, wg, wu, h)
+        c.check_device()
+        close(h.view, ref.gated_forward(x, wg, wu, "silu")[0], ref.gated_forward_bound(x, wg, wu, "silu")[0])
+        assert h.intact()
