@@ -41,12 +41,8 @@ struct Params {
   uint64_t limit_ns, stall_ns;
 };
 
-// (x, y) += (a, b) * s.
-__device__ __forceinline__ void fma2(float& x, float& y, uint32_t a, uint32_t b, float s) {
-  asm("{ .reg .b64 c, v, w; mov.b64 c, {%0, %1}; mov.b64 v, {%2, %3}; mov.b64 w, {%4, %4};\n"
-      "fma.rn.f32x2 c, v, w, c; mov.b64 {%0, %1}, c; }"
-      : "+f"(x), "+f"(y)
-      : "r"(a), "r"(b), "f"(s));
+__device__ __forceinline__ void fma2(uint64_t& c, uint32_t a, uint32_t b, uint64_t w) {
+  asm("{ .reg .b64 v; mov.b64 v, {%1, %2}; fma.rn.f32x2 %0, v, %3, %0; }" : "+l"(c) : "r"(a), "r"(b), "l"(w));
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) fp8_tc_kernel(const __grid_constant__ Params p) {
@@ -157,14 +153,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) fp8_tc_
       // codes are zeros, or they are not written
       const float* sa = p.sa + (int64_t)min(row, p.rows - 1) * p.blocks;
       const float* sb = p.sb + (int64_t)(min(col0, p.cols - 1) / kBlock) * p.blocks;
-      float sum[kHalf];
+      uint64_t sum[kHalf / 2];
 #pragma unroll
-      for (int i = 0; i < kHalf; ++i) sum[i] = 0.0f;
-      float next = __ldg(sa) * __ldg(sb);
+      for (int i = 0; i < kHalf / 2; ++i) sum[i] = 0;
+      float next_a = __ldg(sa), next_b = __ldg(sb);
       for (int k = 0; k < p.blocks; ++k, ++j) {
         const int b = j & 1;
-        const float s = next;
-        if (k + 1 < p.blocks) next = __ldg(sa + k + 1) * __ldg(sb + k + 1);
+        const uint32_t s1 = __float_as_uint(next_a * next_b);
+        const uint64_t s = ((uint64_t)s1 << 32) | s1;
+        if (k + 1 < p.blocks) next_a = __ldg(sa + k + 1), next_b = __ldg(sb + k + 1);
         if (!bar_wait_warp(sums_full(b), (j / 2) & 1, watch)) {
           go = false;
           break;
@@ -181,8 +178,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) fp8_tc_
           }
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            fma2(sum[c * 64 + 2 * i], sum[c * 64 + 2 * i + 1], v[2 * i], v[2 * i + 1], s);
-            fma2(sum[c * 64 + 32 + 2 * i], sum[c * 64 + 33 + 2 * i], x[2 * i], x[2 * i + 1], s);
+            fma2(sum[c * 32 + i], v[2 * i], v[2 * i + 1], s);
+            fma2(sum[c * 32 + 16 + i], x[2 * i], x[2 * i + 1], s);
           }
         }
       }
@@ -193,7 +190,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) fp8_tc_
         if (row0 < p.rows && col < p.cols) {
           uint32_t o[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = pack_bf16(sum[c * 32 + 2 * i], sum[c * 32 + 2 * i + 1]);
+          for (int i = 0; i < 16; ++i) o[i] = pack_bf16(as_f((uint32_t)sum[c * 16 + i]), as_f((uint32_t)(sum[c * 16 + i] >> 32)));
           out.put(&p.out, o, col, row0);
         }
       }

@@ -40,14 +40,17 @@ __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
 __device__ __forceinline__ void bar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// Arrives on a barrier of another CTA of the cluster (a peer_addr).
+// Arrives on a barrier of another CTA of the cluster (a peer_addr).  It
+// tells of TMEM reads that have completed, not of writes to memory, so it
+// releases at CTA scope: at cluster scope every arrival waited for a memory
+// barrier (28% of the 8-bit product's stalls).
 __device__ __forceinline__ void bar_arrive_peer(uint32_t peer_bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(peer_bar) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(peer_bar) : "memory");
 }
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; selp.b32 %0, 1, 0, p; }"
+      "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.b32 %0, 1, 0, p; }"
       : "=r"(ok)
       : "r"(bar), "r"(parity)
       : "memory");
@@ -257,7 +260,8 @@ struct Outbox {
     const uint32_t box = base + (uint32_t)(next % BOXES) * kBox;
     ++next;
     // 64-byte swizzle: 16-byte piece c of row r lies at piece c ^ (r / 2 % 4)
-    const uint32_t row_at = box + lane * 64, turn = (lane >> 1) & 3;
+    uint32_t row_at = box + lane * 64, turn = (lane >> 1) & 3;
+    asm volatile("" : "+r"(row_at), "+r"(turn));  // computed here: kept across the main loop they cost registers
 #pragma unroll
     for (uint32_t c = 0; c < 4; ++c)
       asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row_at + ((c ^ turn) << 4)), "r"(p[4 * c]),
