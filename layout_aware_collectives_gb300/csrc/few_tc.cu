@@ -1,0 +1,360 @@
+// The gated block and the 8-bit product for few tokens (one to a few
+// hundred), where the weights' bytes are what counts.
+//
+// The tiles of gated_tc.cu and fp8_tc.cu put 256 tokens on the tensor cores'
+// rows; with few tokens most of those are padding and few tiles are left to
+// share out.  Here the weights take the rows: a CTA multiplies 128 of them
+// (for the gated block 128 of Wg and the same 128 of Wu) by NT = 16 to 128
+// tokens, and a cluster of up to 8 CTAs splits the contraction.  Each CTA
+// leaves its sums in its shared memory, [token][feature] in fp32; then every
+// CTA of the cluster finishes its share of the tokens, adding the others'
+// sums over distributed shared memory in the order of their ranks, so the
+// result does not depend on timing.
+//
+// Bound by HBM: the weights stream through a ring of 3-5 stages of 18-48 KiB,
+// with two CTAs to an SM up to 32 tokens.
+#include "compute_device.cuh"
+#include "tc_device.cuh"
+#include "tc_host.h"
+
+namespace tide {
+namespace {
+
+using namespace tc;
+
+constexpr int kRows = 128;             // weights of a tile
+constexpr uint32_t kRowBytes = 128;    // of either operand in one stage
+constexpr uint32_t kWeights = kRows * kRowBytes;
+constexpr int kThreads = 192;          // loads, MMAs, 4 warps for the sums
+constexpr int kMaxSplit = 8;
+
+template <bool FP8, int NT>
+struct Shape {
+  static constexpr int kParts = FP8 ? 1 : 2;  // weight tiles of a stage
+  static constexpr uint32_t kStage = kParts * kWeights + NT * kRowBytes;
+  static constexpr uint32_t kBudget = NT <= 32 ? 108 * 1024 : 200 * 1024;
+  static constexpr int kStages = kBudget / kStage < 6 ? kBudget / kStage : 6;
+  static constexpr int kBufs = FP8 ? 4 : 1;  // accumulators of kParts * NT columns
+  static constexpr int kColumns = kBufs * kParts * NT < 32 ? 32 : kBufs * kParts * NT;
+  static constexpr uint32_t kSums = kParts * NT * kRows * 4;
+  static constexpr size_t kSmem = 1024 + (kStages * kStage > kSums ? kStages * kStage : kSums);
+};
+
+struct Params {
+  CUtensorMap w[2], x;
+  int tokens, features, steps, step_elems;
+  // gated
+  uint16_t* out;
+  int64_t ldo;
+  uint8_t *g8, *u8;
+  float *gs, *us;
+  // 8-bit
+  const float *sx, *sw;
+  int* err;
+  uint64_t limit_ns, stall_ns;
+};
+
+__device__ __forceinline__ float4 peer_read(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+  return v;
+}
+
+// Sum of the cluster's CTAs' sums at this address, in rank order.
+__device__ __forceinline__ float4 cluster_sum(uint32_t addr, int split) {
+  float4 v = peer_read(peer_addr(addr, 0));
+  for (int r = 1; r < split; ++r) {
+    const float4 o = peer_read(peer_addr(addr, r));
+    v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+  }
+  return v;
+}
+
+__device__ __forceinline__ void sums_barrier() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+// 4 codes a lane, one scale a warp: this lane's part of a token's block.
+__device__ __forceinline__ void put_block(const float4& v, uint8_t* codes, float* scale, int lane, bool in) {
+  float amax = fmaxf(fmaxf(finite_abs(v.x), finite_abs(v.y)), fmaxf(finite_abs(v.z), finite_abs(v.w)));
+#pragma unroll
+  for (int d = 16; d; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+  const uint32_t e = scale_exponent(amax);
+  const float inv = exponent_inverse(e);
+  if (in) *(uint32_t*)codes = pack_e4m3x4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+  if (lane == 0) *scale = exponent_value(e);
+}
+
+template <bool FP8, int NT, int ACT>
+__global__ void __launch_bounds__(kThreads) few_tc_kernel(const __grid_constant__ Params p) {
+  using S = Shape<FP8, NT>;
+  constexpr uint32_t kInstr = instr_desc(FP8 ? 0 : 1, 0, 0, kRows, NT);
+  extern __shared__ uint8_t raw[];
+  __shared__ uint64_t bars[2 * S::kStages + 2 * S::kBufs + 1];
+  __shared__ __align__(16) float scales[4][FP8 ? NT : 4];
+  __shared__ uint32_t tmem_at;
+  __shared__ int stop;
+
+  const uint32_t smem = (smem_addr(raw) + 1023u) & ~1023u;
+  const uint32_t bar0 = smem_addr(bars);
+  const auto full = [&](int s) { return bar0 + 8u * s; };
+  const auto empty = [&](int s) { return bar0 + 8u * (S::kStages + s); };
+  const auto sums_full = [&](int b) { return bar0 + 8u * (2 * S::kStages + b); };
+  const auto sums_empty = [&](int b) { return bar0 + 8u * (2 * S::kStages + S::kBufs + b); };
+  const uint32_t spare = bar0 + 8u * (2 * S::kStages + 2 * S::kBufs);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int split = gridDim.x, rank = blockIdx.x;  // the cluster is a row of the grid
+  const int token0 = blockIdx.y * NT, feature0 = blockIdx.z * kRows;
+  const int k0 = (int)((int64_t)p.steps * rank / split), k1 = (int)((int64_t)p.steps * (rank + 1) / split);
+  const Watch watch{&stop, p.err, p.limit_ns};
+
+  if (threadIdx.x == 0) {
+    stop = 0;
+    for (int s = 0; s < S::kStages; ++s) bar_init(full(s), 1), bar_init(empty(s), 1);
+    for (int b = 0; b < S::kBufs; ++b) bar_init(sums_full(b), 1), bar_init(sums_empty(b), 4);
+    bar_init(spare, 1);
+    bar_init_fence();
+  }
+  if (warp == 1) tmem_alloc<1>(smem_addr(&tmem_at), S::kColumns);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = tmem_at;
+  bool done = false;  // this warp has its sums in shared memory
+
+  if (p.stall_ns) {  // test: a wait on a barrier nothing arrives on runs out
+    if (threadIdx.x == 0) bar_wait(spare, 0, Watch{&stop, p.err, p.stall_ns});
+  } else if (warp == 0) {
+    if (lane == 0) {
+      bool go = true;
+      int j = 0;
+      for (int k = k0; k < k1; ++k, ++j) {
+        const int s = j % S::kStages;
+        if (j >= S::kStages && !bar_wait(empty(s), (j / S::kStages + 1) & 1, watch)) {
+          go = false;
+          break;
+        }
+        const uint32_t at = smem + s * S::kStage;
+        bar_expect(full(s), S::kStage);
+#pragma unroll
+        for (int i = 0; i < S::kParts; ++i) load_box<false>(at + i * kWeights, &p.w[i], k * p.step_elems, feature0, full(s));
+        load_box<false>(at + S::kParts * kWeights, &p.x, k * p.step_elems, token0, full(s));
+      }
+      if (!go) {  // copies in flight, with a limit again
+        int never = 0;
+        for (int i = max(0, j - S::kStages); i < j; ++i)
+          bar_wait(full(i % S::kStages), (i / S::kStages) & 1, Watch{&never, p.err, p.limit_ns / 16});
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      bool go = true;
+      int j = 0;
+      for (int k = k0; k < k1; ++k, ++j) {
+        const int s = j % S::kStages, b = j % S::kBufs;
+        if ((FP8 && j >= S::kBufs && !bar_wait(sums_empty(b), (j / S::kBufs + 1) & 1, watch)) ||
+            !bar_wait(full(s), (j / S::kStages) & 1, watch)) {
+          go = false;
+          break;
+        }
+        fence_after();
+        const uint32_t at = smem + s * S::kStage;
+        const uint64_t dx = operand_desc(at + S::kParts * kWeights, 16);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int i = 0; i < S::kParts; ++i)
+            mma<1, FP8>(tmem + (b * S::kParts + i) * NT, operand_desc(at + i * kWeights, 16) + q * 2, dx + q * 2, kInstr,
+                        q > 0 || (!FP8 && j > 0));
+        mma_commit<1>(empty(s));
+        if (FP8 || k + 1 == k1) mma_commit<1>(sums_full(b));
+      }
+      if (!go) {  // the MMAs in flight, with a limit
+        int never = 0;
+        mma_commit<1>(spare);
+        bar_wait(spare, 0, Watch{&never, p.err, p.limit_ns / 16});
+      }
+    }
+  } else {
+    const int lanes = (warp & 3) * 32, feature = lanes + lane;  // TMEM lanes follow the warp's index modulo 4
+    const uint32_t mine = tmem + ((uint32_t)lanes << 16);
+    constexpr int kChunk = NT < 32 ? NT : 32;
+    const auto leave = [&](int row, float v) {
+      asm volatile("st.shared.f32 [%0], %1;" ::"r"(smem + (uint32_t)(row * kRows + feature) * 4), "f"(v) : "memory");
+    };
+    if constexpr (FP8) {
+      const int e = threadIdx.x - 64;  // the token whose scales this thread fetches
+      const float* sx = p.sx + (int64_t)min(token0 + e, p.tokens - 1) * p.steps;
+      const float* sw = p.sw + (int64_t)blockIdx.z * p.steps;
+      float sum[NT];
+#pragma unroll
+      for (int i = 0; i < NT; ++i) sum[i] = 0.0f;
+      float next_x = 0.0f, next_w = 0.0f;
+      if (e < NT && k0 < k1) next_x = __ldg(sx + k0), next_w = __ldg(sw + k0);
+      done = true;
+      int j = 0;
+      for (int k = k0; k < k1; ++k, ++j) {
+        const int b = j % S::kBufs;
+        if (e < NT) {
+          scales[j & 3][e] = next_x * next_w;
+          if (k + 1 < k1) next_x = __ldg(sx + k + 1), next_w = __ldg(sw + k + 1);
+        }
+        sums_barrier();
+        // a warp whose wait ran out goes on meeting the others at the barrier
+        done = done && bar_wait_warp(sums_full(b), (j / S::kBufs) & 1, watch);
+        if (!done) continue;
+        fence_after();
+#pragma unroll
+        for (int c = 0; c < NT / kChunk; ++c) {
+          uint32_t v[kChunk];
+          tmem_read(mine + b * NT + c * kChunk, v);
+          if (c == NT / kChunk - 1) {
+            fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(sums_empty(b));
+          }
+#pragma unroll
+          for (int i = 0; i < kChunk; i += 4) {
+            const float4 s = *(const float4*)&scales[j & 3][c * kChunk + i];
+            float* to = sum + c * kChunk + i;
+            to[0] = fmaf(as_f(v[i]), s.x, to[0]);
+            to[1] = fmaf(as_f(v[i + 1]), s.y, to[1]);
+            to[2] = fmaf(as_f(v[i + 2]), s.z, to[2]);
+            to[3] = fmaf(as_f(v[i + 3]), s.w, to[3]);
+          }
+        }
+      }
+      if (done) {
+        // every warp's last read of the stages is over: all MMAs completed
+#pragma unroll
+        for (int i = 0; i < NT; ++i) leave(i, sum[i]);
+      }
+    } else {
+      done = k0 < k1 ? bar_wait_warp(sums_full(0), 0, watch) : true;
+      if (done) {
+        fence_after();
+#pragma unroll 1
+        for (int c = 0; c < 2 * NT / kChunk; ++c) {
+          uint32_t v[kChunk];
+          if (k0 < k1)
+            tmem_read(mine + c * kChunk, v);
+          else
+            for (int i = 0; i < kChunk; ++i) v[i] = 0;
+#pragma unroll
+          for (int i = 0; i < kChunk; ++i) leave(c * kChunk + i, as_f(v[i]));
+        }
+      }
+    }
+  }
+  __syncthreads();
+  cluster_sync();
+  if (warp >= 2 && !p.stall_ns) {
+    const int col = feature0 + lane * 4;
+    const bool in = col < p.features;
+    const int64_t nb = (p.features + kBlock - 1) / kBlock;
+    for (int t = rank * 4 + (warp & 3); t < NT; t += 4 * split) {
+      const int64_t token = token0 + t;
+      if (token >= p.tokens) break;
+      const float4 a = cluster_sum(smem + (uint32_t)(t * kRows + lane * 4) * 4, split);
+      float4 r = a;
+      if constexpr (!FP8) {
+        const float4 u = cluster_sum(smem + (uint32_t)((NT + t) * kRows + lane * 4) * 4, split);
+        r.x = activation<ACT>(a.x) * u.x, r.y = activation<ACT>(a.y) * u.y;
+        r.z = activation<ACT>(a.z) * u.z, r.w = activation<ACT>(a.w) * u.w;
+        if (p.g8) {  // features past the end hold 0
+          put_block(a, p.g8 + token * p.features + col, p.gs + token * nb + blockIdx.z, lane, in);
+          put_block(u, p.u8 + token * p.features + col, p.us + token * nb + blockIdx.z, lane, in);
+        }
+      }
+      if (in) *(uint2*)(p.out + token * p.ldo + col) = make_uint2(pack_bf16(r.x, r.y), pack_bf16(r.z, r.w));
+    }
+  }
+  cluster_sync();  // the others have read this CTA's sums
+  if (warp == 1) tmem_free<1>(tmem, S::kColumns);
+}
+
+template <bool FP8, int NT, int ACT>
+cudaError_t launch(Params& p, int split, const TcLaunch& l, cudaStream_t stream) {
+  using S = Shape<FP8, NT>;
+  static const cudaError_t ready =
+      cudaFuncSetAttribute(few_tc_kernel<FP8, NT, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
+  if (ready != cudaSuccess) return ready;
+  p.err = l.err;
+  p.limit_ns = TIDE_BULK_TIMEOUT_NS;
+  p.stall_ns = l.stall_ns;
+  cudaLaunchAttribute cluster;
+  cluster.id = cudaLaunchAttributeClusterDimension;
+  cluster.val.clusterDim = {(unsigned)split, 1, 1};
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3(split, (unsigned)ceil_div(p.tokens, NT), (unsigned)ceil_div(p.features, kRows));
+  c.blockDim = dim3(kThreads);
+  c.dynamicSmemBytes = S::kSmem;
+  c.stream = stream;
+  c.attrs = &cluster;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, few_tc_kernel<FP8, NT, ACT>, p);
+}
+
+int tile_of(int64_t tokens) { return tokens <= 16 ? 16 : tokens <= 32 ? 32 : tokens <= 64 ? 64 : 128; }
+
+// CTAs that share a tile's contraction: enough to give every SM one, each
+// with at least two stages of it.
+int split_of(int64_t tiles, int64_t steps, int sms) {
+  int s = 1;
+  while (s < kMaxSplit && tiles * s < sms && steps >= 4 * s) s *= 2;
+  return s;
+}
+
+// Few tokens: up to one tile of 128; above that, while the 256-row tiles of
+// the other kernels would leave over half of the SMs without work.
+bool few(int64_t tokens, int64_t features, int64_t tile_features, int pairs) {
+  if (ceil_div(features, kRows) > 65535) return false;
+  return tokens <= 128 || 2 * ceil_div(tokens, 256) * ceil_div(features, tile_features) <= pairs;
+}
+
+template <int ACT>
+cudaError_t gated(Params& p, int nt, int split, const TcLaunch& l, cudaStream_t stream) {
+  return nt == 16   ? launch<false, 16, ACT>(p, split, l, stream)
+         : nt == 32 ? launch<false, 32, ACT>(p, split, l, stream)
+         : nt == 64 ? launch<false, 64, ACT>(p, split, l, stream)
+                    : launch<false, 128, ACT>(p, split, l, stream);
+}
+
+}  // namespace
+
+bool gated_few_takes(const GatedArgs& a, int pairs) { return few(a.tokens, a.ffn, 128, pairs); }
+bool fp8_few_takes(const MatmulArgs& a, int pairs) { return few(a.m, a.n, 256, pairs); }
+
+cudaError_t launch_gated_forward_few(const GatedArgs& a, const TcLaunch& l, cudaStream_t stream) {
+  constexpr int kElems = kRowBytes / 2;
+  const int nt = tile_of(a.tokens);
+  Params p{};
+  p.tokens = (int)a.tokens, p.features = (int)a.ffn;
+  p.steps = (int)ceil_div(a.hidden, kElems), p.step_elems = kElems;
+  p.out = a.h, p.ldo = a.ldh;
+  p.g8 = a.g8, p.gs = a.gs, p.u8 = a.u8, p.us = a.us;
+  if (!make_map(&p.w[0], a.wg, 2, a.hidden, a.ffn, a.hidden, kElems, kRows, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_map(&p.w[1], a.wu, 2, a.hidden, a.ffn, a.hidden, kElems, kRows, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_map(&p.x, a.x, 2, a.hidden, a.tokens, a.ldx, kElems, nt, CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  const int split = split_of(ceil_div(a.ffn, kRows) * ceil_div(a.tokens, nt), p.steps, l.sms);
+  return a.act == TIDE_ACT_SILU ? gated<TIDE_ACT_SILU>(p, nt, split, l, stream)
+                                : gated<TIDE_ACT_GELU>(p, nt, split, l, stream);
+}
+
+cudaError_t launch_fp8_matmul_few(const MatmulArgs& a, const TcLaunch& l, cudaStream_t stream) {
+  const int nt = tile_of(a.m);
+  Params p{};
+  p.tokens = (int)a.m, p.features = (int)a.n;
+  p.steps = (int)ceil_div(a.k, kRowBytes), p.step_elems = kRowBytes;
+  p.out = a.out, p.ldo = a.ldo;
+  p.sx = a.sa, p.sw = a.sb;
+  if (!make_map(&p.w[0], a.b, 1, a.k, a.n, a.k, kRowBytes, kRows, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_map(&p.x, a.a, 1, a.k, a.m, a.k, kRowBytes, nt, CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  const int split = split_of(ceil_div(a.n, kRows) * ceil_div(a.m, nt), p.steps, l.sms);
+  return nt == 16   ? launch<true, 16, 0>(p, split, l, stream)
+         : nt == 32 ? launch<true, 32, 0>(p, split, l, stream)
+         : nt == 64 ? launch<true, 64, 0>(p, split, l, stream)
+                    : launch<true, 128, 0>(p, split, l, stream);
+}
+
+}  // namespace tide

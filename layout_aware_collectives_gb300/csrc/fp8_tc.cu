@@ -45,6 +45,12 @@ __device__ __forceinline__ void fma2(uint64_t& c, uint32_t a, uint32_t b, uint64
   asm("{ .reg .b64 v; mov.b64 v, {%1, %2}; fma.rn.f32x2 %0, v, %3, %0; }" : "+l"(c) : "r"(a), "r"(b), "l"(w));
 }
 
+template <int C>
+__device__ __forceinline__ void add32(uint64_t (&sum)[kHalf / 2], const uint32_t (&v)[32], uint64_t s) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) fma2(sum[C * 16 + i], v[2 * i], v[2 * i + 1], s);
+}
+
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) fp8_tc_kernel(const __grid_constant__ Params p) {
   constexpr uint32_t kInstr = instr_desc(0, 0, 0, 256, 256);
   extern __shared__ uint8_t raw[];
@@ -167,21 +173,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) fp8_tc_
           break;
         }
         fence_after();
-#pragma unroll
-        for (int c = 0; c < kHalf / 64; ++c) {
-          uint32_t v[32], x[32];
-          tmem_read32x2(taddr + b * 256 + c * 64, taddr + b * 256 + c * 64 + 32, v, x);
-          if (c == kHalf / 64 - 1) {
-            fence_before();
-            __syncwarp();
-            if (lane == 0) bar_arrive_peer(peer_addr(sums_empty(b), 0));
-          }
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            fma2(sum[c * 32 + i], v[2 * i], v[2 * i + 1], s);
-            fma2(sum[c * 32 + 16 + i], x[2 * i], x[2 * i + 1], s);
-          }
-        }
+        // Each half of the sums is on its way while the other is added.
+        uint32_t v[32], x[32];
+        const uint32_t from = taddr + b * 256;
+        tmem_issue32(from, v);
+        tmem_issue32(from + 32, x);
+        tmem_arrived(v, x);
+        add32<0>(sum, v, s);
+        tmem_issue32(from + 64, v);
+        add32<1>(sum, x, s);
+        tmem_issue32(from + 96, x);
+        tmem_arrived(v, x);
+        fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive_peer(peer_addr(sums_empty(b), 0));
+        add32<2>(sum, v, s);
+        add32<3>(sum, x, s);
       }
       if (!go) break;
 #pragma unroll

@@ -145,7 +145,7 @@ __device__ __forceinline__ void epilogue(const Params& p, const TileAt& t, uint3
       const int col = t.n * 2 * kHalf + c * 32;
       if (!any || col >= p.cols) break;
       uint32_t v[32], o[16];
-      tmem_read32(tmem + c * 32, v);
+      tmem_read(tmem + c * 32, v);
 #pragma unroll
       for (int i = 0; i < 16; ++i) o[i] = pack_bf16(as_f(v[2 * i]), as_f(v[2 * i + 1]));
       out.put(map, o, col, row0);

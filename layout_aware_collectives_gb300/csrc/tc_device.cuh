@@ -200,8 +200,8 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
                       "=r"(v[i + 6]), "=r"(v[i + 7])
 #define TIDE_R32(v) TIDE_R8(v, 0), TIDE_R8(v, 8), TIDE_R8(v, 16), TIDE_R8(v, 24)
 
-// 32 columns of this warp's 32 TMEM lanes, one lane a thread; waits for them.
-__device__ __forceinline__ void tmem_read32(uint32_t addr, uint32_t (&v)[32]) {
+// 32 (or 16) columns of this warp's 32 TMEM lanes, one lane a thread; waits for them.
+__device__ __forceinline__ void tmem_read(uint32_t addr, uint32_t (&v)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
       "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
@@ -210,6 +210,34 @@ __device__ __forceinline__ void tmem_read32(uint32_t addr, uint32_t (&v)[32]) {
       : "r"(addr)
       : "memory");
 }
+__device__ __forceinline__ void tmem_read(uint32_t addr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : TIDE_R8(v, 0), TIDE_R8(v, 8)
+      : "r"(addr)
+      : "memory");
+}
+// The same without the wait: `v` may be used after tmem_arrived(v).
+__device__ __forceinline__ void tmem_issue32(uint32_t addr, uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : TIDE_R32(v)
+      : "r"(addr)
+      : "memory");
+}
+#define TIDE_RW8(v, i) "+r"(v[i]), "+r"(v[i + 1]), "+r"(v[i + 2]), "+r"(v[i + 3]), "+r"(v[i + 4]), "+r"(v[i + 5]), \
+                       "+r"(v[i + 6]), "+r"(v[i + 7])
+#define TIDE_RW32(v) TIDE_RW8(v, 0), TIDE_RW8(v, 8), TIDE_RW8(v, 16), TIDE_RW8(v, 24)
+// Waits for every read issued so far; no use of v moves ahead of it.
+__device__ __forceinline__ void tmem_arrived(uint32_t (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : TIDE_RW32(v)::"memory");
+}
+__device__ __forceinline__ void tmem_arrived(uint32_t (&v)[32], uint32_t (&w)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : TIDE_RW32(v), TIDE_RW32(w)::"memory");
+}
+
 // The same for two runs of 32 columns.
 __device__ __forceinline__ void tmem_read32x2(uint32_t a0, uint32_t a1, uint32_t (&v)[32], uint32_t (&w)[32]) {
   asm volatile(

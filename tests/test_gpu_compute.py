@@ -129,7 +129,8 @@ def test_restore(compute, rows, cols, block_rows, pad):
 # ------------------------------------------------------------------ products
 
 MATMUL_SHAPES = [(1, 128, 128), (1, 8, 16), (2, 264, 400), (3, 1, 1), (7, 130, 129), (37, 768, 2048), (129, 264, 1040),
-                 (250, 704, 256), (300, 520, 144), (33, 100, 300), (513, 1024, 4096)]
+                 (250, 704, 256), (300, 520, 144), (33, 100, 300), (513, 1024, 4096),
+                 (300, 5000, 272), (64, 136, 8192), (70, 1160, 1296)]
 
 
 def fp8(g, rows, cols, block_rows, scale=1.0):
@@ -173,7 +174,8 @@ def test_matmul_nan_stays_in_its_row_and_column(compute):
 # tokens, hidden, ffn: one token, single columns, ragged and unaligned sizes,
 # several tiles each way
 GATED_SHAPES = [(1, 256, 704), (1, 8, 8), (3, 1, 1), (5, 250, 130), (16, 128, 128), (17, 264, 136), (37, 2048, 768),
-                (129, 72, 1000), (250, 256, 704), (300, 1032, 264), (513, 512, 1408)]
+                (129, 72, 1000), (250, 256, 704), (300, 1032, 264), (513, 512, 1408),
+                (300, 136, 2568), (20, 4104, 256), (50, 1000, 1400)]
 
 
 def checkpoint(tokens, hidden, ffn, with_x):
