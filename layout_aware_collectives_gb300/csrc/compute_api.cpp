@@ -209,7 +209,7 @@ tide_status_t tide_fp8_matmul(tide_compute_t c, int64_t m, int64_t n, int64_t k,
   const MatmulArgs args{m, n, k, a, a_scales, b, b_scales, out, ld_out};
   if (k % 16 == 0 && n % 8 == 0 && ld_out % 8 == 0) {
     const TcLaunch l = launch_of(c);
-    return launched(fp8_few_takes(args, l.pairs) ? launch_fp8_matmul_few(args, l, stream)
+    return launched(fp8_few_takes(args, l.sms) ? launch_fp8_matmul_few(args, l, stream)
                                                  : launch_fp8_matmul_tc(args, l, stream),
                     "tide_fp8_matmul");
   }
@@ -239,7 +239,7 @@ tide_status_t tide_gated_forward(tide_compute_t c, int64_t tokens, int64_t hidde
   if (ffn == 0) return TIDE_OK;
   if (gated_tc_takes(a) && ld_x % 8 == 0 && ld_h % 8 == 0) {
     const TcLaunch l = launch_of(c);
-    return launched(gated_few_takes(a, l.pairs) ? launch_gated_forward_few(a, l, stream)
+    return launched(gated_few_takes(a, l.sms) ? launch_gated_forward_few(a, l, stream)
                                                 : launch_gated_forward_tc(a, l, stream),
                     "tide_gated_forward");
   }

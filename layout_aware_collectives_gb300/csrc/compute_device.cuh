@@ -37,16 +37,13 @@ __device__ __forceinline__ float exponent_value(uint32_t e) { return __uint_as_f
 // 1 / 2^(e - 127), exact: e is within [1, 247].
 __device__ __forceinline__ float exponent_inverse(uint32_t e) { return __uint_as_float((254u - e) << 23); }
 
-// |v| where v is finite, else 0.
-__device__ __forceinline__ float finite_abs(float v) {
-  const float a = fabsf(v);
-  return a < CUDART_INF_F ? a : 0.0f;  // false for infinities and NaN
-}
+// A block's largest magnitude is taken with fmaxf, which passes over NaN.  If
+// it is infinite, infinities are made NaN (which is what their codes are)
+// and the maximum is taken again: so finite blocks pay for no checks.
+__device__ __forceinline__ float no_infinity(float v) { return fabsf(v) < CUDART_INF_F ? v : CUDART_NAN_F; }
 
-// Two scaled values to e4m3, to nearest even, infinities and NaN to NaN.
+// Two scaled values to e4m3, to nearest even, NaN to NaN.
 __device__ __forceinline__ uint16_t pack_e4m3(float lo, float hi) {
-  lo = fabsf(lo) < CUDART_INF_F ? lo : CUDART_NAN_F;
-  hi = fabsf(hi) < CUDART_INF_F ? hi : CUDART_NAN_F;
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;

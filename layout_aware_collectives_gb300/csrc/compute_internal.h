@@ -98,8 +98,8 @@ cudaError_t launch_gated_dw_tc(const GatedArgs& a, const TcLaunch& l, cudaStream
 cudaError_t launch_fp8_matmul_tc(const MatmulArgs& a, const TcLaunch& l, cudaStream_t stream);
 
 // The same two products for few tokens (few_tc.cu).
-bool gated_few_takes(const GatedArgs& a, int pairs);
-bool fp8_few_takes(const MatmulArgs& a, int pairs);
+bool gated_few_takes(const GatedArgs& a, int sms);
+bool fp8_few_takes(const MatmulArgs& a, int sms);
 cudaError_t launch_gated_forward_few(const GatedArgs& a, const TcLaunch& l, cudaStream_t stream);
 cudaError_t launch_fp8_matmul_few(const MatmulArgs& a, const TcLaunch& l, cudaStream_t stream);
 

@@ -26,7 +26,6 @@ constexpr int kRows = 128;             // weights of a tile
 constexpr uint32_t kRowBytes = 128;    // of either operand in one stage
 constexpr uint32_t kWeights = kRows * kRowBytes;
 constexpr int kThreads = 192;          // loads, MMAs, 4 warps for the sums
-constexpr int kMaxSplit = 8;
 
 template <bool FP8, int NT>
 struct Shape {
@@ -60,23 +59,44 @@ __device__ __forceinline__ float4 peer_read(uint32_t addr) {
   return v;
 }
 
-// Sum of the cluster's CTAs' sums at this address, in rank order.
-__device__ __forceinline__ float4 cluster_sum(uint32_t addr, int split) {
-  float4 v = peer_read(peer_addr(addr, 0));
-  for (int r = 1; r < split; ++r) {
-    const float4 o = peer_read(peer_addr(addr, r));
-    v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+// Sums of the cluster's CTAs' sums at N addresses, in rank order.  The reads
+// of two ranks are on their way before the first is added.
+template <int N>
+__device__ __forceinline__ void cluster_sums(const uint32_t (&addr)[N], int split, float4 (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int r = 0; r < split; r += 2) {
+    float4 a[N], b[N];
+    const bool two = r + 1 < split;
+#pragma unroll
+    for (int i = 0; i < N; ++i) a[i] = peer_read(peer_addr(addr[i], r));
+    if (two)
+#pragma unroll
+      for (int i = 0; i < N; ++i) b[i] = peer_read(peer_addr(addr[i], r + 1));
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i].x += a[i].x, v[i].y += a[i].y, v[i].z += a[i].z, v[i].w += a[i].w;
+    if (two)
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i].x += b[i].x, v[i].y += b[i].y, v[i].z += b[i].z, v[i].w += b[i].w;
   }
-  return v;
 }
 
 __device__ __forceinline__ void sums_barrier() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
-// 4 codes a lane, one scale a warp: this lane's part of a token's block.
-__device__ __forceinline__ void put_block(const float4& v, uint8_t* codes, float* scale, int lane, bool in) {
-  float amax = fmaxf(fmaxf(finite_abs(v.x), finite_abs(v.y)), fmaxf(finite_abs(v.z), finite_abs(v.w)));
+__device__ __forceinline__ float warp_amax(const float4& v) {
+  float m = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
 #pragma unroll
-  for (int d = 16; d; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+  for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  return m;
+}
+
+// 4 codes a lane, one scale a warp: this lane's part of a token's block.
+__device__ __forceinline__ void put_block(float4 v, uint8_t* codes, float* scale, int lane, bool in) {
+  float amax = warp_amax(v);
+  if (amax == CUDART_INF_F) {
+    v = make_float4(no_infinity(v.x), no_infinity(v.y), no_infinity(v.z), no_infinity(v.w));
+    amax = warp_amax(v);
+  }
   const uint32_t e = scale_exponent(amax);
   const float inv = exponent_inverse(e);
   if (in) *(uint32_t*)codes = pack_e4m3x4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
@@ -246,17 +266,22 @@ __global__ void __launch_bounds__(kThreads) few_tc_kernel(const __grid_constant_
   }
   __syncthreads();
   cluster_sync();
-  if (warp >= 2 && !p.stall_ns) {
+  if (!p.stall_ns) {
+    constexpr int kWarps = kThreads / 32;
     const int col = feature0 + lane * 4;
     const bool in = col < p.features;
     const int64_t nb = (p.features + kBlock - 1) / kBlock;
-    for (int t = rank * 4 + (warp & 3); t < NT; t += 4 * split) {
+    const int live = min(NT, p.tokens - token0);
+    for (int t = rank * kWarps + warp; t < live; t += kWarps * split) {
       const int64_t token = token0 + t;
-      if (token >= p.tokens) break;
-      const float4 a = cluster_sum(smem + (uint32_t)(t * kRows + lane * 4) * 4, split);
-      float4 r = a;
+      uint32_t addr[S::kParts];
+      float4 v[S::kParts];
+#pragma unroll
+      for (int q = 0; q < S::kParts; ++q) addr[q] = smem + (uint32_t)((q * NT + t) * kRows + lane * 4) * 4;
+      cluster_sums(addr, split, v);
+      float4 r = v[0];
       if constexpr (!FP8) {
-        const float4 u = cluster_sum(smem + (uint32_t)((NT + t) * kRows + lane * 4) * 4, split);
+        const float4 a = v[0], u = v[1];
         r.x = activation<ACT>(a.x) * u.x, r.y = activation<ACT>(a.y) * u.y;
         r.z = activation<ACT>(a.z) * u.z, r.w = activation<ACT>(a.w) * u.w;
         if (p.g8) {  // features past the end hold 0
@@ -271,8 +296,43 @@ __global__ void __launch_bounds__(kThreads) few_tc_kernel(const __grid_constant_
   if (warp == 1) tmem_free<1>(tmem, S::kColumns);
 }
 
+// Clusters of `split` CTAs that the device holds at one time; a cluster lies
+// within one GPC, so these are fewer than SMs / split.
 template <bool FP8, int NT, int ACT>
-cudaError_t launch(Params& p, int split, const TcLaunch& l, cudaStream_t stream) {
+int clusters_of(int split) {
+  using S = Shape<FP8, NT>;
+  cudaLaunchAttribute cluster;
+  cluster.id = cudaLaunchAttributeClusterDimension;
+  cluster.val.clusterDim = {(unsigned)split, 1, 1};
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3(split);
+  c.blockDim = dim3(kThreads);
+  c.dynamicSmemBytes = S::kSmem;
+  c.attrs = &cluster;
+  c.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, few_tc_kernel<FP8, NT, ACT>, &c) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  return n;
+}
+
+// CTAs that share a tile's contraction: up to one for each SM, all at work at
+// one time, each with at least two stages of it.  (One tile for each of 112
+// SMs streams 4096 x 14336 weights in 44 us, split in two 45.5; 16 tiles of
+// 64 tokens take 13.4 us split in four, 20.5 split in eight, where the last
+// clusters wait for the first.)
+template <bool FP8, int NT, int ACT>
+int split_of(int64_t tiles, int64_t steps, int sms) {
+  static const int held[3] = {clusters_of<FP8, NT, ACT>(2), clusters_of<FP8, NT, ACT>(4), clusters_of<FP8, NT, ACT>(8)};
+  int s = 1;
+  for (int i = 0; i < 3 && 2 * s * tiles <= sms && tiles <= held[i] && steps >= 4 * s; ++i) s *= 2;
+  return s;
+}
+
+template <bool FP8, int NT, int ACT>
+cudaError_t launch(Params& p, const TcLaunch& l, cudaStream_t stream) {
   using S = Shape<FP8, NT>;
   static const cudaError_t ready =
       cudaFuncSetAttribute(few_tc_kernel<FP8, NT, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
@@ -280,11 +340,13 @@ cudaError_t launch(Params& p, int split, const TcLaunch& l, cudaStream_t stream)
   p.err = l.err;
   p.limit_ns = TIDE_BULK_TIMEOUT_NS;
   p.stall_ns = l.stall_ns;
+  const int64_t tiles_t = ceil_div(p.tokens, NT), tiles_f = ceil_div(p.features, kRows);
+  const int split = split_of<FP8, NT, ACT>(tiles_t * tiles_f, p.steps, l.sms);
   cudaLaunchAttribute cluster;
   cluster.id = cudaLaunchAttributeClusterDimension;
   cluster.val.clusterDim = {(unsigned)split, 1, 1};
   cudaLaunchConfig_t c{};
-  c.gridDim = dim3(split, (unsigned)ceil_div(p.tokens, NT), (unsigned)ceil_div(p.features, kRows));
+  c.gridDim = dim3(split, (unsigned)tiles_t, (unsigned)tiles_f);
   c.blockDim = dim3(kThreads);
   c.dynamicSmemBytes = S::kSmem;
   c.stream = stream;
@@ -293,35 +355,30 @@ cudaError_t launch(Params& p, int split, const TcLaunch& l, cudaStream_t stream)
   return cudaLaunchKernelEx(&c, few_tc_kernel<FP8, NT, ACT>, p);
 }
 
-int tile_of(int64_t tokens) { return tokens <= 16 ? 16 : tokens <= 32 ? 32 : tokens <= 64 ? 64 : 128; }
+int tile_of(int64_t tokens) { return tokens <= 16 ? 16 : tokens <= 32 ? 32 : 64; }
 
-// CTAs that share a tile's contraction: enough to give every SM one, each
-// with at least two stages of it.
-int split_of(int64_t tiles, int64_t steps, int sms) {
-  int s = 1;
-  while (s < kMaxSplit && tiles * s < sms && steps >= 4 * s) s *= 2;
-  return s;
-}
-
-// Few tokens: up to one tile of 128; above that, while the 256-row tiles of
-// the other kernels would leave over half of the SMs without work.
-bool few(int64_t tokens, int64_t features, int64_t tile_features, int pairs) {
-  if (ceil_div(features, kRows) > 65535) return false;
-  return tokens <= 128 || 2 * ceil_div(tokens, 256) * ceil_div(features, tile_features) <= pairs;
+// One tile of tokens, or so few tiles in all that the 256-token tiles of the
+// other kernels would leave most SMs without work.
+bool few(int64_t tokens, int64_t features, int64_t most) {
+  const int64_t tiles = ceil_div(features, kRows);
+  return tiles <= 65535 && (tokens <= 64 || tiles * ceil_div(tokens, 64) <= most);
 }
 
 template <int ACT>
-cudaError_t gated(Params& p, int nt, int split, const TcLaunch& l, cudaStream_t stream) {
-  return nt == 16   ? launch<false, 16, ACT>(p, split, l, stream)
-         : nt == 32 ? launch<false, 32, ACT>(p, split, l, stream)
-         : nt == 64 ? launch<false, 64, ACT>(p, split, l, stream)
-                    : launch<false, 128, ACT>(p, split, l, stream);
+cudaError_t gated(Params& p, int nt, const TcLaunch& l, cudaStream_t stream) {
+  return nt == 16   ? launch<false, 16, ACT>(p, l, stream)
+         : nt == 32 ? launch<false, 32, ACT>(p, l, stream)
+                    : launch<false, 64, ACT>(p, l, stream);
 }
 
 }  // namespace
 
-bool gated_few_takes(const GatedArgs& a, int pairs) { return few(a.tokens, a.ffn, 128, pairs); }
-bool fp8_few_takes(const MatmulArgs& a, int pairs) { return few(a.m, a.n, 256, pairs); }
+// Past 64 tokens the 256-row tiles read fewer operand bytes: they are ahead
+// for the gated block from about half as many of these tiles as SMs (1021 x
+// 2048 x 768, 96 tiles: 14.8 us against 19.6), for the 8-bit product, whose
+// large tiles are slower each, from as many as SMs.
+bool gated_few_takes(const GatedArgs& a, int sms) { return few(a.tokens, a.ffn, sms / 2); }
+bool fp8_few_takes(const MatmulArgs& a, int sms) { return few(a.m, a.n, sms); }
 
 cudaError_t launch_gated_forward_few(const GatedArgs& a, const TcLaunch& l, cudaStream_t stream) {
   constexpr int kElems = kRowBytes / 2;
@@ -335,9 +392,8 @@ cudaError_t launch_gated_forward_few(const GatedArgs& a, const TcLaunch& l, cuda
       !make_map(&p.w[1], a.wu, 2, a.hidden, a.ffn, a.hidden, kElems, kRows, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_map(&p.x, a.x, 2, a.hidden, a.tokens, a.ldx, kElems, nt, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
-  const int split = split_of(ceil_div(a.ffn, kRows) * ceil_div(a.tokens, nt), p.steps, l.sms);
-  return a.act == TIDE_ACT_SILU ? gated<TIDE_ACT_SILU>(p, nt, split, l, stream)
-                                : gated<TIDE_ACT_GELU>(p, nt, split, l, stream);
+  return a.act == TIDE_ACT_SILU ? gated<TIDE_ACT_SILU>(p, nt, l, stream)
+                                : gated<TIDE_ACT_GELU>(p, nt, l, stream);
 }
 
 cudaError_t launch_fp8_matmul_few(const MatmulArgs& a, const TcLaunch& l, cudaStream_t stream) {
@@ -350,11 +406,9 @@ cudaError_t launch_fp8_matmul_few(const MatmulArgs& a, const TcLaunch& l, cudaSt
   if (!make_map(&p.w[0], a.b, 1, a.k, a.n, a.k, kRowBytes, kRows, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_map(&p.x, a.a, 1, a.k, a.m, a.k, kRowBytes, nt, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
-  const int split = split_of(ceil_div(a.n, kRows) * ceil_div(a.m, nt), p.steps, l.sms);
-  return nt == 16   ? launch<true, 16, 0>(p, split, l, stream)
-         : nt == 32 ? launch<true, 32, 0>(p, split, l, stream)
-         : nt == 64 ? launch<true, 64, 0>(p, split, l, stream)
-                    : launch<true, 128, 0>(p, split, l, stream);
+  return nt == 16   ? launch<true, 16, 0>(p, l, stream)
+         : nt == 32 ? launch<true, 32, 0>(p, l, stream)
+                    : launch<true, 64, 0>(p, l, stream);
 }
 
 }  // namespace tide

@@ -8,63 +8,107 @@ namespace tide {
 namespace {
 
 constexpr int kThreads = 256;
+// Up to here indexes are 32-bit (no grid overshoots it by 2^30), whose
+// divisions are a third of the 64-bit ones' instructions.
+constexpr int64_t kSmall = (int64_t)3 << 30;
 
 // ------------------------------------------------------------------ store
+
+// Magnitudes of packed bf16 are ordered as 16-bit whole numbers, infinity at
+// 0x7f80 and NaN above: two elements a comparison.
+constexpr uint32_t kInf16 = 0x7f80;
+
+template <int N>
+__device__ __forceinline__ uint32_t packed_max(const uint32_t (&v)[N]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) m = __vmaxu2(m, v[i] & 0x7fff7fffu);
+  return m;
+}
+// The same without infinities and NaN.
+template <int N>
+__device__ __forceinline__ uint32_t packed_max_finite(const uint32_t (&v)[N]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const uint32_t lo = v[i] & 0x7fffu, hi = (v[i] >> 16) & 0x7fffu;
+    m = __vmaxu2(m, (lo < kInf16 ? lo : 0) | ((hi < kInf16 ? hi : 0) << 16));
+  }
+  return m;
+}
+__device__ __forceinline__ uint32_t fold(uint32_t m) { return max(m & 0xffffu, m >> 16); }
+
+// 8 packed bf16 to 8 codes.
+template <bool CLEAN>
+__device__ __forceinline__ uint2 codes8(const uint32_t (&w)[4], float inv) {
+  float f[8];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    f[2 * j] = bf16_lo(w[j]);
+    f[2 * j + 1] = bf16_hi(w[j]);
+  }
+  if (!CLEAN)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = no_infinity(f[j]);
+  return make_uint2(pack_e4m3x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv),
+                    pack_e4m3x4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv));
+}
 
 // One scale for each 1 x 128: half a warp takes a block, 8 columns (16
 // bytes) a lane, so the block's maximum is four shuffles and nothing is read
 // twice.  U blocks are loaded before the first is reduced.
-template <int U>
-__global__ void __launch_bounds__(kThreads) store_rows_kernel(Fp8Args a, int64_t blocks_per_row, int64_t blocks) {
+template <int U, class Index>
+__global__ void __launch_bounds__(kThreads) store_rows_kernel(Fp8Args a, Index blocks_per_row, Index blocks) {
   const int lane = threadIdx.x & 15;
-  const int64_t group = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 4;
-  uint4 v[U];
+  const Index group = (Index)blockIdx.x * (U * kThreads / 16) + (threadIdx.x >> 4);
+  uint32_t v[U][4];
   int64_t row[U], col[U];
 #pragma unroll
   for (int i = 0; i < U; ++i) {
-    const int64_t blk = group + (int64_t)i * gridDim.x * (kThreads / 16);
-    row[i] = blk < blocks ? blk / blocks_per_row : -1;
-    col[i] = (blk - row[i] * blocks_per_row) * kBlock + lane * 8;
-    v[i] = make_uint4(0, 0, 0, 0);
-    if (row[i] >= 0 && col[i] < a.cols) v[i] = __ldcs((const uint4*)(a.bf16 + row[i] * a.ld + col[i]));
+    const Index blk = group + (Index)(i * (kThreads / 16));
+    const Index r = blk / blocks_per_row;
+    row[i] = blk < blocks ? (int64_t)r : -1;
+    col[i] = (int64_t)(blk - r * blocks_per_row) * kBlock + lane * 8;
+    uint4 q = make_uint4(0, 0, 0, 0);
+    if (row[i] >= 0 && col[i] < a.cols) q = __ldcs((const uint4*)(a.bf16 + row[i] * a.ld + col[i]));
+    v[i][0] = q.x, v[i][1] = q.y, v[i][2] = q.z, v[i][3] = q.w;
   }
 #pragma unroll
   for (int i = 0; i < U; ++i) {
-    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-    float f[8], amax = 0.0f;
+    uint32_t m = packed_max(v[i]);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      f[2 * j] = bf16_lo(w[j]);
-      f[2 * j + 1] = bf16_hi(w[j]);
-      amax = fmaxf(amax, fmaxf(finite_abs(f[2 * j]), finite_abs(f[2 * j + 1])));
+    for (int d = 8; d; d >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, d));
+    m = fold(m);
+    const bool clean = !__any_sync(0xffffffffu, m >= kInf16);
+    if (!clean) {
+      m = packed_max_finite(v[i]);
+#pragma unroll
+      for (int d = 8; d; d >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, d));
+      m = fold(m);
     }
-#pragma unroll
-    for (int d = 8; d; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
-    const uint32_t e = scale_exponent(amax);
+    const uint32_t e = scale_exponent(bf16_lo(m));
     const float inv = exponent_inverse(e);
     if (row[i] < 0) continue;
-    if (col[i] < a.cols) {
-      const uint2 c = make_uint2(pack_e4m3x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv),
-                                 pack_e4m3x4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv));
-      *(uint2*)(a.codes + row[i] * a.cols + col[i]) = c;
-    }
+    if (col[i] < a.cols)
+      *(uint2*)(a.codes + row[i] * a.cols + col[i]) = clean ? codes8<true>(v[i], inv) : codes8<false>(v[i], inv);
     if (lane == 0) a.scales[row[i] * blocks_per_row + col[i] / kBlock] = exponent_value(e);
   }
 }
 
 // The same for rows whose stride or width is no multiple of 8: a warp takes
 // a block, 4 single columns a lane, 32 apart.
-template <int U>
-__global__ void __launch_bounds__(kThreads) store_rows_any_kernel(Fp8Args a, int64_t blocks_per_row, int64_t blocks) {
+template <int U, class Index>
+__global__ void __launch_bounds__(kThreads) store_rows_any_kernel(Fp8Args a, Index blocks_per_row, Index blocks) {
   const int lane = threadIdx.x & 31;
-  const int64_t warp = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5;
+  const Index warp = (Index)blockIdx.x * (U * kThreads / 32) + (threadIdx.x >> 5);
   uint16_t v[U][4];
   int64_t row[U], col[U];
 #pragma unroll
   for (int i = 0; i < U; ++i) {
-    const int64_t blk = warp + (int64_t)i * gridDim.x * (kThreads / 32);
-    row[i] = blk < blocks ? blk / blocks_per_row : -1;
-    col[i] = (blk - row[i] * blocks_per_row) * kBlock + lane;
+    const Index blk = warp + (Index)(i * (kThreads / 32));
+    const Index r = blk / blocks_per_row;
+    row[i] = blk < blocks ? (int64_t)r : -1;
+    col[i] = (int64_t)(blk - r * blocks_per_row) * kBlock + lane;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       v[i][j] = 0;
@@ -73,9 +117,12 @@ __global__ void __launch_bounds__(kThreads) store_rows_any_kernel(Fp8Args a, int
   }
 #pragma unroll
   for (int i = 0; i < U; ++i) {
-    float amax = 0.0f;
+    float f[4], amax = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) amax = fmaxf(amax, finite_abs(bf16_value(v[i][j])));
+    for (int j = 0; j < 4; ++j) {
+      f[j] = no_infinity(bf16_value(v[i][j]));
+      amax = fmaxf(amax, fabsf(f[j]));
+    }
 #pragma unroll
     for (int d = 16; d; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
     const uint32_t e = scale_exponent(amax);
@@ -83,8 +130,7 @@ __global__ void __launch_bounds__(kThreads) store_rows_any_kernel(Fp8Args a, int
     if (row[i] < 0) continue;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      if (col[i] + 32 * j < a.cols)
-        a.codes[row[i] * a.cols + col[i] + 32 * j] = (uint8_t)pack_e4m3(bf16_value(v[i][j]) * inv, 0.0f);
+      if (col[i] + 32 * j < a.cols) a.codes[row[i] * a.cols + col[i] + 32 * j] = (uint8_t)pack_e4m3(f[j] * inv, 0.0f);
     if (lane == 0) a.scales[row[i] * blocks_per_row + col[i] / kBlock] = exponent_value(e);
   }
 }
@@ -93,16 +139,17 @@ __global__ void __launch_bounds__(kThreads) store_rows_any_kernel(Fp8Args a, int
 // (VEC: 8 16-byte vectors a thread; else 64 single columns), so it is read
 // once.
 template <bool VEC>
-__global__ void __launch_bounds__(kThreads) store_square_kernel(Fp8Args a, int64_t blocks_per_row) {
+__global__ void __launch_bounds__(kThreads) store_square_kernel(Fp8Args a, uint32_t blocks_per_row) {
   constexpr int kPerLoad = VEC ? 8 : 1;
   constexpr int kLanes = kBlock / kPerLoad;        // threads across a row
   constexpr int kRows = kThreads / kLanes;         // rows a pass
   constexpr int kPasses = kBlock / kRows;
-  const int64_t br = blockIdx.x / blocks_per_row, bc = blockIdx.x - br * blocks_per_row;
-  const int64_t col = bc * kBlock + (threadIdx.x % kLanes) * kPerLoad;
-  const int64_t row0 = br * kBlock + threadIdx.x / kLanes;
-  uint32_t v[kPasses][VEC ? 4 : 1];
-  float amax = 0.0f;
+  constexpr int kWords = VEC ? 4 : 1;
+  __shared__ uint32_t part[2][kThreads / 32];
+  const uint32_t br = blockIdx.x / blocks_per_row, bc = blockIdx.x - br * blocks_per_row;
+  const int64_t col = (int64_t)bc * kBlock + (threadIdx.x % kLanes) * kPerLoad;
+  const int64_t row0 = (int64_t)br * kBlock + threadIdx.x / kLanes;
+  uint32_t v[kPasses][kWords];
 #pragma unroll
   for (int p = 0; p < kPasses; ++p) {
     const int64_t row = row0 + p * kRows;
@@ -115,34 +162,37 @@ __global__ void __launch_bounds__(kThreads) store_square_kernel(Fp8Args a, int64
       v[p][0] = in ? a.bf16[row * a.ld + col] : 0;
     }
   }
+  // the block's maximum, of 32-bit words that each hold two magnitudes
+  const auto all = [&](uint32_t m, int turn) {
 #pragma unroll
-  for (int p = 0; p < kPasses; ++p)
+    for (int d = 16; d; d >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, d));
+    if ((threadIdx.x & 31) == 0) part[turn][threadIdx.x >> 5] = m;
+    __syncthreads();
 #pragma unroll
-    for (int j = 0; j < (VEC ? 4 : 1); ++j)
-      amax = fmaxf(amax, fmaxf(finite_abs(bf16_lo(v[p][j])), finite_abs(bf16_hi(v[p][j]))));
+    for (int w = 0; w < kThreads / 32; ++w) m = __vmaxu2(m, part[turn][w]);
+    return fold(m);
+  };
+  uint32_t m = 0;
 #pragma unroll
-  for (int d = 16; d; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
-  __shared__ float part[kThreads / 32];
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = amax;
-  __syncthreads();
+  for (int p = 0; p < kPasses; ++p) m = __vmaxu2(m, packed_max(v[p]));
+  m = all(m, 0);
+  const bool clean = m < kInf16;  // the same for the whole CTA
+  if (!clean) {
+    m = 0;
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) amax = fmaxf(amax, part[w]);
-  const uint32_t e = scale_exponent(amax);
+    for (int p = 0; p < kPasses; ++p) m = __vmaxu2(m, packed_max_finite(v[p]));
+    m = all(m, 1);
+  }
+  const uint32_t e = scale_exponent(bf16_lo(m));
   const float inv = exponent_inverse(e);
 #pragma unroll
   for (int p = 0; p < kPasses; ++p) {
     const int64_t row = row0 + p * kRows;
     if (row >= a.rows || col >= a.cols) continue;
-    if constexpr (VEC) {
-      uint32_t c[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        c[j] = pack_e4m3x4(bf16_lo(v[p][2 * j]) * inv, bf16_hi(v[p][2 * j]) * inv, bf16_lo(v[p][2 * j + 1]) * inv,
-                           bf16_hi(v[p][2 * j + 1]) * inv);
-      *(uint2*)(a.codes + row * a.cols + col) = make_uint2(c[0], c[1]);
-    } else {
-      a.codes[row * a.cols + col] = (uint8_t)pack_e4m3(bf16_lo(v[p][0]) * inv, 0.0f);
-    }
+    if constexpr (VEC)
+      *(uint2*)(a.codes + row * a.cols + col) = clean ? codes8<true>(v[p], inv) : codes8<false>(v[p], inv);
+    else
+      a.codes[row * a.cols + col] = (uint8_t)pack_e4m3(no_infinity(bf16_lo(v[p][0])) * inv, 0.0f);
   }
   if (threadIdx.x == 0) a.scales[blockIdx.x] = exponent_value(e);
 }
@@ -156,24 +206,25 @@ __device__ __forceinline__ float scale_at(const Fp8Args& a, int64_t blocks_per_r
 // Contiguous on both sides: the matrix is one run of elements, taken 8 at a
 // time (8 bytes of codes, 16 of bf16) whatever the width; a group of 8 that
 // passes a block's or a row's end looks its scales up one by one.
-template <int U>
-__global__ void __launch_bounds__(kThreads) restore_flat_kernel(Fp8Args a, int64_t blocks_per_row, int64_t numel) {
+template <int U, class Index>
+__global__ void __launch_bounds__(kThreads) restore_flat_kernel(Fp8Args a, int64_t blocks_per_row, Index numel) {
+  const Index cols = (Index)a.cols;
   uint2 c[U];
-  int64_t at[U];
+  Index at[U];
 #pragma unroll
   for (int i = 0; i < U; ++i) {
-    at[i] = (((int64_t)blockIdx.x * U + i) * kThreads + threadIdx.x) * 8;
+    at[i] = (((Index)blockIdx.x * U + i) * kThreads + threadIdx.x) * 8;
     c[i] = make_uint2(0, 0);
     if (at[i] + 8 <= numel) c[i] = __ldcs((const uint2*)(a.codes + at[i]));
   }
 #pragma unroll
   for (int i = 0; i < U; ++i) {
     if (at[i] >= numel) continue;
-    int64_t row = at[i] / a.cols, col = at[i] - row * a.cols;
+    Index row = at[i] / cols, col = at[i] - row * cols;
     if (at[i] + 8 > numel) {
-      for (int64_t e = at[i]; e < numel; ++e) {
+      for (Index e = at[i]; e < numel; ++e) {
         a.bf16[e] = to_bf16(e4m3_values(a.codes[e]).x * scale_at(a, blocks_per_row, row, col));
-        if (++col == a.cols) ++row, col = 0;
+        if (++col == cols) ++row, col = 0;
       }
       continue;
     }
@@ -185,7 +236,7 @@ __global__ void __launch_bounds__(kThreads) restore_flat_kernel(Fp8Args a, int64
       f[2 * j] = t.x;
       f[2 * j + 1] = t.y;
     }
-    if (col + 8 <= a.cols && (col & (kBlock - 1)) <= kBlock - 8) {
+    if (col + 8 <= cols && (col & (kBlock - 1)) <= kBlock - 8) {
       const float s = scale_at(a, blocks_per_row, row, col);
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[j] *= s;
@@ -193,7 +244,7 @@ __global__ void __launch_bounds__(kThreads) restore_flat_kernel(Fp8Args a, int64
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         f[j] *= scale_at(a, blocks_per_row, row, col);
-        if (++col == a.cols) ++row, col = 0;
+        if (++col == cols) ++row, col = 0;
       }
     }
     __stcs((uint4*)(a.bf16 + at[i]), make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
@@ -215,12 +266,13 @@ __global__ void __launch_bounds__(kThreads) restore_any_kernel(Fp8Args a, int64_
 // and u read from their codes: 4 bytes in and 4 (6) out an element, so the
 // pre-activations are never spelled out in memory.  V = 8 columns a thread
 // where rows allow 16-byte accesses, else 1.
-template <int ACT, int V>
-__global__ void __launch_bounds__(kThreads) grad_stored_kernel(GatedArgs a, int64_t groups_per_row, int64_t groups) {
+template <int ACT, int V, class Index>
+__global__ void __launch_bounds__(kThreads) grad_stored_kernel(GatedArgs a, Index groups_per_row, Index groups) {
   const int64_t nb = (a.ffn + kBlock - 1) / kBlock;
-  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  const Index i = (Index)blockIdx.x * kThreads + threadIdx.x;
   if (i >= groups) return;
-  const int64_t row = i / groups_per_row, col = (i - row * groups_per_row) * V;
+  const Index r = i / groups_per_row;
+  const int64_t row = r, col = (int64_t)(i - r * groups_per_row) * V;
   const int64_t at = row * a.ffn + col, sat = row * nb + col / kBlock;
   const float sg = a.gs[sat], su = a.us[sat];
   float g[V], u[V], d[V], dg[V], du[V], h[V];
@@ -269,10 +321,15 @@ cudaError_t grad_stored(const GatedArgs& a, cudaStream_t stream) {
   const bool vec = a.ffn % 8 == 0 && a.lddh % 8 == 0 && (!a.h || a.ldh % 8 == 0);
   const int64_t per_row = vec ? a.ffn / 8 : a.ffn, groups = per_row * a.tokens;
   const unsigned grid = (unsigned)ceil_div(groups, kThreads);
-  if (vec)
-    grad_stored_kernel<ACT, 8><<<grid, kThreads, 0, stream>>>(a, per_row, groups);
+  const bool small = groups <= kSmall;
+  if (vec && small)
+    grad_stored_kernel<ACT, 8, uint32_t><<<grid, kThreads, 0, stream>>>(a, (uint32_t)per_row, (uint32_t)groups);
+  else if (vec)
+    grad_stored_kernel<ACT, 8, int64_t><<<grid, kThreads, 0, stream>>>(a, per_row, groups);
+  else if (small)
+    grad_stored_kernel<ACT, 1, uint32_t><<<grid, kThreads, 0, stream>>>(a, (uint32_t)per_row, (uint32_t)groups);
   else
-    grad_stored_kernel<ACT, 1><<<grid, kThreads, 0, stream>>>(a, per_row, groups);
+    grad_stored_kernel<ACT, 1, int64_t><<<grid, kThreads, 0, stream>>>(a, per_row, groups);
   return cudaGetLastError();
 }
 
@@ -281,21 +338,26 @@ cudaError_t grad_stored(const GatedArgs& a, cudaStream_t stream) {
 cudaError_t launch_fp8_store(const Fp8Args& a, cudaStream_t stream) {
   const int64_t per_row = ceil_div(a.cols, kBlock);
   const bool vec = a.cols % 8 == 0 && a.ld % 8 == 0;
-  if (a.block_rows == 1) {
-    const int64_t blocks = per_row * a.rows;
-    const int64_t per_cta = (vec ? kThreads / 16 : kThreads / 32) * 4;
-    const unsigned grid = (unsigned)ceil_div(blocks, per_cta);
-    if (vec)
-      store_rows_kernel<4><<<grid, kThreads, 0, stream>>>(a, per_row, blocks);
-    else
-      store_rows_any_kernel<4><<<grid, kThreads, 0, stream>>>(a, per_row, blocks);
-  } else {
+  if (a.block_rows != 1) {
     const unsigned grid = (unsigned)(per_row * ceil_div(a.rows, kBlock));
     if (vec)
-      store_square_kernel<true><<<grid, kThreads, 0, stream>>>(a, per_row);
+      store_square_kernel<true><<<grid, kThreads, 0, stream>>>(a, (uint32_t)per_row);
     else
-      store_square_kernel<false><<<grid, kThreads, 0, stream>>>(a, per_row);
+      store_square_kernel<false><<<grid, kThreads, 0, stream>>>(a, (uint32_t)per_row);
+    return cudaGetLastError();
   }
+  constexpr int kUnroll = 4;
+  const int64_t blocks = per_row * a.rows;
+  const unsigned grid = (unsigned)ceil_div(blocks, (int64_t)kUnroll * (vec ? kThreads / 16 : kThreads / 32));
+  const bool small = blocks <= kSmall;
+  if (vec && small)
+    store_rows_kernel<kUnroll, uint32_t><<<grid, kThreads, 0, stream>>>(a, (uint32_t)per_row, (uint32_t)blocks);
+  else if (vec)
+    store_rows_kernel<kUnroll, int64_t><<<grid, kThreads, 0, stream>>>(a, per_row, blocks);
+  else if (small)
+    store_rows_any_kernel<kUnroll, uint32_t><<<grid, kThreads, 0, stream>>>(a, (uint32_t)per_row, (uint32_t)blocks);
+  else
+    store_rows_any_kernel<kUnroll, int64_t><<<grid, kThreads, 0, stream>>>(a, per_row, blocks);
   return cudaGetLastError();
 }
 
@@ -303,8 +365,11 @@ cudaError_t launch_fp8_restore(const Fp8Args& a, cudaStream_t stream) {
   const int64_t per_row = ceil_div(a.cols, kBlock), numel = a.rows * a.cols;
   if (a.ld == a.cols) {
     constexpr int kUnroll = 4;
-    restore_flat_kernel<kUnroll><<<(unsigned)ceil_div(numel, (int64_t)kThreads * 8 * kUnroll), kThreads, 0, stream>>>(
-        a, per_row, numel);
+    const unsigned grid = (unsigned)ceil_div(numel, (int64_t)kThreads * 8 * kUnroll);
+    if (numel <= kSmall)
+      restore_flat_kernel<kUnroll, uint32_t><<<grid, kThreads, 0, stream>>>(a, per_row, (uint32_t)numel);
+    else
+      restore_flat_kernel<kUnroll, int64_t><<<grid, kThreads, 0, stream>>>(a, per_row, numel);
   } else {
     const int64_t grid = ceil_div(numel, kThreads);
     restore_any_kernel<<<(unsigned)(grid < 65536 ? grid : 65536), kThreads, 0, stream>>>(a, per_row, numel);

@@ -92,8 +92,8 @@ __global__ void __launch_bounds__(kThreads) gated_simple_kernel(GatedArgs a) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int64_t col = col0 + tx + 32 * j;
-      gmax = fmaxf(gmax, finite_abs(g.v[i][j]));  // columns past the end hold 0
-      umax = fmaxf(umax, finite_abs(u.v[i][j]));
+      gmax = fmaxf(gmax, fabsf(no_infinity(g.v[i][j])));  // columns past the end hold 0
+      umax = fmaxf(umax, fabsf(no_infinity(u.v[i][j])));
       if (col >= a.ffn) continue;
       if (GRAD) {
         const float d = bf16_value(a.dh[row * a.lddh + col]);
@@ -117,8 +117,8 @@ __global__ void __launch_bounds__(kThreads) gated_simple_kernel(GatedArgs a) {
       for (int j = 0; j < 4; ++j) {
         const int64_t col = col0 + tx + 32 * j;
         if (col >= a.ffn) continue;
-        a.g8[row * a.ffn + col] = (uint8_t)pack_e4m3(g.v[i][j] * exponent_inverse(eg), 0.0f);
-        a.u8[row * a.ffn + col] = (uint8_t)pack_e4m3(u.v[i][j] * exponent_inverse(eu), 0.0f);
+        a.g8[row * a.ffn + col] = (uint8_t)pack_e4m3(no_infinity(g.v[i][j]) * exponent_inverse(eg), 0.0f);
+        a.u8[row * a.ffn + col] = (uint8_t)pack_e4m3(no_infinity(u.v[i][j]) * exponent_inverse(eu), 0.0f);
       }
       if (tx == 0) {
         a.gs[row * nb + blockIdx.y] = exponent_value(eg);

@@ -55,11 +55,18 @@ struct Params {
 };
 
 // 32 codes of one row.  Rows are whole multiples of 8 codes.
-__device__ __forceinline__ void put_codes(uint8_t* dst, const uint32_t (&v)[32], float inv, int valid) {
+__device__ __forceinline__ void put_codes(uint8_t* dst, const uint32_t (&v)[32], float inv, int valid, bool clean) {
   uint32_t c[8];
+  if (clean) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    c[i] = pack_e4m3x4(as_f(v[4 * i]) * inv, as_f(v[4 * i + 1]) * inv, as_f(v[4 * i + 2]) * inv, as_f(v[4 * i + 3]) * inv);
+    for (int i = 0; i < 8; ++i)
+      c[i] = pack_e4m3x4(as_f(v[4 * i]) * inv, as_f(v[4 * i + 1]) * inv, as_f(v[4 * i + 2]) * inv, as_f(v[4 * i + 3]) * inv);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      c[i] = pack_e4m3x4(no_infinity(as_f(v[4 * i])) * inv, no_infinity(as_f(v[4 * i + 1])) * inv,
+                         no_infinity(as_f(v[4 * i + 2])) * inv, no_infinity(as_f(v[4 * i + 3])) * inv);
+  }
   if (((uintptr_t)dst & 15) == 0 && valid >= 32) {
     ((uint4*)dst)[0] = make_uint4(c[0], c[1], c[2], c[3]);
     ((uint4*)dst)[1] = make_uint4(c[4], c[5], c[6], c[7]);
@@ -77,6 +84,7 @@ __device__ __forceinline__ void epilogue(const Params& p, const TileAt& t, uint3
   if constexpr (FORM == kForward || FORM == kGrad) {
     const int col0 = t.n * kHalf;
     float ginv = 0.0f, uinv = 0.0f;
+    bool clean = true;  // no infinities to be made NaN in the codes
     if constexpr (FORM == kForward) {
       if (p.g8) {  // the tile is one scale block wide: a thread holds a whole block of its token
         float gmax = 0.0f, umax = 0.0f;
@@ -86,8 +94,22 @@ __device__ __forceinline__ void epilogue(const Params& p, const TileAt& t, uint3
           tmem_read32x2(tmem + c * 32, tmem + kHalf + c * 32, g, u);
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            gmax = fmaxf(gmax, finite_abs(as_f(g[i])));
-            umax = fmaxf(umax, finite_abs(as_f(u[i])));
+            gmax = fmaxf(gmax, fabsf(as_f(g[i])));
+            umax = fmaxf(umax, fabsf(as_f(u[i])));
+          }
+        }
+        clean = !__any_sync(0xffffffffu, gmax == CUDART_INF_F || umax == CUDART_INF_F);
+        if (!clean) {  // again without the infinities
+          gmax = umax = 0.0f;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t g[32], u[32];
+            tmem_read32x2(tmem + c * 32, tmem + kHalf + c * 32, g, u);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              gmax = fmaxf(gmax, fabsf(no_infinity(as_f(g[i]))));
+              umax = fmaxf(umax, fabsf(no_infinity(as_f(u[i]))));
+            }
           }
         }
         const uint32_t eg = scale_exponent(gmax), eu = scale_exponent(umax);
@@ -107,8 +129,8 @@ __device__ __forceinline__ void epilogue(const Params& p, const TileAt& t, uint3
       tmem_read32x2(tmem + c * 32, tmem + kHalf + c * 32, g, u);
       if constexpr (FORM == kForward) {
         if (p.g8 && mine) {
-          put_codes(p.g8 + (int64_t)row * p.cols + col, g, ginv, p.cols - col);
-          put_codes(p.u8 + (int64_t)row * p.cols + col, u, uinv, p.cols - col);
+          put_codes(p.g8 + (int64_t)row * p.cols + col, g, ginv, p.cols - col, clean);
+          put_codes(p.u8 + (int64_t)row * p.cols + col, u, uinv, p.cols - col, clean);
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i)
