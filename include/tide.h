@@ -550,11 +550,15 @@ TIDE_API tide_status_t tide_fp8_restore(tide_compute_t compute, int64_t rows, in
  *   a    [m, k] codes, a_scales [m, ceil(k / 128)]             (block_rows = 1)
  *   b    [n, k] codes, b_scales [ceil(n / 128), ceil(k / 128)] (block_rows = 128)
  *   out  [m, n] bf16, row stride ld_out
- * Scales may be any fp32 values.
+ *   any_scales  0: the scales are powers of two from 2^-126 on, as
+ *        tide_fp8_store writes them, which the tensor cores take as they are;
+ *        any other scale makes its row or columns NaN.
+ *        1: any fp32 scales.  Up to 64 rows and for small products at the
+ *        same speed, else at about half of it.
  */
 TIDE_API tide_status_t tide_fp8_matmul(tide_compute_t compute, int64_t m, int64_t n, int64_t k, const uint8_t* a,
                                        const float* a_scales, const uint8_t* b, const float* b_scales,
-                                       uint16_t* out, int64_t ld_out, cudaStream_t stream);
+                                       int32_t any_scales, uint16_t* out, int64_t ld_out, cudaStream_t stream);
 
 /*
  * A gated block's activations in 8-bit blocks (block_rows = 1), kept from

@@ -31,8 +31,11 @@ class Compute:
         _t.tide_fp8_restore(self.handle, rows, cols, codes, scales, block_rows, dst, cols if ld_dst is None else ld_dst,
                             stream)
 
-    def fp8_matmul(self, m: int, n: int, k: int, a, a_scales, b, b_scales, out, ld_out=None, stream=None):
-        _t.tide_fp8_matmul(self.handle, m, n, k, a, a_scales, b, b_scales, out, n if ld_out is None else ld_out, stream)
+    def fp8_matmul(self, m: int, n: int, k: int, a, a_scales, b, b_scales, out, any_scales: bool = False, ld_out=None,
+                   stream=None):
+        """any_scales: scales other than the powers of two that fp8_store writes."""
+        _t.tide_fp8_matmul(self.handle, m, n, k, a, a_scales, b, b_scales, any_scales, out,
+                           n if ld_out is None else ld_out, stream)
 
     def gated_forward(self, tokens: int, hidden: int, ffn: int, x, w_gate, w_up, h, activation: str = "silu",
                       checkpoint: GatedCheckpoint | None = None, ld_x=None, ld_h=None, stream=None):

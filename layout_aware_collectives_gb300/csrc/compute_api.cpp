@@ -193,8 +193,8 @@ tide_status_t tide_fp8_restore(tide_compute_t c, int64_t rows, int64_t cols, con
 }
 
 tide_status_t tide_fp8_matmul(tide_compute_t c, int64_t m, int64_t n, int64_t k, const uint8_t* a,
-                              const float* a_scales, const uint8_t* b, const float* b_scales, uint16_t* out,
-                              int64_t ld_out, cudaStream_t stream) {
+                              const float* a_scales, const uint8_t* b, const float* b_scales, int32_t any_scales,
+                              uint16_t* out, int64_t ld_out, cudaStream_t stream) {
   if (!c) return invalid("compute is NULL");
   TIDE_TRY(check_dims(m, k, "tide_fp8_matmul"));
   TIDE_TRY(check_dims(n, k, "tide_fp8_matmul"));
@@ -206,7 +206,7 @@ tide_status_t tide_fp8_matmul(tide_compute_t c, int64_t m, int64_t n, int64_t k,
   TIDE_TRY(bind(c, stream));
   if (k == 0)  // an empty sum
     return launched(cudaMemset2DAsync(out, ld_out * 2, 0, n * 2, m, stream), "tide_fp8_matmul");
-  const MatmulArgs args{m, n, k, a, a_scales, b, b_scales, out, ld_out};
+  const MatmulArgs args{m, n, k, a, a_scales, b, b_scales, out, ld_out, any_scales != 0};
   if (k % 16 == 0 && n % 8 == 0 && ld_out % 8 == 0) {
     const TcLaunch l = launch_of(c);
     return launched(fp8_few_takes(args, l.sms) ? launch_fp8_matmul_few(args, l, stream)

@@ -37,6 +37,17 @@ __device__ __forceinline__ float exponent_value(uint32_t e) { return __uint_as_f
 // 1 / 2^(e - 127), exact: e is within [1, 247].
 __device__ __forceinline__ float exponent_inverse(uint32_t e) { return __uint_as_float((254u - e) << 23); }
 
+// A scale that is a power of two, at least 2^-126, as itself; any other as NaN.
+__device__ __forceinline__ float power_of_two(float s) {
+  const uint32_t b = __float_as_uint(s), e = b >> 23;
+  return (b & 0x7fffffu) == 0 && e - 1u < 254u ? s : CUDART_NAN_F;
+}
+// The same as an exponent byte (E8M0, whose 255 is NaN) in all four bytes.
+__device__ __forceinline__ uint32_t exponent_bytes(float s) {
+  const uint32_t b = __float_as_uint(s), e = b >> 23;
+  return ((b & 0x7fffffu) == 0 && e - 1u < 254u ? e : 255u) * 0x01010101u;
+}
+
 // A block's largest magnitude is taken with fmaxf, which passes over NaN.  If
 // it is infinite, infinities are made NaN (which is what their codes are)
 // and the maximum is taken again: so finite blocks pay for no checks.

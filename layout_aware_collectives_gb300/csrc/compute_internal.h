@@ -60,6 +60,7 @@ struct MatmulArgs {
   const float* sb;
   uint16_t* out;
   int64_t ldo;
+  bool any_scales;  // else powers of two
 };
 
 // Bytes <-> blocks (fp8_blocks.cu).

@@ -49,6 +49,7 @@ struct Params {
   float *gs, *us;
   // 8-bit
   const float *sx, *sw;
+  bool any_scales;
   int* err;
   uint64_t limit_ns, stall_ns;
 };
@@ -214,7 +215,7 @@ __global__ void __launch_bounds__(kThreads) few_tc_kernel(const __grid_constant_
       for (int k = k0; k < k1; ++k, ++j) {
         const int b = j % S::kBufs;
         if (e < NT) {
-          scales[j & 3][e] = next_x * next_w;
+          scales[j & 3][e] = p.any_scales ? next_x * next_w : power_of_two(next_x) * power_of_two(next_w);
           if (k + 1 < k1) next_x = __ldg(sx + k + 1), next_w = __ldg(sw + k + 1);
         }
         sums_barrier();
@@ -402,7 +403,7 @@ cudaError_t launch_fp8_matmul_few(const MatmulArgs& a, const TcLaunch& l, cudaSt
   p.tokens = (int)a.m, p.features = (int)a.n;
   p.steps = (int)ceil_div(a.k, kRowBytes), p.step_elems = kRowBytes;
   p.out = a.out, p.ldo = a.ldo;
-  p.sx = a.sa, p.sw = a.sb;
+  p.sx = a.sa, p.sw = a.sb, p.any_scales = a.any_scales;
   if (!make_map(&p.w[0], a.b, 1, a.k, a.n, a.k, kRowBytes, kRows, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_map(&p.x, a.a, 1, a.k, a.m, a.k, kRowBytes, nt, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;

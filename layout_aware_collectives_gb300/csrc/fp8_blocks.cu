@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(kThreads) store_rows_kernel(Fp8Args a, Index b
     const float inv = exponent_inverse(e);
     if (row[i] < 0) continue;
     if (col[i] < a.cols)
-      *(uint2*)(a.codes + row[i] * a.cols + col[i]) = clean ? codes8<true>(v[i], inv) : codes8<false>(v[i], inv);
+      __stcs((uint2*)(a.codes + row[i] * a.cols + col[i]), clean ? codes8<true>(v[i], inv) : codes8<false>(v[i], inv));
     if (lane == 0) a.scales[row[i] * blocks_per_row + col[i] / kBlock] = exponent_value(e);
   }
 }
@@ -102,18 +102,18 @@ __global__ void __launch_bounds__(kThreads) store_rows_any_kernel(Fp8Args a, Ind
   const int lane = threadIdx.x & 31;
   const Index warp = (Index)blockIdx.x * (U * kThreads / 32) + (threadIdx.x >> 5);
   uint16_t v[U][4];
-  int64_t row[U], col[U];
+  int wide[U];  // columns of the block from this lane's first on
+  int64_t at[U];
 #pragma unroll
   for (int i = 0; i < U; ++i) {
     const Index blk = warp + (Index)(i * (kThreads / 32));
-    const Index r = blk / blocks_per_row;
-    row[i] = blk < blocks ? (int64_t)r : -1;
-    col[i] = (int64_t)(blk - r * blocks_per_row) * kBlock + lane;
+    const Index r = blk / blocks_per_row, b = blk - r * blocks_per_row;
+    const int64_t col = (int64_t)b * kBlock + lane;
+    wide[i] = blk < blocks ? (int)min((int64_t)kBlock, a.cols - col) : 0;
+    at[i] = (int64_t)r * a.cols + col;
+    const uint16_t* src = a.bf16 + (int64_t)r * a.ld + col;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[i][j] = 0;
-      if (row[i] >= 0 && col[i] + 32 * j < a.cols) v[i][j] = a.bf16[row[i] * a.ld + col[i] + 32 * j];
-    }
+    for (int j = 0; j < 4; ++j) v[i][j] = 32 * j < wide[i] ? src[32 * j] : 0;
   }
 #pragma unroll
   for (int i = 0; i < U; ++i) {
@@ -127,11 +127,11 @@ __global__ void __launch_bounds__(kThreads) store_rows_any_kernel(Fp8Args a, Ind
     for (int d = 16; d; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
     const uint32_t e = scale_exponent(amax);
     const float inv = exponent_inverse(e);
-    if (row[i] < 0) continue;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      if (col[i] + 32 * j < a.cols) a.codes[row[i] * a.cols + col[i] + 32 * j] = (uint8_t)pack_e4m3(f[j] * inv, 0.0f);
-    if (lane == 0) a.scales[row[i] * blocks_per_row + col[i] / kBlock] = exponent_value(e);
+      if (32 * j < wide[i]) a.codes[at[i] + 32 * j] = (uint8_t)pack_e4m3(f[j] * inv, 0.0f);
+    const Index blk = warp + (Index)(i * (kThreads / 32));
+    if (lane == 0 && blk < blocks) a.scales[blk] = exponent_value(e);
   }
 }
 
@@ -149,18 +149,21 @@ __global__ void __launch_bounds__(kThreads) store_square_kernel(Fp8Args a, uint3
   const uint32_t br = blockIdx.x / blocks_per_row, bc = blockIdx.x - br * blocks_per_row;
   const int64_t col = (int64_t)bc * kBlock + (threadIdx.x % kLanes) * kPerLoad;
   const int64_t row0 = (int64_t)br * kBlock + threadIdx.x / kLanes;
+  const int high = col < a.cols ? (int)min((int64_t)kBlock, a.rows - row0) : 0;  // rows from this thread's first on
+  const uint16_t* src = a.bf16 + row0 * a.ld + col;
+  uint8_t* dst = a.codes + row0 * a.cols + col;
   uint32_t v[kPasses][kWords];
 #pragma unroll
   for (int p = 0; p < kPasses; ++p) {
-    const int64_t row = row0 + p * kRows;
-    const bool in = row < a.rows && col < a.cols;
+    const bool in = p * kRows < high;
     if constexpr (VEC) {
       uint4 q = make_uint4(0, 0, 0, 0);
-      if (in) q = __ldcs((const uint4*)(a.bf16 + row * a.ld + col));
+      if (in) q = __ldcs((const uint4*)src);
       v[p][0] = q.x, v[p][1] = q.y, v[p][2] = q.z, v[p][3] = q.w;
     } else {
-      v[p][0] = in ? a.bf16[row * a.ld + col] : 0;
+      v[p][0] = in ? *src : 0;
     }
+    src += kRows * a.ld;
   }
   // the block's maximum, of 32-bit words that each hold two magnitudes
   const auto all = [&](uint32_t m, int turn) {
@@ -187,12 +190,13 @@ __global__ void __launch_bounds__(kThreads) store_square_kernel(Fp8Args a, uint3
   const float inv = exponent_inverse(e);
 #pragma unroll
   for (int p = 0; p < kPasses; ++p) {
-    const int64_t row = row0 + p * kRows;
-    if (row >= a.rows || col >= a.cols) continue;
-    if constexpr (VEC)
-      *(uint2*)(a.codes + row * a.cols + col) = clean ? codes8<true>(v[p], inv) : codes8<false>(v[p], inv);
-    else
-      a.codes[row * a.cols + col] = (uint8_t)pack_e4m3(no_infinity(bf16_lo(v[p][0])) * inv, 0.0f);
+    if (p * kRows < high) {
+      if constexpr (VEC)
+        __stcs((uint2*)dst, clean ? codes8<true>(v[p], inv) : codes8<false>(v[p], inv));
+      else
+        *dst = (uint8_t)pack_e4m3(no_infinity(bf16_lo(v[p][0])) * inv, 0.0f);
+    }
+    dst += kRows * a.cols;
   }
   if (threadIdx.x == 0) a.scales[blockIdx.x] = exponent_value(e);
 }
@@ -346,7 +350,7 @@ cudaError_t launch_fp8_store(const Fp8Args& a, cudaStream_t stream) {
       store_square_kernel<false><<<grid, kThreads, 0, stream>>>(a, (uint32_t)per_row);
     return cudaGetLastError();
   }
-  constexpr int kUnroll = 4;
+  constexpr int kUnroll = 2;
   const int64_t blocks = per_row * a.rows;
   const unsigned grid = (unsigned)ceil_div(blocks, (int64_t)kUnroll * (vec ? kThreads / 16 : kThreads / 32));
   const bool small = blocks <= kSmall;

@@ -2,17 +2,21 @@
 //
 //   out[i, j] = sum_b sa[i, b] sb[j / 128, b] sum_{k in b} a[i, k] b[j, k]
 //
-// A block is 128 steps of the contraction: one pipeline stage.  Its codes'
-// product is summed by the tensor cores into one of two TMEM accumulators;
-// from there 8 warps add it, times sa sb, to fp32 sums in registers (one
-// fused multiply-add each, a row's scale being a thread's), while the tensor
-// cores sum the next block into the other.  So scales need not be powers of
-// two, and the sum across blocks is fp32's own.
+// A block is 128 steps of the contraction: one pipeline stage.  A pair of
+// CTAs works on a 256 x 256 tile, each with 128 rows of A and 128 of B as in
+// the gated block's kernel.  Two kernels:
 //
-// A pair of CTAs works on a 256 x 256 tile, each with 128 rows of A and 128
-// of B as in the gated block's kernel.  One block of it is 512 cycles of the
-// tensor cores at their 8-bit rate, against 256 of TMEM reads and 256 of
-// multiply-adds (the latter halved by the two-wide form).
+// scaled_kernel: scales that are powers of two.  The tensor cores take them
+// as exponent bytes beside the codes, so the whole contraction is summed in
+// TMEM at their 8-bit rate.  Four warps write each stage's scales to TMEM.
+//
+// summed_kernel: any scales.  A block's sums go from one of two TMEM
+// accumulators, times sa sb, into fp32 sums in the registers of 8 warps (one
+// fused multiply-add each, a row's scale being a thread's) while the tensor
+// cores sum the next block into the other.  A block is 512 cycles of the
+// tensor cores, but handing an accumulator there and back takes some 1,700:
+// 1,000 for the barriers' way between the two CTAs, the rest for TMEM reads
+// and the multiply-adds between them, and TMEM holds no third accumulator.
 #include "compute_device.cuh"
 #include "tc_device.cuh"
 #include "tc_host.h"
@@ -51,7 +55,7 @@ __device__ __forceinline__ void add32(uint64_t (&sum)[kHalf / 2], const uint32_t
   for (int i = 0; i < 16; ++i) fma2(sum[C * 16 + i], v[2 * i], v[2 * i + 1], s);
 }
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) fp8_tc_kernel(const __grid_constant__ Params p) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) summed_kernel(const __grid_constant__ Params p) {
   constexpr uint32_t kInstr = instr_desc(0, 0, 0, 256, 256);
   extern __shared__ uint8_t raw[];
   __shared__ uint64_t bars[2 * kStages + 5];
@@ -209,12 +213,214 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) fp8_tc_
   if (warp == 2) tmem_free<2>(tmem, 512);
 }
 
+// ------------------------------------------------------ powers of two only
+
+// TMEM: a tile's 256 columns of sums start at 0 or at 160 in turn, the
+// scales' ring takes 6 x 12 from 416 on.  Two tiles' sums share 96 columns;
+// those are read first, and the next tile starts as soon as they are.
+constexpr int kOdd = 160;
+constexpr int kShared = 3;  // chunks of 32 columns
+constexpr int kScales = 416;
+constexpr int kScaledThreads = 384;  // loads, MMAs, -, -, 4 warps of results, 4 of scales
+constexpr int kScaledBoxes = 4;
+constexpr size_t kScaledSmem = 1024 + kStages * kStage + 4 * kScaledBoxes * kBox;
+
+__global__ void __cluster_dims__(2, 1, 1)
+    __launch_bounds__(kScaledThreads, 1) scaled_kernel(const __grid_constant__ Params p) {
+  constexpr uint32_t kInstr = instr_desc_scaled(256, 256);
+  extern __shared__ uint8_t raw[];
+  __shared__ uint64_t bars[2 * kStages + 3];
+  __shared__ uint32_t tmem_at;
+  __shared__ int stop;
+
+  const uint32_t smem = (smem_addr(raw) + 1023u) & ~1023u;
+  const uint32_t bar0 = smem_addr(bars);
+  const auto full = [&](int s) { return bar0 + 8u * s; };
+  const auto empty = [&](int s) { return bar0 + 8u * (kStages + s); };
+  const uint32_t sums_full = bar0 + 8u * (2 * kStages), sums_empty = sums_full + 8, spare = sums_full + 16;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const Watch watch{&stop, p.err, p.limit_ns};
+
+  if (threadIdx.x == 0) {
+    stop = 0;
+    // full: the copies, and four warps' scales in each CTA
+    for (int s = 0; s < kStages; ++s) bar_init(full(s), 1 + 2 * 4), bar_init(empty(s), 1);
+    bar_init(sums_full, 1), bar_init(sums_empty, 2 * 4), bar_init(spare, 1);
+    bar_init_fence();
+    prefetch_map(&p.a), prefetch_map(&p.b), prefetch_map(&p.out);
+  }
+  if (warp == 2) tmem_alloc<2>(smem_addr(&tmem_at), 512);
+  fence_before();
+  __syncthreads();
+  cluster_sync();
+  fence_after();
+  const uint32_t tmem = tmem_at;
+
+  if (p.stall_ns) {  // test: a wait on a barrier nothing arrives on runs out
+    if (threadIdx.x == 0) bar_wait(spare, 0, Watch{&stop, p.err, p.stall_ns});
+  } else if (warp == 0) {
+    if (lane == 0) {
+      int j = 0;  // stages filled so far
+      bool go = true;
+      for (int t = pair; t < p.tiles && go; t += pairs) {
+        const TileAt at = tile_at(p.tiles_m, p.tiles_n, t);
+        for (int k = 0; k < p.blocks; ++k, ++j) {
+          const int s = j % kStages;
+          if (j >= kStages && !bar_wait(empty(s), (j / kStages + 1) & 1, watch)) {
+            go = false;
+            break;
+          }
+          if (rank == 0) bar_expect(full(s), 2 * kStage);
+          const uint32_t bar = peer_addr(full(s), 0);
+          const uint32_t a = smem + s * kStage;
+          load_box<true>(a, &p.a, k * kBlock, (at.m * 2 + rank) * kHalf, bar);
+          load_box<true>(a + kOperand, &p.b, k * kBlock, (at.n * 2 + rank) * kHalf, bar);
+        }
+      }
+      // the MMAs' last arrivals reach this CTA while it is still there
+      for (int i = max(0, j - kStages); i < j && go; ++i) go = bar_wait(empty(i % kStages), (i / kStages) & 1, watch);
+      // after a wait that ran out: both CTAs' copies in flight, with a limit
+      // again; the peer's memory stays until the cluster's last barrier
+      if (!go && rank == 0) {
+        int never = 0;
+        for (int i = max(0, j - kStages); i < j; ++i)
+          bar_wait(full(i % kStages), (i / kStages) & 1, Watch{&never, p.err, p.limit_ns / 16});
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      int j = 0, i = 0;  // blocks and tiles so far
+      bool go = true;
+      for (int t = pair; t < p.tiles && go; t += pairs, ++i) {
+        if (i > 0 && !bar_wait(sums_empty, (i + 1) & 1, watch)) break;
+        fence_after();
+        const uint32_t sums = tmem + (i & 1) * kOdd;
+        for (int k = 0; k < p.blocks; ++k, ++j) {
+          const int s = j % kStages;
+          if (!bar_wait(full(s), (j / kStages) & 1, watch)) {
+            go = false;
+            break;
+          }
+          fence_after();
+          const uint32_t a = smem + s * kStage, scales = tmem + kScales + s * 12;
+          const uint64_t da = operand_desc(a, 16), db = operand_desc(a + kOperand, 16);
+#pragma unroll
+          for (int q = 0; q < kBlock / 32; ++q)
+            mma_scaled(sums, da + q * 2, db + q * 2, kInstr, scales, scales + 4, k > 0 || q > 0);
+          mma_commit<2>(empty(s));
+        }
+        if (go) mma_commit<2>(sums_full);
+      }
+      if (*watch.stop) {  // the MMAs in flight, with a limit
+        int never = 0;
+        mma_commit<2>(spare);
+        bar_wait(spare, 0, Watch{&never, p.err, p.limit_ns / 16});
+      }
+    }
+  } else if (warp >= 8) {
+    // Scales.  Every warp writes all 128 rows' (A, 4 columns) and both column
+    // blocks' (B, 8 columns) to its own 32 lanes.  They are fetched four
+    // blocks at a time, a batch ahead.
+    const uint32_t mine = tmem + ((uint32_t)(warp & 3) * 32 << 16) + kScales;
+    int j = 0;
+    bool go = true;
+    for (int t = pair; t < p.tiles && go; t += pairs) {
+      const TileAt at = tile_at(p.tiles_m, p.tiles_n, t);
+      const float* from[6];  // rows and columns past the end take any scale that is there
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        from[c] = p.sa + (int64_t)min((int)(at.m * 2 + rank) * kHalf + c * 32 + lane, p.rows - 1) * p.blocks;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) from[4 + c] = p.sb + (int64_t)min(at.n * 2 + c, (p.cols - 1) / kBlock) * p.blocks;
+      float next[6][4];
+      const auto fetch = [&](int k) {
+#pragma unroll
+        for (int c = 0; c < 6; ++c)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) next[c][q] = __ldg(from[c] + min(k + q, p.blocks - 1));
+      };
+      fetch(0);
+      for (int k = 0; k < p.blocks && go; k += 4) {
+        uint32_t now[6][4];
+#pragma unroll
+        for (int c = 0; c < 6; ++c)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) now[c][q] = exponent_bytes(next[c][q]);
+        if (k + 4 < p.blocks) fetch(k + 4);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (k + q >= p.blocks || !go) break;
+          const int s = j % kStages;
+          go = j < kStages || bar_wait_warp(empty(s), (j / kStages + 1) & 1, watch);
+          if (!go) break;
+          fence_after();
+          const uint32_t to = mine + s * 12;
+          tmem_write4(to, now[0][q], now[1][q], now[2][q], now[3][q]);
+          tmem_write4(to + 4, now[4][q], now[4][q], now[4][q], now[4][q]);
+          tmem_write4(to + 8, now[5][q], now[5][q], now[5][q], now[5][q]);
+          tmem_written();
+          fence_before();
+          __syncwarp();
+          if (lane == 0) bar_arrive_peer(peer_addr(full(s), 0));
+          ++j;
+        }
+      }
+    }
+  } else if (warp >= 4) {
+    Outbox<kScaledBoxes> out{smem + kStages * kStage + (warp - 4) * kScaledBoxes * kBox, 0, lane};
+    const uint32_t lanes = (uint32_t)(warp - 4) * 32;
+    int i = 0;
+    for (int t = pair; t < p.tiles; t += pairs, ++i) {
+      if (!bar_wait_warp(sums_full, i & 1, watch)) break;
+      fence_after();
+      const TileAt at = tile_at(p.tiles_m, p.tiles_n, t);
+      const int row0 = (at.m * 2 + rank) * kHalf + lanes, col0 = at.n * 2 * kHalf;
+      const uint32_t sums = tmem + (lanes << 16) + (i & 1) * kOdd;
+      const int first = i & 1 ? 0 : 8 - kShared;  // the chunks the next tile shares
+      uint32_t o[kShared][16];
+#pragma unroll
+      for (int c = 0; c < kShared; ++c) {
+        uint32_t v[32];
+        tmem_read(sums + (first + c) * 32, v);
+#pragma unroll
+        for (int q = 0; q < 16; ++q) o[c][q] = pack_bf16(as_f(v[2 * q]), as_f(v[2 * q + 1]));
+      }
+      fence_before();
+      __syncwarp();
+      if (lane == 0) bar_arrive_peer(peer_addr(sums_empty, 0));
+#pragma unroll
+      for (int c = 0; c < kShared; ++c) {
+        const int col = col0 + (first + c) * 32;
+        if (row0 < p.rows && col < p.cols) out.put(&p.out, o[c], col, row0);
+      }
+#pragma unroll 1
+      for (int c = 0; c < 8 - kShared; ++c) {
+        const int chunk = i & 1 ? kShared + c : c, col = col0 + chunk * 32;
+        uint32_t v[32];
+        tmem_read(sums + chunk * 32, v);
+        if (row0 >= p.rows || col >= p.cols) continue;
+#pragma unroll
+        for (int q = 0; q < 16; ++q) o[0][q] = pack_bf16(as_f(v[2 * q]), as_f(v[2 * q + 1]));
+        out.put(&p.out, o[0], col, row0);
+      }
+      fence_before();
+    }
+    if (lane == 0) stores_done();
+  }
+  __syncthreads();
+  cluster_sync();
+  if (warp == 2) tmem_free<2>(tmem, 512);
+}
+
 }  // namespace
 
 cudaError_t launch_fp8_matmul_tc(const MatmulArgs& a, const TcLaunch& l, cudaStream_t stream) {
-  static const cudaError_t ready =
-      cudaFuncSetAttribute(fp8_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
-  if (ready != cudaSuccess) return ready;
+  static const cudaError_t ready[2] = {
+      cudaFuncSetAttribute(summed_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem),
+      cudaFuncSetAttribute(scaled_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kScaledSmem)};
+  if (ready[0] != cudaSuccess || ready[1] != cudaSuccess) return ready[ready[0] == cudaSuccess];
   Params p{};
   p.sa = a.sa, p.sb = a.sb;
   p.rows = (int)a.m, p.cols = (int)a.n;
@@ -229,7 +435,10 @@ cudaError_t launch_fp8_matmul_tc(const MatmulArgs& a, const TcLaunch& l, cudaStr
       !make_map(&p.out, a.out, 2, a.n, a.m, a.ldo, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
     return cudaErrorInvalidValue;
   const int pairs = p.tiles < l.pairs ? p.tiles : l.pairs;
-  fp8_tc_kernel<<<2 * pairs, kThreads, kSmem, stream>>>(p);
+  if (a.any_scales)
+    summed_kernel<<<2 * pairs, kThreads, kSmem, stream>>>(p);
+  else
+    scaled_kernel<<<2 * pairs, kScaledThreads, kScaledSmem, stream>>>(p);
   return cudaGetLastError();
 }
 

@@ -203,11 +203,12 @@ __global__ void __launch_bounds__(kThreads) matmul_simple_kernel(MatmulArgs a) {
           [&](int k, int n) {
             return col0 + n < a.n && k0 + k < a.k ? e4m3_values(a.b[(col0 + n) * a.k + k0 + k]).x : 0.0f;
           });
-    const float sb = a.sb[blockIdx.y * nb + kb];
+    const auto scale = [&](float s) { return a.any_scales ? s : power_of_two(s); };
+    const float sb = scale(a.sb[blockIdx.y * nb + kb]);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int64_t row = row0 + ty + 8 * i;
-      const float s = row < a.m ? a.sa[row * nb + kb] * sb : 0.0f;
+      const float s = row < a.m ? scale(a.sa[row * nb + kb]) * sb : 0.0f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) sum.v[i][j] = fmaf(c.v[i][j], s, sum.v[i][j]);
     }

@@ -183,6 +183,31 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t
 #undef TIDE_MMA
 }
 
+// Instruction descriptor of the block-scaled 8-bit form: e4m3 operands, both
+// K-major, scales that are powers of two (E8M0).
+constexpr uint32_t instr_desc_scaled(uint32_t m, uint32_t n) { return ((n >> 3) << 17) | (1u << 23) | ((m >> 4) << 24); }
+
+// D (+)= (A * scales) (B * scales) for 32 steps of the contraction by a pair.
+// A's scale of row r lies in column r / 32 of sa, lane r % 32 of each of the
+// four groups of 32 lanes, and B's alike; a scale for 32 steps is one byte of
+// that column's word.
+__device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
+                                           bool add) {
+  const uint32_t p = add ? 1u : 0u;
+  asm volatile(
+      "{ .reg .pred p; setp.ne.b32 p, %6, 0;\n tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X"
+      " [%0], %1, %2, %3, [%4], [%5], p; }" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(p)
+      : "memory");
+}
+
+// Four or eight columns of this warp's TMEM lanes, one lane a thread.
+__device__ __forceinline__ void tmem_write4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_written() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
 // Arrives on `bar` (at this address in both CTAs of a pair) once the MMAs
 // issued so far have completed.
 template <int GROUP>

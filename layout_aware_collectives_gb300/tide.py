@@ -103,7 +103,7 @@ _sig("tide_compute_check_device", _st, _vp)
 _sig("tide_compute_set_test_stall", _st, _vp, _i64)
 _sig("tide_fp8_store", _st, _vp, _i64, _i64, _vp, _i64, _vp, _vp, ctypes.c_int32, _vp)
 _sig("tide_fp8_restore", _st, _vp, _i64, _i64, _vp, _vp, ctypes.c_int32, _vp, _i64, _vp)
-_sig("tide_fp8_matmul", _st, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _vp)
+_sig("tide_fp8_matmul", _st, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, ctypes.c_int32, _vp, _i64, _vp)
 _sig("tide_gated_forward", _st, _vp, _i64, _i64, _i64, ctypes.c_int, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _vp)
 _sig("tide_gated_workspace", _st, _i64, _i64, _i64, _i64p)
 _sig("tide_gated_backward", _st, _vp, _i64, _i64, _i64, ctypes.c_int, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i64,
@@ -418,10 +418,10 @@ def tide_fp8_restore(compute, rows, cols, codes, scales, block_rows, dst, ld_dst
                                  _stream(stream)), "tide_fp8_restore")
 
 
-def tide_fp8_matmul(compute, m, n, k, a, a_scales, b, b_scales, out, ld_out, stream=None) -> None:
+def tide_fp8_matmul(compute, m, n, k, a, a_scales, b, b_scales, any_scales, out, ld_out, stream=None) -> None:
     """out [m, n] = a [m, k] b [n, k]^T, a in 1 x 128 blocks and b in 128 x 128."""
-    _check(_lib.tide_fp8_matmul(compute, m, n, k, _addr(a), _addr(a_scales), _addr(b), _addr(b_scales), _addr(out),
-                                ld_out, _stream(stream)), "tide_fp8_matmul")
+    _check(_lib.tide_fp8_matmul(compute, m, n, k, _addr(a), _addr(a_scales), _addr(b), _addr(b_scales),
+                                1 if any_scales else 0, _addr(out), ld_out, _stream(stream)), "tide_fp8_matmul")
 
 
 def _checkpoint(c):

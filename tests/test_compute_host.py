@@ -102,7 +102,7 @@ def test_null_handle_refused():
     assert lib.tide_compute_create(None) == BAD
     assert lib.tide_fp8_store(None, 1, 1, A, 1, A, A, 1, None) == BAD
     assert lib.tide_fp8_restore(None, 1, 1, A, A, 1, A, 1, None) == BAD
-    assert lib.tide_fp8_matmul(None, 1, 1, 1, A, A, A, A, A, 1, None) == BAD
+    assert lib.tide_fp8_matmul(None, 1, 1, 1, A, A, A, A, 0, A, 1, None) == BAD
     assert lib.tide_gated_forward(None, 1, 1, 1, 0, A, 1, A, A, A, 1, None, None) == BAD
     assert lib.tide_gated_backward(None, 1, 1, 1, 0, A, 1, A, 1, A, A, None, A, 1, A, A, None, 1, A, 1 << 20, None) == BAD
     assert lib.tide_gated_workspace(1, 1, 1, None) == BAD

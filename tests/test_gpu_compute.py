@@ -133,22 +133,51 @@ MATMUL_SHAPES = [(1, 128, 128), (1, 8, 16), (2, 264, 400), (3, 1, 1), (7, 130, 1
                  (300, 5000, 272), (64, 136, 8192), (70, 1160, 1296)]
 
 
-def fp8(g, rows, cols, block_rows, scale=1.0):
-    v = torch.randn(rows, cols, generator=g, device="cuda") * scale
+def fp8(g, rows, cols, block_rows, any_scales=False):
+    v = torch.randn(rows, cols, generator=g, device="cuda")
     codes = (v * 64).clamp(-448, 448).to(torch.float8_e4m3fn)
-    scales = torch.randn(-(-rows // block_rows), -(-cols // 128), generator=g, device="cuda").exp()
-    return codes, scales
+    shape = -(-rows // block_rows), -(-cols // 128)
+    if any_scales:
+        return codes, torch.randn(*shape, generator=g, device="cuda").exp()
+    return codes, torch.exp2(torch.randint(-9, 10, shape, generator=g, device="cuda").float())
 
 
 @pytest.mark.parametrize("m,n,k", MATMUL_SHAPES)
 @pytest.mark.parametrize("pad", [0, 1, 8])
-def test_matmul(compute, m, n, k, pad):
+@pytest.mark.parametrize("any_scales", [False, True])
+def test_matmul(compute, m, n, k, pad, any_scales):
     g = gen(m + n + k)
-    (a, sa), (b, sb) = fp8(g, m, k, 1), fp8(g, n, k, 128)
+    (a, sa), (b, sb) = fp8(g, m, k, 1, any_scales), fp8(g, n, k, 128, any_scales)
     out = Guarded(m, n, n + pad)
-    compute.fp8_matmul(m, n, k, a, sa, b, sb, out, ld_out=n + pad)
+    compute.fp8_matmul(m, n, k, a, sa, b, sb, out, any_scales=any_scales, ld_out=n + pad)
     close(out.view, *ref.matmul(a, sa, b, sb))
     assert out.intact()
+
+
+@pytest.mark.parametrize("m,n,k", [(3, 264, 512), (300, 5000, 272), (5, 130, 129)])
+@pytest.mark.parametrize("bad", [1.5, 0.0, -2.0, math.inf, math.nan, 1e-40])
+def test_matmul_scale_that_is_no_power_of_two(compute, m, n, k, bad):
+    g = gen(77)
+    (a, sa), (b, sb) = fp8(g, m, k, 1), fp8(g, n, k, 128)
+    sa[1, 1], sb[1, 0] = bad, bad
+    out = Guarded(m, n)
+    compute.fp8_matmul(m, n, k, a, sa, b, sb, out)
+    nan = torch.zeros(m, n, dtype=torch.bool, device="cuda")
+    nan[1], nan[:, 128:256] = True, True
+    assert torch.equal(torch.isnan(out.view), nan) and out.intact()
+
+
+@pytest.mark.parametrize("m,n", [(4, 264), (300, 5000)])
+def test_matmul_extreme_scales(compute, m, n):
+    """Scales over their whole range; results that fp32 holds keep their value."""
+    k = 384
+    g = gen(78)
+    (a, sa), (b, sb) = fp8(g, m, k, 1), fp8(g, n, k, 128)
+    up = torch.randint(0, 2, (m, 1), generator=g, device="cuda").float() * 200 - 100  # 2^-100 or 2^100 a row
+    sa, sb = torch.exp2(up).expand(m, 3).contiguous(), torch.exp2(torch.zeros_like(sb))
+    out = Guarded(m, n)
+    compute.fp8_matmul(m, n, k, a, sa, b, sb, out)
+    close(out.view, *ref.matmul(a, sa, b, sb))
 
 
 def test_matmul_empty_sum(compute):
@@ -159,14 +188,16 @@ def test_matmul_empty_sum(compute):
 
 def test_matmul_nan_stays_in_its_row_and_column(compute):
     g = gen(5)
-    (a, sa), (b, sb) = fp8(g, 140, 512, 1), fp8(g, 264, 512, 128)
-    a.view(torch.uint8)[3, 200] = 0x7F
-    b.view(torch.uint8)[129, 17] = 0xFF
-    out = Guarded(140, 264)
-    compute.fp8_matmul(140, 264, 512, a, sa, b, sb, out)
-    nan = torch.zeros(140, 264, dtype=torch.bool, device="cuda")
-    nan[3], nan[:, 129] = True, True
-    assert torch.equal(torch.isnan(out.view), nan)
+    for m, n in ((20, 264), (140, 5000)):
+        for any_scales in (False, True):
+            (a, sa), (b, sb) = fp8(g, m, 512, 1), fp8(g, n, 512, 128)
+            a.view(torch.uint8)[3, 200] = 0x7F
+            b.view(torch.uint8)[129, 17] = 0xFF
+            out = Guarded(m, n)
+            compute.fp8_matmul(m, n, 512, a, sa, b, sb, out, any_scales=any_scales)
+            nan = torch.zeros(m, n, dtype=torch.bool, device="cuda")
+            nan[3], nan[:, 129] = True, True
+            assert torch.equal(torch.isnan(out.view), nan)
 
 
 # --------------------------------------------------------------------- gated
@@ -432,10 +463,16 @@ def test_wait_that_runs_out_is_reported():
     g = gen(30)
     x, (wg, wu), dh = randn(g, tokens, hidden), weights(g, hidden, ffn), randn(g, tokens, ffn)
     h = Guarded(tokens, ffn)
+    (a, sa), (b, sb) = fp8(g, 2000, hidden, 1), fp8(g, 5000, hidden, 128)
+    out = Guarded(2000, 5000)
     with tide.Compute() as c:
         c.check_device()
         c.set_test_stall(1_000_000)
         for call in (lambda: c.gated_forward(tokens, hidden, ffn, x, wg, wu, h),
+                     lambda: c.gated_forward(2, hidden, ffn, x, wg, wu, h),
+                     lambda: c.fp8_matmul(2000, 5000, hidden, a, sa, b, sb, out),
+                     lambda: c.fp8_matmul(2000, 5000, hidden, a, sa, b, sb, out, any_scales=True),
+                     lambda: c.fp8_matmul(2, 5000, hidden, a, sa, b, sb, out),
                      lambda: run_backward(c, tokens, hidden, ffn, "silu", dh, x, wg, wu)):
             call()
             with pytest.raises(tide.TideError) as e:
