@@ -222,7 +222,7 @@ constexpr int kOdd = 160;
 constexpr int kShared = 3;  // chunks of 32 columns
 constexpr int kScales = 416;
 constexpr int kScaledThreads = 384;  // loads, MMAs, -, -, 4 warps of results, 4 of scales
-constexpr int kScaledBoxes = 4;
+constexpr int kScaledBoxes = 3;
 constexpr size_t kScaledSmem = 1024 + kStages * kStage + 4 * kScaledBoxes * kBox;
 
 __global__ void __cluster_dims__(2, 1, 1)
@@ -230,6 +230,7 @@ __global__ void __cluster_dims__(2, 1, 1)
   constexpr uint32_t kInstr = instr_desc_scaled(256, 256);
   extern __shared__ uint8_t raw[];
   __shared__ uint64_t bars[2 * kStages + 3];
+  __shared__ uint32_t words[2][4][kHalf];  // scales of two batches of four blocks
   __shared__ uint32_t tmem_at;
   __shared__ int stop;
 
@@ -321,45 +322,51 @@ __global__ void __cluster_dims__(2, 1, 1)
     }
   } else if (warp >= 8) {
     // Scales.  Every warp writes all 128 rows' (A, 4 columns) and both column
-    // blocks' (B, 8 columns) to its own 32 lanes.  They are fetched four
-    // blocks at a time, a batch ahead.
-    const uint32_t mine = tmem + ((uint32_t)(warp & 3) * 32 << 16) + kScales;
-    int j = 0;
+    // blocks' (B, 8 columns) to its own 32 lanes.  Four blocks at a time, a
+    // batch ahead, each warp fetches 32 rows' and the four exchange them: a
+    // load that touches 32 rows takes L1 32 cycles, and with every warp
+    // fetching all rows these loads were 40% slower than the products.
+    const int w = warp & 3;
+    const uint32_t mine = tmem + ((uint32_t)w * 32 << 16) + kScales;
+    int j = 0, batch = 0;
     bool go = true;
-    for (int t = pair; t < p.tiles && go; t += pairs) {
+    for (int t = pair; t < p.tiles; t += pairs) {
       const TileAt at = tile_at(p.tiles_m, p.tiles_n, t);
-      const float* from[6];  // rows and columns past the end take any scale that is there
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        from[c] = p.sa + (int64_t)min((int)(at.m * 2 + rank) * kHalf + c * 32 + lane, p.rows - 1) * p.blocks;
-#pragma unroll
-      for (int c = 0; c < 2; ++c) from[4 + c] = p.sb + (int64_t)min(at.n * 2 + c, (p.cols - 1) / kBlock) * p.blocks;
-      float next[6][4];
+      // rows and columns past the end take any scale that is there
+      const float* sa = p.sa + (int64_t)min((int)(at.m * 2 + rank) * kHalf + w * 32 + lane, p.rows - 1) * p.blocks;
+      const float* sb = p.sb + (int64_t)min(at.n * 2 + (lane & 1), (p.cols - 1) / kBlock) * p.blocks;
+      float next_a[4], next_b[4];
       const auto fetch = [&](int k) {
 #pragma unroll
-        for (int c = 0; c < 6; ++c)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) next[c][q] = __ldg(from[c] + min(k + q, p.blocks - 1));
+        for (int q = 0; q < 4; ++q) {
+          next_a[q] = __ldg(sa + min(k + q, p.blocks - 1));
+          next_b[q] = __ldg(sb + min(k + q, p.blocks - 1));
+        }
       };
       fetch(0);
-      for (int k = 0; k < p.blocks && go; k += 4) {
-        uint32_t now[6][4];
-#pragma unroll
-        for (int c = 0; c < 6; ++c)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) now[c][q] = exponent_bytes(next[c][q]);
-        if (k + 4 < p.blocks) fetch(k + 4);
+      for (int k = 0; k < p.blocks; k += 4, ++batch) {
+        uint32_t b[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          if (k + q >= p.blocks || !go) break;
+          words[batch & 1][q][w * 32 + lane] = exponent_bytes(next_a[q]);
+          b[q] = exponent_bytes(next_b[q]);
+        }
+        if (k + 4 < p.blocks) fetch(k + 4);
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (k + q >= p.blocks) break;
           const int s = j % kStages;
-          go = j < kStages || bar_wait_warp(empty(s), (j / kStages + 1) & 1, watch);
-          if (!go) break;
+          // a warp whose wait ran out goes on meeting the others at the barrier
+          go = go && (j < kStages || bar_wait_warp(empty(s), (j / kStages + 1) & 1, watch));
+          if (!go) continue;
           fence_after();
           const uint32_t to = mine + s * 12;
-          tmem_write4(to, now[0][q], now[1][q], now[2][q], now[3][q]);
-          tmem_write4(to + 4, now[4][q], now[4][q], now[4][q], now[4][q]);
-          tmem_write4(to + 8, now[5][q], now[5][q], now[5][q], now[5][q]);
+          const uint32_t b0 = __shfl_sync(0xffffffffu, b[q], 0), b1 = __shfl_sync(0xffffffffu, b[q], 1);
+          const uint32_t* row = words[batch & 1][q] + lane;
+          tmem_write4(to, row[0], row[32], row[64], row[96]);
+          tmem_write4(to + 4, b0, b0, b0, b0);
+          tmem_write4(to + 8, b1, b1, b1, b1);
           tmem_written();
           fence_before();
           __syncwarp();
