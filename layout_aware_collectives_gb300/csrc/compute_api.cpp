@@ -302,22 +302,23 @@ tide_status_t tide_gated_backward(tide_compute_t c, int64_t tokens, int64_t hidd
   a.du = (uint16_t*)((char*)workspace + w.du);
   const TcLaunch l = launch_of(c);
   const bool tc = gated_tc_takes(a);
+  Fp8Args xr{};
+  if (x8 && dw_gate && hidden) {  // the restored input takes x's place
+    xr = Fp8Args{tokens, hidden, hidden, (uint16_t*)((char*)workspace + w.x), ck->x_codes, ck->x_scales, 1};
+    a.x = xr.bf16, a.ldx = hidden;
+  }
   if (ck)
-    TIDE_TRY(launched(launch_gated_grad_stored(a, stream), what));
+    TIDE_TRY(launched(launch_gated_grad_stored(a, xr, stream), what));
   else if (tc && ld_x % 8 == 0 && ld_dh % 8 == 0 && (!h || ld_h % 8 == 0))
     TIDE_TRY(launched(launch_gated_grad_tc(a, l, stream), what));
   else
     TIDE_TRY(launched(launch_gated_grad_simple(a, stream), what));
   if (hidden == 0) return TIDE_OK;
-  if (dx) TIDE_TRY(launched(tc && ld_dx % 8 == 0 ? launch_gated_dx_tc(a, l, stream) : launch_gated_dx_simple(a, stream), what));
-  if (!dw_gate) return TIDE_OK;
-  if (x8) {
-    uint16_t* xr = (uint16_t*)((char*)workspace + w.x);
-    const Fp8Args r{tokens, hidden, hidden, xr, ck->x_codes, ck->x_scales, 1};
-    TIDE_TRY(launched(launch_fp8_restore(r, stream), what));
-    a.x = xr, a.ldx = hidden;
-  }
-  return launched(tc && a.ldx % 8 == 0 ? launch_gated_dw_tc(a, l, stream) : launch_gated_dw_simple(a, stream), what);
+  const bool dx_tc = dx && tc && ld_dx % 8 == 0, dw_tc = dw_gate && tc && a.ldx % 8 == 0;
+  if (dx_tc || dw_tc) TIDE_TRY(launched(launch_gated_back_tc(a, dx_tc, dw_tc, l, stream), what));
+  if (dx && !dx_tc) TIDE_TRY(launched(launch_gated_dx_simple(a, stream), what));
+  if (dw_gate && !dw_tc) TIDE_TRY(launched(launch_gated_dw_simple(a, stream), what));
+  return TIDE_OK;
 }
 
 }  // extern "C"

@@ -67,8 +67,9 @@ struct MatmulArgs {
 cudaError_t launch_fp8_store(const Fp8Args& a, cudaStream_t stream);
 cudaError_t launch_fp8_restore(const Fp8Args& a, cudaStream_t stream);
 
-// dG, dU (and h) from the checkpoint's codes (fp8_blocks.cu).
-cudaError_t launch_gated_grad_stored(const GatedArgs& a, cudaStream_t stream);
+// dG, dU (and h) from the checkpoint's codes, and the input from its own
+// where `x` has any (fp8_blocks.cu).
+cudaError_t launch_gated_grad_stored(const GatedArgs& a, const Fp8Args& x, cudaStream_t stream);
 
 // Plain tiled kernels for every size and stride (gated_simple.cu).
 cudaError_t launch_gated_forward_simple(const GatedArgs& a, cudaStream_t stream);
@@ -91,8 +92,8 @@ int gated_tc_pairs();
 bool gated_tc_takes(const GatedArgs& a);
 cudaError_t launch_gated_forward_tc(const GatedArgs& a, const TcLaunch& l, cudaStream_t stream);
 cudaError_t launch_gated_grad_tc(const GatedArgs& a, const TcLaunch& l, cudaStream_t stream);
-cudaError_t launch_gated_dx_tc(const GatedArgs& a, const TcLaunch& l, cudaStream_t stream);
-cudaError_t launch_gated_dw_tc(const GatedArgs& a, const TcLaunch& l, cudaStream_t stream);
+// dX, dWg and dWu, or either.
+cudaError_t launch_gated_back_tc(const GatedArgs& a, bool dx, bool dw, const TcLaunch& l, cudaStream_t stream);
 
 // Tensor-core product of 8-bit blocks (fp8_tc.cu): k a multiple of 16, n and
 // the output's stride of 8.

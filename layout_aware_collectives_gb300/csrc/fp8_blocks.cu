@@ -211,13 +211,13 @@ __device__ __forceinline__ float scale_at(const Fp8Args& a, int64_t blocks_per_r
 // time (8 bytes of codes, 16 of bf16) whatever the width; a group of 8 that
 // passes a block's or a row's end looks its scales up one by one.
 template <int U, class Index>
-__global__ void __launch_bounds__(kThreads) restore_flat_kernel(Fp8Args a, int64_t blocks_per_row, Index numel) {
+__device__ __forceinline__ void restore_flat(const Fp8Args& a, int64_t blocks_per_row, Index numel, unsigned cta) {
   const Index cols = (Index)a.cols;
   uint2 c[U];
   Index at[U];
 #pragma unroll
   for (int i = 0; i < U; ++i) {
-    at[i] = (((Index)blockIdx.x * U + i) * kThreads + threadIdx.x) * 8;
+    at[i] = (((Index)cta * U + i) * kThreads + threadIdx.x) * 8;
     c[i] = make_uint2(0, 0);
     if (at[i] + 8 <= numel) c[i] = __ldcs((const uint2*)(a.codes + at[i]));
   }
@@ -256,6 +256,11 @@ __global__ void __launch_bounds__(kThreads) restore_flat_kernel(Fp8Args a, int64
   }
 }
 
+template <int U, class Index>
+__global__ void __launch_bounds__(kThreads) restore_flat_kernel(Fp8Args a, int64_t blocks_per_row, Index numel) {
+  restore_flat<U>(a, blocks_per_row, numel, blockIdx.x);
+}
+
 // Strided destination rows: one element a thread and step.
 __global__ void __launch_bounds__(kThreads) restore_any_kernel(Fp8Args a, int64_t blocks_per_row, int64_t numel) {
   for (int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x; e < numel; e += (int64_t)gridDim.x * kThreads) {
@@ -269,9 +274,17 @@ __global__ void __launch_bounds__(kThreads) restore_any_kernel(Fp8Args a, int64_
 // dU = dh act(g), dG = dh u act'(g) and, where asked, h = act(g) u, with g
 // and u read from their codes: 4 bytes in and 4 (6) out an element, so the
 // pre-activations are never spelled out in memory.  V = 8 columns a thread
-// where rows allow 16-byte accesses, else 1.
+// where rows allow 16-byte accesses, else 1.  CTAs past the gradients'
+// restore the input `x`, if it is kept in 8 bits too: one launch for both.
+constexpr int kRestoreUnroll = 4;
+
 template <int ACT, int V, class Index>
-__global__ void __launch_bounds__(kThreads) grad_stored_kernel(GatedArgs a, Index groups_per_row, Index groups) {
+__global__ void __launch_bounds__(kThreads)
+    grad_stored_kernel(GatedArgs a, Index groups_per_row, Index groups, unsigned ctas, Fp8Args x) {
+  if (blockIdx.x >= ctas) {
+    restore_flat<kRestoreUnroll, Index>(x, (x.cols + kBlock - 1) / kBlock, (Index)(x.rows * x.cols), blockIdx.x - ctas);
+    return;
+  }
   const int64_t nb = (a.ffn + kBlock - 1) / kBlock;
   const Index i = (Index)blockIdx.x * kThreads + threadIdx.x;
   if (i >= groups) return;
@@ -321,19 +334,20 @@ __global__ void __launch_bounds__(kThreads) grad_stored_kernel(GatedArgs a, Inde
 }
 
 template <int ACT>
-cudaError_t grad_stored(const GatedArgs& a, cudaStream_t stream) {
+cudaError_t grad_stored(const GatedArgs& a, const Fp8Args& x, cudaStream_t stream) {
   const bool vec = a.ffn % 8 == 0 && a.lddh % 8 == 0 && (!a.h || a.ldh % 8 == 0);
-  const int64_t per_row = vec ? a.ffn / 8 : a.ffn, groups = per_row * a.tokens;
-  const unsigned grid = (unsigned)ceil_div(groups, kThreads);
-  const bool small = groups <= kSmall;
+  const int64_t per_row = vec ? a.ffn / 8 : a.ffn, groups = per_row * a.tokens, more = x.rows * x.cols;
+  const unsigned ctas = (unsigned)ceil_div(groups, kThreads);
+  const unsigned grid = ctas + (unsigned)ceil_div(more, (int64_t)kThreads * 8 * kRestoreUnroll);
+  const bool small = groups <= kSmall && more <= kSmall;
   if (vec && small)
-    grad_stored_kernel<ACT, 8, uint32_t><<<grid, kThreads, 0, stream>>>(a, (uint32_t)per_row, (uint32_t)groups);
+    grad_stored_kernel<ACT, 8, uint32_t><<<grid, kThreads, 0, stream>>>(a, (uint32_t)per_row, (uint32_t)groups, ctas, x);
   else if (vec)
-    grad_stored_kernel<ACT, 8, int64_t><<<grid, kThreads, 0, stream>>>(a, per_row, groups);
+    grad_stored_kernel<ACT, 8, int64_t><<<grid, kThreads, 0, stream>>>(a, per_row, groups, ctas, x);
   else if (small)
-    grad_stored_kernel<ACT, 1, uint32_t><<<grid, kThreads, 0, stream>>>(a, (uint32_t)per_row, (uint32_t)groups);
+    grad_stored_kernel<ACT, 1, uint32_t><<<grid, kThreads, 0, stream>>>(a, (uint32_t)per_row, (uint32_t)groups, ctas, x);
   else
-    grad_stored_kernel<ACT, 1, int64_t><<<grid, kThreads, 0, stream>>>(a, per_row, groups);
+    grad_stored_kernel<ACT, 1, int64_t><<<grid, kThreads, 0, stream>>>(a, per_row, groups, ctas, x);
   return cudaGetLastError();
 }
 
@@ -368,12 +382,11 @@ cudaError_t launch_fp8_store(const Fp8Args& a, cudaStream_t stream) {
 cudaError_t launch_fp8_restore(const Fp8Args& a, cudaStream_t stream) {
   const int64_t per_row = ceil_div(a.cols, kBlock), numel = a.rows * a.cols;
   if (a.ld == a.cols) {
-    constexpr int kUnroll = 4;
-    const unsigned grid = (unsigned)ceil_div(numel, (int64_t)kThreads * 8 * kUnroll);
+    const unsigned grid = (unsigned)ceil_div(numel, (int64_t)kThreads * 8 * kRestoreUnroll);
     if (numel <= kSmall)
-      restore_flat_kernel<kUnroll, uint32_t><<<grid, kThreads, 0, stream>>>(a, per_row, (uint32_t)numel);
+      restore_flat_kernel<kRestoreUnroll, uint32_t><<<grid, kThreads, 0, stream>>>(a, per_row, (uint32_t)numel);
     else
-      restore_flat_kernel<kUnroll, int64_t><<<grid, kThreads, 0, stream>>>(a, per_row, numel);
+      restore_flat_kernel<kRestoreUnroll, int64_t><<<grid, kThreads, 0, stream>>>(a, per_row, numel);
   } else {
     const int64_t grid = ceil_div(numel, kThreads);
     restore_any_kernel<<<(unsigned)(grid < 65536 ? grid : 65536), kThreads, 0, stream>>>(a, per_row, numel);
@@ -381,8 +394,8 @@ cudaError_t launch_fp8_restore(const Fp8Args& a, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-cudaError_t launch_gated_grad_stored(const GatedArgs& a, cudaStream_t stream) {
-  return a.act == TIDE_ACT_SILU ? grad_stored<TIDE_ACT_SILU>(a, stream) : grad_stored<TIDE_ACT_GELU>(a, stream);
+cudaError_t launch_gated_grad_stored(const GatedArgs& a, const Fp8Args& x, cudaStream_t stream) {
+  return a.act == TIDE_ACT_SILU ? grad_stored<TIDE_ACT_SILU>(a, x, stream) : grad_stored<TIDE_ACT_GELU>(a, x, stream);
 }
 
 }  // namespace tide

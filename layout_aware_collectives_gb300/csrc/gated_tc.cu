@@ -1,9 +1,10 @@
 // The gated block's products on the tensor cores, one persistent kernel in
-// four forms:
+// three forms:
 //   forward   [gate | up] = x [Wg | Wu]^T, then h (and the 8-bit checkpoint)
 //   grad      the same products again, then dG, dU (and h) from dh
-//   dx        dX = [dG dU] [Wg; Wu], one sum over both halves
-//   dw        dWg = dG^T x and dWu = dU^T x
+//   back      dX = [dG dU] [Wg; Wu], one sum over both halves, and
+//             dWg = dG^T x, dWu = dU^T x: independent tiles of one launch, so
+//             that neither waits for the other's last ones
 //
 // A pair of CTAs (two SMs) works on one 256 x 256 tile of sums: each CTA
 // loads 128 rows of A and half of B's 256 columns, one MMA instruction of the
@@ -25,7 +26,7 @@ namespace {
 
 using namespace tc;
 
-enum Form { kForward = 0, kGrad = 1, kDx = 2, kDw = 3 };
+enum Form { kForward = 0, kGrad = 1, kBack = 2 };
 
 constexpr int kStages = 6;
 constexpr int kStep = 64;                     // contraction of one stage
@@ -38,12 +39,15 @@ constexpr int kBoxes = 4;                     // boxes in flight for each warp
 constexpr size_t kSmem = 1024 + kStages * kStage + kEpiWarps * kBoxes * kBox;
 
 struct Params {
-  CUtensorMap a[2], b[2];  // the two halves (gate, up) of each operand, where a form has two
-  CUtensorMap out[3];      // forward: h; grad: dG, dU, h; dx: dX; dw: dWg, dWu
-  int rows, cols;          // of one output
+  // forward, grad: a = x, b = Wg, Wu; out = h, or dG, dU, h
+  // back: dX: a = dG, dU, b = Wg, Wu, out[0]; dW: wa = dG, dU, wb = x, out[1..2]
+  CUtensorMap a[2], b[2], wa[2], wb, out[3];
+  int rows, cols;  // of the outputs (back: of dX)
   int tiles_m, tiles_n, tiles;
-  int steps;               // stages of one tile's sum
-  int half_steps;          // dx: stages of the first half
+  int steps;       // stages of one tile's sum
+  int half_steps;  // back: stages of dX's first half
+  int w_rows, w_tiles_m, w_tiles_n, w_tiles, w_steps;  // back: dW, both halves' tiles
+  int extra;       // back: tiles of dW that take as long as one of dX
   // epilogue
   uint8_t *g8, *u8;
   float *gs, *us;
@@ -77,10 +81,53 @@ __device__ __forceinline__ void put_codes(uint8_t* dst, const uint32_t (&v)[32],
   }
 }
 
+// One tile of a pair's work.
+struct Work {
+  TileAt at;
+  bool w;  // a tile of dW
+  int steps;
+};
+
+// The pair's i-th tile; false past the last.  Tiles go round the pairs in
+// turn.  In the back form dX's tiles come first; where they do not come out
+// even, the pairs that are one short take `extra` tiles of dW before the
+// rest goes round, beginning with them again.
+template <int FORM>
+__device__ __forceinline__ bool work_at(const Params& p, int pair, int pairs, int i, Work& r) {
+  int t = pair + i * pairs;
+  r.w = false;
+  r.steps = p.steps;
+  if (FORM != kBack || t < p.tiles) {
+    if (t >= p.tiles) return false;
+    r.at = tile_at(p.tiles_m, p.tiles_n, t);
+    return true;
+  }
+  i -= pair < p.tiles ? (p.tiles - pair + pairs - 1) / pairs : 0;
+  const int full = p.tiles % pairs;  // pairs with one more tile than the others
+  const int light = pairs - full, l = pair - full;
+  int first = 0;
+  if (full) {
+    first = min(p.w_tiles, light * p.extra);
+    if (l >= 0) {
+      const int mine = l < first ? (first - l + light - 1) / light : 0;
+      t = l + i * light;
+      if (i < mine) first = -1;
+      i -= mine;
+    }
+  }
+  if (first >= 0) t = first + (l >= 0 ? l : light + pair) + i * pairs;
+  if (t >= p.w_tiles) return false;
+  r.w = true;
+  r.steps = p.w_steps;
+  r.at = tile_at(p.w_tiles_m, p.w_tiles_n, t);
+  return true;
+}
+
 template <int FORM, int ACT>
-__device__ __forceinline__ void epilogue(const Params& p, const TileAt& t, uint32_t tmem, int row0, Outbox<kBoxes>& out) {
-  const int row = row0 + out.lane;
-  const bool any = row0 < p.rows, mine = row < p.rows;
+__device__ __forceinline__ void epilogue(const Params& p, const Work& work, uint32_t tmem, int row0, Outbox<kBoxes>& out) {
+  const TileAt& t = work.at;
+  const int row = row0 + out.lane, rows = work.w ? p.w_rows : p.rows;
+  const bool any = row0 < rows, mine = row < rows;
   if constexpr (FORM == kForward || FORM == kGrad) {
     const int col0 = t.n * kHalf;
     float ginv = 0.0f, uinv = 0.0f;
@@ -161,7 +208,7 @@ __device__ __forceinline__ void epilogue(const Params& p, const TileAt& t, uint3
       }
     }
   } else {
-    const CUtensorMap* map = &p.out[FORM == kDw ? t.z : 0];
+    const CUtensorMap* map = &p.out[work.w ? 1 + t.z : 0];
 #pragma unroll 1
     for (int c = 0; c < 8; ++c) {
       const int col = t.n * 2 * kHalf + c * 32;
@@ -177,8 +224,7 @@ __device__ __forceinline__ void epilogue(const Params& p, const TileAt& t, uint3
 
 template <int FORM, int ACT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_constant__ Params p) {
-  constexpr bool kAMn = FORM == kDw, kBMn = FORM == kDx || FORM == kDw;
-  constexpr uint32_t kInstr = instr_desc(1, kAMn, kBMn, 256, 256);
+  constexpr bool kBMn = FORM == kBack;
   extern __shared__ uint8_t raw[];
   __shared__ uint64_t bars[2 * kStages + 5];
   __shared__ uint32_t tmem_at;
@@ -202,7 +248,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gated_t
     for (int b = 0; b < 2; ++b) bar_init(sums_full(b), 1), bar_init(sums_empty(b), 2 * kEpiWarps);
     bar_init(spare, 1);
     bar_init_fence();
-    for (int i = 0; i < 2; ++i) prefetch_map(&p.a[i]), prefetch_map(&p.b[i]);
+    prefetch_map(FORM == kBack && !p.tiles ? &p.wa[0] : &p.a[0]), prefetch_map(FORM == kBack && !p.tiles ? &p.wb : &p.b[0]);
   }
   if (warp == 2) tmem_alloc<2>(smem_addr(&tmem_at), 512);
   fence_before();
@@ -217,9 +263,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gated_t
     if (lane == 0) {
       int j = 0;  // stages filled so far
       bool go = true;
-      for (int t = pair; t < p.tiles && go; t += pairs) {
-        const TileAt at = tile_at(p.tiles_m, p.tiles_n, t);
-        for (int k = 0; k < p.steps; ++k, ++j) {
+      Work work;
+      for (int i = 0; go && work_at<FORM>(p, pair, pairs, i, work); ++i) {
+        const TileAt& at = work.at;
+        const int row = (at.m * 2 + rank) * kHalf, col = (at.n * 2 + rank) * kHalf;
+        for (int k = 0; k < work.steps; ++k, ++j) {
           const int s = j % kStages;
           if (j >= kStages && !bar_wait(empty(s), (j / kStages + 1) & 1, watch)) {
             go = false;
@@ -228,20 +276,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gated_t
           if (rank == 0) bar_expect(full(s), 2 * kStage);
           const uint32_t bar = peer_addr(full(s), 0);
           const uint32_t a = smem + s * kStage, b = a + kOperand;
-          const int second = FORM == kDx && k >= p.half_steps;
-          const int k0 = (k - (second ? p.half_steps : 0)) * kStep;
-          const int row = (at.m * 2 + rank) * kHalf, col = (at.n * 2 + rank) * kHalf;
-          if constexpr (kAMn) {
-            load_box<true>(a, &p.a[at.z], row, k0, bar);
-            load_box<true>(a + kOperand / 2, &p.a[at.z], row + 64, k0, bar);
+          if constexpr (FORM != kBack) {
+            load_box<true>(a, &p.a[0], k * kStep, row, bar);
+            load_box<true>(b, &p.b[rank], k * kStep, at.n * kHalf, bar);
           } else {
-            load_box<true>(a, &p.a[second], k0, row, bar);
-          }
-          if constexpr (kBMn) {
-            load_box<true>(b, &p.b[second], col, k0, bar);
-            load_box<true>(b + kOperand / 2, &p.b[second], col + 64, k0, bar);
-          } else {
-            load_box<true>(b, &p.b[rank], k0, at.n * kHalf, bar);
+            const int second = !work.w && k >= p.half_steps, k0 = (k - (second ? p.half_steps : 0)) * kStep;
+            if (work.w) {
+              load_box<true>(a, &p.wa[at.z], row, k0, bar);
+              load_box<true>(a + kOperand / 2, &p.wa[at.z], row + 64, k0, bar);
+            } else {
+              load_box<true>(a, &p.a[second], k0, row, bar);
+            }
+            const CUtensorMap* mb = work.w ? &p.wb : &p.b[second];
+            load_box<true>(b, mb, col, k0, bar);
+            load_box<true>(b + kOperand / 2, mb, col + 64, k0, bar);
           }
         }
       }
@@ -259,11 +307,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gated_t
     if (lane == 0) {
       int j = 0, i = 0;  // stages used, tiles done
       bool go = true;
-      for (int t = pair; t < p.tiles && go; t += pairs, ++i) {
+      Work work;
+      for (; go && work_at<FORM>(p, pair, pairs, i, work); ++i) {
         const int b = i & 1;
+        const bool a_mn = FORM == kBack && work.w;
+        const uint32_t instr = instr_desc(1, 0, kBMn, 256, 256) | (a_mn ? instr_desc_a_mn : 0);
+        // a 32-byte step of the contraction lies 32 bytes on (K-major) or two
+        // groups of 8 rows on (MN-major)
+        const uint32_t a_lbo = a_mn ? kOperand / 2 : 16, a_next = (a_mn ? 2048 : 32) >> 4;
         if (i >= 2 && !bar_wait(sums_empty(b), (i / 2 + 1) & 1, watch)) break;
         fence_after();
-        for (int k = 0; k < p.steps; ++k, ++j) {
+        for (int k = 0; k < work.steps; ++k, ++j) {
           const int s = j % kStages;
           if (!bar_wait(full(s), (j / kStages) & 1, watch)) {
             go = false;
@@ -271,13 +325,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gated_t
           }
           fence_after();
           const uint32_t a = smem + s * kStage;
-          // a 32-byte step of the contraction lies 32 bytes on (K-major) or
-          // two groups of 8 rows on (MN-major)
-          const uint64_t da = operand_desc(a, kAMn ? kOperand / 2 : 16), db = operand_desc(a + kOperand, kBMn ? kOperand / 2 : 16);
+          const uint64_t da = operand_desc(a, a_lbo), db = operand_desc(a + kOperand, kBMn ? kOperand / 2 : 16);
 #pragma unroll
           for (int q = 0; q < kStep / 16; ++q)
-            mma<2, false>(tmem + b * 256, da + q * ((kAMn ? 2048 : 32) >> 4), db + q * ((kBMn ? 2048 : 32) >> 4), kInstr,
-                          k > 0 || q > 0);
+            mma<2, false>(tmem + b * 256, da + q * a_next, db + q * ((kBMn ? 2048 : 32) >> 4), instr, k > 0 || q > 0);
           mma_commit<2>(empty(s));
         }
         if (go) mma_commit<2>(sums_full(b));
@@ -290,14 +341,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gated_t
     }
   } else if (warp >= 4) {
     Outbox<kBoxes> out{smem + kStages * kStage + (warp - 4) * kBoxes * kBox, 0, lane};
-    int i = 0;
-    for (int t = pair; t < p.tiles; t += pairs, ++i) {
+    Work work;
+    for (int i = 0; work_at<FORM>(p, pair, pairs, i, work); ++i) {
       const int b = i & 1;
       if (!bar_wait_warp(sums_full(b), (i / 2) & 1, watch)) break;
       fence_after();
-      const TileAt at = tile_at(p.tiles_m, p.tiles_n, t);
       const uint32_t lanes = (uint32_t)(warp - 4) * 32;
-      epilogue<FORM, ACT>(p, at, tmem + (lanes << 16) + b * 256, (at.m * 2 + rank) * kHalf + lanes, out);
+      epilogue<FORM, ACT>(p, work, tmem + (lanes << 16) + b * 256, (work.at.m * 2 + rank) * kHalf + lanes, out);
       fence_before();
       __syncwarp();
       if (lane == 0) bar_arrive_peer(peer_addr(sums_empty(b), 0));
@@ -317,7 +367,7 @@ cudaError_t launch(Params& p, const TcLaunch& l, cudaStream_t stream) {
   p.err = l.err;
   p.limit_ns = TIDE_BULK_TIMEOUT_NS;
   p.stall_ns = l.stall_ns;
-  const int pairs = p.tiles < l.pairs ? p.tiles : l.pairs;
+  const int pairs = p.tiles + p.w_tiles < l.pairs ? p.tiles + p.w_tiles : l.pairs;
   gated_tc_kernel<FORM, ACT><<<2 * pairs, kThreads, kSmem, stream>>>(p);
   return cudaGetLastError();
 }
@@ -351,13 +401,13 @@ bool fill_pre(Params* p, const GatedArgs& a) {
 int gated_tc_pairs() {
   // The clusters the device holds at one time: a GPC with an odd number of
   // SMs leaves one without a partner.
-  cudaFuncSetAttribute(gated_tc_kernel<kDx, 0>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  cudaFuncSetAttribute(gated_tc_kernel<kBack, 0>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   cudaLaunchConfig_t c{};
   c.gridDim = dim3(2);
   c.blockDim = dim3(kThreads);
   c.dynamicSmemBytes = kSmem;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, gated_tc_kernel<kDx, 0>, &c) != cudaSuccess) return 0;
+  if (cudaOccupancyMaxActiveClusters(&n, gated_tc_kernel<kBack, 0>, &c) != cudaSuccess) return 0;
   return n;
 }
 
@@ -381,32 +431,32 @@ cudaError_t launch_gated_grad_tc(const GatedArgs& a, const TcLaunch& l, cudaStre
   return a.act == TIDE_ACT_SILU ? launch<kGrad, TIDE_ACT_SILU>(p, l, stream) : launch<kGrad, TIDE_ACT_GELU>(p, l, stream);
 }
 
-cudaError_t launch_gated_dx_tc(const GatedArgs& a, const TcLaunch& l, cudaStream_t stream) {
+cudaError_t launch_gated_back_tc(const GatedArgs& a, bool dx, bool dw, const TcLaunch& l, cudaStream_t stream) {
   Params p{};
-  p.rows = (int)a.tokens, p.cols = (int)a.hidden;
-  p.tiles_m = (int)ceil_div(a.tokens, 2 * kHalf), p.tiles_n = (int)ceil_div(a.hidden, 2 * kHalf);
-  p.tiles = p.tiles_m * p.tiles_n;
-  p.half_steps = (int)ceil_div(a.ffn, kStep), p.steps = 2 * p.half_steps;
-  if (!map_k(&p.a[0], a.dg, a.ffn, a.tokens, a.ffn) || !map_k(&p.a[1], a.du, a.ffn, a.tokens, a.ffn) ||
-      !map_mn(&p.b[0], a.wg, a.hidden, a.ffn, a.hidden) || !map_mn(&p.b[1], a.wu, a.hidden, a.ffn, a.hidden) ||
-      !map_out(&p.out[0], a.dx, a.hidden, a.tokens, a.lddx))
-    return cudaErrorInvalidValue;
-  return launch<kDx, 0>(p, l, stream);
-}
-
-cudaError_t launch_gated_dw_tc(const GatedArgs& a, const TcLaunch& l, cudaStream_t stream) {
-  Params p{};
-  p.rows = (int)a.ffn, p.cols = (int)a.hidden;
-  p.tiles_m = (int)ceil_div(a.ffn, 2 * kHalf), p.tiles_n = (int)ceil_div(a.hidden, 2 * kHalf);
-  if ((int64_t)p.tiles_m * p.tiles_n > INT32_MAX / 2) return cudaErrorInvalidValue;
-  p.tiles = 2 * p.tiles_m * p.tiles_n;
-  p.steps = (int)ceil_div(a.tokens, kStep);
-  if (!map_mn(&p.a[0], a.dg, a.ffn, a.tokens, a.ffn) || !map_mn(&p.a[1], a.du, a.ffn, a.tokens, a.ffn) ||
-      !map_mn(&p.b[0], a.x, a.hidden, a.tokens, a.ldx) || !map_out(&p.out[0], a.dwg, a.hidden, a.ffn, a.hidden) ||
-      !map_out(&p.out[1], a.dwu, a.hidden, a.ffn, a.hidden))
-    return cudaErrorInvalidValue;
-  p.b[1] = p.b[0];
-  return launch<kDw, 0>(p, l, stream);
+  p.cols = (int)a.hidden;
+  if (dx) {
+    p.rows = (int)a.tokens;
+    p.tiles_m = (int)ceil_div(a.tokens, 2 * kHalf), p.tiles_n = (int)ceil_div(a.hidden, 2 * kHalf);
+    p.tiles = p.tiles_m * p.tiles_n;
+    p.half_steps = (int)ceil_div(a.ffn, kStep), p.steps = 2 * p.half_steps;
+    if (!map_k(&p.a[0], a.dg, a.ffn, a.tokens, a.ffn) || !map_k(&p.a[1], a.du, a.ffn, a.tokens, a.ffn) ||
+        !map_mn(&p.b[0], a.wg, a.hidden, a.ffn, a.hidden) || !map_mn(&p.b[1], a.wu, a.hidden, a.ffn, a.hidden) ||
+        !map_out(&p.out[0], a.dx, a.hidden, a.tokens, a.lddx))
+      return cudaErrorInvalidValue;
+  }
+  if (dw) {
+    p.w_rows = (int)a.ffn;
+    p.w_tiles_m = (int)ceil_div(a.ffn, 2 * kHalf), p.w_tiles_n = (int)ceil_div(a.hidden, 2 * kHalf);
+    p.w_tiles = 2 * p.w_tiles_m * p.w_tiles_n;
+    p.w_steps = (int)ceil_div(a.tokens, kStep);
+    // what a tile of either takes: its stages, and about one for its way in and out
+    p.extra = (p.steps + 1 + (p.w_steps + 1) / 2) / (p.w_steps + 1);
+    if (!map_mn(&p.wa[0], a.dg, a.ffn, a.tokens, a.ffn) || !map_mn(&p.wa[1], a.du, a.ffn, a.tokens, a.ffn) ||
+        !map_mn(&p.wb, a.x, a.hidden, a.tokens, a.ldx) || !map_out(&p.out[1], a.dwg, a.hidden, a.ffn, a.hidden) ||
+        !map_out(&p.out[2], a.dwu, a.hidden, a.ffn, a.hidden))
+      return cudaErrorInvalidValue;
+  }
+  return launch<kBack, 0>(p, l, stream);
 }
 
 }  // namespace tide

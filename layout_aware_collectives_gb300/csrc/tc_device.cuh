@@ -167,6 +167,8 @@ constexpr uint32_t instr_desc(uint32_t ab, uint32_t a_mn, uint32_t b_mn, uint32_
   return (1u << 4) | (ab << 7) | (ab << 10) | (a_mn << 15) | (b_mn << 16) | ((n >> 3) << 17) | ((m >> 4) << 24);
 }
 
+constexpr uint32_t instr_desc_a_mn = 1u << 15;  // A's major, where it is known at run time
+
 // D (+)= A B for one step of the contraction (32 bytes of it).
 template <int GROUP, bool FP8>
 __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
