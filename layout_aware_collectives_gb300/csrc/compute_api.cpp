@@ -118,14 +118,15 @@ int64_t round256(int64_t v) { return (v + 255) / 256 * 256; }
 
 // Offsets of the workspace's parts.
 struct Workspace {
-  int64_t dg, du, x, bytes;
+  int64_t dg, du, x, parts, bytes;
 };
 Workspace workspace_of(int64_t tokens, int64_t hidden, int64_t ffn) {
   Workspace w;
   w.dg = 0;
   w.du = round256(2 * tokens * ffn);
   w.x = w.du + round256(2 * tokens * ffn);
-  w.bytes = w.x + round256(2 * tokens * hidden);
+  w.parts = w.x + round256(2 * tokens * hidden);
+  w.bytes = w.parts + round256(gated_parts_bytes(tokens, hidden));
   return w;
 }
 
@@ -300,6 +301,7 @@ tide_status_t tide_gated_backward(tide_compute_t c, int64_t tokens, int64_t hidd
   }
   a.dg = (uint16_t*)((char*)workspace + w.dg);
   a.du = (uint16_t*)((char*)workspace + w.du);
+  a.parts = (float*)((char*)workspace + w.parts), a.parts_bytes = w.bytes - w.parts;
   const TcLaunch l = launch_of(c);
   const bool tc = gated_tc_takes(a);
   Fp8Args xr{};
@@ -310,7 +312,7 @@ tide_status_t tide_gated_backward(tide_compute_t c, int64_t tokens, int64_t hidd
   if (ck)
     TIDE_TRY(launched(launch_gated_grad_stored(a, xr, stream), what));
   else if (tc && ld_x % 8 == 0 && ld_dh % 8 == 0 && (!h || ld_h % 8 == 0))
-    TIDE_TRY(launched(launch_gated_grad_tc(a, l, stream), what));
+    TIDE_TRY(launched(gated_few_takes(a, l.sms) ? launch_gated_grad_few(a, l, stream) : launch_gated_grad_tc(a, l, stream), what));
   else
     TIDE_TRY(launched(launch_gated_grad_simple(a, stream), what));
   if (hidden == 0) return TIDE_OK;

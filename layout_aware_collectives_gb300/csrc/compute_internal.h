@@ -50,6 +50,8 @@ struct GatedArgs {
   uint16_t* dwu;
   uint16_t* dg;  // [tokens, ffn] each, workspace
   uint16_t* du;
+  float* parts;  // of dX's sums, workspace
+  int64_t parts_bytes;
 };
 
 struct MatmulArgs {
@@ -90,6 +92,7 @@ struct TcLaunch {
 // whose rows start on 16 bytes.
 int gated_tc_pairs();
 bool gated_tc_takes(const GatedArgs& a);
+int64_t gated_parts_bytes(int64_t tokens, int64_t hidden);  // workspace for the parts of dX's sums
 cudaError_t launch_gated_forward_tc(const GatedArgs& a, const TcLaunch& l, cudaStream_t stream);
 cudaError_t launch_gated_grad_tc(const GatedArgs& a, const TcLaunch& l, cudaStream_t stream);
 // dX, dWg and dWu, or either.
@@ -102,6 +105,7 @@ cudaError_t launch_fp8_matmul_tc(const MatmulArgs& a, const TcLaunch& l, cudaStr
 // The same two products for few tokens (few_tc.cu).
 bool gated_few_takes(const GatedArgs& a, int sms);
 bool fp8_few_takes(const MatmulArgs& a, int sms);
+cudaError_t launch_gated_grad_few(const GatedArgs& a, const TcLaunch& l, cudaStream_t stream);
 cudaError_t launch_gated_forward_few(const GatedArgs& a, const TcLaunch& l, cudaStream_t stream);
 cudaError_t launch_fp8_matmul_few(const MatmulArgs& a, const TcLaunch& l, cudaStream_t stream);
 

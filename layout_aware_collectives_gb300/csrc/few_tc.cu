@@ -27,8 +27,12 @@ constexpr uint32_t kRowBytes = 128;    // of either operand in one stage
 constexpr uint32_t kWeights = kRows * kRowBytes;
 constexpr int kThreads = 192;          // loads, MMAs, 4 warps for the sums
 
-template <bool FP8, int NT>
+// What is computed: h, dG and dU (and h), or the 8-bit product.
+enum Kind { kForward = 0, kGrad = 1, kFp8 = 2 };
+
+template <int KIND, int NT>
 struct Shape {
+  static constexpr bool FP8 = KIND == kFp8;
   static constexpr int kParts = FP8 ? 1 : 2;  // weight tiles of a stage
   static constexpr uint32_t kStage = kParts * kWeights + NT * kRowBytes;
   static constexpr uint32_t kBudget = NT <= 32 ? 108 * 1024 : 200 * 1024;
@@ -47,6 +51,10 @@ struct Params {
   int64_t ldo;
   uint8_t *g8, *u8;
   float *gs, *us;
+  // grad
+  const uint16_t* dh;
+  int64_t lddh;
+  uint16_t *dg, *du;
   // 8-bit
   const float *sx, *sw;
   bool any_scales;
@@ -104,9 +112,10 @@ __device__ __forceinline__ void put_block(float4 v, uint8_t* codes, float* scale
   if (lane == 0) *scale = exponent_value(e);
 }
 
-template <bool FP8, int NT, int ACT>
+template <int KIND, int NT, int ACT>
 __global__ void __launch_bounds__(kThreads) few_tc_kernel(const __grid_constant__ Params p) {
-  using S = Shape<FP8, NT>;
+  using S = Shape<KIND, NT>;
+  constexpr bool FP8 = S::FP8;
   constexpr uint32_t kInstr = instr_desc(FP8 ? 0 : 1, 0, 0, kRows, NT);
   extern __shared__ uint8_t raw[];
   __shared__ uint64_t bars[2 * S::kStages + 2 * S::kBufs + 1];
@@ -281,7 +290,24 @@ __global__ void __launch_bounds__(kThreads) few_tc_kernel(const __grid_constant_
       for (int q = 0; q < S::kParts; ++q) addr[q] = smem + (uint32_t)((q * NT + t) * kRows + lane * 4) * 4;
       cluster_sums(addr, split, v);
       float4 r = v[0];
-      if constexpr (!FP8) {
+      if constexpr (KIND == kGrad) {
+        if (!in) continue;
+        const uint2 dh = *(const uint2*)(p.dh + token * p.lddh + col);
+        const float d[4] = {bf16_lo(dh.x), bf16_hi(dh.x), bf16_lo(dh.y), bf16_hi(dh.y)};
+        const float g[4] = {v[0].x, v[0].y, v[0].z, v[0].w}, u[4] = {v[1].x, v[1].y, v[1].z, v[1].w};
+        float dg[4], du[4], h[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 t = activation_grad<ACT>(g[i]);
+          dg[i] = d[i] * u[i] * t.y, du[i] = d[i] * t.x, h[i] = t.x * u[i];
+        }
+        const int64_t at = token * p.features + col;
+        *(uint2*)(p.dg + at) = make_uint2(pack_bf16(dg[0], dg[1]), pack_bf16(dg[2], dg[3]));
+        *(uint2*)(p.du + at) = make_uint2(pack_bf16(du[0], du[1]), pack_bf16(du[2], du[3]));
+        if (!p.out) continue;
+        r = make_float4(h[0], h[1], h[2], h[3]);
+      }
+      if constexpr (KIND == kForward) {
         const float4 a = v[0], u = v[1];
         r.x = activation<ACT>(a.x) * u.x, r.y = activation<ACT>(a.y) * u.y;
         r.z = activation<ACT>(a.z) * u.z, r.w = activation<ACT>(a.w) * u.w;
@@ -299,9 +325,9 @@ __global__ void __launch_bounds__(kThreads) few_tc_kernel(const __grid_constant_
 
 // Clusters of `split` CTAs that the device holds at one time; a cluster lies
 // within one GPC, so these are fewer than SMs / split.
-template <bool FP8, int NT, int ACT>
+template <int KIND, int NT, int ACT>
 int clusters_of(int split) {
-  using S = Shape<FP8, NT>;
+  using S = Shape<KIND, NT>;
   cudaLaunchAttribute cluster;
   cluster.id = cudaLaunchAttributeClusterDimension;
   cluster.val.clusterDim = {(unsigned)split, 1, 1};
@@ -312,7 +338,7 @@ int clusters_of(int split) {
   c.attrs = &cluster;
   c.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, few_tc_kernel<FP8, NT, ACT>, &c) != cudaSuccess) {
+  if (cudaOccupancyMaxActiveClusters(&n, few_tc_kernel<KIND, NT, ACT>, &c) != cudaSuccess) {
     cudaGetLastError();
     return 0;
   }
@@ -324,25 +350,25 @@ int clusters_of(int split) {
 // SMs streams 4096 x 14336 weights in 44 us, split in two 45.5; 16 tiles of
 // 64 tokens take 13.4 us split in four, 20.5 split in eight, where the last
 // clusters wait for the first.)
-template <bool FP8, int NT, int ACT>
+template <int KIND, int NT, int ACT>
 int split_of(int64_t tiles, int64_t steps, int sms) {
-  static const int held[3] = {clusters_of<FP8, NT, ACT>(2), clusters_of<FP8, NT, ACT>(4), clusters_of<FP8, NT, ACT>(8)};
+  static const int held[3] = {clusters_of<KIND, NT, ACT>(2), clusters_of<KIND, NT, ACT>(4), clusters_of<KIND, NT, ACT>(8)};
   int s = 1;
   for (int i = 0; i < 3 && 2 * s * tiles <= sms && tiles <= held[i] && steps >= 4 * s; ++i) s *= 2;
   return s;
 }
 
-template <bool FP8, int NT, int ACT>
+template <int KIND, int NT, int ACT>
 cudaError_t launch(Params& p, const TcLaunch& l, cudaStream_t stream) {
-  using S = Shape<FP8, NT>;
+  using S = Shape<KIND, NT>;
   static const cudaError_t ready =
-      cudaFuncSetAttribute(few_tc_kernel<FP8, NT, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
+      cudaFuncSetAttribute(few_tc_kernel<KIND, NT, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
   if (ready != cudaSuccess) return ready;
   p.err = l.err;
   p.limit_ns = TIDE_BULK_TIMEOUT_NS;
   p.stall_ns = l.stall_ns;
   const int64_t tiles_t = ceil_div(p.tokens, NT), tiles_f = ceil_div(p.features, kRows);
-  const int split = split_of<FP8, NT, ACT>(tiles_t * tiles_f, p.steps, l.sms);
+  const int split = split_of<KIND, NT, ACT>(tiles_t * tiles_f, p.steps, l.sms);
   cudaLaunchAttribute cluster;
   cluster.id = cudaLaunchAttributeClusterDimension;
   cluster.val.clusterDim = {(unsigned)split, 1, 1};
@@ -353,7 +379,7 @@ cudaError_t launch(Params& p, const TcLaunch& l, cudaStream_t stream) {
   c.stream = stream;
   c.attrs = &cluster;
   c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, few_tc_kernel<FP8, NT, ACT>, p);
+  return cudaLaunchKernelEx(&c, few_tc_kernel<KIND, NT, ACT>, p);
 }
 
 int tile_of(int64_t tokens) { return tokens <= 16 ? 16 : tokens <= 32 ? 32 : 64; }
@@ -365,11 +391,27 @@ bool few(int64_t tokens, int64_t features, int64_t most) {
   return tiles <= 65535 && (tokens <= 64 || tiles * ceil_div(tokens, 64) <= most);
 }
 
-template <int ACT>
-cudaError_t gated(Params& p, int nt, const TcLaunch& l, cudaStream_t stream) {
-  return nt == 16   ? launch<false, 16, ACT>(p, l, stream)
-         : nt == 32 ? launch<false, 32, ACT>(p, l, stream)
-                    : launch<false, 64, ACT>(p, l, stream);
+template <int KIND, int ACT = 0>
+cudaError_t launch_tile(Params& p, int nt, const TcLaunch& l, cudaStream_t stream) {
+  return nt == 16   ? launch<KIND, 16, ACT>(p, l, stream)
+         : nt == 32 ? launch<KIND, 32, ACT>(p, l, stream)
+                    : launch<KIND, 64, ACT>(p, l, stream);
+}
+
+// Both kinds of the gated block: operands and sizes.
+template <int KIND>
+cudaError_t gated(Params& p, const GatedArgs& a, const TcLaunch& l, cudaStream_t stream) {
+  constexpr int kElems = kRowBytes / 2;
+  const int nt = tile_of(a.tokens);
+  p.tokens = (int)a.tokens, p.features = (int)a.ffn;
+  p.steps = (int)ceil_div(a.hidden, kElems), p.step_elems = kElems;
+  p.out = a.h, p.ldo = a.ldh;
+  if (!make_map(&p.w[0], a.wg, 2, a.hidden, a.ffn, a.hidden, kElems, kRows, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_map(&p.w[1], a.wu, 2, a.hidden, a.ffn, a.hidden, kElems, kRows, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_map(&p.x, a.x, 2, a.hidden, a.tokens, a.ldx, kElems, nt, CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  return a.act == TIDE_ACT_SILU ? launch_tile<KIND, TIDE_ACT_SILU>(p, nt, l, stream)
+                                : launch_tile<KIND, TIDE_ACT_GELU>(p, nt, l, stream);
 }
 
 }  // namespace
@@ -382,19 +424,15 @@ bool gated_few_takes(const GatedArgs& a, int sms) { return few(a.tokens, a.ffn, 
 bool fp8_few_takes(const MatmulArgs& a, int sms) { return few(a.m, a.n, sms); }
 
 cudaError_t launch_gated_forward_few(const GatedArgs& a, const TcLaunch& l, cudaStream_t stream) {
-  constexpr int kElems = kRowBytes / 2;
-  const int nt = tile_of(a.tokens);
   Params p{};
-  p.tokens = (int)a.tokens, p.features = (int)a.ffn;
-  p.steps = (int)ceil_div(a.hidden, kElems), p.step_elems = kElems;
-  p.out = a.h, p.ldo = a.ldh;
   p.g8 = a.g8, p.gs = a.gs, p.u8 = a.u8, p.us = a.us;
-  if (!make_map(&p.w[0], a.wg, 2, a.hidden, a.ffn, a.hidden, kElems, kRows, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !make_map(&p.w[1], a.wu, 2, a.hidden, a.ffn, a.hidden, kElems, kRows, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !make_map(&p.x, a.x, 2, a.hidden, a.tokens, a.ldx, kElems, nt, CU_TENSOR_MAP_SWIZZLE_128B))
-    return cudaErrorInvalidValue;
-  return a.act == TIDE_ACT_SILU ? gated<TIDE_ACT_SILU>(p, nt, l, stream)
-                                : gated<TIDE_ACT_GELU>(p, nt, l, stream);
+  return gated<kForward>(p, a, l, stream);
+}
+
+cudaError_t launch_gated_grad_few(const GatedArgs& a, const TcLaunch& l, cudaStream_t stream) {
+  Params p{};
+  p.dh = a.dh, p.lddh = a.lddh, p.dg = a.dg, p.du = a.du;
+  return gated<kGrad>(p, a, l, stream);
 }
 
 cudaError_t launch_fp8_matmul_few(const MatmulArgs& a, const TcLaunch& l, cudaStream_t stream) {
@@ -407,9 +445,7 @@ cudaError_t launch_fp8_matmul_few(const MatmulArgs& a, const TcLaunch& l, cudaSt
   if (!make_map(&p.w[0], a.b, 1, a.k, a.n, a.k, kRowBytes, kRows, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_map(&p.x, a.a, 1, a.k, a.m, a.k, kRowBytes, nt, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
-  return nt == 16   ? launch<true, 16, 0>(p, l, stream)
-         : nt == 32 ? launch<true, 32, 0>(p, l, stream)
-                    : launch<true, 64, 0>(p, l, stream);
+  return launch_tile<kFp8>(p, nt, l, stream);
 }
 
 }  // namespace tide

@@ -46,6 +46,8 @@ struct Params {
   int tiles_m, tiles_n, tiles;
   int steps;       // stages of one tile's sum
   int half_steps;  // back: stages of dX's first half
+  int split;       // back: parts of dX's sums, each in its own tile
+  float* parts;    // [split, rows, cols] of them, where there are several
   int w_rows, w_tiles_m, w_tiles_n, w_tiles, w_steps;  // back: dW, both halves' tiles
   int extra;       // back: tiles of dW that take as long as one of dX
   // epilogue
@@ -83,9 +85,9 @@ __device__ __forceinline__ void put_codes(uint8_t* dst, const uint32_t (&v)[32],
 
 // One tile of a pair's work.
 struct Work {
-  TileAt at;
-  bool w;  // a tile of dW
-  int steps;
+  TileAt at;   // z: the half of dW, or the part of dX's sum
+  bool w;      // a tile of dW
+  int k0, k1;  // stages of the whole sum
 };
 
 // The pair's i-th tile; false past the last.  Tiles go round the pairs in
@@ -96,10 +98,14 @@ template <int FORM>
 __device__ __forceinline__ bool work_at(const Params& p, int pair, int pairs, int i, Work& r) {
   int t = pair + i * pairs;
   r.w = false;
-  r.steps = p.steps;
+  r.k0 = 0, r.k1 = p.steps;
   if (FORM != kBack || t < p.tiles) {
     if (t >= p.tiles) return false;
     r.at = tile_at(p.tiles_m, p.tiles_n, t);
+    if (FORM == kBack) {
+      r.k0 = (int)((int64_t)p.steps * r.at.z / p.split);
+      r.k1 = (int)((int64_t)p.steps * (r.at.z + 1) / p.split);
+    }
     return true;
   }
   i -= pair < p.tiles ? (p.tiles - pair + pairs - 1) / pairs : 0;
@@ -118,7 +124,7 @@ __device__ __forceinline__ bool work_at(const Params& p, int pair, int pairs, in
   if (first >= 0) t = first + (l >= 0 ? l : light + pair) + i * pairs;
   if (t >= p.w_tiles) return false;
   r.w = true;
-  r.steps = p.w_steps;
+  r.k1 = p.w_steps;
   r.at = tile_at(p.w_tiles_m, p.w_tiles_n, t);
   return true;
 }
@@ -215,6 +221,13 @@ __device__ __forceinline__ void epilogue(const Params& p, const Work& work, uint
       if (!any || col >= p.cols) break;
       uint32_t v[32], o[16];
       tmem_read(tmem + c * 32, v);
+      if (FORM == kBack && !work.w && p.split > 1) {
+        uint4* to = (uint4*)(p.parts + ((int64_t)t.z * p.rows + row) * p.cols + col);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (mine && col + 4 * i < p.cols) to[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        continue;
+      }
 #pragma unroll
       for (int i = 0; i < 16; ++i) o[i] = pack_bf16(as_f(v[2 * i]), as_f(v[2 * i + 1]));
       out.put(map, o, col, row0);
@@ -267,7 +280,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gated_t
       for (int i = 0; go && work_at<FORM>(p, pair, pairs, i, work); ++i) {
         const TileAt& at = work.at;
         const int row = (at.m * 2 + rank) * kHalf, col = (at.n * 2 + rank) * kHalf;
-        for (int k = 0; k < work.steps; ++k, ++j) {
+        for (int k = work.k0; k < work.k1; ++k, ++j) {
           const int s = j % kStages;
           if (j >= kStages && !bar_wait(empty(s), (j / kStages + 1) & 1, watch)) {
             go = false;
@@ -317,7 +330,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gated_t
         const uint32_t a_lbo = a_mn ? kOperand / 2 : 16, a_next = (a_mn ? 2048 : 32) >> 4;
         if (i >= 2 && !bar_wait(sums_empty(b), (i / 2 + 1) & 1, watch)) break;
         fence_after();
-        for (int k = 0; k < work.steps; ++k, ++j) {
+        for (int k = work.k0; k < work.k1; ++k, ++j) {
           const int s = j % kStages;
           if (!bar_wait(full(s), (j / kStages) & 1, watch)) {
             go = false;
@@ -328,7 +341,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gated_t
           const uint64_t da = operand_desc(a, a_lbo), db = operand_desc(a + kOperand, kBMn ? kOperand / 2 : 16);
 #pragma unroll
           for (int q = 0; q < kStep / 16; ++q)
-            mma<2, false>(tmem + b * 256, da + q * a_next, db + q * ((kBMn ? 2048 : 32) >> 4), instr, k > 0 || q > 0);
+            mma<2, false>(tmem + b * 256, da + q * a_next, db + q * ((kBMn ? 2048 : 32) >> 4), instr, k > work.k0 || q > 0);
           mma_commit<2>(empty(s));
         }
         if (go) mma_commit<2>(sums_full(b));
@@ -357,6 +370,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gated_t
   __syncthreads();
   cluster_sync();
   if (warp == 2) tmem_free<2>(tmem, 512);
+}
+
+// dX from the parts of its sums, in their order: 8 columns a thread.
+__global__ void __launch_bounds__(kThreads)
+    join_kernel(const float* parts, int split, uint16_t* dx, int64_t ld, uint32_t groups_per_row, uint32_t groups, int64_t numel) {
+  const uint32_t i = blockIdx.x * kThreads + threadIdx.x;
+  if (i >= groups) return;
+  const uint32_t row = i / groups_per_row, col = (i - row * groups_per_row) * 8;
+  const float4* from = (const float4*)(parts + (int64_t)i * 8);
+  float4 a = from[0], b = from[1];
+  for (int s = 1; s < split; ++s) {
+    from += numel / 4;
+    const float4 c = from[0], d = from[1];
+    a.x += c.x, a.y += c.y, a.z += c.z, a.w += c.w;
+    b.x += d.x, b.y += d.y, b.z += d.z, b.w += d.w;
+  }
+  *(uint4*)(dx + (int64_t)row * ld + col) =
+      make_uint4(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w), pack_bf16(b.x, b.y), pack_bf16(b.z, b.w));
 }
 
 template <int FORM, int ACT>
@@ -396,6 +427,18 @@ bool fill_pre(Params* p, const GatedArgs& a) {
   return map_k(&p->b[0], a.wg, a.hidden, a.ffn, a.hidden) && map_k(&p->b[1], a.wu, a.hidden, a.ffn, a.hidden);
 }
 
+// Parts of dX's sums.  dX has few tiles for its long contraction; where they
+// leave half of the pairs or more without one, the sums are split so that
+// every pair has work, each part at least 8 stages long, as far as the
+// workspace holds them (256 tokens of the 8B-shaped block: 16 tiles of 448
+// stages in 4 parts).
+int split_of(int64_t tiles, int64_t steps, int pairs, int64_t room) {
+  int64_t s = pairs / tiles;
+  if (s > steps / 8) s = steps / 8;
+  if (s > room) s = room;
+  return s < 2 ? 1 : (int)s;
+}
+
 }  // namespace
 
 int gated_tc_pairs() {
@@ -409,6 +452,12 @@ int gated_tc_pairs() {
   int n = 0;
   if (cudaOccupancyMaxActiveClusters(&n, gated_tc_kernel<kBack, 0>, &c) != cudaSuccess) return 0;
   return n;
+}
+
+// The parts of at most one tile for each of a GB300's 76 pairs.
+int64_t gated_parts_bytes(int64_t tokens, int64_t hidden) {
+  const int64_t tiles = ceil_div(tokens, 2 * kHalf) * ceil_div(hidden, 2 * kHalf);
+  return tiles && 76 / tiles >= 2 ? 76 / tiles * tokens * hidden * 4 : 0;
 }
 
 bool gated_tc_takes(const GatedArgs& a) { return a.hidden >= 8 && rows16(a.hidden, a.hidden) && rows16(a.ffn, a.ffn); }
@@ -437,8 +486,10 @@ cudaError_t launch_gated_back_tc(const GatedArgs& a, bool dx, bool dw, const TcL
   if (dx) {
     p.rows = (int)a.tokens;
     p.tiles_m = (int)ceil_div(a.tokens, 2 * kHalf), p.tiles_n = (int)ceil_div(a.hidden, 2 * kHalf);
-    p.tiles = p.tiles_m * p.tiles_n;
     p.half_steps = (int)ceil_div(a.ffn, kStep), p.steps = 2 * p.half_steps;
+    p.split = split_of((int64_t)p.tiles_m * p.tiles_n, p.steps, l.pairs, a.parts_bytes / (a.tokens * a.hidden * 4));
+    p.parts = a.parts;
+    p.tiles = p.tiles_m * p.tiles_n * p.split;
     if (!map_k(&p.a[0], a.dg, a.ffn, a.tokens, a.ffn) || !map_k(&p.a[1], a.du, a.ffn, a.tokens, a.ffn) ||
         !map_mn(&p.b[0], a.wg, a.hidden, a.ffn, a.hidden) || !map_mn(&p.b[1], a.wu, a.hidden, a.ffn, a.hidden) ||
         !map_out(&p.out[0], a.dx, a.hidden, a.tokens, a.lddx))
@@ -450,13 +501,18 @@ cudaError_t launch_gated_back_tc(const GatedArgs& a, bool dx, bool dw, const TcL
     p.w_tiles = 2 * p.w_tiles_m * p.w_tiles_n;
     p.w_steps = (int)ceil_div(a.tokens, kStep);
     // what a tile of either takes: its stages, and about one for its way in and out
-    p.extra = (p.steps + 1 + (p.w_steps + 1) / 2) / (p.w_steps + 1);
+    p.extra = ((dx ? p.steps / p.split : 0) + 1 + (p.w_steps + 1) / 2) / (p.w_steps + 1);
     if (!map_mn(&p.wa[0], a.dg, a.ffn, a.tokens, a.ffn) || !map_mn(&p.wa[1], a.du, a.ffn, a.tokens, a.ffn) ||
         !map_mn(&p.wb, a.x, a.hidden, a.tokens, a.ldx) || !map_out(&p.out[1], a.dwg, a.hidden, a.ffn, a.hidden) ||
         !map_out(&p.out[2], a.dwu, a.hidden, a.ffn, a.hidden))
       return cudaErrorInvalidValue;
   }
-  return launch<kBack, 0>(p, l, stream);
+  const cudaError_t e = launch<kBack, 0>(p, l, stream);
+  if (e != cudaSuccess || p.split <= 1) return e;
+  const int64_t numel = a.tokens * a.hidden;
+  join_kernel<<<(unsigned)ceil_div(numel / 8, kThreads), kThreads, 0, stream>>>(
+      p.parts, p.split, a.dx, a.lddx, (uint32_t)(a.hidden / 8), (uint32_t)(numel / 8), numel);
+  return cudaGetLastError();
 }
 
 }  // namespace tide
