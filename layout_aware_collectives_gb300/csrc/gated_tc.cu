@@ -14,7 +14,7 @@
 // and up sums side by side, and the product needs no exchange.
 //
 // Roles: warp 0 loads (6 stages of 32 KiB), warp 1 of the pair's first CTA
-// issues the MMAs, warps 4-7 read finished sums out of TMEM, which holds two
+// issues the MMAs, warps from 4 on read finished sums out of TMEM, which holds two
 // accumulators so that they do so while the next tile is summed.  Bound by
 // the tensor cores at every large size.
 #include "compute_device.cuh"
@@ -33,10 +33,18 @@ constexpr int kStep = 64;                     // contraction of one stage
 constexpr int kHalf = 128;                    // rows of A, columns of B in one CTA
 constexpr uint32_t kOperand = kHalf * kStep * 2;  // bytes of either in one stage
 constexpr uint32_t kStage = 2 * kOperand;
-constexpr int kThreads = 256;
-constexpr int kEpiWarps = 4;
-constexpr int kBoxes = 4;                     // boxes in flight for each warp
-constexpr size_t kSmem = 1024 + kStages * kStage + kEpiWarps * kBoxes * kBox;
+constexpr int kAllBoxes = 16;                 // boxes of results in flight
+constexpr size_t kSmem = 1024 + kStages * kStage + kAllBoxes * kBox;
+// Warps that read finished sums.  Eight for dX and dW, whose tiles write 128
+// KiB and, for few tokens, have few stages to do it behind (64 tokens of the
+// 8B-shaped block: dW 70 us with four); the others need the registers.
+template <int FORM>
+constexpr int kEpiWarps = FORM == kBack ? 8 : 4;
+template <int FORM>
+constexpr int kThreads = 128 + 32 * kEpiWarps<FORM>;
+template <int FORM>
+constexpr int kBoxes = kAllBoxes / kEpiWarps<FORM>;
+constexpr int kJoinThreads = 256;
 
 struct Params {
   // forward, grad: a = x, b = Wg, Wu; out = h, or dG, dU, h
@@ -130,7 +138,8 @@ __device__ __forceinline__ bool work_at(const Params& p, int pair, int pairs, in
 }
 
 template <int FORM, int ACT>
-__device__ __forceinline__ void epilogue(const Params& p, const Work& work, uint32_t tmem, int row0, Outbox<kBoxes>& out) {
+__device__ __forceinline__ void epilogue(const Params& p, const Work& work, uint32_t tmem, int row0, int half,
+                                         Outbox<kBoxes<FORM>>& out) {
   const TileAt& t = work.at;
   const int row = row0 + out.lane, rows = work.w ? p.w_rows : p.rows;
   const bool any = row0 < rows, mine = row < rows;
@@ -216,7 +225,7 @@ __device__ __forceinline__ void epilogue(const Params& p, const Work& work, uint
   } else {
     const CUtensorMap* map = &p.out[work.w ? 1 + t.z : 0];
 #pragma unroll 1
-    for (int c = 0; c < 8; ++c) {
+    for (int c = half * 4; c < half * 4 + 4; ++c) {
       const int col = t.n * 2 * kHalf + c * 32;
       if (!any || col >= p.cols) break;
       uint32_t v[32], o[16];
@@ -236,7 +245,7 @@ __device__ __forceinline__ void epilogue(const Params& p, const Work& work, uint
 }
 
 template <int FORM, int ACT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_constant__ Params p) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<FORM>, 1) gated_tc_kernel(const __grid_constant__ Params p) {
   constexpr bool kBMn = FORM == kBack;
   extern __shared__ uint8_t raw[];
   __shared__ uint64_t bars[2 * kStages + 5];
@@ -258,7 +267,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gated_t
   if (threadIdx.x == 0) {
     stop = 0;
     for (int s = 0; s < kStages; ++s) bar_init(full(s), 1), bar_init(empty(s), 1);
-    for (int b = 0; b < 2; ++b) bar_init(sums_full(b), 1), bar_init(sums_empty(b), 2 * kEpiWarps);
+    for (int b = 0; b < 2; ++b) bar_init(sums_full(b), 1), bar_init(sums_empty(b), 2 * kEpiWarps<FORM>);
     bar_init(spare, 1);
     bar_init_fence();
     prefetch_map(FORM == kBack && !p.tiles ? &p.wa[0] : &p.a[0]), prefetch_map(FORM == kBack && !p.tiles ? &p.wb : &p.b[0]);
@@ -353,14 +362,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gated_t
       }
     }
   } else if (warp >= 4) {
-    Outbox<kBoxes> out{smem + kStages * kStage + (warp - 4) * kBoxes * kBox, 0, lane};
+    Outbox<kBoxes<FORM>> out{smem + kStages * kStage + (warp - 4) * kBoxes<FORM> * kBox, 0, lane};
     Work work;
     for (int i = 0; work_at<FORM>(p, pair, pairs, i, work); ++i) {
       const int b = i & 1;
       if (!bar_wait_warp(sums_full(b), (i / 2) & 1, watch)) break;
       fence_after();
-      const uint32_t lanes = (uint32_t)(warp - 4) * 32;
-      epilogue<FORM, ACT>(p, work, tmem + (lanes << 16) + b * 256, (work.at.m * 2 + rank) * kHalf + lanes, out);
+      const uint32_t lanes = (uint32_t)(warp & 3) * 32;
+      epilogue<FORM, ACT>(p, work, tmem + (lanes << 16) + b * 256, (work.at.m * 2 + rank) * kHalf + lanes, (warp - 4) >> 2, out);
       fence_before();
       __syncwarp();
       if (lane == 0) bar_arrive_peer(peer_addr(sums_empty(b), 0));
@@ -373,9 +382,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gated_t
 }
 
 // dX from the parts of its sums, in their order: 8 columns a thread.
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kJoinThreads)
     join_kernel(const float* parts, int split, uint16_t* dx, int64_t ld, uint32_t groups_per_row, uint32_t groups, int64_t numel) {
-  const uint32_t i = blockIdx.x * kThreads + threadIdx.x;
+  const uint32_t i = blockIdx.x * kJoinThreads + threadIdx.x;
   if (i >= groups) return;
   const uint32_t row = i / groups_per_row, col = (i - row * groups_per_row) * 8;
   const float4* from = (const float4*)(parts + (int64_t)i * 8);
@@ -399,7 +408,7 @@ cudaError_t launch(Params& p, const TcLaunch& l, cudaStream_t stream) {
   p.limit_ns = TIDE_BULK_TIMEOUT_NS;
   p.stall_ns = l.stall_ns;
   const int pairs = p.tiles + p.w_tiles < l.pairs ? p.tiles + p.w_tiles : l.pairs;
-  gated_tc_kernel<FORM, ACT><<<2 * pairs, kThreads, kSmem, stream>>>(p);
+  gated_tc_kernel<FORM, ACT><<<2 * pairs, kThreads<FORM>, kSmem, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -447,7 +456,7 @@ int gated_tc_pairs() {
   cudaFuncSetAttribute(gated_tc_kernel<kBack, 0>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   cudaLaunchConfig_t c{};
   c.gridDim = dim3(2);
-  c.blockDim = dim3(kThreads);
+  c.blockDim = dim3(kThreads<kBack>);
   c.dynamicSmemBytes = kSmem;
   int n = 0;
   if (cudaOccupancyMaxActiveClusters(&n, gated_tc_kernel<kBack, 0>, &c) != cudaSuccess) return 0;
@@ -500,8 +509,10 @@ cudaError_t launch_gated_back_tc(const GatedArgs& a, bool dx, bool dw, const TcL
     p.w_tiles_m = (int)ceil_div(a.ffn, 2 * kHalf), p.w_tiles_n = (int)ceil_div(a.hidden, 2 * kHalf);
     p.w_tiles = 2 * p.w_tiles_m * p.w_tiles_n;
     p.w_steps = (int)ceil_div(a.tokens, kStep);
-    // what a tile of either takes: its stages, and about one for its way in and out
-    p.extra = ((dx ? p.steps / p.split : 0) + 1 + (p.w_steps + 1) / 2) / (p.w_steps + 1);
+    // what a tile of either takes: its stages, at least the six that writing
+    // it takes, and about one for its way in and out
+    const int w_cost = (p.w_steps > 6 ? p.w_steps : 6) + 1;
+    p.extra = ((dx ? p.steps / p.split : 0) + 1 + w_cost / 2) / w_cost;
     if (!map_mn(&p.wa[0], a.dg, a.ffn, a.tokens, a.ffn) || !map_mn(&p.wa[1], a.du, a.ffn, a.tokens, a.ffn) ||
         !map_mn(&p.wb, a.x, a.hidden, a.tokens, a.ldx) || !map_out(&p.out[1], a.dwg, a.hidden, a.ffn, a.hidden) ||
         !map_out(&p.out[2], a.dwu, a.hidden, a.ffn, a.hidden))
@@ -510,7 +521,7 @@ cudaError_t launch_gated_back_tc(const GatedArgs& a, bool dx, bool dw, const TcL
   const cudaError_t e = launch<kBack, 0>(p, l, stream);
   if (e != cudaSuccess || p.split <= 1) return e;
   const int64_t numel = a.tokens * a.hidden;
-  join_kernel<<<(unsigned)ceil_div(numel / 8, kThreads), kThreads, 0, stream>>>(
+  join_kernel<<<(unsigned)ceil_div(numel / 8, kJoinThreads), kJoinThreads, 0, stream>>>(
       p.parts, p.split, a.dx, a.lddx, (uint32_t)(a.hidden / 8), (uint32_t)(numel / 8), numel);
   return cudaGetLastError();
 }
