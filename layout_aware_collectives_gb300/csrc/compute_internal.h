@@ -80,6 +80,28 @@ cudaError_t launch_gated_dx_simple(const GatedArgs& a, cudaStream_t stream);
 cudaError_t launch_gated_dw_simple(const GatedArgs& a, cudaStream_t stream);
 cudaError_t launch_fp8_matmul_simple(const MatmulArgs& a, cudaStream_t stream);
 
+// Launches a kernel that may begin before the work ahead of it on the stream
+// has ended (programmatic dependent launch): it calls after_previous() before
+// it touches memory, so only its set-up overlaps.  cluster: CTAs of a
+// cluster, 0 where the kernel fixes it.
+template <class... P, class... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, unsigned block, size_t smem, unsigned cluster,
+                         cudaStream_t stream, const A&... args) {
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim = {cluster, 1, 1};
+  cudaLaunchConfig_t c{};
+  c.gridDim = grid;
+  c.blockDim = dim3(block);
+  c.dynamicSmemBytes = smem;
+  c.stream = stream;
+  c.attrs = at;
+  c.numAttrs = cluster ? 2 : 1;
+  return cudaLaunchKernelEx(&c, kernel, P(args)...);
+}
+
 // What a tensor-core launch takes from its handle.
 struct TcLaunch {
   int pairs;  // pairs of CTAs the device holds at one time

@@ -142,12 +142,15 @@ __global__ void __launch_bounds__(kThreads) few_tc_kernel(const __grid_constant_
     for (int b = 0; b < S::kBufs; ++b) bar_init(sums_full(b), 1), bar_init(sums_empty(b), 4);
     bar_init(spare, 1);
     bar_init_fence();
+    for (int i = 0; i < S::kParts; ++i) prefetch_map(&p.w[i]);
+    prefetch_map(&p.x);
   }
   if (warp == 1) tmem_alloc<1>(smem_addr(&tmem_at), S::kColumns);
   fence_before();
   __syncthreads();
   fence_after();
   const uint32_t tmem = tmem_at;
+  after_previous();
   bool done = false;  // this warp has its sums in shared memory
 
   if (p.stall_ns) {  // test: a wait on a barrier nothing arrives on runs out
@@ -275,7 +278,7 @@ __global__ void __launch_bounds__(kThreads) few_tc_kernel(const __grid_constant_
     }
   }
   __syncthreads();
-  cluster_sync();
+  if (split > 1) cluster_sync();
   if (!p.stall_ns) {
     constexpr int kWarps = kThreads / 32;
     const int col = feature0 + lane * 4;
@@ -319,7 +322,7 @@ __global__ void __launch_bounds__(kThreads) few_tc_kernel(const __grid_constant_
       if (in) *(uint2*)(p.out + token * p.ldo + col) = make_uint2(pack_bf16(r.x, r.y), pack_bf16(r.z, r.w));
     }
   }
-  cluster_sync();  // the others have read this CTA's sums
+  if (split > 1) cluster_sync();  // the others have read this CTA's sums
   if (warp == 1) tmem_free<1>(tmem, S::kColumns);
 }
 
@@ -369,17 +372,8 @@ cudaError_t launch(Params& p, const TcLaunch& l, cudaStream_t stream) {
   p.stall_ns = l.stall_ns;
   const int64_t tiles_t = ceil_div(p.tokens, NT), tiles_f = ceil_div(p.features, kRows);
   const int split = split_of<KIND, NT, ACT>(tiles_t * tiles_f, p.steps, l.sms);
-  cudaLaunchAttribute cluster;
-  cluster.id = cudaLaunchAttributeClusterDimension;
-  cluster.val.clusterDim = {(unsigned)split, 1, 1};
-  cudaLaunchConfig_t c{};
-  c.gridDim = dim3(split, (unsigned)tiles_t, (unsigned)tiles_f);
-  c.blockDim = dim3(kThreads);
-  c.dynamicSmemBytes = S::kSmem;
-  c.stream = stream;
-  c.attrs = &cluster;
-  c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, few_tc_kernel<KIND, NT, ACT>, p);
+  return launch_early(few_tc_kernel<KIND, NT, ACT>, dim3(split, (unsigned)tiles_t, (unsigned)tiles_f), kThreads, S::kSmem,
+                      (unsigned)split, stream, p);
 }
 
 int tile_of(int64_t tokens) { return tokens <= 16 ? 16 : tokens <= 32 ? 32 : 64; }

@@ -12,6 +12,11 @@ constexpr int kThreads = 256;
 // divisions are a third of the 64-bit ones' instructions.
 constexpr int64_t kSmall = (int64_t)3 << 30;
 
+template <class... P, class... A>
+cudaError_t run(void (*kernel)(P...), unsigned grid, cudaStream_t stream, const A&... args) {
+  return launch_early(kernel, dim3(grid), kThreads, 0, 0, stream, args...);
+}
+
 // ------------------------------------------------------------------ store
 
 // Magnitudes of packed bf16 are ordered as 16-bit whole numbers, infinity at
@@ -59,6 +64,7 @@ __device__ __forceinline__ uint2 codes8(const uint32_t (&w)[4], float inv) {
 // twice.  U blocks are loaded before the first is reduced.
 template <int U, class Index>
 __global__ void __launch_bounds__(kThreads) store_rows_kernel(Fp8Args a, Index blocks_per_row, Index blocks) {
+  after_previous();
   const int lane = threadIdx.x & 15;
   const Index group = (Index)blockIdx.x * (U * kThreads / 16) + (threadIdx.x >> 4);
   uint32_t v[U][4];
@@ -99,6 +105,7 @@ __global__ void __launch_bounds__(kThreads) store_rows_kernel(Fp8Args a, Index b
 // a block, 4 single columns a lane, 32 apart.
 template <int U, class Index>
 __global__ void __launch_bounds__(kThreads) store_rows_any_kernel(Fp8Args a, Index blocks_per_row, Index blocks) {
+  after_previous();
   const int lane = threadIdx.x & 31;
   const Index warp = (Index)blockIdx.x * (U * kThreads / 32) + (threadIdx.x >> 5);
   uint16_t v[U][4];
@@ -140,6 +147,7 @@ __global__ void __launch_bounds__(kThreads) store_rows_any_kernel(Fp8Args a, Ind
 // once.
 template <bool VEC>
 __global__ void __launch_bounds__(kThreads) store_square_kernel(Fp8Args a, uint32_t blocks_per_row) {
+  after_previous();
   constexpr int kPerLoad = VEC ? 8 : 1;
   constexpr int kLanes = kBlock / kPerLoad;        // threads across a row
   constexpr int kRows = kThreads / kLanes;         // rows a pass
@@ -258,11 +266,13 @@ __device__ __forceinline__ void restore_flat(const Fp8Args& a, int64_t blocks_pe
 
 template <int U, class Index>
 __global__ void __launch_bounds__(kThreads) restore_flat_kernel(Fp8Args a, int64_t blocks_per_row, Index numel) {
+  after_previous();
   restore_flat<U>(a, blocks_per_row, numel, blockIdx.x);
 }
 
 // Strided destination rows: one element a thread and step.
 __global__ void __launch_bounds__(kThreads) restore_any_kernel(Fp8Args a, int64_t blocks_per_row, int64_t numel) {
+  after_previous();
   for (int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x; e < numel; e += (int64_t)gridDim.x * kThreads) {
     const int64_t row = e / a.cols, col = e - row * a.cols;
     a.bf16[row * a.ld + col] = to_bf16(e4m3_values(a.codes[e]).x * scale_at(a, blocks_per_row, row, col));
@@ -281,6 +291,7 @@ constexpr int kRestoreUnroll = 4;
 template <int ACT, int V, class Index>
 __global__ void __launch_bounds__(kThreads)
     grad_stored_kernel(GatedArgs a, Index groups_per_row, Index groups, unsigned ctas, Fp8Args x) {
+  after_previous();
   if (blockIdx.x >= ctas) {
     restore_flat<kRestoreUnroll, Index>(x, (x.cols + kBlock - 1) / kBlock, (Index)(x.rows * x.cols), blockIdx.x - ctas);
     return;
@@ -340,15 +351,10 @@ cudaError_t grad_stored(const GatedArgs& a, const Fp8Args& x, cudaStream_t strea
   const unsigned ctas = (unsigned)ceil_div(groups, kThreads);
   const unsigned grid = ctas + (unsigned)ceil_div(more, (int64_t)kThreads * 8 * kRestoreUnroll);
   const bool small = groups <= kSmall && more <= kSmall;
-  if (vec && small)
-    grad_stored_kernel<ACT, 8, uint32_t><<<grid, kThreads, 0, stream>>>(a, (uint32_t)per_row, (uint32_t)groups, ctas, x);
-  else if (vec)
-    grad_stored_kernel<ACT, 8, int64_t><<<grid, kThreads, 0, stream>>>(a, per_row, groups, ctas, x);
-  else if (small)
-    grad_stored_kernel<ACT, 1, uint32_t><<<grid, kThreads, 0, stream>>>(a, (uint32_t)per_row, (uint32_t)groups, ctas, x);
-  else
-    grad_stored_kernel<ACT, 1, int64_t><<<grid, kThreads, 0, stream>>>(a, per_row, groups, ctas, x);
-  return cudaGetLastError();
+  if (vec && small) return run(grad_stored_kernel<ACT, 8, uint32_t>, grid, stream, a, (uint32_t)per_row, (uint32_t)groups, ctas, x);
+  if (vec) return run(grad_stored_kernel<ACT, 8, int64_t>, grid, stream, a, per_row, groups, ctas, x);
+  if (small) return run(grad_stored_kernel<ACT, 1, uint32_t>, grid, stream, a, (uint32_t)per_row, (uint32_t)groups, ctas, x);
+  return run(grad_stored_kernel<ACT, 1, int64_t>, grid, stream, a, per_row, groups, ctas, x);
 }
 
 }  // namespace
@@ -358,40 +364,27 @@ cudaError_t launch_fp8_store(const Fp8Args& a, cudaStream_t stream) {
   const bool vec = a.cols % 8 == 0 && a.ld % 8 == 0;
   if (a.block_rows != 1) {
     const unsigned grid = (unsigned)(per_row * ceil_div(a.rows, kBlock));
-    if (vec)
-      store_square_kernel<true><<<grid, kThreads, 0, stream>>>(a, (uint32_t)per_row);
-    else
-      store_square_kernel<false><<<grid, kThreads, 0, stream>>>(a, (uint32_t)per_row);
-    return cudaGetLastError();
+    return run(vec ? store_square_kernel<true> : store_square_kernel<false>, grid, stream, a, (uint32_t)per_row);
   }
   constexpr int kUnroll = 2;
   const int64_t blocks = per_row * a.rows;
   const unsigned grid = (unsigned)ceil_div(blocks, (int64_t)kUnroll * (vec ? kThreads / 16 : kThreads / 32));
   const bool small = blocks <= kSmall;
-  if (vec && small)
-    store_rows_kernel<kUnroll, uint32_t><<<grid, kThreads, 0, stream>>>(a, (uint32_t)per_row, (uint32_t)blocks);
-  else if (vec)
-    store_rows_kernel<kUnroll, int64_t><<<grid, kThreads, 0, stream>>>(a, per_row, blocks);
-  else if (small)
-    store_rows_any_kernel<kUnroll, uint32_t><<<grid, kThreads, 0, stream>>>(a, (uint32_t)per_row, (uint32_t)blocks);
-  else
-    store_rows_any_kernel<kUnroll, int64_t><<<grid, kThreads, 0, stream>>>(a, per_row, blocks);
-  return cudaGetLastError();
+  if (vec && small) return run(store_rows_kernel<kUnroll, uint32_t>, grid, stream, a, (uint32_t)per_row, (uint32_t)blocks);
+  if (vec) return run(store_rows_kernel<kUnroll, int64_t>, grid, stream, a, per_row, blocks);
+  if (small) return run(store_rows_any_kernel<kUnroll, uint32_t>, grid, stream, a, (uint32_t)per_row, (uint32_t)blocks);
+  return run(store_rows_any_kernel<kUnroll, int64_t>, grid, stream, a, per_row, blocks);
 }
 
 cudaError_t launch_fp8_restore(const Fp8Args& a, cudaStream_t stream) {
   const int64_t per_row = ceil_div(a.cols, kBlock), numel = a.rows * a.cols;
-  if (a.ld == a.cols) {
-    const unsigned grid = (unsigned)ceil_div(numel, (int64_t)kThreads * 8 * kRestoreUnroll);
-    if (numel <= kSmall)
-      restore_flat_kernel<kRestoreUnroll, uint32_t><<<grid, kThreads, 0, stream>>>(a, per_row, (uint32_t)numel);
-    else
-      restore_flat_kernel<kRestoreUnroll, int64_t><<<grid, kThreads, 0, stream>>>(a, per_row, numel);
-  } else {
+  if (a.ld != a.cols) {
     const int64_t grid = ceil_div(numel, kThreads);
-    restore_any_kernel<<<(unsigned)(grid < 65536 ? grid : 65536), kThreads, 0, stream>>>(a, per_row, numel);
+    return run(restore_any_kernel, (unsigned)(grid < 65536 ? grid : 65536), stream, a, per_row, numel);
   }
-  return cudaGetLastError();
+  const unsigned grid = (unsigned)ceil_div(numel, (int64_t)kThreads * 8 * kRestoreUnroll);
+  if (numel <= kSmall) return run(restore_flat_kernel<kRestoreUnroll, uint32_t>, grid, stream, a, per_row, (uint32_t)numel);
+  return run(restore_flat_kernel<kRestoreUnroll, int64_t>, grid, stream, a, per_row, numel);
 }
 
 cudaError_t launch_gated_grad_stored(const GatedArgs& a, const Fp8Args& x, cudaStream_t stream) {

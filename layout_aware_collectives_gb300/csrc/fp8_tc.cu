@@ -88,6 +88,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) summed_
   cluster_sync();
   fence_after();
   const uint32_t tmem = tmem_at;
+  after_previous();
 
   if (p.stall_ns) {  // test: a wait on a barrier nothing arrives on runs out
     if (threadIdx.x == 0) bar_wait(spare, 0, Watch{&stop, p.err, p.stall_ns});
@@ -258,6 +259,7 @@ __global__ void __cluster_dims__(2, 1, 1)
   cluster_sync();
   fence_after();
   const uint32_t tmem = tmem_at;
+  after_previous();
 
   if (p.stall_ns) {  // test: a wait on a barrier nothing arrives on runs out
     if (threadIdx.x == 0) bar_wait(spare, 0, Watch{&stop, p.err, p.stall_ns});
@@ -442,11 +444,8 @@ cudaError_t launch_fp8_matmul_tc(const MatmulArgs& a, const TcLaunch& l, cudaStr
       !make_map(&p.out, a.out, 2, a.n, a.m, a.ldo, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
     return cudaErrorInvalidValue;
   const int pairs = p.tiles < l.pairs ? p.tiles : l.pairs;
-  if (a.any_scales)
-    summed_kernel<<<2 * pairs, kThreads, kSmem, stream>>>(p);
-  else
-    scaled_kernel<<<2 * pairs, kScaledThreads, kScaledSmem, stream>>>(p);
-  return cudaGetLastError();
+  return a.any_scales ? launch_early(summed_kernel, dim3(2 * pairs), kThreads, kSmem, 0, stream, p)
+                      : launch_early(scaled_kernel, dim3(2 * pairs), kScaledThreads, kScaledSmem, 0, stream, p);
 }
 
 }  // namespace tide

@@ -278,6 +278,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<FORM>, 1) g
   cluster_sync();
   fence_after();
   const uint32_t tmem = tmem_at;
+  after_previous();
 
   if (p.stall_ns) {  // test: a wait on a barrier nothing arrives on runs out
     if (threadIdx.x == 0) bar_wait(spare, 0, Watch{&stop, p.err, p.stall_ns});
@@ -384,6 +385,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<FORM>, 1) g
 // dX from the parts of its sums, in their order: 8 columns a thread.
 __global__ void __launch_bounds__(kJoinThreads)
     join_kernel(const float* parts, int split, uint16_t* dx, int64_t ld, uint32_t groups_per_row, uint32_t groups, int64_t numel) {
+  after_previous();
   const uint32_t i = blockIdx.x * kJoinThreads + threadIdx.x;
   if (i >= groups) return;
   const uint32_t row = i / groups_per_row, col = (i - row * groups_per_row) * 8;
@@ -408,8 +410,7 @@ cudaError_t launch(Params& p, const TcLaunch& l, cudaStream_t stream) {
   p.limit_ns = TIDE_BULK_TIMEOUT_NS;
   p.stall_ns = l.stall_ns;
   const int pairs = p.tiles + p.w_tiles < l.pairs ? p.tiles + p.w_tiles : l.pairs;
-  gated_tc_kernel<FORM, ACT><<<2 * pairs, kThreads<FORM>, kSmem, stream>>>(p);
-  return cudaGetLastError();
+  return launch_early(gated_tc_kernel<FORM, ACT>, dim3(2 * pairs), kThreads<FORM>, kSmem, 0, stream, p);
 }
 
 bool rows16(int64_t width, int64_t ld) { return width % 8 == 0 && ld % 8 == 0; }
@@ -438,14 +439,14 @@ bool fill_pre(Params* p, const GatedArgs& a) {
 
 // Parts of dX's sums.  dX has few tiles for its long contraction; where they
 // leave half of the pairs or more without one, the sums are split so that
-// every pair has work, each part at least 8 stages long, as far as the
-// workspace holds them (256 tokens of the 8B-shaped block: 16 tiles of 448
-// stages in 4 parts).
+// every pair has work, as far as the workspace holds them (256 tokens of the
+// 8B-shaped block: 16 tiles of 448 stages in 4 parts, 120 -> 55 us), unless
+// that saves fewer stages (0.27 us each) than joining them costs.
 int split_of(int64_t tiles, int64_t steps, int pairs, int64_t room) {
   int64_t s = pairs / tiles;
-  if (s > steps / 8) s = steps / 8;
+  if (s > steps / 6) s = steps / 6;
   if (s > room) s = room;
-  return s < 2 ? 1 : (int)s;
+  return s < 2 || steps - steps / s < 12 ? 1 : (int)s;
 }
 
 }  // namespace
@@ -521,9 +522,8 @@ cudaError_t launch_gated_back_tc(const GatedArgs& a, bool dx, bool dw, const TcL
   const cudaError_t e = launch<kBack, 0>(p, l, stream);
   if (e != cudaSuccess || p.split <= 1) return e;
   const int64_t numel = a.tokens * a.hidden;
-  join_kernel<<<(unsigned)ceil_div(numel / 8, kJoinThreads), kJoinThreads, 0, stream>>>(
-      p.parts, p.split, a.dx, a.lddx, (uint32_t)(a.hidden / 8), (uint32_t)(numel / 8), numel);
-  return cudaGetLastError();
+  return launch_early(join_kernel, dim3((unsigned)ceil_div(numel / 8, kJoinThreads)), kJoinThreads, 0, 0, stream,
+                      (const float*)p.parts, p.split, a.dx, a.lddx, (uint32_t)(a.hidden / 8), (uint32_t)(numel / 8), numel);
 }
 
 }  // namespace tide
