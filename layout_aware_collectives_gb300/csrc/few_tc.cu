@@ -68,26 +68,25 @@ __device__ __forceinline__ float4 peer_read(uint32_t addr) {
   return v;
 }
 
-// Sums of the cluster's CTAs' sums at N addresses, in rank order.  The reads
-// of two ranks are on their way before the first is added.
+// Sums of the cluster's CTAs' sums at N addresses, in rank order.  All of one
+// rank's reads are on their way before the first is added.
 template <int N>
 __device__ __forceinline__ void cluster_sums(const uint32_t (&addr)[N], int split, float4 (&v)[N]) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  for (int r = 0; r < split; r += 2) {
-    float4 a[N], b[N];
-    const bool two = r + 1 < split;
+  for (int i = 0; i < N; ++i) v[i] = peer_read(peer_addr(addr[i], 0));
+#pragma unroll 1
+  for (int r = 1; r < split; ++r) {
+    float4 a[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) a[i] = peer_read(peer_addr(addr[i], r));
-    if (two)
-#pragma unroll
-      for (int i = 0; i < N; ++i) b[i] = peer_read(peer_addr(addr[i], r + 1));
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i].x += a[i].x, v[i].y += a[i].y, v[i].z += a[i].z, v[i].w += a[i].w;
-    if (two)
-#pragma unroll
-      for (int i = 0; i < N; ++i) v[i].x += b[i].x, v[i].y += b[i].y, v[i].z += b[i].z, v[i].w += b[i].w;
   }
+}
+__device__ __forceinline__ float4 own_read(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+  return v;
 }
 
 __device__ __forceinline__ void sums_barrier() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
@@ -285,29 +284,25 @@ __global__ void __launch_bounds__(kThreads) few_tc_kernel(const __grid_constant_
     const bool in = col < p.features;
     const int64_t nb = (p.features + kBlock - 1) / kBlock;
     const int live = min(NT, p.tokens - token0);
-    for (int t = rank * kWarps + warp; t < live; t += kWarps * split) {
+    // One token's results from its sums.
+    const auto finish = [&](int t, const float4* v) {
       const int64_t token = token0 + t;
-      uint32_t addr[S::kParts];
-      float4 v[S::kParts];
-#pragma unroll
-      for (int q = 0; q < S::kParts; ++q) addr[q] = smem + (uint32_t)((q * NT + t) * kRows + lane * 4) * 4;
-      cluster_sums(addr, split, v);
       float4 r = v[0];
       if constexpr (KIND == kGrad) {
-        if (!in) continue;
+        if (!in) return;
         const uint2 dh = *(const uint2*)(p.dh + token * p.lddh + col);
         const float d[4] = {bf16_lo(dh.x), bf16_hi(dh.x), bf16_lo(dh.y), bf16_hi(dh.y)};
         const float g[4] = {v[0].x, v[0].y, v[0].z, v[0].w}, u[4] = {v[1].x, v[1].y, v[1].z, v[1].w};
         float dg[4], du[4], h[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float2 t = activation_grad<ACT>(g[i]);
-          dg[i] = d[i] * u[i] * t.y, du[i] = d[i] * t.x, h[i] = t.x * u[i];
+          const float2 s = activation_grad<ACT>(g[i]);
+          dg[i] = d[i] * u[i] * s.y, du[i] = d[i] * s.x, h[i] = s.x * u[i];
         }
         const int64_t at = token * p.features + col;
         *(uint2*)(p.dg + at) = make_uint2(pack_bf16(dg[0], dg[1]), pack_bf16(dg[2], dg[3]));
         *(uint2*)(p.du + at) = make_uint2(pack_bf16(du[0], du[1]), pack_bf16(du[2], du[3]));
-        if (!p.out) continue;
+        if (!p.out) return;
         r = make_float4(h[0], h[1], h[2], h[3]);
       }
       if constexpr (KIND == kForward) {
@@ -320,6 +315,31 @@ __global__ void __launch_bounds__(kThreads) few_tc_kernel(const __grid_constant_
         }
       }
       if (in) *(uint2*)(p.out + token * p.ldo + col) = make_uint2(pack_bf16(r.x, r.y), pack_bf16(r.z, r.w));
+    };
+    const auto sums_at = [&](int t, int q) { return smem + (uint32_t)((q * NT + t) * kRows + lane * 4) * 4; };
+    constexpr int P = S::kParts;
+    const int each = kWarps * split;
+    for (int t = rank * kWarps + warp; t < live; t += 2 * each) {
+      uint32_t addr[2 * P];
+      float4 v[2 * P];
+      const bool two = t + each < live;
+#pragma unroll
+      for (int q = 0; q < P; ++q) addr[q] = sums_at(t, q), addr[P + q] = sums_at(t + each, q);
+      if (split == 1) {
+#pragma unroll
+        for (int q = 0; q < P; ++q) {
+          v[q] = own_read(addr[q]);
+          if (two) v[P + q] = own_read(addr[P + q]);
+        }
+      } else if (two) {
+        cluster_sums(addr, split, v);
+      } else {
+        const uint32_t (&first)[P] = *(const uint32_t(*)[P])addr;
+        float4 (&w)[P] = *(float4(*)[P])v;
+        cluster_sums(first, split, w);
+      }
+      finish(t, v);
+      if (two) finish(t + each, v + P);
     }
   }
   if (split > 1) cluster_sync();  // the others have read this CTA's sums
@@ -349,7 +369,8 @@ int clusters_of(int split) {
 }
 
 // CTAs that share a tile's contraction: up to one for each SM, all at work at
-// one time, each with at least two stages of it.  (One tile for each of 112
+// one time, each with at least four stages of it (fewer stages less save
+// less than the clusters' exchange takes).  (One tile for each of 112
 // SMs streams 4096 x 14336 weights in 44 us, split in two 45.5; 16 tiles of
 // 64 tokens take 13.4 us split in four, 20.5 split in eight, where the last
 // clusters wait for the first.)
@@ -357,7 +378,7 @@ template <int KIND, int NT, int ACT>
 int split_of(int64_t tiles, int64_t steps, int sms) {
   static const int held[3] = {clusters_of<KIND, NT, ACT>(2), clusters_of<KIND, NT, ACT>(4), clusters_of<KIND, NT, ACT>(8)};
   int s = 1;
-  for (int i = 0; i < 3 && 2 * s * tiles <= sms && tiles <= held[i] && steps >= 4 * s; ++i) s *= 2;
+  for (int i = 0; i < 3 && 2 * s * tiles <= sms && tiles <= held[i] && steps >= 8 * s; ++i) s *= 2;
   return s;
 }
 
@@ -412,10 +433,11 @@ cudaError_t gated(Params& p, const GatedArgs& a, const TcLaunch& l, cudaStream_t
 
 // Past 64 tokens the 256-row tiles read fewer operand bytes: they are ahead
 // for the gated block from about half as many of these tiles as SMs (1021 x
-// 2048 x 768, 96 tiles: 14.8 us against 19.6), for the 8-bit product, whose
-// large tiles are slower each, from as many as SMs.
+// 2048 x 768, 96 tiles: 13.2 us against 19.6; 512 tokens, 48 tiles: 13.0
+// against 11.7), for the 8-bit product from two thirds (128 x 28672 x 8192,
+// 128 tiles: 76 us against 87; 1021 x 2048 x 768: 9.6 against 9.1).
 bool gated_few_takes(const GatedArgs& a, int sms) { return few(a.tokens, a.ffn, sms / 2); }
-bool fp8_few_takes(const MatmulArgs& a, int sms) { return few(a.m, a.n, sms); }
+bool fp8_few_takes(const MatmulArgs& a, int sms) { return few(a.m, a.n, 2 * sms / 3); }
 
 cudaError_t launch_gated_forward_few(const GatedArgs& a, const TcLaunch& l, cudaStream_t stream) {
   Params p{};

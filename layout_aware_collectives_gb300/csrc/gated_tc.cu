@@ -35,15 +35,13 @@ constexpr uint32_t kOperand = kHalf * kStep * 2;  // bytes of either in one stag
 constexpr uint32_t kStage = 2 * kOperand;
 constexpr int kAllBoxes = 16;                 // boxes of results in flight
 constexpr size_t kSmem = 1024 + kStages * kStage + kAllBoxes * kBox;
-// Warps that read finished sums.  Eight for dX and dW, whose tiles write 128
-// KiB and, for few tokens, have few stages to do it behind (64 tokens of the
-// 8B-shaped block: dW 70 us with four); the others need the registers.
-template <int FORM>
-constexpr int kEpiWarps = FORM == kBack ? 8 : 4;
-template <int FORM>
-constexpr int kThreads = 128 + 32 * kEpiWarps<FORM>;
-template <int FORM>
-constexpr int kBoxes = kAllBoxes / kEpiWarps<FORM>;
+// Eight warps read finished sums, each 32 rows of one half of the columns:
+// with a short contraction there is little of the next tile's sum to do it
+// behind (64 tokens of the 8B-shaped block: dW 70 us with four, 52 with
+// eight).
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 128 + 32 * kEpiWarps;
+constexpr int kBoxes = kAllBoxes / kEpiWarps;
 constexpr int kJoinThreads = 256;
 
 struct Params {
@@ -139,7 +137,7 @@ __device__ __forceinline__ bool work_at(const Params& p, int pair, int pairs, in
 
 template <int FORM, int ACT>
 __device__ __forceinline__ void epilogue(const Params& p, const Work& work, uint32_t tmem, int row0, int half,
-                                         Outbox<kBoxes<FORM>>& out) {
+                                         uint32_t* maxima, Outbox<kBoxes>& out) {
   const TileAt& t = work.at;
   const int row = row0 + out.lane, rows = work.w ? p.w_rows : p.rows;
   const bool any = row0 < rows, mine = row < rows;
@@ -148,10 +146,23 @@ __device__ __forceinline__ void epilogue(const Params& p, const Work& work, uint
     float ginv = 0.0f, uinv = 0.0f;
     bool clean = true;  // no infinities to be made NaN in the codes
     if constexpr (FORM == kForward) {
-      if (p.g8) {  // the tile is one scale block wide: a thread holds a whole block of its token
+      if (p.g8) {
+        // The tile is one scale block wide: a thread holds half a block of
+        // its token, and meets the thread that holds the other half.  The
+        // block's exponent is the larger of the halves'.
+        const auto meet = [&](float g, float u) {
+          const auto code = [](float m) { return m == 0.0f ? 0u : m == CUDART_INF_F ? 255u : scale_exponent(m); };
+          const uint32_t mine = code(g) | (code(u) << 16);
+          uint32_t* at = maxima + (row & (kHalf - 1));
+          at[half * kHalf] = mine;
+          asm volatile("bar.sync %0, 64;" ::"r"(1 + ((row0 >> 5) & 3)) : "memory");
+          const uint32_t both = __vmaxu2(mine, at[(half ^ 1) * kHalf]);
+          asm volatile("bar.sync %0, 64;" ::"r"(1 + ((row0 >> 5) & 3)) : "memory");
+          return both;
+        };
         float gmax = 0.0f, umax = 0.0f;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 2 * half; c < 2 * half + 2; ++c) {
           uint32_t g[32], u[32];
           tmem_read32x2(tmem + c * 32, tmem + kHalf + c * 32, g, u);
 #pragma unroll
@@ -160,11 +171,13 @@ __device__ __forceinline__ void epilogue(const Params& p, const Work& work, uint
             umax = fmaxf(umax, fabsf(as_f(u[i])));
           }
         }
-        clean = !__any_sync(0xffffffffu, gmax == CUDART_INF_F || umax == CUDART_INF_F);
+        uint32_t top = meet(gmax, umax);
+        // the same for both warps: each sees both halves' maxima of 32 rows
+        clean = !__any_sync(0xffffffffu, (top & 0xffffu) == 255u || (top >> 16) == 255u);
         if (!clean) {  // again without the infinities
           gmax = umax = 0.0f;
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 2 * half; c < 2 * half + 2; ++c) {
             uint32_t g[32], u[32];
             tmem_read32x2(tmem + c * 32, tmem + kHalf + c * 32, g, u);
 #pragma unroll
@@ -173,10 +186,11 @@ __device__ __forceinline__ void epilogue(const Params& p, const Work& work, uint
               umax = fmaxf(umax, fabsf(no_infinity(as_f(u[i]))));
             }
           }
+          top = meet(gmax, umax);
         }
-        const uint32_t eg = scale_exponent(gmax), eu = scale_exponent(umax);
+        const uint32_t eg = (top & 0xffffu) ? top & 0xffffu : 127u, eu = (top >> 16) ? top >> 16 : 127u;
         ginv = exponent_inverse(eg), uinv = exponent_inverse(eu);
-        if (mine) {
+        if (mine && half == 0) {
           const int64_t nb = (p.cols + kBlock - 1) / kBlock;
           p.gs[row * nb + t.n] = exponent_value(eg);
           p.us[row * nb + t.n] = exponent_value(eu);
@@ -184,12 +198,13 @@ __device__ __forceinline__ void epilogue(const Params& p, const Work& work, uint
       }
     }
 #pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
+    for (int c = 2 * half; c < 2 * half + 2; ++c) {
       const int col = col0 + c * 32;
       if (!any || col >= p.cols) break;
-      uint32_t g[32], u[32], o[16];
-      tmem_read32x2(tmem + c * 32, tmem + kHalf + c * 32, g, u);
+      uint32_t o[16];
       if constexpr (FORM == kForward) {
+        uint32_t g[32], u[32];
+        tmem_read32x2(tmem + c * 32, tmem + kHalf + c * 32, g, u);
         if (p.g8 && mine) {
           put_codes(p.g8 + (int64_t)row * p.cols + col, g, ginv, p.cols - col, clean);
           put_codes(p.u8 + (int64_t)row * p.cols + col, u, uinv, p.cols - col, clean);
@@ -202,16 +217,23 @@ __device__ __forceinline__ void epilogue(const Params& p, const Work& work, uint
       } else {
         uint32_t o1[16], o2[16];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint4 d = make_uint4(0, 0, 0, 0);
-          if (mine && col + 8 * q < p.cols) d = __ldcs((const uint4*)(p.dh + row * p.lddh + col + 8 * q));
-          const uint32_t w[4] = {d.x, d.y, d.z, d.w};
+        for (int q = 0; q < 2; ++q) {  // 16 columns at a time, for the registers
+          uint32_t g[16], u[16], w[8];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int i = 4 * q + j;
+          for (int j = 0; j < 2; ++j) {
+            uint4 d = make_uint4(0, 0, 0, 0);
+            if (mine && col + 16 * q + 8 * j < p.cols)
+              d = __ldcs((const uint4*)(p.dh + row * p.lddh + col + 16 * q + 8 * j));
+            w[4 * j] = d.x, w[4 * j + 1] = d.y, w[4 * j + 2] = d.z, w[4 * j + 3] = d.w;
+          }
+          tmem_read(tmem + c * 32 + 16 * q, g);
+          tmem_read(tmem + kHalf + c * 32 + 16 * q, u);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int i = 8 * q + j;
             const float d0 = bf16_lo(w[j]), d1 = bf16_hi(w[j]);
-            const float2 t0 = activation_grad<ACT>(as_f(g[2 * i])), t1 = activation_grad<ACT>(as_f(g[2 * i + 1]));
-            const float u0 = as_f(u[2 * i]), u1 = as_f(u[2 * i + 1]);
+            const float2 t0 = activation_grad<ACT>(as_f(g[2 * j])), t1 = activation_grad<ACT>(as_f(g[2 * j + 1]));
+            const float u0 = as_f(u[2 * j]), u1 = as_f(u[2 * j + 1]);
             o[i] = pack_bf16(d0 * u0 * t0.y, d1 * u1 * t1.y);
             o1[i] = pack_bf16(d0 * t0.x, d1 * t1.x);
             o2[i] = pack_bf16(t0.x * u0, t1.x * u1);
@@ -245,10 +267,11 @@ __device__ __forceinline__ void epilogue(const Params& p, const Work& work, uint
 }
 
 template <int FORM, int ACT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<FORM>, 1) gated_tc_kernel(const __grid_constant__ Params p) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_constant__ Params p) {
   constexpr bool kBMn = FORM == kBack;
   extern __shared__ uint8_t raw[];
   __shared__ uint64_t bars[2 * kStages + 5];
+  __shared__ uint32_t maxima[FORM == kForward ? 2 * kHalf : 1];  // of the checkpoint's half blocks, as exponents
   __shared__ uint32_t tmem_at;
   __shared__ int stop;
 
@@ -267,7 +290,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<FORM>, 1) g
   if (threadIdx.x == 0) {
     stop = 0;
     for (int s = 0; s < kStages; ++s) bar_init(full(s), 1), bar_init(empty(s), 1);
-    for (int b = 0; b < 2; ++b) bar_init(sums_full(b), 1), bar_init(sums_empty(b), 2 * kEpiWarps<FORM>);
+    for (int b = 0; b < 2; ++b) bar_init(sums_full(b), 1), bar_init(sums_empty(b), 2 * kEpiWarps);
     bar_init(spare, 1);
     bar_init_fence();
     prefetch_map(FORM == kBack && !p.tiles ? &p.wa[0] : &p.a[0]), prefetch_map(FORM == kBack && !p.tiles ? &p.wb : &p.b[0]);
@@ -363,14 +386,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<FORM>, 1) g
       }
     }
   } else if (warp >= 4) {
-    Outbox<kBoxes<FORM>> out{smem + kStages * kStage + (warp - 4) * kBoxes<FORM> * kBox, 0, lane};
+    Outbox<kBoxes> out{smem + kStages * kStage + (warp - 4) * kBoxes * kBox, 0, lane};
     Work work;
     for (int i = 0; work_at<FORM>(p, pair, pairs, i, work); ++i) {
       const int b = i & 1;
       if (!bar_wait_warp(sums_full(b), (i / 2) & 1, watch)) break;
       fence_after();
       const uint32_t lanes = (uint32_t)(warp & 3) * 32;
-      epilogue<FORM, ACT>(p, work, tmem + (lanes << 16) + b * 256, (work.at.m * 2 + rank) * kHalf + lanes, (warp - 4) >> 2, out);
+      epilogue<FORM, ACT>(p, work, tmem + (lanes << 16) + b * 256, (work.at.m * 2 + rank) * kHalf + lanes, (warp - 4) >> 2, maxima, out);
       fence_before();
       __syncwarp();
       if (lane == 0) bar_arrive_peer(peer_addr(sums_empty(b), 0));
@@ -410,7 +433,7 @@ cudaError_t launch(Params& p, const TcLaunch& l, cudaStream_t stream) {
   p.limit_ns = TIDE_BULK_TIMEOUT_NS;
   p.stall_ns = l.stall_ns;
   const int pairs = p.tiles + p.w_tiles < l.pairs ? p.tiles + p.w_tiles : l.pairs;
-  return launch_early(gated_tc_kernel<FORM, ACT>, dim3(2 * pairs), kThreads<FORM>, kSmem, 0, stream, p);
+  return launch_early(gated_tc_kernel<FORM, ACT>, dim3(2 * pairs), kThreads, kSmem, 0, stream, p);
 }
 
 bool rows16(int64_t width, int64_t ld) { return width % 8 == 0 && ld % 8 == 0; }
@@ -457,7 +480,7 @@ int gated_tc_pairs() {
   cudaFuncSetAttribute(gated_tc_kernel<kBack, 0>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   cudaLaunchConfig_t c{};
   c.gridDim = dim3(2);
-  c.blockDim = dim3(kThreads<kBack>);
+  c.blockDim = dim3(kThreads);
   c.dynamicSmemBytes = kSmem;
   int n = 0;
   if (cudaOccupancyMaxActiveClusters(&n, gated_tc_kernel<kBack, 0>, &c) != cudaSuccess) return 0;
