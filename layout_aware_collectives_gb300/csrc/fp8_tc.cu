@@ -96,7 +96,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) summed_
     // 384 threads start with 168 registers each (64,512); this warpgroup goes
     // down to 56 and the two that hold sums go up to 216: 62,464.
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    if (warp == 0 && lane == 0) {
+    if ((warp == 0 || warp == 3) && lane == 0) {
+      const bool load_a = warp == 0;  // one thread loads A, another B
       int j = 0;  // stages filled so far
       bool go = true;
       for (int t = pair; t < p.tiles && go; t += pairs) {
@@ -107,11 +108,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) summed_
             go = false;
             break;
           }
-          if (rank == 0) bar_expect(full(s), 2 * kStage);
+          if (load_a && rank == 0) bar_expect(full(s), 2 * kStage);
           const uint32_t bar = peer_addr(full(s), 0);
           const uint32_t a = smem + s * kStage;
-          load_box<true>(a, &p.a, k * kBlock, (at.m * 2 + rank) * kHalf, bar);
-          load_box<true>(a + kOperand, &p.b, k * kBlock, (at.n * 2 + rank) * kHalf, bar);
+          if (load_a)
+            load_box<true>(a, &p.a, k * kBlock, (at.m * 2 + rank) * kHalf, bar);
+          else
+            load_box<true>(a + kOperand, &p.b, k * kBlock, (at.n * 2 + rank) * kHalf, bar);
         }
       }
       // the MMAs' last arrivals reach this CTA while it is still there
@@ -263,8 +266,9 @@ __global__ void __cluster_dims__(2, 1, 1)
 
   if (p.stall_ns) {  // test: a wait on a barrier nothing arrives on runs out
     if (threadIdx.x == 0) bar_wait(spare, 0, Watch{&stop, p.err, p.stall_ns});
-  } else if (warp == 0) {
+  } else if (warp == 0 || warp == 3) {
     if (lane == 0) {
+      const bool load_a = warp == 0;  // one thread loads A, another B
       int j = 0;  // stages filled so far
       bool go = true;
       for (int t = pair; t < p.tiles && go; t += pairs) {
@@ -275,11 +279,13 @@ __global__ void __cluster_dims__(2, 1, 1)
             go = false;
             break;
           }
-          if (rank == 0) bar_expect(full(s), 2 * kStage);
+          if (load_a && rank == 0) bar_expect(full(s), 2 * kStage);
           const uint32_t bar = peer_addr(full(s), 0);
           const uint32_t a = smem + s * kStage;
-          load_box<true>(a, &p.a, k * kBlock, (at.m * 2 + rank) * kHalf, bar);
-          load_box<true>(a + kOperand, &p.b, k * kBlock, (at.n * 2 + rank) * kHalf, bar);
+          if (load_a)
+            load_box<true>(a, &p.a, k * kBlock, (at.m * 2 + rank) * kHalf, bar);
+          else
+            load_box<true>(a + kOperand, &p.b, k * kBlock, (at.n * 2 + rank) * kHalf, bar);
         }
       }
       // the MMAs' last arrivals reach this CTA while it is still there

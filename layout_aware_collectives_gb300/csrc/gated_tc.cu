@@ -13,7 +13,7 @@
 // same 128 features of Wu: each CTA's accumulator then holds its tokens' gate
 // and up sums side by side, and the product needs no exchange.
 //
-// Roles: warp 0 loads (6 stages of 32 KiB), warp 1 of the pair's first CTA
+// Roles: warps 0 and 3 load (6 stages of 32 KiB), warp 1 of the pair's first CTA
 // issues the MMAs, warps from 4 on read finished sums out of TMEM, which holds two
 // accumulators so that they do so while the next tile is summed.  Bound by
 // the tensor cores at every large size.
@@ -56,6 +56,7 @@ struct Params {
   float* parts;    // [split, rows, cols] of them, where there are several
   int w_rows, w_tiles_m, w_tiles_n, w_tiles, w_steps;  // back: dW, both halves' tiles
   int extra;       // back: tiles of dW that take as long as one of dX
+  bool one_a, one_b;  // back: wa's, b's and wb's operands are one box each (map_mn)
   // epilogue
   uint8_t *g8, *u8;
   float *gs, *us;
@@ -86,6 +87,16 @@ __device__ __forceinline__ void put_codes(uint8_t* dst, const uint32_t (&v)[32],
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (8 * i < valid) ((uint2*)dst)[i] = make_uint2(c[2 * i], c[2 * i + 1]);
+  }
+}
+
+// 128 columns x 64 of the contraction: a box of both halves, or one each.
+__device__ __forceinline__ void load_mn(uint32_t dst, const CUtensorMap* m, int col, int k0, uint32_t bar, bool one) {
+  if (one) {
+    load_box3(dst, m, 0, k0, col / 64, bar);
+  } else {
+    load_box<true>(dst, m, col, k0, bar);
+    load_box<true>(dst + kOperand / 2, m, col + 64, k0, bar);
   }
 }
 
@@ -305,8 +316,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gated_t
 
   if (p.stall_ns) {  // test: a wait on a barrier nothing arrives on runs out
     if (threadIdx.x == 0) bar_wait(spare, 0, Watch{&stop, p.err, p.stall_ns});
-  } else if (warp == 0) {
+  } else if (warp == 0 || warp == 3) {
+    // One thread loads A, another B: issuing a copy takes long enough that
+    // one thread with all four of a stage fell behind the MMAs.
     if (lane == 0) {
+      const bool load_a = warp == 0;
       int j = 0;  // stages filled so far
       bool go = true;
       Work work;
@@ -319,23 +333,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gated_t
             go = false;
             break;
           }
-          if (rank == 0) bar_expect(full(s), 2 * kStage);
+          if (load_a && rank == 0) bar_expect(full(s), 2 * kStage);
           const uint32_t bar = peer_addr(full(s), 0);
           const uint32_t a = smem + s * kStage, b = a + kOperand;
           if constexpr (FORM != kBack) {
-            load_box<true>(a, &p.a[0], k * kStep, row, bar);
-            load_box<true>(b, &p.b[rank], k * kStep, at.n * kHalf, bar);
+            if (load_a)
+              load_box<true>(a, &p.a[0], k * kStep, row, bar);
+            else
+              load_box<true>(b, &p.b[rank], k * kStep, at.n * kHalf, bar);
           } else {
             const int second = !work.w && k >= p.half_steps, k0 = (k - (second ? p.half_steps : 0)) * kStep;
-            if (work.w) {
-              load_box<true>(a, &p.wa[at.z], row, k0, bar);
-              load_box<true>(a + kOperand / 2, &p.wa[at.z], row + 64, k0, bar);
+            if (!load_a) {
+              const CUtensorMap* mb = work.w ? &p.wb : &p.b[second];
+              load_mn(b, mb, col, k0, bar, p.one_b);
+            } else if (work.w) {
+              load_mn(a, &p.wa[at.z], row, k0, bar, p.one_a);
             } else {
               load_box<true>(a, &p.a[second], k0, row, bar);
             }
-            const CUtensorMap* mb = work.w ? &p.wb : &p.b[second];
-            load_box<true>(b, mb, col, k0, bar);
-            load_box<true>(b + kOperand / 2, mb, col + 64, k0, bar);
           }
         }
       }
@@ -439,12 +454,17 @@ cudaError_t launch(Params& p, const TcLaunch& l, cudaStream_t stream) {
 bool rows16(int64_t width, int64_t ld) { return width % 8 == 0 && ld % 8 == 0; }
 
 // Operand boxes: 64 of the contraction x 128 rows (K-major), or 64 columns x
-// 64 of the contraction (MN-major); both are 128 bytes wide.
+// 64 of the contraction (MN-major); both are 128 bytes wide.  Where the width
+// is a multiple of 64 the latter's matrix is taken as slabs of 64 columns, so
+// that one box holds two of them: the fewer boxes a stage has, the less its
+// loads lag (70B-shaped dX and dW: 5.25 ms with four boxes by one thread, 4.81
+// by two threads, 4.74 with two boxes).
 bool map_k(CUtensorMap* m, const uint16_t* p, int64_t cols, int64_t rows, int64_t ld) {
   return make_map(m, p, 2, cols, rows, ld, kStep, kHalf, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 bool map_mn(CUtensorMap* m, const uint16_t* p, int64_t cols, int64_t rows, int64_t ld) {
-  return make_map(m, p, 2, cols, rows, ld, 64, kStep, CU_TENSOR_MAP_SWIZZLE_128B);
+  return cols % 64 == 0 ? make_slab_map(m, p, cols, rows, ld, kStep)
+                        : make_map(m, p, 2, cols, rows, ld, 64, kStep, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 bool map_out(CUtensorMap* m, const uint16_t* p, int64_t cols, int64_t rows, int64_t ld) {
   return make_map(m, p, 2, cols, rows, ld, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
@@ -516,6 +536,7 @@ cudaError_t launch_gated_grad_tc(const GatedArgs& a, const TcLaunch& l, cudaStre
 cudaError_t launch_gated_back_tc(const GatedArgs& a, bool dx, bool dw, const TcLaunch& l, cudaStream_t stream) {
   Params p{};
   p.cols = (int)a.hidden;
+  p.one_a = a.ffn % 64 == 0, p.one_b = a.hidden % 64 == 0;
   if (dx) {
     p.rows = (int)a.tokens;
     p.tiles_m = (int)ceil_div(a.tokens, 2 * kHalf), p.tiles_n = (int)ceil_div(a.hidden, 2 * kHalf);

@@ -17,4 +17,9 @@ namespace tide {
 bool make_map(CUtensorMap* map, const void* p, int elem, int64_t cols, int64_t rows, int64_t ld, uint32_t box_cols,
               uint32_t box_rows, CUtensorMapSwizzle swizzle);
 
+// Map of a row-major bf16 matrix, `cols` a multiple of 64, as slabs of 64
+// columns: coordinates (column of the slab, row, slab), boxes of two slabs by
+// box_rows rows, 128-byte swizzle.
+bool make_slab_map(CUtensorMap* map, const void* p, int64_t cols, int64_t rows, int64_t ld, uint32_t box_rows);
+
 }  // namespace tide
