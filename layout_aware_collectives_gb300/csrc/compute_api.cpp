@@ -118,15 +118,16 @@ int64_t round256(int64_t v) { return (v + 255) / 256 * 256; }
 
 // Offsets of the workspace's parts.
 struct Workspace {
-  int64_t dg, du, x, parts, bytes;
+  int64_t dg, du, x, dx_parts, dw_parts, bytes;
 };
 Workspace workspace_of(int64_t tokens, int64_t hidden, int64_t ffn) {
-  Workspace w;
-  w.dg = 0;
+  Workspace w{};
+  if (tokens == 0) return w;
   w.du = round256(2 * tokens * ffn);
   w.x = w.du + round256(2 * tokens * ffn);
-  w.parts = w.x + round256(2 * tokens * hidden);
-  w.bytes = w.parts + round256(gated_parts_bytes(tokens, hidden));
+  w.dx_parts = w.x + round256(2 * tokens * hidden);
+  w.dw_parts = w.dx_parts + round256(gated_dx_parts_bytes(tokens, hidden));
+  w.bytes = w.dw_parts + round256(gated_dw_parts_bytes(hidden, ffn));
   return w;
 }
 
@@ -301,7 +302,8 @@ tide_status_t tide_gated_backward(tide_compute_t c, int64_t tokens, int64_t hidd
   }
   a.dg = (uint16_t*)((char*)workspace + w.dg);
   a.du = (uint16_t*)((char*)workspace + w.du);
-  a.parts = (float*)((char*)workspace + w.parts), a.parts_bytes = w.bytes - w.parts;
+  a.dx_parts = (float*)((char*)workspace + w.dx_parts), a.dx_parts_bytes = w.dw_parts - w.dx_parts;
+  a.dw_parts = (float*)((char*)workspace + w.dw_parts), a.dw_parts_bytes = w.bytes - w.dw_parts;
   const TcLaunch l = launch_of(c);
   const bool tc = gated_tc_takes(a);
   Fp8Args xr{};

@@ -50,8 +50,8 @@ struct GatedArgs {
   uint16_t* dwu;
   uint16_t* dg;  // [tokens, ffn] each, workspace
   uint16_t* du;
-  float* parts;  // of dX's sums, workspace
-  int64_t parts_bytes;
+  float *dx_parts, *dw_parts;  // of dX's and dW's sums, workspace
+  int64_t dx_parts_bytes, dw_parts_bytes;
 };
 
 struct MatmulArgs {
@@ -114,7 +114,9 @@ struct TcLaunch {
 // whose rows start on 16 bytes.
 int gated_tc_pairs();
 bool gated_tc_takes(const GatedArgs& a);
-int64_t gated_parts_bytes(int64_t tokens, int64_t hidden);  // workspace for the parts of dX's sums
+// Workspace for the parts of dX's and dW's sums.
+int64_t gated_dx_parts_bytes(int64_t tokens, int64_t hidden);
+int64_t gated_dw_parts_bytes(int64_t hidden, int64_t ffn);
 cudaError_t launch_gated_forward_tc(const GatedArgs& a, const TcLaunch& l, cudaStream_t stream);
 cudaError_t launch_gated_grad_tc(const GatedArgs& a, const TcLaunch& l, cudaStream_t stream);
 // dX, dWg and dWu, or either.

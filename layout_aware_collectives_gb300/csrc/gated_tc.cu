@@ -52,8 +52,8 @@ struct Params {
   int tiles_m, tiles_n, tiles;
   int steps;       // stages of one tile's sum
   int half_steps;  // back: stages of dX's first half
-  int split;       // back: parts of dX's sums, each in its own tile
-  float* parts;    // [split, rows, cols] of them, where there are several
+  int split, w_split;  // back: parts of dX's and of dW's sums, each in its own tile
+  float *parts, *w_parts;  // of [split, cols, rows], [w_split, half, cols, w_rows], where there are several
   int w_rows, w_tiles_m, w_tiles_n, w_tiles, w_steps;  // back: dW, both halves' tiles
   int extra;       // back: tiles of dW that take as long as one of dX
   bool one_a, one_b;  // back: wa's, b's and wb's operands are one box each (map_mn)
@@ -102,8 +102,10 @@ __device__ __forceinline__ void load_mn(uint32_t dst, const CUtensorMap* m, int 
 
 // One tile of a pair's work.
 struct Work {
-  TileAt at;   // z: the half of dW, or the part of dX's sum
+  TileAt at;
   bool w;      // a tile of dW
+  int half;    // of dW
+  float* part;  // this part of the sums, [cols, rows], where there are several
   int k0, k1;  // stages of the whole sum
 };
 
@@ -122,6 +124,7 @@ __device__ __forceinline__ bool work_at(const Params& p, int pair, int pairs, in
     if (FORM == kBack) {
       r.k0 = (int)((int64_t)p.steps * r.at.z / p.split);
       r.k1 = (int)((int64_t)p.steps * (r.at.z + 1) / p.split);
+      r.part = p.split > 1 ? p.parts + (int64_t)r.at.z * p.rows * p.cols : nullptr;
     }
     return true;
   }
@@ -141,8 +144,11 @@ __device__ __forceinline__ bool work_at(const Params& p, int pair, int pairs, in
   if (first >= 0) t = first + (l >= 0 ? l : light + pair) + i * pairs;
   if (t >= p.w_tiles) return false;
   r.w = true;
-  r.k1 = p.w_steps;
   r.at = tile_at(p.w_tiles_m, p.w_tiles_n, t);
+  r.half = r.at.z & 1;
+  r.k0 = (int)((int64_t)p.w_steps * (r.at.z >> 1) / p.w_split);
+  r.k1 = (int)((int64_t)p.w_steps * ((r.at.z >> 1) + 1) / p.w_split);
+  r.part = p.w_split > 1 ? p.w_parts + (int64_t)r.at.z * p.w_rows * p.cols : nullptr;
   return true;
 }
 
@@ -256,18 +262,19 @@ __device__ __forceinline__ void epilogue(const Params& p, const Work& work, uint
       }
     }
   } else {
-    const CUtensorMap* map = &p.out[work.w ? 1 + t.z : 0];
+    const CUtensorMap* map = &p.out[work.w ? 1 + work.half : 0];
 #pragma unroll 1
     for (int c = half * 4; c < half * 4 + 4; ++c) {
       const int col = t.n * 2 * kHalf + c * 32;
       if (!any || col >= p.cols) break;
       uint32_t v[32], o[16];
       tmem_read(tmem + c * 32, v);
-      if (FORM == kBack && !work.w && p.split > 1) {
-        uint4* to = (uint4*)(p.parts + ((int64_t)t.z * p.rows + row) * p.cols + col);
+      if (work.part) {
+        // a column of the warp's 32 rows lies together, so its threads do
+        uint32_t* to = (uint32_t*)work.part + (int64_t)col * rows + row;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (mine && col + 4 * i < p.cols) to[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        for (int i = 0; i < 32; ++i)
+          if (mine && col + i < p.cols) to[(int64_t)i * rows] = v[i];
         continue;
       }
 #pragma unroll
@@ -347,7 +354,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gated_t
               const CUtensorMap* mb = work.w ? &p.wb : &p.b[second];
               load_mn(b, mb, col, k0, bar, p.one_b);
             } else if (work.w) {
-              load_mn(a, &p.wa[at.z], row, k0, bar, p.one_a);
+              load_mn(a, &p.wa[work.half], row, k0, bar, p.one_a);
             } else {
               load_box<true>(a, &p.a[second], k0, row, bar);
             }
@@ -420,23 +427,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gated_t
   if (warp == 2) tmem_free<2>(tmem, 512);
 }
 
-// dX from the parts of its sums, in their order: 8 columns a thread.
-__global__ void __launch_bounds__(kJoinThreads)
-    join_kernel(const float* parts, int split, uint16_t* dx, int64_t ld, uint32_t groups_per_row, uint32_t groups, int64_t numel) {
+// Results from the parts of their sums, in the parts' order.  A part lies
+// column by column, `out0`'s parts before `out1`'s: 32 rows x 64 columns a
+// CTA, turned in shared memory.
+struct Join {
+  const float* parts;
+  int split;
+  uint16_t* out[2];
+  int64_t ld;
+  int rows, cols;
+};
+
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(Join a) {
   after_previous();
-  const uint32_t i = blockIdx.x * kJoinThreads + threadIdx.x;
-  if (i >= groups) return;
-  const uint32_t row = i / groups_per_row, col = (i - row * groups_per_row) * 8;
-  const float4* from = (const float4*)(parts + (int64_t)i * 8);
-  float4 a = from[0], b = from[1];
-  for (int s = 1; s < split; ++s) {
-    from += numel / 4;
-    const float4 c = from[0], d = from[1];
-    a.x += c.x, a.y += c.y, a.z += c.z, a.w += c.w;
-    b.x += d.x, b.y += d.y, b.z += d.z, b.w += d.w;
+  __shared__ float tile[64][33];
+  const int row0 = blockIdx.x * 32, col0 = blockIdx.y * 64;
+  const int r = threadIdx.x & 31, c0 = threadIdx.x >> 5;
+  const int64_t numel = (int64_t)a.rows * a.cols, next = numel * gridDim.z;
+  float sum[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sum[i] = 0.0f;
+  if (row0 + r < a.rows) {
+    const float* from = a.parts + blockIdx.z * numel + (int64_t)(col0 + c0) * a.rows + row0 + r;
+    for (int s = 0; s < a.split; s += 4) {  // 32 reads on their way at a time
+      float v[4][8];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          v[q][i] = s + q < a.split && col0 + c0 + 8 * i < a.cols ? from[(s + q) * next + (int64_t)8 * i * a.rows] : 0.0f;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[i] += v[q][i];
+    }
   }
-  *(uint4*)(dx + (int64_t)row * ld + col) =
-      make_uint4(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w), pack_bf16(b.x, b.y), pack_bf16(b.z, b.w));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) tile[c0 + 8 * i][r] = sum[i];
+  __syncthreads();
+  const int row = threadIdx.x >> 3, col = (threadIdx.x & 7) * 8;
+  if (row0 + row >= a.rows || col0 + col >= a.cols) return;  // widths are multiples of 8
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = pack_bf16(tile[col + 2 * i][row], tile[col + 2 * i + 1][row]);
+  uint16_t* out = blockIdx.z ? a.out[1] : a.out[0];
+  *(uint4*)(out + (int64_t)(row0 + row) * a.ld + col0 + col) = make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+cudaError_t join(const Join& a, int outputs, cudaStream_t stream) {
+  return launch_early(join_kernel, dim3((unsigned)ceil_div(a.rows, 32), (unsigned)ceil_div(a.cols, 64), outputs),
+                      kJoinThreads, 0, 0, stream, a);
 }
 
 template <int FORM, int ACT>
@@ -480,17 +520,24 @@ bool fill_pre(Params* p, const GatedArgs& a) {
   return map_k(&p->b[0], a.wg, a.hidden, a.ffn, a.hidden) && map_k(&p->b[1], a.wu, a.hidden, a.ffn, a.hidden);
 }
 
-// Parts of dX's sums.  dX has few tiles for its long contraction; where they
-// leave half of the pairs or more without one, the sums are split so that
-// every pair has work, as far as the workspace holds them (256 tokens of the
-// 8B-shaped block: 16 tiles of 448 stages in 4 parts, 120 -> 55 us), unless
-// that saves fewer stages (0.27 us each) than joining them costs.
-int split_of(int64_t tiles, int64_t steps, int pairs, int64_t room) {
-  int64_t s = pairs / tiles;
-  if (s > steps / 6) s = steps / 6;
-  if (s > room) s = room;
-  return s < 2 || steps - steps / s < 12 ? 1 : (int)s;
+// Parts of the sums of dX or dW.  Where there are fewer than half as many
+// tiles as pairs (dX of few tokens, dW of a small block), the contraction is
+// split and the parts, in fp32, are joined by another kernel.  In stages (0.27
+// us): a tile's share, 18 for the join, and one for each 650 KB of parts.
+// (256 tokens of the 8B-shaped block: 16 tiles of 448 stages, 132 -> 54 us
+// in 4 parts; 1021 x 2048 x 768, 32 tiles of 24: 11 us whole, 18 in two.)
+int split_of(int64_t tiles, int64_t steps, int pairs, int64_t part_bytes, int64_t room) {
+  int best = 1;
+  double least = (double)steps;
+  for (int s = 2; s <= pairs / tiles && 4 * s <= steps && s * part_bytes <= room; ++s) {
+    const double cost = (double)steps / s + 18 + (double)s * part_bytes / 650e3;
+    if (cost < least) least = cost, best = s;
+  }
+  return best;
 }
+
+// The parts of at most one tile for each of a GB300's 76 pairs.
+int64_t parts_bytes(int64_t tiles, int64_t part_bytes) { return tiles ? 76 / tiles * part_bytes : 0; }
 
 }  // namespace
 
@@ -507,10 +554,11 @@ int gated_tc_pairs() {
   return n;
 }
 
-// The parts of at most one tile for each of a GB300's 76 pairs.
-int64_t gated_parts_bytes(int64_t tokens, int64_t hidden) {
-  const int64_t tiles = ceil_div(tokens, 2 * kHalf) * ceil_div(hidden, 2 * kHalf);
-  return tiles && 76 / tiles >= 2 ? 76 / tiles * tokens * hidden * 4 : 0;
+int64_t gated_dx_parts_bytes(int64_t tokens, int64_t hidden) {
+  return parts_bytes(ceil_div(tokens, 2 * kHalf) * ceil_div(hidden, 2 * kHalf), 4 * tokens * hidden);
+}
+int64_t gated_dw_parts_bytes(int64_t hidden, int64_t ffn) {
+  return parts_bytes(2 * ceil_div(ffn, 2 * kHalf) * ceil_div(hidden, 2 * kHalf), 8 * ffn * hidden);
 }
 
 bool gated_tc_takes(const GatedArgs& a) { return a.hidden >= 8 && rows16(a.hidden, a.hidden) && rows16(a.ffn, a.ffn); }
@@ -541,8 +589,8 @@ cudaError_t launch_gated_back_tc(const GatedArgs& a, bool dx, bool dw, const TcL
     p.rows = (int)a.tokens;
     p.tiles_m = (int)ceil_div(a.tokens, 2 * kHalf), p.tiles_n = (int)ceil_div(a.hidden, 2 * kHalf);
     p.half_steps = (int)ceil_div(a.ffn, kStep), p.steps = 2 * p.half_steps;
-    p.split = split_of((int64_t)p.tiles_m * p.tiles_n, p.steps, l.pairs, a.parts_bytes / (a.tokens * a.hidden * 4));
-    p.parts = a.parts;
+    p.split = split_of((int64_t)p.tiles_m * p.tiles_n, p.steps, l.pairs, 4 * a.tokens * a.hidden, a.dx_parts_bytes);
+    p.parts = a.dx_parts;
     p.tiles = p.tiles_m * p.tiles_n * p.split;
     if (!map_k(&p.a[0], a.dg, a.ffn, a.tokens, a.ffn) || !map_k(&p.a[1], a.du, a.ffn, a.tokens, a.ffn) ||
         !map_mn(&p.b[0], a.wg, a.hidden, a.ffn, a.hidden) || !map_mn(&p.b[1], a.wu, a.hidden, a.ffn, a.hidden) ||
@@ -554,20 +602,24 @@ cudaError_t launch_gated_back_tc(const GatedArgs& a, bool dx, bool dw, const TcL
     p.w_tiles_m = (int)ceil_div(a.ffn, 2 * kHalf), p.w_tiles_n = (int)ceil_div(a.hidden, 2 * kHalf);
     p.w_tiles = 2 * p.w_tiles_m * p.w_tiles_n;
     p.w_steps = (int)ceil_div(a.tokens, kStep);
+    p.w_split = split_of(p.w_tiles, p.w_steps, l.pairs, 8 * a.ffn * a.hidden, a.dw_parts_bytes);
+    p.w_parts = a.dw_parts;
+    p.w_tiles *= p.w_split;
     // what a tile of either takes: its stages, at least the six that writing
     // it takes, and about one for its way in and out
-    const int w_cost = (p.w_steps > 6 ? p.w_steps : 6) + 1;
+    const int w_part = p.w_steps / p.w_split, w_cost = (w_part > 6 ? w_part : 6) + 1;
     p.extra = ((dx ? p.steps / p.split : 0) + 1 + w_cost / 2) / w_cost;
     if (!map_mn(&p.wa[0], a.dg, a.ffn, a.tokens, a.ffn) || !map_mn(&p.wa[1], a.du, a.ffn, a.tokens, a.ffn) ||
         !map_mn(&p.wb, a.x, a.hidden, a.tokens, a.ldx) || !map_out(&p.out[1], a.dwg, a.hidden, a.ffn, a.hidden) ||
         !map_out(&p.out[2], a.dwu, a.hidden, a.ffn, a.hidden))
       return cudaErrorInvalidValue;
   }
-  const cudaError_t e = launch<kBack, 0>(p, l, stream);
-  if (e != cudaSuccess || p.split <= 1) return e;
-  const int64_t numel = a.tokens * a.hidden;
-  return launch_early(join_kernel, dim3((unsigned)ceil_div(numel / 8, kJoinThreads)), kJoinThreads, 0, 0, stream,
-                      (const float*)p.parts, p.split, a.dx, a.lddx, (uint32_t)(a.hidden / 8), (uint32_t)(numel / 8), numel);
+  cudaError_t e = launch<kBack, 0>(p, l, stream);
+  if (e == cudaSuccess && p.split > 1)
+    e = join(Join{p.parts, p.split, {a.dx, nullptr}, a.lddx, p.rows, p.cols}, 1, stream);
+  if (e == cudaSuccess && p.w_split > 1)
+    e = join(Join{p.w_parts, p.w_split, {a.dwg, a.dwu}, a.hidden, p.w_rows, p.cols}, 2, stream);
+  return e;
 }
 
 }  // namespace tide

@@ -206,7 +206,7 @@ def test_matmul_nan_stays_in_its_row_and_column(compute):
 # several tiles each way
 GATED_SHAPES = [(1, 256, 704), (1, 8, 8), (3, 1, 1), (5, 250, 130), (16, 128, 128), (17, 264, 136), (37, 2048, 768),
                 (129, 72, 1000), (250, 256, 704), (300, 1032, 264), (513, 512, 1408),
-                (300, 136, 2568), (20, 4104, 256), (50, 1000, 1400)]
+                (300, 136, 2568), (20, 4104, 256), (50, 1000, 1400), (60, 264, 4104), (3000, 72, 136)]
 
 
 def checkpoint(tokens, hidden, ffn, with_x):
