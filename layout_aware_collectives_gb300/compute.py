@@ -45,9 +45,10 @@ class Compute:
     def gated_backward(self, tokens: int, hidden: int, ffn: int, dh, x, w_gate, w_up, dx, dw_gate, dw_up, workspace,
                        activation: str = "silu", checkpoint: GatedCheckpoint | None = None, h=None,
                        workspace_bytes=None, ld_dh=None, ld_x=None, ld_dx=None, ld_h=None, stream=None):
+        """workspace_bytes: a tensor's own size where it is left out; to be
+        given with an address."""
         if workspace_bytes is None:
-            workspace_bytes = (workspace.numel() * workspace.element_size() if hasattr(workspace, "numel")
-                               else _t.gated_workspace_bytes(tokens, hidden, ffn))
+            workspace_bytes = workspace.numel() * workspace.element_size()
         _t.tide_gated_backward(self.handle, tokens, hidden, ffn, activation, dh, ffn if ld_dh is None else ld_dh, x,
                                hidden if ld_x is None else ld_x, w_gate, w_up, checkpoint, dx,
                                hidden if ld_dx is None else ld_dx, dw_gate, dw_up, h, ffn if ld_h is None else ld_h,

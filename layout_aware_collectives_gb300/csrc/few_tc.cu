@@ -27,13 +27,16 @@ constexpr uint32_t kRowBytes = 128;    // of either operand in one stage
 constexpr uint32_t kWeights = kRows * kRowBytes;
 constexpr int kThreads = 192;          // loads, MMAs, 4 warps for the sums
 
-// What is computed: h, dG and dU (and h), or the 8-bit product.
-enum Kind { kForward = 0, kGrad = 1, kFp8 = 2 };
+// What is computed: h, dG and dU (and h), the 8-bit product, or dX.  For dX
+// the rows are the hidden features, columns of Wg and Wu, which lie along
+// memory (MN-major), and the contraction runs over dG's features and then
+// dU's.
+enum Kind { kForward = 0, kGrad = 1, kFp8 = 2, kDx = 3 };
 
 template <int KIND, int NT>
 struct Shape {
   static constexpr bool FP8 = KIND == kFp8;
-  static constexpr int kParts = FP8 ? 1 : 2;  // weight tiles of a stage
+  static constexpr int kParts = KIND == kFp8 || KIND == kDx ? 1 : 2;  // weight tiles of a stage
   static constexpr uint32_t kStage = kParts * kWeights + NT * kRowBytes;
   static constexpr uint32_t kBudget = NT <= 32 ? 108 * 1024 : 200 * 1024;
   static constexpr int kStages = kBudget / kStage < 6 ? kBudget / kStage : 6;
@@ -44,8 +47,11 @@ struct Shape {
 };
 
 struct Params {
-  CUtensorMap w[2], x;
+  CUtensorMap w[2], x[2];
   int tokens, features, steps, step_elems;
+  int half_steps;  // dX: stages of dG's half
+  bool one_box;    // dX: a stage's weights are one box of two slabs
+  bool beside;     // dX: runs beside the kernel ahead of it
   // gated
   uint16_t* out;
   int64_t ldo;
@@ -115,7 +121,8 @@ template <int KIND, int NT, int ACT>
 __global__ void __launch_bounds__(kThreads) few_tc_kernel(const __grid_constant__ Params p) {
   using S = Shape<KIND, NT>;
   constexpr bool FP8 = S::FP8;
-  constexpr uint32_t kInstr = instr_desc(FP8 ? 0 : 1, 0, 0, kRows, NT);
+  constexpr bool kMn = KIND == kDx;
+  constexpr uint32_t kInstr = instr_desc(FP8 ? 0 : 1, kMn, 0, kRows, NT);
   extern __shared__ uint8_t raw[];
   __shared__ uint64_t bars[2 * S::kStages + 2 * S::kBufs + 1];
   __shared__ __align__(16) float scales[4][FP8 ? NT : 4];
@@ -141,15 +148,18 @@ __global__ void __launch_bounds__(kThreads) few_tc_kernel(const __grid_constant_
     for (int b = 0; b < S::kBufs; ++b) bar_init(sums_full(b), 1), bar_init(sums_empty(b), 4);
     bar_init(spare, 1);
     bar_init_fence();
-    for (int i = 0; i < S::kParts; ++i) prefetch_map(&p.w[i]);
-    prefetch_map(&p.x);
+    prefetch_map(&p.w[0]), prefetch_map(&p.x[0]);
   }
   if (warp == 1) tmem_alloc<1>(smem_addr(&tmem_at), S::kColumns);
   fence_before();
   __syncthreads();
   fence_after();
   const uint32_t tmem = tmem_at;
-  after_previous();
+  // Beside dW's kernel, which it does not depend on: this one begins once all
+  // of that one's CTAs are past their own wait, so what came before both has
+  // ended; it waits for that one's end at its own.
+  const bool beside = KIND == kDx && p.beside;
+  if (!beside) after_previous();
   bool done = false;  // this warp has its sums in shared memory
 
   if (p.stall_ns) {  // test: a wait on a barrier nothing arrives on runs out
@@ -166,9 +176,21 @@ __global__ void __launch_bounds__(kThreads) few_tc_kernel(const __grid_constant_
         }
         const uint32_t at = smem + s * S::kStage;
         bar_expect(full(s), S::kStage);
+        if constexpr (KIND == kDx) {
+          const int second = k >= p.half_steps, f = (k - (second ? p.half_steps : 0)) * p.step_elems;
+          if (p.one_box) {
+            load_box3<false>(at, &p.w[second], 0, f, feature0 / 64, full(s));
+          } else {
+            load_box<false>(at, &p.w[second], feature0, f, full(s));
+            load_box<false>(at + kWeights / 2, &p.w[second], feature0 + 64, f, full(s));
+          }
+          load_box<false>(at + kWeights, &p.x[second], f, token0, full(s));
+        } else {
 #pragma unroll
-        for (int i = 0; i < S::kParts; ++i) load_box<false>(at + i * kWeights, &p.w[i], k * p.step_elems, feature0, full(s));
-        load_box<false>(at + S::kParts * kWeights, &p.x, k * p.step_elems, token0, full(s));
+          for (int i = 0; i < S::kParts; ++i)
+            load_box<false>(at + i * kWeights, &p.w[i], k * p.step_elems, feature0, full(s));
+          load_box<false>(at + S::kParts * kWeights, &p.x[0], k * p.step_elems, token0, full(s));
+        }
       }
       if (!go) {  // copies in flight, with a limit again
         int never = 0;
@@ -194,8 +216,9 @@ __global__ void __launch_bounds__(kThreads) few_tc_kernel(const __grid_constant_
         for (int q = 0; q < 4; ++q)
 #pragma unroll
           for (int i = 0; i < S::kParts; ++i)
-            mma<1, FP8>(tmem + (b * S::kParts + i) * NT, operand_desc(at + i * kWeights, 16) + q * 2, dx + q * 2, kInstr,
-                        q > 0 || (!FP8 && j > 0));
+            mma<1, FP8>(tmem + (b * S::kParts + i) * NT,
+                        operand_desc(at + i * kWeights, kMn ? kWeights / 2 : 16) + q * ((kMn ? 2048 : 32) >> 4), dx + q * 2,
+                        kInstr, q > 0 || (!FP8 && j > 0));
         mma_commit<1>(empty(s));
         if (FP8 || k + 1 == k1) mma_commit<1>(sums_full(b));
       }
@@ -264,7 +287,7 @@ __global__ void __launch_bounds__(kThreads) few_tc_kernel(const __grid_constant_
       if (done) {
         fence_after();
 #pragma unroll 1
-        for (int c = 0; c < 2 * NT / kChunk; ++c) {
+        for (int c = 0; c < S::kParts * NT / kChunk; ++c) {
           uint32_t v[kChunk];
           if (k0 < k1)
             tmem_read(mine + c * kChunk, v);
@@ -344,6 +367,7 @@ __global__ void __launch_bounds__(kThreads) few_tc_kernel(const __grid_constant_
   }
   if (split > 1) cluster_sync();  // the others have read this CTA's sums
   if (warp == 1) tmem_free<1>(tmem, S::kColumns);
+  if (beside) after_previous();
 }
 
 // Clusters of `split` CTAs that the device holds at one time; a cluster lies
@@ -423,7 +447,7 @@ cudaError_t gated(Params& p, const GatedArgs& a, const TcLaunch& l, cudaStream_t
   p.out = a.h, p.ldo = a.ldh;
   if (!make_map(&p.w[0], a.wg, 2, a.hidden, a.ffn, a.hidden, kElems, kRows, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_map(&p.w[1], a.wu, 2, a.hidden, a.ffn, a.hidden, kElems, kRows, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !make_map(&p.x, a.x, 2, a.hidden, a.tokens, a.ldx, kElems, nt, CU_TENSOR_MAP_SWIZZLE_128B))
+      !make_map(&p.x[0], a.x, 2, a.hidden, a.tokens, a.ldx, kElems, nt, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   return a.act == TIDE_ACT_SILU ? launch_tile<KIND, TIDE_ACT_SILU>(p, nt, l, stream)
                                 : launch_tile<KIND, TIDE_ACT_GELU>(p, nt, l, stream);
@@ -437,6 +461,17 @@ cudaError_t gated(Params& p, const GatedArgs& a, const TcLaunch& l, cudaStream_t
 // against 11.7), for the 8-bit product from two thirds (128 x 28672 x 8192,
 // 128 tiles: 76 us against 87; 1021 x 2048 x 768: 9.6 against 9.1).
 bool gated_few_takes(const GatedArgs& a, int sms) { return few(a.tokens, a.ffn, sms / 2); }
+// dX up to 64 tokens (1 x 4096 x 14336: 33 us against 54 in 256-row tiles),
+// and for more where it has few tiles and dW's leave SMs for it (190 x 240 x
+// 8032, backward: 28.8 us against 32.1; 500 x 1024 x 1024, 64 tiles: 26.1
+// against 23.1).  Below 48 stages the launch that dX then has to itself costs
+// the host more than it saves (2 x 5792 x 160: 8.7 us, but 3 more to enqueue).
+bool gated_dx_few_takes(const GatedArgs& a, int pairs) {
+  if (2 * ceil_div(a.ffn, kRowBytes / 2) < 48) return false;
+  if (a.tokens <= 64) return few(a.tokens, a.hidden, 0);
+  return a.tokens <= 512 && few(a.tokens, a.hidden, 32) && 2 * ceil_div(a.ffn, 256) * ceil_div(a.hidden, 256) <= pairs;
+}
+
 bool fp8_few_takes(const MatmulArgs& a, int sms) { return few(a.m, a.n, 2 * sms / 3); }
 
 cudaError_t launch_gated_forward_few(const GatedArgs& a, const TcLaunch& l, cudaStream_t stream) {
@@ -451,6 +486,24 @@ cudaError_t launch_gated_grad_few(const GatedArgs& a, const TcLaunch& l, cudaStr
   return gated<kGrad>(p, a, l, stream);
 }
 
+cudaError_t launch_gated_dx_few(const GatedArgs& a, bool beside, const TcLaunch& l, cudaStream_t stream) {
+  constexpr int kElems = kRowBytes / 2;
+  const int nt = tile_of(a.tokens);
+  const uint16_t *w[2] = {a.wg, a.wu}, *d[2] = {a.dg, a.du};
+  Params p{};
+  p.tokens = (int)a.tokens, p.features = (int)a.hidden;
+  p.half_steps = (int)ceil_div(a.ffn, kElems), p.steps = 2 * p.half_steps, p.step_elems = kElems;
+  p.one_box = a.hidden % 64 == 0;
+  p.out = a.dx, p.ldo = a.lddx;
+  p.beside = beside;
+  for (int i = 0; i < 2; ++i)
+    if (!(p.one_box ? make_slab_map(&p.w[i], w[i], a.hidden, a.ffn, a.hidden, kElems)
+                    : make_map(&p.w[i], w[i], 2, a.hidden, a.ffn, a.hidden, 64, kElems, CU_TENSOR_MAP_SWIZZLE_128B)) ||
+        !make_map(&p.x[i], d[i], 2, a.ffn, a.tokens, a.ffn, kElems, nt, CU_TENSOR_MAP_SWIZZLE_128B))
+      return cudaErrorInvalidValue;
+  return launch_tile<kDx>(p, nt, l, stream);
+}
+
 cudaError_t launch_fp8_matmul_few(const MatmulArgs& a, const TcLaunch& l, cudaStream_t stream) {
   const int nt = tile_of(a.m);
   Params p{};
@@ -459,7 +512,7 @@ cudaError_t launch_fp8_matmul_few(const MatmulArgs& a, const TcLaunch& l, cudaSt
   p.out = a.out, p.ldo = a.ldo;
   p.sx = a.sa, p.sw = a.sb, p.any_scales = a.any_scales;
   if (!make_map(&p.w[0], a.b, 1, a.k, a.n, a.k, kRowBytes, kRows, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !make_map(&p.x, a.a, 1, a.k, a.m, a.k, kRowBytes, nt, CU_TENSOR_MAP_SWIZZLE_128B))
+      !make_map(&p.x[0], a.a, 1, a.k, a.m, a.k, kRowBytes, nt, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   return launch_tile<kFp8>(p, nt, l, stream);
 }

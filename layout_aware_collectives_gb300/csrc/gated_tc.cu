@@ -93,7 +93,7 @@ __device__ __forceinline__ void put_codes(uint8_t* dst, const uint32_t (&v)[32],
 // 128 columns x 64 of the contraction: a box of both halves, or one each.
 __device__ __forceinline__ void load_mn(uint32_t dst, const CUtensorMap* m, int col, int k0, uint32_t bar, bool one) {
   if (one) {
-    load_box3(dst, m, 0, k0, col / 64, bar);
+    load_box3<true>(dst, m, 0, k0, col / 64, bar);
   } else {
     load_box<true>(dst, m, col, k0, bar);
     load_box<true>(dst + kOperand / 2, m, col + 64, k0, bar);
@@ -581,7 +581,8 @@ cudaError_t launch_gated_grad_tc(const GatedArgs& a, const TcLaunch& l, cudaStre
   return a.act == TIDE_ACT_SILU ? launch<kGrad, TIDE_ACT_SILU>(p, l, stream) : launch<kGrad, TIDE_ACT_GELU>(p, l, stream);
 }
 
-cudaError_t launch_gated_back_tc(const GatedArgs& a, bool dx, bool dw, const TcLaunch& l, cudaStream_t stream) {
+cudaError_t launch_gated_back_tc(const GatedArgs& a, bool dx, bool dw, bool dx_beside, const TcLaunch& l,
+                                 cudaStream_t stream) {
   Params p{};
   p.cols = (int)a.hidden;
   p.one_a = a.ffn % 64 == 0, p.one_b = a.hidden % 64 == 0;
@@ -615,6 +616,7 @@ cudaError_t launch_gated_back_tc(const GatedArgs& a, bool dx, bool dw, const TcL
       return cudaErrorInvalidValue;
   }
   cudaError_t e = launch<kBack, 0>(p, l, stream);
+  if (e == cudaSuccess && dx_beside) e = launch_gated_dx_few(a, true, l, stream);
   if (e == cudaSuccess && p.split > 1)
     e = join(Join{p.parts, p.split, {a.dx, nullptr}, a.lddx, p.rows, p.cols}, 1, stream);
   if (e == cudaSuccess && p.w_split > 1)

@@ -114,13 +114,21 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* m, int
         "l"(m), "r"(x), "r"(y), "r"(bar)
         : "memory");
 }
-// The same of a 3-D tensor, by a pair.
+// The same of a 3-D tensor.
+template <bool PAIR>
 __device__ __forceinline__ void load_box3(uint32_t dst, const CUtensorMap* m, int x, int y, int z, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
-      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(m), "r"(x), "r"(y), "r"(z), "r"(bar)
-      : "memory");
+  if constexpr (PAIR)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(m), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(m), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
 }
 // A box of shared memory to a 2-D tensor, clipped at its end.
 __device__ __forceinline__ void store_box(const CUtensorMap* m, int x, int y, uint32_t src) {

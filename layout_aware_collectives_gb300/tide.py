@@ -130,7 +130,7 @@ def _addr(x) -> int:
         return 0
     if isinstance(x, int):
         return x
-    return int(x.data_ptr())
+    return x.data_ptr()
 
 
 def _stream(s) -> int:
@@ -138,7 +138,7 @@ def _stream(s) -> int:
         return 0
     if isinstance(s, int):
         return s
-    return int(s.cuda_stream)
+    return s.cuda_stream
 
 
 class PointerTable:
