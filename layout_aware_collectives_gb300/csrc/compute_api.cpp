@@ -19,6 +19,10 @@ constexpr int64_t kMaxNumel = (int64_t)1 << 38;
     if (s_ != TIDE_OK) return s_;       \
   } while (0)
 
+// No exception (of a message's or a lock's making) leaves a C entry.
+#define TIDE_CATCH \
+  catch (...) { return TIDE_ERR_OUT_OF_MEMORY; }
+
 tide_status_t invalid(const std::string& msg) { return set_error(TIDE_ERR_INVALID_ARG, msg); }
 
 tide_status_t check_dims(int64_t a, int64_t b, const char* what) {
@@ -75,11 +79,13 @@ tide_status_t bind(tide_compute_s* c, cudaStream_t stream) {
                      "the handle's first call sets it up on the device and cannot be captured; make one call before");
   e = cudaDeviceGetAttribute(&c->num_sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute(MultiProcessorCount)");
-  c->pairs = gated_tc_pairs();
-  if (c->pairs < 1) {
-    cudaGetLastError();
-    return set_error(TIDE_ERR_CUDA, "the device holds no pair of tensor-core CTAs");
-  }
+  static std::mutex once;  // the set-up's results are shared by all handles
+  std::lock_guard<std::mutex> o(once);
+  e = gated_tc_prepare(&c->pairs);
+  if (e == cudaSuccess) e = fp8_tc_prepare();
+  if (e == cudaSuccess) e = few_tc_prepare();
+  if (e != cudaSuccess) return cuda_fail(e, "set-up of the tensor-core kernels");
+  if (c->pairs < 1) return set_error(TIDE_ERR_CUDA, "the device holds no pair of tensor-core CTAs");
   if (!c->err) {
     e = cudaHostAlloc((void**)&c->err, sizeof(int), cudaHostAllocMapped);
     if (e != cudaSuccess) return cuda_fail(e, "cudaHostAlloc(error word)");
@@ -135,11 +141,12 @@ Workspace workspace_of(int64_t tokens, int64_t hidden, int64_t ffn) {
 
 extern "C" {
 
-tide_status_t tide_compute_create(tide_compute_t* out) {
+tide_status_t tide_compute_create(tide_compute_t* out) try {
   if (!out) return invalid("out is NULL");
   *out = new (std::nothrow) tide_compute_s();
   return *out ? TIDE_OK : set_error(TIDE_ERR_OUT_OF_MEMORY, "host allocation failed");
 }
+TIDE_CATCH
 
 void tide_compute_destroy(tide_compute_t c) {
   if (!c) return;
@@ -147,7 +154,7 @@ void tide_compute_destroy(tide_compute_t c) {
   delete c;
 }
 
-tide_status_t tide_compute_check_device(tide_compute_t c) {
+tide_status_t tide_compute_check_device(tide_compute_t c) try {
   if (!c) return invalid("compute is NULL");
   std::lock_guard<std::mutex> g(c->mu);
   if (c->device < 0) return TIDE_OK;  // nothing launched yet
@@ -158,16 +165,18 @@ tide_status_t tide_compute_check_device(tide_compute_t c) {
   *err = 0;
   return set_error(TIDE_ERR_TIMEOUT, "a bounded wait in a tensor-core kernel ran out; its outputs are incomplete");
 }
+TIDE_CATCH
 
-tide_status_t tide_compute_set_test_stall(tide_compute_t c, int64_t ns) {
+tide_status_t tide_compute_set_test_stall(tide_compute_t c, int64_t ns) try {
   if (!c || ns < 0) return invalid("NULL handle or negative time");
   std::lock_guard<std::mutex> g(c->mu);
   c->test_stall_ns = ns;
   return TIDE_OK;
 }
+TIDE_CATCH
 
 tide_status_t tide_fp8_store(tide_compute_t c, int64_t rows, int64_t cols, const uint16_t* src, int64_t ld_src,
-                             uint8_t* codes, float* scales, int32_t block_rows, cudaStream_t stream) {
+                             uint8_t* codes, float* scales, int32_t block_rows, cudaStream_t stream) try {
   if (!c) return invalid("compute is NULL");
   if (block_rows != 1 && block_rows != kBlock) return invalid("block_rows must be 1 or 128");
   TIDE_TRY(check_dims(rows, cols, "tide_fp8_store"));
@@ -178,10 +187,11 @@ tide_status_t tide_fp8_store(tide_compute_t c, int64_t rows, int64_t cols, const
   const Fp8Args a{rows, cols, ld_src, const_cast<uint16_t*>(src), codes, scales, block_rows};
   return launched(launch_fp8_store(a, stream), "tide_fp8_store");
 }
+TIDE_CATCH
 
 tide_status_t tide_fp8_restore(tide_compute_t c, int64_t rows, int64_t cols, const uint8_t* codes,
                                const float* scales, int32_t block_rows, uint16_t* dst, int64_t ld_dst,
-                               cudaStream_t stream) {
+                               cudaStream_t stream) try {
   if (!c) return invalid("compute is NULL");
   if (block_rows != 1 && block_rows != kBlock) return invalid("block_rows must be 1 or 128");
   TIDE_TRY(check_dims(rows, cols, "tide_fp8_restore"));
@@ -193,10 +203,11 @@ tide_status_t tide_fp8_restore(tide_compute_t c, int64_t rows, int64_t cols, con
                   block_rows};
   return launched(launch_fp8_restore(a, stream), "tide_fp8_restore");
 }
+TIDE_CATCH
 
 tide_status_t tide_fp8_matmul(tide_compute_t c, int64_t m, int64_t n, int64_t k, const uint8_t* a,
                               const float* a_scales, const uint8_t* b, const float* b_scales, int32_t any_scales,
-                              uint16_t* out, int64_t ld_out, cudaStream_t stream) {
+                              uint16_t* out, int64_t ld_out, cudaStream_t stream) try {
   if (!c) return invalid("compute is NULL");
   TIDE_TRY(check_dims(m, k, "tide_fp8_matmul"));
   TIDE_TRY(check_dims(n, k, "tide_fp8_matmul"));
@@ -217,10 +228,11 @@ tide_status_t tide_fp8_matmul(tide_compute_t c, int64_t m, int64_t n, int64_t k,
   }
   return launched(launch_fp8_matmul_simple(args, stream), "tide_fp8_matmul");
 }
+TIDE_CATCH
 
 tide_status_t tide_gated_forward(tide_compute_t c, int64_t tokens, int64_t hidden, int64_t ffn, tide_activation_t act,
                                  const uint16_t* x, int64_t ld_x, const uint16_t* w_gate, const uint16_t* w_up,
-                                 uint16_t* h, int64_t ld_h, const tide_gated_checkpoint_t* ck, cudaStream_t stream) {
+                                 uint16_t* h, int64_t ld_h, const tide_gated_checkpoint_t* ck, cudaStream_t stream) try {
   if (!c) return invalid("compute is NULL");
   GatedArgs a{};
   a.tokens = tokens, a.hidden = hidden, a.ffn = ffn, a.act = act;
@@ -247,8 +259,9 @@ tide_status_t tide_gated_forward(tide_compute_t c, int64_t tokens, int64_t hidde
   }
   return launched(launch_gated_forward_simple(a, stream), "tide_gated_forward");
 }
+TIDE_CATCH
 
-tide_status_t tide_gated_workspace(int64_t tokens, int64_t hidden, int64_t ffn, int64_t* bytes) {
+tide_status_t tide_gated_workspace(int64_t tokens, int64_t hidden, int64_t ffn, int64_t* bytes) try {
   if (!bytes) return invalid("bytes is NULL");
   *bytes = 0;
   TIDE_TRY(check_dims(tokens, hidden, "tide_gated_workspace"));
@@ -257,13 +270,14 @@ tide_status_t tide_gated_workspace(int64_t tokens, int64_t hidden, int64_t ffn, 
   *bytes = workspace_of(tokens, hidden, ffn).bytes;
   return TIDE_OK;
 }
+TIDE_CATCH
 
 tide_status_t tide_gated_backward(tide_compute_t c, int64_t tokens, int64_t hidden, int64_t ffn,
                                   tide_activation_t act, const uint16_t* dh, int64_t ld_dh, const uint16_t* x,
                                   int64_t ld_x, const uint16_t* w_gate, const uint16_t* w_up,
                                   const tide_gated_checkpoint_t* ck, uint16_t* dx, int64_t ld_dx, uint16_t* dw_gate,
                                   uint16_t* dw_up, uint16_t* h, int64_t ld_h, void* workspace,
-                                  int64_t workspace_bytes, cudaStream_t stream) {
+                                  int64_t workspace_bytes, cudaStream_t stream) try {
   const char* what = "tide_gated_backward";
   if (!c) return invalid("compute is NULL");
   GatedArgs a{};
@@ -327,5 +341,6 @@ tide_status_t tide_gated_backward(tide_compute_t c, int64_t tokens, int64_t hidd
   if (dw_gate && !dw_tc) TIDE_TRY(launched(launch_gated_dw_simple(a, stream), what));
   return TIDE_OK;
 }
+TIDE_CATCH
 
 }  // extern "C"

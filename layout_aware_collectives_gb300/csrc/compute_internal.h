@@ -112,7 +112,11 @@ struct TcLaunch {
 
 // Tensor-core kernels of the gated block (gated_tc.cu).  They take matrices
 // whose rows start on 16 bytes.
-int gated_tc_pairs();
+// prepare: sets a file's kernels up on the current device (shared-memory
+// limits, what the device holds at one time); once for each handle.
+cudaError_t gated_tc_prepare(int* pairs);
+cudaError_t fp8_tc_prepare();
+cudaError_t few_tc_prepare();
 bool gated_tc_takes(const GatedArgs& a);
 // Workspace for the parts of dX's and dW's sums.
 int64_t gated_dx_parts_bytes(int64_t tokens, int64_t hidden);

@@ -370,26 +370,40 @@ __global__ void __launch_bounds__(kThreads) few_tc_kernel(const __grid_constant_
   if (beside) after_previous();
 }
 
-// Clusters of `split` CTAs that the device holds at one time; a cluster lies
-// within one GPC, so these are fewer than SMs / split.
+// One kernel's shape for the launches: set up once for each device.
 template <int KIND, int NT, int ACT>
-int clusters_of(int split) {
+struct Held {
+  // clusters of 2, 4 and 8 CTAs that the device holds at one time; a cluster
+  // lies within one GPC, so these are fewer than SMs by their size
+  static int clusters[3];
+};
+template <int KIND, int NT, int ACT>
+int Held<KIND, NT, ACT>::clusters[3] = {0, 0, 0};
+
+template <int KIND, int NT, int ACT>
+cudaError_t prepare() {
   using S = Shape<KIND, NT>;
-  cudaLaunchAttribute cluster;
-  cluster.id = cudaLaunchAttributeClusterDimension;
-  cluster.val.clusterDim = {(unsigned)split, 1, 1};
-  cudaLaunchConfig_t c{};
-  c.gridDim = dim3(split);
-  c.blockDim = dim3(kThreads);
-  c.dynamicSmemBytes = S::kSmem;
-  c.attrs = &cluster;
-  c.numAttrs = 1;
-  int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, few_tc_kernel<KIND, NT, ACT>, &c) != cudaSuccess) {
-    cudaGetLastError();
-    return 0;
+  cudaError_t e = cudaFuncSetAttribute(few_tc_kernel<KIND, NT, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
+  for (int i = 0; i < 3 && e == cudaSuccess; ++i) {
+    cudaLaunchAttribute cluster;
+    cluster.id = cudaLaunchAttributeClusterDimension;
+    cluster.val.clusterDim = {2u << i, 1, 1};
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3(2u << i);
+    c.blockDim = dim3(kThreads);
+    c.dynamicSmemBytes = S::kSmem;
+    c.attrs = &cluster;
+    c.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&Held<KIND, NT, ACT>::clusters[i], few_tc_kernel<KIND, NT, ACT>, &c);
   }
-  return n;
+  return e;
+}
+
+template <int KIND, int ACT = 0>
+cudaError_t prepare_tiles() {
+  cudaError_t e = prepare<KIND, 16, ACT>();
+  if (e == cudaSuccess) e = prepare<KIND, 32, ACT>();
+  return e == cudaSuccess ? prepare<KIND, 64, ACT>() : e;
 }
 
 // CTAs that share a tile's contraction: up to one for each SM, all at work at
@@ -400,7 +414,7 @@ int clusters_of(int split) {
 // clusters wait for the first.)
 template <int KIND, int NT, int ACT>
 int split_of(int64_t tiles, int64_t steps, int sms) {
-  static const int held[3] = {clusters_of<KIND, NT, ACT>(2), clusters_of<KIND, NT, ACT>(4), clusters_of<KIND, NT, ACT>(8)};
+  const int* held = Held<KIND, NT, ACT>::clusters;
   int s = 1;
   for (int i = 0; i < 3 && 2 * s * tiles <= sms && tiles <= held[i] && steps >= 8 * s; ++i) s *= 2;
   return s;
@@ -409,9 +423,6 @@ int split_of(int64_t tiles, int64_t steps, int sms) {
 template <int KIND, int NT, int ACT>
 cudaError_t launch(Params& p, const TcLaunch& l, cudaStream_t stream) {
   using S = Shape<KIND, NT>;
-  static const cudaError_t ready =
-      cudaFuncSetAttribute(few_tc_kernel<KIND, NT, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
-  if (ready != cudaSuccess) return ready;
   p.err = l.err;
   p.limit_ns = TIDE_BULK_TIMEOUT_NS;
   p.stall_ns = l.stall_ns;
@@ -454,6 +465,17 @@ cudaError_t gated(Params& p, const GatedArgs& a, const TcLaunch& l, cudaStream_t
 }
 
 }  // namespace
+
+cudaError_t few_tc_prepare() {
+  cudaError_t (*const all[])() = {prepare_tiles<kForward, TIDE_ACT_SILU>, prepare_tiles<kForward, TIDE_ACT_GELU>,
+                                  prepare_tiles<kGrad, TIDE_ACT_SILU>,    prepare_tiles<kGrad, TIDE_ACT_GELU>,
+                                  prepare_tiles<kFp8>,                    prepare_tiles<kDx>};
+  for (auto p : all) {
+    const cudaError_t e = p();
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
 
 // Past 64 tokens the 256-row tiles read fewer operand bytes: they are ahead
 // for the gated block from about half as many of these tiles as SMs (1021 x

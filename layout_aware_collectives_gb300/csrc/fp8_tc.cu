@@ -431,11 +431,13 @@ __global__ void __cluster_dims__(2, 1, 1)
 
 }  // namespace
 
+cudaError_t fp8_tc_prepare() {
+  const cudaError_t e = cudaFuncSetAttribute(summed_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(scaled_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kScaledSmem);
+}
+
 cudaError_t launch_fp8_matmul_tc(const MatmulArgs& a, const TcLaunch& l, cudaStream_t stream) {
-  static const cudaError_t ready[2] = {
-      cudaFuncSetAttribute(summed_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem),
-      cudaFuncSetAttribute(scaled_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kScaledSmem)};
-  if (ready[0] != cudaSuccess || ready[1] != cudaSuccess) return ready[ready[0] == cudaSuccess];
   Params p{};
   p.sa = a.sa, p.sb = a.sb;
   p.rows = (int)a.m, p.cols = (int)a.n;

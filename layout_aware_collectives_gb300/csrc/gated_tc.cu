@@ -481,9 +481,6 @@ cudaError_t join(const Join& a, int outputs, cudaStream_t stream) {
 
 template <int FORM, int ACT>
 cudaError_t launch(Params& p, const TcLaunch& l, cudaStream_t stream) {
-  static const cudaError_t ready =
-      cudaFuncSetAttribute(gated_tc_kernel<FORM, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
-  if (ready != cudaSuccess) return ready;
   p.err = l.err;
   p.limit_ns = TIDE_BULK_TIMEOUT_NS;
   p.stall_ns = l.stall_ns;
@@ -541,17 +538,21 @@ int64_t parts_bytes(int64_t tiles, int64_t part_bytes) { return tiles ? 76 / til
 
 }  // namespace
 
-int gated_tc_pairs() {
+cudaError_t gated_tc_prepare(int* pairs) {
+  void (*const kernels[])(Params) = {gated_tc_kernel<kForward, TIDE_ACT_SILU>, gated_tc_kernel<kForward, TIDE_ACT_GELU>,
+                                     gated_tc_kernel<kGrad, TIDE_ACT_SILU>, gated_tc_kernel<kGrad, TIDE_ACT_GELU>,
+                                     gated_tc_kernel<kBack, 0>};
+  for (auto k : kernels) {
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    if (e != cudaSuccess) return e;
+  }
   // The clusters the device holds at one time: a GPC with an odd number of
   // SMs leaves one without a partner.
-  cudaFuncSetAttribute(gated_tc_kernel<kBack, 0>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   cudaLaunchConfig_t c{};
   c.gridDim = dim3(2);
   c.blockDim = dim3(kThreads);
   c.dynamicSmemBytes = kSmem;
-  int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, gated_tc_kernel<kBack, 0>, &c) != cudaSuccess) return 0;
-  return n;
+  return cudaOccupancyMaxActiveClusters(pairs, gated_tc_kernel<kBack, 0>, &c);
 }
 
 int64_t gated_dx_parts_bytes(int64_t tokens, int64_t hidden) {

@@ -396,9 +396,10 @@ def test_saturated_gates(compute, value, kind):
         close(a, b, e)
 
 
-def test_streams_and_capture(compute):
+# merged dX and dW; dX beside dW; sums in parts; 256-row tiles throughout
+@pytest.mark.parametrize("tokens,hidden,ffn", [(64, 256, 704), (40, 264, 2056), (700, 264, 2056), (300, 136, 2568)])
+def test_streams_and_capture(compute, tokens, hidden, ffn):
     """Calls follow their own stream, and replay from a CUDA graph."""
-    tokens, hidden, ffn = 64, 256, 704
     g = gen(4)
     (wg, wu), dh = weights(g, hidden, ffn), randn(g, tokens, ffn)
     x = torch.zeros(tokens, hidden, dtype=torch.bfloat16, device="cuda")
