@@ -130,7 +130,7 @@ def test_restore(compute, rows, cols, block_rows, pad):
 
 MATMUL_SHAPES = [(1, 128, 128), (1, 8, 16), (2, 264, 400), (3, 1, 1), (7, 130, 129), (37, 768, 2048), (129, 264, 1040),
                  (250, 704, 256), (300, 520, 144), (33, 100, 300), (513, 1024, 4096),
-                 (300, 5000, 272), (64, 136, 8192), (70, 1160, 1296)]
+                 (300, 5000, 272), (64, 136, 8192), (70, 1160, 1296), (300, 5200, 400), (1000, 4864, 160)]
 
 
 def fp8(g, rows, cols, block_rows, any_scales=False):
