@@ -154,7 +154,7 @@ __device__ __forceinline__ bool work_at(const Params& p, int pair, int pairs, in
 
 template <int FORM, int ACT>
 __device__ __forceinline__ void epilogue(const Params& p, const Work& work, uint32_t tmem, int row0, int half,
-                                         uint32_t* maxima, Outbox<kBoxes>& out) {
+                                         uint32_t* maxima, const uint4 (&dh)[8], Outbox<kBoxes>& out) {
   const TileAt& t = work.at;
   const int row = row0 + out.lane, rows = work.w ? p.w_rows : p.rows;
   const bool any = row0 < rows, mine = row < rows;
@@ -214,9 +214,9 @@ __device__ __forceinline__ void epilogue(const Params& p, const Work& work, uint
         }
       }
     }
-#pragma unroll 1
-    for (int c = 2 * half; c < 2 * half + 2; ++c) {
-      const int col = col0 + c * 32;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int c = 2 * half + h, col = col0 + c * 32;
       if (!any || col >= p.cols) break;
       uint32_t o[16];
       if constexpr (FORM == kForward) {
@@ -235,14 +235,9 @@ __device__ __forceinline__ void epilogue(const Params& p, const Work& work, uint
         uint32_t o1[16], o2[16];
 #pragma unroll
         for (int q = 0; q < 2; ++q) {  // 16 columns at a time, for the registers
-          uint32_t g[16], u[16], w[8];
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            uint4 d = make_uint4(0, 0, 0, 0);
-            if (mine && col + 16 * q + 8 * j < p.cols)
-              d = __ldcs((const uint4*)(p.dh + row * p.lddh + col + 16 * q + 8 * j));
-            w[4 * j] = d.x, w[4 * j + 1] = d.y, w[4 * j + 2] = d.z, w[4 * j + 3] = d.w;
-          }
+          uint32_t g[16], u[16];
+          const uint4 d0 = dh[4 * h + 2 * q], d1 = dh[4 * h + 2 * q + 1];
+          const uint32_t w[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
           tmem_read(tmem + c * 32 + 16 * q, g);
           tmem_read(tmem + kHalf + c * 32 + 16 * q, u);
 #pragma unroll
@@ -256,8 +251,7 @@ __device__ __forceinline__ void epilogue(const Params& p, const Work& work, uint
             o2[i] = pack_bf16(t0.x * u0, t1.x * u1);
           }
         }
-        out.put(&p.out[0], o, col, row0);
-        out.put(&p.out[1], o1, col, row0);
+        out.put2(&p.out[0], o, &p.out[1], o1, col, row0);
         if (p.with_h) out.put(&p.out[2], o2, col, row0);
       }
     }
@@ -412,10 +406,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gated_t
     Work work;
     for (int i = 0; work_at<FORM>(p, pair, pairs, i, work); ++i) {
       const int b = i & 1;
+      uint4 dh[8];
+      if constexpr (FORM == kGrad) {  // 64 columns of dh on their way while the sums are not there yet
+        const int row = (work.at.m * 2 + rank) * kHalf + (warp & 3) * 32 + lane;
+        const int col = work.at.n * kHalf + ((warp - 4) >> 2) * 64;
+        const uint4* from = (const uint4*)(p.dh + row * p.lddh + col);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          dh[j] = row < p.rows && col + 8 * j < p.cols ? __ldcs(from + j) : make_uint4(0, 0, 0, 0);
+      }
       if (!bar_wait_warp(sums_full(b), (i / 2) & 1, watch)) break;
       fence_after();
       const uint32_t lanes = (uint32_t)(warp & 3) * 32;
-      epilogue<FORM, ACT>(p, work, tmem + (lanes << 16) + b * 256, (work.at.m * 2 + rank) * kHalf + lanes, (warp - 4) >> 2, maxima, out);
+      epilogue<FORM, ACT>(p, work, tmem + (lanes << 16) + b * 256, (work.at.m * 2 + rank) * kHalf + lanes, (warp - 4) >> 2, maxima, dh, out);
       fence_before();
       __syncwarp();
       if (lane == 0) bar_arrive_peer(peer_addr(sums_empty(b), 0));

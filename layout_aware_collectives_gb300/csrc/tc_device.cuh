@@ -325,22 +325,36 @@ struct Outbox {
   int next;
   int lane;
 
-  __device__ __forceinline__ void put(const CUtensorMap* map, const uint32_t (&p)[16], int col, int row) {
-    if (lane == 0) stores_read<BOXES - 1>();
-    __syncwarp();
+  // 64-byte swizzle: 16-byte piece c of row r lies at piece c ^ (r / 2 % 4)
+  __device__ __forceinline__ uint32_t fill(const uint32_t (&p)[16]) {
     const uint32_t box = base + (uint32_t)(next % BOXES) * kBox;
     ++next;
-    // 64-byte swizzle: 16-byte piece c of row r lies at piece c ^ (r / 2 % 4)
-    uint32_t row_at = box + lane * 64, turn = (lane >> 1) & 3;
-    asm volatile("" : "+r"(row_at), "+r"(turn));  // computed here: kept across the main loop they cost registers
+    const uint32_t row_at = box + lane * 64, turn = (lane >> 1) & 3;
 #pragma unroll
     for (uint32_t c = 0; c < 4; ++c)
       asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row_at + ((c ^ turn) << 4)), "r"(p[4 * c]),
                    "r"(p[4 * c + 1]), "r"(p[4 * c + 2]), "r"(p[4 * c + 3])
                    : "memory");
+    return box;
+  }
+
+  __device__ __forceinline__ void put(const CUtensorMap* map, const uint32_t (&p)[16], int col, int row) {
+    if (lane == 0) stores_read<BOXES - 1>();
+    __syncwarp();
+    const uint32_t box = fill(p);
     async_fence();
     __syncwarp();
     if (lane == 0) store_box(map, col, row, box);
+  }
+  // Two at once, behind one fence.
+  __device__ __forceinline__ void put2(const CUtensorMap* map0, const uint32_t (&p0)[16], const CUtensorMap* map1,
+                                       const uint32_t (&p1)[16], int col, int row) {
+    if (lane == 0) stores_read<BOXES - 2>();
+    __syncwarp();
+    const uint32_t box0 = fill(p0), box1 = fill(p1);
+    async_fence();
+    __syncwarp();
+    if (lane == 0) store_box(map0, col, row, box0), store_box(map1, col, row, box1);
   }
 };
 
