@@ -1,18 +1,22 @@
-// The gated block and the 8-bit product for few tokens (one to a few
-// hundred), where the weights' bytes are what counts.
+// The gated block, forward and backward, and the 8-bit product for few tokens
+// (one to a few hundred), where the weights' bytes are what counts.
 //
 // The tiles of gated_tc.cu and fp8_tc.cu put 256 tokens on the tensor cores'
 // rows; with few tokens most of those are padding and few tiles are left to
 // share out.  Here the weights take the rows: a CTA multiplies 128 of them
-// (for the gated block 128 of Wg and the same 128 of Wu) by NT = 16 to 128
+// (for the gated block 128 of Wg and the same 128 of Wu) by NT = 16 to 64
 // tokens, and a cluster of up to 8 CTAs splits the contraction.  Each CTA
 // leaves its sums in its shared memory, [token][feature] in fp32; then every
 // CTA of the cluster finishes its share of the tokens, adding the others'
 // sums over distributed shared memory in the order of their ranks, so the
 // result does not depend on timing.
 //
-// Bound by HBM: the weights stream through a ring of 3-5 stages of 18-48 KiB,
-// with two CTAs to an SM up to 32 tokens.
+// Bound by HBM: the weights stream through a ring of 3-6 stages of 18-40 KiB,
+// with room for two CTAs to an SM up to 32 tokens.  One token: 4096 x 14336
+// gate and up 40 us (5.8 TB/s; once they flow the rest is the ramp), their dX
+// 33 us, an 8192 x 28672 8-bit product 45 us (5.2 TB/s).  Small blocks take
+// 4-7 us of waits one after the other: the first stage's 0.6 us, 0.3 us a
+// stage, the clusters' meetings 0.7 us each.
 #include "compute_device.cuh"
 #include "tc_device.cuh"
 #include "tc_host.h"
