@@ -501,6 +501,8 @@ TIDE_API tide_status_t tide_layout_check_tiles(tide_layout_t layout, tide_op_t o
  *    word.  Its first call binds it to the current device and cannot be
  *    captured into a CUDA graph; later calls can.
  *  - Results do not depend on timing: no call sums in an order that changes.
+ *  - A call that takes several kernels and whose later launch fails reports
+ *    it with the earlier ones enqueued; its outputs are then incomplete.
  */
 typedef struct tide_compute_s* tide_compute_t;
 

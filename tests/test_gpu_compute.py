@@ -523,3 +523,98 @@ def test_feed_forward_unit_learns():
         # e4m3 rounds each of g, u, x, h and the down weights by up to 2^-4:
         # as independent errors (rms 2^-5.6 each) well under a fifth in norm
         assert float((got - want).norm() / want.norm()) < 0.2
+
+
+# ------------------------------------------------- offsets past 32 bits
+
+def pick8(codes, rows):
+    return codes.view(torch.uint8)[rows].view(torch.float8_e4m3fn)
+
+
+@pytest.mark.parametrize("rows", [70001, 100003])  # past 2^31 elements; past 3 * 2^30
+@pytest.mark.parametrize("cols", [32776, 32777])
+def test_blocks_past_32_bits(compute, rows, cols):
+    src = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda")
+    g = gen(rows + cols)
+    picks = [0, 2 ** 31 // cols // 128 * 128, rows // 128 * 128 - 128]
+    src.zero_()
+    for r in picks:
+        src[r:r + 128] = randn(g, 128, cols)
+    for block_rows in (1, 128):
+        codes = torch.empty(rows, cols, dtype=torch.float8_e4m3fn, device="cuda")
+        scales = torch.empty(-(-rows // block_rows), -(-cols // 128), device="cuda")
+        back = torch.empty_like(src)
+        compute.fp8_store(rows, cols, src, codes, scales, block_rows=block_rows)
+        compute.fp8_restore(rows, cols, codes, scales, back, block_rows=block_rows)
+        for r in picks:
+            v = src[r:r + 128].float()
+            j = torch.arange(cols, device="cuda") // 128
+            top = torch.zeros(128 // block_rows, scales.shape[1], device="cuda")
+            i = torch.arange(128, device="cuda") // block_rows
+            top = top.reshape(-1).scatter_reduce(0, (i[:, None] * scales.shape[1] + j).reshape(-1), v.abs().reshape(-1),
+                                                 "amax").view_as(top)
+            s = scales[r // block_rows:(r + 128) // block_rows]
+            assert ((top <= 448 * s) & (top > 224 * s)).all()
+            each = s[i][:, j]
+            assert torch.equal(codes[r:r + 128].float(), (v / each).to(torch.float8_e4m3fn).float())
+            assert torch.equal(back[r:r + 128].float(), codes[r:r + 128].float() * each)
+        assert float(back.abs().float().sum(dtype=torch.float64)) == sum(
+            float(back[r:r + 128].abs().float().sum(dtype=torch.float64)) for r in picks)
+        del codes, scales, back
+
+
+def test_gated_past_32_bits(compute):
+    tokens, hidden, ffn = 80003, 64, 28680
+    g = gen(99)
+    x, (wg, wu) = randn(g, tokens, hidden), weights(g, hidden, ffn)
+    dh = randn(g, tokens, ffn)
+    new = dict(device="cuda", dtype=torch.bfloat16)
+    h, dx = torch.empty(tokens, ffn, **new), torch.empty(tokens, hidden, **new)
+    dwg, dwu = torch.empty(ffn, hidden, **new), torch.empty(ffn, hidden, **new)
+    codes = [torch.empty(tokens, ffn, dtype=torch.float8_e4m3fn, device="cuda") for _ in range(2)]
+    scales = [torch.empty(tokens, -(-ffn // 128), device="cuda") for _ in range(2)]
+    ck = tide.GatedCheckpoint(codes[0], scales[0], codes[1], scales[1])
+    compute.gated_forward(tokens, hidden, ffn, x, wg, wu, h, checkpoint=ck)
+    ws = torch.empty(tide.gated_workspace_bytes(tokens, hidden, ffn), dtype=torch.uint8, device="cuda")
+    rows = torch.tensor([0, 40000, 2 ** 31 // ffn, 2 ** 31 // ffn + 1, 79999, tokens - 1], device="cuda")
+    cols = torch.tensor([0, 1, 14340, ffn - 129, ffn - 1], device="cuda")
+    want, gg, uu = ref.gated_forward(x[rows], wg, wu, "silu")
+    bh, eg, eu = ref.gated_forward_bound(x[rows], wg, wu, "silu")
+    close(h[rows], want, bh)
+    close_to_stored(pick8(codes[0], rows), scales[0][rows], gg, eg)
+    close_to_stored(pick8(codes[1], rows), scales[1][rows], uu, eu)
+    for kept in (None, ck):
+        h.fill_(0)
+        compute.gated_backward(tokens, hidden, ffn, dh, x, wg, wu, dx, dwg, dwu, ws, checkpoint=kept, h=h)
+        compute.check_device()
+        if kept is None:
+            pre = ref.gated_forward(x[rows], wg, wu, "silu")[1:]
+            err = ref.gated_forward_bound(x[rows], wg, wu, "silu")[1:]
+            part = ref.gated_forward(x, wg[cols], wu[cols], "silu")[1:]
+            part_err = ref.gated_forward_bound(x, wg[cols], wu[cols], "silu")[1:]
+        else:
+            pre = [ref.blocks_value(pick8(codes[i], rows), scales[i][rows], 1) for i in range(2)]
+            j = cols // 128
+            part = [codes[i].view(torch.uint8)[:, cols].view(torch.float8_e4m3fn).float().double() * scales[i][:, j].double() for i in range(2)]
+            err = part_err = (0.0, 0.0)
+        want = ref.gated_backward_from(dh[rows], *pre, x[rows], wg, wu, "silu")
+        close(dx[rows], want[0], ref.gated_backward_bound(dh[rows], *pre, x[rows], wg, wu, "silu", *err)[0])
+        want = ref.gated_backward_from(dh[:, cols], *part, x, wg[cols], wu[cols], "silu")
+        bounds = ref.gated_backward_bound(dh[:, cols], *part, x, wg[cols], wu[cols], "silu", *part_err)
+        close(dwg[cols], want[1], bounds[1])
+        close(dwu[cols], want[2], bounds[2])
+        hw = ref.act(pre[0], "silu") * pre[1]
+        off = bh if kept is None else hw.abs() * (ref.arithmetic(pre[0], "silu") + 1.01 * ref.U_BF16) + ref.TINY * (
+            1 + pre[1].abs() * (1 + pre[0].abs()) ** 3)
+        close(h[rows], hw, off)
+
+
+@pytest.mark.parametrize("any_scales", [False, True])
+def test_matmul_past_32_bits(compute, any_scales):
+    m, n, k = 80003, 28680, 144
+    g = gen(98)
+    (a, sa), (b, sb) = fp8(g, m, k, 1, any_scales), fp8(g, n, k, 128, any_scales)
+    out = torch.empty(m, n, dtype=torch.bfloat16, device="cuda")
+    compute.fp8_matmul(m, n, k, a, sa, b, sb, out, any_scales=any_scales)
+    rows = torch.tensor([0, 2 ** 31 // n, 2 ** 31 // n + 1, m - 1], device="cuda")
+    close(out[rows], *ref.matmul(pick8(a, rows), sa[rows], b, sb))
