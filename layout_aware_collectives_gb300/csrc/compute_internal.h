@@ -136,7 +136,7 @@ cudaError_t launch_fp8_matmul_tc(const MatmulArgs& a, const TcLaunch& l, cudaStr
 bool gated_few_takes(const GatedArgs& a, int sms);
 bool fp8_few_takes(const MatmulArgs& a, int sms);
 cudaError_t launch_gated_grad_few(const GatedArgs& a, const TcLaunch& l, cudaStream_t stream);
-bool gated_dx_few_takes(const GatedArgs& a, int pairs);
+bool gated_dx_few_takes(const GatedArgs& a, const TcLaunch& l);
 // beside: straight after launch_gated_back_tc's dW on this stream, and beside it.
 cudaError_t launch_gated_dx_few(const GatedArgs& a, bool beside, const TcLaunch& l, cudaStream_t stream);
 cudaError_t launch_gated_forward_few(const GatedArgs& a, const TcLaunch& l, cudaStream_t stream);

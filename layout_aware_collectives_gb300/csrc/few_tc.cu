@@ -487,15 +487,25 @@ cudaError_t few_tc_prepare() {
 // against 11.7), for the 8-bit product from two thirds (128 x 28672 x 8192,
 // 128 tiles: 76 us against 87; 1021 x 2048 x 768: 9.6 against 9.1).
 bool gated_few_takes(const GatedArgs& a, int sms) { return few(a.tokens, a.ffn, sms / 2); }
-// dX up to 64 tokens (1 x 4096 x 14336: 33 us against 54 in 256-row tiles),
-// and for more where it has few tiles and dW's leave SMs for it (190 x 240 x
-// 8032, backward: 28.8 us against 32.1; 500 x 1024 x 1024, 64 tiles: 26.1
-// against 23.1).  Below 48 stages the launch that dX then has to itself costs
-// the host more than it saves (2 x 5792 x 160: 8.7 us, but 3 more to enqueue).
-bool gated_dx_few_takes(const GatedArgs& a, int pairs) {
-  if (2 * ceil_div(a.ffn, kRowBytes / 2) < 48) return false;
+// dX up to 64 tokens, and for more where it has few tiles and dW's leave SMs
+// for it (500 x 1024 x 1024, 64 tiles: 26.1 us for the backward pass against
+// 23.1 in 256-row tiles).  In microseconds, here 0.21 a stage and 3 more, in
+// 256-row tiles 0.3 and 4, or 8 where their sums are split (1 x 4096 x 14336:
+// 33 against 54; 64 x 512 x 2048: 7 against 12; 2 x 336 x 25264, where a
+// cluster's 8 CTAs are too few: 32 against 22).  Below 48 stages the launch
+// that dX then has to itself costs the host more than it saves (2 x 5792 x
+// 160: 8.7 us, but 3 more to enqueue).
+bool gated_dx_few_takes(const GatedArgs& a, const TcLaunch& l) {
+  const int64_t steps = 2 * ceil_div(a.ffn, kRowBytes / 2);
+  if (steps < 48) return false;
+  const int64_t tiles = ceil_div(a.hidden, kRows) * ceil_div(a.tokens, 64);
+  const int64_t large = ceil_div(a.hidden, 256) * ceil_div(a.tokens, 256);
+  int64_t split = 1;
+  while (split < 8 && 2 * split * tiles <= l.sms) split *= 2;
+  const int64_t parts = l.pairs / large > 1 ? l.pairs / large : 1;
+  if (0.21 * steps / split + 3 > 0.3 * steps / parts + (parts > 1 ? 8 : 4)) return false;
   if (a.tokens <= 64) return few(a.tokens, a.hidden, 0);
-  return a.tokens <= 512 && few(a.tokens, a.hidden, 32) && 2 * ceil_div(a.ffn, 256) * ceil_div(a.hidden, 256) <= pairs;
+  return a.tokens <= 512 && few(a.tokens, a.hidden, 32) && 2 * ceil_div(a.ffn, 256) * ceil_div(a.hidden, 256) <= l.pairs;
 }
 
 bool fp8_few_takes(const MatmulArgs& a, int sms) { return few(a.m, a.n, 2 * sms / 3); }

@@ -435,8 +435,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gated_t
 }
 
 // Results from the parts of their sums, in the parts' order.  A part lies
-// column by column, `out0`'s parts before `out1`'s: 32 rows x 64 columns a
-// CTA, turned in shared memory.
+// column by column, `out0`'s parts before `out1`'s: 32 rows x COLS columns a
+// CTA, turned in shared memory, AT_ONCE parts of COLS / 8 columns a thread on
+// their way at a time.  Few parts are many bytes each, many parts a latency
+// for every turn: 64 columns and 4 parts, 32 and 8 or 16 and 16 (256 x 4096
+// of 4 parts: 8 us less than in 16 columns; 849 x 144 of 19: 5 us less than in
+// 64).
 struct Join {
   const float* parts;
   int split;
@@ -445,35 +449,37 @@ struct Join {
   int rows, cols;
 };
 
+template <int COLS, int AT_ONCE>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(Join a) {
   after_previous();
-  __shared__ float tile[64][33];
-  const int row0 = blockIdx.x * 32, col0 = blockIdx.y * 64;
+  constexpr int kCols = COLS / 8;
+  __shared__ float tile[COLS][33];
+  const int row0 = blockIdx.x * 32, col0 = blockIdx.y * COLS;
   const int r = threadIdx.x & 31, c0 = threadIdx.x >> 5;
   const int64_t numel = (int64_t)a.rows * a.cols, next = numel * gridDim.z;
-  float sum[8];
+  float sum[kCols];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) sum[i] = 0.0f;
+  for (int i = 0; i < kCols; ++i) sum[i] = 0.0f;
   if (row0 + r < a.rows) {
     const float* from = a.parts + blockIdx.z * numel + (int64_t)(col0 + c0) * a.rows + row0 + r;
-    for (int s = 0; s < a.split; s += 4) {  // 32 reads on their way at a time
-      float v[4][8];
+    for (int s = 0; s < a.split; s += AT_ONCE) {
+      float v[AT_ONCE][kCols];
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
+      for (int q = 0; q < AT_ONCE; ++q)
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < kCols; ++i)
           v[q][i] = s + q < a.split && col0 + c0 + 8 * i < a.cols ? from[(s + q) * next + (int64_t)8 * i * a.rows] : 0.0f;
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
+      for (int q = 0; q < AT_ONCE; ++q)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum[i] += v[q][i];
+        for (int i = 0; i < kCols; ++i) sum[i] += v[q][i];
     }
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) tile[c0 + 8 * i][r] = sum[i];
+  for (int i = 0; i < kCols; ++i) tile[c0 + 8 * i][r] = sum[i];
   __syncthreads();
-  const int row = threadIdx.x >> 3, col = (threadIdx.x & 7) * 8;
-  if (row0 + row >= a.rows || col0 + col >= a.cols) return;  // widths are multiples of 8
+  const int row = threadIdx.x / kCols, col = threadIdx.x % kCols * 8;
+  if (row >= 32 || row0 + row >= a.rows || col0 + col >= a.cols) return;  // widths are multiples of 8
   uint32_t o[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) o[i] = pack_bf16(tile[col + 2 * i][row], tile[col + 2 * i + 1][row]);
@@ -481,9 +487,16 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(Join a) {
   *(uint4*)(out + (int64_t)(row0 + row) * a.ld + col0 + col) = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+template <int COLS, int AT_ONCE>
 cudaError_t join(const Join& a, int outputs, cudaStream_t stream) {
-  return launch_early(join_kernel, dim3((unsigned)ceil_div(a.rows, 32), (unsigned)ceil_div(a.cols, 64), outputs),
-                      kJoinThreads, 0, 0, stream, a);
+  return launch_early(join_kernel<COLS, AT_ONCE>,
+                      dim3((unsigned)ceil_div(a.rows, 32), (unsigned)ceil_div(a.cols, COLS), outputs), kJoinThreads, 0, 0,
+                      stream, a);
+}
+cudaError_t join(const Join& a, int outputs, cudaStream_t stream) {
+  return a.split <= 4   ? join<64, 4>(a, outputs, stream)
+         : a.split <= 8 ? join<32, 8>(a, outputs, stream)
+                        : join<16, 16>(a, outputs, stream);
 }
 
 template <int FORM, int ACT>
