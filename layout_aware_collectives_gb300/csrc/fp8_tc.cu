@@ -45,7 +45,8 @@ struct Params {
   CUtensorMap a, b, out;
   const float *sa, *sb;
   int rows, cols;
-  int tiles_m, tiles_n, tiles;
+  TileGrid grid;
+  int tiles;
   int blocks;  // of the contraction
   int* err;
   uint64_t limit_ns, stall_ns;
@@ -107,7 +108,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) summed_
       int j = 0;  // stages filled so far
       bool go = true;
       for (int t = pair; t < p.tiles && go; t += pairs) {
-        const TileAt at = tile_at(p.tiles_m, p.tiles_n, t);
+        const TileAt at = tile_at(p.grid, t);
         for (int k = 0; k < p.blocks; ++k, ++j) {
           const int s = j % kStages;
           if (j >= kStages && !bar_wait(empty(s), (j / kStages + 1) & 1, watch)) {
@@ -166,7 +167,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) summed_
     int j = 0;
     bool go = true;
     for (int t = pair; t < p.tiles && go; t += pairs) {
-      const TileAt at = tile_at(p.tiles_m, p.tiles_n, t);
+      const TileAt at = tile_at(p.grid, t);
       const int row0 = (at.m * 2 + rank) * kHalf + lanes, row = row0 + lane;
       const int col0 = (at.n * 2 + half) * kHalf;
       // rows and columns past the end take any scale that is there: their
@@ -278,7 +279,7 @@ __global__ void __cluster_dims__(2, 1, 1)
       int j = 0;  // stages filled so far
       bool go = true;
       for (int t = pair; t < p.tiles && go; t += pairs) {
-        const TileAt at = tile_at(p.tiles_m, p.tiles_n, t);
+        const TileAt at = tile_at(p.grid, t);
         for (int k = 0; k < p.blocks; ++k, ++j) {
           const int s = j % kStages;
           if (j >= kStages && !bar_wait(empty(s), (j / kStages + 1) & 1, watch)) {
@@ -345,7 +346,7 @@ __global__ void __cluster_dims__(2, 1, 1)
     int j = 0, batch = 0;
     bool go = true;
     for (int t = pair; t < p.tiles; t += pairs) {
-      const TileAt at = tile_at(p.tiles_m, p.tiles_n, t);
+      const TileAt at = tile_at(p.grid, t);
       // rows and columns past the end take any scale that is there
       const float* sa = p.sa + (int64_t)min((int)(at.m * 2 + rank) * kHalf + w * 32 + lane, p.rows - 1) * p.blocks;
       const float* sb = p.sb + (int64_t)min(at.n * 2 + (lane & 1), (p.cols - 1) / kBlock) * p.blocks;
@@ -396,7 +397,7 @@ __global__ void __cluster_dims__(2, 1, 1)
     for (int t = pair; t < p.tiles; t += pairs, ++i) {
       if (!bar_wait_warp(sums_full, i & 1, watch)) break;
       fence_after();
-      const TileAt at = tile_at(p.tiles_m, p.tiles_n, t);
+      const TileAt at = tile_at(p.grid, t);
       const int row0 = (at.m * 2 + rank) * kHalf + lanes, col0 = at.n * 2 * kHalf;
       const uint32_t sums = tmem + (lanes << 16) + (i & 1) * kOdd;
       const int first = i & 1 ? 0 : 8 - kShared;  // the chunks the next tile shares
@@ -447,8 +448,8 @@ cudaError_t launch_fp8_matmul_tc(const MatmulArgs& a, const TcLaunch& l, cudaStr
   Params p{};
   p.sa = a.sa, p.sb = a.sb;
   p.rows = (int)a.m, p.cols = (int)a.n;
-  p.tiles_m = (int)ceil_div(a.m, 2 * kHalf), p.tiles_n = (int)ceil_div(a.n, 2 * kHalf);
-  p.tiles = p.tiles_m * p.tiles_n;
+  p.grid = TileGrid((int)ceil_div(a.m, 2 * kHalf), (int)ceil_div(a.n, 2 * kHalf));
+  p.tiles = p.grid.all.d;
   p.blocks = (int)ceil_div(a.k, kBlock);
   p.err = l.err;
   p.limit_ns = TIDE_BULK_TIMEOUT_NS;

@@ -48,18 +48,33 @@ constexpr int kThreads = 128 + 32 * kEpiWarps;
 constexpr int kBoxes = kAllBoxes / kEpiWarps;
 constexpr int kJoinThreads = 256;
 
+// Stages of part z of `split` of a sum of `steps`.
+struct Share {
+  int least, more;  // stages of each part; parts with one more
+
+  Share() = default;
+  Share(int steps, int split) : least(steps / split), more(steps % split) {}
+  __device__ __forceinline__ int from(int z) const { return z * least + min(z, more); }
+};
+
 struct Params {
   // forward, grad: a = x, b = Wg, Wu; out = h, or dG, dU, h
   // back: dX: a = dG, dU, b = Wg, Wu, out[0]; dW: wa = dG, dU, wb = x, out[1..2]
   CUtensorMap a[2], b[2], wa[2], wb, out[3];
   int rows, cols;  // of the outputs (back: of dX)
-  int tiles_m, tiles_n, tiles;
+  TileGrid grid;
+  int tiles;
   int steps;       // stages of one tile's sum
   int half_steps;  // back: stages of dX's first half
   int split, w_split;  // back: parts of dX's and of dW's sums, each in its own tile
+  Share share, w_share;
   float *parts, *w_parts;  // of [split, cols, rows], [w_split, half, cols, w_rows], where there are several
-  int w_rows, w_tiles_m, w_tiles_n, w_tiles, w_steps;  // back: dW, both halves' tiles
-  int extra;       // back: tiles of dW that take as long as one of dX
+  TileGrid w_grid;
+  int w_rows, w_tiles, w_steps;  // back: dW, both halves' tiles
+  // back: who takes which tile (work_at).  dX's for each pair, and how many
+  // pairs have one more; the others; dW's that go to those first, and how
+  // many that is for each, and how many have one more
+  int each, full, light, first, first_each, first_more;
   bool one_a, one_b;  // back: wa's, b's and wb's operands are one box each (map_mn)
   // epilogue
   uint8_t *g8, *u8;
@@ -115,43 +130,37 @@ struct Work {
 
 // The pair's i-th tile; false past the last.  Tiles go round the pairs in
 // turn.  In the back form dX's tiles come first; where they do not come out
-// even, the pairs that are one short take `extra` tiles of dW before the
-// rest goes round, beginning with them again.
+// even, the pairs that are one short take as many tiles of dW as one of dX is
+// worth before the rest goes round, beginning with them again.
 template <int FORM>
 __device__ __forceinline__ bool work_at(const Params& p, int pair, int pairs, int i, Work& r) {
   int t = pair + i * pairs;
   r.w = false;
-  r.k0 = 0, r.k1 = p.steps;
-  if (FORM != kBack || t < p.tiles) {
+  if (FORM != kBack) {
     if (t >= p.tiles) return false;
-    r.at = tile_at(p.tiles_m, p.tiles_n, t);
-    if (FORM == kBack) {
-      r.k0 = (int)((int64_t)p.steps * r.at.z / p.split);
-      r.k1 = (int)((int64_t)p.steps * (r.at.z + 1) / p.split);
-      r.part = p.split > 1 ? p.parts + (int64_t)r.at.z * p.rows * p.cols : nullptr;
-    }
+    r.at = tile_at(p.grid, t);
+    r.k0 = 0, r.k1 = p.steps;
     return true;
   }
-  i -= pair < p.tiles ? (p.tiles - pair + pairs - 1) / pairs : 0;
-  const int full = p.tiles % pairs;  // pairs with one more tile than the others
-  const int light = pairs - full, l = pair - full;
-  int first = 0;
-  if (full) {
-    first = min(p.w_tiles, light * p.extra);
-    if (l >= 0) {
-      const int mine = l < first ? (first - l + light - 1) / light : 0;
-      t = l + i * light;
-      if (i < mine) first = -1;
-      i -= mine;
-    }
+  if (t < p.tiles) {
+    r.at = tile_at(p.grid, t);
+    r.k0 = p.share.from(r.at.z), r.k1 = p.share.from(r.at.z + 1);
+    r.part = p.split > 1 ? p.parts + (int64_t)r.at.z * p.rows * p.cols : nullptr;
+    return true;
   }
-  if (first >= 0) t = first + (l >= 0 ? l : light + pair) + i * pairs;
+  const int l = pair - p.full;  // among those without one more, if not below 0
+  i -= p.each + (l < 0);
+  const int mine = l >= 0 ? p.first_each + (l < p.first_more) : 0;
+  if (i < mine)
+    t = l + i * p.light;
+  else
+    t = p.first + (l >= 0 ? l : p.light + pair) + (i - mine) * pairs;
   if (t >= p.w_tiles) return false;
   r.w = true;
-  r.at = tile_at(p.w_tiles_m, p.w_tiles_n, t);
+  r.at = tile_at(p.w_grid, t);
   r.half = r.at.z & 1;
-  r.k0 = (int)((int64_t)p.w_steps * (r.at.z >> 1) / p.w_split);
-  r.k1 = (int)((int64_t)p.w_steps * ((r.at.z >> 1) + 1) / p.w_split);
+  const int z = r.at.z >> 1;
+  r.k0 = p.w_share.from(z), r.k1 = p.w_share.from(z + 1);
   r.part = p.w_split > 1 ? p.w_parts + (int64_t)r.at.z * p.w_rows * p.cols : nullptr;
   return true;
 }
@@ -255,29 +264,35 @@ __device__ __forceinline__ void epilogue(const Params& p, const Work& work, uint
             o2[i] = pack_bf16(t0.x * u0, t1.x * u1);
           }
         }
-        out.put2(&p.out[0], o, &p.out[1], o1, col, row0);
+        out.put2(&p.out[0], o, col, &p.out[1], o1, col, row0);
         if (p.with_h) out.put(&p.out[2], o2, col, row0);
       }
     }
   } else {
     const CUtensorMap* map = &p.out[work.w ? 1 + work.half : 0];
 #pragma unroll 1
-    for (int c = half * 4; c < half * 4 + 4; ++c) {
+    for (int c = half * 4; c < half * 4 + 4; c += 2) {
       const int col = t.n * 2 * kHalf + c * 32;
       if (!any || col >= p.cols) break;
-      uint32_t v[32], o[16];
-      tmem_read(tmem + c * 32, v);
+      uint32_t v[32], u[32];
+      tmem_read32x2(tmem + c * 32, tmem + c * 32 + 32, v, u);
       if (work.part) {
         // a column of the warp's 32 rows lies together, so its threads do
         uint32_t* to = (uint32_t*)work.part + (int64_t)col * rows + row;
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
+        for (int i = 0; i < 32; ++i) {
           if (mine && col + i < p.cols) to[(int64_t)i * rows] = v[i];
+          if (mine && col + 32 + i < p.cols) to[(int64_t)(32 + i) * rows] = u[i];
+        }
         continue;
       }
+      uint32_t o0[16], o1[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) o[i] = pack_bf16(as_f(v[2 * i]), as_f(v[2 * i + 1]));
-      out.put(map, o, col, row0);
+      for (int i = 0; i < 16; ++i) {
+        o0[i] = pack_bf16(as_f(v[2 * i]), as_f(v[2 * i + 1]));
+        o1[i] = pack_bf16(as_f(u[2 * i]), as_f(u[2 * i + 1]));
+      }
+      out.put2(map, o0, col, map, o1, col + 32, row0, col + 32 < p.cols);
     }
   }
 }
@@ -499,13 +514,14 @@ cudaError_t join(const Join& a, int outputs, cudaStream_t stream) {
                         : join<16, 16>(a, outputs, stream);
 }
 
+int pairs_of(const Params& p, const TcLaunch& l) { return p.tiles + p.w_tiles < l.pairs ? p.tiles + p.w_tiles : l.pairs; }
+
 template <int FORM, int ACT>
 cudaError_t launch(Params& p, const TcLaunch& l, cudaStream_t stream) {
   p.err = l.err;
   p.limit_ns = TIDE_BULK_TIMEOUT_NS;
   p.stall_ns = l.stall_ns;
-  const int pairs = p.tiles + p.w_tiles < l.pairs ? p.tiles + p.w_tiles : l.pairs;
-  return launch_early(gated_tc_kernel<FORM, ACT>, dim3(2 * pairs), kThreads, kSmem, 0, stream, p);
+  return launch_early(gated_tc_kernel<FORM, ACT>, dim3(2 * pairs_of(p, l)), kThreads, kSmem, 0, stream, p);
 }
 
 bool rows16(int64_t width, int64_t ld) { return width % 8 == 0 && ld % 8 == 0; }
@@ -529,8 +545,8 @@ bool map_out(CUtensorMap* m, const uint16_t* p, int64_t cols, int64_t rows, int6
 
 bool fill_pre(Params* p, const GatedArgs& a) {
   p->rows = (int)a.tokens, p->cols = (int)a.ffn;
-  p->tiles_m = (int)ceil_div(a.tokens, 2 * kHalf), p->tiles_n = (int)ceil_div(a.ffn, kHalf);
-  p->tiles = p->tiles_m * p->tiles_n;
+  p->grid = TileGrid((int)ceil_div(a.tokens, 2 * kHalf), (int)ceil_div(a.ffn, kHalf));
+  p->tiles = p->grid.all.d;
   p->steps = (int)ceil_div(a.hidden, kStep);
   if (!map_k(&p->a[0], a.x, a.hidden, a.tokens, a.ldx)) return false;
   p->a[1] = p->a[0];
@@ -609,11 +625,12 @@ cudaError_t launch_gated_back_tc(const GatedArgs& a, bool dx, bool dw, bool dx_b
   p.one_a = a.ffn % 64 == 0, p.one_b = a.hidden % 64 == 0;
   if (dx) {
     p.rows = (int)a.tokens;
-    p.tiles_m = (int)ceil_div(a.tokens, 2 * kHalf), p.tiles_n = (int)ceil_div(a.hidden, 2 * kHalf);
+    p.grid = TileGrid((int)ceil_div(a.tokens, 2 * kHalf), (int)ceil_div(a.hidden, 2 * kHalf));
     p.half_steps = (int)ceil_div(a.ffn, kStep), p.steps = 2 * p.half_steps;
-    p.split = split_of((int64_t)p.tiles_m * p.tiles_n, p.steps, l.pairs, 4 * a.tokens * a.hidden, a.dx_parts_bytes);
+    p.split = split_of(p.grid.all.d, p.steps, l.pairs, 4 * a.tokens * a.hidden, a.dx_parts_bytes);
+    p.share = Share(p.steps, p.split);
     p.parts = a.dx_parts;
-    p.tiles = p.tiles_m * p.tiles_n * p.split;
+    p.tiles = p.grid.all.d * p.split;
     if (!map_k(&p.a[0], a.dg, a.ffn, a.tokens, a.ffn) || !map_k(&p.a[1], a.du, a.ffn, a.tokens, a.ffn) ||
         !map_mn(&p.b[0], a.wg, a.hidden, a.ffn, a.hidden) || !map_mn(&p.b[1], a.wu, a.hidden, a.ffn, a.hidden) ||
         !map_out(&p.out[0], a.dx, a.hidden, a.tokens, a.lddx))
@@ -621,21 +638,25 @@ cudaError_t launch_gated_back_tc(const GatedArgs& a, bool dx, bool dw, bool dx_b
   }
   if (dw) {
     p.w_rows = (int)a.ffn;
-    p.w_tiles_m = (int)ceil_div(a.ffn, 2 * kHalf), p.w_tiles_n = (int)ceil_div(a.hidden, 2 * kHalf);
-    p.w_tiles = 2 * p.w_tiles_m * p.w_tiles_n;
+    p.w_grid = TileGrid((int)ceil_div(a.ffn, 2 * kHalf), (int)ceil_div(a.hidden, 2 * kHalf));
+    p.w_tiles = 2 * p.w_grid.all.d;
     p.w_steps = (int)ceil_div(a.tokens, kStep);
     p.w_split = split_of(p.w_tiles, p.w_steps, l.pairs, 8 * a.ffn * a.hidden, a.dw_parts_bytes);
+    p.w_share = Share(p.w_steps, p.w_split);
     p.w_parts = a.dw_parts;
     p.w_tiles *= p.w_split;
-    // what a tile of either takes: its stages, at least the six that writing
-    // it takes, and about one for its way in and out
-    const int w_part = p.w_steps / p.w_split, w_cost = (w_part > 6 ? w_part : 6) + 1;
-    p.extra = ((dx ? p.steps / p.split : 0) + 1 + w_cost / 2) / w_cost;
     if (!map_mn(&p.wa[0], a.dg, a.ffn, a.tokens, a.ffn) || !map_mn(&p.wa[1], a.du, a.ffn, a.tokens, a.ffn) ||
         !map_mn(&p.wb, a.x, a.hidden, a.tokens, a.ldx) || !map_out(&p.out[1], a.dwg, a.hidden, a.ffn, a.hidden) ||
         !map_out(&p.out[2], a.dwu, a.hidden, a.ffn, a.hidden))
       return cudaErrorInvalidValue;
   }
+  // What a tile of either takes: its stages, at least the four that writing it
+  // takes, and about one for its way in and out.
+  const int x_part = dx ? p.share.least : 0, w_part = dw && p.w_share.least > 4 ? p.w_share.least : 4;
+  const int pairs = pairs_of(p, l), extra = (x_part + 1 + (w_part + 1) / 2) / (w_part + 1);
+  p.each = p.tiles / pairs, p.full = p.tiles % pairs, p.light = pairs - p.full;
+  p.first = !p.full ? 0 : p.w_tiles < p.light * extra ? p.w_tiles : p.light * extra;
+  p.first_each = p.first / p.light, p.first_more = p.first % p.light;
   cudaError_t e = launch<kBack, 0>(p, l, stream);
   if (e == cudaSuccess && dx_beside) e = launch_gated_dx_few(a, true, l, stream);
   if (e == cudaSuccess && p.split > 1)

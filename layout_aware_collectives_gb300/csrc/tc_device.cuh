@@ -6,6 +6,8 @@
 #include <cuda.h>
 #include <stdint.h>
 
+#include "tc_host.h"
+
 namespace tide {
 namespace tc {
 
@@ -298,19 +300,20 @@ struct TileAt {
   int z, m, n;  // which of several products; tile indices
 };
 
-// Tiles in bands of 16 down the rows, so that the tiles at work at one time
-// share their operands in L2.
-__device__ __forceinline__ TileAt tile_at(int tiles_m, int tiles_n, int t) {
-  constexpr int kBand = 16;
-  const int per = tiles_m * tiles_n;
+// No division: with few stages a tile they were a quarter of its time.
+__device__ __forceinline__ TileAt tile_at(const TileGrid& g, int t) {
   TileAt r;
-  r.z = t / per;
-  t -= r.z * per;
-  const int band = t / (kBand * tiles_n), first = band * kBand;
-  const int high = min(kBand, tiles_m - first);
-  t -= first * tiles_n;
-  r.n = t / high;
-  r.m = first + t - r.n * high;
+  r.z = g.all.of(t);
+  t -= r.z * g.all.d;
+  const int band = g.band.of(t), first = band * kBand;
+  t -= band * g.band.d;
+  if (first + kBand <= g.tiles_m) {
+    r.n = t / kBand;
+    r.m = first + t % kBand;
+  } else {
+    r.n = g.last.of(t);
+    r.m = first + t - r.n * g.last.d;
+  }
   return r;
 }
 
@@ -346,15 +349,20 @@ struct Outbox {
     __syncwarp();
     if (lane == 0) store_box(map, col, row, box);
   }
-  // Two at once, behind one fence.
-  __device__ __forceinline__ void put2(const CUtensorMap* map0, const uint32_t (&p0)[16], const CUtensorMap* map1,
-                                       const uint32_t (&p1)[16], int col, int row) {
+  // Two at once, behind one fence, the second only if `two`.
+  __device__ __forceinline__ void put2(const CUtensorMap* map0, const uint32_t (&p0)[16], int col0, const CUtensorMap* map1,
+                                       const uint32_t (&p1)[16], int col1, int row, bool two = true) {
     if (lane == 0) stores_read<BOXES - 2>();
     __syncwarp();
-    const uint32_t box0 = fill(p0), box1 = fill(p1);
+    const uint32_t box0 = fill(p0);
+    uint32_t box1 = 0;
+    if (two) box1 = fill(p1);
     async_fence();
     __syncwarp();
-    if (lane == 0) store_box(map0, col, row, box0), store_box(map1, col, row, box1);
+    if (lane == 0) {
+      store_box(map0, col0, row, box0);
+      if (two) store_box(map1, col1, row, box1);
+    }
   }
 };
 
