@@ -437,6 +437,57 @@ def test_streams_and_capture(compute, tokens, hidden, ffn):
         check()
 
 
+def test_streams_side_by_side(compute):
+    """Calls of every kind on three streams at once, one handle, give what they
+    give one after the other."""
+    g = gen(55)
+
+    class Job:
+        def __init__(self, tokens, hidden, ffn):
+            self.size = tokens, hidden, ffn
+            self.x, self.dh, (self.wg, self.wu) = randn(g, tokens, hidden), randn(g, tokens, ffn), weights(g, hidden, ffn)
+            (self.a, self.sa), (self.b, self.sb) = fp8(g, tokens, ffn, 1), fp8(g, hidden, ffn, 128)
+            new = dict(device="cuda", dtype=torch.bfloat16)
+            self.out = [torch.empty(*s, **new) for s in
+                        ((tokens, ffn), (tokens, hidden), (ffn, hidden), (ffn, hidden), (tokens, hidden))]
+            self.codes = torch.empty(tokens, ffn, dtype=torch.uint8, device="cuda")
+            self.scales = torch.empty(tokens, -(-ffn // 128), device="cuda")
+            self.ws = torch.empty(tide.gated_workspace_bytes(tokens, hidden, ffn), dtype=torch.uint8, device="cuda")
+
+        def run(self, stream):
+            m, k, f = self.size
+            h, dx, dwg, dwu, y = self.out
+            compute.gated_forward(m, k, f, self.x, self.wg, self.wu, h, stream=stream)
+            compute.fp8_matmul(m, k, f, self.a, self.sa, self.b, self.sb, y, stream=stream)
+            compute.fp8_store(m, f, h, self.codes, self.scales, stream=stream)
+            compute.gated_backward(m, k, f, self.dh, self.x, self.wg, self.wu, dx, dwg, dwu, self.ws, stream=stream)
+
+        def results(self):
+            return [t.clone() for t in self.out + [self.codes, self.scales]]
+
+    jobs = [Job(*s) for s in ((5, 256, 704), (700, 264, 2056), (40, 512, 2560), (300, 1024, 3328), (130, 2048, 768))]
+    torch.cuda.synchronize()
+    want = []
+    for j in jobs:
+        j.run(None)
+        torch.cuda.synchronize()
+        want.append(j.results())
+        for t in j.out:
+            t.zero_()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for turn in range(20):
+        for i, j in enumerate(jobs):
+            j.run(streams[(i + turn) % 3] if turn == 0 else streams[i % 3])
+        if turn == 0:
+            torch.cuda.synchronize()  # jobs change streams after this turn
+    torch.cuda.synchronize()
+    compute.check_device()
+    for j, w in zip(jobs, want):
+        for a, b in zip(j.results(), w):
+            assert torch.equal(a, b)
+
+
 def test_first_call_is_not_captured():
     with tide.Compute() as c:
         src = torch.zeros(4, 128, dtype=torch.bfloat16, device="cuda")
