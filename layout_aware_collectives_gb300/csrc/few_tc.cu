@@ -78,19 +78,25 @@ __device__ __forceinline__ float4 peer_read(uint32_t addr) {
   return v;
 }
 
-// Sums of the cluster's CTAs' sums at N addresses, in rank order.  All of one
-// rank's reads are on their way before the first is added.
+// Sums of the cluster's CTAs' sums at N addresses, in rank order.  Four ranks'
+// reads are on their way before the first is added.  (split: 2, 4 or 8.)
 template <int N>
 __device__ __forceinline__ void cluster_sums(const uint32_t (&addr)[N], int split, float4 (&v)[N]) {
+  constexpr int kAtOnce = 4;
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = peer_read(peer_addr(addr[i], 0));
+  for (int i = 0; i < N; ++i) v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 1
-  for (int r = 1; r < split; ++r) {
-    float4 a[N];
+  for (int r = 0; r < split; r += kAtOnce) {
+    float4 a[kAtOnce][N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) a[i] = peer_read(peer_addr(addr[i], r));
+    for (int q = 0; q < kAtOnce; ++q)
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i].x += a[i].x, v[i].y += a[i].y, v[i].z += a[i].z, v[i].w += a[i].w;
+      for (int i = 0; i < N; ++i)
+        a[q][i] = r + q < split ? peer_read(peer_addr(addr[i], r + q)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int q = 0; q < kAtOnce; ++q)
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i].x += a[q][i].x, v[i].y += a[q][i].y, v[i].z += a[q][i].z, v[i].w += a[q][i].w;
   }
 }
 __device__ __forceinline__ float4 own_read(uint32_t addr) {
