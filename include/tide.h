@@ -489,12 +489,13 @@ TIDE_API tide_status_t tide_layout_check_tiles(tide_layout_t layout, tide_op_t o
  *  - Matrices are row-major.  Arguments ld* are row strides in elements, at
  *    least the row's width.  Rows whose stride and width are multiples of
  *    8 elements (16 for 8-bit operands) start on 16 bytes and run the
- *    tensor-core kernels; any other width or stride runs plain tiled
- *    kernels, right but many times slower.
+ *    kernels for large operands; any other width or stride runs plain
+ *    tiled kernels, several times slower.
  *  - Sums are fp32; a result is rounded to bf16 once, to nearest even.
  *  - Every buffer is the caller's, 16-byte aligned (scales: 4-byte;
- *    TIDE_ERR_MISALIGNED otherwise) and in memory of the handle's device; outputs must not overlap inputs or
- *    each other.  A pointer to a matrix without elements may be NULL.
+ *    TIDE_ERR_MISALIGNED otherwise) and in memory of the handle's device;
+ *    outputs must not overlap inputs or each other.  A pointer to a matrix
+ *    without elements may be NULL.
  *  - Sizes are 0 .. 2^31 - 1 each, and any matrix has at most 2^38 elements.
  *  - A compute handle may be used from several host threads and streams; it
  *    keeps nothing between calls but its device's properties and an error

@@ -18,7 +18,7 @@
 // accumulators so that they do so while the next tile is summed.
 //
 // Bound by the tensor cores at every large size: 2048 x 4096 x 14336 forward
-// 243-289 us (1.67-1.98 PFLOP/s; their pipe 89% busy), dX and dW of it 538-600
+// 240-290 us (1.66-2.0 PFLOP/s; their pipe 89% busy), dX and dW of it 514-600
 // us (80% busy), the longer times with the card at its power cap, where a
 // plain library product of the forward's size takes 268.
 #include "compute_device.cuh"
@@ -42,7 +42,7 @@ constexpr size_t kSmem = 1024 + kStages * kStage + kAllBoxes * kBox;
 // Eight warps read finished sums, each 32 rows of one half of the columns:
 // with a short contraction there is little of the next tile's sum to do it
 // behind (64 tokens of the 8B-shaped block: dW 70 us with four, 52 with
-// eight).
+// eight, 49 with two boxes of results behind one fence).
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpiWarps;
 constexpr int kBoxes = kAllBoxes / kEpiWarps;
