@@ -352,6 +352,33 @@ def test_no_tokens_give_zero_gradients(compute):
     assert (dwg.view == 0).all() and (dwu.view == 0).all() and dwg.intact() and dwu.intact()
 
 
+def test_sums_of_nothing(compute):
+    """No hidden features: h and the gradients of the pre-activations are those
+    of zeros.  No ffn features: dx is zero."""
+    tokens, ffn = 5, 136
+    h = Guarded(tokens, ffn)
+    bufs, ck = checkpoint(tokens, 0, ffn, False)
+    compute.gated_forward(tokens, 0, ffn, 0, 0, 0, h, checkpoint=ck)
+    assert (h.view == 0).all() and h.intact() and all(b.intact() for b in bufs.values())
+    assert (bufs["g8"].view.float() == 0).all() and (bufs["us"].view == 1).all()
+    dh = randn(gen(1), tokens, ffn)
+    ws = torch.empty(tide.gated_workspace_bytes(tokens, 0, ffn), dtype=torch.uint8, device="cuda")
+    h.t.fill_(1.0)
+    compute.gated_backward(tokens, 0, ffn, dh, 0, 0, 0, None, None, None, ws, h=h)
+    assert (h.view == 0).all() and h.intact()
+    hidden = 40
+    dx = Guarded(tokens, hidden, 48)
+    ws = torch.empty(tide.gated_workspace_bytes(tokens, hidden, 0), dtype=torch.uint8, device="cuda")
+    x = randn(gen(2), tokens, hidden)
+    compute.gated_backward(tokens, hidden, 0, 0, x, 0, 0, dx, None, None, ws, ld_dx=48)
+    assert (dx.view == 0).all() and dx.intact()
+    x8, xs = Guarded(tokens, hidden, dtype=torch.float8_e4m3fn), Guarded(tokens, 1, dtype=torch.float32)
+    compute.gated_forward(tokens, hidden, 0, x, 0, 0, 0, checkpoint=tide.GatedCheckpoint(0, 0, 0, 0, x8, xs))
+    codes, scales = ref.blocks_store(x.float().cpu(), 1)
+    assert torch.equal(xs.view.cpu(), scales) and x8.intact() and xs.intact()
+    same_codes(x8.view.cpu(), codes)
+
+
 def test_nan_and_infinity_stay_in_their_token(compute):
     """A token that holds NaN or infinities spoils its own row of h only, and
     its checkpoint shows them as NaN."""
