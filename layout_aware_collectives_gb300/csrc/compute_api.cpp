@@ -222,7 +222,7 @@ tide_status_t tide_fp8_matmul(tide_compute_t c, int64_t m, int64_t n, int64_t k,
   const MatmulArgs args{m, n, k, a, a_scales, b, b_scales, out, ld_out, any_scales != 0};
   if (k % 16 == 0 && n % 8 == 0 && ld_out % 8 == 0) {
     const TcLaunch l = launch_of(c);
-    return launched(fp8_few_takes(args, l.sms) ? launch_fp8_matmul_few(args, l, stream)
+    return launched(fp8_few_takes(args, l) ? launch_fp8_matmul_few(args, l, stream)
                                                  : launch_fp8_matmul_tc(args, l, stream),
                     "tide_fp8_matmul");
   }

@@ -130,11 +130,13 @@ cudaError_t launch_gated_back_tc(const GatedArgs& a, bool dx, bool dw, bool dx_b
 
 // Tensor-core product of 8-bit blocks (fp8_tc.cu): k a multiple of 16, n and
 // the output's stride of 8.
+// Pairs of CTAs that share a tile's contraction there.
+int fp8_tc_split(const MatmulArgs& a);
 cudaError_t launch_fp8_matmul_tc(const MatmulArgs& a, const TcLaunch& l, cudaStream_t stream);
 
 // The same two products for few tokens (few_tc.cu).
 bool gated_few_takes(const GatedArgs& a, int sms);
-bool fp8_few_takes(const MatmulArgs& a, int sms);
+bool fp8_few_takes(const MatmulArgs& a, const TcLaunch& l);
 cudaError_t launch_gated_grad_few(const GatedArgs& a, const TcLaunch& l, cudaStream_t stream);
 bool gated_dx_few_takes(const GatedArgs& a, const TcLaunch& l);
 // beside: straight after launch_gated_back_tc's dW on this stream, and beside it.

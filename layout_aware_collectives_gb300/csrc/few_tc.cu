@@ -72,12 +72,6 @@ struct Params {
   uint64_t limit_ns, stall_ns;
 };
 
-__device__ __forceinline__ float4 peer_read(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
-  return v;
-}
-
 // Sums of the cluster's CTAs' sums at N addresses, in rank order.  Four ranks'
 // reads are on their way before the first is added.  (split: 2, 4 or 8.)
 template <int N>
@@ -491,7 +485,7 @@ cudaError_t few_tc_prepare() {
 // for the gated block from about half as many of these tiles as SMs (1021 x
 // 2048 x 768, 96 tiles: 13.2 us against 19.6; 512 tokens, 48 tiles: 13.0
 // against 11.7), for the 8-bit product from two thirds (128 x 28672 x 8192,
-// 128 tiles: 76 us against 87; 1021 x 2048 x 768: 9.6 against 9.1).
+// 128 tiles: 76 us against 87).
 bool gated_few_takes(const GatedArgs& a, int sms) { return few(a.tokens, a.ffn, sms / 2); }
 // dX up to 64 tokens, and for more where it has few tiles and dW's leave SMs
 // for it (500 x 1024 x 1024, 64 tiles: 26.1 us for the backward pass against
@@ -514,7 +508,16 @@ bool gated_dx_few_takes(const GatedArgs& a, const TcLaunch& l) {
   return a.tokens <= 512 && few(a.tokens, a.hidden, 32) && 2 * ceil_div(a.ffn, 256) * ceil_div(a.hidden, 256) <= l.pairs;
 }
 
-bool fp8_few_takes(const MatmulArgs& a, int sms) { return few(a.m, a.n, 2 * sms / 3); }
+// Past 64 tokens also by time: in microseconds here 0.35 a stage and 3 more, or
+// 4.5 where clusters split it, in 256-row tiles 0.33 and 4, or 8 (209 x 2368 x
+// 7904: 16.8 us here, 13.3 there; 532 x 656 x 16480 28.8 and 17.5; 256 x 1024
+// x 4096 7.6 and 9.9; 300 x 304 x 25008 14.6 and 25).
+bool fp8_few_takes(const MatmulArgs& a, const TcLaunch& l) {
+  if (a.m <= 64 || !few(a.m, a.n, 2 * l.sms / 3)) return few(a.m, a.n, 0);
+  const int64_t steps = ceil_div(a.k, kRowBytes);
+  const int split = split_of<kFp8, 64, 0>(ceil_div(a.m, 64) * ceil_div(a.n, kRows), steps, l.sms), there = fp8_tc_split(a);
+  return 0.35 * steps / split + (split > 1 ? 4.5 : 3) <= 0.33 * steps / there + (there > 1 ? 8 : 4);
+}
 
 cudaError_t launch_gated_forward_few(const GatedArgs& a, const TcLaunch& l, cudaStream_t stream) {
   Params p{};

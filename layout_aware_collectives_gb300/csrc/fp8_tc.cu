@@ -48,6 +48,9 @@ struct Params {
   TileGrid grid;
   int tiles;
   int blocks;  // of the contraction
+  int split;   // pairs of a cluster, which share its blocks
+  uint16_t* to;  // out and its rows' length
+  int64_t ldo;
   int* err;
   uint64_t limit_ns, stall_ns;
 };
@@ -235,9 +238,17 @@ constexpr int kScales = 416;
 constexpr int kScaledThreads = 384;  // loads, MMAs, -, -, 4 warps of results, 4 of scales
 constexpr int kScaledBoxes = 3;
 constexpr size_t kScaledSmem = 1024 + kStages * kStage + 4 * kScaledBoxes * kBox;
+constexpr uint32_t kSumRow = 2 * kHalf * 4;  // a row of fp32 sums
+static_assert(kHalf * kSumRow <= kStages * kStage, "the sums lie where the stages were");
 
-__global__ void __cluster_dims__(2, 1, 1)
-    __launch_bounds__(kScaledThreads, 1) scaled_kernel(const __grid_constant__ Params p) {
+// SPLIT: where the tiles leave SMs without work, a cluster of two to four
+// pairs works on one, each pair on a part of the contraction; the sums meet
+// over distributed shared memory, in the order of the parts (1024 x 1024 x
+// 8192, 16 tiles: 25.2 us by single pairs, 14.9 in threes and fours;
+// 1021 x 768 x 2048, 12 tiles: 9.7, in twos 8.9).  A stage takes 0.33 us, the
+// sums' meeting some 4.
+template <bool SPLIT>
+__global__ void __launch_bounds__(kScaledThreads, 1) scaled_kernel(const __grid_constant__ Params p) {
   constexpr uint32_t kInstr = instr_desc_scaled(256, 256);
   extern __shared__ uint8_t raw[];
   __shared__ uint64_t bars[2 * kStages + 3];
@@ -251,8 +262,11 @@ __global__ void __cluster_dims__(2, 1, 1)
   const auto empty = [&](int s) { return bar0 + 8u * (kStages + s); };
   const uint32_t sums_full = bar0 + 8u * (2 * kStages), sums_empty = sums_full + 8, spare = sums_full + 16;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_rank();
-  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const uint32_t cta = cluster_rank(), rank = cta & 1, leader = SPLIT ? cta & ~1u : 0;
+  const uint16_t both = (uint16_t)(3u << leader);  // the pair's CTAs
+  const int split = SPLIT ? p.split : 1, part = cta >> 1;
+  const int pair = blockIdx.x / (2 * split), pairs = gridDim.x / (2 * split);
+  const int k0 = SPLIT ? p.blocks * part / split : 0, k1 = SPLIT ? p.blocks * (part + 1) / split : p.blocks;
   const Watch watch{&stop, p.err, p.limit_ns};
 
   if (threadIdx.x == 0) {
@@ -271,6 +285,26 @@ __global__ void __cluster_dims__(2, 1, 1)
   const uint32_t tmem = tmem_at;
   after_previous();
 
+  // SPLIT: half of the columns' sums of this warp's 32 rows into the stages'
+  // memory, which the products have read by then.  Piece c (16 bytes) of row
+  // r lies at c ^ (r % 8).
+  const auto leave_sums = [&](uint32_t first) {
+    if (!bar_wait_warp(sums_full, 0, watch)) return;
+    fence_after();
+    const uint32_t lanes = (uint32_t)(warp & 3) * 32, to = smem + (lanes + lane) * kSumRow, turn = lane & 7;
+#pragma unroll 1
+    for (uint32_t c = first; c < first + 4; ++c) {
+      uint32_t v[32];
+      tmem_read(tmem + (lanes << 16) + c * 32, v);
+#pragma unroll
+      for (uint32_t q = 0; q < 8; ++q)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + (((c * 8 + q) ^ turn) << 4)), "r"(v[4 * q]),
+                     "r"(v[4 * q + 1]), "r"(v[4 * q + 2]), "r"(v[4 * q + 3])
+                     : "memory");
+    }
+    fence_before();
+  };
+
   if (p.stall_ns) {  // test: a wait on a barrier nothing arrives on runs out
     if (threadIdx.x == 0) bar_wait(spare, 0, Watch{&stop, p.err, p.stall_ns});
   } else if (warp == 0 || warp == 3) {
@@ -280,14 +314,14 @@ __global__ void __cluster_dims__(2, 1, 1)
       bool go = true;
       for (int t = pair; t < p.tiles && go; t += pairs) {
         const TileAt at = tile_at(p.grid, t);
-        for (int k = 0; k < p.blocks; ++k, ++j) {
+        for (int k = k0; k < k1; ++k, ++j) {
           const int s = j % kStages;
           if (j >= kStages && !bar_wait(empty(s), (j / kStages + 1) & 1, watch)) {
             go = false;
             break;
           }
           if (load_a && rank == 0) bar_expect(full(s), 2 * kStage);
-          const uint32_t bar = peer_addr(full(s), 0);
+          const uint32_t bar = peer_addr(full(s), leader);
           const uint32_t a = smem + s * kStage;
           if (load_a)
             load_box<true>(a, &p.a, k * kBlock, (at.m * 2 + rank) * kHalf, bar);
@@ -313,7 +347,7 @@ __global__ void __cluster_dims__(2, 1, 1)
         if (i > 0 && !bar_wait(sums_empty, (i + 1) & 1, watch)) break;
         fence_after();
         const uint32_t sums = tmem + (i & 1) * kOdd;
-        for (int k = 0; k < p.blocks; ++k, ++j) {
+        for (int k = k0; k < k1; ++k, ++j) {
           const int s = j % kStages;
           if (!bar_wait(full(s), (j / kStages) & 1, watch)) {
             go = false;
@@ -324,14 +358,14 @@ __global__ void __cluster_dims__(2, 1, 1)
           const uint64_t da = operand_desc(a, 16), db = operand_desc(a + kOperand, 16);
 #pragma unroll
           for (int q = 0; q < kBlock / 32; ++q)
-            mma_scaled(sums, da + q * 2, db + q * 2, kInstr, scales, scales + 4, k > 0 || q > 0);
-          mma_commit<2>(empty(s));
+            mma_scaled(sums, da + q * 2, db + q * 2, kInstr, scales, scales + 4, k > k0 || q > 0);
+          mma_commit<2>(empty(s), both);
         }
-        if (go) mma_commit<2>(sums_full);
+        if (go) mma_commit<2>(sums_full, both);
       }
       if (*watch.stop) {  // the MMAs in flight, with a limit
         int never = 0;
-        mma_commit<2>(spare);
+        mma_commit<2>(spare, both);
         bar_wait(spare, 0, Watch{&never, p.err, p.limit_ns / 16});
       }
     }
@@ -354,23 +388,23 @@ __global__ void __cluster_dims__(2, 1, 1)
       const auto fetch = [&](int k) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          next_a[q] = __ldg(sa + min(k + q, p.blocks - 1));
-          next_b[q] = __ldg(sb + min(k + q, p.blocks - 1));
+          next_a[q] = __ldg(sa + min(k + q, k1 - 1));
+          next_b[q] = __ldg(sb + min(k + q, k1 - 1));
         }
       };
-      fetch(0);
-      for (int k = 0; k < p.blocks; k += 4, ++batch) {
+      fetch(k0);
+      for (int k = k0; k < k1; k += 4, ++batch) {
         uint32_t b[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           words[batch & 1][q][w * 32 + lane] = exponent_bytes(next_a[q]);
           b[q] = exponent_bytes(next_b[q]);
         }
-        if (k + 4 < p.blocks) fetch(k + 4);
+        if (k + 4 < k1) fetch(k + 4);
         asm volatile("bar.sync 1, 128;" ::: "memory");
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          if (k + q >= p.blocks) break;
+          if (k + q >= k1) break;
           const int s = j % kStages;
           // a warp whose wait ran out goes on meeting the others at the barrier
           go = go && (j < kStages || bar_wait_warp(empty(s), (j / kStages + 1) & 1, watch));
@@ -385,16 +419,18 @@ __global__ void __cluster_dims__(2, 1, 1)
           tmem_written();
           fence_before();
           __syncwarp();
-          if (lane == 0) bar_arrive_peer(peer_addr(full(s), 0));
+          if (lane == 0) bar_arrive_peer(peer_addr(full(s), leader));
           ++j;
         }
       }
     }
+    if constexpr (SPLIT) leave_sums(4);
   } else if (warp >= 4) {
+    if constexpr (SPLIT) leave_sums(0);
     Outbox<kScaledBoxes> out{smem + kStages * kStage + (warp - 4) * kScaledBoxes * kBox, 0, lane};
     const uint32_t lanes = (uint32_t)(warp - 4) * 32;
     int i = 0;
-    for (int t = pair; t < p.tiles; t += pairs, ++i) {
+    for (int t = pair; t < p.tiles && !SPLIT; t += pairs, ++i) {
       if (!bar_wait_warp(sums_full, i & 1, watch)) break;
       fence_after();
       const TileAt at = tile_at(p.grid, t);
@@ -411,7 +447,7 @@ __global__ void __cluster_dims__(2, 1, 1)
       }
       fence_before();
       __syncwarp();
-      if (lane == 0) bar_arrive_peer(peer_addr(sums_empty, 0));
+      if (lane == 0) bar_arrive_peer(peer_addr(sums_empty, leader));
 #pragma unroll
       for (int c = 0; c < kShared; ++c) {
         const int col = col0 + (first + c) * 32;
@@ -433,15 +469,55 @@ __global__ void __cluster_dims__(2, 1, 1)
   }
   __syncthreads();
   cluster_sync();
+  if constexpr (SPLIT) {
+    // Each CTA finishes its share of the pair's rows.
+    const TileAt at = tile_at(p.grid, pair);
+    const int row0 = (at.m * 2 + rank) * kHalf, col0 = at.n * 2 * kHalf + lane * 4;
+    const int r1 = min(kHalf * (part + 1) / split, p.rows - row0);
+    if (!p.stall_ns) {
+      for (int r = kHalf * part / split + warp; r < r1; r += kScaledThreads / 32) {
+        const uint32_t from = smem + r * kSumRow + ((lane ^ (r & 7)) << 4);
+        float4 v[kMaxSplit][2];
+#pragma unroll
+        for (int q = 0; q < kMaxSplit; ++q)
+          if (q < split) {
+            const uint32_t a = peer_addr(from, 2 * q + rank);
+            v[q][0] = peer_read(a), v[q][1] = peer_read(a + kSumRow / 2);
+          }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float4 sum = v[0][c];
+#pragma unroll
+          for (int q = 1; q < kMaxSplit; ++q)
+            if (q < split) sum.x += v[q][c].x, sum.y += v[q][c].y, sum.z += v[q][c].z, sum.w += v[q][c].w;
+          const int col = col0 + c * kHalf;
+          if (col < p.cols)
+            *(uint2*)(p.to + (int64_t)(row0 + r) * p.ldo + col) = make_uint2(pack_bf16(sum.x, sum.y), pack_bf16(sum.z, sum.w));
+        }
+      }
+    }
+    cluster_sync();  // the others have read this CTA's sums
+  }
   if (warp == 2) tmem_free<2>(tmem, 512);
 }
+
+PairClusters clusters;  // of scaled_kernel<true>
 
 }  // namespace
 
 cudaError_t fp8_tc_prepare() {
-  const cudaError_t e = cudaFuncSetAttribute(summed_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(scaled_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kScaledSmem);
+  cudaError_t e = cudaFuncSetAttribute(summed_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(scaled_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kScaledSmem);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(scaled_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kScaledSmem);
+  if (e == cudaSuccess) e = clusters.prepare((const void*)scaled_kernel<true>, kScaledThreads, kScaledSmem);
+  return e;
+}
+
+int fp8_tc_split(const MatmulArgs& a) {
+  if (a.any_scales) return 1;
+  return clusters.split(ceil_div(a.m, 2 * kHalf) * ceil_div(a.n, 2 * kHalf), ceil_div(a.k, kBlock));
 }
 
 cudaError_t launch_fp8_matmul_tc(const MatmulArgs& a, const TcLaunch& l, cudaStream_t stream) {
@@ -451,6 +527,7 @@ cudaError_t launch_fp8_matmul_tc(const MatmulArgs& a, const TcLaunch& l, cudaStr
   p.grid = TileGrid((int)ceil_div(a.m, 2 * kHalf), (int)ceil_div(a.n, 2 * kHalf));
   p.tiles = p.grid.all.d;
   p.blocks = (int)ceil_div(a.k, kBlock);
+  p.to = a.out, p.ldo = a.ldo;
   p.err = l.err;
   p.limit_ns = TIDE_BULK_TIMEOUT_NS;
   p.stall_ns = l.stall_ns;
@@ -459,8 +536,11 @@ cudaError_t launch_fp8_matmul_tc(const MatmulArgs& a, const TcLaunch& l, cudaStr
       !make_map(&p.out, a.out, 2, a.n, a.m, a.ldo, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
     return cudaErrorInvalidValue;
   const int pairs = p.tiles < l.pairs ? p.tiles : l.pairs;
+  p.split = fp8_tc_split(a);
+  if (p.split > 1)
+    return launch_early(scaled_kernel<true>, dim3(2 * p.split * p.tiles), kScaledThreads, kScaledSmem, 2 * p.split, stream, p);
   return a.any_scales ? launch_early(summed_kernel, dim3(2 * pairs), kThreads, kSmem, 0, stream, p)
-                      : launch_early(scaled_kernel, dim3(2 * pairs), kScaledThreads, kScaledSmem, 0, stream, p);
+                      : launch_early(scaled_kernel<false>, dim3(2 * pairs), kScaledThreads, kScaledSmem, 2, stream, p);
 }
 
 }  // namespace tide

@@ -26,6 +26,12 @@ __device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
   return r;
 }
 
+__device__ __forceinline__ float4 peer_read(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+  return v;
+}
+
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -228,14 +234,14 @@ __device__ __forceinline__ void tmem_write4(uint32_t addr, uint32_t a, uint32_t 
 }
 __device__ __forceinline__ void tmem_written() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Arrives on `bar` (at this address in both CTAs of a pair) once the MMAs
-// issued so far have completed.
+// Arrives on `bar` (at this address in both CTAs of a pair, `ctas` being
+// their bits among the cluster's) once the MMAs issued so far have completed.
 template <int GROUP>
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
+__device__ __forceinline__ void mma_commit(uint32_t bar, uint16_t ctas = 3) {
   if constexpr (GROUP == 2)
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"((uint16_t)3)
+        "h"(ctas)
         : "memory");
   else
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");

@@ -44,4 +44,21 @@ bool make_slab_map(CUtensorMap* map, const void* p, int64_t cols, int64_t rows, 
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+cudaError_t PairClusters::prepare(const void* kernel, int threads, size_t smem) {
+  for (int s = 2; s <= kMaxSplit; ++s) {
+    cudaLaunchAttribute cluster;
+    cluster.id = cudaLaunchAttributeClusterDimension;
+    cluster.val.clusterDim = {2u * s, 1, 1};
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3(2 * s);
+    c.blockDim = dim3(threads);
+    c.dynamicSmemBytes = smem;
+    c.attrs = &cluster;
+    c.numAttrs = 1;
+    const cudaError_t e = cudaOccupancyMaxActiveClusters(&held[s], kernel, &c);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
 }  // namespace tide

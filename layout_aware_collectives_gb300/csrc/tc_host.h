@@ -48,4 +48,21 @@ struct TileGrid {
       : tiles_m(m), tiles_n(n), all(m * n), band(kBand * n), last(m % kBand ? m % kBand : kBand) {}
 };
 
+// Clusters of 2 to 4 pairs of CTAs that work on one tile, each pair on a part
+// of its contraction.  A cluster lies within one GPC, so the device holds
+// fewer than it has SMs by their size.
+constexpr int kMaxSplit = 4;
+struct PairClusters {
+  int held[kMaxSplit + 1];  // at one time, of so many pairs
+
+  cudaError_t prepare(const void* kernel, int threads, size_t smem);
+  // Pairs for a tile: as many as all tiles find at one time, each with at
+  // least eight stages, or 1.
+  int split(int64_t tiles, int64_t stages) const {
+    int s = kMaxSplit;
+    while (s > 1 && (held[s] < tiles || stages < 8 * s)) --s;
+    return s;
+  }
+};
+
 }  // namespace tide

@@ -154,6 +154,46 @@ def test_matmul(compute, m, n, k, pad, any_scales):
     assert out.intact()
 
 
+# few tiles and a long contraction: split in two, three and four
+@pytest.mark.parametrize("m,n,k", [(1014, 752, 9200), (200, 2368, 7904), (1100, 1000, 3216), (1500, 1288, 2064), (65, 8192, 2176)])
+@pytest.mark.parametrize("pad", [0, 8])
+def test_matmul_split(compute, m, n, k, pad):
+    g = gen(m + n + k)
+    (a, sa), (b, sb) = fp8(g, m, k, 1), fp8(g, n, k, 128)
+    out = Guarded(m, n, n + pad)
+    compute.fp8_matmul(m, n, k, a, sa, b, sb, out, ld_out=n + pad)
+    close(out.view, *ref.matmul(a, sa, b, sb))
+    assert out.intact()
+    first = out.view.clone()
+    for _ in range(3):
+        compute.fp8_matmul(m, n, k, a, sa, b, sb, out, ld_out=n + pad)
+        assert torch.equal(out.view, first)
+    sa[m - 1, -1] = 1.5  # no power of two
+    a.view(torch.uint8)[3, k - 1] = 0x7F
+    compute.fp8_matmul(m, n, k, a, sa, b, sb, out, ld_out=n + pad)
+    nan = torch.zeros(m, n, dtype=torch.bool, device="cuda")
+    nan[m - 1], nan[3] = True, True
+    assert torch.equal(torch.isnan(out.view), nan) and torch.equal(out.view[:3], first[:3])
+
+
+def test_matmul_split_wait_that_runs_out_is_reported():
+    m, n, k = 1014, 752, 9200
+    g = gen(31)
+    (a, sa), (b, sb) = fp8(g, m, k, 1), fp8(g, n, k, 128)
+    out = Guarded(m, n)
+    with tide.Compute() as c:
+        c.set_test_stall(1_000_000)
+        c.fp8_matmul(m, n, k, a, sa, b, sb, out)
+        with pytest.raises(tide.TideError) as e:
+            c.check_device()
+        assert e.value.status == tide.TIDE_ERR_TIMEOUT
+        c.set_test_stall(0)
+        c.fp8_matmul(m, n, k, a, sa, b, sb, out)
+        c.check_device()
+        close(out.view, *ref.matmul(a, sa, b, sb))
+        assert out.intact()
+
+
 @pytest.mark.parametrize("m,n,k", [(3, 264, 512), (300, 5000, 272), (5, 130, 129)])
 @pytest.mark.parametrize("bad", [1.5, 0.0, -2.0, math.inf, math.nan, 1e-40])
 def test_matmul_scale_that_is_no_power_of_two(compute, m, n, k, bad):
