@@ -253,7 +253,7 @@ tide_status_t tide_gated_forward(tide_compute_t c, int64_t tokens, int64_t hidde
   if (ffn == 0) return TIDE_OK;
   if (gated_tc_takes(a) && ld_x % 8 == 0 && ld_h % 8 == 0) {
     const TcLaunch l = launch_of(c);
-    return launched(gated_few_takes(a, l.sms) ? launch_gated_forward_few(a, l, stream)
+    return launched(gated_few_takes(a, l) ? launch_gated_forward_few(a, l, stream)
                                                 : launch_gated_forward_tc(a, l, stream),
                     "tide_gated_forward");
   }
@@ -328,7 +328,7 @@ tide_status_t tide_gated_backward(tide_compute_t c, int64_t tokens, int64_t hidd
   if (ck)
     TIDE_TRY(launched(launch_gated_grad_stored(a, xr, stream), what));
   else if (tc && ld_x % 8 == 0 && ld_dh % 8 == 0 && (!h || ld_h % 8 == 0))
-    TIDE_TRY(launched(gated_few_takes(a, l.sms) ? launch_gated_grad_few(a, l, stream) : launch_gated_grad_tc(a, l, stream), what));
+    TIDE_TRY(launched(gated_few_takes(a, l) ? launch_gated_grad_few(a, l, stream) : launch_gated_grad_tc(a, l, stream), what));
   else
     TIDE_TRY(launched(launch_gated_grad_simple(a, stream), what));
   if (hidden == 0) return TIDE_OK;

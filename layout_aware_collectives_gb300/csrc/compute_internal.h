@@ -118,6 +118,8 @@ cudaError_t gated_tc_prepare(int* pairs);
 cudaError_t fp8_tc_prepare();
 cudaError_t few_tc_prepare();
 bool gated_tc_takes(const GatedArgs& a);
+// Pairs of CTAs that share a tile's contraction in forward and grad.
+int gated_tc_split(const GatedArgs& a);
 // Workspace for the parts of dX's and dW's sums.
 int64_t gated_dx_parts_bytes(int64_t tokens, int64_t hidden);
 int64_t gated_dw_parts_bytes(int64_t hidden, int64_t ffn);
@@ -135,7 +137,7 @@ int fp8_tc_split(const MatmulArgs& a);
 cudaError_t launch_fp8_matmul_tc(const MatmulArgs& a, const TcLaunch& l, cudaStream_t stream);
 
 // The same two products for few tokens (few_tc.cu).
-bool gated_few_takes(const GatedArgs& a, int sms);
+bool gated_few_takes(const GatedArgs& a, const TcLaunch& l);
 bool fp8_few_takes(const MatmulArgs& a, const TcLaunch& l);
 cudaError_t launch_gated_grad_few(const GatedArgs& a, const TcLaunch& l, cudaStream_t stream);
 bool gated_dx_few_takes(const GatedArgs& a, const TcLaunch& l);

@@ -18,6 +18,7 @@
 // 4-7 us of waits one after the other: the first stage's 0.6 us, 0.3 us a
 // stage, the clusters' meetings 0.7 us each.
 #include "compute_device.cuh"
+#include "gated_finish.cuh"
 #include "tc_device.cuh"
 #include "tc_host.h"
 
@@ -50,21 +51,12 @@ struct Shape {
   static constexpr size_t kSmem = 1024 + (kStages * kStage > kSums ? kStages * kStage : kSums);
 };
 
-struct Params {
+struct Params : GatedOut {  // 8-bit product, dX: out, ldo and features of it
   CUtensorMap w[2], x[2];
-  int tokens, features, steps, step_elems;
+  int tokens, steps, step_elems;
   int half_steps;  // dX: stages of dG's half
   bool one_box;    // dX: a stage's weights are one box of two slabs
   bool beside;     // dX: runs beside the kernel ahead of it
-  // gated
-  uint16_t* out;
-  int64_t ldo;
-  uint8_t *g8, *u8;
-  float *gs, *us;
-  // grad
-  const uint16_t* dh;
-  int64_t lddh;
-  uint16_t *dg, *du;
   // 8-bit
   const float *sx, *sw;
   bool any_scales;
@@ -100,26 +92,6 @@ __device__ __forceinline__ float4 own_read(uint32_t addr) {
 }
 
 __device__ __forceinline__ void sums_barrier() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-
-__device__ __forceinline__ float warp_amax(const float4& v) {
-  float m = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
-#pragma unroll
-  for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-  return m;
-}
-
-// 4 codes a lane, one scale a warp: this lane's part of a token's block.
-__device__ __forceinline__ void put_block(float4 v, uint8_t* codes, float* scale, int lane, bool in) {
-  float amax = warp_amax(v);
-  if (amax == CUDART_INF_F) {
-    v = make_float4(no_infinity(v.x), no_infinity(v.y), no_infinity(v.z), no_infinity(v.w));
-    amax = warp_amax(v);
-  }
-  const uint32_t e = scale_exponent(amax);
-  const float inv = exponent_inverse(e);
-  if (in) *(uint32_t*)codes = pack_e4m3x4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
-  if (lane == 0) *scale = exponent_value(e);
-}
 
 template <int KIND, int NT, int ACT>
 __global__ void __launch_bounds__(kThreads) few_tc_kernel(const __grid_constant__ Params p) {
@@ -308,40 +280,16 @@ __global__ void __launch_bounds__(kThreads) few_tc_kernel(const __grid_constant_
   if (!p.stall_ns) {
     constexpr int kWarps = kThreads / 32;
     const int col = feature0 + lane * 4;
-    const bool in = col < p.features;
-    const int64_t nb = (p.features + kBlock - 1) / kBlock;
     const int live = min(NT, p.tokens - token0);
     // One token's results from its sums.
     const auto finish = [&](int t, const float4* v) {
       const int64_t token = token0 + t;
-      float4 r = v[0];
-      if constexpr (KIND == kGrad) {
-        if (!in) return;
-        const uint2 dh = *(const uint2*)(p.dh + token * p.lddh + col);
-        const float d[4] = {bf16_lo(dh.x), bf16_hi(dh.x), bf16_lo(dh.y), bf16_hi(dh.y)};
-        const float g[4] = {v[0].x, v[0].y, v[0].z, v[0].w}, u[4] = {v[1].x, v[1].y, v[1].z, v[1].w};
-        float dg[4], du[4], h[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 s = activation_grad<ACT>(g[i]);
-          dg[i] = d[i] * u[i] * s.y, du[i] = d[i] * s.x, h[i] = s.x * u[i];
-        }
-        const int64_t at = token * p.features + col;
-        *(uint2*)(p.dg + at) = make_uint2(pack_bf16(dg[0], dg[1]), pack_bf16(dg[2], dg[3]));
-        *(uint2*)(p.du + at) = make_uint2(pack_bf16(du[0], du[1]), pack_bf16(du[2], du[3]));
-        if (!p.out) return;
-        r = make_float4(h[0], h[1], h[2], h[3]);
-      }
-      if constexpr (KIND == kForward) {
-        const float4 a = v[0], u = v[1];
-        r.x = activation<ACT>(a.x) * u.x, r.y = activation<ACT>(a.y) * u.y;
-        r.z = activation<ACT>(a.z) * u.z, r.w = activation<ACT>(a.w) * u.w;
-        if (p.g8) {  // features past the end hold 0
-          put_block(a, p.g8 + token * p.features + col, p.gs + token * nb + blockIdx.z, lane, in);
-          put_block(u, p.u8 + token * p.features + col, p.us + token * nb + blockIdx.z, lane, in);
-        }
-      }
-      if (in) *(uint2*)(p.out + token * p.ldo + col) = make_uint2(pack_bf16(r.x, r.y), pack_bf16(r.z, r.w));
+      if constexpr (KIND == kForward)
+        finish_forward<ACT>(p, token, blockIdx.z, lane, v[0], v[1]);
+      else if constexpr (KIND == kGrad)
+        finish_grad<ACT>(p, token, blockIdx.z, lane, v[0], v[1]);
+      else if (col < p.features)
+        put_bf16(p.out + token * p.ldo + col, v[0]);
     };
     const auto sums_at = [&](int t, int q) { return smem + (uint32_t)((q * NT + t) * kRows + lane * 4) * 4; };
     constexpr int P = S::kParts;
@@ -481,12 +429,27 @@ cudaError_t few_tc_prepare() {
   return cudaSuccess;
 }
 
-// Past 64 tokens the 256-row tiles read fewer operand bytes: they are ahead
+// Past 64 tokens the 256-row tiles read fewer operand bytes; they are ahead
 // for the gated block from about half as many of these tiles as SMs (1021 x
-// 2048 x 768, 96 tiles: 13.2 us against 19.6; 512 tokens, 48 tiles: 13.0
-// against 11.7), for the 8-bit product from two thirds (128 x 28672 x 8192,
-// 128 tiles: 76 us against 87).
-bool gated_few_takes(const GatedArgs& a, int sms) { return few(a.tokens, a.ffn, sms / 2); }
+// 2048 x 768, 96 tiles: 19.6 us), for the 8-bit product from two thirds (128 x
+// 28672 x 8192, 128 tiles: 87 us, 76 there).  Below that it goes by the
+// stages of a CTA, in microseconds:
+//                    here                     256-row tiles
+//   gated            0.24 each and 3          0.265 and 4.3
+//     split          0.4 and 6.4              0.265 and 8.5
+//   8-bit            0.35 and 3               0.33 and 4
+//     split          0.35 and 4.5             0.33 and 8
+// (Gated, 209 x 7904 x 2368: 31.7 here, 21.5 there; 532 x 16480 x 656 57.4 and
+// 32; 256 x 1024 x 1024 8.0 and 8.5; 65 x 28672 x 256 29.1 and 36.  8-bit, 209
+// x 2368 x 7904: 16.8 and 13.3; 532 x 656 x 16480 28.8 and 17.5; 256 x 1024 x
+// 4096 7.6 and 9.9; 300 x 304 x 25008 14.6 and 25.)
+bool gated_few_takes(const GatedArgs& a, const TcLaunch& l) {
+  if (a.tokens <= 64 || !few(a.tokens, a.ffn, l.sms / 2)) return few(a.tokens, a.ffn, 0);
+  const int64_t steps = ceil_div(a.hidden, kRowBytes / 2);
+  const int split = split_of<kForward, 64, TIDE_ACT_SILU>(ceil_div(a.tokens, 64) * ceil_div(a.ffn, kRows), steps, l.sms);
+  const int there = gated_tc_split(a);
+  return (split > 1 ? 0.4 * steps / split + 6.4 : 0.24 * steps + 3) <= 0.265 * steps / there + (there > 1 ? 8.5 : 4.3);
+}
 // dX up to 64 tokens, and for more where it has few tiles and dW's leave SMs
 // for it (500 x 1024 x 1024, 64 tiles: 26.1 us for the backward pass against
 // 23.1 in 256-row tiles).  In microseconds, here 0.21 a stage and 3 more, in
@@ -508,10 +471,6 @@ bool gated_dx_few_takes(const GatedArgs& a, const TcLaunch& l) {
   return a.tokens <= 512 && few(a.tokens, a.hidden, 32) && 2 * ceil_div(a.ffn, 256) * ceil_div(a.hidden, 256) <= l.pairs;
 }
 
-// Past 64 tokens also by time: in microseconds here 0.35 a stage and 3 more, or
-// 4.5 where clusters split it, in 256-row tiles 0.33 and 4, or 8 (209 x 2368 x
-// 7904: 16.8 us here, 13.3 there; 532 x 656 x 16480 28.8 and 17.5; 256 x 1024
-// x 4096 7.6 and 9.9; 300 x 304 x 25008 14.6 and 25).
 bool fp8_few_takes(const MatmulArgs& a, const TcLaunch& l) {
   if (a.m <= 64 || !few(a.m, a.n, 2 * l.sms / 3)) return few(a.m, a.n, 0);
   const int64_t steps = ceil_div(a.k, kRowBytes);

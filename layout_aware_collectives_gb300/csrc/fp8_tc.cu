@@ -238,7 +238,6 @@ constexpr int kScales = 416;
 constexpr int kScaledThreads = 384;  // loads, MMAs, -, -, 4 warps of results, 4 of scales
 constexpr int kScaledBoxes = 3;
 constexpr size_t kScaledSmem = 1024 + kStages * kStage + 4 * kScaledBoxes * kBox;
-constexpr uint32_t kSumRow = 2 * kHalf * 4;  // a row of fp32 sums
 static_assert(kHalf * kSumRow <= kStages * kStage, "the sums lie where the stages were");
 
 // SPLIT: where the tiles leave SMs without work, a cluster of two to four
@@ -285,23 +284,12 @@ __global__ void __launch_bounds__(kScaledThreads, 1) scaled_kernel(const __grid_
   const uint32_t tmem = tmem_at;
   after_previous();
 
-  // SPLIT: half of the columns' sums of this warp's 32 rows into the stages'
-  // memory, which the products have read by then.  Piece c (16 bytes) of row
-  // r lies at c ^ (r % 8).
-  const auto leave_sums = [&](uint32_t first) {
+  // SPLIT: half of the columns' sums of this warp's 32 rows
+  const auto leave_half = [&](int first) {
     if (!bar_wait_warp(sums_full, 0, watch)) return;
     fence_after();
-    const uint32_t lanes = (uint32_t)(warp & 3) * 32, to = smem + (lanes + lane) * kSumRow, turn = lane & 7;
-#pragma unroll 1
-    for (uint32_t c = first; c < first + 4; ++c) {
-      uint32_t v[32];
-      tmem_read(tmem + (lanes << 16) + c * 32, v);
-#pragma unroll
-      for (uint32_t q = 0; q < 8; ++q)
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + (((c * 8 + q) ^ turn) << 4)), "r"(v[4 * q]),
-                     "r"(v[4 * q + 1]), "r"(v[4 * q + 2]), "r"(v[4 * q + 3])
-                     : "memory");
-    }
+    const uint32_t lanes = (uint32_t)(warp & 3) * 32;
+    leave_sums(smem, tmem + (lanes << 16), lanes + lane, first);
     fence_before();
   };
 
@@ -424,9 +412,9 @@ __global__ void __launch_bounds__(kScaledThreads, 1) scaled_kernel(const __grid_
         }
       }
     }
-    if constexpr (SPLIT) leave_sums(4);
+    if constexpr (SPLIT) leave_half(4);
   } else if (warp >= 4) {
-    if constexpr (SPLIT) leave_sums(0);
+    if constexpr (SPLIT) leave_half(0);
     Outbox<kScaledBoxes> out{smem + kStages * kStage + (warp - 4) * kScaledBoxes * kBox, 0, lane};
     const uint32_t lanes = (uint32_t)(warp - 4) * 32;
     int i = 0;
@@ -476,23 +464,14 @@ __global__ void __launch_bounds__(kScaledThreads, 1) scaled_kernel(const __grid_
     const int r1 = min(kHalf * (part + 1) / split, p.rows - row0);
     if (!p.stall_ns) {
       for (int r = kHalf * part / split + warp; r < r1; r += kScaledThreads / 32) {
-        const uint32_t from = smem + r * kSumRow + ((lane ^ (r & 7)) << 4);
-        float4 v[kMaxSplit][2];
-#pragma unroll
-        for (int q = 0; q < kMaxSplit; ++q)
-          if (q < split) {
-            const uint32_t a = peer_addr(from, 2 * q + rank);
-            v[q][0] = peer_read(a), v[q][1] = peer_read(a + kSumRow / 2);
-          }
+        float4 sum[2];
+        split_sums(smem, r, lane, rank, split, sum);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          float4 sum = v[0][c];
-#pragma unroll
-          for (int q = 1; q < kMaxSplit; ++q)
-            if (q < split) sum.x += v[q][c].x, sum.y += v[q][c].y, sum.z += v[q][c].z, sum.w += v[q][c].w;
           const int col = col0 + c * kHalf;
           if (col < p.cols)
-            *(uint2*)(p.to + (int64_t)(row0 + r) * p.ldo + col) = make_uint2(pack_bf16(sum.x, sum.y), pack_bf16(sum.z, sum.w));
+            *(uint2*)(p.to + (int64_t)(row0 + r) * p.ldo + col) =
+                make_uint2(pack_bf16(sum[c].x, sum[c].y), pack_bf16(sum[c].z, sum[c].w));
         }
       }
     }
@@ -517,7 +496,7 @@ cudaError_t fp8_tc_prepare() {
 
 int fp8_tc_split(const MatmulArgs& a) {
   if (a.any_scales) return 1;
-  return clusters.split(ceil_div(a.m, 2 * kHalf) * ceil_div(a.n, 2 * kHalf), ceil_div(a.k, kBlock));
+  return clusters.split(ceil_div(a.m, 2 * kHalf) * ceil_div(a.n, 2 * kHalf), ceil_div(a.k, kBlock), 16);
 }
 
 cudaError_t launch_fp8_matmul_tc(const MatmulArgs& a, const TcLaunch& l, cudaStream_t stream) {

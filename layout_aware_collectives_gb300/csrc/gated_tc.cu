@@ -22,6 +22,7 @@
 // us (80% busy), the longer times with the card at its power cap, where a
 // plain library product of the forward's size takes 268.
 #include "compute_device.cuh"
+#include "gated_finish.cuh"
 #include "tc_device.cuh"
 #include "tc_host.h"
 
@@ -57,16 +58,18 @@ struct Share {
   __device__ __forceinline__ int from(int z) const { return z * least + min(z, more); }
 };
 
-struct Params {
+struct Params : GatedOut {  // of forward and grad
   // forward, grad: a = x, b = Wg, Wu; out = h, or dG, dU, h
   // back: dX: a = dG, dU, b = Wg, Wu, out[0]; dW: wa = dG, dU, wb = x, out[1..2]
-  CUtensorMap a[2], b[2], wa[2], wb, out[3];
+  CUtensorMap a[2], b[2], wa[2], wb, outs[3];
   int rows, cols;  // of the outputs (back: of dX)
   TileGrid grid;
   int tiles;
   int steps;       // stages of one tile's sum
   int half_steps;  // back: stages of dX's first half
-  int split, w_split;  // back: parts of dX's and of dW's sums, each in its own tile
+  // back: parts of dX's and of dW's sums, each in its own tile; forward,
+  // grad: pairs of a cluster
+  int split, w_split;
   Share share, w_share;
   float *parts, *w_parts;  // of [split, cols, rows], [w_split, half, cols, w_rows], where there are several
   TileGrid w_grid;
@@ -76,12 +79,6 @@ struct Params {
   // many that is for each, and how many have one more
   int each, full, light, first, first_each, first_more;
   bool one_a, one_b;  // back: wa's, b's and wb's operands are one box each (map_mn)
-  // epilogue
-  uint8_t *g8, *u8;
-  float *gs, *us;
-  const uint16_t* dh;
-  int64_t lddh;
-  bool with_h;
   int* err;
   uint64_t limit_ns, stall_ns;
 };
@@ -133,13 +130,13 @@ struct Work {
 // even, the pairs that are one short take as many tiles of dW as one of dX is
 // worth before the rest goes round, beginning with them again.
 template <int FORM>
-__device__ __forceinline__ bool work_at(const Params& p, int pair, int pairs, int i, Work& r) {
+__device__ __forceinline__ bool work_at(const Params& p, int pair, int pairs, int part, int i, Work& r) {
   int t = pair + i * pairs;
   r.w = false;
   if (FORM != kBack) {
     if (t >= p.tiles) return false;
     r.at = tile_at(p.grid, t);
-    r.k0 = 0, r.k1 = p.steps;
+    r.k0 = p.share.from(part), r.k1 = p.share.from(part + 1);
     return true;
   }
   if (t < p.tiles) {
@@ -243,7 +240,7 @@ __device__ __forceinline__ void epilogue(const Params& p, const Work& work, uint
         for (int i = 0; i < 16; ++i)
           o[i] = pack_bf16(activation<ACT>(as_f(g[2 * i])) * as_f(u[2 * i]),
                            activation<ACT>(as_f(g[2 * i + 1])) * as_f(u[2 * i + 1]));
-        out.put(&p.out[0], o, col, row0);
+        out.put(&p.outs[0], o, col, row0);
       } else {
         uint32_t o1[16], o2[16];
 #pragma unroll
@@ -264,12 +261,12 @@ __device__ __forceinline__ void epilogue(const Params& p, const Work& work, uint
             o2[i] = pack_bf16(t0.x * u0, t1.x * u1);
           }
         }
-        out.put2(&p.out[0], o, col, &p.out[1], o1, col, row0);
-        if (p.with_h) out.put(&p.out[2], o2, col, row0);
+        out.put2(&p.outs[0], o, col, &p.outs[1], o1, col, row0);
+        if (p.out) out.put(&p.outs[2], o2, col, row0);
       }
     }
   } else {
-    const CUtensorMap* map = &p.out[work.w ? 1 + work.half : 0];
+    const CUtensorMap* map = &p.outs[work.w ? 1 + work.half : 0];
 #pragma unroll 1
     for (int c = half * 4; c < half * 4 + 4; c += 2) {
       const int col = t.n * 2 * kHalf + c * 32;
@@ -297,8 +294,14 @@ __device__ __forceinline__ void epilogue(const Params& p, const Work& work, uint
   }
 }
 
-template <int FORM, int ACT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_constant__ Params p) {
+// SPLIT (forward, grad): where the tiles leave SMs without work, a cluster of
+// two to four pairs works on one, each pair on a part of the contraction; the
+// sums meet over distributed shared memory, in the order of the parts (512 x
+// 7168 x 2048, 32 tiles: 34.8 us by single pairs, 24.5 in twos; 532 x 16480 x
+// 656, 18 tiles: 72.7 and, in threes, 32).  A stage takes 0.27 us, the sums'
+// meeting some 4.
+template <int FORM, int ACT, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_constant__ Params p) {
   constexpr bool kBMn = FORM == kBack;
   extern __shared__ uint8_t raw[];
   __shared__ uint64_t bars[2 * kStages + 5];
@@ -314,8 +317,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gated_t
   const auto sums_empty = [&](int b) { return bar0 + 8u * (2 * kStages + 2 + b); };
   const uint32_t spare = bar0 + 8u * (2 * kStages + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_rank();
-  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const uint32_t cta = cluster_rank(), rank = cta & 1, leader = SPLIT ? cta & ~1u : 0;
+  const uint16_t both = (uint16_t)(3u << leader);  // the pair's CTAs
+  const int split = SPLIT ? p.split : 1, part = SPLIT ? cta >> 1 : 0;
+  const int pair = blockIdx.x / (2 * split), pairs = gridDim.x / (2 * split);
   const Watch watch{&stop, p.err, p.limit_ns};
 
   if (threadIdx.x == 0) {
@@ -344,7 +349,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gated_t
       int j = 0;  // stages filled so far
       bool go = true;
       Work work;
-      for (int i = 0; go && work_at<FORM>(p, pair, pairs, i, work); ++i) {
+      for (int i = 0; go && work_at<FORM>(p, pair, pairs, part, i, work); ++i) {
         const TileAt& at = work.at;
         const int row = (at.m * 2 + rank) * kHalf, col = (at.n * 2 + rank) * kHalf;
         for (int k = work.k0; k < work.k1; ++k, ++j) {
@@ -354,7 +359,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gated_t
             break;
           }
           if (load_a && rank == 0) bar_expect(full(s), 2 * kStage);
-          const uint32_t bar = peer_addr(full(s), 0);
+          const uint32_t bar = peer_addr(full(s), leader);
           const uint32_t a = smem + s * kStage, b = a + kOperand;
           if constexpr (FORM != kBack) {
             if (load_a)
@@ -389,7 +394,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gated_t
       int j = 0, i = 0;  // stages used, tiles done
       bool go = true;
       Work work;
-      for (; go && work_at<FORM>(p, pair, pairs, i, work); ++i) {
+      for (; go && work_at<FORM>(p, pair, pairs, part, i, work); ++i) {
         const int b = i & 1;
         const bool a_mn = FORM == kBack && work.w;
         const uint32_t instr = instr_desc(1, 0, kBMn, 256, 256) | (a_mn ? instr_desc_a_mn : 0);
@@ -410,23 +415,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gated_t
 #pragma unroll
           for (int q = 0; q < kStep / 16; ++q)
             mma<2, false>(tmem + b * 256, da + q * a_next, db + q * ((kBMn ? 2048 : 32) >> 4), instr, k > work.k0 || q > 0);
-          mma_commit<2>(empty(s));
+          mma_commit<2>(empty(s), both);
         }
-        if (go) mma_commit<2>(sums_full(b));
+        if (go) mma_commit<2>(sums_full(b), both);
       }
       if (*watch.stop) {  // the MMAs in flight, with a limit
         int never = 0;
-        mma_commit<2>(spare);
+        mma_commit<2>(spare, both);
         bar_wait(spare, 0, Watch{&never, p.err, p.limit_ns / 16});
       }
     }
   } else if (warp >= 4) {
     Outbox<kBoxes> out{smem + kStages * kStage + (warp - 4) * kBoxes * kBox, 0, lane};
     Work work;
-    for (int i = 0; work_at<FORM>(p, pair, pairs, i, work); ++i) {
+    for (int i = 0; work_at<FORM>(p, pair, pairs, part, i, work); ++i) {
       const int b = i & 1;
       uint4 dh[8];
-      if constexpr (FORM == kGrad) {  // 64 columns of dh on their way while the sums are not there yet
+      if constexpr (FORM == kGrad && !SPLIT) {  // 64 columns of dh on their way while the sums are not there yet
         const int row = (work.at.m * 2 + rank) * kHalf + (warp & 3) * 32 + lane;
         const int col = work.at.n * kHalf + ((warp - 4) >> 2) * 64;
         const uint4* from = (const uint4*)(p.dh + row * p.lddh + col);
@@ -437,15 +442,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gated_t
       if (!bar_wait_warp(sums_full(b), (i / 2) & 1, watch)) break;
       fence_after();
       const uint32_t lanes = (uint32_t)(warp & 3) * 32;
+      if constexpr (SPLIT) {
+        leave_sums(smem, tmem + (lanes << 16), lanes + lane, (warp - 4) >> 2 << 2);
+        fence_before();
+        break;
+      }
       epilogue<FORM, ACT>(p, work, tmem + (lanes << 16) + b * 256, (work.at.m * 2 + rank) * kHalf + lanes, (warp - 4) >> 2, maxima, dh, out);
       fence_before();
       __syncwarp();
-      if (lane == 0) bar_arrive_peer(peer_addr(sums_empty(b), 0));
+      if (lane == 0) bar_arrive_peer(peer_addr(sums_empty(b), leader));
     }
     if (lane == 0) stores_done();
   }
   __syncthreads();
   cluster_sync();
+  if constexpr (SPLIT) {
+    // Each CTA finishes its share of the pair's rows.
+    const TileAt at = tile_at(p.grid, pair);
+    const int row0 = (at.m * 2 + rank) * kHalf, r1 = min(kHalf * (part + 1) / split, p.rows - row0);
+    if (!p.stall_ns) {
+      for (int r = kHalf * part / split + warp; r < r1; r += kThreads / 32) {
+        float4 sum[2];
+        split_sums(smem, r, lane, rank, split, sum);
+        if constexpr (FORM == kForward)
+          finish_forward<ACT>(p, row0 + r, at.n, lane, sum[0], sum[1]);
+        else
+          finish_grad<ACT>(p, row0 + r, at.n, lane, sum[0], sum[1]);
+      }
+    }
+    cluster_sync();  // the others have read this CTA's sums
+  }
   if (warp == 2) tmem_free<2>(tmem, 512);
 }
 
@@ -514,6 +540,13 @@ cudaError_t join(const Join& a, int outputs, cudaStream_t stream) {
                         : join<16, 16>(a, outputs, stream);
 }
 
+PairClusters clusters;  // of the split kernels, which take the same shape
+
+// Pairs that share a tile of the forward or grad form.  (300 x 1024 x 2048,
+// 32 tiles of 16 stages: 9.0 us whole, 9.5 in twos; 1021 x 2048 x 768, 24 of
+// 32: 12.9 and 11.9.)
+int split_pre(int64_t tiles, int64_t steps) { return clusters.split(tiles, steps, 24); }
+
 int pairs_of(const Params& p, const TcLaunch& l) { return p.tiles + p.w_tiles < l.pairs ? p.tiles + p.w_tiles : l.pairs; }
 
 template <int FORM, int ACT>
@@ -521,7 +554,13 @@ cudaError_t launch(Params& p, const TcLaunch& l, cudaStream_t stream) {
   p.err = l.err;
   p.limit_ns = TIDE_BULK_TIMEOUT_NS;
   p.stall_ns = l.stall_ns;
-  return launch_early(gated_tc_kernel<FORM, ACT>, dim3(2 * pairs_of(p, l)), kThreads, kSmem, 0, stream, p);
+  if constexpr (FORM != kBack) {
+    p.split = split_pre(p.tiles, p.steps);
+    p.share = Share(p.steps, p.split);
+    if (p.split > 1)
+      return launch_early(gated_tc_kernel<FORM, ACT, true>, dim3(2 * p.split * p.tiles), kThreads, kSmem, 2 * p.split, stream, p);
+  }
+  return launch_early(gated_tc_kernel<FORM, ACT, false>, dim3(2 * pairs_of(p, l)), kThreads, kSmem, 2, stream, p);
 }
 
 bool rows16(int64_t width, int64_t ld) { return width % 8 == 0 && ld % 8 == 0; }
@@ -544,7 +583,7 @@ bool map_out(CUtensorMap* m, const uint16_t* p, int64_t cols, int64_t rows, int6
 }
 
 bool fill_pre(Params* p, const GatedArgs& a) {
-  p->rows = (int)a.tokens, p->cols = (int)a.ffn;
+  p->rows = (int)a.tokens, p->cols = p->features = (int)a.ffn;
   p->grid = TileGrid((int)ceil_div(a.tokens, 2 * kHalf), (int)ceil_div(a.ffn, kHalf));
   p->tiles = p->grid.all.d;
   p->steps = (int)ceil_div(a.hidden, kStep);
@@ -575,20 +614,30 @@ int64_t parts_bytes(int64_t tiles, int64_t part_bytes) { return tiles ? 76 / til
 }  // namespace
 
 cudaError_t gated_tc_prepare(int* pairs) {
-  void (*const kernels[])(Params) = {gated_tc_kernel<kForward, TIDE_ACT_SILU>, gated_tc_kernel<kForward, TIDE_ACT_GELU>,
-                                     gated_tc_kernel<kGrad, TIDE_ACT_SILU>, gated_tc_kernel<kGrad, TIDE_ACT_GELU>,
-                                     gated_tc_kernel<kBack, 0>};
+  void (*const kernels[])(Params) = {
+      gated_tc_kernel<kForward, TIDE_ACT_SILU, false>, gated_tc_kernel<kForward, TIDE_ACT_GELU, false>,
+      gated_tc_kernel<kForward, TIDE_ACT_SILU, true>,  gated_tc_kernel<kForward, TIDE_ACT_GELU, true>,
+      gated_tc_kernel<kGrad, TIDE_ACT_SILU, false>,    gated_tc_kernel<kGrad, TIDE_ACT_GELU, false>,
+      gated_tc_kernel<kGrad, TIDE_ACT_SILU, true>,     gated_tc_kernel<kGrad, TIDE_ACT_GELU, true>,
+      gated_tc_kernel<kBack, 0, false>};
   for (auto k : kernels) {
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e != cudaSuccess) return e;
   }
-  // The clusters the device holds at one time: a GPC with an odd number of
+  const cudaError_t held = clusters.prepare((const void*)gated_tc_kernel<kForward, TIDE_ACT_SILU, true>, kThreads, kSmem);
+  if (held != cudaSuccess) return held;
+  // The pairs the device holds at one time: a GPC with an odd number of
   // SMs leaves one without a partner.
+  cudaLaunchAttribute cluster;
+  cluster.id = cudaLaunchAttributeClusterDimension;
+  cluster.val.clusterDim = {2, 1, 1};
   cudaLaunchConfig_t c{};
   c.gridDim = dim3(2);
   c.blockDim = dim3(kThreads);
   c.dynamicSmemBytes = kSmem;
-  return cudaOccupancyMaxActiveClusters(pairs, gated_tc_kernel<kBack, 0>, &c);
+  c.attrs = &cluster;
+  c.numAttrs = 1;
+  return cudaOccupancyMaxActiveClusters(pairs, gated_tc_kernel<kBack, 0, false>, &c);
 }
 
 int64_t gated_dx_parts_bytes(int64_t tokens, int64_t hidden) {
@@ -598,23 +647,26 @@ int64_t gated_dw_parts_bytes(int64_t hidden, int64_t ffn) {
   return parts_bytes(2 * ceil_div(ffn, 2 * kHalf) * ceil_div(hidden, 2 * kHalf), 8 * ffn * hidden);
 }
 
+int gated_tc_split(const GatedArgs& a) {
+  return split_pre(ceil_div(a.tokens, 2 * kHalf) * ceil_div(a.ffn, kHalf), ceil_div(a.hidden, kStep));
+}
+
 bool gated_tc_takes(const GatedArgs& a) { return a.hidden >= 8 && rows16(a.hidden, a.hidden) && rows16(a.ffn, a.ffn); }
 
 cudaError_t launch_gated_forward_tc(const GatedArgs& a, const TcLaunch& l, cudaStream_t stream) {
   Params p{};
-  if (!fill_pre(&p, a) || !map_out(&p.out[0], a.h, a.ffn, a.tokens, a.ldh)) return cudaErrorInvalidValue;
-  p.g8 = a.g8, p.gs = a.gs, p.u8 = a.u8, p.us = a.us;
+  if (!fill_pre(&p, a) || !map_out(&p.outs[0], a.h, a.ffn, a.tokens, a.ldh)) return cudaErrorInvalidValue;
+  p.out = a.h, p.ldo = a.ldh, p.g8 = a.g8, p.gs = a.gs, p.u8 = a.u8, p.us = a.us;
   return a.act == TIDE_ACT_SILU ? launch<kForward, TIDE_ACT_SILU>(p, l, stream)
                                 : launch<kForward, TIDE_ACT_GELU>(p, l, stream);
 }
 
 cudaError_t launch_gated_grad_tc(const GatedArgs& a, const TcLaunch& l, cudaStream_t stream) {
   Params p{};
-  if (!fill_pre(&p, a) || !map_out(&p.out[0], a.dg, a.ffn, a.tokens, a.ffn) ||
-      !map_out(&p.out[1], a.du, a.ffn, a.tokens, a.ffn) || (a.h && !map_out(&p.out[2], a.h, a.ffn, a.tokens, a.ldh)))
+  if (!fill_pre(&p, a) || !map_out(&p.outs[0], a.dg, a.ffn, a.tokens, a.ffn) ||
+      !map_out(&p.outs[1], a.du, a.ffn, a.tokens, a.ffn) || (a.h && !map_out(&p.outs[2], a.h, a.ffn, a.tokens, a.ldh)))
     return cudaErrorInvalidValue;
-  p.with_h = a.h != nullptr;
-  p.dh = a.dh, p.lddh = a.lddh;
+  p.out = a.h, p.ldo = a.ldh, p.dh = a.dh, p.lddh = a.lddh, p.dg = a.dg, p.du = a.du;
   return a.act == TIDE_ACT_SILU ? launch<kGrad, TIDE_ACT_SILU>(p, l, stream) : launch<kGrad, TIDE_ACT_GELU>(p, l, stream);
 }
 
@@ -633,7 +685,7 @@ cudaError_t launch_gated_back_tc(const GatedArgs& a, bool dx, bool dw, bool dx_b
     p.tiles = p.grid.all.d * p.split;
     if (!map_k(&p.a[0], a.dg, a.ffn, a.tokens, a.ffn) || !map_k(&p.a[1], a.du, a.ffn, a.tokens, a.ffn) ||
         !map_mn(&p.b[0], a.wg, a.hidden, a.ffn, a.hidden) || !map_mn(&p.b[1], a.wu, a.hidden, a.ffn, a.hidden) ||
-        !map_out(&p.out[0], a.dx, a.hidden, a.tokens, a.lddx))
+        !map_out(&p.outs[0], a.dx, a.hidden, a.tokens, a.lddx))
       return cudaErrorInvalidValue;
   }
   if (dw) {
@@ -646,8 +698,8 @@ cudaError_t launch_gated_back_tc(const GatedArgs& a, bool dx, bool dw, bool dx_b
     p.w_parts = a.dw_parts;
     p.w_tiles *= p.w_split;
     if (!map_mn(&p.wa[0], a.dg, a.ffn, a.tokens, a.ffn) || !map_mn(&p.wa[1], a.du, a.ffn, a.tokens, a.ffn) ||
-        !map_mn(&p.wb, a.x, a.hidden, a.tokens, a.ldx) || !map_out(&p.out[1], a.dwg, a.hidden, a.ffn, a.hidden) ||
-        !map_out(&p.out[2], a.dwu, a.hidden, a.ffn, a.hidden))
+        !map_mn(&p.wb, a.x, a.hidden, a.tokens, a.ldx) || !map_out(&p.outs[1], a.dwg, a.hidden, a.ffn, a.hidden) ||
+        !map_out(&p.outs[2], a.dwu, a.hidden, a.ffn, a.hidden))
       return cudaErrorInvalidValue;
   }
   // What a tile of either takes: its stages, at least the four that writing it

@@ -372,5 +372,45 @@ struct Outbox {
   }
 };
 
+// A pair's sums of its part of a contraction, on their way to the cluster's
+// other pairs: 128 rows of 256 fp32 a CTA, where its stages were (their
+// products have completed).  16-byte piece c of row r lies at c ^ (r % 8).
+constexpr uint32_t kSumRow = 256 * 4;
+
+// Four of the eight chunks of 32 columns, from this warp's 32 TMEM lanes.
+__device__ __forceinline__ void leave_sums(uint32_t smem, uint32_t tmem, int row, int first) {
+  const uint32_t to = smem + row * kSumRow, turn = row & 7;
+#pragma unroll 1
+  for (uint32_t c = first; c < first + 4; ++c) {
+    uint32_t v[32];
+    tmem_read(tmem + c * 32, v);
+#pragma unroll
+    for (uint32_t q = 0; q < 8; ++q)
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + (((c * 8 + q) ^ turn) << 4)), "r"(v[4 * q]),
+                   "r"(v[4 * q + 1]), "r"(v[4 * q + 2]), "r"(v[4 * q + 3])
+                   : "memory");
+  }
+}
+
+// The whole contraction's sums of row `row` and columns lane * 4 on, and 128
+// columns further, in the parts' order.  rank: in the pair.
+__device__ __forceinline__ void split_sums(uint32_t smem, int row, int lane, uint32_t rank, int split, float4 (&sum)[2]) {
+  const uint32_t from = smem + row * kSumRow + ((lane ^ (row & 7)) << 4);
+  float4 v[kMaxSplit][2];
+#pragma unroll
+  for (int q = 0; q < kMaxSplit; ++q)
+    if (q < split) {
+      const uint32_t a = peer_addr(from, 2 * q + rank);
+      v[q][0] = peer_read(a), v[q][1] = peer_read(a + kSumRow / 2);
+    }
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    sum[c] = v[0][c];
+#pragma unroll
+    for (int q = 1; q < kMaxSplit; ++q)
+      if (q < split) sum[c].x += v[q][c].x, sum[c].y += v[q][c].y, sum[c].z += v[q][c].z, sum[c].w += v[q][c].w;
+  }
+}
+
 }  // namespace tc
 }  // namespace tide

@@ -57,9 +57,9 @@ struct PairClusters {
 
   cudaError_t prepare(const void* kernel, int threads, size_t smem);
   // Pairs for a tile: as many as all tiles find at one time, each with at
-  // least eight stages, or 1.
-  int split(int64_t tiles, int64_t stages) const {
-    int s = kMaxSplit;
+  // least eight stages, or 1, as with fewer stages than `least` in all.
+  int split(int64_t tiles, int64_t stages, int least) const {
+    int s = stages < least ? 1 : kMaxSplit;
     while (s > 1 && (held[s] < tiles || stages < 8 * s)) --s;
     return s;
   }

@@ -299,6 +299,57 @@ def test_gated_forward(compute, tokens, hidden, ffn, kind, keep):
         same_codes(bufs["x8"].view.cpu(), codes)
 
 
+# few tiles and a long contraction: split in two, three and four
+SPLIT_SHAPES = [(1014, 9200, 752), (200, 7904, 2368), (100, 8200, 1000), (1021, 2048, 768), (300, 1544, 136)]
+
+
+@pytest.mark.parametrize("tokens,hidden,ffn", SPLIT_SHAPES)
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+@pytest.mark.parametrize("keep", ["none", "pre"])
+def test_gated_forward_split(compute, tokens, hidden, ffn, kind, keep):
+    test_gated_forward(compute, tokens, hidden, ffn, kind, keep)
+
+
+@pytest.mark.parametrize("tokens,hidden,ffn", SPLIT_SHAPES)
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+def test_gated_backward_split(compute, tokens, hidden, ffn, kind):
+    test_gated_backward_recomputed(compute, tokens, hidden, ffn, kind, True)
+
+
+def test_gated_split_same_results_every_time(compute):
+    """In the parts' order each time, with a checkpoint or without one."""
+    tokens, hidden, ffn = 200, 7904, 2368
+    g = gen(22)
+    x, (wg, wu), dh = randn(g, tokens, hidden), weights(g, hidden, ffn), randn(g, tokens, ffn)
+    h = Guarded(tokens, ffn, ffn + 8)
+    compute.gated_forward(tokens, hidden, ffn, x, wg, wu, h, ld_h=ffn + 8)
+    first, grads = h.view.clone(), [t.clone() for t in run_backward(compute, tokens, hidden, ffn, "silu", dh, x, wg, wu)]
+    for _ in range(5):
+        bufs, ck = checkpoint(tokens, hidden, ffn, False)
+        compute.gated_forward(tokens, hidden, ffn, x, wg, wu, h, checkpoint=ck, ld_h=ffn + 8)
+        assert torch.equal(h.view, first) and h.intact() and all(b.intact() for b in bufs.values())
+        for a, b in zip(grads, run_backward(compute, tokens, hidden, ffn, "silu", dh, x, wg, wu)):
+            assert torch.equal(a, b)
+
+
+def test_gated_split_wait_that_runs_out_is_reported():
+    tokens, hidden, ffn = 200, 7904, 2368
+    g = gen(23)
+    x, (wg, wu) = randn(g, tokens, hidden), weights(g, hidden, ffn)
+    h = Guarded(tokens, ffn)
+    with tide.Compute() as c:
+        c.set_test_stall(1_000_000)
+        c.gated_forward(tokens, hidden, ffn, x, wg, wu, h)
+        with pytest.raises(tide.TideError) as e:
+            c.check_device()
+        assert e.value.status == tide.TIDE_ERR_TIMEOUT
+        c.set_test_stall(0)
+        c.gated_forward(tokens, hidden, ffn, x, wg, wu, h)
+        c.check_device()
+        close(h.view, ref.gated_forward(x, wg, wu, "silu")[0], ref.gated_forward_bound(x, wg, wu, "silu")[0])
+        assert h.intact()
+
+
 @pytest.mark.parametrize("pad_x,pad_h", [(8, 16), (1, 0), (0, 3)])
 @pytest.mark.parametrize("tokens", [1, 40, 200])
 def test_gated_forward_strided(compute, pad_x, pad_h, tokens):
