@@ -11,12 +11,14 @@
 // sums over distributed shared memory in the order of their ranks, so the
 // result does not depend on timing.
 //
-// Bound by HBM: the weights stream through a ring of 3-6 stages of 18-40 KiB,
-// with room for two CTAs to an SM up to 32 tokens.  One token: 4096 x 14336
-// gate and up 40 us (5.8 TB/s; once they flow the rest is the ramp), their dX
-// 33 us, an 8192 x 28672 8-bit product 45 us (5.2 TB/s).  Small blocks take
-// 4-7 us of waits one after the other: the first stage's 0.6 us, 0.3 us a
-// stage, the clusters' meetings 0.7 us each.
+// Bound by HBM: the weights stream through a ring of 5-12 stages of 18-40 KiB
+// (a ring of 3-6, with room for two CTAs to an SM, was slower for the gated
+// block, 8192 x 28672 gate and up 152 us against 140, and faster for the 8-bit
+// product, 43.8 against 45.5).  One token: 4096 x 14336 gate and up 36 us (6.5
+// TB/s; once they flow the rest is the ramp), their dX 37 us, an 8192 x 28672
+// 8-bit product 43 us (5.5 TB/s).  Small blocks take 4-7 us of waits one after
+// the other: the first stage's 0.6 us, 0.15-0.3 us a stage, the clusters'
+// meetings 0.7 us each.
 #include "compute_device.cuh"
 #include "gated_finish.cuh"
 #include "tc_device.cuh"
@@ -43,8 +45,8 @@ struct Shape {
   static constexpr bool FP8 = KIND == kFp8;
   static constexpr int kParts = KIND == kFp8 || KIND == kDx ? 1 : 2;  // weight tiles of a stage
   static constexpr uint32_t kStage = kParts * kWeights + NT * kRowBytes;
-  static constexpr uint32_t kBudget = NT <= 32 ? 108 * 1024 : 200 * 1024;
-  static constexpr int kStages = kBudget / kStage < 6 ? kBudget / kStage : 6;
+  static constexpr uint32_t kBudget = FP8 && NT <= 32 ? 108 * 1024 : 210 * 1024;
+  static constexpr int kStages = kBudget / kStage < 12 ? kBudget / kStage : 12;
   static constexpr int kBufs = FP8 ? 4 : 1;  // accumulators of kParts * NT columns
   static constexpr int kColumns = kBufs * kParts * NT < 32 ? 32 : kBufs * kParts * NT;
   static constexpr uint32_t kSums = kParts * NT * kRows * 4;
@@ -112,7 +114,7 @@ __global__ void __launch_bounds__(kThreads) few_tc_kernel(const __grid_constant_
   const auto sums_full = [&](int b) { return bar0 + 8u * (2 * S::kStages + b); };
   const auto sums_empty = [&](int b) { return bar0 + 8u * (2 * S::kStages + S::kBufs + b); };
   const uint32_t spare = bar0 + 8u * (2 * S::kStages + 2 * S::kBufs);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int split = gridDim.x, rank = blockIdx.x;  // the cluster is a row of the grid
   const int token0 = blockIdx.y * NT, feature0 = blockIdx.z * kRows;
   const int k0 = (int)((int64_t)p.steps * rank / split), k1 = (int)((int64_t)p.steps * (rank + 1) / split);
@@ -141,7 +143,7 @@ __global__ void __launch_bounds__(kThreads) few_tc_kernel(const __grid_constant_
   if (p.stall_ns) {  // test: a wait on a barrier nothing arrives on runs out
     if (threadIdx.x == 0) bar_wait(spare, 0, Watch{&stop, p.err, p.stall_ns});
   } else if (warp == 0) {
-    if (lane == 0) {
+    if (elected()) {
       bool go = true;
       int j = 0;
       for (int k = k0; k < k1; ++k, ++j) {
@@ -175,7 +177,7 @@ __global__ void __launch_bounds__(kThreads) few_tc_kernel(const __grid_constant_
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (elected()) {
       bool go = true;
       int j = 0;
       for (int k = k0; k < k1; ++k, ++j) {
@@ -431,24 +433,24 @@ cudaError_t few_tc_prepare() {
 
 // Past 64 tokens the 256-row tiles read fewer operand bytes; they are ahead
 // for the gated block from about half as many of these tiles as SMs (1021 x
-// 2048 x 768, 96 tiles: 19.6 us), for the 8-bit product from two thirds (128 x
-// 28672 x 8192, 128 tiles: 87 us, 76 there).  Below that it goes by the
-// stages of a CTA, in microseconds:
+// 2048 x 768, 96 tiles: 19.6 us, 11.8 there), for the 8-bit product from two
+// thirds (128 x 28672 x 8192, 128 tiles: 87 us, 76 there).  Below that it goes
+// by the stages of a CTA, in microseconds:
 //                    here                     256-row tiles
 //   gated            0.24 each and 3          0.265 and 4.3
-//     split          0.4 and 6.4              0.265 and 8.5
+//     split          0.3 and 6.2              0.265 and 8.5
 //   8-bit            0.35 and 3               0.33 and 4
-//     split          0.35 and 4.5             0.33 and 8
-// (Gated, 209 x 7904 x 2368: 31.7 here, 21.5 there; 532 x 16480 x 656 57.4 and
-// 32; 256 x 1024 x 1024 8.0 and 8.5; 65 x 28672 x 256 29.1 and 36.  8-bit, 209
-// x 2368 x 7904: 16.8 and 13.3; 532 x 656 x 16480 28.8 and 17.5; 256 x 1024 x
-// 4096 7.6 and 9.9; 300 x 304 x 25008 14.6 and 25.)
+//     split          0.35 and 4.5             0.33 and 7
+// (Gated, 420 x 10864 x 208: 14.0 here, 19.1 there; 123 x 7712 x 960 15.4 and
+// 17.0; 110 x 11584 x 3104 34.4 and 34.2; 1162 x 12880 x 544 62.9 and 35.7.
+// 8-bit, 420 x 208 x 10864: 9.1 and 15.2; 123 x 960 x 7712 10.1 and 11.7; 110
+// x 3104 x 11584 21.6 and 15.3; 1162 x 544 x 12880 40.0 and 18.0.)
 bool gated_few_takes(const GatedArgs& a, const TcLaunch& l) {
   if (a.tokens <= 64 || !few(a.tokens, a.ffn, l.sms / 2)) return few(a.tokens, a.ffn, 0);
   const int64_t steps = ceil_div(a.hidden, kRowBytes / 2);
   const int split = split_of<kForward, 64, TIDE_ACT_SILU>(ceil_div(a.tokens, 64) * ceil_div(a.ffn, kRows), steps, l.sms);
   const int there = gated_tc_split(a);
-  return (split > 1 ? 0.4 * steps / split + 6.4 : 0.24 * steps + 3) <= 0.265 * steps / there + (there > 1 ? 8.5 : 4.3);
+  return (split > 1 ? 0.3 * steps / split + 6.2 : 0.24 * steps + 3) <= 0.265 * steps / there + (there > 1 ? 8.5 : 4.3);
 }
 // dX up to 64 tokens, and for more where it has few tiles and dW's leave SMs
 // for it (500 x 1024 x 1024, 64 tiles: 26.1 us for the backward pass against
@@ -475,7 +477,7 @@ bool fp8_few_takes(const MatmulArgs& a, const TcLaunch& l) {
   if (a.m <= 64 || !few(a.m, a.n, 2 * l.sms / 3)) return few(a.m, a.n, 0);
   const int64_t steps = ceil_div(a.k, kRowBytes);
   const int split = split_of<kFp8, 64, 0>(ceil_div(a.m, 64) * ceil_div(a.n, kRows), steps, l.sms), there = fp8_tc_split(a);
-  return 0.35 * steps / split + (split > 1 ? 4.5 : 3) <= 0.33 * steps / there + (there > 1 ? 8 : 4);
+  return 0.35 * steps / split + (split > 1 ? 4.5 : 3) <= 0.33 * steps / there + (there > 1 ? 7 : 4);
 }
 
 cudaError_t launch_gated_forward_few(const GatedArgs& a, const TcLaunch& l, cudaStream_t stream) {

@@ -79,7 +79,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) summed_
   const auto sums_full = [&](int b) { return bar0 + 8u * (2 * kStages + b); };
   const auto sums_empty = [&](int b) { return bar0 + 8u * (2 * kStages + 2 + b); };
   const uint32_t spare = bar0 + 8u * (2 * kStages + 4);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const Watch watch{&stop, p.err, p.limit_ns};
@@ -106,7 +106,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) summed_
     // 384 threads start with 168 registers each (64,512); this warpgroup goes
     // down to 56 and the two that hold sums go up to 216: 62,464.
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    if ((warp == 0 || warp == 3) && lane == 0) {
+    if ((warp == 0 || warp == 3) && elected()) {
       const bool load_a = warp == 0;  // one thread loads A, another B
       int j = 0;  // stages filled so far
       bool go = true;
@@ -136,7 +136,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) summed_
         for (int i = max(0, j - kStages); i < j; ++i)
           bar_wait(full(i % kStages), (i / kStages) & 1, Watch{&never, p.err, p.limit_ns / 16});
       }
-    } else if (warp == 1 && lane == 0 && rank == 0) {
+    } else if (warp == 1 && rank == 0 && elected()) {
       int j = 0;  // blocks so far
       bool go = true;
       for (int t = pair; t < p.tiles && go; t += pairs) {
@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kScaledThreads, 1) scaled_kernel(const __grid_
   const auto full = [&](int s) { return bar0 + 8u * s; };
   const auto empty = [&](int s) { return bar0 + 8u * (kStages + s); };
   const uint32_t sums_full = bar0 + 8u * (2 * kStages), sums_empty = sums_full + 8, spare = sums_full + 16;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t cta = cluster_rank(), rank = cta & 1, leader = SPLIT ? cta & ~1u : 0;
   const uint16_t both = (uint16_t)(3u << leader);  // the pair's CTAs
   const int split = SPLIT ? p.split : 1, part = cta >> 1;
@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(kScaledThreads, 1) scaled_kernel(const __grid_
   if (p.stall_ns) {  // test: a wait on a barrier nothing arrives on runs out
     if (threadIdx.x == 0) bar_wait(spare, 0, Watch{&stop, p.err, p.stall_ns});
   } else if (warp == 0 || warp == 3) {
-    if (lane == 0) {
+    if (elected()) {
       const bool load_a = warp == 0;  // one thread loads A, another B
       int j = 0;  // stages filled so far
       bool go = true;
@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(kScaledThreads, 1) scaled_kernel(const __grid_
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0 && elected()) {
       int j = 0, i = 0;  // blocks and tiles so far
       bool go = true;
       for (int t = pair; t < p.tiles && go; t += pairs, ++i) {

@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
   const auto sums_full = [&](int b) { return bar0 + 8u * (2 * kStages + b); };
   const auto sums_empty = [&](int b) { return bar0 + 8u * (2 * kStages + 2 + b); };
   const uint32_t spare = bar0 + 8u * (2 * kStages + 4);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t cta = cluster_rank(), rank = cta & 1, leader = SPLIT ? cta & ~1u : 0;
   const uint16_t both = (uint16_t)(3u << leader);  // the pair's CTAs
   const int split = SPLIT ? p.split : 1, part = SPLIT ? cta >> 1 : 0;
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
   } else if (warp == 0 || warp == 3) {
     // One thread loads A, another B: issuing a copy takes long enough that
     // one thread with all four of a stage fell behind the MMAs.
-    if (lane == 0) {
+    if (elected()) {
       const bool load_a = warp == 0;
       int j = 0;  // stages filled so far
       bool go = true;
@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
       }
     }
   } else if (warp == 1 && rank == 0) {
-    if (lane == 0) {
+    if (elected()) {
       int j = 0, i = 0;  // stages used, tiles done
       bool go = true;
       Work work;
