@@ -438,7 +438,8 @@ cudaError_t few_tc_prepare() {
 // by the stages of a CTA, in microseconds:
 //                    here                     256-row tiles
 //   gated            0.24 each and 3          0.265 and 4.3
-//     split          0.3 and 6.2              0.265 and 8.5
+//     split          0.3 and 6.2              0.265 and 7.6
+//     checkpoint     4 more, by the split     1.1 more
 //   8-bit            0.35 and 3               0.33 and 4
 //     split          0.35 and 4.5             0.33 and 7
 // (Gated, 420 x 10864 x 208: 14.0 here, 19.1 there; 123 x 7712 x 960 15.4 and
@@ -450,7 +451,8 @@ bool gated_few_takes(const GatedArgs& a, const TcLaunch& l) {
   const int64_t steps = ceil_div(a.hidden, kRowBytes / 2);
   const int split = split_of<kForward, 64, TIDE_ACT_SILU>(ceil_div(a.tokens, 64) * ceil_div(a.ffn, kRows), steps, l.sms);
   const int there = gated_tc_split(a);
-  return (split > 1 ? 0.3 * steps / split + 6.2 : 0.24 * steps + 3) <= 0.265 * steps / there + (there > 1 ? 8.5 : 4.3);
+  const double here = split > 1 ? 0.3 * steps / split + 6.2 : 0.24 * steps + 3;
+  return here + (a.g8 ? 4.0 / split : 0) <= 0.265 * steps / there + (there > 1 ? 7.6 : 4.3) + (a.g8 ? 1.1 : 0);
 }
 // dX up to 64 tokens, and for more where it has few tiles and dW's leave SMs
 // for it (500 x 1024 x 1024, 64 tiles: 26.1 us for the backward pass against

@@ -21,11 +21,10 @@ struct GatedOut {
   uint16_t *dg, *du;
 };
 
+// Largest magnitude of a block, as whole numbers, which order alike; NaN is none.
 __device__ __forceinline__ float warp_amax(const float4& v) {
-  float m = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
-#pragma unroll
-  for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-  return m;
+  const float m = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, m == m ? __float_as_uint(m) : 0u));
 }
 
 // 4 codes a lane, one scale a warp: this lane's part of a token's block.
