@@ -67,7 +67,7 @@ struct Params : GatedOut {  // 8-bit product, dX: out, ldo and features of it
 };
 
 // Sums of the cluster's CTAs' sums at N addresses, in rank order.  Four ranks'
-// reads are on their way before the first is added.  (split: 2, 4 or 8.)
+// reads are on their way before the first is added.
 template <int N>
 __device__ __forceinline__ void cluster_sums(const uint32_t (&addr)[N], int split, float4 (&v)[N]) {
   constexpr int kAtOnce = 4;
@@ -324,31 +324,33 @@ __global__ void __launch_bounds__(kThreads) few_tc_kernel(const __grid_constant_
   if (beside) after_previous();
 }
 
+constexpr int kMaxCluster = 8;
+
 // One kernel's shape for the launches: set up once for each device.
 template <int KIND, int NT, int ACT>
 struct Held {
-  // clusters of 2, 4 and 8 CTAs that the device holds at one time; a cluster
+  // clusters of so many CTAs that the device holds at one time; a cluster
   // lies within one GPC, so these are fewer than SMs by their size
-  static int clusters[3];
+  static int clusters[kMaxCluster + 1];
 };
 template <int KIND, int NT, int ACT>
-int Held<KIND, NT, ACT>::clusters[3] = {0, 0, 0};
+int Held<KIND, NT, ACT>::clusters[kMaxCluster + 1] = {};
 
 template <int KIND, int NT, int ACT>
 cudaError_t prepare() {
   using S = Shape<KIND, NT>;
   cudaError_t e = cudaFuncSetAttribute(few_tc_kernel<KIND, NT, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
-  for (int i = 0; i < 3 && e == cudaSuccess; ++i) {
+  for (int n = 2; n <= kMaxCluster && e == cudaSuccess; ++n) {
     cudaLaunchAttribute cluster;
     cluster.id = cudaLaunchAttributeClusterDimension;
-    cluster.val.clusterDim = {2u << i, 1, 1};
+    cluster.val.clusterDim = {(unsigned)n, 1, 1};
     cudaLaunchConfig_t c{};
-    c.gridDim = dim3(2u << i);
+    c.gridDim = dim3(n);
     c.blockDim = dim3(kThreads);
     c.dynamicSmemBytes = S::kSmem;
     c.attrs = &cluster;
     c.numAttrs = 1;
-    e = cudaOccupancyMaxActiveClusters(&Held<KIND, NT, ACT>::clusters[i], few_tc_kernel<KIND, NT, ACT>, &c);
+    e = cudaOccupancyMaxActiveClusters(&Held<KIND, NT, ACT>::clusters[n], few_tc_kernel<KIND, NT, ACT>, &c);
   }
   return e;
 }
@@ -361,16 +363,17 @@ cudaError_t prepare_tiles() {
 }
 
 // CTAs that share a tile's contraction: up to one for each SM, all at work at
-// one time, each with at least four stages of it (fewer stages less save
-// less than the clusters' exchange takes).  (One tile for each of 112
-// SMs streams 4096 x 14336 weights in 44 us, split in two 45.5; 16 tiles of
-// 64 tokens take 13.4 us split in four, 20.5 split in eight, where the last
-// clusters wait for the first.)
+// one time, each with at least four stages of it, or, where more than four
+// exchange 64 tokens' gate and up sums, twelve (fewer save less than the
+// exchange takes).  (16 tiles of 64 tokens, gated, 8192 x 2048: 18.1 us split
+// in four, 17.6 in six, 28.1 in eight, where the last clusters wait for the
+// first; 4096 x 2048: 12.4 in four, 12.9 in six; dX of 7 x 2048 x 8192: 15.6
+// in four, 13.0 in six.)
 template <int KIND, int NT, int ACT>
 int split_of(int64_t tiles, int64_t steps, int sms) {
   const int* held = Held<KIND, NT, ACT>::clusters;
-  int s = 1;
-  for (int i = 0; i < 3 && 2 * s * tiles <= sms && tiles <= held[i] && steps >= 8 * s; ++i) s *= 2;
+  int s = kMaxCluster;
+  while (s > 1 && (s * tiles > sms || held[s] < tiles || steps < (NT == 64 && Shape<KIND, NT>::kParts == 2 && s > 4 ? 12 : 4) * s)) --s;
   return s;
 }
 
@@ -467,8 +470,7 @@ bool gated_dx_few_takes(const GatedArgs& a, const TcLaunch& l) {
   if (steps < 48) return false;
   const int64_t tiles = ceil_div(a.hidden, kRows) * ceil_div(a.tokens, 64);
   const int64_t large = ceil_div(a.hidden, 256) * ceil_div(a.tokens, 256);
-  int64_t split = 1;
-  while (split < 8 && 2 * split * tiles <= l.sms) split *= 2;
+  const int split = split_of<kDx, 64, 0>(tiles, steps, l.sms);
   const int64_t parts = l.pairs / large > 1 ? l.pairs / large : 1;
   if (0.21 * steps / split + 3 > 0.3 * steps / parts + (parts > 1 ? 8 : 4)) return false;
   if (a.tokens <= 64) return few(a.tokens, a.hidden, 0);

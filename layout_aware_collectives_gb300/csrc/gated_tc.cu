@@ -18,9 +18,9 @@
 // accumulators so that they do so while the next tile is summed.
 //
 // Bound by the tensor cores at every large size: 2048 x 4096 x 14336 forward
-// 240-290 us (1.66-2.0 PFLOP/s; their pipe 89% busy), dX and dW of it 514-600
-// us (80% busy), the longer times with the card at its power cap, where a
-// plain library product of the forward's size takes 268.
+// 236-282 us (1.7-2.04 PFLOP/s; their pipe 94% busy), dX and dW of it 490-600
+// us (94% busy), the longer times with the card at its power cap, where a
+// plain library product of the forward's size takes 271.
 #include "compute_device.cuh"
 #include "gated_finish.cuh"
 #include "tc_device.cuh"
