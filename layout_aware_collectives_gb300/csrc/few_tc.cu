@@ -462,13 +462,14 @@ bool gated_few_takes(const GatedArgs& a, const TcLaunch& l) {
 // 23.1 in 256-row tiles).  In microseconds, here 0.21 a stage and 3 more, in
 // 256-row tiles 0.3 and 4, or 8 where their sums are split (1 x 4096 x 14336:
 // 33 against 54; 64 x 512 x 2048: 7 against 12; 2 x 336 x 25264, where a
-// cluster's 8 CTAs are too few: 32 against 22).  Below 48 stages the launch
-// that dX then has to itself costs the host more than it saves (2 x 5792 x
-// 160: 8.7 us, but 3 more to enqueue).
+// cluster's 8 CTAs are too few: 32 against 22).  Below 48 stages it
+// takes a launch more than it saves, but for so few tiles that it ends beside
+// dW (250 x 256 x 704, 8 tiles: backward pass 13.9 us against 16.0; 500 x 512
+// x 512, 32 tiles: 19.9 against 15.8).
 bool gated_dx_few_takes(const GatedArgs& a, const TcLaunch& l) {
   const int64_t steps = 2 * ceil_div(a.ffn, kRowBytes / 2);
-  if (steps < 48) return false;
   const int64_t tiles = ceil_div(a.hidden, kRows) * ceil_div(a.tokens, 64);
+  if (steps < (tiles <= 8 ? 16 : 48)) return false;
   const int64_t large = ceil_div(a.hidden, 256) * ceil_div(a.tokens, 256);
   const int split = split_of<kDx, 64, 0>(tiles, steps, l.sms);
   const int64_t parts = l.pairs / large > 1 ? l.pairs / large : 1;
