@@ -372,8 +372,9 @@ cudaError_t prepare_tiles() {
 template <int KIND, int NT, int ACT>
 int split_of(int64_t tiles, int64_t steps, int sms) {
   const int* held = Held<KIND, NT, ACT>::clusters;
+  constexpr int kMany = NT == 64 && Shape<KIND, NT>::kParts == 2 ? 12 : 4;  // stages, of more than four
   int s = kMaxCluster;
-  while (s > 1 && (s * tiles > sms || held[s] < tiles || steps < (NT == 64 && Shape<KIND, NT>::kParts == 2 && s > 4 ? 12 : 4) * s)) --s;
+  while (s > 1 && (s * tiles > sms || held[s] < tiles || steps < (s > 4 ? kMany : 4) * s)) --s;
   return s;
 }
 
@@ -458,14 +459,14 @@ bool gated_few_takes(const GatedArgs& a, const TcLaunch& l) {
   return here + (a.g8 ? 4.0 / split : 0) <= 0.265 * steps / there + (there > 1 ? 7.6 : 4.3) + (a.g8 ? 1.1 : 0);
 }
 // dX up to 64 tokens, and for more where it has few tiles and dW's leave SMs
-// for it (500 x 1024 x 1024, 64 tiles: 26.1 us for the backward pass against
-// 23.1 in 256-row tiles).  In microseconds, here 0.21 a stage and 3 more, in
-// 256-row tiles 0.3 and 4, or 8 where their sums are split (1 x 4096 x 14336:
-// 33 against 54; 64 x 512 x 2048: 7 against 12; 2 x 336 x 25264, where a
-// cluster's 8 CTAs are too few: 32 against 22).  Below 48 stages it
-// takes a launch more than it saves, but for so few tiles that it ends beside
-// dW (250 x 256 x 704, 8 tiles: backward pass 13.9 us against 16.0; 500 x 512
-// x 512, 32 tiles: 19.9 against 15.8).
+// for it (500 x 1024 x 1024, 64 tiles: 24.7 us for the backward pass against
+// 22.6 in 256-row tiles).  In microseconds, here 0.21 a stage and 3 more, in
+// 256-row tiles 0.3 and 4, or 8 where their sums are split (4 x 4096 x 14336:
+// 37 against 54; 64 x 512 x 2048: 6 against 8; 2 x 336 x 25264, where a
+// cluster's 8 CTAs are too few: 23 against 19).  Below 48 stages it takes a
+// launch more than it saves, but for so few tiles that it ends beside dW (250
+// x 256 x 704, 8 tiles: backward pass 13.9 us against 16.0; 500 x 512 x 512,
+// 32 tiles: 19.9 against 15.8).
 bool gated_dx_few_takes(const GatedArgs& a, const TcLaunch& l) {
   const int64_t steps = 2 * ceil_div(a.ffn, kRowBytes / 2);
   const int64_t tiles = ceil_div(a.hidden, kRows) * ceil_div(a.tokens, 64);

@@ -43,7 +43,8 @@ constexpr size_t kSmem = 1024 + kStages * kStage + kAllBoxes * kBox;
 // Eight warps read finished sums, each 32 rows of one half of the columns:
 // with a short contraction there is little of the next tile's sum to do it
 // behind (64 tokens of the 8B-shaped block: dW 70 us with four, 52 with
-// eight, 49 with two boxes of results behind one fence).
+// eight, 49 with two boxes of results behind one fence, 38 with the copies and
+// MMAs from an elected thread).
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpiWarps;
 constexpr int kBoxes = kAllBoxes / kEpiWarps;
@@ -596,7 +597,7 @@ bool fill_pre(Params* p, const GatedArgs& a) {
 // tiles as pairs (dX of few tokens, dW of a small block), the contraction is
 // split and the parts, in fp32, are joined by another kernel.  In stages (0.27
 // us): a tile's share, 18 for the join, and one for each 650 KB of parts.
-// (256 tokens of the 8B-shaped block: 16 tiles of 448 stages, 132 -> 54 us
+// (256 tokens of the 8B-shaped block: 16 tiles of 448 stages, 130 -> 52 us
 // in 4 parts; 1021 x 2048 x 768, 32 tiles of 24: 11 us whole, 18 in two.)
 int split_of(int64_t tiles, int64_t steps, int pairs, int64_t part_bytes, int64_t room) {
   int best = 1;
