@@ -526,6 +526,12 @@ TIDE_API tide_status_t tide_compute_check_device(tide_compute_t compute);
  * barrier nothing arrives on, reports it and computes nothing. */
 TIDE_API tide_status_t tide_compute_set_test_stall(tide_compute_t compute, int64_t ns);
 
+/* The same for one warp: with ns > 0, in every following tensor-core launch
+ * the first warp of each CTA that reads finished sums gives up after ns
+ * nanoseconds although they are there, while the other warps go on.  The
+ * call ends, is reported, and its outputs are incomplete. */
+TIDE_API tide_status_t tide_compute_set_test_late_warp(tide_compute_t compute, int64_t ns);
+
 /*
  * 8-bit blocks: a matrix [rows, cols] held as e4m3 codes (one byte each,
  * contiguous) and one fp32 scale for each block of block_rows x 128

@@ -60,6 +60,9 @@ class Compute:
     def set_test_stall(self, ns: int) -> None:
         _t.tide_compute_set_test_stall(self.handle, ns)
 
+    def set_test_late_warp(self, ns: int) -> None:
+        _t.tide_compute_set_test_late_warp(self.handle, ns)
+
     # -------- lifetime
     def close(self) -> None:
         if getattr(self, "handle", None):

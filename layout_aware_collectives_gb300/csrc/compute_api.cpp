@@ -99,7 +99,7 @@ tide_status_t bind(tide_compute_s* c, cudaStream_t stream) {
 
 TcLaunch launch_of(tide_compute_s* c) {
   std::lock_guard<std::mutex> g(c->mu);
-  return TcLaunch{c->pairs, c->num_sms, c->d_err, (uint64_t)c->test_stall_ns};
+  return TcLaunch{c->pairs, c->num_sms, c->d_err, (uint64_t)c->test_stall_ns, (uint64_t)c->test_late_ns};
 }
 
 tide_status_t launched(cudaError_t e, const char* what) { return e == cudaSuccess ? TIDE_OK : cuda_fail(e, what); }
@@ -171,6 +171,14 @@ tide_status_t tide_compute_set_test_stall(tide_compute_t c, int64_t ns) try {
   if (!c || ns < 0) return invalid("NULL handle or negative time");
   std::lock_guard<std::mutex> g(c->mu);
   c->test_stall_ns = ns;
+  return TIDE_OK;
+}
+TIDE_CATCH
+
+tide_status_t tide_compute_set_test_late_warp(tide_compute_t c, int64_t ns) try {
+  if (!c || ns < 0) return invalid("NULL handle or negative time");
+  std::lock_guard<std::mutex> g(c->mu);
+  c->test_late_ns = ns;
   return TIDE_OK;
 }
 TIDE_CATCH

@@ -108,6 +108,7 @@ struct TcLaunch {
   int sms;
   int* err;   // the handle's error word
   uint64_t stall_ns;  // test: a wait that must run out
+  uint64_t late_ns;   // test: the same of one warp, beside others whose do not
 };
 
 // Tensor-core kernels of the gated block (gated_tc.cu).  They take matrices
@@ -156,6 +157,6 @@ struct tide_compute_s {
   // runs out, so that nothing has to be zeroed on a stream.
   int* err = nullptr;
   int* d_err = nullptr;
-  int64_t test_stall_ns = 0;
+  int64_t test_stall_ns = 0, test_late_ns = 0;
   std::mutex mu;
 };

@@ -63,7 +63,7 @@ struct Params : GatedOut {  // 8-bit product, dX: out, ldo and features of it
   const float *sx, *sw;
   bool any_scales;
   int* err;
-  uint64_t limit_ns, stall_ns;
+  uint64_t limit_ns, stall_ns, late_ns;
 };
 
 // Sums of the cluster's CTAs' sums at N addresses, in rank order.  Four ranks'
@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kThreads) few_tc_kernel(const __grid_constant_
   constexpr bool kMn = KIND == kDx;
   constexpr uint32_t kInstr = instr_desc(FP8 ? 0 : 1, kMn, 0, kRows, NT);
   extern __shared__ uint8_t raw[];
-  __shared__ uint64_t bars[2 * S::kStages + 2 * S::kBufs + 1];
+  __shared__ uint64_t bars[2 * S::kStages + 2 * S::kBufs + 2];
   __shared__ __align__(16) float scales[4][FP8 ? NT : 4];
   __shared__ uint32_t tmem_at;
   __shared__ int stop;
@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kThreads) few_tc_kernel(const __grid_constant_
   const auto empty = [&](int s) { return bar0 + 8u * (S::kStages + s); };
   const auto sums_full = [&](int b) { return bar0 + 8u * (2 * S::kStages + b); };
   const auto sums_empty = [&](int b) { return bar0 + 8u * (2 * S::kStages + S::kBufs + b); };
-  const uint32_t spare = bar0 + 8u * (2 * S::kStages + 2 * S::kBufs);
+  const uint32_t spare = bar0 + 8u * (2 * S::kStages + 2 * S::kBufs), silent = spare + 8;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int split = gridDim.x, rank = blockIdx.x;  // the cluster is a row of the grid
   const int token0 = blockIdx.y * NT, feature0 = blockIdx.z * kRows;
@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kThreads) few_tc_kernel(const __grid_constant_
     stop = 0;
     for (int s = 0; s < S::kStages; ++s) bar_init(full(s), 1), bar_init(empty(s), 1);
     for (int b = 0; b < S::kBufs; ++b) bar_init(sums_full(b), 1), bar_init(sums_empty(b), 4);
-    bar_init(spare, 1);
+    bar_init(spare, 1), bar_init(silent, 1);
     bar_init_fence();
     prefetch_map(&p.w[0]), prefetch_map(&p.x[0]);
   }
@@ -141,17 +141,13 @@ __global__ void __launch_bounds__(kThreads) few_tc_kernel(const __grid_constant_
   bool done = false;  // this warp has its sums in shared memory
 
   if (p.stall_ns) {  // test: a wait on a barrier nothing arrives on runs out
-    if (threadIdx.x == 0) bar_wait(spare, 0, Watch{&stop, p.err, p.stall_ns});
+    if (threadIdx.x == 0) bar_wait(silent, 0, Watch{&stop, p.err, p.stall_ns});
   } else if (warp == 0) {
     if (elected()) {
-      bool go = true;
       int j = 0;
       for (int k = k0; k < k1; ++k, ++j) {
         const int s = j % S::kStages;
-        if (j >= S::kStages && !bar_wait(empty(s), (j / S::kStages + 1) & 1, watch)) {
-          go = false;
-          break;
-        }
+        if (j >= S::kStages && !bar_wait(empty(s), (j / S::kStages + 1) & 1, watch)) break;
         const uint32_t at = smem + s * S::kStage;
         bar_expect(full(s), S::kStage);
         if constexpr (KIND == kDx) {
@@ -170,23 +166,19 @@ __global__ void __launch_bounds__(kThreads) few_tc_kernel(const __grid_constant_
           load_box<false>(at + S::kParts * kWeights, &p.x[0], k * p.step_elems, token0, full(s));
         }
       }
-      if (!go) {  // copies in flight, with a limit again
-        int never = 0;
-        for (int i = max(0, j - S::kStages); i < j; ++i)
-          bar_wait(full(i % S::kStages), (i / S::kStages) & 1, Watch{&never, p.err, p.limit_ns / 16});
-      }
+      // the copies in flight, whoever of the others has left
+      int never = 0;
+      for (int i = max(0, j - S::kStages); i < j; ++i)
+        bar_wait(full(i % S::kStages), (i / S::kStages) & 1, Watch{&never, p.err, p.limit_ns / 16});
     }
   } else if (warp == 1) {
     if (elected()) {
-      bool go = true;
       int j = 0;
       for (int k = k0; k < k1; ++k, ++j) {
         const int s = j % S::kStages, b = j % S::kBufs;
         if ((FP8 && j >= S::kBufs && !bar_wait(sums_empty(b), (j / S::kBufs + 1) & 1, watch)) ||
-            !bar_wait(full(s), (j / S::kStages) & 1, watch)) {
-          go = false;
+            !bar_wait(full(s), (j / S::kStages) & 1, watch))
           break;
-        }
         fence_after();
         const uint32_t at = smem + s * S::kStage;
         const uint64_t dx = operand_desc(at + S::kParts * kWeights, 16);
@@ -200,11 +192,7 @@ __global__ void __launch_bounds__(kThreads) few_tc_kernel(const __grid_constant_
         mma_commit<1>(empty(s));
         if (FP8 || k + 1 == k1) mma_commit<1>(sums_full(b));
       }
-      if (!go) {  // the MMAs in flight, with a limit
-        int never = 0;
-        mma_commit<1>(spare);
-        bar_wait(spare, 0, Watch{&never, p.err, p.limit_ns / 16});
-      }
+      await_mmas<1>(spare, 1, watch);
     }
   } else {
     const int lanes = (warp & 3) * 32, feature = lanes + lane;  // TMEM lanes follow the warp's index modulo 4
@@ -232,7 +220,7 @@ __global__ void __launch_bounds__(kThreads) few_tc_kernel(const __grid_constant_
         }
         sums_barrier();
         // a warp whose wait ran out goes on meeting the others at the barrier
-        done = done && bar_wait_warp(sums_full(b), (j / S::kBufs) & 1, watch);
+        done = done && await_sums(sums_full(b), (j / S::kBufs) & 1, silent, p.late_ns && warp == 2, p.late_ns, watch);
         if (!done) continue;
         fence_after();
 #pragma unroll
@@ -261,7 +249,7 @@ __global__ void __launch_bounds__(kThreads) few_tc_kernel(const __grid_constant_
         for (int i = 0; i < NT; ++i) leave(i, sum[i]);
       }
     } else {
-      done = k0 < k1 ? bar_wait_warp(sums_full(0), 0, watch) : true;
+      done = k0 < k1 ? await_sums(sums_full(0), 0, silent, p.late_ns && warp == 2, p.late_ns, watch) : true;
       if (done) {
         fence_after();
 #pragma unroll 1
@@ -383,7 +371,7 @@ cudaError_t launch(Params& p, const TcLaunch& l, cudaStream_t stream) {
   using S = Shape<KIND, NT>;
   p.err = l.err;
   p.limit_ns = TIDE_BULK_TIMEOUT_NS;
-  p.stall_ns = l.stall_ns;
+  p.stall_ns = l.stall_ns, p.late_ns = l.late_ns;
   const int64_t tiles_t = ceil_div(p.tokens, NT), tiles_f = ceil_div(p.features, kRows);
   const int split = split_of<KIND, NT, ACT>(tiles_t * tiles_f, p.steps, l.sms);
   return launch_early(few_tc_kernel<KIND, NT, ACT>, dim3(split, (unsigned)tiles_t, (unsigned)tiles_f), kThreads, S::kSmem,

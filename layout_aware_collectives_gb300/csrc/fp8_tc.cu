@@ -51,7 +51,7 @@ struct Params {
   uint16_t* to;  // out and its rows' length
   int64_t ldo;
   int* err;
-  uint64_t limit_ns, stall_ns;
+  uint64_t limit_ns, stall_ns, late_ns;
 };
 
 __device__ __forceinline__ void fma2(uint64_t& c, uint32_t a, uint32_t b, uint64_t w) {
@@ -67,7 +67,7 @@ __device__ __forceinline__ void add32(uint64_t (&sum)[kHalf / 2], const uint32_t
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) summed_kernel(const __grid_constant__ Params p) {
   constexpr uint32_t kInstr = instr_desc(0, 0, 0, 256, 256);
   extern __shared__ uint8_t raw[];
-  __shared__ uint64_t bars[2 * kStages + 5];
+  __shared__ uint64_t bars[2 * kStages + 6];
   __shared__ uint32_t tmem_at;
   __shared__ int stop;
 
@@ -77,7 +77,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) summed_
   const auto empty = [&](int s) { return bar0 + 8u * (kStages + s); };
   const auto sums_full = [&](int b) { return bar0 + 8u * (2 * kStages + b); };
   const auto sums_empty = [&](int b) { return bar0 + 8u * (2 * kStages + 2 + b); };
-  const uint32_t spare = bar0 + 8u * (2 * kStages + 4);
+  const uint32_t spare = bar0 + 8u * (2 * kStages + 4), silent = spare + 8;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -87,7 +87,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) summed_
     stop = 0;
     for (int s = 0; s < kStages; ++s) bar_init(full(s), 1), bar_init(empty(s), 1);
     for (int b = 0; b < 2; ++b) bar_init(sums_full(b), 1), bar_init(sums_empty(b), 2 * kSumWarps);
-    bar_init(spare, 1);
+    bar_init(spare, 1), bar_init(silent, 1);
     bar_init_fence();
     prefetch_map(&p.a), prefetch_map(&p.b), prefetch_map(&p.out);
   }
@@ -100,7 +100,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) summed_
   after_previous();
 
   if (p.stall_ns) {  // test: a wait on a barrier nothing arrives on runs out
-    if (threadIdx.x == 0) bar_wait(spare, 0, Watch{&stop, p.err, p.stall_ns});
+    if (threadIdx.x == 0) bar_wait(silent, 0, Watch{&stop, p.err, p.stall_ns});
   } else if (warp < 4) {
     // 384 threads start with 168 registers each (64,512); this warpgroup goes
     // down to 56 and the two that hold sums go up to 216: 62,464.
@@ -154,11 +154,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) summed_
           mma_commit<2>(sums_full(b));
         }
       }
-      if (!go) {  // the MMAs in flight, with a limit
-        int never = 0;
-        mma_commit<2>(spare);
-        bar_wait(spare, 0, Watch{&never, p.err, p.limit_ns / 16});
-      }
+      await_mmas<2>(spare, 1, watch);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
@@ -185,7 +181,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) summed_
         const uint32_t s1 = __float_as_uint(next_a * next_b);
         const uint64_t s = ((uint64_t)s1 << 32) | s1;
         if (k + 1 < p.blocks) next_a = __ldg(sa + k + 1), next_b = __ldg(sb + k + 1);
-        if (!bar_wait_warp(sums_full(b), (j / 2) & 1, watch)) {
+        if (!await_sums(sums_full(b), (j / 2) & 1, silent, p.late_ns && warp == 4, p.late_ns, watch)) {
           go = false;
           break;
         }
@@ -249,7 +245,7 @@ template <bool SPLIT>
 __global__ void __launch_bounds__(kScaledThreads, 1) scaled_kernel(const __grid_constant__ Params p) {
   constexpr uint32_t kInstr = instr_desc_scaled(256, 256);
   extern __shared__ uint8_t raw[];
-  __shared__ uint64_t bars[2 * kStages + 3];
+  __shared__ uint64_t bars[2 * kStages + 4];
   __shared__ uint32_t words[2][4][kHalf];  // scales of two batches of four blocks
   __shared__ uint32_t tmem_at;
   __shared__ int stop;
@@ -258,7 +254,7 @@ __global__ void __launch_bounds__(kScaledThreads, 1) scaled_kernel(const __grid_
   const uint32_t bar0 = smem_addr(bars);
   const auto full = [&](int s) { return bar0 + 8u * s; };
   const auto empty = [&](int s) { return bar0 + 8u * (kStages + s); };
-  const uint32_t sums_full = bar0 + 8u * (2 * kStages), sums_empty = sums_full + 8, spare = sums_full + 16;
+  const uint32_t sums_full = bar0 + 8u * (2 * kStages), sums_empty = sums_full + 8, spare = sums_full + 16, silent = sums_full + 24;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t cta = cluster_rank(), rank = cta & 1, leader = SPLIT ? cta & ~1u : 0;
   const uint16_t both = (uint16_t)(3u << leader);  // the pair's CTAs
@@ -271,7 +267,7 @@ __global__ void __launch_bounds__(kScaledThreads, 1) scaled_kernel(const __grid_
     stop = 0;
     // full: the copies, and four warps' scales in each CTA
     for (int s = 0; s < kStages; ++s) bar_init(full(s), 1 + 2 * 4), bar_init(empty(s), 1);
-    bar_init(sums_full, 1), bar_init(sums_empty, 2 * 4), bar_init(spare, 1);
+    bar_init(sums_full, 1), bar_init(sums_empty, 2 * 4), bar_init(spare, 1), bar_init(silent, 1);
     bar_init_fence();
     prefetch_map(&p.a), prefetch_map(&p.b), prefetch_map(&p.out);
   }
@@ -285,7 +281,7 @@ __global__ void __launch_bounds__(kScaledThreads, 1) scaled_kernel(const __grid_
 
   // SPLIT: half of the columns' sums of this warp's 32 rows
   const auto leave_half = [&](int first) {
-    if (!bar_wait_warp(sums_full, 0, watch)) return;
+    if (!await_sums(sums_full, 0, silent, p.late_ns && warp == 4, p.late_ns, watch)) return;
     fence_after();
     const uint32_t lanes = (uint32_t)(warp & 3) * 32;
     leave_sums(smem, tmem + (lanes << 16), lanes + lane, first);
@@ -293,7 +289,7 @@ __global__ void __launch_bounds__(kScaledThreads, 1) scaled_kernel(const __grid_
   };
 
   if (p.stall_ns) {  // test: a wait on a barrier nothing arrives on runs out
-    if (threadIdx.x == 0) bar_wait(spare, 0, Watch{&stop, p.err, p.stall_ns});
+    if (threadIdx.x == 0) bar_wait(silent, 0, Watch{&stop, p.err, p.stall_ns});
   } else if (warp == 0 || warp == 3) {
     if (elected()) {
       const bool load_a = warp == 0;  // one thread loads A, another B
@@ -350,11 +346,7 @@ __global__ void __launch_bounds__(kScaledThreads, 1) scaled_kernel(const __grid_
         }
         if (go) mma_commit<2>(sums_full, both);
       }
-      if (*watch.stop) {  // the MMAs in flight, with a limit
-        int never = 0;
-        mma_commit<2>(spare, both);
-        bar_wait(spare, 0, Watch{&never, p.err, p.limit_ns / 16});
-      }
+      await_mmas<2>(spare, (uint16_t)(1u << leader), watch);
     }
   } else if (warp >= 8) {
     // Scales.  Every warp writes all 128 rows' (A, 4 columns) and both column
@@ -418,7 +410,7 @@ __global__ void __launch_bounds__(kScaledThreads, 1) scaled_kernel(const __grid_
     const uint32_t lanes = (uint32_t)(warp - 4) * 32;
     int i = 0;
     for (int t = pair; t < p.tiles && !SPLIT; t += pairs, ++i) {
-      if (!bar_wait_warp(sums_full, i & 1, watch)) break;
+      if (!await_sums(sums_full, i & 1, silent, p.late_ns && warp == 4, p.late_ns, watch)) break;
       fence_after();
       const TileAt at = tile_at(p.grid, t);
       const int row0 = (at.m * 2 + rank) * kHalf + lanes, col0 = at.n * 2 * kHalf;
@@ -508,7 +500,7 @@ cudaError_t launch_fp8_matmul_tc(const MatmulArgs& a, const TcLaunch& l, cudaStr
   p.to = a.out, p.ldo = a.ldo;
   p.err = l.err;
   p.limit_ns = TIDE_BULK_TIMEOUT_NS;
-  p.stall_ns = l.stall_ns;
+  p.stall_ns = l.stall_ns, p.late_ns = l.late_ns;
   if (!make_map(&p.a, a.a, 1, a.k, a.m, a.k, kBlock, kHalf, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_map(&p.b, a.b, 1, a.k, a.n, a.k, kBlock, kHalf, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_map(&p.out, a.out, 2, a.n, a.m, a.ldo, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))

@@ -81,7 +81,7 @@ struct Params : GatedOut {  // of forward and grad
   int each, full, light, first, first_each, first_more;
   bool one_a, one_b;  // back: wa's, b's and wb's operands are one box each (map_mn)
   int* err;
-  uint64_t limit_ns, stall_ns;
+  uint64_t limit_ns, stall_ns, late_ns;
 };
 
 // 32 codes of one row.  Rows are whole multiples of 8 codes.
@@ -305,7 +305,7 @@ template <int FORM, int ACT, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_constant__ Params p) {
   constexpr bool kBMn = FORM == kBack;
   extern __shared__ uint8_t raw[];
-  __shared__ uint64_t bars[2 * kStages + 5];
+  __shared__ uint64_t bars[2 * kStages + 6];
   __shared__ uint32_t maxima[FORM == kForward ? 2 * kHalf : 1];  // of the checkpoint's half blocks, as exponents
   __shared__ uint32_t tmem_at;
   __shared__ int stop;
@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
   const auto empty = [&](int s) { return bar0 + 8u * (kStages + s); };
   const auto sums_full = [&](int b) { return bar0 + 8u * (2 * kStages + b); };
   const auto sums_empty = [&](int b) { return bar0 + 8u * (2 * kStages + 2 + b); };
-  const uint32_t spare = bar0 + 8u * (2 * kStages + 4);
+  const uint32_t spare = bar0 + 8u * (2 * kStages + 4), silent = spare + 8;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t cta = cluster_rank(), rank = cta & 1, leader = SPLIT ? cta & ~1u : 0;
   const uint16_t both = (uint16_t)(3u << leader);  // the pair's CTAs
@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
     stop = 0;
     for (int s = 0; s < kStages; ++s) bar_init(full(s), 1), bar_init(empty(s), 1);
     for (int b = 0; b < 2; ++b) bar_init(sums_full(b), 1), bar_init(sums_empty(b), 2 * kEpiWarps);
-    bar_init(spare, 1);
+    bar_init(spare, 1), bar_init(silent, 1);
     bar_init_fence();
     prefetch_map(FORM == kBack && !p.tiles ? &p.wa[0] : &p.a[0]), prefetch_map(FORM == kBack && !p.tiles ? &p.wb : &p.b[0]);
   }
@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
   after_previous();
 
   if (p.stall_ns) {  // test: a wait on a barrier nothing arrives on runs out
-    if (threadIdx.x == 0) bar_wait(spare, 0, Watch{&stop, p.err, p.stall_ns});
+    if (threadIdx.x == 0) bar_wait(silent, 0, Watch{&stop, p.err, p.stall_ns});
   } else if (warp == 0 || warp == 3) {
     // One thread loads A, another B: issuing a copy takes long enough that
     // one thread with all four of a stage fell behind the MMAs.
@@ -420,11 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
         }
         if (go) mma_commit<2>(sums_full(b), both);
       }
-      if (*watch.stop) {  // the MMAs in flight, with a limit
-        int never = 0;
-        mma_commit<2>(spare, both);
-        bar_wait(spare, 0, Watch{&never, p.err, p.limit_ns / 16});
-      }
+      await_mmas<2>(spare, (uint16_t)(1u << leader), watch);
     }
   } else if (warp >= 4) {
     Outbox<kBoxes> out{smem + kStages * kStage + (warp - 4) * kBoxes * kBox, 0, lane};
@@ -440,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
         for (int j = 0; j < 8; ++j)
           dh[j] = row < p.rows && col + 8 * j < p.cols ? __ldcs(from + j) : make_uint4(0, 0, 0, 0);
       }
-      if (!bar_wait_warp(sums_full(b), (i / 2) & 1, watch)) break;
+      if (!await_sums(sums_full(b), (i / 2) & 1, silent, p.late_ns && warp == 4, p.late_ns, watch)) break;
       fence_after();
       const uint32_t lanes = (uint32_t)(warp & 3) * 32;
       if constexpr (SPLIT) {
@@ -554,7 +550,7 @@ template <int FORM, int ACT>
 cudaError_t launch(Params& p, const TcLaunch& l, cudaStream_t stream) {
   p.err = l.err;
   p.limit_ns = TIDE_BULK_TIMEOUT_NS;
-  p.stall_ns = l.stall_ns;
+  p.stall_ns = l.stall_ns, p.late_ns = l.late_ns;
   if constexpr (FORM != kBack) {
     p.split = split_pre(p.tiles, p.steps);
     p.share = Share(p.steps, p.split);

@@ -101,6 +101,7 @@ _sig("tide_compute_create", _st, ctypes.POINTER(_vp))
 _sig("tide_compute_destroy", None, _vp)
 _sig("tide_compute_check_device", _st, _vp)
 _sig("tide_compute_set_test_stall", _st, _vp, _i64)
+_sig("tide_compute_set_test_late_warp", _st, _vp, _i64)
 _sig("tide_fp8_store", _st, _vp, _i64, _i64, _vp, _i64, _vp, _vp, ctypes.c_int32, _vp)
 _sig("tide_fp8_restore", _st, _vp, _i64, _i64, _vp, _vp, ctypes.c_int32, _vp, _i64, _vp)
 _sig("tide_fp8_matmul", _st, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, ctypes.c_int32, _vp, _i64, _vp)
@@ -404,6 +405,10 @@ def tide_compute_check_device(compute) -> None:
 
 def tide_compute_set_test_stall(compute, ns: int) -> None:
     _check(_lib.tide_compute_set_test_stall(compute, ns), "tide_compute_set_test_stall")
+
+
+def tide_compute_set_test_late_warp(compute, ns: int) -> None:
+    _check(_lib.tide_compute_set_test_late_warp(compute, ns), "tide_compute_set_test_late_warp")
 
 
 def tide_fp8_store(compute, rows, cols, src, ld_src, codes, scales, block_rows, stream=None) -> None:

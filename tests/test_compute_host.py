@@ -140,3 +140,11 @@ def test_formulas_against_differences(kind):
 
 def test_checkpoint_struct_matches_header():
     assert ctypes.sizeof(tide.tide.GatedCheckpointStruct) == 6 * ctypes.sizeof(ctypes.c_void_p)
+
+
+def test_test_hooks_refuse(compute):
+    lib = tide.tide._lib
+    for hook in (lib.tide_compute_set_test_stall, lib.tide_compute_set_test_late_warp):
+        assert hook(None, 0) == BAD
+        assert hook(compute.handle, -1) == BAD
+        assert hook(compute.handle, 0) == tide.TIDE_OK

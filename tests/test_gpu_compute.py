@@ -787,3 +787,65 @@ def test_matmul_past_32_bits(compute, any_scales):
     compute.fp8_matmul(m, n, k, a, sa, b, sb, out, any_scales=any_scales)
     rows = torch.tensor([0, 2 ** 31 // n, 2 ** 31 // n + 1, m - 1], device="cuda")
     close(out[rows], *ref.matmul(pick8(a, rows), sa[rows], b, sb))
+
+
+# ------------------------------------- one warp's wait runs out, others' do not
+
+def late_calls():
+    """(name, call(compute), results) of every tensor-core kernel: one tile a
+    pair of CTAs and several, whole contractions and split ones."""
+    g = gen(60)
+    calls = []
+
+    def matmul(m, n, k, any_scales=False):
+        (a, sa), (b, sb) = fp8(g, m, k, 1), fp8(g, n, k, 128)
+        out = Guarded(m, n)
+        calls.append((f"matmul {m} {n} {k} {any_scales}",
+                      lambda c: c.fp8_matmul(m, n, k, a, sa, b, sb, out, any_scales=any_scales), [out]))
+
+    def gated(tokens, hidden, ffn):
+        x, (wg, wu), dh = randn(g, tokens, hidden), weights(g, hidden, ffn), randn(g, tokens, ffn)
+        h, dx = Guarded(tokens, ffn), Guarded(tokens, hidden)
+        dwg, dwu = Guarded(ffn, hidden), Guarded(ffn, hidden)
+        ws = torch.empty(tide.gated_workspace_bytes(tokens, hidden, ffn), dtype=torch.uint8, device="cuda")
+        calls.append((f"forward {tokens} {hidden} {ffn}",
+                      lambda c: c.gated_forward(tokens, hidden, ffn, x, wg, wu, h), [h]))
+        calls.append((f"backward {tokens} {hidden} {ffn}",
+                      lambda c: c.gated_backward(tokens, hidden, ffn, dh, x, wg, wu, dx, dwg, dwu, ws), [dx, dwg, dwu]))
+
+    matmul(2, 264, 2064)
+    matmul(64, 136, 8192)
+    matmul(300, 5200, 400)
+    matmul(2100, 5200, 1040)
+    matmul(300, 5200, 400, True)
+    matmul(2100, 5200, 1040, True)
+    matmul(1014, 752, 9200)
+    gated(2, 256, 704)
+    gated(64, 512, 2560)
+    gated(3000, 72, 136)
+    gated(4200, 264, 2056)
+    gated(200, 7904, 2368)
+    return calls
+
+
+def test_warp_whose_wait_runs_out_leaves_alone():
+    """One warp of a kernel gives up while the sums are there: the call ends, the
+    error is reported, nothing outside the outputs is written, and the same call
+    afterwards gives what it gave before."""
+    with tide.Compute() as c:
+        for name, call, results in late_calls():
+            call(c)
+            c.check_device()
+            want = [r.view.clone() for r in results]
+            c.set_test_late_warp(1_000_000)
+            for _ in range(3):
+                call(c)
+                with pytest.raises(tide.TideError) as e:
+                    c.check_device()
+                assert e.value.status == tide.TIDE_ERR_TIMEOUT, name
+                assert all(r.intact() for r in results), name
+            c.set_test_late_warp(0)
+            call(c)
+            c.check_device()
+            for r, w in zip(results, want):
+                assert torch.equal(r.view, w), name
