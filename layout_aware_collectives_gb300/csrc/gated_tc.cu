@@ -163,6 +163,18 @@ __device__ __forceinline__ bool work_at(const Params& p, int pair, int pairs, in
   return true;
 }
 
+// The two warps of 32 tokens, which meet in the epilogue of a checkpoint's
+// tiles, enter it together or not at all: each has its own wait for the sums,
+// and one's may run out where the other's does not.
+__device__ __forceinline__ bool both_halves(int rows32, bool go) {
+  uint32_t both;
+  asm volatile("{ .reg .pred p, q; setp.ne.u32 p, %2, 0; bar.red.and.pred q, %1, 64, p; selp.b32 %0, 1, 0, q; }"
+               : "=r"(both)
+               : "r"(1 + rows32), "r"((uint32_t)go)
+               : "memory");
+  return both != 0;
+}
+
 template <int FORM, int ACT>
 __device__ __forceinline__ void epilogue(const Params& p, const Work& work, uint32_t tmem, int row0, int half,
                                          uint32_t* maxima, const uint4 (&dh)[8], Outbox<kBoxes>& out) {
@@ -436,7 +448,11 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
         for (int j = 0; j < 8; ++j)
           dh[j] = row < p.rows && col + 8 * j < p.cols ? __ldcs(from + j) : make_uint4(0, 0, 0, 0);
       }
-      if (!await_sums(sums_full(b), (i / 2) & 1, silent, p.late_ns && warp == 4, p.late_ns, watch)) break;
+      bool go = await_sums(sums_full(b), (i / 2) & 1, silent, p.late_ns && warp == 4, p.late_ns, watch);
+      if constexpr (FORM == kForward && !SPLIT) {
+        if (p.g8) go = both_halves(warp & 3, go);
+      }
+      if (!go) break;
       fence_after();
       const uint32_t lanes = (uint32_t)(warp & 3) * 32;
       if constexpr (SPLIT) {

@@ -849,3 +849,29 @@ def test_warp_whose_wait_runs_out_leaves_alone():
             c.check_device()
             for r, w in zip(results, want):
                 assert torch.equal(r.view, w), name
+
+
+@pytest.mark.parametrize("tokens,hidden,ffn", [(3000, 72, 136), (4200, 264, 2056), (300, 1544, 2600)])
+def test_half_a_block_s_warp_that_leaves_takes_the_other_along(tokens, hidden, ffn):
+    """A checkpoint's block is two warps' and they meet over its maximum: where
+    one gives up the other does not wait for it."""
+    g = gen(61)
+    x, (wg, wu) = randn(g, tokens, hidden), weights(g, hidden, ffn)
+    h = Guarded(tokens, ffn)
+    bufs, ck = checkpoint(tokens, hidden, ffn, False)
+    with tide.Compute() as c:
+        c.gated_forward(tokens, hidden, ffn, x, wg, wu, h, checkpoint=ck)
+        c.check_device()
+        want = [b.view.clone().view(torch.uint8) for b in [h, *bufs.values()]]
+        c.set_test_late_warp(1_000_000)
+        for _ in range(3):
+            c.gated_forward(tokens, hidden, ffn, x, wg, wu, h, checkpoint=ck)
+            with pytest.raises(tide.TideError) as e:
+                c.check_device()
+            assert e.value.status == tide.TIDE_ERR_TIMEOUT
+            assert h.intact() and all(b.intact() for b in bufs.values())
+        c.set_test_late_warp(0)
+        c.gated_forward(tokens, hidden, ffn, x, wg, wu, h, checkpoint=ck)
+        c.check_device()
+        for b, w in zip([h, *bufs.values()], want):
+            assert torch.equal(b.view.view(torch.uint8), w)
