@@ -875,3 +875,32 @@ def test_half_a_block_s_warp_that_leaves_takes_the_other_along(tokens, hidden, f
         c.check_device()
         for b, w in zip([h, *bufs.values()], want):
             assert torch.equal(b.view.view(torch.uint8), w)
+
+
+# ------------------------- more columns than 65535 tiles of the plain kernels
+
+@pytest.mark.parametrize("tokens,hidden,ffn", [(1, 1, 9_000_001), (2, 3, 8_388_481), (1, 9_000_001, 1), (2, 8_388_481, 3)])
+def test_gated_very_wide(compute, tokens, hidden, ffn):
+    g = gen(tokens + hidden + ffn)
+    x, (wg, wu), dh = randn(g, tokens, hidden), weights(g, hidden, ffn), randn(g, tokens, ffn)
+    h = Guarded(tokens, ffn)
+    compute.gated_forward(tokens, hidden, ffn, x, wg, wu, h)
+    want, gg, uu = ref.gated_forward(x, wg, wu, "silu")
+    bh, eg, eu = ref.gated_forward_bound(x, wg, wu, "silu")
+    close(h.view, want, bh)
+    assert h.intact()
+    got = run_backward(compute, tokens, hidden, ffn, "silu", dh, x, wg, wu)
+    for a, b, e in zip(got, ref.gated_backward_from(dh, gg, uu, x, wg, wu, "silu"),
+                       ref.gated_backward_bound(dh, gg, uu, x, wg, wu, "silu", eg, eu)):
+        close(a, b, e)
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 9_000_001, 16), (3, 8_388_481, 5)])
+@pytest.mark.parametrize("any_scales", [False, True])
+def test_matmul_very_wide(compute, m, n, k, any_scales):
+    g = gen(m + n + k)
+    (a, sa), (b, sb) = fp8(g, m, k, 1, any_scales), fp8(g, n, k, 128, any_scales)
+    out = Guarded(m, n)
+    compute.fp8_matmul(m, n, k, a, sa, b, sb, out, any_scales=any_scales)
+    close(out.view, *ref.matmul(a, sa, b, sb))
+    assert out.intact()
