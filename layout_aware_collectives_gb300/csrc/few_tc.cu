@@ -119,6 +119,8 @@ __global__ void __launch_bounds__(kThreads) few_tc_kernel(const __grid_constant_
   const int token0 = blockIdx.y * NT, feature0 = blockIdx.z * kRows;
   const int k0 = (int)((int64_t)p.steps * rank / split), k1 = (int)((int64_t)p.steps * (rank + 1) / split);
   const Watch watch{&stop, p.err, p.limit_ns};
+  const bool late = p.late_ns && warp == 2;  // test: this warp waits for sums where nothing arrives
+  const Watch sums_watch{&stop, p.err, late ? p.late_ns : p.limit_ns};
 
   if (threadIdx.x == 0) {
     stop = 0;
@@ -139,6 +141,7 @@ __global__ void __launch_bounds__(kThreads) few_tc_kernel(const __grid_constant_
   const bool beside = KIND == kDx && p.beside;
   if (!beside) after_previous();
   bool done = false;  // this warp has its sums in shared memory
+  int filled = 0;     // stages this thread has filled
 
   if (p.stall_ns) {  // test: a wait on a barrier nothing arrives on runs out
     if (threadIdx.x == 0) bar_wait(silent, 0, Watch{&stop, p.err, p.stall_ns});
@@ -166,10 +169,7 @@ __global__ void __launch_bounds__(kThreads) few_tc_kernel(const __grid_constant_
           load_box<false>(at + S::kParts * kWeights, &p.x[0], k * p.step_elems, token0, full(s));
         }
       }
-      // the copies in flight, whoever of the others has left
-      int never = 0;
-      for (int i = max(0, j - S::kStages); i < j; ++i)
-        bar_wait(full(i % S::kStages), (i / S::kStages) & 1, Watch{&never, p.err, p.limit_ns / 16});
+      filled = j;
     }
   } else if (warp == 1) {
     if (elected()) {
@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kThreads) few_tc_kernel(const __grid_constant_
         mma_commit<1>(empty(s));
         if (FP8 || k + 1 == k1) mma_commit<1>(sums_full(b));
       }
-      await_mmas<1>(spare, 1, watch);
+      mma_commit<1>(spare);
     }
   } else {
     const int lanes = (warp & 3) * 32, feature = lanes + lane;  // TMEM lanes follow the warp's index modulo 4
@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(kThreads) few_tc_kernel(const __grid_constant_
         }
         sums_barrier();
         // a warp whose wait ran out goes on meeting the others at the barrier
-        done = done && await_sums(sums_full(b), (j / S::kBufs) & 1, silent, p.late_ns && warp == 2, p.late_ns, watch);
+        done = done && bar_wait_warp(late ? silent : sums_full(b), (j / S::kBufs) & 1, sums_watch);
         if (!done) continue;
         fence_after();
 #pragma unroll
@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(kThreads) few_tc_kernel(const __grid_constant_
         for (int i = 0; i < NT; ++i) leave(i, sum[i]);
       }
     } else {
-      done = k0 < k1 ? await_sums(sums_full(0), 0, silent, p.late_ns && warp == 2, p.late_ns, watch) : true;
+      done = k0 < k1 ? bar_wait_warp(late ? silent : sums_full(0), 0, sums_watch) : true;
       if (done) {
         fence_after();
 #pragma unroll 1
@@ -266,6 +266,11 @@ __global__ void __launch_bounds__(kThreads) few_tc_kernel(const __grid_constant_
     }
   }
   __syncthreads();
+  if (stop && !p.stall_ns) {  // copies and MMAs in flight, with a limit again
+    for (int i = max(0, filled - S::kStages); i < filled; ++i) await(full(i % S::kStages), (i / S::kStages) & 1, watch);
+    if (warp == 1) await(spare, 0, watch);
+    __syncwarp();
+  }
   if (split > 1) cluster_sync();
   if (!p.stall_ns) {
     constexpr int kWarps = kThreads / 32;

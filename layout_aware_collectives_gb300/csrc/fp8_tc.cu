@@ -82,6 +82,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) summed_
   const uint32_t rank = cluster_rank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const Watch watch{&stop, p.err, p.limit_ns};
+  const bool late = p.late_ns && warp == 4;  // test: this warp waits for sums where nothing arrives
+  const Watch sums_watch{&stop, p.err, late ? p.late_ns : p.limit_ns};
 
   if (threadIdx.x == 0) {
     stop = 0;
@@ -130,11 +132,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) summed_
       for (int i = max(0, j - kStages); i < j && go; ++i) go = bar_wait(empty(i % kStages), (i / kStages) & 1, watch);
       // after a wait that ran out: both CTAs' copies in flight, with a limit
       // again; the peer's memory stays until the cluster's last barrier
-      if (!go && rank == 0) {
-        int never = 0;
-        for (int i = max(0, j - kStages); i < j; ++i)
-          bar_wait(full(i % kStages), (i / kStages) & 1, Watch{&never, p.err, p.limit_ns / 16});
-      }
+      if (!go && rank == 0)
+        for (int i = max(0, j - kStages); i < j; ++i) await(full(i % kStages), (i / kStages) & 1, watch);
     } else if (warp == 1 && rank == 0 && elected()) {
       int j = 0;  // blocks so far
       bool go = true;
@@ -154,7 +153,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) summed_
           mma_commit<2>(sums_full(b));
         }
       }
-      await_mmas<2>(spare, 1, watch);
+      mma_commit<2>(spare, 1);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
@@ -181,7 +180,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) summed_
         const uint32_t s1 = __float_as_uint(next_a * next_b);
         const uint64_t s = ((uint64_t)s1 << 32) | s1;
         if (k + 1 < p.blocks) next_a = __ldg(sa + k + 1), next_b = __ldg(sb + k + 1);
-        if (!await_sums(sums_full(b), (j / 2) & 1, silent, p.late_ns && warp == 4, p.late_ns, watch)) {
+        if (!bar_wait_warp(late ? silent : sums_full(b), (j / 2) & 1, sums_watch)) {
           go = false;
           break;
         }
@@ -218,6 +217,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) summed_
     if (lane == 0) stores_done();
   }
   __syncthreads();
+  if (stop && warp == 1 && rank == 0 && !p.stall_ns) {
+    await(spare, 0, watch);  // the MMAs in flight
+    __syncwarp();
+  }
   cluster_sync();
   if (warp == 2) tmem_free<2>(tmem, 512);
 }
@@ -262,6 +265,8 @@ __global__ void __launch_bounds__(kScaledThreads, 1) scaled_kernel(const __grid_
   const int pair = blockIdx.x / (2 * split), pairs = gridDim.x / (2 * split);
   const int k0 = SPLIT ? p.blocks * part / split : 0, k1 = SPLIT ? p.blocks * (part + 1) / split : p.blocks;
   const Watch watch{&stop, p.err, p.limit_ns};
+  const bool late = p.late_ns && warp == 4;  // test: this warp waits for sums where nothing arrives
+  const Watch sums_watch{&stop, p.err, late ? p.late_ns : p.limit_ns};
 
   if (threadIdx.x == 0) {
     stop = 0;
@@ -281,7 +286,7 @@ __global__ void __launch_bounds__(kScaledThreads, 1) scaled_kernel(const __grid_
 
   // SPLIT: half of the columns' sums of this warp's 32 rows
   const auto leave_half = [&](int first) {
-    if (!await_sums(sums_full, 0, silent, p.late_ns && warp == 4, p.late_ns, watch)) return;
+    if (!bar_wait_warp(late ? silent : sums_full, 0, sums_watch)) return;
     fence_after();
     const uint32_t lanes = (uint32_t)(warp & 3) * 32;
     leave_sums(smem, tmem + (lanes << 16), lanes + lane, first);
@@ -316,11 +321,8 @@ __global__ void __launch_bounds__(kScaledThreads, 1) scaled_kernel(const __grid_
       for (int i = max(0, j - kStages); i < j && go; ++i) go = bar_wait(empty(i % kStages), (i / kStages) & 1, watch);
       // after a wait that ran out: both CTAs' copies in flight, with a limit
       // again; the peer's memory stays until the cluster's last barrier
-      if (!go && rank == 0) {
-        int never = 0;
-        for (int i = max(0, j - kStages); i < j; ++i)
-          bar_wait(full(i % kStages), (i / kStages) & 1, Watch{&never, p.err, p.limit_ns / 16});
-      }
+      if (!go && rank == 0)
+        for (int i = max(0, j - kStages); i < j; ++i) await(full(i % kStages), (i / kStages) & 1, watch);
     }
   } else if (warp == 1) {
     if (rank == 0 && elected()) {
@@ -346,7 +348,7 @@ __global__ void __launch_bounds__(kScaledThreads, 1) scaled_kernel(const __grid_
         }
         if (go) mma_commit<2>(sums_full, both);
       }
-      await_mmas<2>(spare, (uint16_t)(1u << leader), watch);
+      mma_commit<2>(spare, (uint16_t)(1u << leader));
     }
   } else if (warp >= 8) {
     // Scales.  Every warp writes all 128 rows' (A, 4 columns) and both column
@@ -410,7 +412,7 @@ __global__ void __launch_bounds__(kScaledThreads, 1) scaled_kernel(const __grid_
     const uint32_t lanes = (uint32_t)(warp - 4) * 32;
     int i = 0;
     for (int t = pair; t < p.tiles && !SPLIT; t += pairs, ++i) {
-      if (!await_sums(sums_full, i & 1, silent, p.late_ns && warp == 4, p.late_ns, watch)) break;
+      if (!bar_wait_warp(late ? silent : sums_full, i & 1, sums_watch)) break;
       fence_after();
       const TileAt at = tile_at(p.grid, t);
       const int row0 = (at.m * 2 + rank) * kHalf + lanes, col0 = at.n * 2 * kHalf;
@@ -447,6 +449,10 @@ __global__ void __launch_bounds__(kScaledThreads, 1) scaled_kernel(const __grid_
     if (lane == 0) stores_done();
   }
   __syncthreads();
+  if (stop && warp == 1 && rank == 0 && !p.stall_ns) {
+    await(spare, 0, watch);  // the MMAs in flight
+    __syncwarp();
+  }
   cluster_sync();
   if constexpr (SPLIT) {
     // Each CTA finishes its share of the pair's rows.

@@ -335,6 +335,8 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
   const int split = SPLIT ? p.split : 1, part = SPLIT ? cta >> 1 : 0;
   const int pair = blockIdx.x / (2 * split), pairs = gridDim.x / (2 * split);
   const Watch watch{&stop, p.err, p.limit_ns};
+  const bool late = p.late_ns && warp == 4;  // test: this warp waits for sums where nothing arrives
+  const Watch sums_watch{&stop, p.err, late ? p.late_ns : p.limit_ns};
 
   if (threadIdx.x == 0) {
     stop = 0;
@@ -396,11 +398,8 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
       for (int i = max(0, j - kStages); i < j && go; ++i) go = bar_wait(empty(i % kStages), (i / kStages) & 1, watch);
       // after a wait that ran out: both CTAs' copies in flight, with a limit
       // again; the peer's memory stays until the cluster's last barrier
-      if (!go && rank == 0) {
-        int never = 0;
-        for (int i = max(0, j - kStages); i < j; ++i)
-          bar_wait(full(i % kStages), (i / kStages) & 1, Watch{&never, p.err, p.limit_ns / 16});
-      }
+      if (!go && rank == 0)
+        for (int i = max(0, j - kStages); i < j; ++i) await(full(i % kStages), (i / kStages) & 1, watch);
     }
   } else if (warp == 1 && rank == 0) {
     if (elected()) {
@@ -432,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
         }
         if (go) mma_commit<2>(sums_full(b), both);
       }
-      await_mmas<2>(spare, (uint16_t)(1u << leader), watch);
+      mma_commit<2>(spare, (uint16_t)(1u << leader));
     }
   } else if (warp >= 4) {
     Outbox<kBoxes> out{smem + kStages * kStage + (warp - 4) * kBoxes * kBox, 0, lane};
@@ -448,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
         for (int j = 0; j < 8; ++j)
           dh[j] = row < p.rows && col + 8 * j < p.cols ? __ldcs(from + j) : make_uint4(0, 0, 0, 0);
       }
-      bool go = await_sums(sums_full(b), (i / 2) & 1, silent, p.late_ns && warp == 4, p.late_ns, watch);
+      bool go = bar_wait_warp(late ? silent : sums_full(b), (i / 2) & 1, sums_watch);
       if constexpr (FORM == kForward && !SPLIT) {
         if (p.g8) go = both_halves(warp & 3, go);
       }
@@ -468,6 +467,10 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
     if (lane == 0) stores_done();
   }
   __syncthreads();
+  if (stop && warp == 1 && rank == 0 && !p.stall_ns) {
+    await(spare, 0, watch);  // the MMAs in flight
+    __syncwarp();
+  }
   cluster_sync();
   if constexpr (SPLIT) {
     // Each CTA finishes its share of the pair's rows.

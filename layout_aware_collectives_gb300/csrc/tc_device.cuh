@@ -108,12 +108,13 @@ __device__ __forceinline__ bool bar_wait_warp(uint32_t bar, uint32_t parity, con
   return __all_sync(0xffffffffu, bar_wait(bar, parity, w));
 }
 
-// A warp's wait for finished sums.  late (test): what it waits for is there,
-// but its wait runs out, on a barrier nothing arrives on.
-__device__ __forceinline__ bool await_sums(uint32_t bar, uint32_t parity, uint32_t silent, bool late, uint64_t late_ns,
-                                           const Watch& w) {
-  if (!bar_wait_warp(bar, parity, w)) return false;
-  return !late || bar_wait_warp(silent, 0, Watch{w.stop, w.err, late_ns});
+// What is in flight after a wait ran out: copies, or MMAs (whose issuing thread
+// ends with a commit on a spare barrier).  Every role has left, so `stop` is
+// set, and a CTA frees TMEM and ends only behind these.  Where no wait ran out
+// the last sums were waited for, and with them all of it.
+__device__ __forceinline__ void await(uint32_t bar, uint32_t parity, const Watch& w) {
+  int never = 0;
+  bar_wait(bar, parity, Watch{&never, w.err, w.limit_ns / 16});
 }
 
 // ------------------------------------------------------- tensor-map copies
@@ -262,16 +263,6 @@ __device__ __forceinline__ void mma_commit(uint32_t bar, uint16_t ctas = 3) {
         : "memory");
   else
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-}
-
-// The end of the thread that issues the MMAs: those in flight have completed,
-// whatever ran out elsewhere, so that TMEM can be freed and the stages with
-// the CTA.  cta: this CTA's bit among the cluster's.
-template <int GROUP>
-__device__ __forceinline__ void await_mmas(uint32_t spare, uint16_t cta, const Watch& w) {
-  int never = 0;
-  mma_commit<GROUP>(spare, cta);
-  bar_wait(spare, 0, Watch{&never, w.err, w.limit_ns});
 }
 
 #define TIDE_R8(v, i) "=r"(v[i]), "=r"(v[i + 1]), "=r"(v[i + 2]), "=r"(v[i + 3]), "=r"(v[i + 4]), "=r"(v[i + 5]), \
