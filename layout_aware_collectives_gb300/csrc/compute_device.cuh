@@ -55,6 +55,42 @@ __device__ __forceinline__ uint32_t exponent_bytes(float s) {
   return ((b & 0x7fffffu) == 0 && e - 1u < 254u ? e : 255u) * 0x01010101u;
 }
 
+// Two 32-bit operations as one instruction: c += (a, b) * w.
+__device__ __forceinline__ void fma2(uint64_t& c, uint32_t a, uint32_t b, uint64_t w) {
+  asm("{ .reg .b64 v; mov.b64 v, {%1, %2}; fma.rn.f32x2 %0, v, %3, %0; }" : "+l"(c) : "r"(a), "r"(b), "l"(w));
+}
+// c += (a, b) * v * w, in this order.
+__device__ __forceinline__ void mul_fma2(uint64_t& c, uint32_t a, uint32_t b, uint64_t v, uint64_t w) {
+  asm("{ .reg .b64 t; mov.b64 t, {%1, %2}; mul.rn.f32x2 t, t, %3; fma.rn.f32x2 %0, t, %4, %0; }"
+      : "+l"(c)
+      : "r"(a), "r"(b), "l"(v), "l"(w));
+}
+__device__ __forceinline__ uint64_t twice(float v) {
+  const uint32_t b = __float_as_uint(v);
+  return ((uint64_t)b << 32) | b;
+}
+
+// Neither zero, subnormal, infinite nor NaN.
+__device__ __forceinline__ bool normal(float v) { return (__float_as_uint(v) & 0x7fffffffu) - 0x800000u < 0x7f000000u; }
+
+// A block's two scales may have a product that fp32 does not hold where it
+// holds the result.  So the block's sum v, a multiple of 2^-18 below 2^25, is
+// multiplied by one scale w and then, in the multiply-add, by the other, x: v w
+// stays a normal number for w within 2^-100 and 2^100.  Outside, w leaves a
+// power of two to x.  Returns it, 1 within.  No branches: this stands in every
+// block's way.
+__device__ __forceinline__ float leave_power(float& w) {
+  const float m = fabsf(w);
+  const bool high = m > 0x1p100f, low = m < 0x1p-100f;
+  w *= high ? 0x1p-27f : low ? 0x1p49f : 1.0f;
+  return high ? 0x1p27f : low ? 0x1p-49f : 1.0f;
+}
+// x takes it.  Past fp32 the largest number does: v w x is past it too, or v is 0.
+__device__ __forceinline__ float take_power(float x, float power) {
+  const float r = x * power;
+  return fabsf(x) < CUDART_INF_F ? fminf(fmaxf(r, -0x1.fffffep127f), 0x1.fffffep127f) : r;
+}
+
 // A block's largest magnitude is taken with fmaxf, which passes over NaN.  If
 // it is infinite, infinities are made NaN (which is what their codes are)
 // and the maximum is taken again: so finite blocks pay for no checks.

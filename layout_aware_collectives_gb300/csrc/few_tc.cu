@@ -205,48 +205,65 @@ __global__ void __launch_bounds__(kThreads) few_tc_kernel(const __grid_constant_
       const int e = threadIdx.x - 64;  // the token whose scales this thread fetches
       const float* sx = p.sx + (int64_t)min(token0 + e, p.tokens - 1) * p.steps;
       const float* sw = p.sw + (int64_t)blockIdx.z * p.steps;
-      float sum[NT];
+      uint64_t sum[NT / 2];
 #pragma unroll
-      for (int i = 0; i < NT; ++i) sum[i] = 0.0f;
+      for (int i = 0; i < NT / 2; ++i) sum[i] = 0;
+      // Each step's scales: the tokens' in shared memory, the weights' as the
+      // result.  A step ahead, behind the issue of the read of the sums.
       float next_x = 0.0f, next_w = 0.0f;
-      if (e < NT && k0 < k1) next_x = __ldg(sx + k0), next_w = __ldg(sw + k0);
+      const auto fetch = [&](int k) {
+        if (k >= k1) return;
+        next_w = __ldg(sw + k);
+        if (e < NT) next_x = __ldg(sx + k);
+      };
+      const auto prepare = [&](int k, int j) {
+        float w = p.any_scales ? next_w : power_of_two(next_w);
+        const float power = leave_power(w);
+        if (e < NT) scales[j & 3][e] = take_power(p.any_scales ? next_x : power_of_two(next_x), power);
+        fetch(k + 1);
+        return twice(w);
+      };
+      fetch(k0);
+      uint64_t next = prepare(k0, 0);
       done = true;
       int j = 0;
       for (int k = k0; k < k1; ++k, ++j) {
         const int b = j % S::kBufs;
-        if (e < NT) {
-          scales[j & 3][e] = p.any_scales ? next_x * next_w : power_of_two(next_x) * power_of_two(next_w);
-          if (k + 1 < k1) next_x = __ldg(sx + k + 1), next_w = __ldg(sw + k + 1);
-        }
         sums_barrier();
         // a warp whose wait ran out goes on meeting the others at the barrier
         done = done && bar_wait_warp(late ? silent : sums_full(b), (j / S::kBufs) & 1, sums_watch);
         if (!done) continue;
         fence_after();
+        const uint64_t w = next;
+        uint32_t v[NT / kChunk][kChunk];
+        if constexpr (NT == 16) {
+          tmem_issue16(mine + b * NT, v[0]);
+        } else {
 #pragma unroll
-        for (int c = 0; c < NT / kChunk; ++c) {
-          uint32_t v[kChunk];
-          tmem_read(mine + b * NT + c * kChunk, v);
-          if (c == NT / kChunk - 1) {
-            fence_before();
-            __syncwarp();
-            if (lane == 0) bar_arrive(sums_empty(b));
-          }
+          for (int c = 0; c < NT / kChunk; ++c) tmem_issue32(mine + b * NT + c * kChunk, v[c]);
+        }
+        next = prepare(k + 1, j + 1);
+        if constexpr (NT == 64)
+          tmem_arrived(v[0], v[1]);
+        else
+          tmem_arrived(v[0]);
+        fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(sums_empty(b));
+#pragma unroll
+        for (int c = 0; c < NT / kChunk; ++c)
 #pragma unroll
           for (int i = 0; i < kChunk; i += 4) {
-            const float4 s = *(const float4*)&scales[j & 3][c * kChunk + i];
-            float* to = sum + c * kChunk + i;
-            to[0] = fmaf(as_f(v[i]), s.x, to[0]);
-            to[1] = fmaf(as_f(v[i + 1]), s.y, to[1]);
-            to[2] = fmaf(as_f(v[i + 2]), s.z, to[2]);
-            to[3] = fmaf(as_f(v[i + 3]), s.w, to[3]);
+            const ulonglong2 s = *(const ulonglong2*)&scales[j & 3][c * kChunk + i];
+            uint64_t* to = sum + (c * kChunk + i) / 2;
+            mul_fma2(to[0], v[c][i], v[c][i + 1], w, s.x);
+            mul_fma2(to[1], v[c][i + 2], v[c][i + 3], w, s.y);
           }
-        }
       }
       if (done) {
         // every warp's last read of the stages is over: all MMAs completed
 #pragma unroll
-        for (int i = 0; i < NT; ++i) leave(i, sum[i]);
+        for (int i = 0; i < NT; ++i) leave(i, as_f((uint32_t)(sum[i / 2] >> 32 * (i & 1))));
       }
     } else {
       done = k0 < k1 ? bar_wait_warp(late ? silent : sums_full(0), 0, sums_watch) : true;

@@ -54,14 +54,15 @@ struct Params {
   uint64_t limit_ns, stall_ns, late_ns;
 };
 
-__device__ __forceinline__ void fma2(uint64_t& c, uint32_t a, uint32_t b, uint64_t w) {
-  asm("{ .reg .b64 v; mov.b64 v, {%1, %2}; fma.rn.f32x2 %0, v, %3, %0; }" : "+l"(c) : "r"(a), "r"(b), "l"(w));
-}
-
 template <int C>
 __device__ __forceinline__ void add32(uint64_t (&sum)[kHalf / 2], const uint32_t (&v)[32], uint64_t s) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) fma2(sum[C * 16 + i], v[2 * i], v[2 * i + 1], s);
+}
+
+__device__ __forceinline__ void times32(uint32_t (&v)[32], float w) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(as_f(v[i]) * w);
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) summed_kernel(const __grid_constant__ Params p) {
@@ -177,8 +178,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) summed_
       float next_a = __ldg(sa), next_b = __ldg(sb);
       for (int k = 0; k < p.blocks; ++k, ++j) {
         const int b = j & 1;
-        const uint32_t s1 = __float_as_uint(next_a * next_b);
-        const uint64_t s = ((uint64_t)s1 << 32) | s1;
+        float both = next_a * next_b, w = next_b;
+        const bool apart = __any_sync(0xffffffffu, !normal(both));  // the sums times w, then times both
+        if (apart) {
+          const float power = leave_power(w);
+          both = take_power(next_a, power);
+        }
+        const uint64_t s = twice(both);
         if (k + 1 < p.blocks) next_a = __ldg(sa + k + 1), next_b = __ldg(sb + k + 1);
         if (!bar_wait_warp(late ? silent : sums_full(b), (j / 2) & 1, sums_watch)) {
           go = false;
@@ -191,6 +197,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) summed_
         tmem_issue32(from, v);
         tmem_issue32(from + 32, x);
         tmem_arrived(v, x);
+        if (apart) times32(v, w), times32(x, w);
         add32<0>(sum, v, s);
         tmem_issue32(from + 64, v);
         add32<1>(sum, x, s);
@@ -199,6 +206,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) summed_
         fence_before();
         __syncwarp();
         if (lane == 0) bar_arrive_peer(peer_addr(sums_empty(b), 0));
+        if (apart) times32(v, w), times32(x, w);
         add32<2>(sum, v, s);
         add32<3>(sum, x, s);
       }

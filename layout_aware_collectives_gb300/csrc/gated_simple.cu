@@ -326,18 +326,19 @@ __global__ void __launch_bounds__(kThreads) matmul_simple_kernel(MatmulArgs a) {
           return two(a.b + (col0 + n) * a.k + k0 + k, 1, k, wide, col0 + n < a.n);
         });
     const auto scale = [&](float s) { return a.any_scales ? s : power_of_two(s); };
-    const float sb = scale(a.sb[(WIDE ? col0 / kTn : blockIdx.y) * nb + kb]);
+    float sb = scale(a.sb[(WIDE ? col0 / kTn : blockIdx.y) * nb + kb]);
+    const float power = leave_power(sb);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int64_t row = row0 + element(i, 0, 2 * h).row;
-        const float s = row < a.m ? scale(a.sa[row * nb + kb]) * sb : 0.0f;
+        const float s = row < a.m ? take_power(scale(a.sa[row * nb + kb]), power) : 0.0f;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
           for (int q = 0; q < 2; ++q)
-            total.v[i][j][2 * h + q] = fmaf(sums[0].v[i][j][2 * h + q], s, total.v[i][j][2 * h + q]);
+            total.v[i][j][2 * h + q] = fmaf(sums[0].v[i][j][2 * h + q] * sb, s, total.v[i][j][2 * h + q]);
       }
   }
   write_tile(total, a.out, a.ldo, row0, col0, a.m, a.n);

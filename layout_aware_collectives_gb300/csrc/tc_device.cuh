@@ -296,10 +296,20 @@ __device__ __forceinline__ void tmem_issue32(uint32_t addr, uint32_t (&v)[32]) {
       : "r"(addr)
       : "memory");
 }
+__device__ __forceinline__ void tmem_issue16(uint32_t addr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : TIDE_R8(v, 0), TIDE_R8(v, 8)
+      : "r"(addr)
+      : "memory");
+}
 #define TIDE_RW8(v, i) "+r"(v[i]), "+r"(v[i + 1]), "+r"(v[i + 2]), "+r"(v[i + 3]), "+r"(v[i + 4]), "+r"(v[i + 5]), \
                        "+r"(v[i + 6]), "+r"(v[i + 7])
 #define TIDE_RW32(v) TIDE_RW8(v, 0), TIDE_RW8(v, 8), TIDE_RW8(v, 16), TIDE_RW8(v, 24)
 // Waits for every read issued so far; no use of v moves ahead of it.
+__device__ __forceinline__ void tmem_arrived(uint32_t (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : TIDE_RW8(v, 0), TIDE_RW8(v, 8)::"memory");
+}
 __device__ __forceinline__ void tmem_arrived(uint32_t (&v)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" : TIDE_RW32(v)::"memory");
 }

@@ -904,3 +904,61 @@ def test_matmul_very_wide(compute, m, n, k, any_scales):
     compute.fp8_matmul(m, n, k, a, sa, b, sb, out, any_scales=any_scales)
     close(out.view, *ref.matmul(a, sa, b, sb))
     assert out.intact()
+
+
+# ------------------------------- two scales whose product fp32 does not hold
+
+# few tokens; unaligned; 256-row tiles; clusters of them
+WIDE_SCALE_SHAPES = [(4, 264, 1024), (40, 264, 1024), (7, 130, 1027), (300, 5200, 1024), (1014, 752, 9216)]
+
+
+@pytest.mark.parametrize("m,n,k", WIDE_SCALE_SHAPES)
+@pytest.mark.parametrize("sa,sb,any_scales", [(2.0 ** 70, 2.0 ** 60, False), (2.0 ** 70, 2.0 ** 60, True), (2.0 ** 127, 2.0 ** 127, False),
+                                              (2.0 ** 127, 2.0 ** 127, True), (-1.5 * 2.0 ** 70, 1.25 * 2.0 ** 60, True)])
+def test_matmul_scales_whose_product_is_past_fp32(compute, m, n, k, sa, sb, any_scales):
+    """A sum of zeros is zero whatever its scales; one small product is finite
+    where the value is; what is past fp32 is infinite.  Other blocks of the row
+    are as they were."""
+    one = torch.ones(m, n, dtype=torch.float64, device="cuda")
+    a = torch.zeros(m, k, device="cuda").to(torch.float8_e4m3fn)
+    b = torch.zeros(n, k, device="cuda").to(torch.float8_e4m3fn)
+    nb = -(-k // 128)
+    za, zb = torch.full((m, nb), sa, device="cuda"), torch.full((-(-n // 128), nb), sb, device="cuda")
+    za[:, 1], zb[:, 1] = 1.0, 0.5
+    bv = b.view(torch.uint8)
+    av = a.view(torch.uint8)
+    bv[:, 128], av[:, 128] = 0x38, 0x40  # 1 and 2: the second block's sum is 2, its value 1
+    out = Guarded(m, n)
+    compute.fp8_matmul(m, n, k, a, za, b, zb, out, any_scales=any_scales)
+    close(out.view, one, 0.0 * one)
+    if abs(sa * sb) < 2.0 ** 140:
+        av[1, 5], bv[:, 5] = 0x01, 0x01  # 2^-18 in all
+        compute.fp8_matmul(m, n, k, a, za, b, zb, out, any_scales=any_scales)
+        want = one.clone()
+        want[1] += 2.0 ** -18 * sa * sb
+        close(out.view, want, want.abs() * ref.U_BF16)
+    av[2, 7], bv[:, 7] = 0x7E, 0x7E
+    compute.fp8_matmul(m, n, k, a, za, b, zb, out, any_scales=any_scales)
+    assert (out.view[2] == math.copysign(math.inf, sa)).all()
+    assert torch.isfinite(out.view[0]).all() and torch.isfinite(out.view[3:]).all() and out.intact()
+
+
+@pytest.mark.parametrize("m,n,k", WIDE_SCALE_SHAPES)
+@pytest.mark.parametrize("sa,sb,any_scales", [(2.0 ** -80, 2.0 ** -72, False), (2.0 ** -80, 2.0 ** -72, True),
+                                              (2.0 ** -126, 2.0 ** -26, False), (1.5 * 2.0 ** -80, 1.25 * 2.0 ** -72, True),
+                                              (1e-42, 2.0 ** -12, True)])
+def test_matmul_scales_whose_product_is_below_fp32(compute, m, n, k, sa, sb, any_scales):
+    """Block sums times such scales add up to what fp32 holds.  Every term is
+    up to 2^-126, of which fp32 keeps at least 2^-149: within 2^-149 for each
+    block, its sum's and the scales' own rounding beside it."""
+    a = torch.full((m, k), 448.0, device="cuda").to(torch.float8_e4m3fn)
+    b = torch.full((n, k), 416.0, device="cuda").to(torch.float8_e4m3fn)
+    nb = -(-k // 128)
+    za, zb = torch.full((m, nb), sa, device="cuda"), torch.full((-(-n // 128), nb), sb, device="cuda")
+    out = Guarded(m, n)
+    compute.fp8_matmul(m, n, k, a, za, b, zb, out, any_scales=any_scales)
+    want = ref.blocks_value(a, za, 1) @ ref.blocks_value(b, zb, 128).T
+    assert float(want.min()) > 2.0 ** -126
+    off = want * (k + 8) * ref.U_F32 + nb * 2.0 ** -149
+    close(out.view, want, off + ref.U_BF16 * (want + off))
+    assert out.intact()
