@@ -117,20 +117,33 @@ __device__ __forceinline__ float2 e4m3_values(uint16_t v) {
   return f;
 }
 
+// sigmoid(v) from e = exp(-|v|): 1 or e over 1 + e.  exp(-v) itself passes
+// 2^126 at v = -87.3, where __fdividef gives 0, and then fp32's range, both while
+// e is still a normal number.
+struct Sigmoid {
+  float over, under;
+};
+__device__ __forceinline__ Sigmoid sigmoid(float v) {
+  const float e = __expf(-fabsf(v));
+  return Sigmoid{v < 0.0f ? e : 1.0f, 1.0f + e};
+}
+
 // The tanh form of GELU is g * sigmoid(2 z), z = sqrt(2/pi) (g + 0.044715 g^3),
 // since 0.5 (1 + tanh z) = sigmoid(2 z).  Past |g| = 64 the sigmoid is 0 or 1
 // in 32 bits; the clamp keeps the cube and the square there finite.
 __device__ __forceinline__ float gelu_clamp(float g) { return fminf(fmaxf(g, -64.0f), 64.0f); }
 __device__ __forceinline__ float gelu_sigmoid(float c) {
-  const float z = 0.7978845608028654f * (c + 0.044715f * c * c * c);
-  return __fdividef(1.0f, 1.0f + __expf(-2.0f * z));
+  const Sigmoid s = sigmoid(2.0f * 0.7978845608028654f * (c + 0.044715f * c * c * c));
+  return __fdividef(s.over, s.under);
 }
 
-// Gate activations, in 32 bits.  expf's argument may overflow to infinity,
-// which gives the sigmoid's limit 0.
+// Gate activations, in 32 bits.
 template <int ACT>
 __device__ __forceinline__ float activation(float g) {
-  if (ACT == TIDE_ACT_SILU) return __fdividef(g, 1.0f + __expf(-g));
+  if (ACT == TIDE_ACT_SILU) {
+    const Sigmoid s = sigmoid(g);
+    return __fdividef(g * s.over, s.under);
+  }
   return g * gelu_sigmoid(gelu_clamp(g));
 }
 
@@ -138,7 +151,8 @@ __device__ __forceinline__ float activation(float g) {
 template <int ACT>
 __device__ __forceinline__ float2 activation_grad(float g) {
   if (ACT == TIDE_ACT_SILU) {
-    const float s = __fdividef(1.0f, 1.0f + __expf(-g));
+    const Sigmoid q = sigmoid(g);
+    const float s = __fdividef(q.over, q.under);
     return make_float2(g * s, s * (1.0f + g * (1.0f - s)));
   }
   const float c = gelu_clamp(g);

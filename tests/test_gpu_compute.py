@@ -962,3 +962,56 @@ def test_matmul_scales_whose_product_is_below_fp32(compute, m, n, k, sa, sb, any
     off = want * (k + 8) * ref.U_F32 + nb * 2.0 ** -149
     close(out.view, want, off + ref.U_BF16 * (want + off))
     assert out.intact()
+
+
+# ------------------------------------------------- gates far below zero
+
+FAR_SHAPES = [(1, 8, 136), (40, 264, 392), (3, 9, 131), (3000, 72, 136)]  # few tokens, plain kernels, 256-row tiles
+
+
+@pytest.mark.parametrize("tokens,hidden,ffn", FAR_SHAPES)
+@pytest.mark.parametrize("kept", [False, True])
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+def test_gates_far_below_zero(compute, tokens, hidden, ffn, kept, kind):
+    """The activations fall to 1e-37 and on into the subnormal numbers: what
+    fp32 holds of the sigmoid is there in h, dU and dG.  Rounding as
+    ref.arithmetic has it, two units of the smallest subnormal number times
+    what the sigmoid is multiplied by, bf16's rounding last."""
+    if kept:  # as e4m3 has them
+        values = [-80.0, -88.0, -96.0] if kind == "silu" else [-9.0, -10.0, -11.0]
+    elif kind == "silu":
+        values = [-80.0, -84.0, -87.0, -87.5, -88.0, -88.5, -89.0, -90.0, -92.0, -94.0, -96.0]
+    else:
+        values = [-9.5, -9.875, -10.0, -10.0625, -10.125, -10.1875, -10.25, -10.375, -10.5, -10.625]
+    values = torch.tensor(values, device="cuda")
+    g = values[torch.arange(ffn, device="cuda") % len(values)]
+    up = 2.0 ** 90
+    x = torch.zeros(tokens, hidden, dtype=torch.bfloat16, device="cuda")
+    x[:, :2] = 1.0
+    wg, wu = (torch.zeros(ffn, hidden, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    wg[:, 0], wu[:, 1] = g.bfloat16(), up
+    dh = torch.ones(tokens, ffn, dtype=torch.bfloat16, device="cuda")
+    gd = g.double()
+    a, d = ref.act(gd, kind), ref.act_grad(gd, kind)
+    rel = ref.arithmetic(gd, kind)
+    slope = 1.0 if kind == "silu" else 2 * math.sqrt(2 / math.pi) * (1 + 3 * 0.044715 * gd ** 2)
+    off_a, off_d = gd.abs() * 2.0 ** -148, (1 + gd.abs() * slope) * 2.0 ** -148
+    tiny = 2.0 ** -134  # half of bf16's smallest subnormal number
+
+    def rounded(v, e):
+        return e + ref.U_BF16 * (v.abs() + e) + tiny
+
+    h = Guarded(tokens, ffn)
+    bufs, ck = checkpoint(tokens, hidden, ffn, False) if kept else ({}, None)
+    compute.gated_forward(tokens, hidden, ffn, x, wg, wu, h, activation=kind, checkpoint=ck)
+    one = torch.ones(tokens, 1, dtype=torch.float64, device="cuda")
+    want_h, bound_h = one * (a * up), one * rounded(a * up, (a.abs() * rel + off_a) * up)
+    close(h.view, want_h, bound_h)
+    h.t.zero_()
+    _, dwg, dwu = run_backward(compute, tokens, hidden, ffn, kind, dh, x, wg, wu, ck, h=h)
+    close(h.view, want_h, bound_h)
+    sums = tokens * (tokens + 8) * ref.U_F32
+    for got, v, scale, off in ((dwg, d, up, off_d), (dwu, a, 1.0, off_a)):
+        e = rounded(v * scale, (v.abs() * 2 * rel + off) * scale)  # dG or dU
+        want = tokens * v * scale
+        close(got[:, 0], want, rounded(want, tokens * e + sums * (v.abs() * scale + e)))
