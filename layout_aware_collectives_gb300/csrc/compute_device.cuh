@@ -158,7 +158,8 @@ __device__ __forceinline__ float2 activation_grad(float g) {
   const float c = gelu_clamp(g);
   const float s = gelu_sigmoid(c);
   const float dz = 0.7978845608028654f * (1.0f + 3.0f * 0.044715f * c * c);
-  return make_float2(g * s, s + 2.0f * g * s * (1.0f - s) * dz);
+  // 2 g alone may pass fp32's range; its factors are 0 long before
+  return make_float2(g * s, s + 2.0f * (g * (s * (1.0f - s) * dz)));
 }
 
 }  // namespace tide

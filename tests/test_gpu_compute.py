@@ -1015,3 +1015,27 @@ def test_gates_far_below_zero(compute, tokens, hidden, ffn, kept, kind):
         e = rounded(v * scale, (v.abs() * 2 * rel + off) * scale)  # dG or dU
         want = tokens * v * scale
         close(got[:, 0], want, rounded(want, tokens * e + sums * (v.abs() * scale + e)))
+
+
+@pytest.mark.parametrize("tokens,hidden,ffn", FAR_SHAPES)
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+@pytest.mark.parametrize("kept", [False, True])
+def test_gates_near_the_largest_number(compute, tokens, hidden, ffn, kind, kept):
+    """Twice the gate is past fp32, the slope 1 or 0 is not: everything here is
+    a power of two or exact in bf16, so every result is."""
+    x = torch.zeros(tokens, hidden, dtype=torch.bfloat16, device="cuda")
+    x[:, 0], x[:, 1] = 2.0 ** 64, 1.0
+    wg, wu = (torch.zeros(ffn, hidden, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    wg[::2, 0], wg[1::2, 0], wu[:, 1] = 1.75 * 2.0 ** 63, -1.75 * 2.0 ** 63, 1.0
+    dh = torch.zeros(tokens, ffn, dtype=torch.bfloat16, device="cuda")
+    dh[0] = 2.0 ** -70
+    h = Guarded(tokens, ffn)
+    bufs, ck = checkpoint(tokens, hidden, ffn, False) if kept else ({}, None)
+    compute.gated_forward(tokens, hidden, ffn, x, wg, wu, h, activation=kind, checkpoint=ck)
+    on = (torch.arange(ffn, device="cuda") % 2 == 0).double()
+    g = 1.75 * 2.0 ** 127
+    assert torch.equal(h.view.double(), (on * g).expand(tokens, ffn))
+    _, dwg, dwu = run_backward(compute, tokens, hidden, ffn, kind, dh, x, wg, wu, ck)
+    assert torch.equal(dwg[:, 1].double(), on * 2.0 ** -70)
+    assert torch.equal(dwg[:, 0].double(), on * 2.0 ** -6)
+    assert torch.equal(dwu[:, 1].double(), on * g * 2.0 ** -70)
