@@ -518,7 +518,8 @@ TIDE_API void tide_compute_destroy(tide_compute_t compute);
 /* Synchronises the device, then reads and clears the handle's error word:
  * TIDE_ERR_TIMEOUT if, since the last check, a bounded wait inside one of its
  * tensor-core kernels ran out (that call's outputs are incomplete), else
- * TIDE_OK.  The wait bound is 2 s. */
+ * TIDE_OK.  The handle's device has to be the current one, as for every call.
+ * The wait bound is 2 s. */
 TIDE_API tide_status_t tide_compute_check_device(tide_compute_t compute);
 
 /* Test hook for the bounded waits, as tide_layout_set_test_stall: with ns > 0

@@ -62,22 +62,26 @@ bool capturing(cudaStream_t stream) {
   return st == cudaStreamCaptureStatusActive;
 }
 
+// The current device, which is a bound handle's.
+tide_status_t current_device(const tide_compute_s* c, int* dev) {
+  const cudaError_t e = cudaGetDevice(dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  if (c->device >= 0 && *dev != c->device)
+    return invalid("handle is bound to device " + std::to_string(c->device) + " but device " + std::to_string(*dev) +
+                   " is current");
+  return TIDE_OK;
+}
+
 // Binds the handle to the current device on first use.
 tide_status_t bind(tide_compute_s* c, cudaStream_t stream) {
   std::lock_guard<std::mutex> g(c->mu);
   int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-  if (c->device >= 0) {
-    if (dev != c->device)
-      return invalid("handle is bound to device " + std::to_string(c->device) + " but device " + std::to_string(dev) +
-                     " is current");
-    return TIDE_OK;
-  }
+  TIDE_TRY(current_device(c, &dev));
+  if (c->device >= 0) return TIDE_OK;
   if (capturing(stream))
     return set_error(TIDE_ERR_UNSUPPORTED,
                      "the handle's first call sets it up on the device and cannot be captured; make one call before");
-  e = cudaDeviceGetAttribute(&c->num_sms, cudaDevAttrMultiProcessorCount, dev);
+  cudaError_t e = cudaDeviceGetAttribute(&c->num_sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute(MultiProcessorCount)");
   static std::mutex once;  // the set-up's results are shared by all handles
   std::lock_guard<std::mutex> o(once);
@@ -158,6 +162,8 @@ tide_status_t tide_compute_check_device(tide_compute_t c) try {
   if (!c) return invalid("compute is NULL");
   std::lock_guard<std::mutex> g(c->mu);
   if (c->device < 0) return TIDE_OK;  // nothing launched yet
+  int dev = 0;
+  TIDE_TRY(current_device(c, &dev));  // another device's end says nothing of this handle's kernels
   const cudaError_t e = cudaDeviceSynchronize();
   if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize");
   volatile int* err = c->err;
