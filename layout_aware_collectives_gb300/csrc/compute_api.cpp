@@ -81,15 +81,13 @@ tide_status_t bind(tide_compute_s* c, cudaStream_t stream) {
   if (capturing(stream))
     return set_error(TIDE_ERR_UNSUPPORTED,
                      "the handle's first call sets it up on the device and cannot be captured; make one call before");
-  cudaError_t e = cudaDeviceGetAttribute(&c->num_sms, cudaDevAttrMultiProcessorCount, dev);
+  cudaError_t e = cudaDeviceGetAttribute(&c->dev.sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute(MultiProcessorCount)");
-  static std::mutex once;  // the set-up's results are shared by all handles
-  std::lock_guard<std::mutex> o(once);
-  e = gated_tc_prepare(&c->pairs);
-  if (e == cudaSuccess) e = fp8_tc_prepare();
-  if (e == cudaSuccess) e = few_tc_prepare();
+  e = gated_tc_prepare(&c->dev);
+  if (e == cudaSuccess) e = fp8_tc_prepare(&c->dev);
+  if (e == cudaSuccess) e = few_tc_prepare(&c->dev);
   if (e != cudaSuccess) return cuda_fail(e, "set-up of the tensor-core kernels");
-  if (c->pairs < 1) return set_error(TIDE_ERR_CUDA, "the device holds no pair of tensor-core CTAs");
+  if (c->dev.pairs < 1) return set_error(TIDE_ERR_CUDA, "the device holds no pair of tensor-core CTAs");
   if (!c->err) {
     e = cudaHostAlloc((void**)&c->err, sizeof(int), cudaHostAllocMapped);
     if (e != cudaSuccess) return cuda_fail(e, "cudaHostAlloc(error word)");
@@ -103,7 +101,7 @@ tide_status_t bind(tide_compute_s* c, cudaStream_t stream) {
 
 TcLaunch launch_of(tide_compute_s* c) {
   std::lock_guard<std::mutex> g(c->mu);
-  return TcLaunch{c->pairs, c->num_sms, c->d_err, (uint64_t)c->test_stall_ns, (uint64_t)c->test_late_ns};
+  return TcLaunch{&c->dev, c->d_err, (uint64_t)c->test_stall_ns, (uint64_t)c->test_late_ns};
 }
 
 tide_status_t launched(cudaError_t e, const char* what) { return e == cudaSuccess ? TIDE_OK : cuda_fail(e, what); }

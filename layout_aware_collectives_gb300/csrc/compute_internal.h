@@ -102,10 +102,40 @@ cudaError_t launch_early(void (*kernel)(P...), dim3 grid, unsigned block, size_t
   return cudaLaunchKernelEx(&c, kernel, P(args)...);
 }
 
+// Clusters of 2 to 4 pairs of CTAs that work on one tile, each pair on a part
+// of its contraction.  A cluster lies within one GPC, so the device holds
+// fewer than it has SMs by their size.
+constexpr int kMaxSplit = 4;
+struct PairClusters {
+  int held[kMaxSplit + 1];  // at one time, of so many pairs
+
+  cudaError_t prepare(const void* kernel, int threads, size_t smem);
+  // Pairs for a tile: as many as all tiles find at one time, each with at
+  // least eight stages, or 1, as with fewer stages than `least` in all.
+  int split(int64_t tiles, int64_t stages, int least) const {
+    int s = stages < least ? 1 : kMaxSplit;
+    while (s > 1 && (held[s] < tiles || stages < 8 * s)) --s;
+    return s;
+  }
+};
+
+// Clusters of 2 to 8 CTAs of the few-token kernels, likewise: of so many CTAs
+// that the device holds at one time.
+constexpr int kMaxCluster = 8;
+using FewClusters = int[kMaxCluster + 1];
+
+// What a device holds at one time, which the splits go by.  A handle keeps its
+// own device's.
+struct TcDevice {
+  int sms;
+  int pairs;               // of CTAs
+  PairClusters gated, fp8;  // of the split kernels
+  FewClusters few[4][3][2];  // by kind, tile of tokens and activation
+};
+
 // What a tensor-core launch takes from its handle.
 struct TcLaunch {
-  int pairs;  // pairs of CTAs the device holds at one time
-  int sms;
+  const TcDevice* dev;
   int* err;   // the handle's error word
   uint64_t stall_ns;  // test: a wait that must run out
   uint64_t late_ns;   // test: the same of one warp, beside others whose do not
@@ -115,12 +145,12 @@ struct TcLaunch {
 // whose rows start on 16 bytes.
 // prepare: sets a file's kernels up on the current device (shared-memory
 // limits, what the device holds at one time); once for each handle.
-cudaError_t gated_tc_prepare(int* pairs);
-cudaError_t fp8_tc_prepare();
-cudaError_t few_tc_prepare();
+cudaError_t gated_tc_prepare(TcDevice* dev);
+cudaError_t fp8_tc_prepare(TcDevice* dev);
+cudaError_t few_tc_prepare(TcDevice* dev);
 bool gated_tc_takes(const GatedArgs& a);
 // Pairs of CTAs that share a tile's contraction in forward and grad.
-int gated_tc_split(const GatedArgs& a);
+int gated_tc_split(const GatedArgs& a, const TcDevice& dev);
 // Workspace for the parts of dX's and dW's sums.
 int64_t gated_dx_parts_bytes(int64_t tokens, int64_t hidden);
 int64_t gated_dw_parts_bytes(int64_t hidden, int64_t ffn);
@@ -134,7 +164,7 @@ cudaError_t launch_gated_back_tc(const GatedArgs& a, bool dx, bool dw, bool dx_b
 // Tensor-core product of 8-bit blocks (fp8_tc.cu): k a multiple of 16, n and
 // the output's stride of 8.
 // Pairs of CTAs that share a tile's contraction there.
-int fp8_tc_split(const MatmulArgs& a);
+int fp8_tc_split(const MatmulArgs& a, const TcDevice& dev);
 cudaError_t launch_fp8_matmul_tc(const MatmulArgs& a, const TcLaunch& l, cudaStream_t stream);
 
 // The same two products for few tokens (few_tc.cu).
@@ -151,8 +181,7 @@ cudaError_t launch_fp8_matmul_few(const MatmulArgs& a, const TcLaunch& l, cudaSt
 
 struct tide_compute_s {
   int device = -1;  // bound by the first call
-  int num_sms = 0;
-  int pairs = 0;
+  tide::TcDevice dev{};  // written once, before `device`
   // Error word: pinned host memory that a kernel writes when a bounded wait
   // runs out, so that nothing has to be zeroed on a stream.
   int* err = nullptr;

@@ -334,20 +334,10 @@ __global__ void __launch_bounds__(kThreads) few_tc_kernel(const __grid_constant_
   if (beside) after_previous();
 }
 
-constexpr int kMaxCluster = 8;
-
-// One kernel's shape for the launches: set up once for each device.
-template <int KIND, int NT, int ACT>
-struct Held {
-  // clusters of so many CTAs that the device holds at one time; a cluster
-  // lies within one GPC, so these are fewer than SMs by their size
-  static int clusters[kMaxCluster + 1];
-};
-template <int KIND, int NT, int ACT>
-int Held<KIND, NT, ACT>::clusters[kMaxCluster + 1] = {};
+constexpr int tile_index(int nt) { return nt == 16 ? 0 : nt == 32 ? 1 : 2; }
 
 template <int KIND, int NT, int ACT>
-cudaError_t prepare() {
+cudaError_t prepare(TcDevice* dev) {
   using S = Shape<KIND, NT>;
   cudaError_t e = cudaFuncSetAttribute(few_tc_kernel<KIND, NT, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
   for (int n = 2; n <= kMaxCluster && e == cudaSuccess; ++n) {
@@ -360,16 +350,16 @@ cudaError_t prepare() {
     c.dynamicSmemBytes = S::kSmem;
     c.attrs = &cluster;
     c.numAttrs = 1;
-    e = cudaOccupancyMaxActiveClusters(&Held<KIND, NT, ACT>::clusters[n], few_tc_kernel<KIND, NT, ACT>, &c);
+    e = cudaOccupancyMaxActiveClusters(&dev->few[KIND][tile_index(NT)][ACT][n], few_tc_kernel<KIND, NT, ACT>, &c);
   }
   return e;
 }
 
 template <int KIND, int ACT = 0>
-cudaError_t prepare_tiles() {
-  cudaError_t e = prepare<KIND, 16, ACT>();
-  if (e == cudaSuccess) e = prepare<KIND, 32, ACT>();
-  return e == cudaSuccess ? prepare<KIND, 64, ACT>() : e;
+cudaError_t prepare_tiles(TcDevice* dev) {
+  cudaError_t e = prepare<KIND, 16, ACT>(dev);
+  if (e == cudaSuccess) e = prepare<KIND, 32, ACT>(dev);
+  return e == cudaSuccess ? prepare<KIND, 64, ACT>(dev) : e;
 }
 
 // CTAs that share a tile's contraction: up to one for each SM, all at work at
@@ -380,11 +370,11 @@ cudaError_t prepare_tiles() {
 // first; 4096 x 2048: 12.4 in four, 12.9 in six; dX of 7 x 2048 x 8192: 15.6
 // in four, 13.0 in six.)
 template <int KIND, int NT, int ACT>
-int split_of(int64_t tiles, int64_t steps, int sms) {
-  const int* held = Held<KIND, NT, ACT>::clusters;
+int split_of(int64_t tiles, int64_t steps, const TcDevice& dev) {
+  const FewClusters& clusters = dev.few[KIND][tile_index(NT)][ACT];
   constexpr int kMany = NT == 64 && Shape<KIND, NT>::kParts == 2 ? 12 : 4;  // stages, of more than four
   int s = kMaxCluster;
-  while (s > 1 && (s * tiles > sms || held[s] < tiles || steps < (s > 4 ? kMany : 4) * s)) --s;
+  while (s > 1 && (s * tiles > dev.sms || clusters[s] < tiles || steps < (s > 4 ? kMany : 4) * s)) --s;
   return s;
 }
 
@@ -395,7 +385,7 @@ cudaError_t launch(Params& p, const TcLaunch& l, cudaStream_t stream) {
   p.limit_ns = TIDE_BULK_TIMEOUT_NS;
   p.stall_ns = l.stall_ns, p.late_ns = l.late_ns;
   const int64_t tiles_t = ceil_div(p.tokens, NT), tiles_f = ceil_div(p.features, kRows);
-  const int split = split_of<KIND, NT, ACT>(tiles_t * tiles_f, p.steps, l.sms);
+  const int split = split_of<KIND, NT, ACT>(tiles_t * tiles_f, p.steps, *l.dev);
   return launch_early(few_tc_kernel<KIND, NT, ACT>, dim3(split, (unsigned)tiles_t, (unsigned)tiles_f), kThreads, S::kSmem,
                       (unsigned)split, stream, p);
 }
@@ -434,12 +424,12 @@ cudaError_t gated(Params& p, const GatedArgs& a, const TcLaunch& l, cudaStream_t
 
 }  // namespace
 
-cudaError_t few_tc_prepare() {
-  cudaError_t (*const all[])() = {prepare_tiles<kForward, TIDE_ACT_SILU>, prepare_tiles<kForward, TIDE_ACT_GELU>,
+cudaError_t few_tc_prepare(TcDevice* dev) {
+  cudaError_t (*const all[])(TcDevice*) = {prepare_tiles<kForward, TIDE_ACT_SILU>, prepare_tiles<kForward, TIDE_ACT_GELU>,
                                   prepare_tiles<kGrad, TIDE_ACT_SILU>,    prepare_tiles<kGrad, TIDE_ACT_GELU>,
                                   prepare_tiles<kFp8>,                    prepare_tiles<kDx>};
   for (auto p : all) {
-    const cudaError_t e = p();
+    const cudaError_t e = p(dev);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
@@ -461,10 +451,10 @@ cudaError_t few_tc_prepare() {
 // 8-bit, 420 x 208 x 10864: 9.1 and 15.2; 123 x 960 x 7712 10.1 and 11.7; 110
 // x 3104 x 11584 21.6 and 15.3; 1162 x 544 x 12880 40.0 and 18.0.)
 bool gated_few_takes(const GatedArgs& a, const TcLaunch& l) {
-  if (a.tokens <= 64 || !few(a.tokens, a.ffn, l.sms / 2)) return few(a.tokens, a.ffn, 0);
+  if (a.tokens <= 64 || !few(a.tokens, a.ffn, l.dev->sms / 2)) return few(a.tokens, a.ffn, 0);
   const int64_t steps = ceil_div(a.hidden, kRowBytes / 2);
-  const int split = split_of<kForward, 64, TIDE_ACT_SILU>(ceil_div(a.tokens, 64) * ceil_div(a.ffn, kRows), steps, l.sms);
-  const int there = gated_tc_split(a);
+  const int split = split_of<kForward, 64, TIDE_ACT_SILU>(ceil_div(a.tokens, 64) * ceil_div(a.ffn, kRows), steps, *l.dev);
+  const int there = gated_tc_split(a, *l.dev);
   const double here = split > 1 ? 0.3 * steps / split + 6.2 : 0.24 * steps + 3;
   return here + (a.g8 ? 4.0 / split : 0) <= 0.265 * steps / there + (there > 1 ? 7.6 : 4.3) + (a.g8 ? 1.1 : 0);
 }
@@ -482,17 +472,17 @@ bool gated_dx_few_takes(const GatedArgs& a, const TcLaunch& l) {
   const int64_t tiles = ceil_div(a.hidden, kRows) * ceil_div(a.tokens, 64);
   if (steps < (tiles <= 8 ? 16 : 48)) return false;
   const int64_t large = ceil_div(a.hidden, 256) * ceil_div(a.tokens, 256);
-  const int split = split_of<kDx, 64, 0>(tiles, steps, l.sms);
-  const int64_t parts = l.pairs / large > 1 ? l.pairs / large : 1;
+  const int split = split_of<kDx, 64, 0>(tiles, steps, *l.dev);
+  const int64_t parts = l.dev->pairs / large > 1 ? l.dev->pairs / large : 1;
   if (0.21 * steps / split + 3 > 0.3 * steps / parts + (parts > 1 ? 8 : 4)) return false;
   if (a.tokens <= 64) return few(a.tokens, a.hidden, 0);
-  return a.tokens <= 512 && few(a.tokens, a.hidden, 32) && 2 * ceil_div(a.ffn, 256) * ceil_div(a.hidden, 256) <= l.pairs;
+  return a.tokens <= 512 && few(a.tokens, a.hidden, 32) && 2 * ceil_div(a.ffn, 256) * ceil_div(a.hidden, 256) <= l.dev->pairs;
 }
 
 bool fp8_few_takes(const MatmulArgs& a, const TcLaunch& l) {
-  if (a.m <= 64 || !few(a.m, a.n, 2 * l.sms / 3)) return few(a.m, a.n, 0);
+  if (a.m <= 64 || !few(a.m, a.n, 2 * l.dev->sms / 3)) return few(a.m, a.n, 0);
   const int64_t steps = ceil_div(a.k, kRowBytes);
-  const int split = split_of<kFp8, 64, 0>(ceil_div(a.m, 64) * ceil_div(a.n, kRows), steps, l.sms), there = fp8_tc_split(a);
+  const int split = split_of<kFp8, 64, 0>(ceil_div(a.m, 64) * ceil_div(a.n, kRows), steps, *l.dev), there = fp8_tc_split(a, *l.dev);
   return 0.35 * steps / split + (split > 1 ? 4.5 : 3) <= 0.33 * steps / there + (there > 1 ? 7 : 4);
 }
 

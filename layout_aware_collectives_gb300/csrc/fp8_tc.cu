@@ -485,23 +485,21 @@ __global__ void __launch_bounds__(kScaledThreads, 1) scaled_kernel(const __grid_
   if (warp == 2) tmem_free<2>(tmem, 512);
 }
 
-PairClusters clusters;  // of scaled_kernel<true>
-
 }  // namespace
 
-cudaError_t fp8_tc_prepare() {
+cudaError_t fp8_tc_prepare(TcDevice* dev) {
   cudaError_t e = cudaFuncSetAttribute(summed_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(scaled_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kScaledSmem);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(scaled_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kScaledSmem);
-  if (e == cudaSuccess) e = clusters.prepare((const void*)scaled_kernel<true>, kScaledThreads, kScaledSmem);
+  if (e == cudaSuccess) e = dev->fp8.prepare((const void*)scaled_kernel<true>, kScaledThreads, kScaledSmem);
   return e;
 }
 
-int fp8_tc_split(const MatmulArgs& a) {
+int fp8_tc_split(const MatmulArgs& a, const TcDevice& dev) {
   if (a.any_scales) return 1;
-  return clusters.split(ceil_div(a.m, 2 * kHalf) * ceil_div(a.n, 2 * kHalf), ceil_div(a.k, kBlock), 16);
+  return dev.fp8.split(ceil_div(a.m, 2 * kHalf) * ceil_div(a.n, 2 * kHalf), ceil_div(a.k, kBlock), 16);
 }
 
 cudaError_t launch_fp8_matmul_tc(const MatmulArgs& a, const TcLaunch& l, cudaStream_t stream) {
@@ -519,8 +517,8 @@ cudaError_t launch_fp8_matmul_tc(const MatmulArgs& a, const TcLaunch& l, cudaStr
       !make_map(&p.b, a.b, 1, a.k, a.n, a.k, kBlock, kHalf, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_map(&p.out, a.out, 2, a.n, a.m, a.ldo, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
     return cudaErrorInvalidValue;
-  const int pairs = p.tiles < l.pairs ? p.tiles : l.pairs;
-  p.split = fp8_tc_split(a);
+  const int pairs = p.tiles < l.dev->pairs ? p.tiles : l.dev->pairs;
+  p.split = fp8_tc_split(a, *l.dev);
   if (p.split > 1)
     return launch_early(scaled_kernel<true>, dim3(2 * p.split * p.tiles), kScaledThreads, kScaledSmem, 2 * p.split, stream, p);
   return a.any_scales ? launch_early(summed_kernel, dim3(2 * pairs), kThreads, kSmem, 0, stream, p)

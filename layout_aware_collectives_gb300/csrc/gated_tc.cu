@@ -556,14 +556,14 @@ cudaError_t join(const Join& a, int outputs, cudaStream_t stream) {
                         : join<16, 16>(a, outputs, stream);
 }
 
-PairClusters clusters;  // of the split kernels, which take the same shape
-
 // Pairs that share a tile of the forward or grad form.  (300 x 1024 x 2048,
 // 32 tiles of 16 stages: 9.0 us whole, 9.5 in twos; 1021 x 2048 x 768, 24 of
 // 32: 12.9 and 11.9.)
-int split_pre(int64_t tiles, int64_t steps) { return clusters.split(tiles, steps, 24); }
+int split_pre(int64_t tiles, int64_t steps, const TcDevice& dev) { return dev.gated.split(tiles, steps, 24); }
 
-int pairs_of(const Params& p, const TcLaunch& l) { return p.tiles + p.w_tiles < l.pairs ? p.tiles + p.w_tiles : l.pairs; }
+int pairs_of(const Params& p, const TcLaunch& l) {
+  return p.tiles + p.w_tiles < l.dev->pairs ? p.tiles + p.w_tiles : l.dev->pairs;
+}
 
 template <int FORM, int ACT>
 cudaError_t launch(Params& p, const TcLaunch& l, cudaStream_t stream) {
@@ -571,7 +571,7 @@ cudaError_t launch(Params& p, const TcLaunch& l, cudaStream_t stream) {
   p.limit_ns = TIDE_BULK_TIMEOUT_NS;
   p.stall_ns = l.stall_ns, p.late_ns = l.late_ns;
   if constexpr (FORM != kBack) {
-    p.split = split_pre(p.tiles, p.steps);
+    p.split = split_pre(p.tiles, p.steps, *l.dev);
     p.share = Share(p.steps, p.split);
     if (p.split > 1)
       return launch_early(gated_tc_kernel<FORM, ACT, true>, dim3(2 * p.split * p.tiles), kThreads, kSmem, 2 * p.split, stream, p);
@@ -629,7 +629,7 @@ int64_t parts_bytes(int64_t tiles, int64_t part_bytes) { return tiles ? 76 / til
 
 }  // namespace
 
-cudaError_t gated_tc_prepare(int* pairs) {
+cudaError_t gated_tc_prepare(TcDevice* dev) {
   void (*const kernels[])(Params) = {
       gated_tc_kernel<kForward, TIDE_ACT_SILU, false>, gated_tc_kernel<kForward, TIDE_ACT_GELU, false>,
       gated_tc_kernel<kForward, TIDE_ACT_SILU, true>,  gated_tc_kernel<kForward, TIDE_ACT_GELU, true>,
@@ -640,7 +640,8 @@ cudaError_t gated_tc_prepare(int* pairs) {
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e != cudaSuccess) return e;
   }
-  const cudaError_t held = clusters.prepare((const void*)gated_tc_kernel<kForward, TIDE_ACT_SILU, true>, kThreads, kSmem);
+  // the split kernels take the same shape
+  const cudaError_t held = dev->gated.prepare((const void*)gated_tc_kernel<kForward, TIDE_ACT_SILU, true>, kThreads, kSmem);
   if (held != cudaSuccess) return held;
   // The pairs the device holds at one time: a GPC with an odd number of
   // SMs leaves one without a partner.
@@ -653,7 +654,7 @@ cudaError_t gated_tc_prepare(int* pairs) {
   c.dynamicSmemBytes = kSmem;
   c.attrs = &cluster;
   c.numAttrs = 1;
-  return cudaOccupancyMaxActiveClusters(pairs, gated_tc_kernel<kBack, 0, false>, &c);
+  return cudaOccupancyMaxActiveClusters(&dev->pairs, gated_tc_kernel<kBack, 0, false>, &c);
 }
 
 int64_t gated_dx_parts_bytes(int64_t tokens, int64_t hidden) {
@@ -663,8 +664,8 @@ int64_t gated_dw_parts_bytes(int64_t hidden, int64_t ffn) {
   return parts_bytes(2 * ceil_div(ffn, 2 * kHalf) * ceil_div(hidden, 2 * kHalf), 8 * ffn * hidden);
 }
 
-int gated_tc_split(const GatedArgs& a) {
-  return split_pre(ceil_div(a.tokens, 2 * kHalf) * ceil_div(a.ffn, kHalf), ceil_div(a.hidden, kStep));
+int gated_tc_split(const GatedArgs& a, const TcDevice& dev) {
+  return split_pre(ceil_div(a.tokens, 2 * kHalf) * ceil_div(a.ffn, kHalf), ceil_div(a.hidden, kStep), dev);
 }
 
 bool gated_tc_takes(const GatedArgs& a) { return a.hidden >= 8 && rows16(a.hidden, a.hidden) && rows16(a.ffn, a.ffn); }
@@ -695,7 +696,7 @@ cudaError_t launch_gated_back_tc(const GatedArgs& a, bool dx, bool dw, bool dx_b
     p.rows = (int)a.tokens;
     p.grid = TileGrid((int)ceil_div(a.tokens, 2 * kHalf), (int)ceil_div(a.hidden, 2 * kHalf));
     p.half_steps = (int)ceil_div(a.ffn, kStep), p.steps = 2 * p.half_steps;
-    p.split = split_of(p.grid.all.d, p.steps, l.pairs, 4 * a.tokens * a.hidden, a.dx_parts_bytes);
+    p.split = split_of(p.grid.all.d, p.steps, l.dev->pairs, 4 * a.tokens * a.hidden, a.dx_parts_bytes);
     p.share = Share(p.steps, p.split);
     p.parts = a.dx_parts;
     p.tiles = p.grid.all.d * p.split;
@@ -709,7 +710,7 @@ cudaError_t launch_gated_back_tc(const GatedArgs& a, bool dx, bool dw, bool dx_b
     p.w_grid = TileGrid((int)ceil_div(a.ffn, 2 * kHalf), (int)ceil_div(a.hidden, 2 * kHalf));
     p.w_tiles = 2 * p.w_grid.all.d;
     p.w_steps = (int)ceil_div(a.tokens, kStep);
-    p.w_split = split_of(p.w_tiles, p.w_steps, l.pairs, 8 * a.ffn * a.hidden, a.dw_parts_bytes);
+    p.w_split = split_of(p.w_tiles, p.w_steps, l.dev->pairs, 8 * a.ffn * a.hidden, a.dw_parts_bytes);
     p.w_share = Share(p.w_steps, p.w_split);
     p.w_parts = a.dw_parts;
     p.w_tiles *= p.w_split;

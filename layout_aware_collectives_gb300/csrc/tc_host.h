@@ -48,21 +48,4 @@ struct TileGrid {
       : tiles_m(m), tiles_n(n), all(m * n), band(kBand * n), last(m % kBand ? m % kBand : kBand) {}
 };
 
-// Clusters of 2 to 4 pairs of CTAs that work on one tile, each pair on a part
-// of its contraction.  A cluster lies within one GPC, so the device holds
-// fewer than it has SMs by their size.
-constexpr int kMaxSplit = 4;
-struct PairClusters {
-  int held[kMaxSplit + 1];  // at one time, of so many pairs
-
-  cudaError_t prepare(const void* kernel, int threads, size_t smem);
-  // Pairs for a tile: as many as all tiles find at one time, each with at
-  // least eight stages, or 1, as with fewer stages than `least` in all.
-  int split(int64_t tiles, int64_t stages, int least) const {
-    int s = stages < least ? 1 : kMaxSplit;
-    while (s > 1 && (held[s] < tiles || stages < 8 * s)) --s;
-    return s;
-  }
-};
-
 }  // namespace tide

@@ -72,3 +72,33 @@ assert fake.fake_syncs(0) == 1
 fake.fake_error_at_sync(0, 0)
 c.check_device()
 """)
+
+
+def test_handle_keeps_its_own_device_s_properties(runtime):
+    """How a contraction is split, and with it the order of its sums, goes by
+    the handle's own device, whatever handle was bound since."""
+    child(runtime, """
+def shapes(c):
+    out = []
+    def note(call, *a, **kw):
+        call(*a, **kw)
+        out.append((fake.fake_grid(0), fake.fake_grid(1), fake.fake_grid(2), fake.fake_cluster()))
+    for m, n, k in ((1, 2048, 8192), (1014, 752, 9200), (200, 2368, 7904)):
+        note(c.fp8_matmul, m, n, k, A, A, A, A, A)
+    for t, k, f in ((1, 2048, 8192), (40, 2048, 768), (1014, 9200, 752), (200, 7904, 2368)):
+        note(c.gated_forward, t, k, f, A, A, A, A)
+    return out
+
+first = bound(0)
+want = shapes(first)
+assert any(s[3] > 2 for s in want)
+second = bound(1)
+other = shapes(second)
+assert other != want
+on(0)
+assert shapes(first) == want, (shapes(first), want)
+third = bound(0)
+assert shapes(third) == want
+on(1)
+assert shapes(second) == other
+""")
