@@ -131,7 +131,7 @@ def _addr(x) -> int:
         return 0
     if isinstance(x, int):
         return x
-    return x.data_ptr()
+    return int(x.data_ptr())
 
 
 def _stream(s) -> int:
@@ -139,7 +139,7 @@ def _stream(s) -> int:
         return 0
     if isinstance(s, int):
         return s
-    return s.cuda_stream
+    return int(s.cuda_stream)
 
 
 class PointerTable:

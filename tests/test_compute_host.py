@@ -2,6 +2,7 @@
 GPU tests compare with."""
 import ctypes
 
+import numpy
 import pytest
 import torch
 
@@ -148,3 +149,33 @@ def test_test_hooks_refuse(compute):
         assert hook(None, 0) == BAD
         assert hook(compute.handle, -1) == BAD
         assert hook(compute.handle, 0) == tide.TIDE_OK
+
+
+class Number:
+    """A whole number that is no int."""
+
+    def __init__(self, v):
+        self.v = v
+
+    def __int__(self):
+        return self.v
+
+
+@pytest.mark.parametrize("number", [Number, numpy.int64, numpy.uint64])
+def test_tensors_and_streams_of_other_libraries(compute, number):
+    """A buffer's data_ptr() and a stream's cuda_stream may be any whole number."""
+
+    class Buffer:
+        def data_ptr(self):
+            return number(A)
+
+    class Stream:
+        cuda_stream = number(0)
+
+    b, s = Buffer(), Stream()
+    compute.fp8_store(0, 128, b, b, b, stream=s)
+    refused(MIS, compute.fp8_store, 4, 128, b, b, A + 2, stream=s)
+    with tide.Layout([], 2) as layout:
+        layout.place(b, [], stream=s)
+    with tide.Layout([(0, 4)], 2) as layout:
+        layout.place(b, [b], stream=s)
