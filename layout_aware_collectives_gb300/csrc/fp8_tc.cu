@@ -141,7 +141,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) summed_
       for (int t = pair; t < p.tiles && go; t += pairs) {
         for (int k = 0; k < p.blocks; ++k, ++j) {
           const int s = j % kStages, b = j & 1;
-          if ((j >= 2 && !bar_wait(sums_empty(b), (j / 2 + 1) & 1, watch)) || !bar_wait(full(s), (j / kStages) & 1, watch)) {
+          if ((j >= 2 && !bar_wait<kPeer>(sums_empty(b), (j / 2 + 1) & 1, watch)) || !bar_wait(full(s), (j / kStages) & 1, watch)) {
             go = false;
             break;
           }
@@ -337,12 +337,12 @@ __global__ void __launch_bounds__(kScaledThreads, 1) scaled_kernel(const __grid_
       int j = 0, i = 0;  // blocks and tiles so far
       bool go = true;
       for (int t = pair; t < p.tiles && go; t += pairs, ++i) {
-        if (i > 0 && !bar_wait(sums_empty, (i + 1) & 1, watch)) break;
+        if (i > 0 && !bar_wait<kPeer>(sums_empty, (i + 1) & 1, watch)) break;
         fence_after();
         const uint32_t sums = tmem + (i & 1) * kOdd;
         for (int k = k0; k < k1; ++k, ++j) {
           const int s = j % kStages;
-          if (!bar_wait(full(s), (j / kStages) & 1, watch)) {
+          if (!bar_wait<kOwnAndPeer>(full(s), (j / kStages) & 1, watch)) {
             go = false;
             break;
           }

@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
         // a 32-byte step of the contraction lies 32 bytes on (K-major) or two
         // groups of 8 rows on (MN-major)
         const uint32_t a_lbo = a_mn ? kOperand / 2 : 16, a_next = (a_mn ? 2048 : 32) >> 4;
-        if (i >= 2 && !bar_wait(sums_empty(b), (i / 2 + 1) & 1, watch)) break;
+        if (i >= 2 && !bar_wait<kPeer>(sums_empty(b), (i / 2 + 1) & 1, watch)) break;
         fence_after();
         for (int k = work.k0; k < work.k1; ++k, ++j) {
           const int s = j % kStages;
