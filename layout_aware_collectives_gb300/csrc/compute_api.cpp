@@ -346,9 +346,8 @@ tide_status_t tide_gated_backward(tide_compute_t c, int64_t tokens, int64_t hidd
   if (hidden == 0) return TIDE_OK;
   const bool dx_tc = dx && tc && ld_dx % 8 == 0, dw_tc = dw_gate && tc && a.ldx % 8 == 0;
   const bool dx_few = dx_tc && gated_dx_few_takes(a, l);
-  if (dx_few && !dw_tc) TIDE_TRY(launched(launch_gated_dx_few(a, false, l, stream), what));
-  if ((dx_tc && !dx_few) || dw_tc)
-    TIDE_TRY(launched(launch_gated_back_tc(a, dx_tc && !dx_few, dw_tc, dx_few && dw_tc, l, stream), what));
+  if (dx_few) TIDE_TRY(launched(launch_gated_dx_few(a, l, stream), what));
+  if ((dx_tc && !dx_few) || dw_tc) TIDE_TRY(launched(launch_gated_back_tc(a, dx_tc && !dx_few, dw_tc, l, stream), what));
   if (dx && !dx_tc) TIDE_TRY(launched(launch_gated_dx_simple(a, stream), what));
   if (dw_gate && !dw_tc) TIDE_TRY(launched(launch_gated_dw_simple(a, stream), what));
   return TIDE_OK;

@@ -156,10 +156,8 @@ int64_t gated_dx_parts_bytes(int64_t tokens, int64_t hidden);
 int64_t gated_dw_parts_bytes(int64_t hidden, int64_t ffn);
 cudaError_t launch_gated_forward_tc(const GatedArgs& a, const TcLaunch& l, cudaStream_t stream);
 cudaError_t launch_gated_grad_tc(const GatedArgs& a, const TcLaunch& l, cudaStream_t stream);
-// dX, dWg and dWu, or either.  dx_beside: launch_gated_dx_few between dW's
-// kernel and the one that joins its parts.
-cudaError_t launch_gated_back_tc(const GatedArgs& a, bool dx, bool dw, bool dx_beside, const TcLaunch& l,
-                                 cudaStream_t stream);
+// dX, dWg and dWu, or either.
+cudaError_t launch_gated_back_tc(const GatedArgs& a, bool dx, bool dw, const TcLaunch& l, cudaStream_t stream);
 
 // Tensor-core product of 8-bit blocks (fp8_tc.cu): k a multiple of 16, n and
 // the output's stride of 8.
@@ -172,8 +170,7 @@ bool gated_few_takes(const GatedArgs& a, const TcLaunch& l);
 bool fp8_few_takes(const MatmulArgs& a, const TcLaunch& l);
 cudaError_t launch_gated_grad_few(const GatedArgs& a, const TcLaunch& l, cudaStream_t stream);
 bool gated_dx_few_takes(const GatedArgs& a, const TcLaunch& l);
-// beside: straight after launch_gated_back_tc's dW on this stream, and beside it.
-cudaError_t launch_gated_dx_few(const GatedArgs& a, bool beside, const TcLaunch& l, cudaStream_t stream);
+cudaError_t launch_gated_dx_few(const GatedArgs& a, const TcLaunch& l, cudaStream_t stream);
 cudaError_t launch_gated_forward_few(const GatedArgs& a, const TcLaunch& l, cudaStream_t stream);
 cudaError_t launch_fp8_matmul_few(const MatmulArgs& a, const TcLaunch& l, cudaStream_t stream);
 

@@ -58,7 +58,6 @@ struct Params : GatedOut {  // 8-bit product, dX: out, ldo and features of it
   int tokens, steps, step_elems;
   int half_steps;  // dX: stages of dG's half
   bool one_box;    // dX: a stage's weights are one box of two slabs
-  bool beside;     // dX: runs beside the kernel ahead of it
   // 8-bit
   const float *sx, *sw;
   bool any_scales;
@@ -135,11 +134,7 @@ __global__ void __launch_bounds__(kThreads) few_tc_kernel(const __grid_constant_
   __syncthreads();
   fence_after();
   const uint32_t tmem = tmem_at;
-  // Beside dW's kernel, which it does not depend on: this one begins once all
-  // of that one's CTAs are past their own wait, so what came before both has
-  // ended; it waits for that one's end at its own.
-  const bool beside = KIND == kDx && p.beside;
-  if (!beside) after_previous();
+  after_previous();
   bool done = false;  // this warp has its sums in shared memory
   int filled = 0;     // stages this thread has filled
 
@@ -331,7 +326,6 @@ __global__ void __launch_bounds__(kThreads) few_tc_kernel(const __grid_constant_
   }
   if (split > 1) cluster_sync();  // the others have read this CTA's sums
   if (warp == 1) tmem_free<1>(tmem, S::kColumns);
-  if (beside) after_previous();
 }
 
 constexpr int tile_index(int nt) { return nt == 16 ? 0 : nt == 32 ? 1 : 2; }
@@ -458,25 +452,20 @@ bool gated_few_takes(const GatedArgs& a, const TcLaunch& l) {
   const double here = split > 1 ? 0.3 * steps / split + 6.2 : 0.24 * steps + 3;
   return here + (a.g8 ? 4.0 / split : 0) <= 0.265 * steps / there + (there > 1 ? 7.6 : 4.3) + (a.g8 ? 1.1 : 0);
 }
-// dX up to 64 tokens, and for more where it has few tiles and dW's leave SMs
-// for it (500 x 1024 x 1024, 64 tiles: 24.7 us for the backward pass against
-// 22.6 in 256-row tiles).  In microseconds, here 0.21 a stage and 3 more, in
-// 256-row tiles 0.3 and 4, or 8 where their sums are split (4 x 4096 x 14336:
-// 37 against 54; 64 x 512 x 2048: 6 against 8; 2 x 336 x 25264, where a
-// cluster's 8 CTAs are too few: 23 against 19).  Below 48 stages it takes a
-// launch more than it saves, but for so few tiles that it ends beside dW (250
-// x 256 x 704, 8 tiles: backward pass 13.9 us against 16.0; 500 x 512 x 512,
-// 32 tiles: 19.9 against 15.8).
+// dX up to 64 tokens, where it saves more than its own launch takes beside
+// dW's: from 12 M weights on (a whole backward pass in a graph, here and in
+// 256-row tiles: 1 x 4096 x 14336 122 and 130 us, 8 x 8192 x 1792 35.6 and
+// 41.4, 37 x 2048 x 4096 25.0 and 24.7, 64 x 512 x 2048 18.5 and 16.5).  In
+// microseconds dX takes 0.21 a stage and 3 more here, in 256-row tiles 0.3 and
+// 4, or 8 where their sums are split (4 x 4096 x 14336: 37 against 54; 2 x 336 x
+// 25264, where a cluster's 8 CTAs are too few: 23 against 19).
 bool gated_dx_few_takes(const GatedArgs& a, const TcLaunch& l) {
-  const int64_t steps = 2 * ceil_div(a.ffn, kRowBytes / 2);
-  const int64_t tiles = ceil_div(a.hidden, kRows) * ceil_div(a.tokens, 64);
-  if (steps < (tiles <= 8 ? 16 : 48)) return false;
-  const int64_t large = ceil_div(a.hidden, 256) * ceil_div(a.tokens, 256);
+  if (a.tokens > 64 || a.hidden * a.ffn < (12 << 20) || !few(a.tokens, a.hidden, 0)) return false;
+  const int64_t steps = 2 * ceil_div(a.ffn, kRowBytes / 2), tiles = ceil_div(a.hidden, kRows);
+  const int64_t large = ceil_div(a.hidden, 256);
   const int split = split_of<kDx, 64, 0>(tiles, steps, *l.dev);
   const int64_t parts = l.dev->pairs / large > 1 ? l.dev->pairs / large : 1;
-  if (0.21 * steps / split + 3 > 0.3 * steps / parts + (parts > 1 ? 8 : 4)) return false;
-  if (a.tokens <= 64) return few(a.tokens, a.hidden, 0);
-  return a.tokens <= 512 && few(a.tokens, a.hidden, 32) && 2 * ceil_div(a.ffn, 256) * ceil_div(a.hidden, 256) <= l.dev->pairs;
+  return 0.21 * steps / split + 3 <= 0.3 * steps / parts + (parts > 1 ? 8 : 4);
 }
 
 bool fp8_few_takes(const MatmulArgs& a, const TcLaunch& l) {
@@ -498,7 +487,7 @@ cudaError_t launch_gated_grad_few(const GatedArgs& a, const TcLaunch& l, cudaStr
   return gated<kGrad>(p, a, l, stream);
 }
 
-cudaError_t launch_gated_dx_few(const GatedArgs& a, bool beside, const TcLaunch& l, cudaStream_t stream) {
+cudaError_t launch_gated_dx_few(const GatedArgs& a, const TcLaunch& l, cudaStream_t stream) {
   constexpr int kElems = kRowBytes / 2;
   const int nt = tile_of(a.tokens);
   const uint16_t *w[2] = {a.wg, a.wu}, *d[2] = {a.dg, a.du};
@@ -507,7 +496,6 @@ cudaError_t launch_gated_dx_few(const GatedArgs& a, bool beside, const TcLaunch&
   p.half_steps = (int)ceil_div(a.ffn, kElems), p.steps = 2 * p.half_steps, p.step_elems = kElems;
   p.one_box = a.hidden % 64 == 0;
   p.out = a.dx, p.ldo = a.lddx;
-  p.beside = beside;
   for (int i = 0; i < 2; ++i)
     if (!(p.one_box ? make_slab_map(&p.w[i], w[i], a.hidden, a.ffn, a.hidden, kElems)
                     : make_map(&p.w[i], w[i], 2, a.hidden, a.ffn, a.hidden, 64, kElems, CU_TENSOR_MAP_SWIZZLE_128B)) ||

@@ -687,8 +687,7 @@ cudaError_t launch_gated_grad_tc(const GatedArgs& a, const TcLaunch& l, cudaStre
   return a.act == TIDE_ACT_SILU ? launch<kGrad, TIDE_ACT_SILU>(p, l, stream) : launch<kGrad, TIDE_ACT_GELU>(p, l, stream);
 }
 
-cudaError_t launch_gated_back_tc(const GatedArgs& a, bool dx, bool dw, bool dx_beside, const TcLaunch& l,
-                                 cudaStream_t stream) {
+cudaError_t launch_gated_back_tc(const GatedArgs& a, bool dx, bool dw, const TcLaunch& l, cudaStream_t stream) {
   Params p{};
   p.cols = (int)a.hidden;
   p.one_a = a.ffn % 64 == 0, p.one_b = a.hidden % 64 == 0;
@@ -727,7 +726,6 @@ cudaError_t launch_gated_back_tc(const GatedArgs& a, bool dx, bool dw, bool dx_b
   p.first = !p.full ? 0 : p.w_tiles < p.light * extra ? p.w_tiles : p.light * extra;
   p.first_each = p.first / p.light, p.first_more = p.first % p.light;
   cudaError_t e = launch<kBack, 0>(p, l, stream);
-  if (e == cudaSuccess && dx_beside) e = launch_gated_dx_few(a, true, l, stream);
   if (e == cudaSuccess && p.split > 1)
     e = join(Join{p.parts, p.split, {a.dx, nullptr}, a.lddx, p.rows, p.cols}, 1, stream);
   if (e == cudaSuccess && p.w_split > 1)

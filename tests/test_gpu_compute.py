@@ -1039,3 +1039,41 @@ def test_gates_near_the_largest_number(compute, tokens, hidden, ffn, kind, kept)
     assert torch.equal(dwg[:, 1].double(), on * 2.0 ** -70)
     assert torch.equal(dwg[:, 0].double(), on * 2.0 ** -6)
     assert torch.equal(dwu[:, 1].double(), on * g * 2.0 ** -70)
+
+
+# by the few-token kernel; joined from parts; in one launch with dW
+@pytest.mark.parametrize("tokens,hidden,ffn", [(4, 1032, 14336), (64, 512, 2048), (250, 256, 704)])
+def test_dx_follows_its_gradients(compute, tokens, hidden, ffn):
+    """dX beside dW reads the gradients of its own call: calls back to back, on a
+    stream and from a graph, give what dX alone gives, whatever came before."""
+    g = gen(tokens)
+    x, (wg, wu) = randn(g, tokens, hidden), weights(g, hidden, ffn)
+    dhs = [randn(gen(i), tokens, ffn) for i in range(8)]
+    ws = torch.empty(tide.gated_workspace_bytes(tokens, hidden, ffn), dtype=torch.uint8, device="cuda")
+    alone, both = ([torch.zeros(tokens, hidden, dtype=torch.bfloat16, device="cuda") for _ in dhs] for _ in range(2))
+    dwg, dwu = torch.empty_like(wg), torch.empty_like(wu)
+
+    def run(dxs, with_w):
+        for dh, dx in zip(dhs, dxs):
+            compute.gated_backward(tokens, hidden, ffn, dh, x, wg, wu, dx, dwg if with_w else None, dwu if with_w else None,
+                                   ws, stream=torch.cuda.current_stream())
+
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        run(alone, False)
+    s.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        run(both, True)
+    for turn in range(20):
+        if turn % 2:
+            graph.replay()
+        else:
+            with torch.cuda.stream(s):
+                run(both, True)
+        torch.cuda.synchronize()
+        for a, b in zip(alone, both):
+            assert torch.equal(a, b)
+            b.zero_()
+        torch.cuda.synchronize()
