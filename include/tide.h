@@ -487,10 +487,13 @@ TIDE_API tide_status_t tide_layout_check_tiles(tide_layout_t layout, tide_op_t o
  *
  * Conventions, besides those above:
  *  - Matrices are row-major.  Arguments ld* are row strides in elements, at
- *    least the row's width.  Rows whose stride and width are multiples of
- *    8 elements (16 for 8-bit operands) start on 16 bytes and run the
- *    kernels for large operands; any other width or stride runs plain
- *    tiled kernels, several times slower.
+ *    least the row's width.  Products whose rows' strides and widths are
+ *    multiples of 8 elements (16 for 8-bit operands) start their rows on
+ *    16 bytes and run the kernels for large operands; any other width or
+ *    stride runs plain tiled kernels, some 10 times slower.  Stores of other
+ *    widths or strides take single elements, at a third to a half of the
+ *    speed, and so do restores into rows that do not follow one another
+ *    (ld_dst > cols, whatever the stride), at a ninth to a quarter.
  *  - Sums are fp32; a result is rounded to bf16 once, to nearest even.
  *  - Every buffer is the caller's, 16-byte aligned (scales: 4-byte;
  *    TIDE_ERR_MISALIGNED otherwise) and in memory of the handle's device;
@@ -507,7 +510,8 @@ TIDE_API tide_status_t tide_layout_check_tiles(tide_layout_t layout, tide_op_t o
  */
 typedef struct tide_compute_s* tide_compute_t;
 
-/* Gate activation: x sigmoid(x), or the tanh form of GELU. */
+/* Gate activation: x sigmoid(x), or the tanh form of GELU, down to where the
+ * sigmoid ends among fp32's subnormal numbers. */
 typedef enum { TIDE_ACT_SILU = 0, TIDE_ACT_GELU = 1 } tide_activation_t;
 
 /* Create a handle (host-only; no CUDA call is made) / free it (work that
@@ -564,7 +568,9 @@ TIDE_API tide_status_t tide_fp8_restore(tide_compute_t compute, int64_t rows, in
  *        tide_fp8_store writes them, which the tensor cores take as they are;
  *        any other scale makes its row or columns NaN.
  *        1: any fp32 scales.  Up to 64 rows and for small products at the
- *        same speed, else at about half of it.
+ *        same speed, else at about 0.85 of it.
+ *        Either way the product of two scales may be past fp32's range where
+ *        the result is not; a block whose sum is zero adds zero.
  */
 TIDE_API tide_status_t tide_fp8_matmul(tide_compute_t compute, int64_t m, int64_t n, int64_t k, const uint8_t* a,
                                        const float* a_scales, const uint8_t* b, const float* b_scales,

@@ -1,5 +1,6 @@
 // Internal interface between the feed-forward unit's C ABI (compute_api.cpp)
-// and its kernels (fp8_blocks.cu, gated_simple.cu).
+// and its kernels (gated_tc.cu, few_tc.cu, fp8_tc.cu, fp8_blocks.cu,
+// gated_simple.cu).
 #pragma once
 
 #include <cuda_runtime_api.h>
@@ -48,7 +49,7 @@ struct GatedArgs {
   int64_t lddx;
   uint16_t* dwg;
   uint16_t* dwu;
-  uint16_t* dg;  // [tokens, ffn] each, workspace
+  uint16_t* dg;  // [tokens, ffn] each, workspace; bf16, the operands of dX's and dW's products
   uint16_t* du;
   float *dx_parts, *dw_parts;  // of dX's and dW's sums, workspace
   int64_t dx_parts_bytes, dw_parts_bytes;

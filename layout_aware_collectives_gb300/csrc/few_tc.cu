@@ -16,7 +16,7 @@
 // block, 8192 x 28672 gate and up 152 us against 140, and faster for the 8-bit
 // product, 43.8 against 45.5).  One token: 4096 x 14336 gate and up 36 us (6.5
 // TB/s; once they flow the rest is the ramp), their dX 37 us, an 8192 x 28672
-// 8-bit product 43 us (5.5 TB/s).  Small blocks take 4-7 us of waits one after
+// 8-bit product 41 us (5.7 TB/s).  Small blocks take 4-7 us of waits one after
 // the other: the first stage's 0.6 us, 0.15-0.3 us a stage, the clusters'
 // meetings 0.7 us each.
 #include "compute_device.cuh"
@@ -442,8 +442,10 @@ cudaError_t few_tc_prepare(TcDevice* dev) {
 //     split          0.35 and 4.5             0.33 and 7
 // (Gated, 420 x 10864 x 208: 14.0 here, 19.1 there; 123 x 7712 x 960 15.4 and
 // 17.0; 110 x 11584 x 3104 34.4 and 34.2; 1162 x 12880 x 544 62.9 and 35.7.
-// 8-bit, 420 x 208 x 10864: 9.1 and 15.2; 123 x 960 x 7712 10.1 and 11.7; 110
-// x 3104 x 11584 21.6 and 15.3; 1162 x 544 x 12880 40.0 and 18.0.)
+// 8-bit, 420 x 208 x 10864: 8.8 and 15.2; 123 x 960 x 7712 8.8 and 11.7; 110
+// x 3104 x 11584 21.6 and 15.3; 1162 x 544 x 12880 40.0 and 18.0.)  Clusters are
+// the forward kernel's for its gradients too, which take the same shared memory
+// and threads.
 bool gated_few_takes(const GatedArgs& a, const TcLaunch& l) {
   if (a.tokens <= 64 || !few(a.tokens, a.ffn, l.dev->sms / 2)) return few(a.tokens, a.ffn, 0);
   const int64_t steps = ceil_div(a.hidden, kRowBytes / 2);

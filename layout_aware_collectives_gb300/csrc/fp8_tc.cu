@@ -9,19 +9,22 @@
 // scaled_kernel: scales that are powers of two.  The tensor cores take them
 // as exponent bytes beside the codes, so the whole contraction is summed in
 // TMEM at their 8-bit rate.  Four warps write each stage's scales to TMEM.
-// 4096 x 8192 x 28672: 485-564 us, 3.4-4.0 PFLOP/s, by what the card's power
-// management allows: with all-zero codes the same kernel takes 427 us, 4.5
-// PFLOP/s, which is the tensor cores' nominal rate.  Reading a quarter less
+// 4096 x 8192 x 28672: 525-555 us in short bursts (3.5-3.7 PFLOP/s), 634 in a
+// run of passes (3.0), by what the card's power management allows: with all-zero
+// codes the same kernel takes 427 us, 4.5 PFLOP/s, which is the tensor cores'
+// nominal rate.  Reading a quarter less
 // from L2, by sharing rows between two pairs, changed nothing.
 //
 // summed_kernel: any scales.  A block's sums go from one of two TMEM
 // accumulators, times sa sb, into fp32 sums in the registers of 8 warps (one
-// fused multiply-add each, a row's scale being a thread's) while the tensor
+// fused multiply-add each, a row's scale being a thread's; times the one and
+// then the other where fp32 does not hold their product) while the tensor
 // cores sum the next block into the other.  A block is 512 cycles of the
 // tensor cores, but handing an accumulator there and back takes some 1,500:
 // the barriers' way between the two CTAs, TMEM reads and the multiply-adds
-// between them; and TMEM holds no third accumulator (4096 x 8192 x 28672:
-// 705-773 us, 2.5-2.7 PFLOP/s; 630 with all-zero codes).
+// between them; and TMEM holds no third accumulator (4096 x 8192 x 28672: 664 us
+// in short bursts, 745 in a run of passes, 2.6-2.9 PFLOP/s; 630 with all-zero
+// codes).
 #include "compute_device.cuh"
 #include "tc_device.cuh"
 #include "tc_host.h"
