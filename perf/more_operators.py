@@ -297,7 +297,7 @@ def _run_own(s):
     if kind == "orthogonalize":
         r, q = c["rows"], c["cols"]
         if "tables" not in s:
-            s["tables"] = [t.data_ptr() for t in s["grads"]], [t.data_ptr() for t in s["updates"]]
+            s["tables"] = tide.PointerTable(s["grads"].unbind(0)), tide.PointerTable(s["updates"].unbind(0))
             s["workspace"] = new(tide.orthogonalize_workspace_bytes(c["count"], r, q))
         o.orthogonalize(r, q, *s["tables"], s["workspace"], steps=STEPS, coefficients=COEFFICIENTS, eps=EPS,
                         src_type="fp32" if c["dtype"] == "float32" else "bf16", stream=stream)
