@@ -628,6 +628,153 @@ TIDE_API tide_status_t tide_gated_backward(tide_compute_t compute, int64_t token
                                            uint16_t* h, int64_t ld_h, void* workspace, int64_t workspace_bytes,
                                            cudaStream_t stream);
 
+/*
+ * The expert layer: what surrounds the gated blocks of a layer whose tokens
+ * each go to a few of its experts, and what becomes of its gradients.
+ *
+ * Conventions, besides those above: arrays of ids, slots, offsets, weights,
+ * biases and logits, gradients and updates are aligned to their elements
+ * (TIDE_ERR_MISALIGNED otherwise), the other buffers to 16 bytes; ids, slots and weights are [tokens, topk], contiguous.
+ */
+
+/* Element type of a router's logits and of an update's gradients. */
+typedef enum { TIDE_BF16 = 0, TIDE_FP32 = 1 } tide_dtype_t;
+
+/* An expert's score: softmax over a token's logits, or each one's sigmoid. */
+typedef enum { TIDE_SCORE_SOFTMAX = 0, TIDE_SCORE_SIGMOID = 1 } tide_score_t;
+
+#define TIDE_MAX_EXPERTS 1024
+#define TIDE_MAX_TOPK 16
+
+/*
+ * How a router chooses.
+ *   experts, topk   1 .. TIDE_MAX_EXPERTS; 1 .. TIDE_MAX_TOPK
+ *   score           tide_score_t
+ *   groups          the experts in order, in so many groups of one size (1: no
+ *                   groups; at most 32).  Only experts of the top_groups best
+ *                   groups are chosen, which hold at least topk experts.  A
+ *                   group's score is its best expert's or, with group_best =
+ *                   2, the sum of its best two (of its one, if it has one).
+ *   renormalize     0: weights are scores; 1: scores over the sum of the
+ *                   chosen ones'
+ *   scale           a factor of every weight
+ */
+typedef struct {
+  int32_t experts;
+  int32_t topk;
+  int32_t score;
+  int32_t groups;
+  int32_t top_groups;
+  int32_t group_best;
+  int32_t renormalize;
+  float scale;
+} tide_router_t;
+
+/*
+ * Routing of tokens to experts.
+ *   logits   [tokens, experts], bf16 or fp32 (`type`), row stride ld_logits
+ *   bias     [experts] or NULL: added to the scores for the choice alone
+ *   ids      receives each token's experts, the best first
+ *   weights  receives their weights, fp32
+ * A choice goes by score plus bias; equals go to the lowest index.  Scores
+ * that 32 bits may not tell apart are compared in 64 (without a bias, and
+ * unless groups go by two scores, logits themselves are compared).  A logit
+ * of -infinity is a masked expert: its score is 0; a token whose experts are
+ * all masked has weights of 0 and the lowest indices the bias leaves it.  NaN
+ * ranks below everything, and a token's ids are valid and distinct whatever
+ * its logits are.  A softmax with a NaN or +infinity among its logits has NaN
+ * weights.
+ */
+TIDE_API tide_status_t tide_route(tide_compute_t compute, int64_t tokens, const tide_router_t* router,
+                                  tide_dtype_t type, const void* logits, int64_t ld_logits, const float* bias,
+                                  int32_t* ids, float* weights, cudaStream_t stream);
+
+/*
+ * The logits' gradients from the weights' (the choice itself has none, nor has
+ * the bias).  dlogits [tokens, experts] has the logits' type; all of it is
+ * written, zeros where a logit has no part in a weight.  An id outside the
+ * experts is passed over; one that stands twice counts twice.
+ */
+TIDE_API tide_status_t tide_route_backward(tide_compute_t compute, int64_t tokens, const tide_router_t* router,
+                                           tide_dtype_t type, const void* logits, int64_t ld_logits,
+                                           const int32_t* ids, const float* dweights, void* dlogits,
+                                           int64_t ld_dlogits, cudaStream_t stream);
+
+/* Bytes of tide_expert_slots's workspace. */
+TIDE_API tide_status_t tide_expert_slots_workspace(int64_t tokens, int64_t topk, int64_t experts, int64_t* bytes);
+
+/*
+ * Expert order: the pairs (token, choice) by expert, and within an expert by
+ * token.
+ *   ids      [tokens, topk]; one outside the experts belongs to none
+ *   slots    receives each pair's place in that order, -1 for none
+ *   offsets  [experts + 1] receives each expert's first place, and the end
+ * tokens * topk is below 2^31, topk at most 1024, experts 1 ..
+ * TIDE_MAX_EXPERTS.
+ */
+TIDE_API tide_status_t tide_expert_slots(tide_compute_t compute, int64_t tokens, int64_t topk, int64_t experts,
+                                         const int32_t* ids, int32_t* slots, int32_t* offsets, void* workspace,
+                                         int64_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Tokens' rows to their experts and back.  `rows` is [num_rows, hidden] in
+ * expert order; a slot outside it is passed over, and rows without a slot
+ * stay as they are.  Two pairs do not share a slot.
+ *
+ *   tide_expert_gather   rows[slots[t, j]] = x[t]
+ *   tide_expert_combine  y[t] = sum over j, in order, of weights[t, j] *
+ *       rows[slots[t, j]]; weights NULL: 1 each, which makes it the
+ *       gather's backward pass
+ *   tide_expert_combine_backward
+ *       drows[slots[t, j]] = weights[t, j] * dy[t]
+ *       dweights[t, j] = sum of dy[t] * rows[slots[t, j]], 0 for a slot
+ *       outside.  weights NULL: 1 each; either output may be NULL, and rows
+ *       may be where dweights is.
+ */
+TIDE_API tide_status_t tide_expert_gather(tide_compute_t compute, int64_t tokens, int64_t hidden, int64_t topk,
+                                          const uint16_t* x, int64_t ld_x, const int32_t* slots, uint16_t* rows,
+                                          int64_t num_rows, int64_t ld_rows, cudaStream_t stream);
+TIDE_API tide_status_t tide_expert_combine(tide_compute_t compute, int64_t tokens, int64_t hidden, int64_t topk,
+                                           const uint16_t* rows, int64_t num_rows, int64_t ld_rows,
+                                           const int32_t* slots, const float* weights, uint16_t* y, int64_t ld_y,
+                                           cudaStream_t stream);
+TIDE_API tide_status_t tide_expert_combine_backward(tide_compute_t compute, int64_t tokens, int64_t hidden,
+                                                    int64_t topk, const uint16_t* dy, int64_t ld_dy,
+                                                    const uint16_t* rows, int64_t num_rows, int64_t ld_rows,
+                                                    const int32_t* slots, const float* weights, uint16_t* drows,
+                                                    int64_t ld_drows, float* dweights, cudaStream_t stream);
+
+/* Bytes of tide_orthogonalize's workspace for `count` matrices. */
+TIDE_API tide_status_t tide_orthogonalize_workspace(int64_t count, int64_t rows, int64_t cols, int64_t* bytes);
+
+#define TIDE_MAX_ORTHOGONALIZE_STEPS 16
+
+/*
+ * Orthogonalised updates: each of `count` matrices G, [rows, cols], is brought
+ * towards the orthogonal factor of its polar decomposition by Newton-Schulz
+ * products.  With X = G / (|G| + eps), |G| the root of the sum of its squares,
+ * `steps` times
+ *   X = a X + (b A + c A A) X,  A = X X^T   (X^T X on the other side, where
+ *                                            rows > cols)
+ *   src, dst      HOST tables of `count` device pointers; src bf16 or fp32
+ *                 (`type`), dst bf16; row strides ld_src, ld_dst
+ *   coefficients  HOST, a, b and c of each step, or NULL: 3.4445, -4.7750 and
+ *                 2.0315 in every step; finite, and such that singular values
+ *                 stay below 2^16
+ *   workspace     at least tide_orthogonalize_workspace bytes
+ * Rows and columns of zeros stay zero, so a padded gradient may be passed
+ * as it is.  A matrix with an infinity or NaN becomes NaN.
+ * X and A are kept as two fp16 terms.  Products take their first, and the
+ * diagonals of A and of b A + c A A in fp32 beside them: what that leaves is
+ * below the result's own rounding to bf16.  Sums are fp32.  What is below 2^-37
+ * of the largest norm that X can have in a step counts as nothing.
+ */
+TIDE_API tide_status_t tide_orthogonalize(tide_compute_t compute, int64_t count, int64_t rows, int64_t cols,
+                                          tide_dtype_t type, const void* const* src, int64_t ld_src,
+                                          uint16_t* const* dst, int64_t ld_dst, int32_t steps,
+                                          const float* coefficients, float eps, void* workspace,
+                                          int64_t workspace_bytes, cudaStream_t stream);
+
 /* "release", or "debug: device range checks" for the library built with
  * TIDE_DEBUG=1 (libtide_debug.so). */
 TIDE_API const char* tide_build_info(void);

@@ -1,5 +1,6 @@
-"""Owning wrapper around a tide_compute_t handle: the feed-forward unit's
-operators between a placement and the reduce-scatter (marshalling only)."""
+"""Owning wrapper around a tide_compute_t handle: the operators of the
+feed-forward unit between a placement and the reduce-scatter, and of an expert
+layer around it (marshalling only)."""
 from __future__ import annotations
 
 from . import tide as _t
@@ -15,8 +16,23 @@ class GatedCheckpoint:
         self.struct = _t.GatedCheckpointStruct(*(_t._addr(b) for b in self.keep))
 
 
+class Router:
+    """How tokens choose their experts (tide_router_t); see include/tide.h."""
+
+    def __init__(self, experts: int, topk: int, score: str = "softmax", groups: int = 1, top_groups: int = 1,
+                 group_best: int = 1, renormalize: bool = True, scale: float = 1.0):
+        self.experts, self.topk = experts, topk
+        self.struct = _t.RouterStruct(experts, topk, _t._named(_t._SCORES, score, "score"), groups, top_groups,
+                                      group_best, 1 if renormalize else 0, scale)
+
+
+def _bytes(workspace, given):
+    """A tensor's own size where it is left out; an address has none."""
+    return workspace.numel() * workspace.element_size() if given is None else given
+
+
 class Compute:
-    """Feed-forward operators; see include/tide.h.
+    """Operators of the feed-forward unit and the expert layer; see include/tide.h.
 
     Row strides (ld_*) default to the row's width."""
 
@@ -47,12 +63,54 @@ class Compute:
                        workspace_bytes=None, ld_dh=None, ld_x=None, ld_dx=None, ld_h=None, stream=None):
         """workspace_bytes: a tensor's own size where it is left out; to be
         given with an address."""
-        if workspace_bytes is None:
-            workspace_bytes = workspace.numel() * workspace.element_size()
+        workspace_bytes = _bytes(workspace, workspace_bytes)
         _t.tide_gated_backward(self.handle, tokens, hidden, ffn, activation, dh, ffn if ld_dh is None else ld_dh, x,
                                hidden if ld_x is None else ld_x, w_gate, w_up, checkpoint, dx,
                                hidden if ld_dx is None else ld_dx, dw_gate, dw_up, h, ffn if ld_h is None else ld_h,
                                workspace, workspace_bytes, stream)
+
+    # -------- the expert layer
+    def route(self, router: Router, tokens: int, logits, ids, weights, bias=None, logits_type: str = "fp32",
+              ld_logits=None, stream=None):
+        _t.tide_route(self.handle, tokens, router, logits_type, logits,
+                      router.experts if ld_logits is None else ld_logits, bias, ids, weights, stream)
+
+    def route_backward(self, router: Router, tokens: int, logits, ids, dweights, dlogits, logits_type: str = "fp32",
+                       ld_logits=None, ld_dlogits=None, stream=None):
+        _t.tide_route_backward(self.handle, tokens, router, logits_type, logits,
+                               router.experts if ld_logits is None else ld_logits, ids, dweights, dlogits,
+                               router.experts if ld_dlogits is None else ld_dlogits, stream)
+
+    def expert_slots(self, tokens: int, topk: int, experts: int, ids, slots, offsets, workspace, workspace_bytes=None,
+                     stream=None):
+        """workspace_bytes: as in gated_backward."""
+        _t.tide_expert_slots(self.handle, tokens, topk, experts, ids, slots, offsets, workspace,
+                             _bytes(workspace, workspace_bytes), stream)
+
+    def expert_gather(self, tokens: int, hidden: int, topk: int, x, slots, rows, num_rows: int, ld_x=None, ld_rows=None,
+                      stream=None):
+        _t.tide_expert_gather(self.handle, tokens, hidden, topk, x, hidden if ld_x is None else ld_x, slots, rows,
+                              num_rows, hidden if ld_rows is None else ld_rows, stream)
+
+    def expert_combine(self, tokens: int, hidden: int, topk: int, rows, num_rows: int, slots, weights, y, ld_rows=None,
+                       ld_y=None, stream=None):
+        _t.tide_expert_combine(self.handle, tokens, hidden, topk, rows, num_rows,
+                               hidden if ld_rows is None else ld_rows, slots, weights, y,
+                               hidden if ld_y is None else ld_y, stream)
+
+    def expert_combine_backward(self, tokens: int, hidden: int, topk: int, dy, rows, num_rows: int, slots, weights,
+                                drows, dweights, ld_dy=None, ld_rows=None, ld_drows=None, stream=None):
+        _t.tide_expert_combine_backward(self.handle, tokens, hidden, topk, dy, hidden if ld_dy is None else ld_dy, rows,
+                                        num_rows, hidden if ld_rows is None else ld_rows, slots, weights, drows,
+                                        hidden if ld_drows is None else ld_drows, dweights, stream)
+
+    def orthogonalize(self, rows: int, cols: int, src, dst, workspace, steps: int = 5, coefficients=None,
+                      eps: float = 1e-7, src_type: str = "fp32", workspace_bytes=None, ld_src=None, ld_dst=None,
+                      stream=None):
+        """src, dst: lists of matrices of one size; workspace_bytes: as in gated_backward."""
+        _t.tide_orthogonalize(self.handle, rows, cols, src_type, src, cols if ld_src is None else ld_src, dst,
+                              cols if ld_dst is None else ld_dst, steps, coefficients, eps, workspace,
+                              _bytes(workspace, workspace_bytes), stream)
 
     def check_device(self) -> None:
         _t.tide_compute_check_device(self.handle)

@@ -4,107 +4,11 @@
 #include <new>
 #include <string>
 
-#include "compute_internal.h"
+#include "compute_checks.h"
 
 using namespace tide;
 
 namespace {
-
-constexpr int64_t kMaxDim = INT32_MAX;
-constexpr int64_t kMaxNumel = (int64_t)1 << 38;
-
-#define TIDE_TRY(call)                  \
-  do {                                  \
-    const tide_status_t s_ = (call);    \
-    if (s_ != TIDE_OK) return s_;       \
-  } while (0)
-
-// No exception (of a message's or a lock's making) leaves a C entry.
-#define TIDE_CATCH \
-  catch (...) { return TIDE_ERR_OUT_OF_MEMORY; }
-
-tide_status_t invalid(const std::string& msg) { return set_error(TIDE_ERR_INVALID_ARG, msg); }
-
-tide_status_t check_dims(int64_t a, int64_t b, const char* what) {
-  if (a < 0 || b < 0 || a > kMaxDim || b > kMaxDim || (b && a > kMaxNumel / b))
-    return invalid(std::string(what) + ": sizes out of range");
-  return TIDE_OK;
-}
-
-tide_status_t check_buffer(const void* p, int64_t numel, const char* what) {
-  if (numel == 0) return TIDE_OK;
-  if (!p) return invalid(std::string(what) + " is NULL");
-  if ((uintptr_t)p & 15u) return set_error(TIDE_ERR_MISALIGNED, std::string(what) + " is not 16-byte aligned");
-  return TIDE_OK;
-}
-
-// A matrix of `rows` rows of `cols` elements, `ld` apart.
-tide_status_t check_matrix(const void* p, int64_t rows, int64_t cols, int64_t ld, const char* what) {
-  TIDE_TRY(check_buffer(p, rows * cols, what));
-  if (ld < cols || (rows && ld > kMaxNumel / rows)) return invalid(std::string(what) + ": row stride out of range");
-  return TIDE_OK;
-}
-
-tide_status_t check_blocks(const void* codes, const void* scales, int64_t rows, int64_t cols, const char* what) {
-  TIDE_TRY(check_buffer(codes, rows * cols, (std::string(what) + " codes").c_str()));
-  if (rows * cols == 0) return TIDE_OK;
-  if (!scales) return invalid(std::string(what) + " scales is NULL");
-  if ((uintptr_t)scales & 3u) return set_error(TIDE_ERR_MISALIGNED, std::string(what) + " scales is not 4-byte aligned");
-  return TIDE_OK;
-}
-
-bool capturing(cudaStream_t stream) {
-  cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
-  if (cudaStreamIsCapturing(stream, &st) != cudaSuccess) {
-    cudaGetLastError();
-    return false;
-  }
-  return st == cudaStreamCaptureStatusActive;
-}
-
-// The current device, which is a bound handle's.
-tide_status_t current_device(const tide_compute_s* c, int* dev) {
-  const cudaError_t e = cudaGetDevice(dev);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-  if (c->device >= 0 && *dev != c->device)
-    return invalid("handle is bound to device " + std::to_string(c->device) + " but device " + std::to_string(*dev) +
-                   " is current");
-  return TIDE_OK;
-}
-
-// Binds the handle to the current device on first use.
-tide_status_t bind(tide_compute_s* c, cudaStream_t stream) {
-  std::lock_guard<std::mutex> g(c->mu);
-  int dev = 0;
-  TIDE_TRY(current_device(c, &dev));
-  if (c->device >= 0) return TIDE_OK;
-  if (capturing(stream))
-    return set_error(TIDE_ERR_UNSUPPORTED,
-                     "the handle's first call sets it up on the device and cannot be captured; make one call before");
-  cudaError_t e = cudaDeviceGetAttribute(&c->dev.sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute(MultiProcessorCount)");
-  e = gated_tc_prepare(&c->dev);
-  if (e == cudaSuccess) e = fp8_tc_prepare(&c->dev);
-  if (e == cudaSuccess) e = few_tc_prepare(&c->dev);
-  if (e != cudaSuccess) return cuda_fail(e, "set-up of the tensor-core kernels");
-  if (c->dev.pairs < 1) return set_error(TIDE_ERR_CUDA, "the device holds no pair of tensor-core CTAs");
-  if (!c->err) {
-    e = cudaHostAlloc((void**)&c->err, sizeof(int), cudaHostAllocMapped);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaHostAlloc(error word)");
-    *c->err = 0;
-    e = cudaHostGetDevicePointer((void**)&c->d_err, c->err, 0);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaHostGetDevicePointer(error word)");
-  }
-  c->device = dev;
-  return TIDE_OK;
-}
-
-TcLaunch launch_of(tide_compute_s* c) {
-  std::lock_guard<std::mutex> g(c->mu);
-  return TcLaunch{&c->dev, c->d_err, (uint64_t)c->test_stall_ns, (uint64_t)c->test_late_ns};
-}
-
-tide_status_t launched(cudaError_t e, const char* what) { return e == cudaSuccess ? TIDE_OK : cuda_fail(e, what); }
 
 tide_status_t check_gated(const GatedArgs& a, const char* what) {
   TIDE_TRY(check_dims(a.tokens, a.hidden, what));
@@ -122,8 +26,6 @@ tide_status_t check_checkpoint(const tide_gated_checkpoint_t* c, int64_t tokens,
   return TIDE_OK;
 }
 
-int64_t round256(int64_t v) { return (v + 255) / 256 * 256; }
-
 // Offsets of the workspace's parts.
 struct Workspace {
   int64_t dg, du, x, dx_parts, dw_parts, bytes;
@@ -140,6 +42,34 @@ Workspace workspace_of(int64_t tokens, int64_t hidden, int64_t ffn) {
 }
 
 }  // namespace
+
+// Binds the handle to the current device on first use.
+tide_status_t tide::bind(tide_compute_s* c, cudaStream_t stream) {
+  std::lock_guard<std::mutex> g(c->mu);
+  int dev = 0;
+  TIDE_TRY(current_device(c, &dev));
+  if (c->device >= 0) return TIDE_OK;
+  if (capturing(stream))
+    return set_error(TIDE_ERR_UNSUPPORTED,
+                     "the handle's first call sets it up on the device and cannot be captured; make one call before");
+  cudaError_t e = cudaDeviceGetAttribute(&c->dev.sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute(MultiProcessorCount)");
+  e = gated_tc_prepare(&c->dev);
+  if (e == cudaSuccess) e = fp8_tc_prepare(&c->dev);
+  if (e == cudaSuccess) e = few_tc_prepare(&c->dev);
+  if (e == cudaSuccess) e = ortho_prepare(&c->dev);
+  if (e != cudaSuccess) return cuda_fail(e, "set-up of the tensor-core kernels");
+  if (c->dev.pairs < 1) return set_error(TIDE_ERR_CUDA, "the device holds no pair of tensor-core CTAs");
+  if (!c->err) {
+    e = cudaHostAlloc((void**)&c->err, sizeof(int), cudaHostAllocMapped);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaHostAlloc(error word)");
+    *c->err = 0;
+    e = cudaHostGetDevicePointer((void**)&c->d_err, c->err, 0);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaHostGetDevicePointer(error word)");
+  }
+  c->device = dev;
+  return TIDE_OK;
+}
 
 extern "C" {
 

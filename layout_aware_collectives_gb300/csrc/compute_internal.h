@@ -1,6 +1,7 @@
 // Internal interface between the feed-forward unit's C ABI (compute_api.cpp)
 // and its kernels (gated_tc.cu, few_tc.cu, fp8_tc.cu, fp8_blocks.cu,
-// gated_simple.cu).
+// gated_simple.cu), and between the expert layer's (expert_api.cpp) and its
+// own (router.cu, expert_rows.cu, ortho.cu).
 #pragma once
 
 #include <cuda_runtime_api.h>
@@ -64,6 +65,61 @@ struct MatmulArgs {
   uint16_t* out;
   int64_t ldo;
   bool any_scales;  // else powers of two
+};
+
+// One call of a router, forward or backward.
+struct RouterArgs {
+  int64_t tokens;
+  int experts, topk, score, groups, top_groups, group_best;
+  bool renormalize;
+  float scale;
+  bool bf16;  // the logits' type
+  const void* logits;
+  int64_t ld;
+  const float* bias;
+  int32_t* ids;  // read by the backward pass
+  float* weights;
+  const float* dweights;  // backward
+  void* dlogits;
+  int64_t ldd;
+};
+
+struct SlotsArgs {
+  int64_t pairs;  // tokens * topk
+  int experts;
+  const int32_t* ids;
+  int32_t* slots;
+  int32_t* offsets;
+  int32_t* counts;  // of each chunk of pairs, workspace
+};
+
+// Tokens' rows and experts' rows.  `row` [num_rows, hidden] is what the slots
+// point into, `token` [tokens, hidden].
+struct RowsArgs {
+  int64_t tokens, hidden, num_rows;
+  int topk;
+  const int32_t* slots;
+  const float* weights;  // NULL: 1 each
+  const uint16_t* in;    // gather, combine_backward: of tokens; combine: rows
+  int64_t ld_in;
+  const uint16_t* rows;  // combine_backward: the rows, for the weights' gradients
+  int64_t ld_rows;
+  uint16_t* out;  // gather, combine_backward: rows (NULL: none); combine: of tokens
+  int64_t ld_out;
+  float* dweights;  // NULL: none
+};
+
+struct OrthoArgs {
+  int64_t count, rows, cols;
+  bool bf16;  // the gradients' type
+  const void* const* src;  // host tables
+  int64_t ld_src;
+  uint16_t* const* dst;
+  int64_t ld_dst;
+  int steps;
+  const float* coefficients;  // a, b, c of each step
+  float eps;
+  char* workspace;
 };
 
 // Bytes <-> blocks (fp8_blocks.cu).
@@ -174,6 +230,20 @@ bool gated_dx_few_takes(const GatedArgs& a, const TcLaunch& l);
 cudaError_t launch_gated_dx_few(const GatedArgs& a, const TcLaunch& l, cudaStream_t stream);
 cudaError_t launch_gated_forward_few(const GatedArgs& a, const TcLaunch& l, cudaStream_t stream);
 cudaError_t launch_fp8_matmul_few(const MatmulArgs& a, const TcLaunch& l, cudaStream_t stream);
+
+// The expert layer (router.cu, expert_rows.cu, ortho.cu).
+cudaError_t launch_route(const RouterArgs& a, cudaStream_t stream);
+cudaError_t launch_route_backward(const RouterArgs& a, cudaStream_t stream);
+int64_t slots_workspace_bytes(int64_t pairs, int64_t experts);
+cudaError_t launch_expert_slots(const SlotsArgs& a, cudaStream_t stream);
+cudaError_t launch_expert_gather(const RowsArgs& a, cudaStream_t stream);
+cudaError_t launch_expert_combine(const RowsArgs& a, cudaStream_t stream);
+cudaError_t launch_expert_combine_backward(const RowsArgs& a, cudaStream_t stream);
+cudaError_t ortho_prepare(TcDevice* dev);
+int64_t ortho_workspace_bytes(int64_t count, int64_t rows, int64_t cols);
+// Whether singular values stay within what the kernels' scales hold.
+bool ortho_bounded(int steps, const float* coefficients);
+cudaError_t launch_orthogonalize(const OrthoArgs& a, const TcLaunch& l, cudaStream_t stream);
 
 }  // namespace tide
 

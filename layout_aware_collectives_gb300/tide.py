@@ -45,6 +45,16 @@ TIDE_OP_STAGED_RS = 4
 TIDE_ACT_SILU = 0
 TIDE_ACT_GELU = 1
 
+TIDE_BF16 = 0
+TIDE_FP32 = 1
+
+TIDE_SCORE_SOFTMAX = 0
+TIDE_SCORE_SIGMOID = 1
+
+TIDE_MAX_EXPERTS = 1024
+TIDE_MAX_TOPK = 16
+TIDE_MAX_ORTHOGONALIZE_STEPS = 16
+
 TIDE_MAX_RANKS = 4096
 TIDE_IPC_HANDLE_BYTES = 64
 TIDE_NOALLOC_SCRATCH_BYTES = 4 << 20
@@ -109,6 +119,18 @@ _sig("tide_gated_forward", _st, _vp, _i64, _i64, _i64, ctypes.c_int, _vp, _i64, 
 _sig("tide_gated_workspace", _st, _i64, _i64, _i64, _i64p)
 _sig("tide_gated_backward", _st, _vp, _i64, _i64, _i64, ctypes.c_int, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i64,
      _vp, _vp, _vp, _i64, _vp, _i64, _vp)
+_i32 = ctypes.c_int32
+_sig("tide_route", _st, _vp, _i64, _vp, ctypes.c_int, _vp, _i64, _vp, _vp, _vp, _vp)
+_sig("tide_route_backward", _st, _vp, _i64, _vp, ctypes.c_int, _vp, _i64, _vp, _vp, _vp, _i64, _vp)
+_sig("tide_expert_slots_workspace", _st, _i64, _i64, _i64, _i64p)
+_sig("tide_expert_slots", _st, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _i64, _vp)
+_sig("tide_expert_gather", _st, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _vp)
+_sig("tide_expert_combine", _st, _vp, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _vp, _i64, _vp)
+_sig("tide_expert_combine_backward", _st, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _vp, _vp, _i64, _vp,
+     _vp)
+_sig("tide_orthogonalize_workspace", _st, _i64, _i64, _i64, _i64p)
+_sig("tide_orthogonalize", _st, _vp, _i64, _i64, _i64, ctypes.c_int, _vp, _i64, _vp, _i64, _i32, _vp, ctypes.c_float,
+     _vp, _i64, _vp)
 _sig("tide_build_info", ctypes.c_char_p)
 _sig("tide_status_string", ctypes.c_char_p, _st)
 _sig("tide_last_error", ctypes.c_char_p)
@@ -453,6 +475,100 @@ def tide_gated_backward(compute, tokens, hidden, ffn, act, dh, ld_dh, x, ld_x, w
                                     _addr(w_gate), _addr(w_up), _checkpoint(checkpoint), _addr(dx), ld_dx,
                                     _addr(dw_gate), _addr(dw_up), _addr(h), ld_h, _addr(workspace), workspace_bytes,
                                     _stream(stream)), "tide_gated_backward")
+
+
+class RouterStruct(ctypes.Structure):
+    """tide_router_t."""
+
+    _fields_ = [(n, ctypes.c_int32)
+                for n in ("experts", "topk", "score", "groups", "top_groups", "group_best", "renormalize")] + [
+                    ("scale", ctypes.c_float)]
+
+
+def _named(names, v, what) -> int:
+    if isinstance(v, str):
+        if v not in names:
+            raise ValueError(f"{what} {v!r}: one of {sorted(names)}")
+        return names[v]
+    return int(v)
+
+
+_TYPES = {"bf16": TIDE_BF16, "fp32": TIDE_FP32}
+_SCORES = {"softmax": TIDE_SCORE_SOFTMAX, "sigmoid": TIDE_SCORE_SIGMOID}
+
+
+def _router(r):
+    return ctypes.addressof(r.struct) if r is not None else 0
+
+
+def tide_route(compute, tokens, router, type, logits, ld_logits, bias, ids, weights, stream=None) -> None:
+    """ids and weights [tokens, topk] from logits [tokens, experts]; see include/tide.h."""
+    _check(_lib.tide_route(compute, tokens, _router(router), _named(_TYPES, type, "logits' type"), _addr(logits),
+                           ld_logits, _addr(bias), _addr(ids), _addr(weights), _stream(stream)), "tide_route")
+
+
+def tide_route_backward(compute, tokens, router, type, logits, ld_logits, ids, dweights, dlogits, ld_dlogits,
+                        stream=None) -> None:
+    """dlogits [tokens, experts] from dweights [tokens, topk]."""
+    _check(_lib.tide_route_backward(compute, tokens, _router(router), _named(_TYPES, type, "logits' type"),
+                                    _addr(logits), ld_logits, _addr(ids), _addr(dweights), _addr(dlogits), ld_dlogits,
+                                    _stream(stream)), "tide_route_backward")
+
+
+def expert_slots_workspace_bytes(tokens: int, topk: int, experts: int) -> int:
+    """Bytes of tide_expert_slots's workspace."""
+    return _q64("tide_expert_slots_workspace", tokens, topk, experts)
+
+
+def tide_expert_slots(compute, tokens, topk, experts, ids, slots, offsets, workspace, workspace_bytes,
+                      stream=None) -> None:
+    """slots [tokens, topk] and offsets [experts + 1] of the pairs in expert order."""
+    _check(_lib.tide_expert_slots(compute, tokens, topk, experts, _addr(ids), _addr(slots), _addr(offsets),
+                                  _addr(workspace), workspace_bytes, _stream(stream)), "tide_expert_slots")
+
+
+def tide_expert_gather(compute, tokens, hidden, topk, x, ld_x, slots, rows, num_rows, ld_rows, stream=None) -> None:
+    """rows[slots[t, j]] = x[t]."""
+    _check(_lib.tide_expert_gather(compute, tokens, hidden, topk, _addr(x), ld_x, _addr(slots), _addr(rows), num_rows,
+                                   ld_rows, _stream(stream)), "tide_expert_gather")
+
+
+def tide_expert_combine(compute, tokens, hidden, topk, rows, num_rows, ld_rows, slots, weights, y, ld_y,
+                        stream=None) -> None:
+    """y[t] = sum of weights[t, j] * rows[slots[t, j]]."""
+    _check(_lib.tide_expert_combine(compute, tokens, hidden, topk, _addr(rows), num_rows, ld_rows, _addr(slots),
+                                    _addr(weights), _addr(y), ld_y, _stream(stream)), "tide_expert_combine")
+
+
+def tide_expert_combine_backward(compute, tokens, hidden, topk, dy, ld_dy, rows, num_rows, ld_rows, slots, weights,
+                                 drows, ld_drows, dweights, stream=None) -> None:
+    """drows and dweights from dy."""
+    _check(_lib.tide_expert_combine_backward(compute, tokens, hidden, topk, _addr(dy), ld_dy, _addr(rows), num_rows,
+                                             ld_rows, _addr(slots), _addr(weights), _addr(drows), ld_drows,
+                                             _addr(dweights), _stream(stream)), "tide_expert_combine_backward")
+
+
+def orthogonalize_workspace_bytes(count: int, rows: int, cols: int) -> int:
+    """Bytes of tide_orthogonalize's workspace."""
+    return _q64("tide_orthogonalize_workspace", count, rows, cols)
+
+
+def tide_orthogonalize(compute, rows, cols, type, src, ld_src, dst, ld_dst, steps, coefficients, eps, workspace,
+                       workspace_bytes, stream=None) -> None:
+    """src, dst: as many matrices each; coefficients: a, b, c of each step, of all steps, or None."""
+    s, d = _table(src), _table(dst)
+    if s.n != d.n:
+        raise ValueError(f"{s.n} sources, {d.n} destinations")
+    c = None
+    if coefficients is not None:
+        c = np.ascontiguousarray(coefficients, dtype=np.float32).reshape(-1)
+        if c.size == 3:
+            c = np.tile(c, max(1, steps))
+        if c.size != 3 * max(1, steps):
+            raise ValueError(f"{c.size} coefficients: three, or three for each of {steps} steps")
+    _check(_lib.tide_orthogonalize(compute, s.n, rows, cols, _named(_TYPES, type, "gradients' type"), _tptr(s),
+                                   ld_src, _tptr(d), ld_dst, steps, 0 if c is None else c.ctypes.data, eps,
+                                   _addr(workspace), workspace_bytes, _stream(stream)), "tide_orthogonalize")
 
 
 def exported_symbols():
