@@ -1,4 +1,4 @@
-// Newton-Schulz orthogonalisation: norms, the first X, and the products.
+// Newton-Schulz orthogonalisation: norms, the first X, and the steps.
 #include <cmath>
 
 #include "ortho.cuh"
@@ -12,9 +12,6 @@ constexpr int kMaxParts = 64;
 
 struct Sources {
   const void* p[kOrthoTable];
-};
-struct Targets {
-  uint16_t* p[kOrthoTable];
 };
 
 template <class T>
@@ -101,7 +98,7 @@ __device__ Inverse inverse_norm(const OrthoPlan& p, int64_t z, float eps) {
 // no steps to come it goes to the caller instead.
 constexpr int kTile = 64;
 template <class T>
-__global__ void __launch_bounds__(kThreads) first_kernel(OrthoPlan p, Sources s, Targets out, int64_t first, int64_t rows,
+__global__ void __launch_bounds__(kThreads) first_kernel(OrthoPlan p, Sources s, OrthoTargets out, int64_t first, int64_t rows,
                                                          int64_t cols, int64_t ld, float eps, float scale, int64_t ld_out) {
   after_previous();
   __shared__ float tile[kTile][kTile + 1];
@@ -131,74 +128,6 @@ __global__ void __launch_bounds__(kThreads) first_kernel(OrthoPlan p, Sources s,
     const int64_t at = (z * p.m + i0 + y) * p.ld_x + j0 + x;
     split_half(tile[y][x] * scale, p.x[0][0][at], p.x[0][1][at]);
   }
-}
-
-// One product, 64 x 64 of it a CTA, 4 x 4 a thread.
-template <OrthoForm FORM>
-__global__ void __launch_bounds__(kThreads) product_kernel(OrthoPlan p, OrthoStep s, int turn, Targets out, int64_t first,
-                                                           int64_t ld_out) {
-  after_previous();
-  constexpr int kK = 16;
-  __shared__ float left[kK][kTile + 4], right[kK][kTile + 4];
-  const int64_t z = first + blockIdx.z;
-  const __half* xh = p.x[turn][0] + z * p.m * p.ld_x;
-  const __half* xl = p.x[turn][1] + z * p.m * p.ld_x;
-  const int64_t za = z * p.m * p.ld_a;
-  const __half* l = FORM == kGram ? xh : FORM == kSquare ? p.o[0] + za : p.p + za;
-  const __half* r = FORM == kSquare ? p.o[0] + za : xh;
-  const int64_t ldl = FORM == kGram ? p.ld_x : p.ld_a, ldr = FORM == kSquare ? p.ld_a : p.ld_x;
-  const int depth = FORM == kGram ? p.n : p.m, wide = FORM >= kUpdate ? p.n : p.m;
-  const int i0 = blockIdx.y * kTile, j0 = blockIdx.x * kTile;
-  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-  float sum[4][4] = {};
-  for (int k0 = 0; k0 < depth; k0 += kK) {
-    for (int e = threadIdx.x; e < kTile * kK; e += kThreads) {
-      int k = e % kK, i = e / kK;
-      left[k][i] = i0 + i < p.m && k0 + k < depth ? __half2float(l[(i0 + i) * ldl + k0 + k]) : 0.0f;
-      if (FORM >= kUpdate) {
-        i = e % kTile, k = e / kTile;
-        right[k][i] = j0 + i < wide && k0 + k < depth ? __half2float(r[(k0 + k) * ldr + j0 + i]) : 0.0f;
-      } else {
-        right[k][i] = j0 + i < wide && k0 + k < depth ? __half2float(r[(j0 + i) * ldr + k0 + k]) : 0.0f;
-      }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kK; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) sum[i][j] = fmaf(left[k][ty * 4 + i], right[k][tx * 4 + j], sum[i][j]);
-    __syncthreads();
-  }
-  for (int u = 0; u < 4; ++u)
-    for (int v = 0; v < 4; ++v) {
-      const int i = i0 + ty * 4 + u, j = j0 + tx * 4 + v;
-      if (i >= p.m || j >= wide) continue;
-      const float acc = sum[u][v];
-      const int64_t at = za + i * p.ld_a + j;
-      if (FORM == kGram) {
-        const float g = acc / (s.x_scale * s.x_scale);
-        if (i == j) p.d[z * p.m + i] = g;
-        split_half(i == j ? 0.0f : g * s.a_scale, p.o[0][at], p.o[1][at]);
-      } else if (FORM == kSquare) {
-        const float di = p.d[z * p.m + i], dj = p.d[z * p.m + j];
-        const float o = (__half2float(p.o[0][at]) + __half2float(p.o[1][at])) / s.a_scale;
-        const float aa = acc / (s.a_scale * s.a_scale) + (di + dj) * o + (i == j ? di * di : 0.0f);
-        const float b = s.b * (i == j ? di : o) + s.c * aa;
-        if (i == j) p.e[z * p.m + i] = b;
-        p.p[at] = __float2half_rn(i == j ? 0.0f : b * s.b_scale);
-      } else {
-        const float x = (__half2float(xh[i * p.ld_x + j]) + __half2float(xl[i * p.ld_x + j])) / s.x_scale;
-        const float y = (s.a + p.e[z * p.m + i]) * x + acc / (s.b_scale * s.x_scale);
-        if (FORM == kUpdate) {
-          const int64_t to = (z * p.m + i) * p.ld_x + j;
-          split_half(y * s.next_scale, p.x[turn ^ 1][0][to], p.x[turn ^ 1][1][to]);
-        } else {
-          out.p[blockIdx.z][p.tall ? j * ld_out + i : i * ld_out + j] = to_bf16(y);
-        }
-      }
-    }
 }
 
 // ------------------------------------------------------------ host side
@@ -271,23 +200,7 @@ bool steps_of(int steps, const float* k, OrthoStep* out) {
   return true;
 }
 
-template <OrthoForm FORM>
-cudaError_t product(const OrthoPlan& p, const OrthoStep& s, int turn, const OrthoArgs* a, cudaStream_t stream) {
-  const unsigned down = (unsigned)ceil_div(p.m, kTile), across = (unsigned)ceil_div(FORM >= kUpdate ? p.n : p.m, kTile);
-  for (int64_t first = 0; first < p.count; first += kOrthoTable) {
-    const int64_t some = p.count - first < kOrthoTable ? p.count - first : kOrthoTable;
-    Targets out{};
-    for (int64_t i = 0; a && i < some; ++i) out.p[i] = a->dst[first + i];
-    const cudaError_t e = launch_early(product_kernel<FORM>, dim3(across, down, (unsigned)some), kThreads, 0, 0, stream, p, s,
-                                       turn, out, first, a ? a->ld_dst : (int64_t)0);
-    if (e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
-}
-
 }  // namespace
-
-cudaError_t ortho_prepare(TcDevice*) { return cudaSuccess; }
 
 int64_t ortho_workspace_bytes(int64_t count, int64_t rows, int64_t cols) {
   int64_t bytes = 0;
@@ -297,7 +210,7 @@ int64_t ortho_workspace_bytes(int64_t count, int64_t rows, int64_t cols) {
 
 bool ortho_bounded(int steps, const float* coefficients) { return steps_of(steps, coefficients, nullptr); }
 
-cudaError_t launch_orthogonalize(const OrthoArgs& a, const TcLaunch&, cudaStream_t stream) {
+cudaError_t launch_orthogonalize(const OrthoArgs& a, const TcLaunch& l, cudaStream_t stream) {
   int64_t bytes = 0;
   const OrthoPlan p = plan_of(a.count, a.rows, a.cols, a.workspace, &bytes);
   OrthoStep steps[TIDE_MAX_ORTHOGONALIZE_STEPS] = {};
@@ -306,7 +219,7 @@ cudaError_t launch_orthogonalize(const OrthoArgs& a, const TcLaunch&, cudaStream
   for (int64_t first = 0; first < a.count; first += kOrthoTable) {
     const unsigned some = (unsigned)(a.count - first < kOrthoTable ? a.count - first : kOrthoTable);
     Sources s{};
-    Targets out{};
+    OrthoTargets out{};
     for (unsigned i = 0; i < some; ++i) {
       s.p[i] = a.src[first + i];
       if (!a.steps) out.p[i] = a.dst[first + i];
@@ -318,13 +231,11 @@ cudaError_t launch_orthogonalize(const OrthoArgs& a, const TcLaunch&, cudaStream
                        out, first, a.rows, a.cols, a.ld_src, a.eps, steps[0].x_scale, a.ld_dst);
     if (e != cudaSuccess) return e;
   }
-  for (int i = 0; i < a.steps; ++i) {
-    cudaError_t e = product<kGram>(p, steps[i], i & 1, nullptr, stream);
-    if (e == cudaSuccess) e = product<kSquare>(p, steps[i], i & 1, nullptr, stream);
-    if (e == cudaSuccess)
-      e = i + 1 < a.steps ? product<kUpdate>(p, steps[i], i & 1, nullptr, stream) : product<kLast>(p, steps[i], i & 1, &a, stream);
-    if (e != cudaSuccess) return e;
-  }
+  for (int i = 0; i < a.steps; ++i)
+    for (OrthoForm form : {kGram, kSquare, i + 1 < a.steps ? kUpdate : kLast}) {
+      const cudaError_t e = launch_ortho_product(form, p, steps[i], i & 1, a, l, stream);
+      if (e != cudaSuccess) return e;
+    }
   return cudaSuccess;
 }
 

@@ -41,7 +41,17 @@ struct OrthoStep {
   float x_scale, a_scale, b_scale, next_scale;  // of X, A, B and the next X
 };
 
-// v * scale as two fp16 terms.
+// The caller's matrices of one launch.
+struct OrthoTargets {
+  uint16_t* p[kOrthoTable];
+};
+
+// One product of every matrix (ortho_tc.cu): X by turn, the last step's result
+// to the caller's matrices.
+cudaError_t launch_ortho_product(OrthoForm form, const OrthoPlan& p, const OrthoStep& s, int turn, const OrthoArgs& a,
+                                 const TcLaunch& l, cudaStream_t stream);
+
+// v as two fp16 terms.
 __device__ __forceinline__ void split_half(float v, __half& hi, __half& lo) {
   hi = __float2half_rn(v);
   lo = __float2half_rn(v - __half2float(hi));
