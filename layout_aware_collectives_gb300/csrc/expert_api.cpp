@@ -199,7 +199,7 @@ tide_status_t tide_orthogonalize_workspace(int64_t count, int64_t rows, int64_t 
   const int64_t numel = rows * cols;
   if (count < 0 || (numel != 0 && count > kMaxNumel / numel))
     return invalid("tide_orthogonalize_workspace: count out of range");
-  if (numel != 0) *bytes = ortho_workspace_bytes(count, rows, cols);
+  if (numel != 0 && count != 0) *bytes = ortho_workspace_bytes(count, rows, cols);
   return TIDE_OK;
 }
 TIDE_CATCH

@@ -7,127 +7,181 @@ namespace tide {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPerThread = 16;  // elements of a thread and turn of the norm
-constexpr int kMaxParts = 64;
+constexpr int kWarps = kThreads / 32;
+constexpr int kFlight = 4;       // 16-byte loads of a lane on their way
+constexpr int kMaxParts = 1216;  // eight CTAs an SM
 
 struct Sources {
   const void* p[kOrthoTable];
 };
 
-template <class T>
-__device__ __forceinline__ float element(const T* p);
-template <>
-__device__ __forceinline__ float element(const float* p) {
-  return *p;
-}
-template <>
-__device__ __forceinline__ float element(const uint16_t* p) {
-  return bf16_value(*p);
-}
+__device__ __forceinline__ float element(const float* p) { return *p; }
+__device__ __forceinline__ float element(const uint16_t* p) { return bf16_value(*p); }
 
-// The whole CTA's; every thread gets it.
-template <bool MAX>
-__device__ __forceinline__ float reduce(float v, float* shared) {
+// V neighbours of a row, `left` of which there are; 0 past them.
+template <int V, bool VEC, class T>
+__device__ __forceinline__ void load_some(const T* p, int64_t left, float (&v)[V]) {
+  if constexpr (VEC) {
+    if (left >= V) {
+      const uint4 q = *(const uint4*)p;
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-  for (int d = 16; d; d >>= 1) {
-    const float o = __shfl_xor_sync(0xffffffffu, v, d);
-    v = MAX ? fmaxf(v, o) : v + o;
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(T) == 4)
+          v[i] = __uint_as_float(w[i]);
+        else
+          v[2 * i] = bf16_lo(w[i]), v[2 * i + 1] = bf16_hi(w[i]);
+      }
+      return;
+    }
   }
-  if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = shared[0];
 #pragma unroll
-  for (int w = 1; w < kThreads / 32; ++w) v = MAX ? fmaxf(v, shared[w]) : v + shared[w];
-  __syncthreads();
-  return v;
+  for (int i = 0; i < V; ++i) v[i] = i < left ? element(p + i) : 0.0f;
 }
 
-// A part of a matrix's sum of squares.  Each turn's elements are brought near
-// 1 by a power of two first, so neither large nor small ones leave fp32.
-template <class T>
+// A part of a matrix's sum of squares: a warp takes every so-manieth row.
+// Elements whose squares might leave fp32 are brought near 1 by a power of
+// two first; what they sum to is kept in 64 bits.  VEC: rows start on 16 bytes.
+template <class T, bool VEC>
 __global__ void __launch_bounds__(kThreads) norm_kernel(OrthoPlan p, Sources s, int64_t first, int64_t rows, int64_t cols,
                                                         int64_t ld) {
   after_previous();
-  __shared__ float shared[kThreads / 32];
-  const T* src = (const T*)s.p[blockIdx.y];
-  const int64_t numel = rows * cols, turn = (int64_t)kThreads * kPerThread;
+  constexpr int V = VEC ? 16 / sizeof(T) : 1;
+  __shared__ double shared[kWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   double sum = 0.0;
-  for (int64_t at = blockIdx.x * turn; at < numel; at += p.parts * turn) {
-    float v[kPerThread], top = 0.0f;
-    bool odd = false;
+  for (int64_t r = (int64_t)blockIdx.x * kWarps + warp; r < rows; r += (int64_t)p.parts * kWarps) {
+    const T* row = (const T*)s.p[blockIdx.y] + r * ld;
+    for (int64_t c = 0; c < cols; c += 32 * V * kFlight) {
+      float v[kFlight][V];
+      uint32_t top = 0;  // of the magnitudes' bits: infinity and NaN above all
 #pragma unroll
-    for (int i = 0; i < kPerThread; ++i) {
-      const int64_t q = at + i * kThreads + threadIdx.x, r = q / cols;
-      v[i] = q < numel ? element(src + r * ld + (q - r * cols)) : 0.0f;
-      top = fmaxf(top, fabsf(v[i]));
-      odd |= v[i] != v[i];
+      for (int q = 0; q < kFlight; ++q) {
+        const int64_t at = c + (q * 32 + lane) * V;
+        load_some<V, VEC>(row + at, cols - at, v[q]);
+#pragma unroll
+        for (int i = 0; i < V; ++i) top = max(top, __float_as_uint(v[q][i]) & 0x7fffffffu);
+      }
+      top = __reduce_max_sync(0xffffffffu, top);
+      const int e = (int)(top >> 23) - 127;
+      const int k = e >= -40 && e <= 40 || top >= 0x7f800000u ? 0 : min(max(-e, -126), 126);
+      const float by = __uint_as_float((uint32_t)(127 + k) << 23);
+      float part = 0.0f;
+#pragma unroll
+      for (int q = 0; q < kFlight; ++q)
+#pragma unroll
+        for (int i = 0; i < V; ++i) part = fmaf(v[q][i] * by, v[q][i] * by, part);
+      sum += k ? ldexp((double)part, -2 * k) : (double)part;
     }
-    if (odd) top = CUDART_INF_F;
-    top = reduce<true>(top, shared);
-    if (top == 0.0f) continue;
-    // 2^k, within the normal numbers
-    const int k = top == CUDART_INF_F ? 0 : min(max(127 - (int)(__float_as_uint(top) >> 23), -126), 126);
-    const float by = __uint_as_float((uint32_t)(127 + k) << 23);
-    float part = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kPerThread; ++i) part = fmaf(v[i] * by, v[i] * by, part);
-    part = reduce<false>(part, shared);
-    sum += ldexp((double)part, -2 * k);
   }
-  if (threadIdx.x == 0) p.norms[(first + blockIdx.y) * p.parts + blockIdx.x] = sum;
+#pragma unroll
+  for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  if (lane == 0) shared[warp] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < kWarps; ++w) sum += shared[w];
+    p.norms[(first + blockIdx.y) * p.parts + blockIdx.x] = sum;
+  }
 }
 
-// 1 / (norm + eps) as f 2^(i + j), f in [1, 2): each factor is one that fp32
-// holds, whatever the norm.
+// 1 / (norm + eps) as f 2^(i + j): each factor is one that fp32 holds,
+// whatever the norm.
 struct Inverse {
   float f, i, j;
 };
-__device__ Inverse inverse_norm(const OrthoPlan& p, int64_t z, float eps) {
-  double sum = 0.0;
-  for (int q = 0; q < p.parts; ++q) sum += p.norms[z * p.parts + q];
-  const double v = 1.0 / (sqrt(sum) + (double)eps);
-  int e = 0;
-  if (v == 0.0 || !(v < CUDART_INF)) return Inverse{(float)v, 1.0f, 1.0f};  // of infinity, 0 or NaN
-  const double f = frexp(v, &e) * 2.0;
-  e = min(max(e - 1, -240), 240);
-  const int i = e / 2, j = e - i;
-  return Inverse{(float)f, __uint_as_float((uint32_t)(127 + i) << 23), __uint_as_float((uint32_t)(127 + j) << 23)};
+// 2^e, from the smallest normal number to the largest power.
+__device__ __forceinline__ float power_of(int e) { return __uint_as_float((uint32_t)(127 + min(max(e, -126), 127)) << 23); }
+// The sum is q 4^h, q in [1, 4): its root is taken in 32 bits, as 64-bit
+// arithmetic would take longer than the kernel's loads.
+__device__ __forceinline__ Inverse inverse_of(double sum, float eps) {
+  if (!(sum < CUDART_INF)) return Inverse{sum == CUDART_INF ? 0.0f : CUDART_NAN_F, 1.0f, 1.0f};
+  const uint64_t b = (uint64_t)__double_as_longlong(sum);
+  const int e = (int)(b >> 52) - 1023, h = e >> 1;
+  float root = 0.0f;
+  if (sum > 0.0) root = sqrtf(__double2float_rn(__longlong_as_double((int64_t)((b & 0xfffffffffffffull) | (uint64_t)(1023 + (e & 1)) << 52))));
+  const int g = eps > 0.0f ? (int)(__float_as_uint(eps) >> 23) - 127 : -400;
+  const int top = sum > 0.0 ? max(h, g) : g;
+  // both over 2^top; where they are far apart the smaller one does not count
+  const float norm = root * power_of(h - top) + (eps > 0.0f ? eps * power_of(-top) : 0.0f);
+  const int i = -top / 2, j = -top - i;
+  return Inverse{1.0f / norm, power_of(i), power_of(j)};
+}
+// One warp's; the parts in a fixed order.
+__device__ __forceinline__ Inverse inverse_norm(const OrthoPlan& p, int64_t z, float eps) {
+  __shared__ Inverse shared;
+  if (threadIdx.x < 32) {
+    double sum = 0.0;
+    for (int q = threadIdx.x; q < p.parts; q += 32) sum += p.norms[z * p.parts + q];
+    const int parts = min(p.parts, 32);
+    for (int d = 1; d < parts; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    if (threadIdx.x == 0) shared = inverse_of(sum, eps);
+  }
+  __syncthreads();
+  return shared;
 }
 
-// The first X, 64 x 64 elements a CTA, turned where the matrix is tall.  With
-// no steps to come it goes to the caller instead.
+// The first X, 64 x 64 elements a CTA, turned where the matrix is tall, 8
+// neighbours of a row of X a thread.
 constexpr int kTile = 64;
-template <class T>
-__global__ void __launch_bounds__(kThreads) first_kernel(OrthoPlan p, Sources s, OrthoTargets out, int64_t first, int64_t rows,
-                                                         int64_t cols, int64_t ld, float eps, float scale, int64_t ld_out) {
+template <class T, bool VEC>
+__global__ void __launch_bounds__(kThreads) first_kernel(OrthoPlan p, Sources s, int64_t first, int64_t rows, int64_t cols,
+                                                         int64_t ld, int wide, float eps, float scale) {
   after_previous();
+  constexpr int V = VEC ? 16 / sizeof(T) : 1;
+  constexpr int kAcross = kTile / V, kPass = kThreads / kAcross, kPasses = kTile / kPass;
   __shared__ float tile[kTile][kTile + 1];
   const int64_t z = first + blockIdx.y;
-  const int64_t wide = (cols + kTile - 1) / kTile;
-  const int64_t r0 = blockIdx.x / wide * kTile, c0 = blockIdx.x % wide * kTile;
-  const T* src = (const T*)s.p[blockIdx.y];
-  const Inverse inv = inverse_norm(p, z, eps);
-  const int x = threadIdx.x % kTile, y0 = threadIdx.x / kTile;
-  for (int y = y0; y < kTile; y += kThreads / kTile) {
-    float v = 0.0f;
-    if (r0 + y < rows && c0 + x < cols) v = element(src + (r0 + y) * ld + c0 + x) * inv.i * inv.f * inv.j;
-    if (out.p[blockIdx.y]) {
-      if (r0 + y < rows && c0 + x < cols) out.p[blockIdx.y][(r0 + y) * ld_out + c0 + x] = to_bf16(v);
-      continue;
+  const int64_t r0 = (int64_t)(blockIdx.x / wide) * kTile, c0 = (int64_t)(blockIdx.x % wide) * kTile;
+  const int x = threadIdx.x % kAcross * V, y0 = threadIdx.x / kAcross;
+  const T* src = (const T*)s.p[blockIdx.y] + (r0 + y0) * ld + c0 + x;
+  float v[kPasses][V];
+#pragma unroll
+  for (int q = 0; q < kPasses; ++q) {
+    if (r0 + y0 + q * kPass < rows) {
+      load_some<V, VEC>(src + q * kPass * ld, cols - c0 - x, v[q]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[q][i] = 0.0f;
     }
-    if (p.tall)
-      tile[x][y] = v;
-    else
-      tile[y][x] = v;
   }
-  if (out.p[blockIdx.y]) return;
+  const Inverse inv = inverse_norm(p, z, eps);
+#pragma unroll
+  for (int q = 0; q < kPasses; ++q)
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float f = v[q][i] * inv.i * inv.f * inv.j * scale;
+      const int y = y0 + q * kPass;
+      if (p.tall)
+        tile[x + i][y] = f;
+      else
+        tile[y][x + i] = f;
+    }
   __syncthreads();
   const int64_t i0 = p.tall ? c0 : r0, j0 = p.tall ? r0 : c0;
-  for (int y = y0; y < kTile; y += kThreads / kTile) {
-    if (i0 + y >= p.m || j0 + x >= p.n) continue;
-    const int64_t at = (z * p.m + i0 + y) * p.ld_x + j0 + x;
-    split_half(tile[y][x] * scale, p.x[0][0][at], p.x[0][1][at]);
+  const int xo = threadIdx.x % 8 * 8;
+#pragma unroll
+  for (int y = threadIdx.x / 8; y < kTile; y += kThreads / 8) {
+    if (i0 + y >= p.m) continue;
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) split_half2(tile[y][xo + 2 * i], tile[y][xo + 2 * i + 1], hi[i], lo[i]);
+    // rows are whole 64s wide
+    const int64_t at = (z * p.m + i0 + y) * p.ld_x + j0 + xo;
+    *(uint4*)(p.x[0][0] + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *(uint4*)(p.x[0][1] + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
   }
+}
+
+// No steps: the normalised matrix itself.
+template <class T>
+__global__ void __launch_bounds__(kThreads) normalised_kernel(OrthoPlan p, Sources s, OrthoTargets out, int64_t first,
+                                                              int64_t rows, int64_t cols, int64_t ld, int64_t ld_out, float eps) {
+  after_previous();
+  const T* src = (const T*)s.p[blockIdx.y];
+  const Inverse inv = inverse_norm(p, first + blockIdx.y, eps);
+  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
+    for (int64_t c = threadIdx.x; c < cols; c += kThreads)
+      out.p[blockIdx.y][r * ld_out + c] = to_bf16(element(src + r * ld + c) * inv.i * inv.f * inv.j);
 }
 
 // ------------------------------------------------------------ host side
@@ -140,8 +194,9 @@ OrthoPlan plan_of(int64_t count, int64_t rows, int64_t cols, char* base, int64_t
   p.tall = rows > cols;
   p.m = (int)(p.tall ? cols : rows), p.n = (int)(p.tall ? rows : cols);
   p.count = count, p.ld_x = line(p.n), p.ld_a = line(p.m);
-  const int64_t parts = ceil_div(rows * cols, (int64_t)kThreads * kPerThread);
-  p.parts = (int)(parts < kMaxParts ? parts : kMaxParts);
+  // a row a warp, and no more CTAs than the device holds
+  const int64_t room = ceil_div(kMaxParts, count), parts = ceil_div(rows, kWarps);
+  p.parts = (int)(parts < room ? parts : room);
   int64_t at = 0;
   const auto take = [&](int64_t n) {
     char* r = base + at;
@@ -150,20 +205,19 @@ OrthoPlan plan_of(int64_t count, int64_t rows, int64_t cols, char* base, int64_t
   };
   for (auto& turn : p.x)
     for (auto& plane : turn) plane = (__half*)take(count * p.m * p.ld_x * 2);
-  for (auto& plane : p.o) plane = (__half*)take(count * p.m * p.ld_a * 2);
-  p.p = (__half*)take(count * p.m * p.ld_a * 2);
-  p.d = (float*)take(count * p.m * 4), p.e = (float*)take(count * p.m * 4);
+  for (auto& plane : p.t) plane = (__half*)take(count * p.m * p.ld_a * 2);
+  for (auto& diagonal : p.d) diagonal = (float*)take(count * p.m * 4);
   p.norms = (double*)take(count * p.parts * 8);
   *bytes = at;
   return p;
 }
 
-// The largest magnitude of b x + c x x within [0, top].
-double largest_b(double b, double c, double top) {
-  double r = std::fabs(top * (b + c * top));
-  const double x = -b / (2 * c);
-  if (x > 0 && x < top) r = std::fmax(r, std::fabs(x * (b + c * x)));
-  return r;
+// The largest magnitude of a + b x + c x x within [0, top].
+double largest_c(double a, double b, double c, double top) {
+  const auto f = [&](double x) { return std::fabs(a + x * (b + c * x)); };
+  const double x = -b / (2 * c);  // NaN or infinity where there is no such place
+  const double r = std::fmax(f(0), f(top));
+  return x > 0 && x < top ? std::fmax(r, f(x)) : r;
 }
 // And of s (a + b s^2 + c s^4).
 double largest_x(double a, double b, double c, double top) {
@@ -184,20 +238,28 @@ double scale_for(double top) {
   return std::ldexp(1.0, 14 - e);
 }
 
-// Each step's scales, from bounds of its matrices' norms; false where one
-// passes 2^16.
-bool steps_of(int steps, const float* k, OrthoStep* out) {
-  double top = 1.0;
+// Bounds of norms: of each step's X, and of its C.
+struct Bounds {
+  double x[TIDE_MAX_ORTHOGONALIZE_STEPS + 1], c[TIDE_MAX_ORTHOGONALIZE_STEPS];
+};
+// False where one of X passes 2^16.
+bool bounds_of(int steps, const float* k, Bounds* out) {
+  out->x[0] = 1.0;
   for (int i = 0; i < steps; ++i) {
-    const double a = k[3 * i], b = k[3 * i + 1], c = k[3 * i + 2];
-    const double next = largest_x(a, b, c, top);
-    if (!(std::isfinite(a) && std::isfinite(b) && std::isfinite(c) && next <= 0x1p16)) return false;
-    if (out)
-      out[i] = OrthoStep{k[3 * i], k[3 * i + 1], k[3 * i + 2], (float)scale_for(top), (float)scale_for(top * top),
-                         (float)scale_for(largest_b(b, c, top * top)), (float)scale_for(next)};
-    top = next;
+    const double a = k[3 * i], b = k[3 * i + 1], c = k[3 * i + 2], top = out->x[i];
+    out->x[i + 1] = largest_x(a, b, c, top);
+    out->c[i] = largest_c(a, b, c, top * top);
+    if (!(std::isfinite(a) && std::isfinite(b) && std::isfinite(c) && out->x[i + 1] <= 0x1p16)) return false;
   }
   return true;
+}
+
+// Whether step i and the next share a pass over X: 5 products of m^3 / 2
+// operations and 3 of m m n / 2 instead of 2 and 6.  An error of A grows by up
+// to a^2 on its way to the second step's, which a moderate a only allows.
+bool paired(const OrthoPlan& p, const OrthoArgs& a, int i) {
+  const float k = a.coefficients[3 * i];
+  return i + 1 < a.steps && 2 * (int64_t)p.n >= 3 * (int64_t)p.m && k * k <= 16.0f;
 }
 
 }  // namespace
@@ -208,34 +270,75 @@ int64_t ortho_workspace_bytes(int64_t count, int64_t rows, int64_t cols) {
   return bytes;
 }
 
-bool ortho_bounded(int steps, const float* coefficients) { return steps_of(steps, coefficients, nullptr); }
+bool ortho_bounded(int steps, const float* coefficients) {
+  Bounds b;
+  return bounds_of(steps, coefficients, &b);
+}
 
 cudaError_t launch_orthogonalize(const OrthoArgs& a, const TcLaunch& l, cudaStream_t stream) {
   int64_t bytes = 0;
   const OrthoPlan p = plan_of(a.count, a.rows, a.cols, a.workspace, &bytes);
-  OrthoStep steps[TIDE_MAX_ORTHOGONALIZE_STEPS] = {};
-  if (!steps_of(a.steps, a.coefficients, steps)) return cudaErrorInvalidValue;
-  const unsigned tiles = (unsigned)(ceil_div(a.rows, kTile) * ceil_div(a.cols, kTile));
+  Bounds bound;
+  if (!bounds_of(a.steps, a.coefficients, &bound)) return cudaErrorInvalidValue;
+  const int64_t wide = ceil_div(a.cols, kTile), tiles = ceil_div(a.rows, kTile) * wide;
   for (int64_t first = 0; first < a.count; first += kOrthoTable) {
     const unsigned some = (unsigned)(a.count - first < kOrthoTable ? a.count - first : kOrthoTable);
     Sources s{};
     OrthoTargets out{};
+    bool vec = a.ld_src % (a.bf16 ? 8 : 4) == 0;
     for (unsigned i = 0; i < some; ++i) {
       s.p[i] = a.src[first + i];
-      if (!a.steps) out.p[i] = a.dst[first + i];
+      vec = vec && (uintptr_t)s.p[i] % 16 == 0;
+      out.p[i] = a.dst[first + i];
     }
-    cudaError_t e = launch_early(a.bf16 ? norm_kernel<uint16_t> : norm_kernel<float>, dim3(p.parts, some), kThreads, 0, 0,
-                                 stream, p, s, first, a.rows, a.cols, a.ld_src);
-    if (e == cudaSuccess)
-      e = launch_early(a.bf16 ? first_kernel<uint16_t> : first_kernel<float>, dim3(tiles, some), kThreads, 0, 0, stream, p, s,
-                       out, first, a.rows, a.cols, a.ld_src, a.eps, steps[0].x_scale, a.ld_dst);
+    cudaError_t e = launch_early(a.bf16 ? vec ? norm_kernel<uint16_t, true> : norm_kernel<uint16_t, false>
+                                 : vec  ? norm_kernel<float, true>
+                                        : norm_kernel<float, false>,
+                                 dim3(p.parts, some), kThreads, 0, 0, stream, p, s, first, a.rows, a.cols, a.ld_src);
+    if (e == cudaSuccess && a.steps)
+      e = launch_early(a.bf16 ? vec ? first_kernel<uint16_t, true> : first_kernel<uint16_t, false>
+                       : vec  ? first_kernel<float, true>
+                              : first_kernel<float, false>,
+                       dim3((unsigned)tiles, some), kThreads, 0, 0, stream, p, s, first, a.rows, a.cols, a.ld_src, (int)wide,
+                       a.eps, (float)scale_for(1.0));
+    else if (e == cudaSuccess)
+      e = launch_early(a.bf16 ? normalised_kernel<uint16_t> : normalised_kernel<float>,
+                       dim3((unsigned)(a.rows < 4096 ? a.rows : 4096), some), kThreads, 0, 0, stream, p, s, out, first, a.rows,
+                       a.cols, a.ld_src, a.ld_dst, a.eps);
     if (e != cudaSuccess) return e;
   }
-  for (int i = 0; i < a.steps; ++i)
-    for (OrthoForm form : {kGram, kSquare, i + 1 < a.steps ? kUpdate : kLast}) {
-      const cudaError_t e = launch_ortho_product(form, p, steps[i], i & 1, a, l, stream);
-      if (e != cudaSuccess) return e;
+  int turn = 0;
+  for (int i = 0; i < a.steps; turn ^= 1) {
+    const bool two = paired(p, a, i);
+    const float x = (float)scale_for(bound.x[i]);
+    float t[3] = {};  // scales of what lies in the symmetric places
+    cudaError_t e = cudaSuccess;
+    const auto sym = [&](int left, int right, int out, double top, float s2, float s1, float s0) {
+      if (e != cudaSuccess) return;
+      const float scale = (float)scale_for(top);
+      e = launch_ortho_product(p, OrthoProduct{kSym, turn, left, right, out, s2, s1, s0, t[left], t[right], scale}, a, l, stream);
+      t[out] = scale;
+    };
+    const auto square = [&](int from, int out, int step) {
+      const float* k = a.coefficients + 3 * step;
+      sym(from, from, out, bound.c[step], k[2], k[1], k[0]);
+    };
+    t[0] = (float)scale_for(bound.x[i] * bound.x[i]);
+    e = launch_ortho_product(p, OrthoProduct{kGram, turn, 0, 0, 0, 1, 0, 0, x, x, t[0]}, a, l, stream);
+    square(0, 1, i);  // C
+    if (two) {
+      sym(1, 0, 2, bound.c[i] * bound.x[i] * bound.x[i], 1, 0, 0);      // C A
+      sym(2, 1, 0, bound.x[i + 1] * bound.x[i + 1], 1, 0, 0);           // C A C: the next A
+      square(0, 2, i + 1);                                              // C'
+      sym(2, 1, 0, bound.c[i] * bound.c[i + 1], 1, 0, 0);               // C' C
     }
+    if (e != cudaSuccess) return e;
+    i += two ? 2 : 1;
+    const int by = two ? 0 : 1;
+    e = launch_ortho_product(
+        p, OrthoProduct{i < a.steps ? kUpdate : kLast, turn, by, 0, 0, 1, 0, 0, t[by], x, (float)scale_for(bound.x[i])}, a, l, stream);
+    if (e != cudaSuccess) return e;
+  }
   return cudaSuccess;
 }
 

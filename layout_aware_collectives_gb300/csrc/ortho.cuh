@@ -1,15 +1,18 @@
 // Newton-Schulz orthogonalisation: what its kernels share.
 //
 // One step takes X [m, n], m <= n (the matrix, or its transpose where it has
-// more rows), to a X + B X, B = b A + c A A, A = X X^T.  X and A are kept as
-// two fp16 terms (hi + lo: 22 bits) of power-of-two scales; the products take
-// hi alone.  What its rounding leaves would be 0.002-0.003 of the result, as
-// much as the result's own rounding to bf16 or twice that, were it not for
-// the diagonals: near the end A is close to the identity and its diagonal,
-// and B's, carry most of a product.  So they are kept apart in fp32:
-//   A A = O O + D O + O D + D D   with A = O + D, O's diagonal 0,
-//   B X = P X + E X               with B = P + E, likewise,
-// and the products see O and P only.  That leaves 0.0002-0.0007.
+// more rows), to C X, C = a + b A + c A A, A = X X^T.  Two steps may share one
+// pass over X: the second's A is C A C, and X becomes C' C X.
+//
+// X is kept as two fp16 terms (hi + lo: 22 bits) of a power-of-two scale, the
+// symmetric matrices as one, all but their diagonals, which are kept in fp32
+// beside them.  The products take hi alone.  What its rounding leaves would be
+// 0.002-0.003 of the result, as much as the result's own rounding to bf16 or
+// twice that, were it not for the diagonals: near the end A is close to the
+// identity, and the diagonals carry most of a product.  With L = D + P, P's
+// diagonal 0,
+//   L L' = P P' + D P' + P D' + D D',   L X = P X + D X,
+// and the tensor cores see the first terms only.  That leaves 0.0002-0.0011.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -18,27 +21,30 @@
 
 namespace tide {
 
-enum OrthoForm { kGram = 0, kSquare = 1, kUpdate = 2, kLast = 3 };
+enum OrthoForm { kGram = 0, kSym = 1, kUpdate = 2, kLast = 3 };
 
 constexpr int kOrthoTable = 128;  // matrices of a launch that goes by the caller's pointers
 
-// The workspace's parts, and a step's scales: a plane holds values times its
-// scale.
+// The workspace's parts.
 struct OrthoPlan {
   int m, n;
   int64_t count, ld_x, ld_a;  // row strides: whole 128-byte lines
   bool tall;
-  __half *x[2][2];  // of two turns: hi, lo [count, m, ld_x]
-  __half *o[2];     // A without its diagonal: hi, lo [count, m, ld_a]
-  __half *p;        // B without its diagonal: hi [count, m, ld_a]
-  float *d, *e;     // their diagonals [count, m]
-  double *norms;    // parts of the sums of squares [count, parts]
+  __half* x[2][2];  // of two turns: hi, lo [count, m, ld_x]
+  __half* t[3];     // symmetric matrices without their diagonals [count, m, ld_a]
+  float* d[3];      // the diagonals [count, m]
+  double* norms;    // parts of the sums of squares [count, parts]
   int parts;
 };
 
-struct OrthoStep {
-  float a, b, c;
-  float x_scale, a_scale, b_scale, next_scale;  // of X, A, B and the next X
+// One product of every matrix.  A plane holds values times its scale.
+struct OrthoProduct {
+  OrthoForm form;
+  int turn;            // which X is read
+  int left, right;     // kSym: t's; kUpdate, kLast: left times X
+  int out;             // kGram, kSym: a t
+  float s2, s1, s0;    // kSym: s2 (left right) + s1 left + s0
+  float left_scale, right_scale, out_scale;
 };
 
 // The caller's matrices of one launch.
@@ -46,15 +52,25 @@ struct OrthoTargets {
   uint16_t* p[kOrthoTable];
 };
 
-// One product of every matrix (ortho_tc.cu): X by turn, the last step's result
-// to the caller's matrices.
-cudaError_t launch_ortho_product(OrthoForm form, const OrthoPlan& p, const OrthoStep& s, int turn, const OrthoArgs& a,
-                                 const TcLaunch& l, cudaStream_t stream);
+// One product of every matrix (ortho_tc.cu); the last form's results go to
+// the caller's matrices.
+cudaError_t launch_ortho_product(const OrthoPlan& p, const OrthoProduct& q, const OrthoArgs& a, const TcLaunch& l,
+                                 cudaStream_t stream);
 
-// v as two fp16 terms.
-__device__ __forceinline__ void split_half(float v, __half& hi, __half& lo) {
-  hi = __float2half_rn(v);
-  lo = __float2half_rn(v - __half2float(hi));
+__device__ __forceinline__ float2 unpack_half(uint32_t v) { return __half22float2(*(const __half2*)&v); }
+
+// Two floats as packed fp16, to nearest even: `a` in the low half.
+__device__ __forceinline__ uint32_t pack_half(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *(const uint32_t*)&h;
+}
+
+// Two floats as two fp16 terms each, to nearest even: `a` in the low halves.
+__device__ __forceinline__ void split_half2(float a, float b, uint32_t& hi, uint32_t& lo) {
+  const __half2 h = __floats2half2_rn(a, b);
+  const float2 f = __half22float2(h);
+  const __half2 l = __floats2half2_rn(a - f.x, b - f.y);
+  hi = *(const uint32_t*)&h, lo = *(const uint32_t*)&l;
 }
 
 }  // namespace tide

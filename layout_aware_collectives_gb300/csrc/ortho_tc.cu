@@ -1,18 +1,23 @@
 // The products of Newton-Schulz orthogonalisation on the tensor cores, one
 // persistent kernel in four forms:
-//   gram    A = X X^T, kept as O and its diagonal
-//   square  B = b A + c A A from O O, kept as P and its diagonal
-//   update  the next X = (a + E) X + P X
+//   gram    A = X X^T
+//   sym     s2 L R + s1 L + s0 of two symmetric matrices that commute
+//   update  the next X = L X
 //   last    the same to the caller's matrices, in bf16
-// A and B are symmetric: only tiles on and above the diagonal are summed, and
-// written to both places.
+// What gram and sym make is symmetric: only tiles on and above the diagonal
+// are summed, and written to both places.
 //
 // As in the gated block, a pair of CTAs works on one 256 x 256 tile: each
 // loads 128 rows of the left operand and half of the right one's columns, one
-// MMA instruction of the pair reads both halves.  Warps 0 and 3 load (6 stages
+// MMA instruction of the pair reads both halves.  Warps 0 and 3 load (5 stages
 // of 32 KiB), warp 1 of the pair's first CTA issues the MMAs, warps from 4 on
 // read finished sums out of TMEM, which holds two accumulators so that they do
 // so while the next tile is summed.
+//
+// What those warps add to the sums (32 x 32 elements of two planes at a time)
+// is copied to shared memory while the elements before are at work, and what
+// they make of it goes out by way of the same place.  TMA does neither: each of
+// its copies here would stand behind the operands' large ones.
 #include "ortho.cuh"
 #include "tc_device.cuh"
 #include "tc_host.h"
@@ -22,30 +27,32 @@ namespace {
 
 using namespace tc;
 
-constexpr int kStages = 6;
+constexpr int kStages = 5;
 constexpr int kStep = 64;
 constexpr int kHalf = 128;
 constexpr uint32_t kOperand = kHalf * kStep * 2;
 constexpr uint32_t kStage = 2 * kOperand;
-constexpr int kAllBoxes = 16;
-constexpr size_t kSmem = 1024 + kStages * kStage + kAllBoxes * kBox;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpiWarps;
-constexpr int kBoxes = kAllBoxes / kEpiWarps;
+constexpr uint32_t kSlot = 2 * kBox;  // boxes of two planes
+constexpr int kSlots = 2;             // of a warp
+constexpr size_t kSmem = 1024 + kStages * kStage + kEpiWarps * kSlots * kSlot;
 
 struct Params {
   CUtensorMap left, right;  // operands
-  CUtensorMap out[2];       // gram: O, update: the next X, hi and lo; square: P
+  const __half* in[2];      // planes that are added: sym: left, right; update, last: X, hi and lo
+  __half* out[2];           // gram, sym: the one; update: the next X, hi and lo
+  int64_t ld;               // of those
   int m, wide, steps;       // rows and columns of the result, stages of a tile's sum
+  int planes;               // of `in`
   TileGrid grid;            // update, last
-  Divisor each;             // gram, square: tiles of a matrix
+  Divisor each;             // gram, sym: tiles of a matrix
   int tiles;
   int64_t first;            // matrix, of this launch
-  const __half *hi, *lo;    // square: O, update: X
-  int64_t ld;               // of those
-  float *d, *e;             // diagonals of A and B
-  float a, b, c;
-  float sum_scale, in_scale, out_scale;  // factors of the sums, of hi and lo, of what is kept
+  const float *left_d, *right_d;  // diagonals
+  float* out_d;
+  float s2, s1, s0;
+  float sum_scale, left_scale, right_scale, out_scale;  // factors of the sums, of `in`, of what is kept
   bool tall;
   int64_t ld_out;
   int* err;
@@ -71,157 +78,221 @@ __device__ __forceinline__ bool work_at(const Params& p, int pair, int pairs, in
   return true;
 }
 
-// Two floats to packed fp16, to nearest even: `lo` in the low half.
-__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *(const uint32_t*)&h;
+// A warp's 32 x 32 elements of one plane in shared memory, 64-byte swizzle: 16-byte
+// piece c of row r lies at piece c ^ (r / 2 % 4).
+__device__ __forceinline__ uint32_t piece_at(uint32_t box, uint32_t row, uint32_t piece) {
+  return box + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
 }
-__device__ __forceinline__ float2 unpack_half(uint32_t v) { return __half22float2(*(const __half2*)&v); }
-
-// Results on their way out: 32 x 32 boxes of one warp, as they are or turned.
-struct Boxes : Outbox<kBoxes> {
-  // 64-byte swizzle, as in fill(): row c of the box is column c of the sums
-  __device__ __forceinline__ uint32_t fill_turned(const uint32_t (&p)[16]) {
-    const uint32_t box = base + (uint32_t)(next % kBoxes) * kBox;
-    ++next;
-    const uint32_t piece = lane >> 3, at = box + (lane & 7) * 2;
+// 16 rows of a box, from row r0 on, as the tensor cores' fragments have them:
+// register 2 g + h of a lane holds columns 8 g + 2 (lane % 4) and the next one
+// of row r0 + 8 h + lane / 4.
+__device__ __forceinline__ void get_rows(uint32_t box, uint32_t r0, uint32_t lane, uint32_t (&v)[8]) {
 #pragma unroll
-    for (uint32_t c = 0; c < 32; ++c)
-      asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + c * 64 + ((piece ^ ((c >> 1) & 3)) << 4)),
-                   "h"((uint16_t)(p[c / 2] >> (16 * (c & 1))))
-                   : "memory");
-    return box;
+  for (uint32_t g = 0; g < 4; g += 2)
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v[2 * g]), "=r"(v[2 * g + 1]), "=r"(v[2 * g + 2]), "=r"(v[2 * g + 3])
+                 : "r"(piece_at(box, r0 + (lane & 15), g + (lane >> 4)))
+                 : "memory");
+}
+__device__ __forceinline__ void put_rows(uint32_t box, uint32_t r0, uint32_t lane, const uint32_t (&v)[8]) {
+#pragma unroll
+  for (uint32_t g = 0; g < 4; g += 2)
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
+                     piece_at(box, r0 + (lane & 15), g + (lane >> 4))),
+                 "r"(v[2 * g]), "r"(v[2 * g + 1]), "r"(v[2 * g + 2]), "r"(v[2 * g + 3])
+                 : "memory");
+}
+// Turned: row c of the box is column c.
+__device__ __forceinline__ void put_turned(uint32_t box, uint32_t r0, uint32_t lane, const uint32_t (&v)[8]) {
+#pragma unroll
+  for (uint32_t g = 0; g < 4; g += 2)
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
+                     piece_at(box, (g + (lane >> 4)) * 8 + (lane & 7), r0 / 8 + ((lane >> 3) & 1))),
+                 "r"(v[2 * g]), "r"(v[2 * g + 1]), "r"(v[2 * g + 2]), "r"(v[2 * g + 3])
+                 : "memory");
+}
+// 32 columns of 16 TMEM lanes, likewise: sums 4 g + 2 h and the next one.  They
+// may be used after tmem_arrived.
+__device__ __forceinline__ void tmem_rows(uint32_t addr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : TIDE_R8(v, 0), TIDE_R8(v, 8)
+      : "r"(addr)
+      : "memory");
+}
+
+// Eight rows of four pieces at a time: a lane's piece, in shared memory and out
+// of it.  Planes' rows are whole 64s wide, so a box has all its columns.
+__device__ __forceinline__ void ask_box(uint32_t box, const __half* from, int64_t ld, int rows, int lane) {
+#pragma unroll
+  for (int r0 = 0; r0 < 32; r0 += 8) {
+    const int r = r0 + (lane >> 2);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(piece_at(box, r, lane & 3)),
+                 "l"(from + (r < rows ? r : 0) * ld + (lane & 3) * 8), "r"(r < rows ? 16 : 0)
+                 : "memory");
   }
-  template <bool TURNED>
-  __device__ __forceinline__ void put(const CUtensorMap* m0, const uint32_t (&p0)[16], const CUtensorMap* m1,
-                                      const uint32_t (&p1)[16], int col, int row, int z) {
-    if (lane == 0) stores_read<kBoxes - 2>();
-    __syncwarp();
-    const uint32_t b0 = TURNED ? fill_turned(p0) : fill(p0);
-    uint32_t b1 = 0;
-    if (m1) b1 = TURNED ? fill_turned(p1) : fill(p1);
-    async_fence();
-    __syncwarp();
-    if (lane == 0) {
-      store_box3(m0, TURNED ? row : col, TURNED ? col : row, z, b0);
-      if (m1) store_box3(m1, TURNED ? row : col, TURNED ? col : row, z, b1);
+}
+__device__ __forceinline__ void asked() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void arrived() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+  __syncwarp();
+}
+template <class T>
+__device__ __forceinline__ void send_box(uint32_t box, T* to, int64_t ld, int rows, int lane) {
+#pragma unroll
+  for (int r0 = 0; r0 < 32; r0 += 8) {
+    const int r = r0 + (lane >> 2);
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(piece_at(box, r, lane & 3))
+                 : "memory");
+    if (r < rows) *(uint4*)(to + r * ld + (lane & 3) * 8) = v;
+  }
+}
+
+// A warp's way through its 32 x 32 pieces of the pair's tiles.
+template <int FORM>
+struct Cursor {
+  int i;      // tile
+  TileAt at;
+  int row0, col, left;  // of the piece; pieces left in this tile, it among them
+  bool more;
+
+  // The i-th tile, or the next that has a piece for this warp.
+  __device__ __forceinline__ void open(const Params& p, int pair, int pairs, int first, int half, uint32_t rank, int lanes) {
+    for (i = first;; ++i) {
+      more = work_at<FORM>(p, pair, pairs, i, at);
+      if (!more) return;
+      row0 = (at.m * 2 + (int)rank) * kHalf + lanes;
+      col = at.n * 2 * kHalf + half * kHalf;
+      left = row0 >= p.m || col >= p.wide ? 0 : min(4, (p.wide - col + 31) / 32);
+      if (left) return;
     }
   }
 };
 
-// hi and lo of 32 neighbours.
-__device__ __forceinline__ void load_terms(const Params& p, int64_t at, bool in, uint32_t (&hi)[16], uint32_t (&lo)[16]) {
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    const uint4 h = in ? *(const uint4*)(p.hi + at + 8 * q) : zero, l = in ? *(const uint4*)(p.lo + at + 8 * q) : zero;
-    hi[4 * q] = h.x, hi[4 * q + 1] = h.y, hi[4 * q + 2] = h.z, hi[4 * q + 3] = h.w;
-    lo[4 * q] = l.x, lo[4 * q + 1] = l.y, lo[4 * q + 2] = l.z, lo[4 * q + 3] = l.w;
-  }
-}
-__device__ __forceinline__ float2 both_terms(uint32_t hi, uint32_t lo, float scale) {
-  const float2 h = unpack_half(hi), l = unpack_half(lo);
-  return make_float2((h.x + l.x) * scale, (h.y + l.y) * scale);
-}
-
-// 32 columns of the last result's row: one lane a row.
-__device__ __forceinline__ void put_last(const Params& p, uint16_t* dst, const float (&y)[32], int row0, int col, Boxes& out) {
-  const int lane = out.lane, row = row0 + lane;
-  if (p.tall) {  // a column's rows lie together, and so do the lanes
-    if (row >= p.m) return;
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (col + i < p.wide) dst[(int64_t)(col + i) * p.ld_out + row] = to_bf16(y[i]);
+// 32 x 32 results to the caller: `rows` and `cols` of which there are.
+__device__ __forceinline__ void send_last(uint32_t box, uint16_t* to, int64_t ld, int rows, int cols, int lane) {
+  if (((uintptr_t)to & 15) == 0 && ld % 8 == 0 && cols >= 32) {
+    send_box(box, to, ld, rows, lane);
     return;
   }
-  uint32_t o[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) o[i] = pack_bf16(y[2 * i], y[2 * i + 1]);
-  if (((uintptr_t)dst & 15) == 0 && p.ld_out % 8 == 0 && col + 32 <= p.wide) {
-    if (row >= p.m) return;
-    uint4* to = (uint4*)(dst + (int64_t)row * p.ld_out + col);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) to[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
-    return;
-  }
-  // rows that do not start on 16 bytes: a row at a time, an element a lane
-  __syncwarp();
-  const uint32_t box = out.fill(o);
-  __syncwarp();
-  for (int r = 0; r < 32 && row0 + r < p.m; ++r) {
+  for (int r = 0; r < 32 && r < rows; ++r) {
     uint16_t v;
-    asm volatile("ld.shared.u16 %0, [%1];"
-                 : "=h"(v)
-                 : "r"(box + r * 64 + ((((uint32_t)lane >> 3) ^ ((r >> 1) & 3)) << 4) + (lane & 7) * 2));
-    if (col + lane < p.wide) dst[(int64_t)(row0 + r) * p.ld_out + col + lane] = v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(piece_at(box, r, lane >> 3) + (lane & 7) * 2) : "memory");
+    if (lane < cols) to[r * ld + lane] = v;
   }
 }
 
-// A warp's 32 rows and 128 columns of a tile.
+// Diagonals' elements of a piece: left's of row row0 + lane, right's of column
+// col + lane.
+struct Diagonals {
+  float di, dj;
+};
+
+// What becomes of 32 x 32 sums.
 template <int FORM>
-__device__ __forceinline__ void epilogue(const Params& p, const OrthoTargets& targets, const TileAt& t, uint32_t tmem, int row0,
-                                         int half, Boxes& out) {
-  const int lane = out.lane, row = row0 + lane;
-  const bool mine = row < p.m;
-  if (row0 >= p.m) return;
-  const int64_t at = (int64_t)t.z * p.m + row;
-  float di = 0.0f;  // square: A's diagonal here, update: a + B's
-  if (FORM == kSquare && mine) di = p.d[at];
-  if (FORM >= kUpdate && mine) di = p.a + p.e[at];
-#pragma unroll 1
-  for (int c = half * 4; c < half * 4 + 4; ++c) {
-    const int col = t.n * 2 * kHalf + c * 32;
-    if (col >= p.wide) break;
-    uint32_t hi[16], lo[16], v[32];
-    if constexpr (FORM != kGram) load_terms(p, at * p.ld + col, mine, hi, lo);
-    float dj = 0.0f;
-    if (FORM == kSquare && col + lane < p.wide) dj = p.d[(int64_t)t.z * p.m + col + lane];
-    tmem_read(tmem + c * 32, v);
-    float y[32];
-#pragma unroll
-    for (int i = 0; i < 32; ++i) y[i] = as_f(v[i]) * p.sum_scale;
-    if constexpr (FORM == kSquare) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float2 o = both_terms(hi[i], lo[i], p.in_scale);
-        const float d0 = __shfl_sync(0xffffffffu, dj, 2 * i), d1 = __shfl_sync(0xffffffffu, dj, 2 * i + 1);
-        // A A = O O + D O + O D + D D
-        y[2 * i] = fmaf(p.c, fmaf(di + d0, o.x, y[2 * i]), p.b * o.x);
-        y[2 * i + 1] = fmaf(p.c, fmaf(di + d1, o.y, y[2 * i + 1]), p.b * o.y);
-      }
-    }
-    if constexpr (FORM == kGram || FORM == kSquare) {
-      if (t.m == t.n && (row0 >> 5) == (col >> 5)) {  // the diagonal's box
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (i == lane) {
-            if (mine) (FORM == kGram ? p.d : p.e)[at] = FORM == kGram ? y[i] : y[i] + di * fmaf(p.c, di, p.b);
-            y[i] = 0.0f;
-          }
-      }
+__device__ __forceinline__ void finish(const Params& p, const OrthoTargets& targets, const TileAt& t, int row0, int col,
+                                       int lane, uint32_t tmem, uint32_t slot, Diagonals d) {
+  const int64_t z = (int64_t)t.z * p.m;
+  uint32_t sums[2][16], a[2][8], b[2][8];
+  tmem_rows(tmem, sums[0]);
+  tmem_rows(tmem + (16u << 16), sums[1]);
+  if constexpr (FORM != kGram) {
+    get_rows(slot, 0, lane, a[0]);
+    get_rows(slot, 16, lane, a[1]);
+    if (FORM != kSym || p.planes == 2) {
+      get_rows(slot + kBox, 0, lane, b[0]);
+      get_rows(slot + kBox, 16, lane, b[1]);
     } else {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float2 x = both_terms(hi[i], lo[i], p.in_scale);
-        y[2 * i] = fmaf(di, x.x, y[2 * i]);
-        y[2 * i + 1] = fmaf(di, x.y, y[2 * i + 1]);
-      }
-    }
-    if constexpr (FORM == kLast) {
-      put_last(p, targets.p[t.z - p.first], y, row0, col, out);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float y0 = y[2 * i] * p.out_scale, y1 = y[2 * i + 1] * p.out_scale;
-        hi[i] = pack_half(y0, y1);
-        const float2 h = unpack_half(hi[i]);
-        lo[i] = pack_half(y0 - h.x, y1 - h.y);
-      }
-      const CUtensorMap* second = FORM == kSquare ? nullptr : &p.out[1];
-      out.put<false>(&p.out[0], hi, second, lo, col, row0, t.z);
-      if (FORM != kUpdate && t.m != t.n) out.put<true>(&p.out[0], hi, second, lo, col, row0, t.z);
+      for (int i = 0; i < 8; ++i) b[0][i] = a[0][i], b[1][i] = a[1][i];
     }
   }
+  // What is kept is scale * (s2 (sum + di right + left dj) + s1 left), or
+  // scale * (sum + di (hi + lo)): each factor with its scales taken together.
+  const float k0 = p.sum_scale * p.out_scale * (FORM == kSym ? p.s2 : 1.0f);
+  float by_row = 0.0f, by_col[8];  // of this lane's row; of the fragments' columns
+  if constexpr (FORM == kSym) {
+    by_row = d.di * p.s2 * p.right_scale * p.out_scale;
+    const float mine = fmaf(d.dj, p.s2, p.s1) * p.left_scale * p.out_scale;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) by_col[i] = __shfl_sync(0xffffffffu, mine, (i >> 1) * 8 + (lane & 3) * 2 + (i & 1));
+  } else if constexpr (FORM != kGram) {
+    by_row = d.di * p.right_scale * p.out_scale;
+  }
+  const bool diagonal = (FORM == kGram || FORM == kSym) && t.m == t.n && row0 == col;
+  tmem_arrived(sums[0]);
+  tmem_arrived(sums[1]);
+  __syncwarp();  // every lane has its part of the slot
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    uint32_t hi[8], lo[8];
+    const float row_a = __shfl_sync(0xffffffffu, by_row, q * 16 + (lane >> 2));
+    const float row_b = __shfl_sync(0xffffffffu, by_row, q * 16 + 8 + (lane >> 2));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float by = i & 1 ? row_b : row_a;
+      float y0 = as_f(sums[q][2 * i]) * k0, y1 = as_f(sums[q][2 * i + 1]) * k0;
+      if constexpr (FORM == kSym) {
+        const float2 u = unpack_half(a[q][i]), v = unpack_half(b[q][i]);
+        y0 = fmaf(by, v.x, fmaf(u.x, by_col[i & ~1], y0));
+        y1 = fmaf(by, v.y, fmaf(u.y, by_col[i | 1], y1));
+      } else if constexpr (FORM != kGram) {
+        const float2 u = unpack_half(a[q][i]), v = unpack_half(b[q][i]);
+        y0 = fmaf(by, u.x + v.x, y0);
+        y1 = fmaf(by, u.y + v.y, y1);
+      }
+      if (diagonal) {  // this lane's element of it, if any; its place in the plane is 0
+        const int r = q * 16 + (i & 1) * 8 + (lane >> 2), c = (i >> 1) * 8 + (lane & 3) * 2;
+        if (r == c || r == c + 1) {
+          float v = (r == c ? y0 : y1) / p.out_scale;
+          if (row0 + r < p.m) {
+            if constexpr (FORM == kSym) {
+              const float dl = p.left_d[z + row0 + r], dr = p.right_d[z + row0 + r];
+              v += fmaf(p.s2 * dl, dr, fmaf(p.s1, dl, p.s0));
+            }
+            p.out_d[z + row0 + r] = v;
+          }
+          if (r == c)
+            y0 = 0.0f;
+          else
+            y1 = 0.0f;
+        }
+      }
+      if constexpr (FORM == kUpdate)
+        split_half2(y0, y1, hi[i], lo[i]);
+      else if constexpr (FORM == kLast)
+        hi[i] = pack_bf16(y0, y1);
+      else
+        hi[i] = pack_half(y0, y1);
+    }
+    if (FORM == kLast && p.tall) {
+      put_turned(slot, q * 16, lane, hi);
+    } else {
+      put_rows(slot, q * 16, lane, hi);
+      if constexpr (FORM == kUpdate) put_rows(slot + kBox, q * 16, lane, lo);
+      if constexpr (FORM == kGram || FORM == kSym)
+        if (t.m != t.n) put_turned(slot + kBox, q * 16, lane, hi);
+    }
+  }
+  __syncwarp();
+  if constexpr (FORM == kLast) {
+    uint16_t* dst = targets.p[t.z - p.first];
+    if (p.tall)
+      send_last(slot, dst + (int64_t)col * p.ld_out + row0, p.ld_out, p.wide - col, p.m - row0, lane);
+    else
+      send_last(slot, dst + (int64_t)row0 * p.ld_out + col, p.ld_out, p.m - row0, p.wide - col, lane);
+  } else {
+    send_box(slot, p.out[0] + (z + row0) * p.ld + col, p.ld, p.m - row0, lane);
+    if constexpr (FORM == kUpdate)
+      send_box(slot + kBox, p.out[1] + (z + row0) * p.ld + col, p.ld, p.m - row0, lane);
+    else if (t.m != t.n)
+      send_box(slot + kBox, p.out[0] + (z + col) * p.ld + row0, p.ld, p.m - col, lane);
+  }
+  __syncwarp();
 }
 
 template <int FORM>
@@ -327,20 +398,57 @@ __global__ void __launch_bounds__(kThreads, 1)
       mma_commit<2>(spare, 1);
     }
   } else if (warp >= 4) {
-    Boxes out;
-    out.base = smem + kStages * kStage + (warp - 4) * kBoxes * kBox, out.next = 0, out.lane = lane;
+    const int half = (warp - 4) >> 2, lanes = (warp & 3) * 32;
+    const uint32_t slot0 = smem + kStages * kStage + (warp - 4) * kSlots * kSlot;
+    // Pieces in turn, slot by slot; `next` is the one whose copies go out.
+    constexpr bool kIn = FORM != kGram;
+    Cursor<FORM> now, next;
+    now.open(p, pair, pairs, 0, half, rank, lanes);
+    next = now;
+    int slot = 0;  // of the piece at hand, and of the next to be asked for
+    Diagonals d[kSlots];
+    const auto ask = [&](int to) {
+      if (kIn && next.more) {
+        Diagonals v{0.0f, 0.0f};
+        const int64_t z = (int64_t)next.at.z * p.m;
+        if (next.row0 + lane < p.m) v.di = p.left_d[z + next.row0 + lane];
+        if (FORM == kSym && next.col + lane < p.wide) v.dj = p.right_d[z + next.col + lane];
+#pragma unroll
+        for (int s = 0; s < kSlots; ++s)
+          if (s == to) d[s] = v;
+        for (int q = 0; q < p.planes; ++q)
+          ask_box(slot0 + to * kSlot + q * kBox, p.in[q] + ((int64_t)next.at.z * p.m + next.row0) * p.ld + next.col, p.ld,
+                  p.m - next.row0, lane);
+        next.col += 32;
+        if (--next.left == 0) next.open(p, pair, pairs, next.i + 1, half, rank, lanes);
+      }
+      if (kIn) asked();  // an empty group past the last, so that their number says which have arrived
+    };
+    for (int s = 0; s < kSlots; ++s) ask(s);
     TileAt at;
+    // every tile's sums are waited for and handed back, a piece of it here or not
     for (int i = 0; work_at<FORM>(p, pair, pairs, i, at); ++i) {
       const int b = i & 1;
       if (!bar_wait_warp(late ? silent : sums_full(b), (i / 2) & 1, sums_watch)) break;
       fence_after();
-      const uint32_t lanes = (uint32_t)(warp & 3) * 32;
-      epilogue<FORM>(p, targets, at, tmem + (lanes << 16) + b * 256, (at.m * 2 + rank) * kHalf + lanes, (warp - 4) >> 2, out);
+      while (now.more && now.i == i) {
+        if (kIn) arrived<kSlots - 1>();
+        const int c = (now.col - at.n * 2 * kHalf) / 32;
+        Diagonals mine{0.0f, 0.0f};
+#pragma unroll
+        for (int s = 0; s < kSlots; ++s)
+          if (kIn && s == slot) mine = d[s];
+        finish<FORM>(p, targets, at, now.row0, now.col, lane, tmem + ((uint32_t)lanes << 16) + b * 256 + c * 32, slot0 + slot * kSlot, mine);
+        ask(slot);
+        slot = slot + 1 == kSlots ? 0 : slot + 1;
+        now.col += 32;
+        if (--now.left == 0) now.open(p, pair, pairs, now.i + 1, half, rank, lanes);
+      }
       fence_before();
       __syncwarp();
       if (lane == 0) bar_arrive_peer(peer_addr(sums_empty(b), 0));
     }
-    if (lane == 0) stores_done();
+    if (kIn) arrived<0>();
   }
   __syncthreads();
   if (stop && warp == 1 && rank == 0 && !p.stall_ns) {
@@ -363,14 +471,10 @@ cudaError_t launch(Params& p, const OrthoTargets& targets, const TcLaunch& l, cu
 bool map_k(CUtensorMap* map, const __half* plane, int64_t cols, const OrthoPlan& p, int64_t ld) {
   return make_stack_map(map, plane, cols, p.m, p.count, ld, kStep, kHalf, CU_TENSOR_MAP_SWIZZLE_128B);
 }
-bool map_out(CUtensorMap* map, const __half* plane, int64_t cols, const OrthoPlan& p, int64_t ld) {
-  return make_stack_map(map, plane, cols, p.m, p.count, ld, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
-}
-
 }  // namespace
 
 cudaError_t ortho_prepare(TcDevice*) {
-  void (*const kernels[])(Params, OrthoTargets) = {ortho_tc_kernel<kGram>, ortho_tc_kernel<kSquare>, ortho_tc_kernel<kUpdate>,
+  void (*const kernels[])(Params, OrthoTargets) = {ortho_tc_kernel<kGram>, ortho_tc_kernel<kSym>, ortho_tc_kernel<kUpdate>,
                                                    ortho_tc_kernel<kLast>};
   for (auto k : kernels) {
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
@@ -379,45 +483,42 @@ cudaError_t ortho_prepare(TcDevice*) {
   return cudaSuccess;
 }
 
-cudaError_t launch_ortho_product(OrthoForm form, const OrthoPlan& p, const OrthoStep& s, int turn, const OrthoArgs& a,
-                                 const TcLaunch& l, cudaStream_t stream) {
+cudaError_t launch_ortho_product(const OrthoPlan& p, const OrthoProduct& q, const OrthoArgs& a, const TcLaunch& l,
+                                 cudaStream_t stream) {
   Params k{};
   OrthoTargets targets{};
-  const __half *const *x = p.x[turn], *const *next = p.x[turn ^ 1];
-  const bool update = form >= kUpdate;
+  __half *const *x = p.x[q.turn], *const *next = p.x[q.turn ^ 1];
+  const bool update = q.form >= kUpdate;
   const int64_t down = ceil_div(p.m, 2 * kHalf), across = ceil_div(p.n, 2 * kHalf);
   k.m = p.m, k.wide = update ? p.n : p.m;
-  k.d = p.d, k.e = p.e;
-  k.a = s.a, k.b = s.b, k.c = s.c;
+  k.steps = (int)ceil_div(q.form == kGram ? p.n : p.m, kStep);
+  k.left_d = p.d[q.left], k.right_d = p.d[q.right], k.out_d = p.d[q.out];
+  k.s2 = q.s2, k.s1 = q.s1, k.s0 = q.s0;
+  k.sum_scale = 1.0f / (q.left_scale * q.right_scale);
+  k.left_scale = 1.0f / q.left_scale, k.right_scale = 1.0f / q.right_scale;
+  k.out_scale = q.form == kLast ? 1.0f : q.out_scale;
   k.tall = p.tall, k.ld_out = a.ld_dst;
   bool ok = true;
-  if (form == kGram) {
-    k.steps = (int)ceil_div(p.n, kStep);
-    k.sum_scale = 1.0f / (s.x_scale * s.x_scale), k.out_scale = s.a_scale;
-    ok = map_k(&k.left, x[0], p.n, p, p.ld_x) && map_out(&k.out[0], p.o[0], p.m, p, p.ld_a) &&
-         map_out(&k.out[1], p.o[1], p.m, p, p.ld_a);
+  k.ld = update ? p.ld_x : p.ld_a;
+  if (q.form == kGram) {
+    ok = map_k(&k.left, x[0], p.n, p, p.ld_x);
     k.right = k.left;
-  } else if (form == kSquare) {
-    k.steps = (int)ceil_div(p.m, kStep);
-    k.hi = p.o[0], k.lo = p.o[1], k.ld = p.ld_a;
-    k.sum_scale = 1.0f / (s.a_scale * s.a_scale), k.in_scale = 1.0f / s.a_scale, k.out_scale = s.b_scale;
-    ok = map_k(&k.left, p.o[0], p.m, p, p.ld_a) && map_out(&k.out[0], p.p, p.m, p, p.ld_a);
-    k.right = k.left;
+  } else if (q.form == kSym) {
+    ok = map_k(&k.left, p.t[q.left], p.m, p, p.ld_a) && map_k(&k.right, p.t[q.right], p.m, p, p.ld_a);
+    k.planes = q.left == q.right ? 1 : 2;
+    k.in[0] = p.t[q.left], k.in[1] = p.t[q.right];
   } else {
-    k.steps = (int)ceil_div(p.m, kStep);
-    k.hi = x[0], k.lo = x[1], k.ld = p.ld_x;
-    k.sum_scale = 1.0f / (s.b_scale * s.x_scale), k.in_scale = 1.0f / s.x_scale, k.out_scale = s.next_scale;
-    ok = map_k(&k.left, p.p, p.m, p, p.ld_a) && make_slab_stack_map(&k.right, x[0], p.m, p.count, p.ld_x, kStep);
-    if (form == kUpdate)
-      ok = ok && map_out(&k.out[0], next[0], p.n, p, p.ld_x) && map_out(&k.out[1], next[1], p.n, p, p.ld_x);
+    ok = map_k(&k.left, p.t[q.left], p.m, p, p.ld_a) && make_slab_stack_map(&k.right, x[0], p.m, p.count, p.ld_x, kStep);
+    k.planes = 2;
+    k.in[0] = x[0], k.in[1] = x[1];
   }
+  k.out[0] = update ? next[0] : p.t[q.out], k.out[1] = next[1];
   if (!ok) return cudaErrorInvalidValue;
   const int64_t each = update ? down * across : down * (down + 1) / 2;
-  if (each > INT32_MAX) return cudaErrorInvalidValue;
   // as many matrices as a launch counts tiles, and the last form's table holds
   int64_t most = INT32_MAX / 2 / each;
-  if (most < 1) most = 1;
-  if (form == kLast && most > kOrthoTable) most = kOrthoTable;
+  if (most < 1) return cudaErrorInvalidValue;
+  if (q.form == kLast && most > kOrthoTable) most = kOrthoTable;
   for (k.first = 0; k.first < p.count; k.first += most) {
     const int64_t some = p.count - k.first < most ? p.count - k.first : most;
     k.tiles = (int)(some * each);
@@ -425,12 +526,12 @@ cudaError_t launch_ortho_product(OrthoForm form, const OrthoPlan& p, const Ortho
       k.grid = TileGrid((int)down, (int)across);
     else
       k.each = Divisor((int)each);
-    if (form == kLast)
+    if (q.form == kLast)
       for (int64_t i = 0; i < some; ++i) targets.p[i] = a.dst[k.first + i];
-    const cudaError_t e = form == kGram     ? launch<kGram>(k, targets, l, stream)
-                          : form == kSquare ? launch<kSquare>(k, targets, l, stream)
-                          : form == kUpdate ? launch<kUpdate>(k, targets, l, stream)
-                                            : launch<kLast>(k, targets, l, stream);
+    const cudaError_t e = q.form == kGram     ? launch<kGram>(k, targets, l, stream)
+                          : q.form == kSym    ? launch<kSym>(k, targets, l, stream)
+                          : q.form == kUpdate ? launch<kUpdate>(k, targets, l, stream)
+                                              : launch<kLast>(k, targets, l, stream);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

@@ -183,12 +183,6 @@ __device__ __forceinline__ void store_box(const CUtensorMap* m, int x, int y, ui
                : "memory");
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
-__device__ __forceinline__ void store_box3(const CUtensorMap* m, int x, int y, int z, uint32_t src) {
-  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(m), "r"(x),
-               "r"(y), "r"(z), "r"(src)
-               : "memory");
-  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-}
 template <int N>
 __device__ __forceinline__ void stores_read() {  // all but the last N groups have been read from shared memory
   asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");

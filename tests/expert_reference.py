@@ -179,45 +179,69 @@ def step_of(coefficients, i):
 def orthogonalize_bound(g, steps=5, coefficients=COEFFICIENTS, eps=1e-7):
     """A bound of the error's Frobenius norm, before the rounding to bf16.
 
-    Each operand of a product is off by up to 2^-11 of itself, in directions that
-    have nothing to do with each other: their root mean square is at most u =
-    2^-11 / sqrt(3), and a product of P and X off by u sqrt(2 sum_k |P[:, k]|^2
-    |X[k, :]|^2) in that sense.  Four times that is allowed (a sum of that many
-    independent terms does not come near it), fp32's own sums beside it.
-    Scales bring a matrix's largest possible norm to between 2^13 and 2^14, so
-    fp16's smallest numbers leave out what is below 2^-38 of that norm.
-    What a step is off by, the later ones stretch by at most the largest slope
-    of s -> s (a + b s^2 + c s^4), or of its chords from the origin, over the
-    singular values there are (the norm of a matrix function's derivative)."""
-    x = g.double()
-    if x.shape[0] > x.shape[1]:
-        x = x.T
-    x = x / (x.norm() + eps)
-    u = 4 * U_F16 / math.sqrt(3)
-    small = 2.0 ** -38
-    bound = 1.0  # of X's norm
-    off = 4 * U_F32 * float(x.norm()) + small * math.sqrt(x.numel())  # X as two terms
-
-    def rough(left, right, depth):
-        """Of a product left @ right."""
-        f16 = u * math.sqrt(2 * float((left.square().sum(0) * right.square().sum(1)).sum()))
-        return f16 + (depth + 8) * 2 * U_F32 * float((left.abs() @ right.abs()).norm())
-
+    The roundings that the operator allows itself (X as two fp16 terms, of which
+    products take the first; the symmetric matrices as one beside their diagonals;
+    two steps by one pass over X where rows and columns allow it) are made here in
+    64 bits, and three times what they leave is allowed: other roundings of the same
+    sizes leave as much, not more, and fp32's own are 2^13 times smaller.  fp16's
+    smallest numbers leave out what is below 2^-37 of the largest norm that X can
+    have; every step stretches that by at most the largest slope of s -> s (a + b
+    s^2 + c s^4) for singular values from 0 on."""
+    want = orthogonalize(g, steps, coefficients, eps)
+    off = max(float((_rounded(g, steps, coefficients, eps, pairs) - want).norm()) for pairs in (False, True))
+    stretch, bound, floor = 1.0, 1.0, 2.0 ** -37
     for i in range(steps):
         a, b, c = step_of(coefficients, i)
-        gram = x @ x.T
-        top = float(torch.linalg.matrix_norm(gram, 2))
-        e_gram = rough(x, x.T, x.shape[1])
-        apart = gram - torch.diag(gram.diagonal())
-        e_b = (abs(b) + 2 * abs(c) * top) * e_gram + abs(c) * rough(apart, apart, x.shape[0])
-        poly = b * gram + c * gram @ gram
-        e_b += 8 * U_F32 * float(poly.norm())
-        rest = poly - torch.diag(poly.diagonal())
-        s = torch.linspace(0, math.sqrt(top) * 1.01, 2001, dtype=torch.float64)
-        slope = float(torch.maximum((a + 3 * b * s ** 2 + 5 * c * s ** 4).abs(), (a + b * s ** 2 + c * s ** 4).abs()).max())
-        wide = torch.linspace(0, bound, 2001, dtype=torch.float64)
-        e_b += small * x.shape[0] * (bound ** 2 * (abs(b) + 2 * abs(c) * top) + float((b * wide ** 2 + c * wide ** 4).abs().max()))
-        bound = float((a * wide + b * wide ** 3 + c * wide ** 5).abs().max())
-        off = small * bound * math.sqrt(x.numel()) + slope * off + math.sqrt(top) * e_b + rough(rest, x, x.shape[0]) + 8 * U_F32 * float(x.norm()) * (abs(a) + float(poly.diagonal().abs().max()))
-        x = a * x + poly @ x
-    return off
+        s = torch.linspace(0, bound, 4001, dtype=torch.float64)
+        stretch = max(1.0, float(torch.maximum((a + 3 * b * s ** 2 + 5 * c * s ** 4).abs(), (a + b * s ** 2 + c * s ** 4).abs()).max()))
+        bound = float((a * s + b * s ** 3 + c * s ** 5).abs().max())
+        floor = stretch * floor + bound * 2.0 ** -37
+    return 3 * off + floor * math.sqrt(g.numel())
+
+
+class _Kept:
+    """A symmetric matrix as one fp16 term, its diagonal beside it."""
+
+    def __init__(self, v):
+        self.d = v.diagonal().clone()
+        self.p = _half(v - torch.diag(self.d))
+
+    def __matmul__(self, o):
+        v = self.p @ o.p + self.d[:, None] * o.p + self.p * o.d[None, :] + torch.diag(self.d * o.d)
+        return (v + v.T) / 2
+
+    def value(self):
+        return self.p + torch.diag(self.d)
+
+
+def _half(v):
+    """Rounded to fp16 of a power-of-two scale that brings the largest to 2^13."""
+    top = float(v.abs().max()) if v.numel() else 0.0
+    if top == 0 or not math.isfinite(top):
+        return v
+    scale = 2.0 ** (13 - math.ceil(math.log2(top)))
+    return (v * scale).half().double() / scale
+
+
+def _rounded(g, steps, coefficients, eps, pairs):
+    x = g.double()
+    tall = x.shape[0] > x.shape[1]
+    if tall:
+        x = x.T
+    x = x / (x.norm() + eps)
+    eye = torch.eye(x.shape[0], dtype=torch.float64, device=x.device)
+    i = 0
+    while i < steps:
+        hi = _half(x)
+        x = hi + _half(x - hi)
+        a, b, c = step_of(coefficients, i)
+        gram = _Kept(hi @ hi.T)
+        poly = _Kept(a * eye + b * gram.value() + c * (gram @ gram))
+        i += 1
+        if pairs and i < steps:
+            a, b, c = step_of(coefficients, i)
+            second = _Kept(_Kept(poly @ gram) @ poly)
+            poly = _Kept(_Kept(a * eye + b * second.value() + c * (second @ second)) @ poly)
+            i += 1
+        x = poly.p @ hi + poly.d[:, None] * x
+    return x.T if tall else x

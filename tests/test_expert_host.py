@@ -99,7 +99,8 @@ def test_orthogonalize_refuses(compute):
     for bad in (dict(rows=-1), dict(cols=1 << 31), dict(rows=1 << 20, cols=1 << 20), dict(src=(A, 0)), dict(dst=(0, A)), dict(ld_src=15),
                 dict(ld_dst=15), dict(steps=-1), dict(steps=17), dict(eps=-1.0), dict(eps=math.inf), dict(eps=math.nan),
                 dict(workspace=0), dict(workspace_bytes=n - 1), dict(src_type=3), dict(coefficients=(math.nan, 0, 0)),
-                dict(coefficients=(1e6, 0, 0)), dict(coefficients=(8, 0, 0), steps=6), dict(coefficients=(1, 1, math.inf))):
+                dict(coefficients=(1e6, 0, 0)), dict(coefficients=(8, 0, 0), steps=6), dict(coefficients=(1, 1, math.inf)),
+                dict(steps=4, coefficients=(8.0, -22.0, 16.0, 4.0, -3.0, 0.6, 3.8, -2.8, 0.55, 3.0, -2.2, 0.45))):
         refused(BAD, call, **bad)
     for bad in (dict(src=(A, A + 2)), dict(src=(A, A + 1), src_type="bf16"), dict(dst=(A + 1, A)), dict(workspace=A + 128 + 8)):
         refused(MIS, call, **bad)

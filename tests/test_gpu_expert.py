@@ -312,11 +312,22 @@ def test_orthogonalize(compute, count, rows, cols, kind, pad):
         near(got, grad)
 
 
-@pytest.mark.parametrize("rows,cols", [(96, 200), (200, 96)])
+@pytest.mark.parametrize("rows,cols", [(512, 512), (384, 1024), (1024, 400), (256, 704)])
+def test_orthogonalize_is_as_near_as_bf16_is(compute, rows, cols):
+    """What the products leave is at most the result's own rounding, and independent of it."""
+    for kind in ("fp32", "bf16"):
+        grad = gradients(gen(rows), 1, rows, cols, kind)[0]
+        want = ref.orthogonalize(grad)
+        off = (orthogonalized(compute, [grad], kind)[0].double() - want).norm()
+        assert float(off) <= math.sqrt(2) * float((want.bfloat16().double() - want).norm())
+
+
+@pytest.mark.parametrize("rows,cols", [(96, 200), (200, 96), (128, 150)])
 @pytest.mark.parametrize("kw", [dict(steps=0), dict(steps=1), dict(steps=2), dict(steps=10, coefficients=(1.5, -0.5, 0.0)),
                                 dict(steps=8, coefficients=(1.875, -1.25, 0.375)), dict(steps=3, coefficients=(2.0, 0.0, -0.5)),
                                 dict(steps=2, coefficients=(4.0, -6.0, 2.5, 3.0, -3.5, 1.25)), dict(eps=0.0), dict(eps=10.0),
-                                dict(steps=4, coefficients=(0.0, 0.0, 0.0)), dict(steps=5, coefficients=(6.0, 0.0, 0.0))])
+                                dict(steps=4, coefficients=(0.0, 0.0, 0.0)), dict(steps=5, coefficients=(6.0, 0.0, 0.0)),
+                                dict(steps=3, coefficients=(8.0, -22.0, 16.0, 2.5, -1.0, 0.1, 1.875, -1.25, 0.375))])
 def test_orthogonalize_steps(compute, rows, cols, kw):
     grads = gradients(gen(3), 2, rows, cols, "fp32")
     for got, grad in zip(orthogonalized(compute, grads, **kw), grads):
