@@ -7,7 +7,6 @@ namespace tide {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kAtOnce = 8;  // rows of a token on their way at a time
 
 template <int V>
 struct Piece {
@@ -54,146 +53,184 @@ __device__ __forceinline__ Piece<V> rounded(const float (&f)[V]) {
 }
 
 // Threads of a token: a power of two of lanes, so that small rows share a
-// warp and large ones take a whole CTA.
+// warp and large ones take up to a whole CTA.
 struct Shape {
   int lanes, tokens;  // threads of a token; tokens of a CTA
   int64_t pieces;     // of a row
 };
 
-// The address of a slot's row, or NULL outside the rows.
-__device__ __forceinline__ int64_t row_of(const RowsArgs& a, int64_t pair) {
-  const int s = a.slots[pair];
-  return s >= 0 && s < a.num_rows ? s : -1;
-}
+// K of a token's slots (from pair `p` on, `left` of which there are), those
+// outside the rows as -1, and the weights.
+template <int K>
+struct Slots {
+  int64_t row[K];
+  float w[K];
 
-template <int V>
+  __device__ __forceinline__ void load(const RowsArgs& a, int64_t p, int left) {
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+      const int s = j < left ? a.slots[p + j] : -1;
+      row[j] = s >= 0 && s < a.num_rows ? s : -1;
+      w[j] = j < left && a.weights ? a.weights[p + j] : 1.0f;
+    }
+  }
+};
+
+template <int V, int K>
 __global__ void __launch_bounds__(kThreads) gather_kernel(RowsArgs a, Shape s) {
   after_previous();
   const int64_t t = (int64_t)blockIdx.x * s.tokens + threadIdx.x / s.lanes;
   if (t >= a.tokens) return;
   const int64_t p0 = t * a.topk;
-  for (int64_t q = threadIdx.x % s.lanes; q < s.pieces; q += s.lanes) {
-    const Piece<V> v = load<V>(a.in + t * a.ld_in + q * V);
-    for (int j = 0; j < a.topk; ++j) {
-      const int64_t r = row_of(a, p0 + j);
-      if (r >= 0) store<V>(a.out + r * a.ld_out + q * V, v);
+  for (int j0 = 0; j0 < a.topk; j0 += K) {
+    Slots<K> at;
+    at.load(a, p0 + j0, a.topk - j0);
+    for (int64_t q = threadIdx.x % s.lanes; q < s.pieces; q += s.lanes) {
+      const Piece<V> v = load<V>(a.in + t * a.ld_in + q * V);
+#pragma unroll
+      for (int j = 0; j < K; ++j)
+        if (at.row[j] >= 0) store<V>(a.out + at.row[j] * a.ld_out + q * V, v);
     }
   }
 }
 
-template <int V>
+// U pieces of a row at a time, so that U K loads of a thread are on their way.
+template <int V, int K, int U>
 __global__ void __launch_bounds__(kThreads) combine_kernel(RowsArgs a, Shape s) {
   after_previous();
   const int64_t t = (int64_t)blockIdx.x * s.tokens + threadIdx.x / s.lanes;
   if (t >= a.tokens) return;
   const int64_t p0 = t * a.topk;
-  for (int64_t q = threadIdx.x % s.lanes; q < s.pieces; q += s.lanes) {
-    float sum[V];
+  Slots<K> at;
+  at.load(a, p0, a.topk);
+  for (int64_t q = threadIdx.x % s.lanes; q < s.pieces; q += U * s.lanes) {
+    float sum[U][V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) sum[i] = 0.0f;
-    for (int j0 = 0; j0 < a.topk; j0 += kAtOnce) {
-      Piece<V> v[kAtOnce];
-      float w[kAtOnce];
-      bool in[kAtOnce];
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int j = 0; j < kAtOnce; ++j) {
-        const int64_t r = j0 + j < a.topk ? row_of(a, p0 + j0 + j) : -1;
-        in[j] = r >= 0;
-        w[j] = in[j] && a.weights ? a.weights[p0 + j0 + j] : 1.0f;
-        if (in[j]) v[j] = load<V>(a.in + r * a.ld_in + q * V);
-      }
+      for (int i = 0; i < V; ++i) sum[u][i] = 0.0f;
+    for (int j0 = 0;;) {
+      Piece<V> v[U][K];
 #pragma unroll
-      for (int j = 0; j < kAtOnce; ++j) {
-        if (!in[j]) continue;
-        float f[V];
-        values<V>(v[j], f);
+      for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int i = 0; i < V; ++i) sum[i] = fmaf(w[j], f[i], sum[i]);
-      }
+        for (int j = 0; j < K; ++j)
+          if (at.row[j] >= 0 && q + u * s.lanes < s.pieces) v[u][j] = load<V>(a.in + at.row[j] * a.ld_in + (q + u * s.lanes) * V);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+          if (at.row[j] < 0 || q + u * s.lanes >= s.pieces) continue;
+          float f[V];
+          values<V>(v[u][j], f);
+#pragma unroll
+          for (int i = 0; i < V; ++i) sum[u][i] = fmaf(at.w[j], f[i], sum[u][i]);
+        }
+      if (a.topk <= K) break;
+      // more choices than are held at a time: round to the first ones again
+      j0 = j0 + K < a.topk ? j0 + K : 0;
+      at.load(a, p0 + j0, a.topk - j0);
+      if (j0 == 0) break;
     }
-    store<V>(a.out + t * a.ld_out + q * V, rounded<V>(sum));
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (q + u * s.lanes < s.pieces) store<V>(a.out + t * a.ld_out + (q + u * s.lanes) * V, rounded<V>(sum[u]));
   }
 }
 
 // The weights' gradients are sums along a row: of each thread's pieces in
 // order, then over the token's threads in a fixed order.
-template <int V>
+template <int V, int K, int U>
 __global__ void __launch_bounds__(kThreads) combine_backward_kernel(RowsArgs a, Shape s) {
   after_previous();
-  __shared__ float parts[kThreads / 32][kAtOnce];
+  __shared__ float parts[kThreads / 32][K];
   const int64_t t = (int64_t)blockIdx.x * s.tokens + threadIdx.x / s.lanes;
   const bool mine = t < a.tokens;
   const int64_t p0 = t * a.topk;
   const int me = threadIdx.x % s.lanes;
-  for (int j0 = 0; j0 < a.topk; j0 += kAtOnce) {
-    float dot[kAtOnce], w[kAtOnce];
-    int64_t r[kAtOnce];
+  for (int j0 = 0; j0 < a.topk; j0 += K) {
+    float dot[K];
 #pragma unroll
-    for (int j = 0; j < kAtOnce; ++j) {
-      dot[j] = 0.0f;
-      r[j] = mine && j0 + j < a.topk ? row_of(a, p0 + j0 + j) : -1;
-      w[j] = r[j] >= 0 && a.weights ? a.weights[p0 + j0 + j] : 1.0f;
-    }
-    if (mine)
-      for (int64_t q = me; q < s.pieces; q += s.lanes) {
-        float d[V];
-        values<V>(load<V>(a.in + t * a.ld_in + q * V), d);
-        Piece<V> v[kAtOnce];
-        if (a.dweights)
+    for (int j = 0; j < K; ++j) dot[j] = 0.0f;
+    if (mine) {
+      Slots<K> at;
+      at.load(a, p0 + j0, a.topk - j0);
+      for (int64_t q = me; q < s.pieces; q += U * s.lanes) {
+        Piece<V> dy[U], v[U][K];
 #pragma unroll
-          for (int j = 0; j < kAtOnce; ++j)
-            if (r[j] >= 0) v[j] = load<V>(a.rows + r[j] * a.ld_rows + q * V);
+        for (int u = 0; u < U; ++u) {
+          const int64_t c = q + u * s.lanes;
+          if (c >= s.pieces) continue;
+          dy[u] = load<V>(a.in + t * a.ld_in + c * V);
+          if (a.dweights)
 #pragma unroll
-        for (int j = 0; j < kAtOnce; ++j) {
-          if (r[j] < 0) continue;
-          float f[V];
-          if (a.out) {
+            for (int j = 0; j < K; ++j)
+              if (at.row[j] >= 0) v[u][j] = load<V>(a.rows + at.row[j] * a.ld_rows + c * V);
+        }
 #pragma unroll
-            for (int i = 0; i < V; ++i) f[i] = w[j] * d[i];
-            store<V>(a.out + r[j] * a.ld_out + q * V, rounded<V>(f));
-          }
-          if (a.dweights) {
-            values<V>(v[j], f);
+        for (int u = 0; u < U; ++u) {
+          const int64_t c = q + u * s.lanes;
+          if (c >= s.pieces) continue;
+          float d[V];
+          values<V>(dy[u], d);
 #pragma unroll
-            for (int i = 0; i < V; ++i) dot[j] = fmaf(d[i], f[i], dot[j]);
+          for (int j = 0; j < K; ++j) {
+            if (at.row[j] < 0) continue;
+            float f[V];
+            if (a.out) {
+#pragma unroll
+              for (int i = 0; i < V; ++i) f[i] = at.w[j] * d[i];
+              store<V>(a.out + at.row[j] * a.ld_out + c * V, rounded<V>(f));
+            }
+            if (a.dweights) {
+              values<V>(v[u][j], f);
+#pragma unroll
+              for (int i = 0; i < V; ++i) dot[j] = fmaf(d[i], f[i], dot[j]);
+            }
           }
         }
       }
+    }
     if (!a.dweights) continue;
-    const int within = min(s.lanes, 32);
 #pragma unroll
-    for (int j = 0; j < kAtOnce; ++j)
-      for (int d = within >> 1; d; d >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], d);
+    for (int j = 0; j < K; ++j)
+      for (int d = min(s.lanes, 32) >> 1; d; d >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], d);
     if (s.lanes > 32) {
       if ((threadIdx.x & 31) == 0)
 #pragma unroll
-        for (int j = 0; j < kAtOnce; ++j) parts[threadIdx.x >> 5][j] = dot[j];
+        for (int j = 0; j < K; ++j) parts[threadIdx.x >> 5][j] = dot[j];
       __syncthreads();
       const int w0 = (threadIdx.x - me) >> 5;
 #pragma unroll
-      for (int j = 0; j < kAtOnce; ++j) {
+      for (int j = 0; j < K; ++j) {
         dot[j] = 0.0f;
-        for (int k = 0; k < s.lanes / 32; ++k) dot[j] += parts[w0 + k][j];
+        for (int w = 0; w < s.lanes / 32; ++w) dot[j] += parts[w0 + w][j];
       }
       __syncthreads();
     }
 #pragma unroll
-    for (int j = 0; j < kAtOnce; ++j)
+    for (int j = 0; j < K; ++j)
       if (mine && me == j % s.lanes && j0 + j < a.topk) a.dweights[p0 + j0 + j] = dot[j];
   }
 }
 
-Shape shape_of(const RowsArgs& a, int v) {
+// As many lanes a token as it takes to give every SM `busy` threads, and no
+// more than a row has pieces: fewer threads that stay longer wait less for
+// slots, more have more loads on their way.  (4093 tokens x 2048 x 8, backward:
+// 51 us with 256 to 768 threads, 57 with 1024, 79 with a CTA a token; results
+// of 4096 x 4096 x 2 back: 19.6, 21 and 32; 8191 x 2048 x 8 there: 53 with up
+// to 1024, 48.6 with 2048.)
+Shape shape_of(const RowsArgs& a, int v, int64_t busy) {
+  constexpr int64_t kSms = 152;
   Shape s{1, 0, a.hidden / v};
-  while (s.lanes < kThreads && s.lanes < s.pieces) s.lanes *= 2;
+  while (s.lanes < kThreads && s.lanes < s.pieces && (s.lanes < 32 || s.lanes * a.tokens < kSms * busy)) s.lanes *= 2;
   s.tokens = kThreads / s.lanes;
   return s;
 }
 
-template <class K8, class K1>
-cudaError_t run(K8 vec, K1 single, const RowsArgs& a, bool by8, cudaStream_t stream) {
-  const Shape s = shape_of(a, by8 ? 8 : 1);
-  return launch_early(by8 ? vec : single, dim3((unsigned)ceil_div(a.tokens, s.tokens)), kThreads, 0, 0, stream, a, s);
+cudaError_t run(void (*kernel)(RowsArgs, Shape), const RowsArgs& a, int v, int64_t busy, cudaStream_t stream) {
+  const Shape s = shape_of(a, v, busy);
+  return launch_early(kernel, dim3((unsigned)ceil_div(a.tokens, s.tokens)), kThreads, 0, 0, stream, a, s);
 }
 
 bool by8(const RowsArgs& a) {
@@ -203,15 +240,20 @@ bool by8(const RowsArgs& a) {
 }  // namespace
 
 cudaError_t launch_expert_gather(const RowsArgs& a, cudaStream_t stream) {
-  return run(gather_kernel<8>, gather_kernel<1>, a, by8(a), stream);
+  if (!by8(a)) return run(a.topk <= 2 ? gather_kernel<1, 2> : gather_kernel<1, 8>, a, 1, 2048, stream);
+  return run(a.topk <= 2 ? gather_kernel<8, 2> : gather_kernel<8, 8>, a, 8, 2048, stream);
 }
 
 cudaError_t launch_expert_combine(const RowsArgs& a, cudaStream_t stream) {
-  return run(combine_kernel<8>, combine_kernel<1>, a, by8(a), stream);
+  if (!by8(a))
+    return run(a.topk <= 2 ? combine_kernel<1, 2, 4> : a.topk <= 4 ? combine_kernel<1, 4, 2> : combine_kernel<1, 8, 1>, a, 1, 2048, stream);
+  if (a.topk <= 4) return run(a.topk <= 2 ? combine_kernel<8, 2, 4> : combine_kernel<8, 4, 2>, a, 8, 512, stream);
+  return run(combine_kernel<8, 8, 1>, a, 8, 2048, stream);
 }
 
 cudaError_t launch_expert_combine_backward(const RowsArgs& a, cudaStream_t stream) {
-  return run(combine_backward_kernel<8>, combine_backward_kernel<1>, a, by8(a), stream);
+  if (!by8(a)) return run(a.topk <= 2 ? combine_backward_kernel<1, 2, 8> : combine_backward_kernel<1, 8, 4>, a, 1, 256, stream);
+  return run(a.topk <= 2 ? combine_backward_kernel<8, 2, 1> : combine_backward_kernel<8, 8, 1>, a, 8, 512, stream);
 }
 
 }  // namespace tide

@@ -88,88 +88,109 @@ __device__ __forceinline__ uint64_t max_key(uint64_t k) {
   return (uint64_t)hi << 32 | lo;
 }
 
-__device__ __forceinline__ float exp_of(float v) { return expf(v); }
-__device__ __forceinline__ double exp_of(double v) { return exp(v); }
-
-// The scores of a lane's run, in F (32 or 64 bits).  Softmax: top is the row's
-// largest logit; a row of masked experts has scores of 0.
-template <class F, int N>
-__device__ __forceinline__ void scores_of(const float (&l)[N], bool sigmoid, float top, F (&s)[N]) {
+// The scores of a lane's run.  Softmax: top is the row's largest logit; a row
+// of masked experts has scores of 0.
+template <int N>
+__device__ __forceinline__ void scores_of(const float (&l)[N], bool sigmoid, float top, float (&s)[N]) {
   if (sigmoid) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) s[i] = F(1) / (F(1) + exp_of(-F(l[i])));
+    for (int i = 0; i < N; ++i) s[i] = 1.0f / (1.0f + expf(-l[i]));
     return;
   }
-  F sum = 0;
+  float sum = 0.0f;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    s[i] = top == -CUDART_INF_F && l[i] == top ? F(0) : exp_of(F(l[i]) - F(top));
+    s[i] = top == -CUDART_INF_F && l[i] == top ? 0.0f : expf(l[i] - top);
     sum += s[i];
   }
   sum = warp_sum(sum);
 #pragma unroll
-  for (int i = 0; i < N; ++i) s[i] = sum == F(0) ? F(0) : s[i] / sum;
+  for (int i = 0; i < N; ++i) s[i] = sum == 0.0f ? 0.0f : s[i] / sum;
 }
 
 // What a router's choice needs of its arguments.
 struct Choice {
   int experts, own, topk, groups, each, top_groups, group_best;
+  int lanes;  // of a group, if groups are whole lanes' runs and those a power of two; else 0
 };
 
-// Drops the keys of groups that are not among the best.  A lane's run may
-// lie in several groups.  Returns whether two groups on either side of the
-// border are no further apart than `near` times (1 + their scores' magnitudes).
+// Drops the keys of groups that are not among the best.  Returns whether two
+// groups on either side of the border are no further apart than `near` times
+// (1 + their scores' magnitudes); then nothing is dropped.  `second` receives
+// the key that a group's score goes down to, where a group is whole lanes.
 template <int N, class K>
-__device__ __forceinline__ bool keep_groups(const Choice& c, int first, float near, K (&key)[N]) {
+__device__ __forceinline__ bool keep_groups(const Choice& c, int first, float near, K (&key)[N], K* second = nullptr) {
   using F = decltype(value_of_key(K()));
   const int lane = threadIdx.x & 31;
-  F mine = 0;  // lane g: group g's score
-  for (int g = 0; g < c.groups; ++g) {
-    const int lo = g * c.each - first, hi = lo + c.each;  // the group among this lane's run
+  // Lane g's score of group g, or, where a group is whole lanes, each lane's
+  // of its own group.
+  K order;
+  if (c.lanes) {
     K best = 0, next = 0;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const K k = i >= lo && i < hi ? key[i] : 0;
-      next = k > best ? best : k > next ? k : next;
-      best = k > best ? k : best;
+      const K k = key[i];
+      next = max(next, min(best, k));
+      best = max(best, k);
     }
-    const K top = max_key(best);
-    F score = value_of_key(top);
-    if (c.group_best == 2 && c.each > 1) {
-      const int owner = __ffs(__ballot_sync(0xffffffffu, best == top)) - 1;
-      score += value_of_key(max_key(lane == owner ? next : best));
+    for (int d = 1; d < c.lanes; d <<= 1) {
+      const K b = __shfl_xor_sync(0xffffffffu, best, d), n = __shfl_xor_sync(0xffffffffu, next, d);
+      next = max(max(next, n), min(best, b));
+      best = max(best, b);
     }
-    if (lane == g) mine = score;
+    F score = value_of_key(best);
+    const bool two = c.group_best == 2 && c.each > 1;
+    if (two) score += value_of_key(next);
+    order = key_of(score);
+    if (second) *second = two ? next : best;
+  } else {
+    F mine = 0;
+    for (int g = 0; g < c.groups; ++g) {
+      const int lo = g * c.each - first, hi = lo + c.each;  // the group among this lane's run
+      K best = 0, next = 0;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const K k = i >= lo && i < hi ? key[i] : 0;
+        next = max(next, min(best, k));
+        best = max(best, k);
+      }
+      const K top = max_key(best);
+      F score = value_of_key(top);
+      if (c.group_best == 2 && c.each > 1) {
+        const int owner = __ffs(__ballot_sync(0xffffffffu, best == top)) - 1;
+        score += value_of_key(max_key(lane == owner ? next : best));
+      }
+      if (lane == g) mine = score;
+    }
+    order = lane < c.groups ? key_of(mine) : 0;
   }
-  const K order = lane < c.groups ? key_of(mine) : 0;
+  const int step = c.lanes ? c.lanes : 1, me = lane / step;
   int above = 0;
   for (int g = 0; g < c.groups; ++g) {
-    const K other = __shfl_sync(0xffffffffu, order, g);
-    above += other > order || (other == order && g < lane);
+    const K other = __shfl_sync(0xffffffffu, order, g * step);
+    above += other > order || (other == order && g < me);
   }
-  const uint32_t kept = __ballot_sync(0xffffffffu, lane < c.groups && above < c.top_groups);
-  bool close = false;
+  const bool in = me < c.groups, stays = in && above < c.top_groups;
   if (near > 0.0f && c.top_groups < c.groups) {
     // the border: the lowest kept, the highest left
-    const K low = ~max_key((K)~(kept >> lane & 1 ? order : (K)~(K)0));
-    const K high = max_key(lane < c.groups && !(kept >> lane & 1) ? order : (K)0);
+    const K low = (K)~max_key((K)~(stays ? order : (K)~(K)0)), high = max_key(in && !stays ? order : (K)0);
     const F a = value_of_key(low), b = value_of_key(high);
-    close = a - b <= F(near) * (F(1) + fabs(a) + fabs(b)) && fabs(a) < F(CUDART_INF_F) && fabs(b) < F(CUDART_INF_F);
+    const bool close = a - b <= F(near) * (F(1) + fabs(a) + fabs(b)) && fabs(a) < F(CUDART_INF_F) && fabs(b) < F(CUDART_INF_F);
+    if (close) return true;
   }
+  const uint32_t kept = __ballot_sync(0xffffffffu, stays);
 #pragma unroll
   for (int i = 0; i < N; ++i)
-    if (!(kept >> min((first + i) / c.each, 31) & 1)) key[i] = 0;
-  return close;
+    if (!(c.lanes ? stays : (bool)(kept >> min((first + i) / c.each, 31) & 1))) key[i] = 0;
+  return false;
 }
 
-// The `rounds` largest keys in order: lane j returns the j-th's expert and
-// its key.
+// The largest keys in order, from the `from`-th to before the `to`-th: lane j
+// returns the j-th's expert and its key, other lanes what they had.
 template <int N, class K>
-__device__ __forceinline__ int pick(const Choice& c, int first, int rounds, K (&key)[N], K* picked) {
+__device__ __forceinline__ int pick(const Choice& c, int first, int from, int to, K (&key)[N], int mine, K* picked) {
   const int lane = threadIdx.x & 31;
-  int mine = 0;
-  *picked = 0;
-  for (int j = 0; j < rounds; ++j) {
+  for (int j = from; j < to; ++j) {
     K best = 0;
     int at = 0;
 #pragma unroll
@@ -184,6 +205,11 @@ __device__ __forceinline__ int pick(const Choice& c, int first, int rounds, K (&
       if (lane == owner && i == at) key[i] = 0;
   }
   return mine;
+}
+template <int N, class K>
+__device__ __forceinline__ int pick(const Choice& c, int first, K (&key)[N]) {
+  K picked = 0;
+  return pick(c, first, 0, c.topk, key, 0, &picked);
 }
 
 // A lane's weight from its pick's logit, before the scale.  With
@@ -200,20 +226,55 @@ __device__ __forceinline__ float weight_of(float l, bool in, bool sigmoid, bool 
   return sum == 0.0f ? 0.0f : s / sum;
 }
 
-// Scores in 64 bits, for a token whose borders 32 do not tell.
+// The sum of a softmax's exponentials in 64 bits.
 template <int N>
-__device__ __noinline__ int pick_wide(const Choice& c, int first, const float (&l)[N], bool sigmoid, float top,
-                                      const float* bias) {
-  double s[N];
-  scores_of(l, sigmoid, top, s);
-  uint64_t key[N], picked;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const bool in = i < c.own && first + i < c.experts;
-    key[i] = in ? key_of(s[i] + (bias ? (double)bias[first + i] : 0.0)) : 0;
+__device__ __noinline__ double wide_sum(const float (&l)[N], float top) {
+  double sum = 0.0;
+#pragma unroll 1
+  for (int i = 0; i < N; ++i) sum += top == -CUDART_INF_F && l[i] == top ? 0.0 : exp((double)l[i] - (double)top);
+  return warp_sum(sum);
+}
+// A score plus bias in 64 bits.
+__device__ __noinline__ double wide_choice(float l, float bias, bool sigmoid, float top, double sum) {
+  double s = 0.0;
+  if (sigmoid)
+    s = 1.0 / (1.0 + exp(-(double)l));
+  else if (sum != 0.0 && l != -CUDART_INF_F)
+    s = exp((double)l - (double)top) / sum;
+  return s + (double)bias;
+}
+
+// Keys in 64 bits of what may count: all whose key in 32 is at least `from`.
+template <int N>
+__device__ __noinline__ void wide_keys(const Choice& c, int first, const float (&l)[N], const uint32_t (&key)[N], uint32_t from,
+                                       bool sigmoid, float top, const float* bias, uint64_t (&wide)[N]) {
+  const double sum = sigmoid ? 0.0 : wide_sum(l, top);
+#pragma unroll 1
+  for (int i = 0; i < N; ++i)
+    wide[i] = key[i] && key[i] >= from ? key_of(wide_choice(l[i], bias ? bias[first + i] : 0.0f, sigmoid, top, sum)) : 0;
+}
+
+// Drops groups by their scores in 64 bits.  Where a group is whole lanes,
+// only what may be among its best two is looked at: few a lane.
+template <int N>
+__device__ __noinline__ void keep_groups_wide(const Choice& c, int first, const float (&l)[N], uint32_t second, float near,
+                                              bool sigmoid, float top, const float* bias, uint32_t (&key)[N]) {
+  uint64_t wide[N];
+  uint32_t from = 1;
+  if (c.lanes) {
+    const float v = value_of_key(second);
+    from = fabsf(v) < CUDART_INF_F ? key_of(v - near * (1.0f + fabsf(v))) : second;
   }
-  if (c.groups > 1) keep_groups(c, first, 0.0f, key);
-  return pick(c, first, c.topk, key, &picked);
+  wide_keys(c, first, l, key, from, sigmoid, top, bias, wide);
+  keep_groups(c, first, 0.0f, wide);
+  // a kept group has its best ones' keys; what was not looked at goes with them
+  bool stays = false;
+#pragma unroll
+  for (int i = 0; i < N; ++i) stays |= wide[i] != 0;
+  for (int d = 1; d < c.lanes; d <<= 1) stays |= __shfl_xor_sync(0xffffffffu, (int)stays, d) != 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (c.lanes ? !stays : !wide[i]) key[i] = 0;
 }
 
 // N: logits a lane holds, at least ceil(experts / 32).
@@ -239,11 +300,11 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouterArgs a, Choice c)
   float sum = 0.0f;
   int expert;
   if (direct) {
-    uint32_t key[N], picked;
+    uint32_t key[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) key[i] = i < c.own && first + i < c.experts ? key_of(l[i]) : 0;
     if (c.groups > 1) keep_groups(c, first, 0.0f, key);
-    expert = pick(c, first, c.topk, key, &picked);
+    expert = pick(c, first, key);
   } else {
     float s[N];
     uint32_t key[N], picked;
@@ -255,21 +316,71 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouterArgs a, Choice c)
     }
     // A sigmoid here is off by at most 4 2^-24 of itself, a softmax by 64
     // (its sum of up to 1024 terms 37 of them), a sum with the bias by 2^-24
-    // of itself more: how far apart two of them may seem, with as much again.
-    const float near = sigmoid ? 0x1p-21f : 0x1p-17f;
-    bool close = c.groups > 1 && keep_groups(c, first, 2.0f * near, key);
-    // one more than wanted, for the last border
-    const int rounds = c.topk < c.experts ? c.topk + 1 : c.topk;
-    expert = pick(c, first, rounds, key, &picked);
-    const float mine = value_of_key(picked), next = __shfl_down_sync(0xffffffffu, mine, 1);
-    const float b = a.bias && lane < rounds ? a.bias[expert] : 0.0f, l0 = lane < rounds ? value_of(row + expert) : 0.0f;
-    const float next_b = __shfl_down_sync(0xffffffffu, b, 1), next_l = __shfl_down_sync(0xffffffffu, l0, 1);
-    const uint32_t next_key = __shfl_down_sync(0xffffffffu, picked, 1);
-    // (equal logits with equal biases are equals, whatever the rounding)
-    if (lane + 1 < rounds && next_key > 1u && !(l0 == next_l && b == next_b) && fabsf(mine) < CUDART_INF_F &&
-        fabsf(next) < CUDART_INF_F)
-      close |= mine - next <= near * (fabsf(mine - b) + fabsf(next - next_b)) + 0x1p-22f * (fabsf(mine) + fabsf(next));
-    if (__any_sync(0xffffffffu, close)) expert = pick_wide(c, first, l, sigmoid, top, a.bias);
+    // of itself more.  So `near` is how far apart any two of a row may seem
+    // that are equal, with as much again; what is further apart is in order.
+    float near = 0x1p-20f;
+    if (!sigmoid) {
+      float most = 0.0f;
+#pragma unroll
+      for (int i = 0; i < N; ++i) most = fmaxf(most, s[i]);
+      near = 0x1p-16f * warp_max(most);
+    }
+    if (c.groups > 1) {
+      const float apart = sigmoid ? 0x1p-20f : 0x1p-16f;
+      uint32_t second = 0;
+      if (keep_groups(c, first, apart, key, &second)) keep_groups_wide(c, first, l, second, apart, sigmoid, top, a.bias, key);
+    }
+    uint32_t allowed = 0;  // of this lane's run
+#pragma unroll
+    for (int i = 0; i < N; ++i) allowed |= (key[i] != 0 ? 1u : 0u) << i;
+    // more than are wanted, as long as the last one's neighbour may be before it
+    int rounds = min(c.topk + 1, c.experts), at = 0;
+    expert = 0, picked = 0;
+    bool close = false;
+    while (true) {
+      expert = pick(c, first, at, rounds, key, expert, &picked);
+      const float mine = value_of_key(picked);
+      const float b = a.bias && lane < rounds ? a.bias[expert] : 0.0f, l0 = lane < rounds ? value_of(row + expert) : 0.0f;
+      const float next = __shfl_down_sync(0xffffffffu, mine, 1), next_b = __shfl_down_sync(0xffffffffu, b, 1);
+      const float next_l = __shfl_down_sync(0xffffffffu, l0, 1);
+      const uint32_t next_key = __shfl_down_sync(0xffffffffu, picked, 1);
+      const bool pair = lane + 1 < rounds && next_key > 1u && fabsf(mine) < CUDART_INF_F && fabsf(next) < CUDART_INF_F;
+      // equal logits with equal biases are equals, whatever the rounding
+      const bool equal = pair && l0 == next_l && b == next_b;
+      const uint32_t equals = __ballot_sync(0xffffffffu, equal);
+      const uint32_t which = __ballot_sync(0xffffffffu, pair && !equal && mine - next <= near + 0x1p-22f * (fabsf(mine) + fabsf(next)));
+      close = which != 0;
+      if (rounds < 2 || rounds >= min(c.experts, 32) || !((which | equals) >> (rounds - 2) & 1)) break;
+      at = rounds++;
+    }
+    if (close) {
+      if (rounds == 32 && c.experts > 32) {  // more than a warp holds: all of them again
+        uint64_t wide[N];
+        uint32_t all[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) all[i] = allowed >> i & 1;
+        wide_keys(c, first, l, all, 1, sigmoid, top, a.bias, wide);
+        expert = pick(c, first, wide);
+      } else {
+        const double sum = sigmoid ? 0.0 : wide_sum(l, top);
+        // the picks again, by 64 bits; what cannot be chosen stays last
+        const float b = a.bias ? a.bias[expert] : 0.0f;
+        uint64_t order = 0;
+        if (lane < rounds && picked) order = key_of(wide_choice(value_of(row + expert), b, sigmoid, top, sum));
+        int rank = 0;
+        for (int j = 0; j < rounds; ++j) {
+          const uint64_t other = __shfl_sync(0xffffffffu, order, j);
+          const int e = __shfl_sync(0xffffffffu, expert, j);
+          rank += other > order || (other == order && e < expert);
+        }
+        int mine = expert;
+        for (int j = 0; j < rounds; ++j) {
+          const int r = __shfl_sync(0xffffffffu, rank, j), e = __shfl_sync(0xffffffffu, expert, j);
+          if (r == lane) mine = e;
+        }
+        expert = mine;
+      }
+    }
   }
   if (!sigmoid && !a.renormalize) {
 #pragma unroll
@@ -381,7 +492,9 @@ cudaError_t run(const RouterArgs& a, const Choice& c, bool vec, cudaStream_t str
 template <Pass P, class T>
 cudaError_t run(const RouterArgs& a, cudaStream_t stream) {
   const int own = (int)ceil_div(a.experts, 32);
-  const Choice c{a.experts, own, a.topk, a.groups, a.experts / a.groups, a.top_groups, a.group_best};
+  const int each = a.experts / a.groups, lanes = each / own;
+  const Choice c{a.experts, own, a.topk, a.groups, each, a.top_groups, a.group_best,
+                 each % own == 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0};
   const auto whole = [](const void* p, int64_t ld) { return (uintptr_t)p % (4 * sizeof(T)) == 0 && ld % 4 == 0; };
   const bool vec = own % 4 == 0 && a.experts % 4 == 0 && whole(a.logits, a.ld) && (P == kForward || whole(a.dlogits, a.ldd));
   if (own <= 1) return run<P, 1, T>(a, c, vec, stream);

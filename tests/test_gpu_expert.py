@@ -101,18 +101,21 @@ def test_route_ties_and_masks(compute, router):
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
-def test_route_borders_that_32_bits_do_not_tell(compute, score):
-    """Score plus bias of neighbours a few 2^-26 apart, in 64 bits and no further."""
+@pytest.mark.parametrize("levels,e", [(8, 64), (1, 64), (3, 32), (2, 256), (1, 20)])
+def test_route_borders_that_32_bits_do_not_tell(compute, score, levels, e):
+    """Score plus bias of neighbours a few 2^-26 apart, in 64 bits and no further:
+    of a few, and of more than a warp has lanes."""
     g = gen(12)
-    t, e = 300, 64
+    t = 300
     logits = randn(g, 1, e).repeat(t, 1)
     s = ref.scores(logits, score)
-    # each expert's bias brings it to one of eight levels, as near as fp32 has it
-    level = torch.arange(e, device="cuda") % 8 / 16 + 1
+    # each expert's bias brings it to one of the levels, as near as fp32 has it
+    level = torch.arange(e, device="cuda") % levels / 16 + 1
     bias = (level - s[0]).float()
     logits = (logits.double() + torch.randn(t, e, generator=g, device="cuda", dtype=torch.float64) * 1e-7).float()
     check_route(compute, dict(experts=e, topk=16, score=score, renormalize=False), logits, bias, "fp32")
-    check_route(compute, dict(experts=e, topk=6, score=score, groups=8, top_groups=4, group_best=2), logits, bias, "fp32")
+    check_route(compute, dict(experts=e, topk=6, score=score, groups=4, top_groups=2, group_best=2), logits, bias, "fp32")
+    check_route(compute, dict(experts=e, topk=3, score=score, groups=4, top_groups=3), logits, bias, "fp32")
 
 
 @pytest.mark.parametrize("router", ROUTERS)
