@@ -226,12 +226,16 @@ __device__ __forceinline__ float weight_of(float l, bool in, bool sigmoid, bool 
   return sum == 0.0f ? 0.0f : s / sum;
 }
 
-// The sum of a softmax's exponentials in 64 bits.
+// The sum of a softmax's exponentials in 64 bits, several on their way at a
+// time: one by one they took 17 us of a call's 31.
 template <int N>
 __device__ __noinline__ double wide_sum(const float (&l)[N], float top) {
   double sum = 0.0;
-#pragma unroll 1
-  for (int i = 0; i < N; ++i) sum += top == -CUDART_INF_F && l[i] == top ? 0.0 : exp((double)l[i] - (double)top);
+#pragma unroll(N < 8 ? N : 8)
+  for (int i = 0; i < N; ++i) {
+    const double e = exp((double)l[i] - (double)top);
+    sum += top == -CUDART_INF_F && l[i] == top ? 0.0 : e;
+  }
   return warp_sum(sum);
 }
 // A score plus bias in 64 bits.
@@ -249,9 +253,19 @@ template <int N>
 __device__ __noinline__ void wide_keys(const Choice& c, int first, const float (&l)[N], const uint32_t (&key)[N], uint32_t from,
                                        bool sigmoid, float top, const float* bias, uint64_t (&wide)[N]) {
   const double sum = sigmoid ? 0.0 : wide_sum(l, top);
-#pragma unroll 1
-  for (int i = 0; i < N; ++i)
-    wide[i] = key[i] && key[i] >= from ? key_of(wide_choice(l[i], bias ? bias[first + i] : 0.0f, sigmoid, top, sum)) : 0;
+  // a lane's own ones after another, not the places of all lanes'
+  uint32_t left = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    wide[i] = 0;
+    left |= (key[i] && key[i] >= from ? 1u : 0u) << i;
+  }
+  while (left) {
+    const int i = __ffs(left) - 1;
+    left &= left - 1;
+    wide[i] = key_of(wide_choice(l[i], bias ? bias[first + i] : 0.0f, sigmoid, top, sum));
+  }
+  __syncwarp();
 }
 
 // Drops groups by their scores in 64 bits.  Where a group is whole lanes,
