@@ -187,6 +187,7 @@ struct TcDevice {
   int sms;
   int pairs;               // of CTAs
   PairClusters gated, fp8;  // of the split kernels
+  PairClusters ortho;       // that keep a matrix
   FewClusters few[4][3][2];  // by kind, tile of tokens and activation
 };
 

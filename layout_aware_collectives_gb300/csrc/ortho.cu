@@ -307,16 +307,16 @@ cudaError_t launch_orthogonalize(const OrthoArgs& a, const TcLaunch& l, cudaStre
                        a.cols, a.ld_src, a.ld_dst, a.eps);
     if (e != cudaSuccess) return e;
   }
-  int turn = 0;
+  if (!a.steps) return cudaSuccess;
+  OrthoProduct q[4 * TIDE_MAX_ORTHOGONALIZE_STEPS];  // 3 a step, 7 for two that share a pass
+  int products = 0, turn = 0;
   for (int i = 0; i < a.steps; turn ^= 1) {
     const bool two = paired(p, a, i);
     const float x = (float)scale_for(bound.x[i]);
     float t[3] = {};  // scales of what lies in the symmetric places
-    cudaError_t e = cudaSuccess;
     const auto sym = [&](int left, int right, int out, double top, float s2, float s1, float s0) {
-      if (e != cudaSuccess) return;
       const float scale = (float)scale_for(top);
-      e = launch_ortho_product(p, OrthoProduct{kSym, turn, left, right, out, s2, s1, s0, t[left], t[right], scale}, a, l, stream);
+      q[products++] = OrthoProduct{kSym, turn, left, right, out, s2, s1, s0, t[left], t[right], scale};
       t[out] = scale;
     };
     const auto square = [&](int from, int out, int step) {
@@ -324,22 +324,19 @@ cudaError_t launch_orthogonalize(const OrthoArgs& a, const TcLaunch& l, cudaStre
       sym(from, from, out, bound.c[step], k[2], k[1], k[0]);
     };
     t[0] = (float)scale_for(bound.x[i] * bound.x[i]);
-    e = launch_ortho_product(p, OrthoProduct{kGram, turn, 0, 0, 0, 1, 0, 0, x, x, t[0]}, a, l, stream);
+    q[products++] = OrthoProduct{kGram, turn, 0, 0, 0, 1, 0, 0, x, x, t[0]};
     square(0, 1, i);  // C
     if (two) {
-      sym(1, 0, 2, bound.c[i] * bound.x[i] * bound.x[i], 1, 0, 0);      // C A
-      sym(2, 1, 0, bound.x[i + 1] * bound.x[i + 1], 1, 0, 0);           // C A C: the next A
-      square(0, 2, i + 1);                                              // C'
-      sym(2, 1, 0, bound.c[i] * bound.c[i + 1], 1, 0, 0);               // C' C
+      sym(1, 0, 2, bound.c[i] * bound.x[i] * bound.x[i], 1, 0, 0);  // C A
+      sym(2, 1, 0, bound.x[i + 1] * bound.x[i + 1], 1, 0, 0);       // C A C: the next A
+      square(0, 2, i + 1);                                          // C'
+      sym(2, 1, 0, bound.c[i] * bound.c[i + 1], 1, 0, 0);           // C' C
     }
-    if (e != cudaSuccess) return e;
     i += two ? 2 : 1;
     const int by = two ? 0 : 1;
-    e = launch_ortho_product(
-        p, OrthoProduct{i < a.steps ? kUpdate : kLast, turn, by, 0, 0, 1, 0, 0, t[by], x, (float)scale_for(bound.x[i])}, a, l, stream);
-    if (e != cudaSuccess) return e;
+    q[products++] = OrthoProduct{i < a.steps ? kUpdate : kLast, turn, by, 0, 0, 1, 0, 0, t[by], x, (float)scale_for(bound.x[i])};
   }
-  return cudaSuccess;
+  return launch_ortho_products(p, q, products, a, l, stream);
 }
 
 }  // namespace tide

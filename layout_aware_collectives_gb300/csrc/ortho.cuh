@@ -52,10 +52,10 @@ struct OrthoTargets {
   uint16_t* p[kOrthoTable];
 };
 
-// One product of every matrix (ortho_tc.cu); the last form's results go to
-// the caller's matrices.
-cudaError_t launch_ortho_product(const OrthoPlan& p, const OrthoProduct& q, const OrthoArgs& a, const TcLaunch& l,
-                                 cudaStream_t stream);
+// The products in order (ortho_tc.cu); the last form's results go to the
+// caller's matrices.
+cudaError_t launch_ortho_products(const OrthoPlan& p, const OrthoProduct* q, int products, const OrthoArgs& a,
+                                  const TcLaunch& l, cudaStream_t stream);
 
 __device__ __forceinline__ float2 unpack_half(uint32_t v) { return __half22float2(*(const __half2*)&v); }
 

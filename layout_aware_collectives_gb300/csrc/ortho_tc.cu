@@ -18,6 +18,8 @@
 // is copied to shared memory while the elements before are at work, and what
 // they make of it goes out by way of the same place.  TMA does neither: each of
 // its copies here would stand behind the operands' large ones.
+#include <cmath>
+
 #include "ortho.cuh"
 #include "tc_device.cuh"
 #include "tc_host.h"
@@ -38,8 +40,10 @@ constexpr uint32_t kSlot = 2 * kBox;  // boxes of two planes
 constexpr int kSlots = 2;             // of a warp
 constexpr size_t kSmem = 1024 + kStages * kStage + kEpiWarps * kSlots * kSlot;
 
-struct Params {
-  CUtensorMap left, right;  // operands
+// One product, as the kernels take it.
+struct Phase {
+  int form;
+  int left, right;          // maps of the operands
   const __half* in[2];      // planes that are added: sym: left, right; update, last: X, hi and lo
   __half* out[2];           // gram, sym: the one; update: the next X, hi and lo
   int64_t ld;               // of those
@@ -48,20 +52,49 @@ struct Params {
   TileGrid grid;            // update, last
   Divisor each;             // gram, sym: tiles of a matrix
   int tiles;
-  int64_t first;            // matrix, of this launch
   const float *left_d, *right_d;  // diagonals
   float* out_d;
   float s2, s1, s0;
   float sum_scale, left_scale, right_scale, out_scale;  // factors of the sums, of `in`, of what is kept
   bool tall;
   int64_t ld_out;
+};
+
+// The operands that a step's products have.
+enum Map { kX0 = 0, kX1, kT0, kT1, kT2, kWideX0, kWideX1, kMaps };
+
+struct Limits {
   int* err;
   uint64_t limit_ns, stall_ns, late_ns;
 };
 
+struct Params {  // of one product of all matrices
+  CUtensorMap left, right;
+  Phase phase;
+  int64_t first;  // matrix, of this launch
+  Limits limits;
+};
+
+constexpr int kMaxPhases = 24;
+struct ChainParams {  // of all products of each matrix
+  CUtensorMap maps[kMaps];
+  Phase phase[kMaxPhases];
+  int phases;
+  int64_t first;
+  Limits limits;
+};
+
+// The pairs that share a phase's tiles, which of them this is, and the first
+// of their matrices.
+struct Team {
+  int pair, pairs;
+  int z0;
+  uint32_t rank;  // of this CTA in its pair
+};
+
 template <int FORM>
-__device__ __forceinline__ bool work_at(const Params& p, int pair, int pairs, int i, TileAt& r) {
-  const int t = pair + i * pairs;
+__device__ __forceinline__ bool work_at(const Phase& p, const Team& team, int i, TileAt& r) {
+  const int t = team.pair + i * team.pairs;
   if (t >= p.tiles) return false;
   if constexpr (FORM == kUpdate || FORM == kLast) {
     r = tile_at(p.grid, t);
@@ -74,7 +107,7 @@ __device__ __forceinline__ bool work_at(const Params& p, int pair, int pairs, in
     while ((n + 1) * (n + 2) / 2 <= q) ++n;
     r.n = n, r.m = q - n * (n + 1) / 2;
   }
-  r.z += (int)p.first;
+  r.z += team.z0;
   return true;
 }
 
@@ -161,11 +194,11 @@ struct Cursor {
   bool more;
 
   // The i-th tile, or the next that has a piece for this warp.
-  __device__ __forceinline__ void open(const Params& p, int pair, int pairs, int first, int half, uint32_t rank, int lanes) {
+  __device__ __forceinline__ void open(const Phase& p, const Team& team, int first, int half, int lanes) {
     for (i = first;; ++i) {
-      more = work_at<FORM>(p, pair, pairs, i, at);
+      more = work_at<FORM>(p, team, i, at);
       if (!more) return;
-      row0 = (at.m * 2 + (int)rank) * kHalf + lanes;
+      row0 = (at.m * 2 + (int)team.rank) * kHalf + lanes;
       col = at.n * 2 * kHalf + half * kHalf;
       left = row0 >= p.m || col >= p.wide ? 0 : min(4, (p.wide - col + 31) / 32);
       if (left) return;
@@ -194,8 +227,8 @@ struct Diagonals {
 
 // What becomes of 32 x 32 sums.
 template <int FORM>
-__device__ __forceinline__ void finish(const Params& p, const OrthoTargets& targets, const TileAt& t, int row0, int col,
-                                       int lane, uint32_t tmem, uint32_t slot, Diagonals d) {
+__device__ __forceinline__ void finish(const Phase& p, uint16_t* dst, const TileAt& t, int row0, int col, int lane,
+                                       uint32_t tmem, uint32_t slot, Diagonals d) {
   const int64_t z = (int64_t)t.z * p.m;
   uint32_t sums[2][16], a[2][8], b[2][8];
   tmem_rows(tmem, sums[0]);
@@ -251,7 +284,7 @@ __device__ __forceinline__ void finish(const Params& p, const OrthoTargets& targ
           float v = (r == c ? y0 : y1) / p.out_scale;
           if (row0 + r < p.m) {
             if constexpr (FORM == kSym) {
-              const float dl = p.left_d[z + row0 + r], dr = p.right_d[z + row0 + r];
+              const float dl = __ldcg(p.left_d + z + row0 + r), dr = __ldcg(p.right_d + z + row0 + r);
               v += fmaf(p.s2 * dl, dr, fmaf(p.s1, dl, p.s0));
             }
             p.out_d[z + row0 + r] = v;
@@ -280,7 +313,6 @@ __device__ __forceinline__ void finish(const Params& p, const OrthoTargets& targ
   }
   __syncwarp();
   if constexpr (FORM == kLast) {
-    uint16_t* dst = targets.p[t.z - p.first];
     if (p.tall)
       send_last(slot, dst + (int64_t)col * p.ld_out + row0, p.ld_out, p.wide - col, p.m - row0, lane);
     else
@@ -295,243 +327,420 @@ __device__ __forceinline__ void finish(const Params& p, const OrthoTargets& targ
   __syncwarp();
 }
 
-template <int FORM>
-__global__ void __launch_bounds__(kThreads, 1)
-    ortho_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ OrthoTargets targets) {
-  constexpr bool kBMn = FORM == kUpdate || FORM == kLast;
-  extern __shared__ uint8_t raw[];
-  __shared__ uint64_t bars[2 * kStages + 6];
-  __shared__ uint32_t tmem_at;
-  __shared__ int stop;
+// Barriers of a CTA.
+struct Bars {
+  uint32_t at;
+  __device__ __forceinline__ uint32_t full(int s) const { return at + 8u * s; }
+  __device__ __forceinline__ uint32_t empty(int s) const { return at + 8u * (kStages + s); }
+  __device__ __forceinline__ uint32_t sums_full(int b) const { return at + 8u * (2 * kStages + b); }
+  __device__ __forceinline__ uint32_t sums_empty(int b) const { return at + 8u * (2 * kStages + 2 + b); }
+  __device__ __forceinline__ uint32_t spare() const { return at + 8u * (2 * kStages + 4); }
+  __device__ __forceinline__ uint32_t silent() const { return at + 8u * (2 * kStages + 5); }
+};
+constexpr int kBars = 2 * kStages + 6;
 
-  const uint32_t smem = (smem_addr(raw) + 1023u) & ~1023u;
-  const uint32_t bar0 = smem_addr(bars);
-  const auto full = [&](int s) { return bar0 + 8u * s; };
-  const auto empty = [&](int s) { return bar0 + 8u * (kStages + s); };
-  const auto sums_full = [&](int b) { return bar0 + 8u * (2 * kStages + b); };
-  const auto sums_empty = [&](int b) { return bar0 + 8u * (2 * kStages + 2 + b); };
-  const uint32_t spare = bar0 + 8u * (2 * kStages + 4), silent = spare + 8;
-  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_rank();
-  const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
-  const Watch watch{&stop, p.err, p.limit_ns};
-  const bool late = p.late_ns && warp == 4;  // test: this warp waits for sums where nothing arrives
-  const Watch sums_watch{&stop, p.err, late ? p.late_ns : p.limit_ns};
-
+// What every form's kernel begins with; returns TMEM's address.
+__device__ __forceinline__ uint32_t set_up(const Bars& bars, int* stop, uint32_t* tmem_at, int warp) {
   if (threadIdx.x == 0) {
-    stop = 0;
-    for (int s = 0; s < kStages; ++s) bar_init(full(s), 1), bar_init(empty(s), 1);
-    for (int b = 0; b < 2; ++b) bar_init(sums_full(b), 1), bar_init(sums_empty(b), 2 * kEpiWarps);
-    bar_init(spare, 1), bar_init(silent, 1);
+    *stop = 0;
+    for (int s = 0; s < kStages; ++s) bar_init(bars.full(s), 1), bar_init(bars.empty(s), 1);
+    for (int b = 0; b < 2; ++b) bar_init(bars.sums_full(b), 1), bar_init(bars.sums_empty(b), 2 * kEpiWarps);
+    bar_init(bars.spare(), 1), bar_init(bars.silent(), 1);
     bar_init_fence();
-    prefetch_map(&p.left), prefetch_map(&p.right);
   }
-  if (warp == 2) tmem_alloc<2>(smem_addr(&tmem_at), 512);
+  if (warp == 2) tmem_alloc<2>(smem_addr(tmem_at), 512);
   fence_before();
   __syncthreads();
   cluster_sync();
   fence_after();
-  const uint32_t tmem = tmem_at;
+  return *tmem_at;
+}
+
+// One thread loads the left operand, another the right one.  j: stages
+// filled so far.  `leader`: the pair's first CTA's rank in the cluster.
+template <int FORM>
+__device__ __forceinline__ bool load_phase(const Phase& p, const CUtensorMap* map, const Team& team, bool left, uint32_t smem,
+                                           const Bars& bars, uint32_t leader, const Watch& watch, int& j) {
+  constexpr bool kBMn = FORM == kUpdate || FORM == kLast;
+  TileAt at;
+  for (int i = 0; work_at<FORM>(p, team, i, at); ++i) {
+    const int row = (at.m * 2 + team.rank) * kHalf, col = (at.n * 2 + team.rank) * kHalf;
+    for (int k = 0; k < p.steps; ++k, ++j) {
+      const int s = j % kStages;
+      if (j >= kStages && !bar_wait(bars.empty(s), (j / kStages + 1) & 1, watch)) return false;
+      if (left && team.rank == 0) bar_expect(bars.full(s), 2 * kStage);
+      const uint32_t bar = peer_addr(bars.full(s), leader);
+      const uint32_t a = smem + s * kStage, b = a + kOperand;
+      if (left)
+        load_box3<true>(a, map, k * kStep, row, at.z, bar);
+      else if (kBMn)
+        load_box4(b, map, 0, k * kStep, col / 64, at.z, bar);
+      else
+        load_box3<true>(b, map, k * kStep, col, at.z, bar);
+    }
+  }
+  return true;
+}
+// The MMAs' last arrivals reach this CTA while it is still there.  After a wait
+// that ran out: both CTAs' copies in flight, with a limit again; the peer's
+// memory stays until the cluster's last barrier.
+__device__ __forceinline__ void load_end(bool go, const Team& team, const Bars& bars, const Watch& watch, int j) {
+  for (int i = max(0, j - kStages); i < j && go; ++i) go = bar_wait(bars.empty(i % kStages), (i / kStages) & 1, watch);
+  if (!go && team.rank == 0)
+    for (int i = max(0, j - kStages); i < j; ++i) await(bars.full(i % kStages), (i / kStages) & 1, watch);
+}
+
+// j: stages used so far, done: tiles.  `ctas`: the pair's bits among the cluster's.
+template <int FORM>
+__device__ __forceinline__ bool mma_phase(const Phase& p, const Team& team, uint32_t smem, uint32_t tmem, const Bars& bars,
+                                          uint16_t ctas, const Watch& watch, int& j, int& done) {
+  constexpr bool kBMn = FORM == kUpdate || FORM == kLast;
+  constexpr uint32_t kInstr = instr_desc(0, 0, kBMn, 256, 256);  // fp16 operands
+  TileAt at;
+  for (int i = 0; work_at<FORM>(p, team, i, at); ++i, ++done) {
+    const int b = done & 1;
+    if (done >= 2 && !bar_wait<kPeer>(bars.sums_empty(b), (done / 2 + 1) & 1, watch)) return false;
+    fence_after();
+    for (int k = 0; k < p.steps; ++k, ++j) {
+      const int s = j % kStages;
+      if (!bar_wait(bars.full(s), (j / kStages) & 1, watch)) return false;
+      fence_after();
+      const uint32_t a = smem + s * kStage;
+      const uint64_t da = operand_desc(a, 16), db = operand_desc(a + kOperand, kBMn ? kOperand / 2 : 16);
+#pragma unroll
+      for (int q = 0; q < kStep / 16; ++q)
+        mma<2, false>(tmem + b * 256, da + q * (32 >> 4), db + q * ((kBMn ? 2048 : 32) >> 4), kInstr, k > 0 || q > 0);
+      mma_commit<2>(bars.empty(s), ctas);
+    }
+    mma_commit<2>(bars.sums_full(b), ctas);
+  }
+  return true;
+}
+
+template <int FORM>
+__device__ __forceinline__ bool finish_phase(const Phase& p, const OrthoTargets& targets, const Team& team, int64_t first,
+                                             uint32_t slots, uint32_t tmem, const Bars& bars, uint32_t leader, bool late,
+                                             const Watch& watch, int warp, int lane, int& done) {
+  const int half = warp >> 2, lanes = (warp & 3) * 32;
+  // Pieces in turn, slot by slot; `next` is the one whose copies go out.
+  constexpr bool kIn = FORM != kGram;
+  Cursor<FORM> now, next;
+  now.open(p, team, 0, half, lanes);
+  next = now;
+  int slot = 0;  // of the piece at hand, and of the next to be asked for
+  Diagonals d[kSlots];
+  const auto ask = [&](int to) {
+    if (kIn && next.more) {
+      Diagonals v{0.0f, 0.0f};
+      const int64_t z = (int64_t)next.at.z * p.m;
+      if (next.row0 + lane < p.m) v.di = __ldcg(p.left_d + z + next.row0 + lane);
+      if (FORM == kSym && next.col + lane < p.wide) v.dj = __ldcg(p.right_d + z + next.col + lane);
+#pragma unroll
+      for (int s = 0; s < kSlots; ++s)
+        if (s == to) d[s] = v;
+      for (int q = 0; q < p.planes; ++q)
+        ask_box(slots + to * kSlot + q * kBox, p.in[q] + (z + next.row0) * p.ld + next.col, p.ld, p.m - next.row0, lane);
+      next.col += 32;
+      if (--next.left == 0) next.open(p, team, next.i + 1, half, lanes);
+    }
+    if (kIn) asked();  // an empty group past the last, so that their number says which have arrived
+  };
+  for (int s = 0; s < kSlots; ++s) ask(s);
+  TileAt at;
+  bool go = true;
+  // every tile's sums are waited for and handed back, a piece of it here or not
+  for (int i = 0; work_at<FORM>(p, team, i, at); ++i, ++done) {
+    const int b = done & 1;
+    go = bar_wait_warp(late ? bars.silent() : bars.sums_full(b), (done / 2) & 1, watch);
+    if (!go) break;
+    fence_after();
+    while (now.more && now.i == i) {
+      if (kIn) arrived<kSlots - 1>();
+      const int c = (now.col - at.n * 2 * kHalf) / 32;
+      Diagonals mine{0.0f, 0.0f};
+#pragma unroll
+      for (int s = 0; s < kSlots; ++s)
+        if (kIn && s == slot) mine = d[s];
+      finish<FORM>(p, FORM == kLast ? targets.p[at.z - first] : nullptr, at, now.row0, now.col, lane,
+                   tmem + ((uint32_t)lanes << 16) + b * 256 + c * 32, slots + slot * kSlot, mine);
+      ask(slot);
+      slot = slot + 1 == kSlots ? 0 : slot + 1;
+      now.col += 32;
+      if (--now.left == 0) now.open(p, team, now.i + 1, half, lanes);
+    }
+    fence_before();
+    __syncwarp();
+    if (lane == 0) bar_arrive_peer(peer_addr(bars.sums_empty(b), leader));
+  }
+  if (kIn) arrived<0>();
+  return go;
+}
+
+// One product of all matrices, its tiles over all pairs.
+template <int FORM>
+__global__ void __launch_bounds__(kThreads, 1)
+    ortho_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ OrthoTargets targets) {
+  extern __shared__ uint8_t raw[];
+  __shared__ uint64_t bar_words[kBars];
+  __shared__ uint32_t tmem_at;
+  __shared__ int stop;
+  const uint32_t smem = (smem_addr(raw) + 1023u) & ~1023u;
+  const Bars bars{smem_addr(bar_words)};
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const Team team{(int)blockIdx.x / 2, (int)gridDim.x / 2, (int)p.first, cluster_rank()};
+  const Watch watch{&stop, p.limits.err, p.limits.limit_ns};
+  const bool late = p.limits.late_ns && warp == 4;  // test: this warp waits for sums where nothing arrives
+  if (threadIdx.x == 0) prefetch_map(&p.left), prefetch_map(&p.right);
+  const uint32_t tmem = set_up(bars, &stop, &tmem_at, warp);
   after_previous();
 
-  if (p.stall_ns) {  // test: a wait on a barrier nothing arrives on runs out
-    if (threadIdx.x == 0) bar_wait(silent, 0, Watch{&stop, p.err, p.stall_ns});
+  int j = 0, done = 0;
+  if (p.limits.stall_ns) {  // test: a wait on a barrier nothing arrives on runs out
+    if (threadIdx.x == 0) bar_wait(bars.silent(), 0, Watch{&stop, p.limits.err, p.limits.stall_ns});
   } else if (warp == 0 || warp == 3) {
-    // One thread loads the left operand, another the right one.
     if (elected()) {
       const bool left = warp == 0;
-      int j = 0;  // stages filled so far
-      bool go = true;
-      TileAt at;
-      for (int i = 0; go && work_at<FORM>(p, pair, pairs, i, at); ++i) {
-        const int row = (at.m * 2 + rank) * kHalf, col = (at.n * 2 + rank) * kHalf;
-        for (int k = 0; k < p.steps; ++k, ++j) {
-          const int s = j % kStages;
-          if (j >= kStages && !bar_wait(empty(s), (j / kStages + 1) & 1, watch)) {
-            go = false;
-            break;
-          }
-          if (left && rank == 0) bar_expect(full(s), 2 * kStage);
-          const uint32_t bar = peer_addr(full(s), 0);
-          const uint32_t a = smem + s * kStage, b = a + kOperand;
-          if (left)
-            load_box3<true>(a, &p.left, k * kStep, row, at.z, bar);
-          else if (kBMn)
-            load_box4(b, &p.right, 0, k * kStep, col / 64, at.z, bar);
-          else
-            load_box3<true>(b, &p.right, k * kStep, col, at.z, bar);
-        }
-      }
-      // the MMAs' last arrivals reach this CTA while it is still there
-      for (int i = max(0, j - kStages); i < j && go; ++i) go = bar_wait(empty(i % kStages), (i / kStages) & 1, watch);
-      // after a wait that ran out: both CTAs' copies in flight, with a limit
-      // again; the peer's memory stays until the cluster's last barrier
-      if (!go && rank == 0)
-        for (int i = max(0, j - kStages); i < j; ++i) await(full(i % kStages), (i / kStages) & 1, watch);
+      const bool go = load_phase<FORM>(p.phase, left ? &p.left : &p.right, team, left, smem, bars, 0, watch, j);
+      load_end(go, team, bars, watch, j);
     }
-  } else if (warp == 1 && rank == 0) {
+  } else if (warp == 1 && team.rank == 0) {
     if (elected()) {
-      constexpr uint32_t kInstr = instr_desc(0, 0, kBMn, 256, 256);  // fp16 operands
-      int j = 0;  // stages used
-      bool go = true;
-      TileAt at;
-      for (int i = 0; go && work_at<FORM>(p, pair, pairs, i, at); ++i) {
-        const int b = i & 1;
-        if (i >= 2 && !bar_wait<kPeer>(sums_empty(b), (i / 2 + 1) & 1, watch)) break;
-        fence_after();
-        for (int k = 0; k < p.steps; ++k, ++j) {
-          const int s = j % kStages;
-          if (!bar_wait(full(s), (j / kStages) & 1, watch)) {
-            go = false;
-            break;
-          }
-          fence_after();
-          const uint32_t a = smem + s * kStage;
-          const uint64_t da = operand_desc(a, 16), db = operand_desc(a + kOperand, kBMn ? kOperand / 2 : 16);
-#pragma unroll
-          for (int q = 0; q < kStep / 16; ++q)
-            mma<2, false>(tmem + b * 256, da + q * (32 >> 4), db + q * ((kBMn ? 2048 : 32) >> 4), kInstr, k > 0 || q > 0);
-          mma_commit<2>(empty(s));
-        }
-        if (go) mma_commit<2>(sums_full(b));
-      }
-      mma_commit<2>(spare, 1);
+      mma_phase<FORM>(p.phase, team, smem, tmem, bars, 3, watch, j, done);
+      mma_commit<2>(bars.spare(), 1);
     }
   } else if (warp >= 4) {
-    const int half = (warp - 4) >> 2, lanes = (warp & 3) * 32;
-    const uint32_t slot0 = smem + kStages * kStage + (warp - 4) * kSlots * kSlot;
-    // Pieces in turn, slot by slot; `next` is the one whose copies go out.
-    constexpr bool kIn = FORM != kGram;
-    Cursor<FORM> now, next;
-    now.open(p, pair, pairs, 0, half, rank, lanes);
-    next = now;
-    int slot = 0;  // of the piece at hand, and of the next to be asked for
-    Diagonals d[kSlots];
-    const auto ask = [&](int to) {
-      if (kIn && next.more) {
-        Diagonals v{0.0f, 0.0f};
-        const int64_t z = (int64_t)next.at.z * p.m;
-        if (next.row0 + lane < p.m) v.di = p.left_d[z + next.row0 + lane];
-        if (FORM == kSym && next.col + lane < p.wide) v.dj = p.right_d[z + next.col + lane];
-#pragma unroll
-        for (int s = 0; s < kSlots; ++s)
-          if (s == to) d[s] = v;
-        for (int q = 0; q < p.planes; ++q)
-          ask_box(slot0 + to * kSlot + q * kBox, p.in[q] + ((int64_t)next.at.z * p.m + next.row0) * p.ld + next.col, p.ld,
-                  p.m - next.row0, lane);
-        next.col += 32;
-        if (--next.left == 0) next.open(p, pair, pairs, next.i + 1, half, rank, lanes);
-      }
-      if (kIn) asked();  // an empty group past the last, so that their number says which have arrived
-    };
-    for (int s = 0; s < kSlots; ++s) ask(s);
-    TileAt at;
-    // every tile's sums are waited for and handed back, a piece of it here or not
-    for (int i = 0; work_at<FORM>(p, pair, pairs, i, at); ++i) {
-      const int b = i & 1;
-      if (!bar_wait_warp(late ? silent : sums_full(b), (i / 2) & 1, sums_watch)) break;
-      fence_after();
-      while (now.more && now.i == i) {
-        if (kIn) arrived<kSlots - 1>();
-        const int c = (now.col - at.n * 2 * kHalf) / 32;
-        Diagonals mine{0.0f, 0.0f};
-#pragma unroll
-        for (int s = 0; s < kSlots; ++s)
-          if (kIn && s == slot) mine = d[s];
-        finish<FORM>(p, targets, at, now.row0, now.col, lane, tmem + ((uint32_t)lanes << 16) + b * 256 + c * 32, slot0 + slot * kSlot, mine);
-        ask(slot);
-        slot = slot + 1 == kSlots ? 0 : slot + 1;
-        now.col += 32;
-        if (--now.left == 0) now.open(p, pair, pairs, now.i + 1, half, rank, lanes);
-      }
-      fence_before();
-      __syncwarp();
-      if (lane == 0) bar_arrive_peer(peer_addr(sums_empty(b), 0));
-    }
-    if (kIn) arrived<0>();
+    finish_phase<FORM>(p.phase, targets, team, p.first, smem + kStages * kStage + (warp - 4) * kSlots * kSlot, tmem, bars, 0, late,
+                       Watch{&stop, p.limits.err, late ? p.limits.late_ns : p.limits.limit_ns}, warp - 4, lane, done);
   }
   __syncthreads();
-  if (stop && warp == 1 && rank == 0 && !p.stall_ns) {
-    await(spare, 0, watch);  // the MMAs in flight
+  if (stop && warp == 1 && team.rank == 0 && !p.limits.stall_ns) {
+    await(bars.spare(), 0, watch);  // the MMAs in flight
     __syncwarp();
   }
   cluster_sync();
   if (warp == 2) tmem_free<2>(tmem, 512);
 }
 
-template <int FORM>
-cudaError_t launch(Params& p, const OrthoTargets& targets, const TcLaunch& l, cudaStream_t stream) {
-  p.err = l.err;
-  p.limit_ns = TIDE_BULK_TIMEOUT_NS;
-  p.stall_ns = l.stall_ns, p.late_ns = l.late_ns;
-  const int pairs = p.tiles < l.dev->pairs ? p.tiles : l.dev->pairs;
-  return launch_early(ortho_tc_kernel<FORM>, dim3(2 * pairs), kThreads, kSmem, 2, stream, p, targets);
+// All products of one matrix by a cluster of one to four pairs, which meet
+// between two products: what a launch, its set-up and its last tiles cost is
+// paid once, and a matrix's planes stay in L2 from one product to the next.
+__global__ void __launch_bounds__(kThreads, 1)
+    ortho_chain_kernel(const __grid_constant__ ChainParams p, const __grid_constant__ OrthoTargets targets) {
+  extern __shared__ uint8_t raw[];
+  __shared__ uint64_t bar_words[kBars];
+  __shared__ uint32_t tmem_at;
+  __shared__ int stop, ended_at;  // the phase that a wait ran out in
+  const uint32_t smem = (smem_addr(raw) + 1023u) & ~1023u;
+  const Bars bars{smem_addr(bar_words)};
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const uint32_t cta = cluster_rank(), leader = cta & ~1u;
+  uint32_t ctas;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
+  const uint16_t both = (uint16_t)(3u << leader);
+  const Team team{(int)cta / 2, (int)ctas / 2, (int)(p.first + blockIdx.x / ctas), cta & 1};
+  const Watch watch{&stop, p.limits.err, p.limits.limit_ns};
+  const bool late = p.limits.late_ns && warp == 4;
+  const Watch sums_watch{&stop, p.limits.err, late ? p.limits.late_ns : p.limits.limit_ns};
+  const uint32_t slots = smem + kStages * kStage + (warp - 4) * kSlots * kSlot;
+  if (threadIdx.x == 0) ended_at = INT32_MAX;
+  if (threadIdx.x < kMaps) prefetch_map(&p.maps[threadIdx.x]);
+  const uint32_t tmem = set_up(bars, &stop, &tmem_at, warp);
+  after_previous();
+
+  int j = 0, done = 0;
+  bool go = true, ended = false;
+  if (p.limits.stall_ns && threadIdx.x == 0) bar_wait(bars.silent(), 0, Watch{&stop, p.limits.err, p.limits.stall_ns});
+  const int phases = p.limits.stall_ns ? 0 : p.phases;
+  for (int n = 0; n < phases; ++n) {
+    const Phase& f = p.phase[n];
+    if (warp == 0 || warp == 3) {
+      if (elected()) {
+        async_proxy_fence();  // what others wrote, before copies of it
+        const bool left = warp == 0;
+        const CUtensorMap* map = &p.maps[left ? f.left : f.right];
+        if (f.form == kGram)
+          go = load_phase<kGram>(f, map, team, left, smem, bars, leader, watch, j);
+        else if (f.form == kSym)
+          go = load_phase<kSym>(f, map, team, left, smem, bars, leader, watch, j);
+        else
+          go = load_phase<kUpdate>(f, map, team, left, smem, bars, leader, watch, j);
+        if (!go || n == phases - 1) load_end(go, team, bars, watch, j);
+      }
+    } else if (warp == 1 && team.rank == 0) {
+      if (elected()) {
+        if (f.form == kGram)
+          go = mma_phase<kGram>(f, team, smem, tmem, bars, both, watch, j, done);
+        else if (f.form == kSym)
+          go = mma_phase<kSym>(f, team, smem, tmem, bars, both, watch, j, done);
+        else
+          go = mma_phase<kUpdate>(f, team, smem, tmem, bars, both, watch, j, done);
+      }
+    } else if (warp >= 4) {
+      if (f.form == kGram)
+        finish_phase<kGram>(f, targets, team, p.first, slots, tmem, bars, leader, late, sums_watch, warp - 4, lane, done);
+      else if (f.form == kSym)
+        finish_phase<kSym>(f, targets, team, p.first, slots, tmem, bars, leader, late, sums_watch, warp - 4, lane, done);
+      else if (f.form == kUpdate)
+        finish_phase<kUpdate>(f, targets, team, p.first, slots, tmem, bars, leader, late, sums_watch, warp - 4, lane, done);
+      else
+        finish_phase<kLast>(f, targets, team, p.first, slots, tmem, bars, leader, late, sums_watch, warp - 4, lane, done);
+      async_proxy_fence();  // these results, before others' copies of them
+    }
+    __syncthreads();
+    // A wait that ran out ends all of the cluster at this phase: who tells the
+    // others does so before they meet, and one that is a phase ahead names its own.
+    if (stop && threadIdx.x < ctas) peer_write(peer_addr(smem_addr(&ended_at), threadIdx.x), n);
+    cluster_sync();
+    ended = *(volatile int*)&ended_at <= n;
+    if (ended) break;
+  }
+  if (ended) {  // copies and MMAs in flight
+    if (warp == 0 || warp == 3) {
+      if (elected() && go) load_end(false, team, bars, watch, j);
+    } else if (warp == 1 && team.rank == 0) {
+      if (elected()) mma_commit<2>(bars.spare(), (uint16_t)(1u << leader));
+      __syncwarp();
+      await(bars.spare(), 0, watch);
+    }
+  }
+  __syncwarp();
+  cluster_sync();
+  if (warp == 2) tmem_free<2>(tmem, 512);
 }
 
 bool map_k(CUtensorMap* map, const __half* plane, int64_t cols, const OrthoPlan& p, int64_t ld) {
   return make_stack_map(map, plane, cols, p.m, p.count, ld, kStep, kHalf, CU_TENSOR_MAP_SWIZZLE_128B);
 }
+bool map_of(CUtensorMap* map, int which, const OrthoPlan& p) {
+  if (which <= kX1) return map_k(map, p.x[which - kX0][0], p.n, p, p.ld_x);
+  if (which <= kT2) return map_k(map, p.t[which - kT0], p.m, p, p.ld_a);
+  return make_slab_stack_map(map, p.x[which - kWideX0][0], p.m, p.count, p.ld_x, kStep);
+}
+
+Limits limits_of(const TcLaunch& l) { return Limits{l.err, TIDE_BULK_TIMEOUT_NS, l.stall_ns, l.late_ns}; }
+
+// A product, but for how many tiles there are.
+Phase phase_of(const OrthoPlan& p, const OrthoProduct& q, int64_t ld_dst) {
+  Phase k{};
+  const bool update = q.form >= kUpdate;
+  const int64_t down = ceil_div(p.m, 2 * kHalf), across = ceil_div(p.n, 2 * kHalf);
+  k.form = q.form;
+  k.left = q.form == kGram ? kX0 + q.turn : kT0 + q.left;
+  k.right = q.form == kGram ? k.left : q.form == kSym ? kT0 + q.right : kWideX0 + q.turn;
+  k.m = p.m, k.wide = update ? p.n : p.m;
+  k.steps = (int)ceil_div(q.form == kGram ? p.n : p.m, kStep);
+  k.planes = q.form == kGram ? 0 : q.form == kSym && q.left == q.right ? 1 : 2;
+  k.in[0] = update ? p.x[q.turn][0] : p.t[q.left], k.in[1] = update ? p.x[q.turn][1] : p.t[q.right];
+  k.out[0] = update ? p.x[q.turn ^ 1][0] : p.t[q.out], k.out[1] = p.x[q.turn ^ 1][1];
+  k.ld = update ? p.ld_x : p.ld_a;
+  k.left_d = p.d[q.left], k.right_d = p.d[q.right], k.out_d = p.d[q.out];
+  k.s2 = q.s2, k.s1 = q.s1, k.s0 = q.s0;
+  k.sum_scale = 1.0f / (q.left_scale * q.right_scale);
+  k.left_scale = 1.0f / q.left_scale, k.right_scale = 1.0f / q.right_scale;
+  k.out_scale = q.form == kLast ? 1.0f : q.out_scale;
+  k.tall = p.tall, k.ld_out = ld_dst;
+  if (update)
+    k.grid = TileGrid((int)down, (int)across);
+  else
+    k.each = Divisor((int)(down * (down + 1) / 2));
+  return k;
+}
+int64_t tiles_of(const Phase& k) { return k.form >= kUpdate ? k.grid.all.d : k.each.d; }
+
+cudaError_t launch_product(const OrthoPlan& p, const OrthoProduct& q, const OrthoArgs& a, const TcLaunch& l, cudaStream_t stream) {
+  Params k{};
+  OrthoTargets targets{};
+  k.phase = phase_of(p, q, a.ld_dst);
+  k.limits = limits_of(l);
+  if (!map_of(&k.left, k.phase.left, p) || !map_of(&k.right, k.phase.right, p)) return cudaErrorInvalidValue;
+  // as many matrices as a launch counts tiles, and the last form's table holds
+  const int64_t each = tiles_of(k.phase);
+  int64_t most = INT32_MAX / 2 / each;
+  if (most < 1) return cudaErrorInvalidValue;
+  if (q.form == kLast && most > kOrthoTable) most = kOrthoTable;
+  for (k.first = 0; k.first < p.count; k.first += most) {
+    const int64_t some = p.count - k.first < most ? p.count - k.first : most;
+    k.phase.tiles = (int)(some * each);
+    if (q.form == kLast)
+      for (int64_t i = 0; i < some; ++i) targets.p[i] = a.dst[k.first + i];
+    const int pairs = k.phase.tiles < l.dev->pairs ? k.phase.tiles : l.dev->pairs;
+    const auto kernel = q.form == kGram     ? ortho_tc_kernel<kGram>
+                        : q.form == kSym    ? ortho_tc_kernel<kSym>
+                        : q.form == kUpdate ? ortho_tc_kernel<kUpdate>
+                                            : ortho_tc_kernel<kLast>;
+    const cudaError_t e = launch_early(kernel, dim3(2 * pairs), kThreads, kSmem, 2, stream, k, targets);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+cudaError_t launch_chain(const OrthoPlan& p, const OrthoProduct* q, int products, int pairs, const OrthoArgs& a, const TcLaunch& l,
+                         cudaStream_t stream) {
+  ChainParams k{};
+  OrthoTargets targets{};
+  k.phases = products;
+  k.limits = limits_of(l);
+  for (int i = 0; i < products; ++i) {
+    k.phase[i] = phase_of(p, q[i], a.ld_dst);
+    k.phase[i].tiles = (int)tiles_of(k.phase[i]);
+  }
+  for (int i = 0; i < kMaps; ++i)
+    if (!map_of(&k.maps[i], i, p)) return cudaErrorInvalidValue;
+  for (k.first = 0; k.first < p.count; k.first += kOrthoTable) {
+    const int64_t some = p.count - k.first < kOrthoTable ? p.count - k.first : kOrthoTable;
+    for (int64_t i = 0; i < some; ++i) targets.p[i] = a.dst[k.first + i];
+    const cudaError_t e = launch_early(ortho_chain_kernel, dim3((unsigned)(2 * pairs * some)), kThreads, kSmem, 2 * pairs, stream, k, targets);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+// Pairs of a cluster for each matrix, or 0: every product by all pairs.  By
+// the time that each way takes, in stages (0.27 us): a tile's sum and, as far as it
+// does not hide behind the next one's, its way out; what a product or a meeting
+// of the cluster costs besides.
+int chain_pairs(const OrthoPlan& p, const OrthoProduct* q, int products, const TcDevice& dev) {
+  if (products > kMaxPhases) return 0;
+  constexpr double kOut = 12, kLaunch = 24, kMeet = 14;
+  const auto turns = [](int64_t tiles, int64_t pairs) { return (double)ceil_div(tiles, pairs); };
+  double least = 0;
+  int best = 0;
+  for (int i = 0; i < products; ++i) {
+    const Phase f = phase_of(p, q[i], 0);
+    least += turns(p.count * tiles_of(f), dev.pairs) * std::fmax(f.steps, kOut) + kOut + kLaunch;
+  }
+  for (int pairs = 1; pairs <= kMaxSplit; ++pairs) {
+    const int held = pairs == 1 ? dev.pairs : dev.ortho.held[pairs];
+    if (held < 1) continue;
+    double each = 0;
+    for (int i = 0; i < products; ++i) {
+      const Phase f = phase_of(p, q[i], 0);
+      each += turns(tiles_of(f), pairs) * std::fmax(f.steps, kOut) + kOut + kMeet;
+    }
+    const double all = turns(p.count, held) * each + kLaunch;
+    if (all < least) least = all, best = pairs;
+  }
+  return best;
+}
+
 }  // namespace
 
-cudaError_t ortho_prepare(TcDevice*) {
+cudaError_t ortho_prepare(TcDevice* dev) {
   void (*const kernels[])(Params, OrthoTargets) = {ortho_tc_kernel<kGram>, ortho_tc_kernel<kSym>, ortho_tc_kernel<kUpdate>,
                                                    ortho_tc_kernel<kLast>};
   for (auto k : kernels) {
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e != cudaSuccess) return e;
   }
-  return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(ortho_chain_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  return e != cudaSuccess ? e : dev->ortho.prepare((const void*)ortho_chain_kernel, kThreads, kSmem);
 }
 
-cudaError_t launch_ortho_product(const OrthoPlan& p, const OrthoProduct& q, const OrthoArgs& a, const TcLaunch& l,
-                                 cudaStream_t stream) {
-  Params k{};
-  OrthoTargets targets{};
-  __half *const *x = p.x[q.turn], *const *next = p.x[q.turn ^ 1];
-  const bool update = q.form >= kUpdate;
-  const int64_t down = ceil_div(p.m, 2 * kHalf), across = ceil_div(p.n, 2 * kHalf);
-  k.m = p.m, k.wide = update ? p.n : p.m;
-  k.steps = (int)ceil_div(q.form == kGram ? p.n : p.m, kStep);
-  k.left_d = p.d[q.left], k.right_d = p.d[q.right], k.out_d = p.d[q.out];
-  k.s2 = q.s2, k.s1 = q.s1, k.s0 = q.s0;
-  k.sum_scale = 1.0f / (q.left_scale * q.right_scale);
-  k.left_scale = 1.0f / q.left_scale, k.right_scale = 1.0f / q.right_scale;
-  k.out_scale = q.form == kLast ? 1.0f : q.out_scale;
-  k.tall = p.tall, k.ld_out = a.ld_dst;
-  bool ok = true;
-  k.ld = update ? p.ld_x : p.ld_a;
-  if (q.form == kGram) {
-    ok = map_k(&k.left, x[0], p.n, p, p.ld_x);
-    k.right = k.left;
-  } else if (q.form == kSym) {
-    ok = map_k(&k.left, p.t[q.left], p.m, p, p.ld_a) && map_k(&k.right, p.t[q.right], p.m, p, p.ld_a);
-    k.planes = q.left == q.right ? 1 : 2;
-    k.in[0] = p.t[q.left], k.in[1] = p.t[q.right];
-  } else {
-    ok = map_k(&k.left, p.t[q.left], p.m, p, p.ld_a) && make_slab_stack_map(&k.right, x[0], p.m, p.count, p.ld_x, kStep);
-    k.planes = 2;
-    k.in[0] = x[0], k.in[1] = x[1];
-  }
-  k.out[0] = update ? next[0] : p.t[q.out], k.out[1] = next[1];
-  if (!ok) return cudaErrorInvalidValue;
-  const int64_t each = update ? down * across : down * (down + 1) / 2;
-  // as many matrices as a launch counts tiles, and the last form's table holds
-  int64_t most = INT32_MAX / 2 / each;
-  if (most < 1) return cudaErrorInvalidValue;
-  if (q.form == kLast && most > kOrthoTable) most = kOrthoTable;
-  for (k.first = 0; k.first < p.count; k.first += most) {
-    const int64_t some = p.count - k.first < most ? p.count - k.first : most;
-    k.tiles = (int)(some * each);
-    if (update)
-      k.grid = TileGrid((int)down, (int)across);
-    else
-      k.each = Divisor((int)each);
-    if (q.form == kLast)
-      for (int64_t i = 0; i < some; ++i) targets.p[i] = a.dst[k.first + i];
-    const cudaError_t e = q.form == kGram     ? launch<kGram>(k, targets, l, stream)
-                          : q.form == kSym    ? launch<kSym>(k, targets, l, stream)
-                          : q.form == kUpdate ? launch<kUpdate>(k, targets, l, stream)
-                                              : launch<kLast>(k, targets, l, stream);
+cudaError_t launch_ortho_products(const OrthoPlan& p, const OrthoProduct* q, int products, const OrthoArgs& a, const TcLaunch& l,
+                                  cudaStream_t stream) {
+  if (const int pairs = chain_pairs(p, q, products, *l.dev)) return launch_chain(p, q, products, pairs, a, l, stream);
+  for (int i = 0; i < products; ++i) {
+    const cudaError_t e = launch_product(p, q[i], a, l, stream);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

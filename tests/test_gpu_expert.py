@@ -499,3 +499,21 @@ def test_expert_layer_step(compute):
         assert float((got.double() - want.detach()).norm()) <= roundings * ref.U_BF16 * float(want.detach().norm())
     for o, grad in zip(outs, [*dwg, *dwu]):
         near(o, grad)
+
+
+@pytest.mark.parametrize("count,rows,cols", [(1, 100, 200), (3, 700, 1100), (1, 1500, 4000), (100, 300, 600)])
+def test_orthogonalize_waits_that_run_out_are_reported(count, rows, cols):
+    """Nothing arrives, or one warp of each CTA gives up: the call ends, is reported, and the next one is right."""
+    grads = gradients(gen(count), count, rows, cols, "fp32")
+    with tide.Compute() as c:
+        want = [v.clone() for v in orthogonalized(c, grads)]
+        c.check_device()
+        for hook in (c.set_test_stall, c.set_test_late_warp):
+            hook(1_000_000)
+            orthogonalized(c, grads)
+            with pytest.raises(tide.TideError) as e:
+                c.check_device()
+            assert e.value.status == tide.TIDE_ERR_TIMEOUT
+            hook(0)
+            assert all(torch.equal(a, b) for a, b in zip(orthogonalized(c, grads), want))
+            c.check_device()
