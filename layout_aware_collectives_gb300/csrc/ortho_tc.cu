@@ -7,9 +7,10 @@
 // What gram and sym make is symmetric: only tiles on and above the diagonal
 // are summed, and written to both places.
 //
-// As in the gated block, a pair of CTAs works on one 256 x 256 tile: each
-// loads 128 rows of the left operand and half of the right one's columns, one
-// MMA instruction of the pair reads both halves.  Warps 0 and 3 load (5 stages
+// As in the gated block, a pair of CTAs works on one tile of 256 rows and 256
+// columns (or 128 or 64, where there are few tiles): each loads 128 rows of the
+// left operand and half of the right one's columns, one MMA instruction of the
+// pair reads both halves.  Warps 0 and 3 load (5 stages
 // of 32 KiB), warp 1 of the pair's first CTA issues the MMAs, warps from 4 on
 // read finished sums out of TMEM, which holds two accumulators so that they do
 // so while the next tile is summed.
@@ -49,6 +50,7 @@ struct Phase {
   int64_t ld;               // of those
   int m, wide, steps;       // rows and columns of the result, stages of a tile's sum
   int planes;               // of `in`
+  int width;                // columns of a tile
   TileGrid grid;            // update, last
   Divisor each;             // gram, sym: tiles of a matrix
   int tiles;
@@ -60,8 +62,9 @@ struct Phase {
   int64_t ld_out;
 };
 
-// The operands that a step's products have.
-enum Map { kX0 = 0, kX1, kT0, kT1, kT2, kWideX0, kWideX1, kMaps };
+// The operands that products have: left ones of gram, sym and update, right
+// ones of gram, sym and update.
+enum Map { kLeftX = 0, kLeftT = 2, kRightX = 5, kRightT = 7, kWideX = 10, kMaps = 12 };
 
 struct Limits {
   int* err;
@@ -99,13 +102,16 @@ __device__ __forceinline__ bool work_at(const Phase& p, const Team& team, int i,
   if constexpr (FORM == kUpdate || FORM == kLast) {
     r = tile_at(p.grid, t);
   } else {
-    // down the columns of the triangle m <= n
+    // Down the columns: the tiles of rows up to the diagonal's.  `across`
+    // columns of tiles end at the same row.
+    const int across = 2 * kHalf / p.width;
     r.z = p.each.of(t);
     const int q = t - r.z * p.each.d;
-    int n = (int)((sqrtf(8.0f * (float)q + 1.0f) - 1.0f) * 0.5f);
-    while (n * (n + 1) / 2 > q) --n;
-    while ((n + 1) * (n + 2) / 2 <= q) ++n;
-    r.n = n, r.m = q - n * (n + 1) / 2;
+    int n = (int)((sqrtf(8.0f * (float)(q / across) + 1.0f) - 1.0f) * 0.5f);
+    while (across * (n * (n + 1) / 2) > q) --n;
+    while (across * ((n + 1) * (n + 2) / 2) <= q) ++n;
+    const int rest = q - across * (n * (n + 1) / 2);
+    r.n = n * across + rest / (n + 1), r.m = rest % (n + 1);
   }
   r.z += team.z0;
   return true;
@@ -199,8 +205,8 @@ struct Cursor {
       more = work_at<FORM>(p, team, i, at);
       if (!more) return;
       row0 = (at.m * 2 + (int)team.rank) * kHalf + lanes;
-      col = at.n * 2 * kHalf + half * kHalf;
-      left = row0 >= p.m || col >= p.wide ? 0 : min(4, (p.wide - col + 31) / 32);
+      col = at.n * p.width + half * (p.width / 2);
+      left = row0 >= p.m || col >= p.wide ? 0 : min(p.width / 64, (p.wide - col + 31) / 32);
       if (left) return;
     }
   }
@@ -256,7 +262,8 @@ __device__ __forceinline__ void finish(const Phase& p, uint16_t* dst, const Tile
   } else if constexpr (FORM != kGram) {
     by_row = d.di * p.right_scale * p.out_scale;
   }
-  const bool diagonal = (FORM == kGram || FORM == kSym) && t.m == t.n && row0 == col;
+  const bool upper = t.n * p.width / (2 * kHalf) != t.m;  // above the diagonal's tiles
+  const bool diagonal = (FORM == kGram || FORM == kSym) && !upper && row0 == col;
   tmem_arrived(sums[0]);
   tmem_arrived(sums[1]);
   __syncwarp();  // every lane has its part of the slot
@@ -308,7 +315,7 @@ __device__ __forceinline__ void finish(const Phase& p, uint16_t* dst, const Tile
       put_rows(slot, q * 16, lane, hi);
       if constexpr (FORM == kUpdate) put_rows(slot + kBox, q * 16, lane, lo);
       if constexpr (FORM == kGram || FORM == kSym)
-        if (t.m != t.n) put_turned(slot + kBox, q * 16, lane, hi);
+        if (upper) put_turned(slot + kBox, q * 16, lane, hi);
     }
   }
   __syncwarp();
@@ -321,7 +328,7 @@ __device__ __forceinline__ void finish(const Phase& p, uint16_t* dst, const Tile
     send_box(slot, p.out[0] + (z + row0) * p.ld + col, p.ld, p.m - row0, lane);
     if constexpr (FORM == kUpdate)
       send_box(slot + kBox, p.out[1] + (z + row0) * p.ld + col, p.ld, p.m - row0, lane);
-    else if (t.m != t.n)
+    else if (upper)
       send_box(slot + kBox, p.out[0] + (z + col) * p.ld + row0, p.ld, p.m - col, lane);
   }
   __syncwarp();
@@ -364,11 +371,11 @@ __device__ __forceinline__ bool load_phase(const Phase& p, const CUtensorMap* ma
   constexpr bool kBMn = FORM == kUpdate || FORM == kLast;
   TileAt at;
   for (int i = 0; work_at<FORM>(p, team, i, at); ++i) {
-    const int row = (at.m * 2 + team.rank) * kHalf, col = (at.n * 2 + team.rank) * kHalf;
+    const int row = (at.m * 2 + team.rank) * kHalf, col = at.n * p.width + (int)team.rank * (p.width / 2);
     for (int k = 0; k < p.steps; ++k, ++j) {
       const int s = j % kStages;
       if (j >= kStages && !bar_wait(bars.empty(s), (j / kStages + 1) & 1, watch)) return false;
-      if (left && team.rank == 0) bar_expect(bars.full(s), 2 * kStage);
+      if (left && team.rank == 0) bar_expect(bars.full(s), 2 * kOperand + p.width * (kStep * 2));
       const uint32_t bar = peer_addr(bars.full(s), leader);
       const uint32_t a = smem + s * kStage, b = a + kOperand;
       if (left)
@@ -395,7 +402,7 @@ template <int FORM>
 __device__ __forceinline__ bool mma_phase(const Phase& p, const Team& team, uint32_t smem, uint32_t tmem, const Bars& bars,
                                           uint16_t ctas, const Watch& watch, int& j, int& done) {
   constexpr bool kBMn = FORM == kUpdate || FORM == kLast;
-  constexpr uint32_t kInstr = instr_desc(0, 0, kBMn, 256, 256);  // fp16 operands
+  const uint32_t instr = instr_desc(0, 0, kBMn, 256, 0) | (uint32_t)(p.width >> 3) << 17;  // fp16 operands
   TileAt at;
   for (int i = 0; work_at<FORM>(p, team, i, at); ++i, ++done) {
     const int b = done & 1;
@@ -409,7 +416,7 @@ __device__ __forceinline__ bool mma_phase(const Phase& p, const Team& team, uint
       const uint64_t da = operand_desc(a, 16), db = operand_desc(a + kOperand, kBMn ? kOperand / 2 : 16);
 #pragma unroll
       for (int q = 0; q < kStep / 16; ++q)
-        mma<2, false>(tmem + b * 256, da + q * (32 >> 4), db + q * ((kBMn ? 2048 : 32) >> 4), kInstr, k > 0 || q > 0);
+        mma<2, false>(tmem + b * 256, da + q * (32 >> 4), db + q * ((kBMn ? 2048 : 32) >> 4), instr, k > 0 || q > 0);
       mma_commit<2>(bars.empty(s), ctas);
     }
     mma_commit<2>(bars.sums_full(b), ctas);
@@ -456,7 +463,7 @@ __device__ __forceinline__ bool finish_phase(const Phase& p, const OrthoTargets&
     fence_after();
     while (now.more && now.i == i) {
       if (kIn) arrived<kSlots - 1>();
-      const int c = (now.col - at.n * 2 * kHalf) / 32;
+      const int c = (now.col - at.n * p.width) / 32;
       Diagonals mine{0.0f, 0.0f};
 #pragma unroll
       for (int s = 0; s < kSlots; ++s)
@@ -608,25 +615,39 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 2) tmem_free<2>(tmem, 512);
 }
 
-bool map_k(CUtensorMap* map, const __half* plane, int64_t cols, const OrthoPlan& p, int64_t ld) {
-  return make_stack_map(map, plane, cols, p.m, p.count, ld, kStep, kHalf, CU_TENSOR_MAP_SWIZZLE_128B);
-}
-bool map_of(CUtensorMap* map, int which, const OrthoPlan& p) {
-  if (which <= kX1) return map_k(map, p.x[which - kX0][0], p.n, p, p.ld_x);
-  if (which <= kT2) return map_k(map, p.t[which - kT0], p.m, p, p.ld_a);
-  return make_slab_stack_map(map, p.x[which - kWideX0][0], p.m, p.count, p.ld_x, kStep);
+// Columns of the tiles of each form.
+struct Widths {
+  int gram, sym, update;
+  int of(int form) const { return form == kGram ? gram : form == kSym ? sym : update; }
+};
+
+bool map_of(CUtensorMap* map, int which, const OrthoPlan& p, const Widths& w) {
+  const auto k = [&](const __half* plane, int64_t cols, int64_t ld, int rows) {
+    return make_stack_map(map, plane, cols, p.m, p.count, ld, kStep, rows, CU_TENSOR_MAP_SWIZZLE_128B);
+  };
+  if (which < kLeftT) return k(p.x[which - kLeftX][0], p.n, p.ld_x, kHalf);
+  if (which < kRightX) return k(p.t[which - kLeftT], p.m, p.ld_a, kHalf);
+  if (which < kRightT) return k(p.x[which - kRightX][0], p.n, p.ld_x, w.gram / 2);
+  if (which < kWideX) return k(p.t[which - kRightT], p.m, p.ld_a, w.sym / 2);
+  return make_slab_stack_map(map, p.x[which - kWideX][0], p.m, p.count, p.ld_x, kStep, w.update / 128);
 }
 
 Limits limits_of(const TcLaunch& l) { return Limits{l.err, TIDE_BULK_TIMEOUT_NS, l.stall_ns, l.late_ns}; }
 
+// Tiles on and above the diagonal of [m, m].
+int64_t triangle(int64_t m, int64_t width) {
+  const int64_t across = 2 * kHalf / width, columns = ceil_div(m, width), whole = columns / across, rest = columns % across;
+  return across * (whole * (whole + 1) / 2) + rest * (whole + 1);
+}
+
 // A product, but for how many tiles there are.
-Phase phase_of(const OrthoPlan& p, const OrthoProduct& q, int64_t ld_dst) {
+Phase phase_of(const OrthoPlan& p, const OrthoProduct& q, const Widths& w, int64_t ld_dst) {
   Phase k{};
   const bool update = q.form >= kUpdate;
-  const int64_t down = ceil_div(p.m, 2 * kHalf), across = ceil_div(p.n, 2 * kHalf);
+  k.width = w.of(q.form);
   k.form = q.form;
-  k.left = q.form == kGram ? kX0 + q.turn : kT0 + q.left;
-  k.right = q.form == kGram ? k.left : q.form == kSym ? kT0 + q.right : kWideX0 + q.turn;
+  k.left = q.form == kGram ? kLeftX + q.turn : kLeftT + q.left;
+  k.right = q.form == kGram ? kRightX + q.turn : q.form == kSym ? kRightT + q.right : kWideX + q.turn;
   k.m = p.m, k.wide = update ? p.n : p.m;
   k.steps = (int)ceil_div(q.form == kGram ? p.n : p.m, kStep);
   k.planes = q.form == kGram ? 0 : q.form == kSym && q.left == q.right ? 1 : 2;
@@ -640,19 +661,20 @@ Phase phase_of(const OrthoPlan& p, const OrthoProduct& q, int64_t ld_dst) {
   k.out_scale = q.form == kLast ? 1.0f : q.out_scale;
   k.tall = p.tall, k.ld_out = ld_dst;
   if (update)
-    k.grid = TileGrid((int)down, (int)across);
+    k.grid = TileGrid((int)ceil_div(p.m, 2 * kHalf), (int)ceil_div(p.n, k.width));
   else
-    k.each = Divisor((int)(down * (down + 1) / 2));
+    k.each = Divisor((int)triangle(p.m, k.width));
   return k;
 }
 int64_t tiles_of(const Phase& k) { return k.form >= kUpdate ? k.grid.all.d : k.each.d; }
 
-cudaError_t launch_product(const OrthoPlan& p, const OrthoProduct& q, const OrthoArgs& a, const TcLaunch& l, cudaStream_t stream) {
+cudaError_t launch_product(const OrthoPlan& p, const OrthoProduct& q, const Widths& w, const OrthoArgs& a, const TcLaunch& l,
+                           cudaStream_t stream) {
   Params k{};
   OrthoTargets targets{};
-  k.phase = phase_of(p, q, a.ld_dst);
+  k.phase = phase_of(p, q, w, a.ld_dst);
   k.limits = limits_of(l);
-  if (!map_of(&k.left, k.phase.left, p) || !map_of(&k.right, k.phase.right, p)) return cudaErrorInvalidValue;
+  if (!map_of(&k.left, k.phase.left, p, w) || !map_of(&k.right, k.phase.right, p, w)) return cudaErrorInvalidValue;
   // as many matrices as a launch counts tiles, and the last form's table holds
   const int64_t each = tiles_of(k.phase);
   int64_t most = INT32_MAX / 2 / each;
@@ -674,18 +696,18 @@ cudaError_t launch_product(const OrthoPlan& p, const OrthoProduct& q, const Orth
   return cudaSuccess;
 }
 
-cudaError_t launch_chain(const OrthoPlan& p, const OrthoProduct* q, int products, int pairs, const OrthoArgs& a, const TcLaunch& l,
-                         cudaStream_t stream) {
+cudaError_t launch_chain(const OrthoPlan& p, const OrthoProduct* q, int products, const Widths& w, int pairs, const OrthoArgs& a,
+                         const TcLaunch& l, cudaStream_t stream) {
   ChainParams k{};
   OrthoTargets targets{};
   k.phases = products;
   k.limits = limits_of(l);
   for (int i = 0; i < products; ++i) {
-    k.phase[i] = phase_of(p, q[i], a.ld_dst);
+    k.phase[i] = phase_of(p, q[i], w, a.ld_dst);
     k.phase[i].tiles = (int)tiles_of(k.phase[i]);
   }
   for (int i = 0; i < kMaps; ++i)
-    if (!map_of(&k.maps[i], i, p)) return cudaErrorInvalidValue;
+    if (!map_of(&k.maps[i], i, p, w)) return cudaErrorInvalidValue;
   for (k.first = 0; k.first < p.count; k.first += kOrthoTable) {
     const int64_t some = p.count - k.first < kOrthoTable ? p.count - k.first : kOrthoTable;
     for (int64_t i = 0; i < some; ++i) targets.p[i] = a.dst[k.first + i];
@@ -695,30 +717,50 @@ cudaError_t launch_chain(const OrthoPlan& p, const OrthoProduct* q, int products
   return cudaSuccess;
 }
 
-// Pairs of a cluster for each matrix, or 0: every product by all pairs.  By
-// the time that each way takes, in stages (0.27 us): a tile's sum and, as far as it
-// does not hide behind the next one's, its way out; what a product or a meeting
-// of the cluster costs besides.
-int chain_pairs(const OrthoPlan& p, const OrthoProduct* q, int products, const TcDevice& dev) {
-  if (products > kMaxPhases) return 0;
-  constexpr double kOut = 12, kLaunch = 24, kMeet = 14;
-  const auto turns = [](int64_t tiles, int64_t pairs) { return (double)ceil_div(tiles, pairs); };
-  double least = 0;
-  int best = 0;
-  for (int i = 0; i < products; ++i) {
-    const Phase f = phase_of(p, q[i], 0);
-    least += turns(p.count * tiles_of(f), dev.pairs) * std::fmax(f.steps, kOut) + kOut + kLaunch;
-  }
-  for (int pairs = 1; pairs <= kMaxSplit; ++pairs) {
+// How a call's products are shared out.
+struct Way {
+  int pairs;  // of a cluster for each matrix; 0: every product by all pairs
+  Widths widths;
+};
+
+// The least time, in stages of 256 columns (0.27 us).  A tile takes its sum's
+// stages or its results' way out, whichever is longer, as one hides behind the
+// other but for the last.
+constexpr double kLaunch = 16, kMeet = 10;  // what a product costs besides, alone and in a chain
+double tile_time(int steps, int width) {
+  const double stage = width == 256 ? 1.0 : width == 128 ? 0.6 : 0.5, out = 1 + width / 32;
+  return std::fmax(steps * stage, out);
+}
+double product_time(int64_t tiles, int64_t pairs, int steps, int width) {
+  return (double)ceil_div(tiles, pairs) * tile_time(steps, width) + std::fmin(steps, 1 + width / 32);
+}
+
+Way way_of(const OrthoPlan& p, const OrthoProduct* q, int products, const TcDevice& dev) {
+  int grams = 0, syms = 0, updates = 0;
+  for (int i = 0; i < products; ++i) ++(q[i].form == kGram ? grams : q[i].form == kSym ? syms : updates);
+  const int64_t down = ceil_div(p.m, 2 * kHalf);
+  const int long_steps = (int)ceil_div(p.n, kStep), short_steps = (int)ceil_div(p.m, kStep);
+  // the widths that take the least time with so many pairs for so many matrices
+  const auto best_of = [&](int64_t matrices, int64_t pairs, Widths* w) {
+    double least[3] = {};
+    for (int width = 64; width <= 256; width *= 2) {
+      const double t[3] = {product_time(matrices * triangle(p.m, width), pairs, long_steps, width),
+                           product_time(matrices * triangle(p.m, width), pairs, short_steps, width),
+                           width < 128 ? 1e30 : product_time(matrices * down * ceil_div(p.n, width), pairs, short_steps, width)};
+      int* const at[3] = {&w->gram, &w->sym, &w->update};
+      for (int f = 0; f < 3; ++f)
+        if (width == 64 || t[f] <= least[f]) least[f] = t[f], *at[f] = width;
+    }
+    return grams * least[0] + syms * least[1] + updates * least[2];
+  };
+  Way best{};
+  double least = best_of(p.count, dev.pairs, &best.widths) + products * kLaunch;
+  for (int pairs = 1; pairs <= kMaxSplit && products <= kMaxPhases; ++pairs) {
     const int held = pairs == 1 ? dev.pairs : dev.ortho.held[pairs];
     if (held < 1) continue;
-    double each = 0;
-    for (int i = 0; i < products; ++i) {
-      const Phase f = phase_of(p, q[i], 0);
-      each += turns(tiles_of(f), pairs) * std::fmax(f.steps, kOut) + kOut + kMeet;
-    }
-    const double all = turns(p.count, held) * each + kLaunch;
-    if (all < least) least = all, best = pairs;
+    Way way{pairs, {}};
+    const double all = (double)ceil_div(p.count, held) * (best_of(1, pairs, &way.widths) + products * kMeet) + kLaunch;
+    if (all < least) least = all, best = way;
   }
   return best;
 }
@@ -738,9 +780,10 @@ cudaError_t ortho_prepare(TcDevice* dev) {
 
 cudaError_t launch_ortho_products(const OrthoPlan& p, const OrthoProduct* q, int products, const OrthoArgs& a, const TcLaunch& l,
                                   cudaStream_t stream) {
-  if (const int pairs = chain_pairs(p, q, products, *l.dev)) return launch_chain(p, q, products, pairs, a, l, stream);
+  const Way way = way_of(p, q, products, *l.dev);
+  if (way.pairs) return launch_chain(p, q, products, way.widths, way.pairs, a, l, stream);
   for (int i = 0; i < products; ++i) {
-    const cudaError_t e = launch_product(p, q[i], a, l, stream);
+    const cudaError_t e = launch_product(p, q[i], way.widths, a, l, stream);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

@@ -56,12 +56,13 @@ bool make_stack_map(CUtensorMap* map, const void* p, int64_t cols, int64_t rows,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool make_slab_stack_map(CUtensorMap* map, const void* p, int64_t rows, int64_t count, int64_t ld, uint32_t box_rows) {
+bool make_slab_stack_map(CUtensorMap* map, const void* p, int64_t rows, int64_t count, int64_t ld, uint32_t box_rows,
+                         uint32_t box_slabs) {
   const EncodeTiled encode = encoder();
   if (!encode) return false;
   const cuuint64_t dims[4] = {64, (cuuint64_t)rows, (cuuint64_t)(ld / 64), (cuuint64_t)count};
   const cuuint64_t strides[3] = {(cuuint64_t)ld * 2, 128, (cuuint64_t)(ld * rows) * 2};
-  const cuuint32_t box[4] = {64, box_rows, 2, 1}, step[4] = {1, 1, 1, 1};
+  const cuuint32_t box[4] = {64, box_rows, box_slabs, 1}, step[4] = {1, 1, 1, 1};
   return encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void*>(p), dims, strides, box, step,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;

@@ -25,11 +25,12 @@ bool make_slab_map(CUtensorMap* map, const void* p, int64_t cols, int64_t rows, 
 // Maps of `count` matrices of 16-bit elements one behind another, each
 // contiguous in rows `ld` elements apart (ld a multiple of 64): boxes of
 // box_cols x box_rows of one of them, coordinates (column, row, matrix); or, as
-// slabs of 64 columns (all ld of them), boxes of two slabs by box_rows rows,
+// slabs of 64 columns (all ld of them), boxes of box_slabs by box_rows rows,
 // coordinates (column of the slab, row, slab, matrix).
 bool make_stack_map(CUtensorMap* map, const void* p, int64_t cols, int64_t rows, int64_t count, int64_t ld,
                     uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swizzle);
-bool make_slab_stack_map(CUtensorMap* map, const void* p, int64_t rows, int64_t count, int64_t ld, uint32_t box_rows);
+bool make_slab_stack_map(CUtensorMap* map, const void* p, int64_t rows, int64_t count, int64_t ld, uint32_t box_rows,
+                         uint32_t box_slabs);
 
 // Division of whole numbers below 2^31 by one that a launch knows: with m =
 // floor(2^63 / d) + 1 the quotient is floor(t m / 2^63), as t (m d - 2^63) <
