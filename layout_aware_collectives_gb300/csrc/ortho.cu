@@ -106,11 +106,13 @@ __device__ __forceinline__ Inverse inverse_of(double sum, float eps) {
   const int i = -top / 2, j = -top - i;
   return Inverse{1.0f / norm, power_of(i), power_of(j)};
 }
-// One warp's; the parts in a fixed order.
+// One warp's, the parts in a fixed order: 64-bit sums of all warps would take
+// longer (2048 x 2048: 10.4 us instead of 8.0).
 __device__ __forceinline__ Inverse inverse_norm(const OrthoPlan& p, int64_t z, float eps) {
   __shared__ Inverse shared;
   if (threadIdx.x < 32) {
     double sum = 0.0;
+#pragma unroll 8
     for (int q = threadIdx.x; q < p.parts; q += 32) sum += p.norms[z * p.parts + q];
     const int parts = min(p.parts, 32);
     for (int d = 1; d < parts; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);

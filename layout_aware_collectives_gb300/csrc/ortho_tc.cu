@@ -119,34 +119,41 @@ __device__ __forceinline__ bool work_at(const Phase& p, const Team& team, int i,
 
 // A warp's 32 x 32 elements of one plane in shared memory, 64-byte swizzle: 16-byte
 // piece c of row r lies at piece c ^ (r / 2 % 4).
-__device__ __forceinline__ uint32_t piece_at(uint32_t box, uint32_t row, uint32_t piece) {
-  return box + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
-}
-// 16 rows of a box, from row r0 on, as the tensor cores' fragments have them:
-// register 2 g + h of a lane holds columns 8 g + 2 (lane % 4) and the next one
-// of row r0 + 8 h + lane / 4.
-__device__ __forceinline__ void get_rows(uint32_t box, uint32_t r0, uint32_t lane, uint32_t (&v)[8]) {
+__device__ __forceinline__ uint32_t piece_at(uint32_t row, uint32_t piece) { return row * 64 + ((piece ^ ((row >> 1) & 3)) << 4); }
+
+// Where a lane's part of a box begins; the rest of it is constants further.
+struct Places {
+  uint32_t line;    // eight rows of four pieces at a time: row lane / 4, piece lane % 4
+  uint32_t rows;    // 16 rows as fragments
+  uint32_t turned;  // and turned
+  __device__ __forceinline__ explicit Places(uint32_t lane)
+      : line(piece_at(lane >> 2, lane & 3)),
+        rows(piece_at(lane & 15, lane >> 4)),
+        turned(piece_at((lane >> 4) * 8 + (lane & 7), (lane >> 3) & 1)) {}
+};
+// 16 rows of a box, the first or the second, as the tensor cores' fragments
+// have them: register 2 g + h of a lane holds columns 8 g + 2 (lane % 4) and the
+// next one of row 8 h + lane / 4.
+__device__ __forceinline__ void get_rows(uint32_t box, const Places& at, int q, uint32_t (&v)[8]) {
 #pragma unroll
   for (uint32_t g = 0; g < 4; g += 2)
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v[2 * g]), "=r"(v[2 * g + 1]), "=r"(v[2 * g + 2]), "=r"(v[2 * g + 3])
-                 : "r"(piece_at(box, r0 + (lane & 15), g + (lane >> 4)))
+                 : "r"(box + (at.rows ^ (g << 4)) + q * 1024)
                  : "memory");
 }
-__device__ __forceinline__ void put_rows(uint32_t box, uint32_t r0, uint32_t lane, const uint32_t (&v)[8]) {
+__device__ __forceinline__ void put_rows(uint32_t box, const Places& at, int q, const uint32_t (&v)[8]) {
 #pragma unroll
   for (uint32_t g = 0; g < 4; g += 2)
-    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
-                     piece_at(box, r0 + (lane & 15), g + (lane >> 4))),
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(box + (at.rows ^ (g << 4)) + q * 1024),
                  "r"(v[2 * g]), "r"(v[2 * g + 1]), "r"(v[2 * g + 2]), "r"(v[2 * g + 3])
                  : "memory");
 }
 // Turned: row c of the box is column c.
-__device__ __forceinline__ void put_turned(uint32_t box, uint32_t r0, uint32_t lane, const uint32_t (&v)[8]) {
+__device__ __forceinline__ void put_turned(uint32_t box, const Places& at, int q, const uint32_t (&v)[8]) {
 #pragma unroll
   for (uint32_t g = 0; g < 4; g += 2)
-    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
-                     piece_at(box, (g + (lane >> 4)) * 8 + (lane & 7), r0 / 8 + ((lane >> 3) & 1))),
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(box + (at.turned ^ (q << 5)) + g * 512),
                  "r"(v[2 * g]), "r"(v[2 * g + 1]), "r"(v[2 * g + 2]), "r"(v[2 * g + 3])
                  : "memory");
 }
@@ -160,16 +167,14 @@ __device__ __forceinline__ void tmem_rows(uint32_t addr, uint32_t (&v)[16]) {
       : "memory");
 }
 
-// Eight rows of four pieces at a time: a lane's piece, in shared memory and out
-// of it.  Planes' rows are whole 64s wide, so a box has all its columns.
-__device__ __forceinline__ void ask_box(uint32_t box, const __half* from, int64_t ld, int rows, int lane) {
+// A box of a plane, `from` and `to` being this lane's first piece.  Planes' rows
+// are whole 64s wide, so a box has all its columns; `rows` of its rows are there.
+__device__ __forceinline__ void ask_box(uint32_t box, const Places& at, const __half* from, int64_t ld8, int rows) {
 #pragma unroll
-  for (int r0 = 0; r0 < 32; r0 += 8) {
-    const int r = r0 + (lane >> 2);
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(piece_at(box, r, lane & 3)),
-                 "l"(from + (r < rows ? r : 0) * ld + (lane & 3) * 8), "r"(r < rows ? 16 : 0)
+  for (int q = 0; q < 4; ++q)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(box + at.line + q * 512),
+                 "l"(q * 8 < rows ? from + q * ld8 : from), "r"(q * 8 < rows ? 16 : 0)
                  : "memory");
-  }
 }
 __device__ __forceinline__ void asked() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -178,17 +183,17 @@ __device__ __forceinline__ void arrived() {
   __syncwarp();
 }
 template <class T>
-__device__ __forceinline__ void send_box(uint32_t box, T* to, int64_t ld, int rows, int lane) {
+__device__ __forceinline__ void send_box(uint32_t box, const Places& at, T* to, int64_t ld8, int rows) {
+  uint4 v[4];
 #pragma unroll
-  for (int r0 = 0; r0 < 32; r0 += 8) {
-    const int r = r0 + (lane >> 2);
-    uint4 v;
+  for (int q = 0; q < 4; ++q)
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(piece_at(box, r, lane & 3))
+                 : "=r"(v[q].x), "=r"(v[q].y), "=r"(v[q].z), "=r"(v[q].w)
+                 : "r"(box + at.line + q * 512)
                  : "memory");
-    if (r < rows) *(uint4*)(to + r * ld + (lane & 3) * 8) = v;
-  }
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    if (q * 8 < rows) *(uint4*)(to + q * ld8) = v[q];
 }
 
 // A warp's way through its 32 x 32 pieces of the pair's tiles.
@@ -197,32 +202,61 @@ struct Cursor {
   int i;      // tile
   TileAt at;
   int row0, col, left;  // of the piece; pieces left in this tile, it among them
+  int64_t mine;         // of a plane: this lane's first piece of the box
   bool more;
 
   // The i-th tile, or the next that has a piece for this warp.
-  __device__ __forceinline__ void open(const Phase& p, const Team& team, int first, int half, int lanes) {
+  __device__ __forceinline__ void open(const Phase& p, const Team& team, int first, int half, int lanes, int lane) {
     for (i = first;; ++i) {
       more = work_at<FORM>(p, team, i, at);
       if (!more) return;
       row0 = (at.m * 2 + (int)team.rank) * kHalf + lanes;
       col = at.n * p.width + half * (p.width / 2);
       left = row0 >= p.m || col >= p.wide ? 0 : min(p.width / 64, (p.wide - col + 31) / 32);
+      mine = ((int64_t)at.z * p.m + row0 + (lane >> 2)) * p.ld + col + (lane & 3) * 8;
       if (left) return;
     }
+  }
+  __device__ __forceinline__ void step(const Phase& p, const Team& team, int half, int lanes, int lane) {
+    col += 32, mine += 32;
+    if (--left == 0) open(p, team, i + 1, half, lanes, lane);
   }
 };
 
 // 32 x 32 results to the caller: `rows` and `cols` of which there are.
-__device__ __forceinline__ void send_last(uint32_t box, uint16_t* to, int64_t ld, int rows, int cols, int lane) {
+__device__ __forceinline__ void send_last(uint32_t box, const Places& at, uint16_t* to, int64_t ld, int rows, int cols, int lane) {
   if (((uintptr_t)to & 15) == 0 && ld % 8 == 0 && cols >= 32) {
-    send_box(box, to, ld, rows, lane);
+    send_box(box, at, to + (lane >> 2) * ld + (lane & 3) * 8, 8 * ld, rows - (lane >> 2));
     return;
   }
   for (int r = 0; r < 32 && r < rows; ++r) {
     uint16_t v;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(piece_at(box, r, lane >> 3) + (lane & 7) * 2) : "memory");
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(box + piece_at(r, lane >> 3) + (lane & 7) * 2) : "memory");
     if (lane < cols) to[r * ld + lane] = v;
   }
+}
+
+// Two 32-bit operations as one instruction.
+__device__ __forceinline__ uint64_t two(uint32_t a, uint32_t b) { return (uint64_t)b << 32 | a; }
+__device__ __forceinline__ uint64_t two(float a, float b) { return two(__float_as_uint(a), __float_as_uint(b)); }
+__device__ __forceinline__ uint64_t two_halves(uint32_t v) {
+  const float2 f = unpack_half(v);
+  return two(f.x, f.y);
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t muladd2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
 }
 
 // Diagonals' elements of a piece: left's of row row0 + lane, right's of column
@@ -233,18 +267,19 @@ struct Diagonals {
 
 // What becomes of 32 x 32 sums.
 template <int FORM>
-__device__ __forceinline__ void finish(const Phase& p, uint16_t* dst, const TileAt& t, int row0, int col, int lane,
+__device__ __forceinline__ void finish(const Phase& p, uint16_t* dst, const Cursor<FORM>& now, const Places& at, int lane,
                                        uint32_t tmem, uint32_t slot, Diagonals d) {
-  const int64_t z = (int64_t)t.z * p.m;
+  const TileAt& t = now.at;
+  const int row0 = now.row0, col = now.col;
   uint32_t sums[2][16], a[2][8], b[2][8];
   tmem_rows(tmem, sums[0]);
   tmem_rows(tmem + (16u << 16), sums[1]);
   if constexpr (FORM != kGram) {
-    get_rows(slot, 0, lane, a[0]);
-    get_rows(slot, 16, lane, a[1]);
+    get_rows(slot, at, 0, a[0]);
+    get_rows(slot, at, 1, a[1]);
     if (FORM != kSym || p.planes == 2) {
-      get_rows(slot + kBox, 0, lane, b[0]);
-      get_rows(slot + kBox, 16, lane, b[1]);
+      get_rows(slot + kBox, at, 0, b[0]);
+      get_rows(slot + kBox, at, 1, b[1]);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) b[0][i] = a[0][i], b[1][i] = a[1][i];
@@ -253,83 +288,102 @@ __device__ __forceinline__ void finish(const Phase& p, uint16_t* dst, const Tile
   // What is kept is scale * (s2 (sum + di right + left dj) + s1 left), or
   // scale * (sum + di (hi + lo)): each factor with its scales taken together.
   const float k0 = p.sum_scale * p.out_scale * (FORM == kSym ? p.s2 : 1.0f);
-  float by_row = 0.0f, by_col[8];  // of this lane's row; of the fragments' columns
+  const uint64_t k2 = two(k0, k0);
+  float by_row = 0.0f;
+  uint64_t by_col[4];  // of the fragments' columns
   if constexpr (FORM == kSym) {
     by_row = d.di * p.s2 * p.right_scale * p.out_scale;
-    const float mine = fmaf(d.dj, p.s2, p.s1) * p.left_scale * p.out_scale;
+    const float own = fmaf(d.dj, p.s2, p.s1) * p.left_scale * p.out_scale;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) by_col[i] = __shfl_sync(0xffffffffu, mine, (i >> 1) * 8 + (lane & 3) * 2 + (i & 1));
+    for (int g = 0; g < 4; ++g)
+      by_col[g] = two(__shfl_sync(0xffffffffu, own, g * 8 + (lane & 3) * 2), __shfl_sync(0xffffffffu, own, g * 8 + (lane & 3) * 2 + 1));
   } else if constexpr (FORM != kGram) {
     by_row = d.di * p.right_scale * p.out_scale;
   }
   const bool upper = t.n * p.width / (2 * kHalf) != t.m;  // above the diagonal's tiles
-  const bool diagonal = (FORM == kGram || FORM == kSym) && !upper && row0 == col;
   tmem_arrived(sums[0]);
   tmem_arrived(sums[1]);
   __syncwarp();  // every lane has its part of the slot
+  uint32_t hi[2][8], lo[2][8];
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
-    uint32_t hi[8], lo[8];
-    const float row_a = __shfl_sync(0xffffffffu, by_row, q * 16 + (lane >> 2));
-    const float row_b = __shfl_sync(0xffffffffu, by_row, q * 16 + 8 + (lane >> 2));
+    uint64_t by[2];
+    if constexpr (FORM != kGram) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float v = __shfl_sync(0xffffffffu, by_row, q * 16 + h * 8 + (lane >> 2));
+        by[h] = two(v, v);
+      }
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float by = i & 1 ? row_b : row_a;
-      float y0 = as_f(sums[q][2 * i]) * k0, y1 = as_f(sums[q][2 * i + 1]) * k0;
+      uint64_t y = mul2(two(sums[q][2 * i], sums[q][2 * i + 1]), k2);
       if constexpr (FORM == kSym) {
-        const float2 u = unpack_half(a[q][i]), v = unpack_half(b[q][i]);
-        y0 = fmaf(by, v.x, fmaf(u.x, by_col[i & ~1], y0));
-        y1 = fmaf(by, v.y, fmaf(u.y, by_col[i | 1], y1));
+        y = muladd2(two_halves(a[q][i]), by_col[i >> 1], y);
+        y = muladd2(two_halves(b[q][i]), by[i & 1], y);
       } else if constexpr (FORM != kGram) {
-        const float2 u = unpack_half(a[q][i]), v = unpack_half(b[q][i]);
-        y0 = fmaf(by, u.x + v.x, y0);
-        y1 = fmaf(by, u.y + v.y, y1);
+        y = muladd2(add2(two_halves(a[q][i]), two_halves(b[q][i])), by[i & 1], y);
       }
-      if (diagonal) {  // this lane's element of it, if any; its place in the plane is 0
-        const int r = q * 16 + (i & 1) * 8 + (lane >> 2), c = (i >> 1) * 8 + (lane & 3) * 2;
-        if (r == c || r == c + 1) {
-          float v = (r == c ? y0 : y1) / p.out_scale;
-          if (row0 + r < p.m) {
-            if constexpr (FORM == kSym) {
-              const float dl = __ldcg(p.left_d + z + row0 + r), dr = __ldcg(p.right_d + z + row0 + r);
-              v += fmaf(p.s2 * dl, dr, fmaf(p.s1, dl, p.s0));
-            }
-            p.out_d[z + row0 + r] = v;
-          }
-          if (r == c)
-            y0 = 0.0f;
-          else
-            y1 = 0.0f;
+      const float y0 = __uint_as_float((uint32_t)y), y1 = __uint_as_float((uint32_t)(y >> 32));
+      if constexpr (FORM == kLast) {
+        hi[q][i] = pack_bf16(y0, y1);
+      } else {
+        hi[q][i] = pack_half(y0, y1);
+        if constexpr (FORM == kUpdate) {
+          const uint64_t rest = muladd2(two_halves(hi[q][i]), two(-1.0f, -1.0f), y);
+          lo[q][i] = pack_half(__uint_as_float((uint32_t)rest), __uint_as_float((uint32_t)(rest >> 32)));
         }
       }
-      if constexpr (FORM == kUpdate)
-        split_half2(y0, y1, hi[i], lo[i]);
-      else if constexpr (FORM == kLast)
-        hi[i] = pack_bf16(y0, y1);
-      else
-        hi[i] = pack_half(y0, y1);
     }
+  }
+  if constexpr (FORM == kGram || FORM == kSym) {
+    // The diagonal's elements go to their own place, and 0 to the plane's: row
+    // r and column c of a fragment meet where 8 g + 2 (lane % 4) + {0, 1} = r.
+    const int off = (lane >> 2) - 2 * (lane & 3);
+    if (!upper && row0 == col && (off == 0 || off == 1)) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int i = 2 * (2 * q + h) + h, r = row0 + q * 16 + h * 8 + (lane >> 2);
+          float v = as_f(off ? sums[q][2 * i + 1] : sums[q][2 * i]) * p.sum_scale;
+          const int64_t place = (int64_t)t.z * p.m + r;
+          if (r < p.m) {
+            if constexpr (FORM == kSym) {
+              const float dl = __ldcg(p.left_d + place), dr = __ldcg(p.right_d + place);
+              v = fmaf(p.s2, fmaf(dl, dr, v), fmaf(p.s1, dl, p.s0));
+            }
+            p.out_d[place] = v;
+          }
+          hi[q][i] &= off ? 0xffffu : 0xffff0000u;
+        }
+    }
+    __syncwarp();
+  }
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
     if (FORM == kLast && p.tall) {
-      put_turned(slot, q * 16, lane, hi);
+      put_turned(slot, at, q, hi[q]);
     } else {
-      put_rows(slot, q * 16, lane, hi);
-      if constexpr (FORM == kUpdate) put_rows(slot + kBox, q * 16, lane, lo);
+      put_rows(slot, at, q, hi[q]);
+      if constexpr (FORM == kUpdate) put_rows(slot + kBox, at, q, lo[q]);
       if constexpr (FORM == kGram || FORM == kSym)
-        if (upper) put_turned(slot + kBox, q * 16, lane, hi);
+        if (upper) put_turned(slot + kBox, at, q, hi[q]);
     }
   }
   __syncwarp();
   if constexpr (FORM == kLast) {
     if (p.tall)
-      send_last(slot, dst + (int64_t)col * p.ld_out + row0, p.ld_out, p.wide - col, p.m - row0, lane);
+      send_last(slot, at, dst + (int64_t)col * p.ld_out + row0, p.ld_out, p.wide - col, p.m - row0, lane);
     else
-      send_last(slot, dst + (int64_t)row0 * p.ld_out + col, p.ld_out, p.m - row0, p.wide - col, lane);
+      send_last(slot, at, dst + (int64_t)row0 * p.ld_out + col, p.ld_out, p.m - row0, p.wide - col, lane);
   } else {
-    send_box(slot, p.out[0] + (z + row0) * p.ld + col, p.ld, p.m - row0, lane);
+    send_box(slot, at, p.out[0] + now.mine, 8 * p.ld, p.m - row0 - (lane >> 2));
     if constexpr (FORM == kUpdate)
-      send_box(slot + kBox, p.out[1] + (z + row0) * p.ld + col, p.ld, p.m - row0, lane);
+      send_box(slot + kBox, at, p.out[1] + now.mine, 8 * p.ld, p.m - row0 - (lane >> 2));
     else if (upper)
-      send_box(slot + kBox, p.out[0] + (z + col) * p.ld + row0, p.ld, p.m - col, lane);
+      send_box(slot + kBox, at, p.out[0] + ((int64_t)t.z * p.m + col + (lane >> 2)) * p.ld + row0 + (lane & 3) * 8, 8 * p.ld,
+               p.m - col - (lane >> 2));
   }
   __syncwarp();
 }
@@ -431,24 +485,27 @@ __device__ __forceinline__ bool finish_phase(const Phase& p, const OrthoTargets&
   const int half = warp >> 2, lanes = (warp & 3) * 32;
   // Pieces in turn, slot by slot; `next` is the one whose copies go out.
   constexpr bool kIn = FORM != kGram;
+  const Places places(lane);
   Cursor<FORM> now, next;
-  now.open(p, team, 0, half, lanes);
+  now.open(p, team, 0, half, lanes, lane);
   next = now;
   int slot = 0;  // of the piece at hand, and of the next to be asked for
-  Diagonals d[kSlots];
+  // of the piece at hand and the next: moved on, not chosen by slot, so that
+  // nothing waits for the last one's
+  static_assert(kSlots == 2, "two pieces on their way");
+  Diagonals here{0.0f, 0.0f}, then{0.0f, 0.0f};
   const auto ask = [&](int to) {
+    here = then;
     if (kIn && next.more) {
-      Diagonals v{0.0f, 0.0f};
       const int64_t z = (int64_t)next.at.z * p.m;
-      if (next.row0 + lane < p.m) v.di = __ldcg(p.left_d + z + next.row0 + lane);
-      if (FORM == kSym && next.col + lane < p.wide) v.dj = __ldcg(p.right_d + z + next.col + lane);
-#pragma unroll
-      for (int s = 0; s < kSlots; ++s)
-        if (s == to) d[s] = v;
-      for (int q = 0; q < p.planes; ++q)
-        ask_box(slots + to * kSlot + q * kBox, p.in[q] + (z + next.row0) * p.ld + next.col, p.ld, p.m - next.row0, lane);
-      next.col += 32;
-      if (--next.left == 0) next.open(p, team, next.i + 1, half, lanes);
+      then.di = next.row0 + lane < p.m ? __ldcg(p.left_d + z + next.row0 + lane) : 0.0f;
+      if (FORM == kSym) then.dj = next.col + lane < p.wide ? __ldcg(p.right_d + z + next.col + lane) : 0.0f;
+      const int rows = p.m - next.row0 - (lane >> 2);
+      // (a lane without a row of its own names the piece's first)
+      const int64_t from = rows > 0 ? next.mine : next.mine - (int64_t)(lane >> 2) * p.ld;
+      ask_box(slots + to * kSlot, places, p.in[0] + from, 8 * p.ld, rows);
+      if (FORM != kSym || p.planes == 2) ask_box(slots + to * kSlot + kBox, places, p.in[1] + from, 8 * p.ld, rows);
+      next.step(p, team, half, lanes, lane);
     }
     if (kIn) asked();  // an empty group past the last, so that their number says which have arrived
   };
@@ -463,17 +520,11 @@ __device__ __forceinline__ bool finish_phase(const Phase& p, const OrthoTargets&
     fence_after();
     while (now.more && now.i == i) {
       if (kIn) arrived<kSlots - 1>();
-      const int c = (now.col - at.n * p.width) / 32;
-      Diagonals mine{0.0f, 0.0f};
-#pragma unroll
-      for (int s = 0; s < kSlots; ++s)
-        if (kIn && s == slot) mine = d[s];
-      finish<FORM>(p, FORM == kLast ? targets.p[at.z - first] : nullptr, at, now.row0, now.col, lane,
-                   tmem + ((uint32_t)lanes << 16) + b * 256 + c * 32, slots + slot * kSlot, mine);
+      finish<FORM>(p, FORM == kLast ? targets.p[at.z - first] : nullptr, now, places, lane,
+                   tmem + ((uint32_t)lanes << 16) + b * 256 + (now.col - at.n * p.width), slots + slot * kSlot, here);
       ask(slot);
-      slot = slot + 1 == kSlots ? 0 : slot + 1;
-      now.col += 32;
-      if (--now.left == 0) now.open(p, team, now.i + 1, half, lanes);
+      slot ^= 1;
+      now.step(p, team, half, lanes, lane);
     }
     fence_before();
     __syncwarp();
@@ -723,16 +774,20 @@ struct Way {
   Widths widths;
 };
 
-// The least time, in stages of 256 columns (0.27 us).  A tile takes its sum's
-// stages or its results' way out, whichever is longer, as one hides behind the
-// other but for the last.
-constexpr double kLaunch = 16, kMeet = 10;  // what a product costs besides, alone and in a chain
+// By the time it takes, in stages of 256 columns (0.27 us): a tile's sum or its
+// results' way out, whichever is longer, as one hides behind the other but for the
+// last; and what a product costs besides, alone and in a chain.  Measured (all
+// pairs; one to four pairs a matrix): 704 x 256 105 us; 173, 129, 118, 100.  64
+// of 256 x 704 220; 197, 281, 365, 497.  16 of 300 x 300 132; 273, 164, 125, 213.
+// 100 of 128 x 512 221; 249, 273, 435, 549.  Three of 1021 x 1375 207; 1510, 814,
+// 718, 593, 128 of 768 x 2048 2464; 3211, 2979, 2990, 3851.
+constexpr double kLaunch = 16, kMeet = 12;
 double tile_time(int steps, int width) {
-  const double stage = width == 256 ? 1.0 : width == 128 ? 0.6 : 0.5, out = 1 + width / 32;
+  const double stage = width == 256 ? 1.0 : width == 128 ? 0.65 : 0.55, out = 2 + width / 16;
   return std::fmax(steps * stage, out);
 }
 double product_time(int64_t tiles, int64_t pairs, int steps, int width) {
-  return (double)ceil_div(tiles, pairs) * tile_time(steps, width) + std::fmin(steps, 1 + width / 32);
+  return (double)ceil_div(tiles, pairs) * tile_time(steps, width) + std::fmin(steps, 2 + width / 16);
 }
 
 Way way_of(const OrthoPlan& p, const OrthoProduct* q, int products, const TcDevice& dev) {
@@ -756,6 +811,7 @@ Way way_of(const OrthoPlan& p, const OrthoProduct* q, int products, const TcDevi
   Way best{};
   double least = best_of(p.count, dev.pairs, &best.widths) + products * kLaunch;
   for (int pairs = 1; pairs <= kMaxSplit && products <= kMaxPhases; ++pairs) {
+
     const int held = pairs == 1 ? dev.pairs : dev.ortho.held[pairs];
     if (held < 1) continue;
     Way way{pairs, {}};
