@@ -523,7 +523,7 @@ cudaError_t run(const RouterArgs& a, cudaStream_t stream) {
 
 constexpr int kSlotWarps = 8;
 constexpr int kSlotThreads = 32 * kSlotWarps;
-constexpr int kChunk = 2048;      // pairs of a CTA, at least
+constexpr int kChunk = 1024;      // pairs of a CTA, at least
 constexpr int kMaxChunks = 304;
 
 int64_t chunk_of(int64_t pairs) {
@@ -576,6 +576,7 @@ __global__ void __launch_bounds__(kSlotThreads) place_kernel(SlotsArgs a, int64_
         for (int w = 0; w < kSlotWarps; ++w) all += next[w][e];
       } else {
         const int* count = a.counts + e;
+#pragma unroll 8
         for (int q = 0; q < chunks; ++q, count += a.experts) {
           const int n = *count;
           all += n;
