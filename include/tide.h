@@ -744,7 +744,8 @@ TIDE_API tide_status_t tide_expert_combine_backward(tide_compute_t compute, int6
                                                     const int32_t* slots, const float* weights, uint16_t* drows,
                                                     int64_t ld_drows, float* dweights, cudaStream_t stream);
 
-/* Bytes of tide_orthogonalize's workspace for `count` matrices. */
+/* Bytes of tide_orthogonalize's workspace for `count` matrices of up to 2^30
+ * rows and columns, 2^38 elements in all. */
 TIDE_API tide_status_t tide_orthogonalize_workspace(int64_t count, int64_t rows, int64_t cols, int64_t* bytes);
 
 #define TIDE_MAX_ORTHOGONALIZE_STEPS 16
@@ -764,10 +765,12 @@ TIDE_API tide_status_t tide_orthogonalize_workspace(int64_t count, int64_t rows,
  *   workspace     at least tide_orthogonalize_workspace bytes
  * Rows and columns of zeros stay zero, so a padded gradient may be passed
  * as it is.  A matrix with an infinity or NaN becomes NaN.
- * X and A are kept as two fp16 terms.  Products take their first, and the
- * diagonals of A and of b A + c A A in fp32 beside them: what that leaves is
- * below the result's own rounding to bf16.  Sums are fp32.  What is below 2^-37
- * of the largest norm that X can have in a step counts as nothing.
+ * X is kept as two fp16 terms, A and the matrices made of it as one beside
+ * their diagonals in fp32; products take the first terms, and where that is
+ * less work two steps share a pass over X.  What all this leaves is below the
+ * result's own rounding to bf16 (up to one and a half times it next to
+ * rank one).  Sums are fp32.  What is below 2^-37 of the largest norm that X can
+ * have in a step counts as nothing.
  */
 TIDE_API tide_status_t tide_orthogonalize(tide_compute_t compute, int64_t count, int64_t rows, int64_t cols,
                                           tide_dtype_t type, const void* const* src, int64_t ld_src,

@@ -8,6 +8,7 @@ using namespace tide;
 
 namespace {
 
+constexpr int64_t kMaxSide = (int64_t)1 << 30;  // of a matrix to orthogonalise: tiles pass its end
 const float kCoefficients[3] = {3.4445f, -4.7750f, 2.0315f};
 
 // An array of `bytes`-sized elements, aligned to them.
@@ -195,10 +196,11 @@ TIDE_CATCH
 tide_status_t tide_orthogonalize_workspace(int64_t count, int64_t rows, int64_t cols, int64_t* bytes) try {
   if (!bytes) return invalid("bytes is NULL");
   *bytes = 0;
-  TIDE_TRY(check_dims(rows, cols, "tide_orthogonalize_workspace"));
+  TIDE_TRY(check_dims(rows, cols, "tide_orthogonalize"));
+  if (rows > kMaxSide || cols > kMaxSide) return invalid("tide_orthogonalize: sizes out of range");
   const int64_t numel = rows * cols;
-  if (count < 0 || (numel != 0 && count > kMaxNumel / numel))
-    return invalid("tide_orthogonalize_workspace: count out of range");
+  if (count < 0 || count > kMaxDim || (numel != 0 && count > kMaxNumel / numel))
+    return invalid("tide_orthogonalize: count out of range");
   if (numel != 0 && count != 0) *bytes = ortho_workspace_bytes(count, rows, cols);
   return TIDE_OK;
 }

@@ -110,7 +110,7 @@ def test_orthogonalize_refuses(compute):
         call(coefficients=(1, 2, 3, 4))
     call(src=(), dst=(), workspace=0, workspace_bytes=0)
     call(rows=0, workspace=0, workspace_bytes=0, src=(0, 0), dst=(0, 0))
-    for bad in ((-1, 4, 4), (1, -4, 4), (1 << 38, 4, 4)):
+    for bad in ((-1, 4, 4), (1, -4, 4), (1 << 38, 4, 4), (1 << 31, 1, 1), (1, (1 << 30) + 1, 1), (1, 1, (1 << 31) - 1)):
         with pytest.raises(tide.TideError):
             tide.orthogonalize_workspace_bytes(*bad)
 
