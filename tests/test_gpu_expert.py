@@ -517,3 +517,45 @@ def test_orthogonalize_waits_that_run_out_are_reported(count, rows, cols):
             hook(0)
             assert all(torch.equal(a, b) for a, b in zip(orthogonalized(c, grads), want))
             c.check_device()
+
+
+def test_expert_layer_example():
+    """The example runs, its first step's mean gradients are the definition's, and its updates their orthogonal factors."""
+    import os
+    import sys
+
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import expert_layer as ex
+
+    ranks, tokens, experts, topk, hidden, ffn = 2, 70, 5, 2, 128, 96
+    layer = ex.Layer(ranks, experts, topk, hidden, ffn)
+    inputs, targets = ex.problem(layer, tokens, 1)
+    work = ex.Pass(layer, tokens)
+    with tide.Compute() as c:
+        loss = ex.step(layer, c, work, inputs, targets, 0.0)  # the parameters stay as they were
+        leaves = [p.double().requires_grad_(True) for p in layer.params]
+        total = 0.0
+        for r in range(ranks):
+            logits = inputs[r].double() @ leaves[0].T
+            ids, _ = ref.route(logits.detach().float(), topk)
+            share = torch.softmax(logits, 1).gather(1, ids)
+            share = share / share.sum(1, keepdim=True)
+            y = []
+            for t in range(tokens):
+                z = 0.0
+                for j, e in enumerate(ids[t].tolist()):
+                    gate, up, down = layer.expert(leaves, e)
+                    x = inputs[r][t].double()
+                    z = z + share[t, j] * ((ffn_reference.act(gate @ x, "silu") * (up @ x)) @ down.T)
+                y.append(z)
+            total = total + ((torch.stack(y) - targets[r].double()) ** 2).mean() / ranks
+        assert abs(loss - float(total.detach())) <= 4 * ref.U_BF16 * float(total.detach())
+        grads = torch.autograd.grad(total, leaves)
+        # y - target, dz, h, z, dh, dG and dU, and the gradients themselves have been rounded to bf16, the mean once more
+        for got, want in zip(layer.whole, grads):
+            assert float((got.double() - want).norm()) <= 6 * ref.U_BF16 * float(want.norm())
+        for p, (update, grad) in enumerate(zip(layer.updates, layer.whole)):
+            if p:
+                near(update, grad)
+        losses = [ex.step(layer, c, work, inputs, targets, 0.02) for _ in range(2)]
+        assert all(math.isfinite(v) for v in losses)
