@@ -1,4 +1,8 @@
 // Newton-Schulz orthogonalisation: norms, the first X, and the steps.
+//
+// The first two kernels are passes over the matrices, bound by HBM: norms of
+// one 14336 x 4096 in fp32 46 us (5.1 TB/s), its first X 112 (4.2; turned, and
+// what was in L2 goes out meanwhile); 128 of 768 x 2048 in bf16 110 and 215 us.
 #include <cmath>
 
 #include "ortho.cuh"

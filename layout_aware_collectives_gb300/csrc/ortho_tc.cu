@@ -10,15 +10,23 @@
 // As in the gated block, a pair of CTAs works on one tile of 256 rows and 256
 // columns (or 128 or 64, where there are few tiles): each loads 128 rows of the
 // left operand and half of the right one's columns, one MMA instruction of the
-// pair reads both halves.  Warps 0 and 3 load (5 stages
-// of 32 KiB), warp 1 of the pair's first CTA issues the MMAs, warps from 4 on
-// read finished sums out of TMEM, which holds two accumulators so that they do
-// so while the next tile is summed.
+// pair reads both halves.  Warps 0 and 3 load (5 stages of 32 KiB), warp 1 of the
+// pair's first CTA issues the MMAs, warps from 4 on read finished sums out of
+// TMEM, which holds two accumulators so that they do so while the next tile is
+// summed.
 //
 // What those warps add to the sums (32 x 32 elements of two planes at a time)
 // is copied to shared memory while the elements before are at work, and what
 // they make of it goes out by way of the same place.  TMA does neither: each of
-// its copies here would stand behind the operands' large ones.
+// its copies here would stand behind the operands' large ones.  The sums come
+// out of TMEM as fragments, so that a piece is stored turned, for the tile's
+// other place, by the same instructions.
+//
+// Bound by the tensor cores where sums are long: one 14336 x 4096, gram 148 us
+// (1.72 PFLOP/s of the half that is summed), sym 50 (1.46: 136 tiles on 76
+// pairs), update 288 (1.67).  By the way out where they are short, 3.3 us a tile
+// of gram, 5.3 of sym, 8 of update: 128 of 768 x 2048, gram 139 us, sym 84,
+// update 290, which is also 80% of what their bytes take.
 #include <cmath>
 
 #include "ortho.cuh"

