@@ -491,8 +491,7 @@ def test_expert_layer_step(compute):
     lx, ll, lg, lu = leaves
     s = torch.softmax(ll, 1).gather(1, ids.long())
     s = s / s.sum(1, keepdim=True)
-    hid = torch.stack([torch.stack([ffn_reference.act(lx[i] @ lg[q].T, "silu") * (lx[i] @ lu[q].T) for q in ids[i].tolist()]) for i in range(t)])
-    want_y = (hid * s[:, :, None]).sum(1)
+    want_y = sum((s * (ids == q)).sum(1, keepdim=True) * (ffn_reference.act(lx @ lg[q].T, "silu") * (lx @ lu[q].T)) for q in range(e))
     grads = torch.autograd.grad((want_y * dy.double()).sum(), leaves)
     # each result has passed a few roundings to bf16 (h, dh, dG and dU, the rows' gradients), 2^-8 of what is rounded at most
     for got, want, roundings in ((y, want_y, 2), (dx, grads[0], 4), (dlogits, grads[1], 3), (dwg, grads[2], 3), (dwu, grads[3], 3)):
@@ -540,15 +539,12 @@ def test_expert_layer_example():
             ids, _ = ref.route(logits.detach().float(), topk)
             share = torch.softmax(logits, 1).gather(1, ids)
             share = share / share.sum(1, keepdim=True)
-            y = []
-            for t in range(tokens):
-                z = 0.0
-                for j, e in enumerate(ids[t].tolist()):
-                    gate, up, down = layer.expert(leaves, e)
-                    x = inputs[r][t].double()
-                    z = z + share[t, j] * ((ffn_reference.act(gate @ x, "silu") * (up @ x)) @ down.T)
-                y.append(z)
-            total = total + ((torch.stack(y) - targets[r].double()) ** 2).mean() / ranks
+            x, y = inputs[r].double(), 0.0
+            for e in range(experts):
+                gate, up, down = layer.expert(leaves, e)
+                mine = (share * (ids == e)).sum(1, keepdim=True)
+                y = y + mine * ((ffn_reference.act(x @ gate.T, "silu") * (x @ up.T)) @ down.T)
+            total = total + ((y - targets[r].double()) ** 2).mean() / ranks
         assert abs(loss - float(total.detach())) <= 4 * ref.U_BF16 * float(total.detach())
         grads = torch.autograd.grad(total, leaves)
         # y - target, dz, h, z, dh, dG and dU, and the gradients themselves have been rounded to bf16, the mean once more
@@ -559,3 +555,69 @@ def test_expert_layer_example():
                 near(update, grad)
         losses = [ex.step(layer, c, work, inputs, targets, 0.02) for _ in range(2)]
         assert all(math.isfinite(v) for v in losses)
+
+
+# --------------------------------------------------- past 32-bit offsets
+
+def test_route_past_32_bit_offsets(compute):
+    """The last tokens of 2.1 million among 1024 experts choose as they do alone, forward and back."""
+    t, e, k, some = (1 << 21) + 77, 1024, 4, 300
+    g = gen(40)
+    r = tide.Router(e, k)
+    logits = torch.empty(t, e, dtype=torch.bfloat16, device="cuda")
+    for part in logits.split(1 << 18):
+        part.copy_(torch.randn(part.shape, generator=g, device="cuda", dtype=torch.bfloat16))
+    ids, w = torch.empty(t, k, dtype=torch.int32, device="cuda"), torch.empty(t, k, device="cuda")
+    compute.route(r, t, logits, ids, w, logits_type="bf16")
+    last = logits[-some:].clone()
+    check_route(compute, dict(experts=e, topk=k), last, None, "bf16")
+    ids1, w1 = torch.empty(some, k, dtype=torch.int32, device="cuda"), torch.empty(some, k, device="cuda")
+    compute.route(r, some, last, ids1, w1, logits_type="bf16")
+    assert torch.equal(ids[-some:], ids1) and torch.equal(w[-some:], w1)
+    dlogits, alone = torch.empty_like(logits), torch.empty_like(last)
+    compute.route_backward(r, t, logits, ids, w, dlogits, logits_type="bf16")
+    compute.route_backward(r, some, last, ids1, w1, alone, logits_type="bf16")
+    assert torch.equal(dlogits[-some:], alone)
+
+
+def test_rows_past_32_bit_offsets(compute):
+    """36,000 tokens of 8192 to 8 experts each, 2.4 billion elements, there and back."""
+    t, h, k = 36000, 8192, 8
+    g = gen(41)
+    x = torch.randn(t, h, generator=g, device="cuda", dtype=torch.bfloat16)
+    ids = torch.randint(0, 64, (t, k), generator=g, device="cuda", dtype=torch.int32)
+    slots, offsets = torch.empty_like(ids), torch.empty(65, dtype=torch.int32, device="cuda")
+    ws = torch.empty(tide.expert_slots_workspace_bytes(t, k, 64), dtype=torch.uint8, device="cuda")
+    compute.expert_slots(t, k, 64, ids, slots, offsets, ws)
+    rows = torch.empty(t * k, h, dtype=torch.bfloat16, device="cuda")
+    compute.expert_gather(t, h, k, x, slots, rows, t * k)
+    for i in (0, t // 2, t - 1):
+        assert torch.equal(rows[slots[i].long()], x[i].expand(k, h))
+    y = torch.empty_like(x)
+    w = torch.rand(t, k, generator=g, device="cuda")
+    compute.expert_combine(t, h, k, rows, t * k, slots, w, y)
+    drows, dw = torch.empty_like(rows), torch.empty_like(w)
+    compute.expert_combine_backward(t, h, k, x, rows, t * k, slots, w, drows, dw)
+    for part in (slice(0, 50), slice(t - 50, t)):
+        at = slots[part].reshape(-1).long()
+        few = torch.arange(at.numel(), device="cuda", dtype=torch.int32).view(-1, k)
+        want, bound = ref.combine(rows[at], few, w[part])
+        close(y[part], want, bound)
+        each, each_bound, want_dw, dw_bound = ref.combine_backward(x[part], rows[at], few, w[part])
+        close(drows[at].view(-1, k, h), each, each_bound)
+        close(dw[part], want_dw, dw_bound)
+
+
+def test_orthogonalize_past_32_bit_offsets(compute):
+    """600 matrices of 1000 x 4000 in one call: 2.4 billion elements in each plane."""
+    count, rows, cols = 600, 1000, 4000
+    g = gen(42)
+    grads = torch.empty(count, rows, cols, dtype=torch.bfloat16, device="cuda")
+    for part in grads.split(50):
+        part.copy_(torch.randn(part.shape, generator=g, device="cuda", dtype=torch.bfloat16))
+    outs = torch.empty_like(grads)
+    ws = torch.empty(tide.orthogonalize_workspace_bytes(count, rows, cols), dtype=torch.uint8, device="cuda")
+    compute.orthogonalize(rows, cols, list(grads), list(outs), ws, src_type="bf16")
+    del ws
+    for i in (0, 127, 128, count - 1):
+        near(outs[i], grads[i])
