@@ -110,16 +110,17 @@ __device__ __forceinline__ bool work_at(const Phase& p, const Team& team, int i,
   if constexpr (FORM == kUpdate || FORM == kLast) {
     r = tile_at(p.grid, t);
   } else {
-    // Down the columns: the tiles of rows up to the diagonal's.  `across`
-    // columns of tiles end at the same row.
-    const int across = 2 * kHalf / p.width;
+    // Down the columns: the tiles of rows up to the diagonal's.  One, two or
+    // four columns of tiles end at the same row.
+    const int turns = p.width == 256 ? 0 : p.width == 128 ? 1 : 2;  // 2^turns of them
     r.z = p.each.of(t);
     const int q = t - r.z * p.each.d;
-    int n = (int)((sqrtf(8.0f * (float)(q / across) + 1.0f) - 1.0f) * 0.5f);
-    while (across * (n * (n + 1) / 2) > q) --n;
-    while (across * ((n + 1) * (n + 2) / 2) <= q) ++n;
-    const int rest = q - across * (n * (n + 1) / 2);
-    r.n = n * across + rest / (n + 1), r.m = rest % (n + 1);
+    int n = (int)((__fsqrt_rn(8.0f * (float)(q >> turns) + 1.0f) - 1.0f) * 0.5f);
+    while (((n * (n + 1) / 2) << turns) > q) --n;
+    while ((((n + 1) * (n + 2) / 2) << turns) <= q) ++n;
+    const int rest = q - ((n * (n + 1) / 2) << turns), high = n + 1;
+    const int column = (rest >= high) + (rest >= 2 * high) + (rest >= 3 * high);  // of up to four
+    r.n = (n << turns) + column, r.m = rest - column * high;
   }
   r.z += team.z0;
   return true;
@@ -348,21 +349,19 @@ __device__ __forceinline__ void finish(const Phase& p, uint16_t* dst, const Curs
     // The diagonal's elements go to their own place, and 0 to the plane's: row
     // r and column c of a fragment meet where 8 g + 2 (lane % 4) + {0, 1} = r.
     const int off = (lane >> 2) - 2 * (lane & 3);
-    if (!upper && row0 == col && (off == 0 || off == 1)) {
+    if (!upper && row0 == col) {
 #pragma unroll
       for (int q = 0; q < 2; ++q)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int i = 2 * (2 * q + h) + h, r = row0 + q * 16 + h * 8 + (lane >> 2);
+          const int i = 2 * (2 * q + h) + h, r = q * 16 + h * 8 + (lane >> 2);
           float v = as_f(off ? sums[q][2 * i + 1] : sums[q][2 * i]) * p.sum_scale;
-          const int64_t place = (int64_t)t.z * p.m + r;
-          if (r < p.m) {
-            if constexpr (FORM == kSym) {
-              const float dl = __ldcg(p.left_d + place), dr = __ldcg(p.right_d + place);
-              v = fmaf(p.s2, fmaf(dl, dr, v), fmaf(p.s1, dl, p.s0));
-            }
-            p.out_d[place] = v;
+          if constexpr (FORM == kSym) {
+            const float dl = __shfl_sync(0xffffffffu, d.di, r), dr = __shfl_sync(0xffffffffu, d.dj, r);
+            v = fmaf(p.s2, fmaf(dl, dr, v), fmaf(p.s1, dl, p.s0));
           }
+          if (off != 0 && off != 1) continue;
+          if (row0 + r < p.m) p.out_d[(int64_t)t.z * p.m + row0 + r] = v;
           hi[q][i] &= off ? 0xffffu : 0xffff0000u;
         }
     }
@@ -431,14 +430,18 @@ template <int FORM>
 __device__ __forceinline__ bool load_phase(const Phase& p, const CUtensorMap* map, const Team& team, bool left, uint32_t smem,
                                            const Bars& bars, uint32_t leader, const Watch& watch, int& j) {
   constexpr bool kBMn = FORM == kUpdate || FORM == kLast;
+  const uint32_t leaders = peer_addr(bars.full(0), leader);
+  const uint32_t bytes = 2 * kOperand + p.width * (kStep * 2);
+  const bool expects = left && team.rank == 0;
+  const int steps = p.steps;
+  int s = j % kStages, parity = (j / kStages + 1) & 1;
   TileAt at;
   for (int i = 0; work_at<FORM>(p, team, i, at); ++i) {
     const int row = (at.m * 2 + team.rank) * kHalf, col = at.n * p.width + (int)team.rank * (p.width / 2);
-    for (int k = 0; k < p.steps; ++k, ++j) {
-      const int s = j % kStages;
-      if (j >= kStages && !bar_wait(bars.empty(s), (j / kStages + 1) & 1, watch)) return false;
-      if (left && team.rank == 0) bar_expect(bars.full(s), 2 * kOperand + p.width * (kStep * 2));
-      const uint32_t bar = peer_addr(bars.full(s), leader);
+    for (int k = 0; k < steps; ++k, ++j) {
+      if (j >= kStages && !bar_wait(bars.empty(s), parity, watch)) return false;
+      if (expects) bar_expect(bars.full(s), bytes);
+      const uint32_t bar = leaders + 8u * s;
       const uint32_t a = smem + s * kStage, b = a + kOperand;
       if (left)
         load_box3<true>(a, map, k * kStep, row, at.z, bar);
@@ -446,6 +449,7 @@ __device__ __forceinline__ bool load_phase(const Phase& p, const CUtensorMap* ma
         load_box4(b, map, 0, k * kStep, col / 64, at.z, bar);
       else
         load_box3<true>(b, map, k * kStep, col, at.z, bar);
+      if (++s == kStages) s = 0, parity ^= 1;
     }
   }
   return true;
@@ -465,14 +469,15 @@ __device__ __forceinline__ bool mma_phase(const Phase& p, const Team& team, uint
                                           uint16_t ctas, const Watch& watch, int& j, int& done) {
   constexpr bool kBMn = FORM == kUpdate || FORM == kLast;
   const uint32_t instr = instr_desc(0, 0, kBMn, 256, 0) | (uint32_t)(p.width >> 3) << 17;  // fp16 operands
+  const int steps = p.steps;
+  int s = j % kStages, parity = (j / kStages) & 1;
   TileAt at;
   for (int i = 0; work_at<FORM>(p, team, i, at); ++i, ++done) {
     const int b = done & 1;
     if (done >= 2 && !bar_wait<kPeer>(bars.sums_empty(b), (done / 2 + 1) & 1, watch)) return false;
     fence_after();
-    for (int k = 0; k < p.steps; ++k, ++j) {
-      const int s = j % kStages;
-      if (!bar_wait(bars.full(s), (j / kStages) & 1, watch)) return false;
+    for (int k = 0; k < steps; ++k, ++j) {
+      if (!bar_wait(bars.full(s), parity, watch)) return false;
       fence_after();
       const uint32_t a = smem + s * kStage;
       const uint64_t da = operand_desc(a, 16), db = operand_desc(a + kOperand, kBMn ? kOperand / 2 : 16);
@@ -480,6 +485,7 @@ __device__ __forceinline__ bool mma_phase(const Phase& p, const Team& team, uint
       for (int q = 0; q < kStep / 16; ++q)
         mma<2, false>(tmem + b * 256, da + q * (32 >> 4), db + q * ((kBMn ? 2048 : 32) >> 4), instr, k > 0 || q > 0);
       mma_commit<2>(bars.empty(s), ctas);
+      if (++s == kStages) s = 0, parity ^= 1;
     }
     mma_commit<2>(bars.sums_full(b), ctas);
   }
@@ -596,6 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint64_t bar_words[kBars];
   __shared__ uint32_t tmem_at;
   __shared__ int stop, ended_at;  // the phase that a wait ran out in
+  __shared__ Phase at_hand[2];    // and the next one, which has time to come
   const uint32_t smem = (smem_addr(raw) + 1023u) & ~1023u;
   const Bars bars{smem_addr(bar_words)};
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -608,7 +615,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool late = p.limits.late_ns && warp == 4;
   const Watch sums_watch{&stop, p.limits.err, late ? p.limits.late_ns : p.limits.limit_ns};
   const uint32_t slots = smem + kStages * kStage + (warp - 4) * kSlots * kSlot;
+  const auto fetch = [&](int n, int from, int by) {
+    static_assert(sizeof(Phase) % 4 == 0, "copied by words");
+    for (int i = from; i < (int)(sizeof(Phase) / 4); i += by) ((uint32_t*)&at_hand[n & 1])[i] = ((const uint32_t*)&p.phase[n])[i];
+  };
   if (threadIdx.x == 0) ended_at = INT32_MAX;
+  fetch(0, threadIdx.x, kThreads);
   if (threadIdx.x < kMaps) prefetch_map(&p.maps[threadIdx.x]);
   const uint32_t tmem = set_up(bars, &stop, &tmem_at, warp);
   after_previous();
@@ -618,10 +630,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (p.limits.stall_ns && threadIdx.x == 0) bar_wait(bars.silent(), 0, Watch{&stop, p.limits.err, p.limits.stall_ns});
   const int phases = p.limits.stall_ns ? 0 : p.phases;
   for (int n = 0; n < phases; ++n) {
-    const Phase& f = p.phase[n];
+    const Phase& f = at_hand[n & 1];
+    if (warp == 2 && n + 1 < phases) fetch(n + 1, lane, 32);
     if (warp == 0 || warp == 3) {
       if (elected()) {
-        async_proxy_fence();  // what others wrote, before copies of it
         const bool left = warp == 0;
         const CUtensorMap* map = &p.maps[left ? f.left : f.right];
         if (f.form == kGram)
@@ -650,13 +662,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         finish_phase<kUpdate>(f, targets, team, p.first, slots, tmem, bars, leader, late, sums_watch, warp - 4, lane, done);
       else
         finish_phase<kLast>(f, targets, team, p.first, slots, tmem, bars, leader, late, sums_watch, warp - 4, lane, done);
-      async_proxy_fence();  // these results, before others' copies of them
+      publish();  // these results, to others' reads and copies of them
     }
     __syncthreads();
     // A wait that ran out ends all of the cluster at this phase: who tells the
     // others does so before they meet, and one that is a phase ahead names its own.
     if (stop && threadIdx.x < ctas) peer_write(peer_addr(smem_addr(&ended_at), threadIdx.x), n);
-    cluster_sync();
+    if (stop) publish();
+    cluster_meet();
     ended = *(volatile int*)&ended_at <= n;
     if (ended) break;
   }

@@ -40,6 +40,12 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// The same, but releasing nothing by itself: who has written has published it
+// (a release by every thread waits for all of its CTA's writes once more).
+__device__ __forceinline__ void cluster_meet() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // One thread of a converged warp, for the copies and the MMAs: what it issues
 // behind `lane == 0` instead takes longer (dX of 7 tokens, 2048 x 8192: 24.1 us
 // against 18.7).  The warp's index comes from a shuffle for the same reason.
@@ -192,8 +198,12 @@ __device__ __forceinline__ void stores_read() {  // all but the last N groups ha
   asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
 __device__ __forceinline__ void stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-// Between a CTA's own accesses to memory of either kind and copies of it.
-__device__ __forceinline__ void async_proxy_fence() { asm volatile("fence.proxy.async;" ::: "memory"); }
+// This thread's writes, before what the cluster's other threads read, or copy
+// by tensor maps, behind a cluster_meet().
+__device__ __forceinline__ void publish() {
+  asm volatile("fence.acq_rel.cluster;" ::: "memory");
+  asm volatile("fence.proxy.async;" ::: "memory");
+}
 __device__ __forceinline__ void async_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // ------------------------------------------------------------ tensor cores
