@@ -350,6 +350,7 @@ __device__ __forceinline__ void finish(const Phase& p, uint16_t* dst, const Curs
     // r and column c of a fragment meet where 8 g + 2 (lane % 4) + {0, 1} = r.
     const int off = (lane >> 2) - 2 * (lane & 3);
     if (!upper && row0 == col) {
+      float* diagonal = p.out_d + ((int64_t)t.z * p.m + row0 + (lane >> 2));
 #pragma unroll
       for (int q = 0; q < 2; ++q)
 #pragma unroll
@@ -360,9 +361,8 @@ __device__ __forceinline__ void finish(const Phase& p, uint16_t* dst, const Curs
             const float dl = __shfl_sync(0xffffffffu, d.di, r), dr = __shfl_sync(0xffffffffu, d.dj, r);
             v = fmaf(p.s2, fmaf(dl, dr, v), fmaf(p.s1, dl, p.s0));
           }
-          if (off != 0 && off != 1) continue;
-          if (row0 + r < p.m) p.out_d[(int64_t)t.z * p.m + row0 + r] = v;
-          hi[q][i] &= off ? 0xffffu : 0xffff0000u;
+          if ((off == 0 || off == 1) && row0 + r < p.m) diagonal[q * 16 + h * 8] = v;
+          hi[q][i] &= off == 0 ? 0xffff0000u : off == 1 ? 0xffffu : 0xffffffffu;
         }
     }
     __syncwarp();
@@ -424,19 +424,31 @@ __device__ __forceinline__ uint32_t set_up(const Bars& bars, int* stop, uint32_t
   return *tmem_at;
 }
 
+// A phase's first tile, found ahead of it.
+struct First {
+  TileAt at;
+  bool more;
+};
+__device__ __forceinline__ First first_of(const Phase& p, const Team& team) {
+  First f;
+  f.more = p.form >= kUpdate ? work_at<kUpdate>(p, team, 0, f.at) : work_at<kSym>(p, team, 0, f.at);
+  return f;
+}
+
 // One thread loads the left operand, another the right one.  j: stages
 // filled so far.  `leader`: the pair's first CTA's rank in the cluster.
 template <int FORM>
-__device__ __forceinline__ bool load_phase(const Phase& p, const CUtensorMap* map, const Team& team, bool left, uint32_t smem,
-                                           const Bars& bars, uint32_t leader, const Watch& watch, int& j) {
+__device__ __forceinline__ bool load_phase(const Phase& p, const CUtensorMap* map, const Team& team, const First& first, bool left,
+                                           uint32_t smem, const Bars& bars, uint32_t leader, const Watch& watch, int& j) {
   constexpr bool kBMn = FORM == kUpdate || FORM == kLast;
   const uint32_t leaders = peer_addr(bars.full(0), leader);
   const uint32_t bytes = 2 * kOperand + p.width * (kStep * 2);
   const bool expects = left && team.rank == 0;
   const int steps = p.steps;
   int s = j % kStages, parity = (j / kStages + 1) & 1;
-  TileAt at;
-  for (int i = 0; work_at<FORM>(p, team, i, at); ++i) {
+  TileAt at = first.at;
+  bool more = first.more;
+  for (int i = 1; more; more = work_at<FORM>(p, team, i++, at)) {
     const int row = (at.m * 2 + team.rank) * kHalf, col = at.n * p.width + (int)team.rank * (p.width / 2);
     for (int k = 0; k < steps; ++k, ++j) {
       if (j >= kStages && !bar_wait(bars.empty(s), parity, watch)) return false;
@@ -572,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 0 || warp == 3) {
     if (elected()) {
       const bool left = warp == 0;
-      const bool go = load_phase<FORM>(p.phase, left ? &p.left : &p.right, team, left, smem, bars, 0, watch, j);
+      const bool go = load_phase<FORM>(p.phase, left ? &p.left : &p.right, team, first_of(p.phase, team), left, smem, bars, 0, watch, j);
       load_end(go, team, bars, watch, j);
     }
   } else if (warp == 1 && team.rank == 0) {
@@ -627,6 +639,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   int j = 0, done = 0;
   bool go = true, ended = false;
+  First first{};
+  if (warp == 0 || warp == 3) first = first_of(p.phase[0], team);
   if (p.limits.stall_ns && threadIdx.x == 0) bar_wait(bars.silent(), 0, Watch{&stop, p.limits.err, p.limits.stall_ns});
   const int phases = p.limits.stall_ns ? 0 : p.phases;
   for (int n = 0; n < phases; ++n) {
@@ -637,12 +651,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool left = warp == 0;
         const CUtensorMap* map = &p.maps[left ? f.left : f.right];
         if (f.form == kGram)
-          go = load_phase<kGram>(f, map, team, left, smem, bars, leader, watch, j);
+          go = load_phase<kGram>(f, map, team, first, left, smem, bars, leader, watch, j);
         else if (f.form == kSym)
-          go = load_phase<kSym>(f, map, team, left, smem, bars, leader, watch, j);
+          go = load_phase<kSym>(f, map, team, first, left, smem, bars, leader, watch, j);
         else
-          go = load_phase<kUpdate>(f, map, team, left, smem, bars, leader, watch, j);
-        if (!go || n == phases - 1) load_end(go, team, bars, watch, j);
+          go = load_phase<kUpdate>(f, map, team, first, left, smem, bars, leader, watch, j);
+        if (!go || n == phases - 1)
+          load_end(go, team, bars, watch, j);
+        else
+          first = first_of(p.phase[n + 1], team);
       }
     } else if (warp == 1 && team.rank == 0) {
       if (elected()) {
