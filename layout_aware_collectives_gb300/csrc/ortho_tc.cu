@@ -103,11 +103,19 @@ struct Team {
   uint32_t rank;  // of this CTA in its pair
 };
 
+// A kernel of one form knows it; one of all forms looks it up (kAny) but for
+// results' way out (one code for all of them there: 704 x 256 94 us instead of 87).
+constexpr int kAny = -1;
+template <int FORM>
+__device__ __forceinline__ int form_of(const Phase& p) {
+  return FORM == kAny ? p.form : FORM;
+}
+
 template <int FORM>
 __device__ __forceinline__ bool work_at(const Phase& p, const Team& team, int i, TileAt& r) {
   const int t = team.pair + i * team.pairs;
   if (t >= p.tiles) return false;
-  if constexpr (FORM == kUpdate || FORM == kLast) {
+  if (form_of<FORM>(p) >= kUpdate) {
     r = tile_at(p.grid, t);
   } else {
     // Down the columns: the tiles of rows up to the diagonal's.  One, two or
@@ -257,11 +265,6 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 __device__ __forceinline__ uint64_t muladd2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
@@ -278,38 +281,37 @@ struct Diagonals {
 template <int FORM>
 __device__ __forceinline__ void finish(const Phase& p, uint16_t* dst, const Cursor<FORM>& now, const Places& at, int lane,
                                        uint32_t tmem, uint32_t slot, Diagonals d) {
+  const int form = form_of<FORM>(p);
   const TileAt& t = now.at;
   const int row0 = now.row0, col = now.col;
   uint32_t sums[2][16], a[2][8], b[2][8];
   tmem_rows(tmem, sums[0]);
   tmem_rows(tmem + (16u << 16), sums[1]);
-  if constexpr (FORM != kGram) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a[0][i] = a[1][i] = 0;
+  if (form != kGram) {
     get_rows(slot, at, 0, a[0]);
     get_rows(slot, at, 1, a[1]);
-    if (FORM != kSym || p.planes == 2) {
-      get_rows(slot + kBox, at, 0, b[0]);
-      get_rows(slot + kBox, at, 1, b[1]);
-    } else {
+  }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) b[0][i] = a[0][i], b[1][i] = a[1][i];
-    }
+  for (int i = 0; i < 8; ++i) b[0][i] = a[0][i], b[1][i] = a[1][i];
+  if (p.planes == 2) {
+    get_rows(slot + kBox, at, 0, b[0]);
+    get_rows(slot + kBox, at, 1, b[1]);
   }
   // What is kept is scale * (s2 (sum + di right + left dj) + s1 left), or
-  // scale * (sum + di (hi + lo)): each factor with its scales taken together.
-  const float k0 = p.sum_scale * p.out_scale * (FORM == kSym ? p.s2 : 1.0f);
+  // scale * (sum + di hi + di lo): each factor with its scales taken together.
+  const float k0 = p.sum_scale * p.out_scale * p.s2;
   const uint64_t k2 = two(k0, k0);
-  float by_row = 0.0f;
+  const float by_row = d.di * p.s2 * p.right_scale * p.out_scale;
   uint64_t by_col[4];  // of the fragments' columns
-  if constexpr (FORM == kSym) {
-    by_row = d.di * p.s2 * p.right_scale * p.out_scale;
+  if (form == kSym) {
     const float own = fmaf(d.dj, p.s2, p.s1) * p.left_scale * p.out_scale;
 #pragma unroll
     for (int g = 0; g < 4; ++g)
       by_col[g] = two(__shfl_sync(0xffffffffu, own, g * 8 + (lane & 3) * 2), __shfl_sync(0xffffffffu, own, g * 8 + (lane & 3) * 2 + 1));
-  } else if constexpr (FORM != kGram) {
-    by_row = d.di * p.right_scale * p.out_scale;
   }
-  const bool upper = t.n * p.width / (2 * kHalf) != t.m;  // above the diagonal's tiles
+  const bool upper = form < kUpdate && t.n * p.width / (2 * kHalf) != t.m;  // above the diagonal's tiles
   tmem_arrived(sums[0]);
   tmem_arrived(sums[1]);
   __syncwarp();  // every lane has its part of the slot
@@ -317,80 +319,79 @@ __device__ __forceinline__ void finish(const Phase& p, uint16_t* dst, const Curs
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
     uint64_t by[2];
-    if constexpr (FORM != kGram) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float v = __shfl_sync(0xffffffffu, by_row, q * 16 + h * 8 + (lane >> 2));
-        by[h] = two(v, v);
-      }
+    for (int h = 0; h < 2; ++h) {
+      const float v = __shfl_sync(0xffffffffu, by_row, q * 16 + h * 8 + (lane >> 2));
+      by[h] = two(v, v);
     }
+    uint64_t y[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      uint64_t y = mul2(two(sums[q][2 * i], sums[q][2 * i + 1]), k2);
-      if constexpr (FORM == kSym) {
-        y = muladd2(two_halves(a[q][i]), by_col[i >> 1], y);
-        y = muladd2(two_halves(b[q][i]), by[i & 1], y);
-      } else if constexpr (FORM != kGram) {
-        y = muladd2(add2(two_halves(a[q][i]), two_halves(b[q][i])), by[i & 1], y);
-      }
-      const float y0 = __uint_as_float((uint32_t)y), y1 = __uint_as_float((uint32_t)(y >> 32));
-      if constexpr (FORM == kLast) {
-        hi[q][i] = pack_bf16(y0, y1);
-      } else {
-        hi[q][i] = pack_half(y0, y1);
-        if constexpr (FORM == kUpdate) {
-          const uint64_t rest = muladd2(two_halves(hi[q][i]), two(-1.0f, -1.0f), y);
-          lo[q][i] = pack_half(__uint_as_float((uint32_t)rest), __uint_as_float((uint32_t)(rest >> 32)));
-        }
+      y[i] = mul2(two(sums[q][2 * i], sums[q][2 * i + 1]), k2);
+      if (FORM == kGram) continue;
+      y[i] = muladd2(two_halves(a[q][i]), form == kSym ? by_col[i >> 1] : by[i & 1], y[i]);
+      y[i] = muladd2(two_halves(b[q][i]), by[i & 1], y[i]);
+    }
+    if (form == kLast) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) hi[q][i] = pack_bf16(__uint_as_float((uint32_t)y[i]), __uint_as_float((uint32_t)(y[i] >> 32)));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) hi[q][i] = pack_half(__uint_as_float((uint32_t)y[i]), __uint_as_float((uint32_t)(y[i] >> 32)));
+    }
+    if (form == kUpdate) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint64_t rest = muladd2(two_halves(hi[q][i]), two(-1.0f, -1.0f), y[i]);
+        lo[q][i] = pack_half(__uint_as_float((uint32_t)rest), __uint_as_float((uint32_t)(rest >> 32)));
       }
     }
   }
-  if constexpr (FORM == kGram || FORM == kSym) {
+  if (form < kUpdate && !upper && row0 == col) {
     // The diagonal's elements go to their own place, and 0 to the plane's: row
     // r and column c of a fragment meet where 8 g + 2 (lane % 4) + {0, 1} = r.
     const int off = (lane >> 2) - 2 * (lane & 3);
-    if (!upper && row0 == col) {
-      float* diagonal = p.out_d + ((int64_t)t.z * p.m + row0 + (lane >> 2));
+    float* diagonal = p.out_d + ((int64_t)t.z * p.m + row0 + (lane >> 2));
 #pragma unroll
-      for (int q = 0; q < 2; ++q)
+    for (int q = 0; q < 2; ++q)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int i = 2 * (2 * q + h) + h, r = q * 16 + h * 8 + (lane >> 2);
-          float v = as_f(off ? sums[q][2 * i + 1] : sums[q][2 * i]) * p.sum_scale;
-          if constexpr (FORM == kSym) {
-            const float dl = __shfl_sync(0xffffffffu, d.di, r), dr = __shfl_sync(0xffffffffu, d.dj, r);
-            v = fmaf(p.s2, fmaf(dl, dr, v), fmaf(p.s1, dl, p.s0));
-          }
-          if ((off == 0 || off == 1) && row0 + r < p.m) diagonal[q * 16 + h * 8] = v;
-          hi[q][i] &= off == 0 ? 0xffff0000u : off == 1 ? 0xffffu : 0xffffffffu;
-        }
-    }
-    __syncwarp();
+      for (int h = 0; h < 2; ++h) {
+        const int i = 2 * (2 * q + h) + h, r = q * 16 + h * 8 + (lane >> 2);
+        float v = as_f(off ? sums[q][2 * i + 1] : sums[q][2 * i]) * p.sum_scale;
+        const float dl = __shfl_sync(0xffffffffu, d.di, r), dr = __shfl_sync(0xffffffffu, d.dj, r);
+        v = fmaf(p.s2, fmaf(dl, dr, v), fmaf(p.s1, dl, p.s0));
+        if ((off == 0 || off == 1) && row0 + r < p.m) diagonal[q * 16 + h * 8] = v;
+        hi[q][i] &= off == 0 ? 0xffff0000u : off == 1 ? 0xffffu : 0xffffffffu;
+      }
   }
-#pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    if (FORM == kLast && p.tall) {
-      put_turned(slot, at, q, hi[q]);
-    } else {
-      put_rows(slot, at, q, hi[q]);
-      if constexpr (FORM == kUpdate) put_rows(slot + kBox, at, q, lo[q]);
-      if constexpr (FORM == kGram || FORM == kSym)
-        if (upper) put_turned(slot + kBox, at, q, hi[q]);
-    }
+  if (form == kLast && p.tall) {
+    put_turned(slot, at, 0, hi[0]);
+    put_turned(slot, at, 1, hi[1]);
+  } else {
+    put_rows(slot, at, 0, hi[0]);
+    put_rows(slot, at, 1, hi[1]);
+  }
+  if (form == kUpdate) {
+    put_rows(slot + kBox, at, 0, lo[0]);
+    put_rows(slot + kBox, at, 1, lo[1]);
+  }
+  if (upper) {
+    put_turned(slot + kBox, at, 0, hi[0]);
+    put_turned(slot + kBox, at, 1, hi[1]);
   }
   __syncwarp();
-  if constexpr (FORM == kLast) {
+  if (form == kLast) {
     if (p.tall)
       send_last(slot, at, dst + (int64_t)col * p.ld_out + row0, p.ld_out, p.wide - col, p.m - row0, lane);
     else
       send_last(slot, at, dst + (int64_t)row0 * p.ld_out + col, p.ld_out, p.m - row0, p.wide - col, lane);
   } else {
-    send_box(slot, at, p.out[0] + now.mine, 8 * p.ld, p.m - row0 - (lane >> 2));
-    if constexpr (FORM == kUpdate)
-      send_box(slot + kBox, at, p.out[1] + now.mine, 8 * p.ld, p.m - row0 - (lane >> 2));
-    else if (upper)
-      send_box(slot + kBox, at, p.out[0] + ((int64_t)t.z * p.m + col + (lane >> 2)) * p.ld + row0 + (lane & 3) * 8, 8 * p.ld,
-               p.m - col - (lane >> 2));
+    const int64_t ld8 = 8 * p.ld;
+    send_box(slot, at, p.out[0] + now.mine, ld8, p.m - row0 - (lane >> 2));
+    if (form == kUpdate || upper) {
+      const int64_t turned = ((int64_t)t.z * p.m + col + (lane >> 2)) * p.ld + row0 + (lane & 3) * 8;
+      send_box(slot + kBox, at, upper ? p.out[0] + turned : p.out[1] + now.mine, ld8, p.m - (upper ? col : row0) - (lane >> 2));
+    }
   }
   __syncwarp();
 }
@@ -431,7 +432,7 @@ struct First {
 };
 __device__ __forceinline__ First first_of(const Phase& p, const Team& team) {
   First f;
-  f.more = p.form >= kUpdate ? work_at<kUpdate>(p, team, 0, f.at) : work_at<kSym>(p, team, 0, f.at);
+  f.more = work_at<kAny>(p, team, 0, f.at);
   return f;
 }
 
@@ -440,7 +441,7 @@ __device__ __forceinline__ First first_of(const Phase& p, const Team& team) {
 template <int FORM>
 __device__ __forceinline__ bool load_phase(const Phase& p, const CUtensorMap* map, const Team& team, const First& first, bool left,
                                            uint32_t smem, const Bars& bars, uint32_t leader, const Watch& watch, int& j) {
-  constexpr bool kBMn = FORM == kUpdate || FORM == kLast;
+  const bool b_mn = form_of<FORM>(p) >= kUpdate;  // the right operand's major
   const uint32_t leaders = peer_addr(bars.full(0), leader);
   const uint32_t bytes = 2 * kOperand + p.width * (kStep * 2);
   const bool expects = left && team.rank == 0;
@@ -457,7 +458,7 @@ __device__ __forceinline__ bool load_phase(const Phase& p, const CUtensorMap* ma
       const uint32_t a = smem + s * kStage, b = a + kOperand;
       if (left)
         load_box3<true>(a, map, k * kStep, row, at.z, bar);
-      else if (kBMn)
+      else if (b_mn)
         load_box4(b, map, 0, k * kStep, col / 64, at.z, bar);
       else
         load_box3<true>(b, map, k * kStep, col, at.z, bar);
@@ -479,8 +480,9 @@ __device__ __forceinline__ void load_end(bool go, const Team& team, const Bars& 
 template <int FORM>
 __device__ __forceinline__ bool mma_phase(const Phase& p, const Team& team, uint32_t smem, uint32_t tmem, const Bars& bars,
                                           uint16_t ctas, const Watch& watch, int& j, int& done) {
-  constexpr bool kBMn = FORM == kUpdate || FORM == kLast;
-  const uint32_t instr = instr_desc(0, 0, kBMn, 256, 0) | (uint32_t)(p.width >> 3) << 17;  // fp16 operands
+  const bool b_mn = form_of<FORM>(p) >= kUpdate;
+  const uint32_t instr = instr_desc(0, 0, b_mn, 256, 0) | (uint32_t)(p.width >> 3) << 17;  // fp16 operands
+  const uint32_t b_lbo = b_mn ? kOperand / 2 : 16, b_next = (b_mn ? 2048 : 32) >> 4;
   const int steps = p.steps;
   int s = j % kStages, parity = (j / kStages) & 1;
   TileAt at;
@@ -492,10 +494,10 @@ __device__ __forceinline__ bool mma_phase(const Phase& p, const Team& team, uint
       if (!bar_wait(bars.full(s), parity, watch)) return false;
       fence_after();
       const uint32_t a = smem + s * kStage;
-      const uint64_t da = operand_desc(a, 16), db = operand_desc(a + kOperand, kBMn ? kOperand / 2 : 16);
+      const uint64_t da = operand_desc(a, 16), db = operand_desc(a + kOperand, b_lbo);
 #pragma unroll
       for (int q = 0; q < kStep / 16; ++q)
-        mma<2, false>(tmem + b * 256, da + q * (32 >> 4), db + q * ((kBMn ? 2048 : 32) >> 4), instr, k > 0 || q > 0);
+        mma<2, false>(tmem + b * 256, da + q * (32 >> 4), db + q * b_next, instr, k > 0 || q > 0);
       mma_commit<2>(bars.empty(s), ctas);
       if (++s == kStages) s = 0, parity ^= 1;
     }
@@ -510,7 +512,8 @@ __device__ __forceinline__ bool finish_phase(const Phase& p, const OrthoTargets&
                                              const Watch& watch, int warp, int lane, int& done) {
   const int half = warp >> 2, lanes = (warp & 3) * 32;
   // Pieces in turn, slot by slot; `next` is the one whose copies go out.
-  constexpr bool kIn = FORM != kGram;
+  const int form = form_of<FORM>(p);
+  const bool in = form != kGram;
   const Places places(lane);
   Cursor<FORM> now, next;
   now.open(p, team, 0, half, lanes, lane);
@@ -522,18 +525,18 @@ __device__ __forceinline__ bool finish_phase(const Phase& p, const OrthoTargets&
   Diagonals here{0.0f, 0.0f}, then{0.0f, 0.0f};
   const auto ask = [&](int to) {
     here = then;
-    if (kIn && next.more) {
+    if (in && next.more) {
       const int64_t z = (int64_t)next.at.z * p.m;
       then.di = next.row0 + lane < p.m ? __ldcg(p.left_d + z + next.row0 + lane) : 0.0f;
-      if (FORM == kSym) then.dj = next.col + lane < p.wide ? __ldcg(p.right_d + z + next.col + lane) : 0.0f;
+      if (form == kSym) then.dj = next.col + lane < p.wide ? __ldcg(p.right_d + z + next.col + lane) : 0.0f;
       const int rows = p.m - next.row0 - (lane >> 2);
       // (a lane without a row of its own names the piece's first)
       const int64_t from = rows > 0 ? next.mine : next.mine - (int64_t)(lane >> 2) * p.ld;
       ask_box(slots + to * kSlot, places, p.in[0] + from, 8 * p.ld, rows);
-      if (FORM != kSym || p.planes == 2) ask_box(slots + to * kSlot + kBox, places, p.in[1] + from, 8 * p.ld, rows);
+      if (p.planes == 2) ask_box(slots + to * kSlot + kBox, places, p.in[1] + from, 8 * p.ld, rows);
       next.step(p, team, half, lanes, lane);
     }
-    if (kIn) asked();  // an empty group past the last, so that their number says which have arrived
+    if (in) asked();  // an empty group past the last, so that their number says which have arrived
   };
   for (int s = 0; s < kSlots; ++s) ask(s);
   TileAt at;
@@ -545,8 +548,8 @@ __device__ __forceinline__ bool finish_phase(const Phase& p, const OrthoTargets&
     if (!go) break;
     fence_after();
     while (now.more && now.i == i) {
-      if (kIn) arrived<kSlots - 1>();
-      finish<FORM>(p, FORM == kLast ? targets.p[at.z - first] : nullptr, now, places, lane,
+      if (in) arrived<kSlots - 1>();
+      finish<FORM>(p, form == kLast ? targets.p[at.z - first] : nullptr, now, places, lane,
                    tmem + ((uint32_t)lanes << 16) + b * 256 + (now.col - at.n * p.width), slots + slot * kSlot, here);
       ask(slot);
       slot ^= 1;
@@ -556,7 +559,7 @@ __device__ __forceinline__ bool finish_phase(const Phase& p, const OrthoTargets&
     __syncwarp();
     if (lane == 0) bar_arrive_peer(peer_addr(bars.sums_empty(b), leader));
   }
-  if (kIn) arrived<0>();
+  if (in) arrived<0>();
   return go;
 }
 
@@ -650,26 +653,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (elected()) {
         const bool left = warp == 0;
         const CUtensorMap* map = &p.maps[left ? f.left : f.right];
-        if (f.form == kGram)
-          go = load_phase<kGram>(f, map, team, first, left, smem, bars, leader, watch, j);
-        else if (f.form == kSym)
-          go = load_phase<kSym>(f, map, team, first, left, smem, bars, leader, watch, j);
-        else
-          go = load_phase<kUpdate>(f, map, team, first, left, smem, bars, leader, watch, j);
+        go = load_phase<kAny>(f, map, team, first, left, smem, bars, leader, watch, j);
         if (!go || n == phases - 1)
           load_end(go, team, bars, watch, j);
         else
           first = first_of(p.phase[n + 1], team);
       }
     } else if (warp == 1 && team.rank == 0) {
-      if (elected()) {
-        if (f.form == kGram)
-          go = mma_phase<kGram>(f, team, smem, tmem, bars, both, watch, j, done);
-        else if (f.form == kSym)
-          go = mma_phase<kSym>(f, team, smem, tmem, bars, both, watch, j, done);
-        else
-          go = mma_phase<kUpdate>(f, team, smem, tmem, bars, both, watch, j, done);
-      }
+      if (elected()) go = mma_phase<kAny>(f, team, smem, tmem, bars, both, watch, j, done);
     } else if (warp >= 4) {
       if (f.form == kGram)
         finish_phase<kGram>(f, targets, team, p.first, slots, tmem, bars, leader, late, sums_watch, warp - 4, lane, done);
