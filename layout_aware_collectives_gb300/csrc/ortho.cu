@@ -340,7 +340,7 @@ cudaError_t launch_orthogonalize(const OrthoArgs& a, const TcLaunch& l, cudaStre
     }
     i += two ? 2 : 1;
     const int by = two ? 0 : 1;
-    q[products++] = OrthoProduct{i < a.steps ? kUpdate : kLast, turn, by, 0, 0, 1, 0, 0, t[by], x, (float)scale_for(bound.x[i])};
+    q[products++] = OrthoProduct{i < a.steps ? kUpdate : kLast, turn, 0, by, 0, 1, 0, 0, x, t[by], (float)scale_for(bound.x[i])};
   }
   return launch_ortho_products(p, q, products, a, l, stream);
 }

@@ -41,7 +41,7 @@ struct OrthoPlan {
 struct OrthoProduct {
   OrthoForm form;
   int turn;            // which X is read
-  int left, right;     // kSym: t's; kUpdate, kLast: left times X
+  int left, right;     // kSym: t's; kUpdate, kLast: X turned, times the right t
   int out;             // kGram, kSym: a t
   float s2, s1, s0;    // kSym: s2 (left right) + s1 left + s0
   float left_scale, right_scale, out_scale;

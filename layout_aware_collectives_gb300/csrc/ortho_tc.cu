@@ -7,6 +7,12 @@
 // What gram and sym make is symmetric: only tiles on and above the diagonal
 // are summed, and written to both places.
 //
+// Update's and last's tiles are of X turned, X^T L (L is symmetric): the long
+// side lies along a tile's 256 rows, and the short one along its columns, of
+// which a tile may have 64.  With X as it is, a matrix of 33 rows left seven of
+// eight warps without results (25 of 3582 x 33: 204 us, 153 turned; level where
+// both sides are long).
+//
 // As in the gated block, a pair of CTAs works on one tile of 256 rows and 256
 // columns (or 128 or 64, where there are few tiles): each loads 128 rows of the
 // left operand and half of the right one's columns, one MMA instruction of the
@@ -56,7 +62,7 @@ struct Phase {
   const __half* in[2];      // planes that are added: sym: left, right; update, last: X, hi and lo
   __half* out[2];           // gram, sym: the one; update: the next X, hi and lo
   int64_t ld;               // of those
-  int m, wide, steps;       // rows and columns of the result, stages of a tile's sum
+  int m, wide, steps;       // rows and columns of the result (update, last: of X turned), stages of a tile's sum
   int planes;               // of `in`
   int width;                // columns of a tile
   TileGrid grid;            // update, last
@@ -71,8 +77,8 @@ struct Phase {
 };
 
 // The operands that products have: left ones of gram, sym and update, right
-// ones of gram, sym and update.
-enum Map { kLeftX = 0, kLeftT = 2, kRightX = 5, kRightT = 7, kWideX = 10, kMaps = 12 };
+// ones of the same.
+enum Map { kLeftX = 0, kLeftT = 2, kWideX = 5, kRightX = 7, kRightT = 9, kUpdateT = 12, kMaps = 14 };
 
 struct Limits {
   int* err;
@@ -159,6 +165,25 @@ __device__ __forceinline__ void get_rows(uint32_t box, const Places& at, int q, 
                  : "r"(box + (at.rows ^ (g << 4)) + q * 1024)
                  : "memory");
 }
+// Turned: column c of them is row c of the box.
+__device__ __forceinline__ void get_turned(uint32_t box, const Places& at, int q, uint32_t (&v)[8]) {
+#pragma unroll
+  for (uint32_t g = 0; g < 4; g += 2)
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v[2 * g]), "=r"(v[2 * g + 1]), "=r"(v[2 * g + 2]), "=r"(v[2 * g + 3])
+                 : "r"(box + (at.turned ^ (q << 5)) + g * 512)
+                 : "memory");
+}
+template <bool TURNED>
+__device__ __forceinline__ void get_box(uint32_t box, const Places& at, uint32_t (&v)[2][8]) {
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    if constexpr (TURNED)
+      get_turned(box, at, q, v[q]);
+    else
+      get_rows(box, at, q, v[q]);
+  }
+}
 __device__ __forceinline__ void put_rows(uint32_t box, const Places& at, int q, const uint32_t (&v)[8]) {
 #pragma unroll
   for (uint32_t g = 0; g < 4; g += 2)
@@ -166,7 +191,6 @@ __device__ __forceinline__ void put_rows(uint32_t box, const Places& at, int q, 
                  "r"(v[2 * g]), "r"(v[2 * g + 1]), "r"(v[2 * g + 2]), "r"(v[2 * g + 3])
                  : "memory");
 }
-// Turned: row c of the box is column c.
 __device__ __forceinline__ void put_turned(uint32_t box, const Places& at, int q, const uint32_t (&v)[8]) {
 #pragma unroll
   for (uint32_t g = 0; g < 4; g += 2)
@@ -222,20 +246,27 @@ struct Cursor {
   int64_t mine;         // of a plane: this lane's first piece of the box
   bool more;
 
+  // Rows of the box that are there, from this lane's first one on.
+  __device__ __forceinline__ int rows(const Phase& p, int lane) const {
+    return (form_of<FORM>(p) >= kUpdate ? p.wide - col : p.m - row0) - (lane >> 2);
+  }
+
   // The i-th tile, or the next that has a piece for this warp.
   __device__ __forceinline__ void open(const Phase& p, const Team& team, int first, int half, int lanes, int lane) {
+    const bool turned = form_of<FORM>(p) >= kUpdate;
     for (i = first;; ++i) {
       more = work_at<FORM>(p, team, i, at);
       if (!more) return;
       row0 = (at.m * 2 + (int)team.rank) * kHalf + lanes;
       col = at.n * p.width + half * (p.width / 2);
       left = row0 >= p.m || col >= p.wide ? 0 : min(p.width / 64, (p.wide - col + 31) / 32);
-      mine = ((int64_t)at.z * p.m + row0 + (lane >> 2)) * p.ld + col + (lane & 3) * 8;
+      // (update: X's rows are the result's columns)
+      mine = ((int64_t)at.z * p.wide + (turned ? col : row0) + (lane >> 2)) * p.ld + (turned ? row0 : col) + (lane & 3) * 8;
       if (left) return;
     }
   }
   __device__ __forceinline__ void step(const Phase& p, const Team& team, int half, int lanes, int lane) {
-    col += 32, mine += 32;
+    col += 32, mine += form_of<FORM>(p) >= kUpdate ? 32 * p.ld : 32;
     if (--left == 0) open(p, team, i + 1, half, lanes, lane);
   }
 };
@@ -289,23 +320,18 @@ __device__ __forceinline__ void finish(const Phase& p, uint16_t* dst, const Curs
   tmem_rows(tmem + (16u << 16), sums[1]);
 #pragma unroll
   for (int i = 0; i < 8; ++i) a[0][i] = a[1][i] = 0;
-  if (form != kGram) {
-    get_rows(slot, at, 0, a[0]);
-    get_rows(slot, at, 1, a[1]);
-  }
+  constexpr bool kTurned = FORM >= kUpdate;
+  if (form != kGram) get_box<kTurned>(slot, at, a);
 #pragma unroll
   for (int i = 0; i < 8; ++i) b[0][i] = a[0][i], b[1][i] = a[1][i];
-  if (p.planes == 2) {
-    get_rows(slot + kBox, at, 0, b[0]);
-    get_rows(slot + kBox, at, 1, b[1]);
-  }
+  if (p.planes == 2) get_box<kTurned>(slot + kBox, at, b);
   // What is kept is scale * (s2 (sum + di right + left dj) + s1 left), or
-  // scale * (sum + di hi + di lo): each factor with its scales taken together.
+  // scale * (sum + dj hi + dj lo): each factor with its scales taken together.
   const float k0 = p.sum_scale * p.out_scale * p.s2;
   const uint64_t k2 = two(k0, k0);
   const float by_row = d.di * p.s2 * p.right_scale * p.out_scale;
   uint64_t by_col[4];  // of the fragments' columns
-  if (form == kSym) {
+  if (form != kGram) {
     const float own = fmaf(d.dj, p.s2, p.s1) * p.left_scale * p.out_scale;
 #pragma unroll
     for (int g = 0; g < 4; ++g)
@@ -329,8 +355,8 @@ __device__ __forceinline__ void finish(const Phase& p, uint16_t* dst, const Curs
     for (int i = 0; i < 8; ++i) {
       y[i] = mul2(two(sums[q][2 * i], sums[q][2 * i + 1]), k2);
       if (FORM == kGram) continue;
-      y[i] = muladd2(two_halves(a[q][i]), form == kSym ? by_col[i >> 1] : by[i & 1], y[i]);
-      y[i] = muladd2(two_halves(b[q][i]), by[i & 1], y[i]);
+      y[i] = muladd2(two_halves(a[q][i]), by_col[i >> 1], y[i]);
+      y[i] = muladd2(two_halves(b[q][i]), form == kSym ? by[i & 1] : by_col[i >> 1], y[i]);
     }
     if (form == kLast) {
 #pragma unroll
@@ -351,7 +377,7 @@ __device__ __forceinline__ void finish(const Phase& p, uint16_t* dst, const Curs
     // The diagonal's elements go to their own place, and 0 to the plane's: row
     // r and column c of a fragment meet where 8 g + 2 (lane % 4) + {0, 1} = r.
     const int off = (lane >> 2) - 2 * (lane & 3);
-    float* diagonal = p.out_d + ((int64_t)t.z * p.m + row0 + (lane >> 2));
+    float* diagonal = p.out_d + ((int64_t)t.z * p.wide + row0 + (lane >> 2));
 #pragma unroll
     for (int q = 0; q < 2; ++q)
 #pragma unroll
@@ -364,7 +390,7 @@ __device__ __forceinline__ void finish(const Phase& p, uint16_t* dst, const Curs
         hi[q][i] &= off == 0 ? 0xffff0000u : off == 1 ? 0xffffu : 0xffffffffu;
       }
   }
-  if (form == kLast && p.tall) {
+  if (form == kUpdate || (form == kLast && !p.tall)) {
     put_turned(slot, at, 0, hi[0]);
     put_turned(slot, at, 1, hi[1]);
   } else {
@@ -372,8 +398,8 @@ __device__ __forceinline__ void finish(const Phase& p, uint16_t* dst, const Curs
     put_rows(slot, at, 1, hi[1]);
   }
   if (form == kUpdate) {
-    put_rows(slot + kBox, at, 0, lo[0]);
-    put_rows(slot + kBox, at, 1, lo[1]);
+    put_turned(slot + kBox, at, 0, lo[0]);
+    put_turned(slot + kBox, at, 1, lo[1]);
   }
   if (upper) {
     put_turned(slot + kBox, at, 0, hi[0]);
@@ -382,15 +408,16 @@ __device__ __forceinline__ void finish(const Phase& p, uint16_t* dst, const Curs
   __syncwarp();
   if (form == kLast) {
     if (p.tall)
-      send_last(slot, at, dst + (int64_t)col * p.ld_out + row0, p.ld_out, p.wide - col, p.m - row0, lane);
-    else
       send_last(slot, at, dst + (int64_t)row0 * p.ld_out + col, p.ld_out, p.m - row0, p.wide - col, lane);
+    else
+      send_last(slot, at, dst + (int64_t)col * p.ld_out + row0, p.ld_out, p.wide - col, p.m - row0, lane);
   } else {
     const int64_t ld8 = 8 * p.ld;
-    send_box(slot, at, p.out[0] + now.mine, ld8, p.m - row0 - (lane >> 2));
+    const int rows = now.rows(p, lane);
+    send_box(slot, at, p.out[0] + now.mine, ld8, rows);
     if (form == kUpdate || upper) {
-      const int64_t turned = ((int64_t)t.z * p.m + col + (lane >> 2)) * p.ld + row0 + (lane & 3) * 8;
-      send_box(slot + kBox, at, upper ? p.out[0] + turned : p.out[1] + now.mine, ld8, p.m - (upper ? col : row0) - (lane >> 2));
+      const int64_t turned = ((int64_t)t.z * p.wide + col + (lane >> 2)) * p.ld + row0 + (lane & 3) * 8;
+      send_box(slot + kBox, at, upper ? p.out[0] + turned : p.out[1] + now.mine, ld8, upper ? p.wide - col - (lane >> 2) : rows);
     }
   }
   __syncwarp();
@@ -441,7 +468,7 @@ __device__ __forceinline__ First first_of(const Phase& p, const Team& team) {
 template <int FORM>
 __device__ __forceinline__ bool load_phase(const Phase& p, const CUtensorMap* map, const Team& team, const First& first, bool left,
                                            uint32_t smem, const Bars& bars, uint32_t leader, const Watch& watch, int& j) {
-  const bool b_mn = form_of<FORM>(p) >= kUpdate;  // the right operand's major
+  const bool a_mn = form_of<FORM>(p) >= kUpdate;  // the left operand's major
   const uint32_t leaders = peer_addr(bars.full(0), leader);
   const uint32_t bytes = 2 * kOperand + p.width * (kStep * 2);
   const bool expects = left && team.rank == 0;
@@ -456,12 +483,12 @@ __device__ __forceinline__ bool load_phase(const Phase& p, const CUtensorMap* ma
       if (expects) bar_expect(bars.full(s), bytes);
       const uint32_t bar = leaders + 8u * s;
       const uint32_t a = smem + s * kStage, b = a + kOperand;
-      if (left)
-        load_box3<true>(a, map, k * kStep, row, at.z, bar);
-      else if (b_mn)
-        load_box4(b, map, 0, k * kStep, col / 64, at.z, bar);
-      else
+      if (!left)
         load_box3<true>(b, map, k * kStep, col, at.z, bar);
+      else if (a_mn)
+        load_box4(a, map, 0, k * kStep, row / 64, at.z, bar);
+      else
+        load_box3<true>(a, map, k * kStep, row, at.z, bar);
       if (++s == kStages) s = 0, parity ^= 1;
     }
   }
@@ -480,9 +507,9 @@ __device__ __forceinline__ void load_end(bool go, const Team& team, const Bars& 
 template <int FORM>
 __device__ __forceinline__ bool mma_phase(const Phase& p, const Team& team, uint32_t smem, uint32_t tmem, const Bars& bars,
                                           uint16_t ctas, const Watch& watch, int& j, int& done) {
-  const bool b_mn = form_of<FORM>(p) >= kUpdate;
-  const uint32_t instr = instr_desc(0, 0, b_mn, 256, 0) | (uint32_t)(p.width >> 3) << 17;  // fp16 operands
-  const uint32_t b_lbo = b_mn ? kOperand / 2 : 16, b_next = (b_mn ? 2048 : 32) >> 4;
+  const bool a_mn = form_of<FORM>(p) >= kUpdate;
+  const uint32_t instr = instr_desc(0, a_mn, 0, 256, 0) | (uint32_t)(p.width >> 3) << 17;  // fp16 operands
+  const uint32_t a_lbo = a_mn ? kOperand / 2 : 16, a_next = (a_mn ? 2048 : 32) >> 4;
   const int steps = p.steps;
   int s = j % kStages, parity = (j / kStages) & 1;
   TileAt at;
@@ -494,10 +521,10 @@ __device__ __forceinline__ bool mma_phase(const Phase& p, const Team& team, uint
       if (!bar_wait(bars.full(s), parity, watch)) return false;
       fence_after();
       const uint32_t a = smem + s * kStage;
-      const uint64_t da = operand_desc(a, 16), db = operand_desc(a + kOperand, b_lbo);
+      const uint64_t da = operand_desc(a, a_lbo), db = operand_desc(a + kOperand, 16);
 #pragma unroll
       for (int q = 0; q < kStep / 16; ++q)
-        mma<2, false>(tmem + b * 256, da + q * (32 >> 4), db + q * b_next, instr, k > 0 || q > 0);
+        mma<2, false>(tmem + b * 256, da + q * a_next, db + q * (32 >> 4), instr, k > 0 || q > 0);
       mma_commit<2>(bars.empty(s), ctas);
       if (++s == kStages) s = 0, parity ^= 1;
     }
@@ -526,10 +553,10 @@ __device__ __forceinline__ bool finish_phase(const Phase& p, const OrthoTargets&
   const auto ask = [&](int to) {
     here = then;
     if (in && next.more) {
-      const int64_t z = (int64_t)next.at.z * p.m;
-      then.di = next.row0 + lane < p.m ? __ldcg(p.left_d + z + next.row0 + lane) : 0.0f;
-      if (form == kSym) then.dj = next.col + lane < p.wide ? __ldcg(p.right_d + z + next.col + lane) : 0.0f;
-      const int rows = p.m - next.row0 - (lane >> 2);
+      const int64_t z = (int64_t)next.at.z * p.wide;
+      if (form == kSym) then.di = next.row0 + lane < p.m ? __ldcg(p.left_d + z + next.row0 + lane) : 0.0f;
+      then.dj = next.col + lane < p.wide ? __ldcg(p.right_d + z + next.col + lane) : 0.0f;
+      const int rows = next.rows(p, lane);
       // (a lane without a row of its own names the piece's first)
       const int64_t from = rows > 0 ? next.mine : next.mine - (int64_t)(lane >> 2) * p.ld;
       ask_box(slots + to * kSlot, places, p.in[0] + from, 8 * p.ld, rows);
@@ -706,10 +733,11 @@ bool map_of(CUtensorMap* map, int which, const OrthoPlan& p, const Widths& w) {
     return make_stack_map(map, plane, cols, p.m, p.count, ld, kStep, rows, CU_TENSOR_MAP_SWIZZLE_128B);
   };
   if (which < kLeftT) return k(p.x[which - kLeftX][0], p.n, p.ld_x, kHalf);
-  if (which < kRightX) return k(p.t[which - kLeftT], p.m, p.ld_a, kHalf);
+  if (which < kWideX) return k(p.t[which - kLeftT], p.m, p.ld_a, kHalf);
+  if (which < kRightX) return make_slab_stack_map(map, p.x[which - kWideX][0], p.m, p.count, p.ld_x, kStep, kHalf / 64);
   if (which < kRightT) return k(p.x[which - kRightX][0], p.n, p.ld_x, w.gram / 2);
-  if (which < kWideX) return k(p.t[which - kRightT], p.m, p.ld_a, w.sym / 2);
-  return make_slab_stack_map(map, p.x[which - kWideX][0], p.m, p.count, p.ld_x, kStep, w.update / 128);
+  if (which < kUpdateT) return k(p.t[which - kRightT], p.m, p.ld_a, w.sym / 2);
+  return k(p.t[which - kUpdateT], p.m, p.ld_a, w.update / 2);
 }
 
 Limits limits_of(const TcLaunch& l) { return Limits{l.err, TIDE_BULK_TIMEOUT_NS, l.stall_ns, l.late_ns}; }
@@ -726,9 +754,9 @@ Phase phase_of(const OrthoPlan& p, const OrthoProduct& q, const Widths& w, int64
   const bool update = q.form >= kUpdate;
   k.width = w.of(q.form);
   k.form = q.form;
-  k.left = q.form == kGram ? kLeftX + q.turn : kLeftT + q.left;
-  k.right = q.form == kGram ? kRightX + q.turn : q.form == kSym ? kRightT + q.right : kWideX + q.turn;
-  k.m = p.m, k.wide = update ? p.n : p.m;
+  k.left = q.form == kGram ? kLeftX + q.turn : q.form == kSym ? kLeftT + q.left : kWideX + q.turn;
+  k.right = q.form == kGram ? kRightX + q.turn : (update ? kUpdateT : kRightT) + q.right;
+  k.m = update ? p.n : p.m, k.wide = p.m;
   k.steps = (int)ceil_div(q.form == kGram ? p.n : p.m, kStep);
   k.planes = q.form == kGram ? 0 : q.form == kSym && q.left == q.right ? 1 : 2;
   k.in[0] = update ? p.x[q.turn][0] : p.t[q.left], k.in[1] = update ? p.x[q.turn][1] : p.t[q.right];
@@ -741,7 +769,7 @@ Phase phase_of(const OrthoPlan& p, const OrthoProduct& q, const Widths& w, int64
   k.out_scale = q.form == kLast ? 1.0f : q.out_scale;
   k.tall = p.tall, k.ld_out = ld_dst;
   if (update)
-    k.grid = TileGrid((int)ceil_div(p.m, 2 * kHalf), (int)ceil_div(p.n, k.width));
+    k.grid = TileGrid((int)ceil_div(p.n, 2 * kHalf), (int)ceil_div(p.m, k.width));
   else
     k.each = Divisor((int)triangle(p.m, k.width));
   return k;
@@ -822,7 +850,7 @@ double product_time(int64_t tiles, int64_t pairs, int steps, int width) {
 Way way_of(const OrthoPlan& p, const OrthoProduct* q, int products, const TcDevice& dev) {
   int grams = 0, syms = 0, updates = 0;
   for (int i = 0; i < products; ++i) ++(q[i].form == kGram ? grams : q[i].form == kSym ? syms : updates);
-  const int64_t down = ceil_div(p.m, 2 * kHalf);
+  const int64_t down = ceil_div(p.n, 2 * kHalf);
   const int long_steps = (int)ceil_div(p.n, kStep), short_steps = (int)ceil_div(p.m, kStep);
   // the widths that take the least time with so many pairs for so many matrices
   const auto best_of = [&](int64_t matrices, int64_t pairs, Widths* w) {
@@ -830,7 +858,7 @@ Way way_of(const OrthoPlan& p, const OrthoProduct* q, int products, const TcDevi
     for (int width = 64; width <= 256; width *= 2) {
       const double t[3] = {product_time(matrices * triangle(p.m, width), pairs, long_steps, width),
                            product_time(matrices * triangle(p.m, width), pairs, short_steps, width),
-                           width < 128 ? 1e30 : product_time(matrices * down * ceil_div(p.n, width), pairs, short_steps, width)};
+                           product_time(matrices * down * ceil_div(p.m, width), pairs, short_steps, width)};
       int* const at[3] = {&w->gram, &w->sym, &w->update};
       for (int f = 0; f < 3; ++f)
         if (width == 64 || t[f] <= least[f]) least[f] = t[f], *at[f] = width;
