@@ -159,6 +159,10 @@ cudaError_t launch_early(void (*kernel)(P...), dim3 grid, unsigned block, size_t
   return cudaLaunchKernelEx(&c, kernel, P(args)...);
 }
 
+// Clusters of 2 to `most` pairs of CTAs that the device holds at one time, by
+// their number of pairs; 0 where it takes none of more than 8 CTAs.
+cudaError_t held_clusters(const void* kernel, int threads, size_t smem, int most, int* held);
+
 // Clusters of 2 to 4 pairs of CTAs that work on one tile, each pair on a part
 // of its contraction.  A cluster lies within one GPC, so the device holds
 // fewer than it has SMs by their size.
@@ -166,7 +170,7 @@ constexpr int kMaxSplit = 4;
 struct PairClusters {
   int held[kMaxSplit + 1];  // at one time, of so many pairs
 
-  cudaError_t prepare(const void* kernel, int threads, size_t smem);
+  cudaError_t prepare(const void* kernel, int threads, size_t smem) { return held_clusters(kernel, threads, smem, kMaxSplit, held); }
   // Pairs for a tile: as many as all tiles find at one time, each with at
   // least eight stages, or 1, as with fewer stages than `least` in all.
   int split(int64_t tiles, int64_t stages, int least) const {
@@ -181,13 +185,16 @@ struct PairClusters {
 constexpr int kMaxCluster = 8;
 using FewClusters = int[kMaxCluster + 1];
 
+// Pairs of CTAs that keep a matrix through all its products (ortho_tc.cu).
+constexpr int kMaxTeam = 8;
+
 // What a device holds at one time, which the splits go by.  A handle keeps its
 // own device's.
 struct TcDevice {
   int sms;
   int pairs;               // of CTAs
   PairClusters gated, fp8;  // of the split kernels
-  PairClusters ortho;       // that keep a matrix
+  int ortho[kMaxTeam + 1];  // of clusters that keep a matrix
   FewClusters few[4][3][2];  // by kind, tile of tokens and activation
 };
 

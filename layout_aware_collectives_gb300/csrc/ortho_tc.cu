@@ -635,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 2) tmem_free<2>(tmem, 512);
 }
 
-// All products of one matrix by a cluster of one to four pairs, which meet
+// All products of one matrix by a cluster of one to eight pairs, which meet
 // between two products: what a launch, its set-up and its last tiles cost is
 // paid once, and a matrix's planes stay in L2 from one product to the next.
 __global__ void __launch_bounds__(kThreads, 1)
@@ -833,11 +833,12 @@ struct Way {
 
 // By the time it takes, in stages of 256 columns (0.27 us): a tile's sum or its
 // results' way out, whichever is longer, as one hides behind the other but for the
-// last; and what a product costs besides, alone and in a chain.  Measured (all
-// pairs; one to four pairs a matrix): 704 x 256 105 us; 173, 129, 118, 100.  64
-// of 256 x 704 220; 197, 281, 365, 497.  16 of 300 x 300 132; 273, 164, 125, 213.
-// 100 of 128 x 512 221; 249, 273, 435, 549.  Three of 1021 x 1375 207; 1510, 814,
-// 718, 593, 128 of 768 x 2048 2464; 3211, 2979, 2990, 3851.
+// last; and what a product costs besides, alone and in a chain.  Measured, in us
+// (all pairs; one, two, three, four, six, eight pairs a matrix): 704 x 256 91; 159,
+// 112, 100, 85, 75, 76.  128 x 2048 96; 163, 113, 103, 94, 92, 83.  64 of 256 x
+// 704 218; 189, 246, 316, 430, 596, 732.  16 of 300 x 300 130; 246, 146, 114, 194,
+// 152, 220.  100 of 128 x 512 176; 189, 211, 335, 433, 784, 898.  Three of 1021 x
+// 1375 195; 1601, 859, 654, 536, 386, 330.
 constexpr double kLaunch = 16, kMeet = 12;
 double tile_time(int steps, int width) {
   const double stage = width == 256 ? 1.0 : width == 128 ? 0.65 : 0.55, out = 2 + width / 16;
@@ -867,9 +868,8 @@ Way way_of(const OrthoPlan& p, const OrthoProduct* q, int products, const TcDevi
   };
   Way best{};
   double least = best_of(p.count, dev.pairs, &best.widths) + products * kLaunch;
-  for (int pairs = 1; pairs <= kMaxSplit && products <= kMaxPhases; ++pairs) {
-
-    const int held = pairs == 1 ? dev.pairs : dev.ortho.held[pairs];
+  for (int pairs = 1; pairs <= kMaxTeam && products <= kMaxPhases; ++pairs) {
+    const int held = pairs == 1 ? dev.pairs : dev.ortho[pairs];
     if (held < 1) continue;
     Way way{pairs, {}};
     const double all = (double)ceil_div(p.count, held) * (best_of(1, pairs, &way.widths) + products * kMeet) + kLaunch;
@@ -887,8 +887,9 @@ cudaError_t ortho_prepare(TcDevice* dev) {
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e != cudaSuccess) return e;
   }
-  const cudaError_t e = cudaFuncSetAttribute(ortho_chain_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
-  return e != cudaSuccess ? e : dev->ortho.prepare((const void*)ortho_chain_kernel, kThreads, kSmem);
+  cudaError_t e = cudaFuncSetAttribute(ortho_chain_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(ortho_chain_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  return e != cudaSuccess ? e : held_clusters((const void*)ortho_chain_kernel, kThreads, kSmem, kMaxTeam, dev->ortho);
 }
 
 cudaError_t launch_ortho_products(const OrthoPlan& p, const OrthoProduct* q, int products, const OrthoArgs& a, const TcLaunch& l,

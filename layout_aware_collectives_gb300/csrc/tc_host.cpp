@@ -68,8 +68,8 @@ bool make_slab_stack_map(CUtensorMap* map, const void* p, int64_t rows, int64_t 
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-cudaError_t PairClusters::prepare(const void* kernel, int threads, size_t smem) {
-  for (int s = 2; s <= kMaxSplit; ++s) {
+cudaError_t held_clusters(const void* kernel, int threads, size_t smem, int most, int* held) {
+  for (int s = 2; s <= most; ++s) {
     cudaLaunchAttribute cluster;
     cluster.id = cudaLaunchAttributeClusterDimension;
     cluster.val.clusterDim = {2u * s, 1, 1};
@@ -80,7 +80,10 @@ cudaError_t PairClusters::prepare(const void* kernel, int threads, size_t smem) 
     c.attrs = &cluster;
     c.numAttrs = 1;
     const cudaError_t e = cudaOccupancyMaxActiveClusters(&held[s], kernel, &c);
-    if (e != cudaSuccess) return e;
+    if (e == cudaSuccess) continue;
+    if (s <= 4) return e;
+    held[s] = 0;  // more CTAs than any device has to take in one cluster
+    (void)cudaGetLastError();
   }
   return cudaSuccess;
 }
