@@ -1,10 +1,9 @@
 // Tokens' rows to their experts and back: one pass over the rows, bound by
-// HBM.  A thread takes 16 bytes of a token's row (V = 8; single elements where
-// rows do not start on 16 bytes) and the same of each of its topk rows.  8191
-// tokens of 2048 there, 8 choices each: 48 us (6.3 TB/s); 4096 of them back 25
-// (6.0), backward 51 (5.6).  2000 of 2049, by single elements: 32, 46 and 52 us.
-// (Pieces put together from the two aligned ones that hold them, for widths
-// like that: 34, 77 and 106, as their ends cost more than the rest saves.)
+// HBM.  A thread takes 16 bytes of a token's row and the same of each of its
+// topk rows.  8191 tokens of 2048 there, 8 choices each: 48 us (6.3 TB/s); 4096
+// of them back 25 (6.0), backward 51 (5.6).  Rows that do not start on 16 bytes
+// take windows of as many, or single elements: 2000 of 2049 there 22 us, back 27,
+// backward 52.
 #include "compute_device.cuh"
 
 namespace tide {
@@ -99,8 +98,9 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(RowsArgs a, Shape s) {
 }
 
 // U pieces of a row at a time, so that U K loads of a thread are on their way.
-template <int V, int K, int U>
+template <int K, int U>
 __global__ void __launch_bounds__(kThreads) combine_kernel(RowsArgs a, Shape s) {
+  constexpr int V = 8;
   after_previous();
   const int64_t t = (int64_t)blockIdx.x * s.tokens + threadIdx.x / s.lanes;
   if (t >= a.tokens) return;
@@ -218,22 +218,175 @@ __global__ void __launch_bounds__(kThreads) combine_backward_kernel(RowsArgs a, 
   }
 }
 
+// ------------------------------------------- rows that do not start on 16 bytes
+
+// Such rows are written by windows of 8 elements that start on 16 bytes; the
+// same elements of another row lie in two blocks of 16 bytes, and are put together
+// from them.  A row's first and last window have elements outside it, which are
+// read where the matrix has them and count for nothing; a window whose blocks
+// pass the matrix's ends is read by elements.  (4183 tokens of 4039, 5 choices:
+// there 109 us by elements, 55 by windows; back 158 and 68.  Backward, where
+// two rows are put together for each choice: 161 and 217, so by elements.)
+
+// Where a matrix's elements lie.
+struct Extent {
+  uintptr_t lo, hi;
+  __device__ __forceinline__ Extent(const uint16_t* p, int64_t rows, int64_t ld, int64_t cols)
+      : lo((uintptr_t)p), hi((uintptr_t)(p + (rows - 1) * ld + cols)) {}
+  // Whether the blocks of the 8 elements from p on lie within.
+  __device__ __forceinline__ bool holds(const uint16_t* p) const {
+    const uintptr_t first = (uintptr_t)p & ~(uintptr_t)15;
+    return first >= lo && first + ((uintptr_t)p & 15 ? 32 : 16) <= hi;
+  }
+};
+
+__device__ __forceinline__ int phase_of(const uint16_t* p) { return (int)((uintptr_t)p >> 1 & 7); }
+
+// The blocks of 8 elements, and those elements out of them.
+struct Blocks {
+  uint4 a, b;
+  __device__ __forceinline__ void load(const uint16_t* p) {
+    const uint4* q = (const uint4*)((uintptr_t)p & ~(uintptr_t)15);
+    a = q[0];
+    b = (uintptr_t)p & 15 ? q[1] : make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ Piece<8> at(uint32_t by) const {  // from so many bytes on
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = by & 8 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = by & 4 ? w[i + 1] : w[i];
+    Piece<8> r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.w[i] = __funnelshift_r(w[i], w[i + 1], by & 2 ? 16 : 0);
+    return r;
+  }
+};
+// The 8 elements from e on of a row of `cols`, 0 for those outside it.
+__device__ __noinline__ uint4 by_elements(const uint16_t* row, int64_t e, int64_t cols) {
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (e + i >= 0 && e + i < cols) w[i / 2] |= (uint32_t)row[e + i] << (i % 2 * 16);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ Piece<8> window(const uint16_t* row, int64_t e, int64_t cols, const Extent& x) {
+  if (x.holds(row + e)) {
+    Blocks b;
+    b.load(row + e);
+    return b.at((uintptr_t)(row + e) & 15);
+  }
+  const uint4 q = by_elements(row, e, cols);
+  return Piece<8>{{q.x, q.y, q.z, q.w}};
+}
+// The 15 elements that windows of other rows, by their phases, have here: from
+// 7 before the q-th 8 on.
+__device__ __forceinline__ Blocks around(const uint16_t* row, int64_t q, int64_t cols, const Extent& x) {
+  const Piece<8> a = window(row, q * 8 - 7, cols, x), b = window(row, q * 8 + 1, cols, x);
+  return Blocks{make_uint4(a.w[0], a.w[1], a.w[2], a.w[3]), make_uint4(b.w[0], b.w[1], b.w[2], b.w[3])};
+}
+// To the 8 elements from e on of a row of `cols`, those outside it left out.
+__device__ __forceinline__ void store_window(uint16_t* row, int64_t e, int64_t cols, const Piece<8>& v) {
+  if (e >= 0 && e + 8 <= cols) {
+    store<8>(row + e, v);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (e + i >= 0 && e + i < cols) row[e + i] = (uint16_t)(v.w[i / 2] >> (i % 2 * 16));
+}
+
+template <int K>
+__global__ void __launch_bounds__(kThreads) gather_windows_kernel(RowsArgs a, Shape s) {
+  after_previous();
+  const int64_t t = (int64_t)blockIdx.x * s.tokens + threadIdx.x / s.lanes;
+  if (t >= a.tokens) return;
+  const Extent x(a.in, a.tokens, a.ld_in, a.hidden);
+  const uint16_t* from = a.in + t * a.ld_in;
+  const int64_t p0 = t * a.topk;
+  for (int j0 = 0; j0 < a.topk; j0 += K) {
+    Slots<K> at;
+    at.load(a, p0 + j0, a.topk - j0);
+    for (int64_t q = threadIdx.x % s.lanes; q < s.pieces; q += s.lanes) {
+      const Blocks v = around(from, q, a.hidden, x);
+#pragma unroll
+      for (int j = 0; j < K; ++j) {
+        if (at.row[j] < 0) continue;
+        uint16_t* to = a.out + at.row[j] * a.ld_out;
+        const int phase = phase_of(to);
+        if (q * 8 - phase < a.hidden) store_window(to, q * 8 - phase, a.hidden, v.at(2 * (7 - phase)));
+      }
+    }
+  }
+}
+
+template <int K>
+__global__ void __launch_bounds__(kThreads) combine_windows_kernel(RowsArgs a, Shape s) {
+  after_previous();
+  const int64_t t = (int64_t)blockIdx.x * s.tokens + threadIdx.x / s.lanes;
+  if (t >= a.tokens) return;
+  const Extent x(a.in, a.num_rows, a.ld_in, a.hidden);
+  uint16_t* to = a.out + t * a.ld_out;
+  const int64_t p0 = t * a.topk;
+  Slots<K> at;
+  at.load(a, p0, a.topk);
+  for (int64_t q = threadIdx.x % s.lanes; q < s.pieces; q += s.lanes) {
+    const int64_t e = q * 8 - phase_of(to);
+    if (e >= a.hidden) break;
+    float sum[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum[i] = 0.0f;
+    const auto add = [&](const Piece<8>& v, float w) {
+      float f[8];
+      values<8>(v, f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[i] = fmaf(w, f[i], sum[i]);
+    };
+    for (int j0 = 0;;) {
+      bool within = true;
+#pragma unroll
+      for (int j = 0; j < K; ++j) within = within && (at.row[j] < 0 || x.holds(a.in + at.row[j] * a.ld_in + e));
+      if (within) {
+        Blocks b[K];
+#pragma unroll
+        for (int j = 0; j < K; ++j)
+          if (at.row[j] >= 0) b[j].load(a.in + at.row[j] * a.ld_in + e);
+#pragma unroll
+        for (int j = 0; j < K; ++j)
+          if (at.row[j] >= 0) add(b[j].at((uintptr_t)(a.in + at.row[j] * a.ld_in + e) & 15), at.w[j]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < K; ++j)
+          if (at.row[j] >= 0) {
+            const uint4 v = by_elements(a.in + at.row[j] * a.ld_in, e, a.hidden);
+            add(Piece<8>{{v.x, v.y, v.z, v.w}}, at.w[j]);
+          }
+      }
+      if (a.topk <= K) break;
+      j0 = j0 + K < a.topk ? j0 + K : 0;
+      at.load(a, p0 + j0, a.topk - j0);
+      if (j0 == 0) break;
+    }
+    store_window(to, e, a.hidden, rounded<8>(sum));
+  }
+}
+
 // As many lanes a token as it takes to give every SM `busy` threads, and no
 // more than a row has pieces: fewer threads that stay longer wait less for
 // slots, more have more loads on their way.  (4093 tokens x 2048 x 8, backward:
 // 51 us with 256 to 768 threads, 57 with 1024, 79 with a CTA a token; results
 // of 4096 x 4096 x 2 back: 19.6, 21 and 32; 8191 x 2048 x 8 there: 53 with up
 // to 1024, 48.6 with 2048.)
-Shape shape_of(const RowsArgs& a, int v, int64_t busy) {
+Shape shape_of(const RowsArgs& a, int64_t pieces, int64_t busy) {
   constexpr int64_t kSms = 152;
-  Shape s{1, 0, a.hidden / v};
+  Shape s{1, 0, pieces};
   while (s.lanes < kThreads && s.lanes < s.pieces && (s.lanes < 32 || s.lanes * a.tokens < kSms * busy)) s.lanes *= 2;
   s.tokens = kThreads / s.lanes;
   return s;
 }
 
-cudaError_t run(void (*kernel)(RowsArgs, Shape), const RowsArgs& a, int v, int64_t busy, cudaStream_t stream) {
-  const Shape s = shape_of(a, v, busy);
+cudaError_t run(void (*kernel)(RowsArgs, Shape), const RowsArgs& a, int64_t pieces, int64_t busy, cudaStream_t stream) {
+  const Shape s = shape_of(a, pieces, busy);
   return launch_early(kernel, dim3((unsigned)ceil_div(a.tokens, s.tokens)), kThreads, 0, 0, stream, a, s);
 }
 
@@ -241,23 +394,34 @@ bool by8(const RowsArgs& a) {
   return a.hidden % 8 == 0 && a.ld_in % 8 == 0 && (!a.out || a.ld_out % 8 == 0) && (!a.dweights || a.ld_rows % 8 == 0);
 }
 
+// At most, of one row.
+int64_t windows(const RowsArgs& a) { return (a.hidden + 14) / 8; }
+
 }  // namespace
 
 cudaError_t launch_expert_gather(const RowsArgs& a, cudaStream_t stream) {
-  if (!by8(a)) return run(a.topk <= 2 ? gather_kernel<1, 2> : gather_kernel<1, 8>, a, 1, 2048, stream);
-  return run(a.topk <= 2 ? gather_kernel<8, 2> : gather_kernel<8, 8>, a, 8, 2048, stream);
+  if (by8(a)) return run(a.topk <= 2 ? gather_kernel<8, 2> : gather_kernel<8, 8>, a, a.hidden / 8, 2048, stream);
+  // a short row's ends, which are written by elements, cost more than the rest
+  // saves (4000 tokens of 333, 8 choices, their order too: 22 us, 19 by
+  // elements; 8000 of 1023, 10 choices: 69 and 101)
+  if (a.hidden < 512) return run(a.topk <= 2 ? gather_kernel<1, 2> : gather_kernel<1, 8>, a, a.hidden, 2048, stream);
+  return run(a.topk <= 2 ? gather_windows_kernel<2> : gather_windows_kernel<8>, a, windows(a), 2048, stream);
 }
 
 cudaError_t launch_expert_combine(const RowsArgs& a, cudaStream_t stream) {
-  if (!by8(a))
-    return run(a.topk <= 2 ? combine_kernel<1, 2, 4> : a.topk <= 4 ? combine_kernel<1, 4, 2> : combine_kernel<1, 8, 1>, a, 1, 2048, stream);
-  if (a.topk <= 4) return run(a.topk <= 2 ? combine_kernel<8, 2, 4> : combine_kernel<8, 4, 2>, a, 8, 512, stream);
-  return run(combine_kernel<8, 8, 1>, a, 8, 2048, stream);
+  if (by8(a)) {
+    if (a.topk <= 4) return run(a.topk <= 2 ? combine_kernel<2, 4> : combine_kernel<4, 2>, a, a.hidden / 8, 512, stream);
+    return run(combine_kernel<8, 1>, a, a.hidden / 8, 2048, stream);
+  }
+  return run(a.topk <= 2   ? combine_windows_kernel<2>
+             : a.topk <= 4 ? combine_windows_kernel<4>
+                           : combine_windows_kernel<8>,
+             a, windows(a), 512, stream);
 }
 
 cudaError_t launch_expert_combine_backward(const RowsArgs& a, cudaStream_t stream) {
-  if (!by8(a)) return run(a.topk <= 2 ? combine_backward_kernel<1, 2, 8> : combine_backward_kernel<1, 8, 4>, a, 1, 256, stream);
-  return run(a.topk <= 2 ? combine_backward_kernel<8, 2, 1> : combine_backward_kernel<8, 8, 1>, a, 8, 512, stream);
+  if (by8(a)) return run(a.topk <= 2 ? combine_backward_kernel<8, 2, 1> : combine_backward_kernel<8, 8, 1>, a, a.hidden / 8, 512, stream);
+  return run(a.topk <= 2 ? combine_backward_kernel<1, 2, 8> : combine_backward_kernel<1, 8, 4>, a, a.hidden, 256, stream);
 }
 
 }  // namespace tide

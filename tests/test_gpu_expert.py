@@ -275,6 +275,54 @@ def test_combine_backward(compute, tokens, hidden, topk, pad, weighted, missing,
     assert drows.intact() and dw.intact()
 
 
+def among_nan(x, ld):
+    """x's rows `ld` apart, NaN between them and nothing behind the last."""
+    held = torch.full(((x.shape[0] - 1) * ld + x.shape[1],), math.nan, dtype=x.dtype, device="cuda")
+    view = held.as_strided(x.shape, (ld, 1))
+    view.copy_(x)
+    return view
+
+
+@pytest.mark.parametrize("hidden", [1, 7, 9, 511, 512, 513, 517, 520, 1035])
+@pytest.mark.parametrize("topk", [1, 3, 9])
+@pytest.mark.parametrize("pads", [(0, 1), (1, 0), (3, 6), (2, 5), (7, 7)])
+def test_rows_from_any_element_on(compute, hidden, topk, pads):
+    """Rows of the tokens and of the experts that start on other parts of 16
+    bytes, there, back and backward; what lies between rows is neither used nor written."""
+    g = gen(hidden + topk)
+    tokens = 19
+    n = tokens * topk + 2
+    ld_t, ld_r = hidden + pads[0], hidden + pads[1]
+    x, rows = randn(g, tokens, hidden, dtype=torch.bfloat16), randn(g, n, hidden, dtype=torch.bfloat16)
+    slots = some_slots(g, tokens, topk, n, False)
+    slots[0, 0], slots[-1, -1] = n - 1, 0  # both ends, once each
+    used, count = torch.unique(slots, return_counts=True)
+    for twice in used[count > 1]:  # a slot that this left to two pairs goes to the first
+        at = (slots == twice).nonzero()
+        keep = 0 if twice == n - 1 else len(at) - 1
+        for i, (a, b) in enumerate(at.tolist()):
+            if i != keep:
+                slots[a, b] = -1
+    inside = slots >= 0
+    w = randn(g, tokens, topk)
+    got = Guarded(n, hidden, ld_r)
+    want = got.view.clone()
+    compute.expert_gather(tokens, hidden, topk, among_nan(x, ld_t), slots, got, n, ld_x=ld_t, ld_rows=ld_r)
+    want[slots[inside].long()] = x.repeat_interleave(topk, 0)[inside.view(-1)]
+    assert torch.equal(got.view.view(torch.int16), want.view(torch.int16)) and got.intact()
+    y = Guarded(tokens, hidden, ld_t)
+    compute.expert_combine(tokens, hidden, topk, among_nan(rows, ld_r), n, slots, w, y, ld_rows=ld_r, ld_y=ld_t)
+    close(y.view, *ref.combine(rows, slots, w))
+    assert y.intact()
+    drows, dw = Guarded(n, hidden, ld_t), Guarded(tokens, topk, dtype=torch.float32)
+    compute.expert_combine_backward(tokens, hidden, topk, among_nan(x, ld_t), among_nan(rows, ld_r), n, slots, w, drows, dw, ld_dy=ld_t,
+                                    ld_rows=ld_r, ld_drows=ld_t)
+    each, each_bound, want_dw, dw_bound = ref.combine_backward(x, rows, slots, w)
+    close(drows.view[slots[inside].long()], each[inside], each_bound[inside])
+    close(dw.view, want_dw, dw_bound)
+    assert drows.intact() and dw.intact()
+
+
 # ------------------------------------------------------- orthogonalisation
 
 MATRICES = [(1, 1, 1), (1, 1, 7), (2, 7, 1), (3, 5, 9), (1, 64, 64), (2, 65, 130), (1, 300, 77), (1, 704, 256), (3, 250, 250), (2, 128, 1000),
