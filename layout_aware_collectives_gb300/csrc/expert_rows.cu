@@ -225,8 +225,9 @@ __global__ void __launch_bounds__(kThreads) combine_backward_kernel(RowsArgs a, 
 // from them.  A row's first and last window have elements outside it, which are
 // read where the matrix has them and count for nothing; a window whose blocks
 // pass the matrix's ends is read by elements.  (4183 tokens of 4039, 5 choices:
-// there 109 us by elements, 55 by windows; back 158 and 68.  Backward, where
-// two rows are put together for each choice: 161 and 217, so by elements.)
+// there 109 us by elements, 55 by windows; back 158 and 68.  Backward, whose
+// windows take registers for two rows of each choice: 161 and 164 at best, and
+// 53 and 71 for 2000 of 2049, so by elements.)
 
 // Where a matrix's elements lie.
 struct Extent {
