@@ -12,7 +12,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kFlight = 4;       // 16-byte loads of a lane on their way
 constexpr int kMaxParts = 1216;  // eight CTAs an SM
 
 struct Sources {
@@ -51,6 +50,7 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(OrthoPlan p, Sources s, 
                                                         int64_t ld) {
   after_previous();
   constexpr int V = VEC ? 16 / sizeof(T) : 1;
+  constexpr int kFlight = VEC ? 4 : 16;  // loads of a lane on their way
   __shared__ double shared[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   double sum = 0.0;

@@ -833,46 +833,46 @@ struct Way {
 
 // By the time it takes, in stages of 256 columns (0.27 us): a tile's sum or its
 // results' way out, whichever is longer, as one hides behind the other but for the
-// last; and what a product costs besides, alone and in a chain.  Measured, in us
-// (all pairs; one, two, three, four, six, eight pairs a matrix): 704 x 256 91; 159,
-// 112, 100, 85, 75, 76.  128 x 2048 96; 163, 113, 103, 94, 92, 83.  64 of 256 x
-// 704 218; 189, 246, 316, 430, 596, 732.  16 of 300 x 300 130; 246, 146, 114, 194,
-// 152, 220.  100 of 128 x 512 176; 189, 211, 335, 433, 784, 898.  Three of 1021 x
-// 1375 195; 1601, 859, 654, 536, 386, 330.
-constexpr double kLaunch = 16, kMeet = 12;
-double tile_time(int steps, int width) {
-  const double stage = width == 256 ? 1.0 : width == 128 ? 0.65 : 0.55, out = 2 + width / 16;
-  return std::fmax(steps * stage, out);
-}
+// last; and what a product costs besides, in a chain or alone, where half of the
+// device's SMs is free for the next one's CTAs to set up or is not.  Measured, in
+// us (all pairs; one, two, three, four, six, eight pairs a matrix): 704 x 256 88;
+// 158, 106, 95, 85, 75, 75.  128 x 2048 96; 163, 113, 103, 94, 92, 83.  64 of 256 x
+// 704 218; 189, 235, 300, 430, 595, 731.  16 of 300 x 300 130; 232, 140, 114, 196,
+// 151, 220.  100 of 128 x 512 171; 188, 211, 334, 433, 781, 897.  512 x 768 107; 375,
+// 248, 180, 175, 119, 119.
+constexpr double kMeet = 12, kLaunch = 16, kLaunchFull = 18;
+double way_out(int width) { return 4.4 + width / 22.0; }
 double product_time(int64_t tiles, int64_t pairs, int steps, int width) {
-  return (double)ceil_div(tiles, pairs) * tile_time(steps, width) + std::fmin(steps, 2 + width / 16);
+  const double sum = steps * (width == 256 ? 1.0 : width == 128 ? 0.65 : 0.55), out = way_out(width);
+  return (double)ceil_div(tiles, pairs) * std::fmax(sum, out) + std::fmin((double)steps, out);
 }
 
 Way way_of(const OrthoPlan& p, const OrthoProduct* q, int products, const TcDevice& dev) {
-  int grams = 0, syms = 0, updates = 0;
-  for (int i = 0; i < products; ++i) ++(q[i].form == kGram ? grams : q[i].form == kSym ? syms : updates);
+  int number[3] = {};  // of products: gram, sym, update and last
+  for (int i = 0; i < products; ++i) ++number[q[i].form == kGram ? 0 : q[i].form == kSym ? 1 : 2];
   const int64_t down = ceil_div(p.n, 2 * kHalf);
   const int long_steps = (int)ceil_div(p.n, kStep), short_steps = (int)ceil_div(p.m, kStep);
   // the widths that take the least time with so many pairs for so many matrices
-  const auto best_of = [&](int64_t matrices, int64_t pairs, Widths* w) {
+  const auto best_of = [&](int64_t matrices, int64_t pairs, bool chain, Widths* w) {
     double least[3] = {};
     for (int width = 64; width <= 256; width *= 2) {
-      const double t[3] = {product_time(matrices * triangle(p.m, width), pairs, long_steps, width),
-                           product_time(matrices * triangle(p.m, width), pairs, short_steps, width),
-                           product_time(matrices * down * ceil_div(p.m, width), pairs, short_steps, width)};
       int* const at[3] = {&w->gram, &w->sym, &w->update};
-      for (int f = 0; f < 3; ++f)
-        if (width == 64 || t[f] <= least[f]) least[f] = t[f], *at[f] = width;
+      for (int f = 0; f < 3; ++f) {
+        const int64_t tiles = matrices * (f < 2 ? triangle(p.m, width) : down * ceil_div(p.m, width));
+        const double t = product_time(tiles, pairs, f == 0 ? long_steps : short_steps, width) +
+                         (chain ? kMeet : 2 * tiles > pairs ? kLaunchFull : kLaunch);
+        if (width == 64 || t <= least[f]) least[f] = t, *at[f] = width;
+      }
     }
-    return grams * least[0] + syms * least[1] + updates * least[2];
+    return number[0] * least[0] + number[1] * least[1] + number[2] * least[2];
   };
   Way best{};
-  double least = best_of(p.count, dev.pairs, &best.widths) + products * kLaunch;
+  double least = best_of(p.count, dev.pairs, false, &best.widths);
   for (int pairs = 1; pairs <= kMaxTeam && products <= kMaxPhases; ++pairs) {
     const int held = pairs == 1 ? dev.pairs : dev.ortho[pairs];
     if (held < 1) continue;
     Way way{pairs, {}};
-    const double all = (double)ceil_div(p.count, held) * (best_of(1, pairs, &way.widths) + products * kMeet) + kLaunch;
+    const double all = (double)ceil_div(p.count, held) * best_of(1, pairs, true, &way.widths) + kLaunch;
     if (all < least) least = all, best = way;
   }
   return best;
