@@ -277,10 +277,15 @@ __device__ __forceinline__ void send_last(uint32_t box, const Places& at, uint16
     send_box(box, at, to + (lane >> 2) * ld + (lane & 3) * 8, 8 * ld, rows - (lane >> 2));
     return;
   }
-  for (int r = 0; r < 32 && r < rows; ++r) {
-    uint16_t v;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(box + piece_at(r, lane >> 3) + (lane & 7) * 2) : "memory");
-    if (lane < cols) to[r * ld + lane] = v;
+  to += lane;
+  for (int r = 0; r < 32 && r < rows; r += 8, to += 8 * ld) {
+    uint16_t v[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v[q]) : "r"(box + piece_at(r + q, lane >> 3) + (lane & 7) * 2) : "memory");
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (r + q < rows && lane < cols) to[q * ld] = v[q];
   }
 }
 
