@@ -326,7 +326,8 @@ def test_rows_from_any_element_on(compute, hidden, topk, pads):
 # ------------------------------------------------------- orthogonalisation
 
 MATRICES = [(1, 1, 1), (1, 1, 7), (2, 7, 1), (3, 5, 9), (1, 64, 64), (2, 65, 130), (1, 300, 77), (1, 704, 256), (3, 250, 250), (2, 128, 1000),
-            (1, 513, 1024), (1, 1021, 333), (5, 256, 257), (1, 8, 5000), (4, 384, 512)]
+            (1, 513, 1024), (1, 1021, 333), (5, 256, 257), (1, 8, 5000), (4, 384, 512),
+            (1, 3457, 63), (7, 33, 2500), (16, 300, 300), (2, 64, 65), (1, 129, 4097)]
 
 
 def gradients(g, count, rows, cols, kind):
@@ -548,7 +549,7 @@ def test_expert_layer_step(compute):
         near(o, grad)
 
 
-@pytest.mark.parametrize("count,rows,cols", [(1, 100, 200), (3, 700, 1100), (1, 1500, 4000), (100, 300, 600)])
+@pytest.mark.parametrize("count,rows,cols", [(1, 100, 200), (1, 704, 256), (3, 700, 1100), (1, 1500, 4000), (100, 300, 600)])
 def test_orthogonalize_waits_that_run_out_are_reported(count, rows, cols):
     """Nothing arrives, or one warp of each CTA gives up: the call ends, is reported, and the next one is right."""
     grads = gradients(gen(count), count, rows, cols, "fp32")
