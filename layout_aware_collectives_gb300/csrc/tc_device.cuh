@@ -199,10 +199,12 @@ __device__ __forceinline__ void stores_read() {  // all but the last N groups ha
 }
 __device__ __forceinline__ void stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 // This thread's writes, before what the cluster's other threads read, or copy
-// by tensor maps, behind a cluster_meet().
+// by tensor maps, behind a cluster_meet().  The proxies' fence comes first: it
+// orders the writes before copies that come behind it, and the release, which
+// the meeting's arrival carries on, puts another CTA's copies behind it.
 __device__ __forceinline__ void publish() {
-  asm volatile("fence.acq_rel.cluster;" ::: "memory");
   asm volatile("fence.proxy.async;" ::: "memory");
+  asm volatile("fence.acq_rel.cluster;" ::: "memory");
 }
 __device__ __forceinline__ void async_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 

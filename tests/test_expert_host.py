@@ -186,3 +186,14 @@ def test_orthogonalize_definition():
             s = a * s + b * s ** 3 + c * s ** 5
         assert float((ref.orthogonalize(m) - u @ torch.diag(s) @ v).abs().max()) < 1e-10
         assert 0.6 < float(s.min()) and float(s.max()) < 1.25
+
+
+def test_published_writes_pass_the_proxies_before_the_release():
+    """What a thread has written reaches other CTAs' copies by tensor maps only if
+    the proxies' fence lies between the writes and the release that carries them."""
+    import os
+
+    csrc = os.path.join(os.path.dirname(tide.__file__), "csrc")
+    with open(os.path.join(csrc, "tc_device.cuh")) as f:
+        body = f.read().split("void publish() {")[1].split("\n}")[0]
+    assert 0 <= body.find("fence.proxy.async;") < body.find("fence.acq_rel.cluster;")
