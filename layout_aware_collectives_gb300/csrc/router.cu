@@ -117,10 +117,20 @@ struct Choice {
   int lanes;  // of a group, if groups are whole lanes' runs and those a power of two; else 0
 };
 
-// Drops the keys of groups that are not among the best.  Returns whether two
+// What a group's score is made of, by magnitude: its rounding goes by that,
+// whatever the terms come to (two of opposite signs leave theirs in a small
+// sum).  Nothing where a term is infinite or NaN, which no rounding moves.
+template <class F>
+__device__ __forceinline__ float reach_of(F best, F next) {
+  const F top = F(CUDART_INF_F);
+  return fabs(best) < top && fabs(next) < top ? (float)(fabs(best) + fabs(next)) : 0.0f;
+}
+
+// Drops the keys of groups that are not among the best.  Returns whether the
 // groups on either side of the border are no further apart than `near` times
-// (1 + their scores' magnitudes); then nothing is dropped.  `second` receives
-// the key that a group's score goes down to, where a group is whole lanes.
+// (1 + twice the largest magnitude of any group's terms), which two scores'
+// roundings stay below; then nothing is dropped.  `second` receives the key
+// that a group's score goes down to, where a group is whole lanes.
 template <int N, class K>
 __device__ __forceinline__ bool keep_groups(const Choice& c, int first, float near, K (&key)[N], K* second = nullptr) {
   using F = decltype(value_of_key(K()));
@@ -128,6 +138,7 @@ __device__ __forceinline__ bool keep_groups(const Choice& c, int first, float ne
   // Lane g's score of group g, or, where a group is whole lanes, each lane's
   // of its own group.
   K order;
+  float reach = 0.0f;
   if (c.lanes) {
     K best = 0, next = 0;
 #pragma unroll
@@ -143,7 +154,9 @@ __device__ __forceinline__ bool keep_groups(const Choice& c, int first, float ne
     }
     F score = value_of_key(best);
     const bool two = c.group_best == 2 && c.each > 1;
-    if (two) score += value_of_key(next);
+    const F rest = two ? value_of_key(next) : F(0);
+    reach = reach_of(score, rest);
+    if (two) score += rest;
     order = key_of(score);
     if (second) *second = two ? next : best;
   } else {
@@ -158,11 +171,13 @@ __device__ __forceinline__ bool keep_groups(const Choice& c, int first, float ne
         best = max(best, k);
       }
       const K top = max_key(best);
-      F score = value_of_key(top);
+      F score = value_of_key(top), rest = 0;
       if (c.group_best == 2 && c.each > 1) {
         const int owner = __ffs(__ballot_sync(0xffffffffu, best == top)) - 1;
-        score += value_of_key(max_key(lane == owner ? next : best));
+        rest = value_of_key(max_key(lane == owner ? next : best));
       }
+      reach = fmaxf(reach, reach_of(score, rest));
+      if (c.group_best == 2 && c.each > 1) score += rest;
       if (lane == g) mine = score;
     }
     order = lane < c.groups ? key_of(mine) : 0;
@@ -178,7 +193,10 @@ __device__ __forceinline__ bool keep_groups(const Choice& c, int first, float ne
     // the border: the lowest kept, the highest left
     const K low = (K)~max_key((K)~(stays ? order : (K)~(K)0)), high = max_key(in && !stays ? order : (K)0);
     const F a = value_of_key(low), b = value_of_key(high);
-    const bool close = a - b <= F(near) * (F(1) + fabs(a) + fabs(b)) && fabs(a) < F(CUDART_INF_F) && fabs(b) < F(CUDART_INF_F);
+    reach = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(reach)));
+    // (scores that leave fp32, but whose terms do not, are as good as equal here)
+    if (reach == CUDART_INF_F) return true;
+    const bool close = a - b <= F(near) * (F(1) + F(2) * F(reach)) && fabs(a) < F(CUDART_INF_F) && fabs(b) < F(CUDART_INF_F);
     if (close) return true;
   }
   const uint32_t kept = __ballot_sync(0xffffffffu, stays);

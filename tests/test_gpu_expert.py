@@ -118,6 +118,24 @@ def test_route_borders_that_32_bits_do_not_tell(compute, score, levels, e):
     check_route(compute, dict(experts=e, topk=3, score=score, groups=4, top_groups=3), logits, bias, "fp32")
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("experts,groups", [(256, 8), (100, 4), (64, 32)])
+@pytest.mark.parametrize("size", [4.0, 64.0, 1000.0, 1e6, 2e38])
+def test_route_groups_whose_terms_cancel(compute, score, experts, groups, size):
+    """Groups of two large biases of opposite signs, whose sum is small and whose
+    roundings are not, a few 1e-5 and less from one another."""
+    g = gen(14)
+    t, each = 400, experts // groups
+    noise = torch.exp(3 * torch.randn(t, 1, generator=g, device="cuda", dtype=torch.float64)) * 1e-6
+    logits = (0.5 + noise * torch.randn(t, experts, generator=g, device="cuda", dtype=torch.float64)).float()
+    bias = torch.full((groups, each), -1.5 * size, device="cuda")
+    bias[:, each // 2], bias[:, 0] = size, -size
+    if size > 1e38:  # two terms of one sign, whose sum leaves fp32
+        bias[:, 0] = size
+    kept = max(1, groups // 2)
+    check_route(compute, dict(experts=experts, topk=2, score=score, groups=groups, top_groups=kept, group_best=2), logits, bias.view(-1), "fp32")
+
+
 @pytest.mark.parametrize("router", ROUTERS)
 @pytest.mark.parametrize("biased", [False, True])
 def test_route_not_finite(compute, router, biased):
