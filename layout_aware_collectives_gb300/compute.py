@@ -70,13 +70,17 @@ class Compute:
                                workspace, workspace_bytes, stream)
 
     # -------- the expert layer
-    def route(self, router: Router, tokens: int, logits, ids, weights, bias=None, logits_type: str = "fp32",
+    def route(self, router: Router, tokens: int, logits, ids, weights, bias=None, logits_type: str | None = None,
               ld_logits=None, stream=None):
+        """logits_type: "bf16" or "fp32"; a tensor's own where it is left out,
+        fp32 of an address.  Tensors of other types than an operator reads or
+        writes are refused (TypeError), here and in the other calls."""
         _t.tide_route(self.handle, tokens, router, logits_type, logits,
                       router.experts if ld_logits is None else ld_logits, bias, ids, weights, stream)
 
-    def route_backward(self, router: Router, tokens: int, logits, ids, dweights, dlogits, logits_type: str = "fp32",
-                       ld_logits=None, ld_dlogits=None, stream=None):
+    def route_backward(self, router: Router, tokens: int, logits, ids, dweights, dlogits,
+                       logits_type: str | None = None, ld_logits=None, ld_dlogits=None, stream=None):
+        """logits_type: as in route, dlogits' too."""
         _t.tide_route_backward(self.handle, tokens, router, logits_type, logits,
                                router.experts if ld_logits is None else ld_logits, ids, dweights, dlogits,
                                router.experts if ld_dlogits is None else ld_dlogits, stream)
@@ -105,9 +109,10 @@ class Compute:
                                         hidden if ld_drows is None else ld_drows, dweights, stream)
 
     def orthogonalize(self, rows: int, cols: int, src, dst, workspace, steps: int = 5, coefficients=None,
-                      eps: float = 1e-7, src_type: str = "fp32", workspace_bytes=None, ld_src=None, ld_dst=None,
+                      eps: float = 1e-7, src_type: str | None = None, workspace_bytes=None, ld_src=None, ld_dst=None,
                       stream=None):
-        """src, dst: lists of matrices of one size; workspace_bytes: as in gated_backward."""
+        """src, dst: lists of matrices of one size; src_type: as logits_type in
+        route; workspace_bytes: as in gated_backward."""
         _t.tide_orthogonalize(self.handle, rows, cols, src_type, src, cols if ld_src is None else ld_src, dst,
                               cols if ld_dst is None else ld_dst, steps, coefficients, eps, workspace,
                               _bytes(workspace, workspace_bytes), stream)

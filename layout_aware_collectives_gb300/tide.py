@@ -156,6 +156,31 @@ def _addr(x) -> int:
     return int(x.data_ptr())
 
 
+_KINDS: dict = {}  # names of the element types seen, by their dtype
+
+
+def _kind(dtype) -> str:
+    """'float32' of torch.float32."""
+    name = _KINDS.get(dtype)
+    if name is None:
+        name = _KINDS[dtype] = str(dtype).rpartition(".")[2]
+    return name
+
+
+_BF16 = ("bfloat16", "uint16", "int16")  # bf16, or its bits
+_FP32 = ("float32",)
+_I32 = ("int32", "uint32")
+
+
+def _typed(x, kinds, what) -> int:
+    """The address of x, which is one of `kinds` if it says what it is: an
+    array's elements are read by the operator's type, whatever its own are."""
+    dtype = getattr(x, "dtype", None)
+    if dtype is not None and _kind(dtype) not in kinds:
+        raise TypeError(f"{what}: {_kind(dtype)} elements, {kinds[0]} wanted")
+    return _addr(x)
+
+
 def _stream(s) -> int:
     if s is None:
         return 0
@@ -172,6 +197,7 @@ class PointerTable:
         self.n = len(addrs)
         self.array = (ctypes.c_void_p * max(1, self.n))(*addrs)
         self.keep = list(items)  # keep tensors alive while the table exists
+        self.dtypes = {getattr(x, "dtype", None) for x in self.keep}  # None: addresses
 
     @property
     def ptr(self) -> int:
@@ -494,7 +520,23 @@ def _named(names, v, what) -> int:
 
 
 _TYPES = {"bf16": TIDE_BF16, "fp32": TIDE_FP32}
+_TYPE_KINDS = {TIDE_BF16: _BF16, TIDE_FP32: _FP32}
 _SCORES = {"softmax": TIDE_SCORE_SOFTMAX, "sigmoid": TIDE_SCORE_SIGMOID}
+
+
+def _type(given, dtypes, what) -> int:
+    """The element type that is given, which arrays that know theirs agree with;
+    theirs where none is given, and fp32 of addresses."""
+    code = None if given is None else _named(_TYPES, given, f"{what}' type")
+    for dtype in dtypes:
+        if dtype is None:
+            continue
+        own = next((c for c, kinds in _TYPE_KINDS.items() if _kind(dtype) in kinds), None)
+        if code is None:
+            code = own
+        if own is None or own != code:
+            raise TypeError(f"{what}: {_kind(dtype)} elements, {'bf16 or fp32' if code is None else 'bf16' if code == TIDE_BF16 else 'fp32'} wanted")
+    return TIDE_FP32 if code is None else code
 
 
 def _router(r):
@@ -502,17 +544,19 @@ def _router(r):
 
 
 def tide_route(compute, tokens, router, type, logits, ld_logits, bias, ids, weights, stream=None) -> None:
-    """ids and weights [tokens, topk] from logits [tokens, experts]; see include/tide.h."""
-    _check(_lib.tide_route(compute, tokens, _router(router), _named(_TYPES, type, "logits' type"), _addr(logits),
-                           ld_logits, _addr(bias), _addr(ids), _addr(weights), _stream(stream)), "tide_route")
+    """ids and weights [tokens, topk] from logits [tokens, experts]; type: theirs, or None; see include/tide.h."""
+    _check(_lib.tide_route(compute, tokens, _router(router), _type(type, (getattr(logits, "dtype", None),), "logits"),
+                           _addr(logits), ld_logits, _typed(bias, _FP32, "bias"), _typed(ids, _I32, "ids"),
+                           _typed(weights, _FP32, "weights"), _stream(stream)), "tide_route")
 
 
 def tide_route_backward(compute, tokens, router, type, logits, ld_logits, ids, dweights, dlogits, ld_dlogits,
                         stream=None) -> None:
     """dlogits [tokens, experts] from dweights [tokens, topk]."""
-    _check(_lib.tide_route_backward(compute, tokens, _router(router), _named(_TYPES, type, "logits' type"),
-                                    _addr(logits), ld_logits, _addr(ids), _addr(dweights), _addr(dlogits), ld_dlogits,
-                                    _stream(stream)), "tide_route_backward")
+    dtypes = getattr(logits, "dtype", None), getattr(dlogits, "dtype", None)
+    _check(_lib.tide_route_backward(compute, tokens, _router(router), _type(type, dtypes, "logits"), _addr(logits),
+                                    ld_logits, _typed(ids, _I32, "ids"), _typed(dweights, _FP32, "dweights"),
+                                    _addr(dlogits), ld_dlogits, _stream(stream)), "tide_route_backward")
 
 
 def expert_slots_workspace_bytes(tokens: int, topk: int, experts: int) -> int:
@@ -523,29 +567,34 @@ def expert_slots_workspace_bytes(tokens: int, topk: int, experts: int) -> int:
 def tide_expert_slots(compute, tokens, topk, experts, ids, slots, offsets, workspace, workspace_bytes,
                       stream=None) -> None:
     """slots [tokens, topk] and offsets [experts + 1] of the pairs in expert order."""
-    _check(_lib.tide_expert_slots(compute, tokens, topk, experts, _addr(ids), _addr(slots), _addr(offsets),
-                                  _addr(workspace), workspace_bytes, _stream(stream)), "tide_expert_slots")
+    _check(_lib.tide_expert_slots(compute, tokens, topk, experts, _typed(ids, _I32, "ids"), _typed(slots, _I32, "slots"),
+                                  _typed(offsets, _I32, "offsets"), _addr(workspace), workspace_bytes, _stream(stream)),
+           "tide_expert_slots")
 
 
 def tide_expert_gather(compute, tokens, hidden, topk, x, ld_x, slots, rows, num_rows, ld_rows, stream=None) -> None:
     """rows[slots[t, j]] = x[t]."""
-    _check(_lib.tide_expert_gather(compute, tokens, hidden, topk, _addr(x), ld_x, _addr(slots), _addr(rows), num_rows,
-                                   ld_rows, _stream(stream)), "tide_expert_gather")
+    _check(_lib.tide_expert_gather(compute, tokens, hidden, topk, _typed(x, _BF16, "x"), ld_x,
+                                   _typed(slots, _I32, "slots"), _typed(rows, _BF16, "rows"), num_rows, ld_rows,
+                                   _stream(stream)), "tide_expert_gather")
 
 
 def tide_expert_combine(compute, tokens, hidden, topk, rows, num_rows, ld_rows, slots, weights, y, ld_y,
                         stream=None) -> None:
     """y[t] = sum of weights[t, j] * rows[slots[t, j]]."""
-    _check(_lib.tide_expert_combine(compute, tokens, hidden, topk, _addr(rows), num_rows, ld_rows, _addr(slots),
-                                    _addr(weights), _addr(y), ld_y, _stream(stream)), "tide_expert_combine")
+    _check(_lib.tide_expert_combine(compute, tokens, hidden, topk, _typed(rows, _BF16, "rows"), num_rows, ld_rows,
+                                    _typed(slots, _I32, "slots"), _typed(weights, _FP32, "weights"),
+                                    _typed(y, _BF16, "y"), ld_y, _stream(stream)), "tide_expert_combine")
 
 
 def tide_expert_combine_backward(compute, tokens, hidden, topk, dy, ld_dy, rows, num_rows, ld_rows, slots, weights,
                                  drows, ld_drows, dweights, stream=None) -> None:
     """drows and dweights from dy."""
-    _check(_lib.tide_expert_combine_backward(compute, tokens, hidden, topk, _addr(dy), ld_dy, _addr(rows), num_rows,
-                                             ld_rows, _addr(slots), _addr(weights), _addr(drows), ld_drows,
-                                             _addr(dweights), _stream(stream)), "tide_expert_combine_backward")
+    _check(_lib.tide_expert_combine_backward(compute, tokens, hidden, topk, _typed(dy, _BF16, "dy"), ld_dy,
+                                             _typed(rows, _BF16, "rows"), num_rows, ld_rows, _typed(slots, _I32, "slots"),
+                                             _typed(weights, _FP32, "weights"), _typed(drows, _BF16, "drows"), ld_drows,
+                                             _typed(dweights, _FP32, "dweights"), _stream(stream)),
+           "tide_expert_combine_backward")
 
 
 def orthogonalize_workspace_bytes(count: int, rows: int, cols: int) -> int:
@@ -555,10 +604,14 @@ def orthogonalize_workspace_bytes(count: int, rows: int, cols: int) -> int:
 
 def tide_orthogonalize(compute, rows, cols, type, src, ld_src, dst, ld_dst, steps, coefficients, eps, workspace,
                        workspace_bytes, stream=None) -> None:
-    """src, dst: as many matrices each; coefficients: a, b, c of each step, of all steps, or None."""
+    """src, dst: as many matrices each; type: src's, or None; coefficients: a, b, c of each step, of all steps, or None."""
     s, d = _table(src), _table(dst)
     if s.n != d.n:
         raise ValueError(f"{s.n} sources, {d.n} destinations")
+    code = _type(type, s.dtypes, "gradients")
+    for dtype in d.dtypes:
+        if dtype is not None and _kind(dtype) not in _BF16:
+            raise TypeError(f"dst: {_kind(dtype)} elements, bfloat16 wanted")
     c = None
     if coefficients is not None:
         c = np.ascontiguousarray(coefficients, dtype=np.float32).reshape(-1)
@@ -566,9 +619,9 @@ def tide_orthogonalize(compute, rows, cols, type, src, ld_src, dst, ld_dst, step
             c = np.tile(c, max(1, steps))
         if c.size != 3 * max(1, steps):
             raise ValueError(f"{c.size} coefficients: three, or three for each of {steps} steps")
-    _check(_lib.tide_orthogonalize(compute, s.n, rows, cols, _named(_TYPES, type, "gradients' type"), _tptr(s),
-                                   ld_src, _tptr(d), ld_dst, steps, 0 if c is None else c.ctypes.data, eps,
-                                   _addr(workspace), workspace_bytes, _stream(stream)), "tide_orthogonalize")
+    _check(_lib.tide_orthogonalize(compute, s.n, rows, cols, code, _tptr(s), ld_src, _tptr(d), ld_dst, steps,
+                                   0 if c is None else c.ctypes.data, eps, _addr(workspace), workspace_bytes,
+                                   _stream(stream)), "tide_orthogonalize")
 
 
 def exported_symbols():

@@ -197,3 +197,75 @@ def test_published_writes_pass_the_proxies_before_the_release():
     with open(os.path.join(csrc, "tc_device.cuh")) as f:
         body = f.read().split("void publish() {")[1].split("\n}")[0]
     assert 0 <= body.find("fence.proxy.async;") < body.find("fence.acq_rel.cluster;")
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """What reaches the library's entries of an expert layer, by name."""
+    class Library:
+        def __init__(self, lib):
+            self.lib, self.made = lib, {}
+
+        def __getattr__(self, name):
+            if name not in ("tide_route", "tide_route_backward", "tide_orthogonalize", "tide_expert_slots", "tide_expert_gather",
+                            "tide_expert_combine", "tide_expert_combine_backward"):
+                return getattr(self.lib, name)
+            return lambda *args: self.made.__setitem__(name, args) or 0
+
+    library = Library(tide.tide._lib)
+    monkeypatch.setattr(tide.tide, "_lib", library)
+    return library.made
+
+
+def test_elements_are_read_as_what_they_are(compute, calls):
+    """bf16 logits and gradients without a word about their type are bf16: as fp32
+    they would be read to twice their length."""
+    r = tide.Router(8, 2)
+    ids, w = torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2)
+    for dtype, code, name in ((torch.bfloat16, 0, "bf16"), (torch.float32, 1, "fp32")):
+        logits = torch.zeros(4, 8, dtype=dtype)
+        for kw in ({}, dict(logits_type=name), dict(logits_type=code)):
+            compute.route(r, 4, logits, ids, w, **kw)
+            assert calls.pop("tide_route")[3] == code
+            compute.route_backward(r, 4, logits, ids, w, torch.zeros_like(logits), **kw)
+            assert calls.pop("tide_route_backward")[3] == code
+        m = [torch.zeros(4, 8, dtype=dtype) for _ in range(2)]
+        out = [torch.zeros(4, 8, dtype=torch.bfloat16) for _ in range(2)]
+        for src in (m, tide.PointerTable(m)):
+            for kw in ({}, dict(src_type=name)):
+                compute.orthogonalize(4, 8, src, out, A, workspace_bytes=1 << 20, **kw)
+                assert calls.pop("tide_orthogonalize")[4] == code
+    compute.route(r, 4, A, ids, w)  # an address says nothing
+    assert calls.pop("tide_route")[3] == 1
+
+
+def test_elements_of_other_types_are_refused(compute, calls):
+    r = tide.Router(8, 2)
+    z = lambda dtype, *s: torch.zeros(*(s or (4, 2)), dtype=dtype)  # noqa: E731
+    i32, i64, f32, f64, bf16, f16 = torch.int32, torch.int64, torch.float32, torch.float64, torch.bfloat16, torch.float16
+
+    def refuses(f, good, bad, **kw):
+        f(*good, **kw)
+        calls.clear()
+        for at, dtypes in bad.items():
+            for dtype in dtypes:
+                args = list(good)
+                args[at] = z(dtype)
+                with pytest.raises(TypeError):
+                    f(*args, **kw)
+        assert not calls
+
+    refuses(compute.route, [r, 4, z(f32), z(i32), z(f32)], {2: (f64, f16, i32), 3: (i64, f32), 4: (bf16, f64)})
+    refuses(compute.route, [r, 4, z(f32), z(i32), z(f32), z(f32)], {5: (bf16, f64)})
+    refuses(compute.route, [r, 4, z(f32), z(i32), z(f32)], {2: (bf16,)}, logits_type="fp32")
+    refuses(compute.route_backward, [r, 4, z(f32), z(i32), z(f32), z(f32)], {2: (bf16, f64), 3: (i64,), 4: (bf16,), 5: (bf16, f64)})
+    refuses(compute.expert_slots, [4, 2, 8, z(i32), z(i32), z(i32), A], {3: (i64,), 4: (i64,), 5: (i64, f32)}, workspace_bytes=0)
+    refuses(compute.expert_gather, [4, 2, 2, z(bf16), z(i32), z(bf16), 8], {3: (f32, f16), 4: (i64,), 5: (f32,)})
+    refuses(compute.expert_combine, [4, 2, 2, z(bf16), 8, z(i32), z(f32), z(bf16)], {3: (f32,), 5: (i64,), 6: (bf16,), 7: (f32,)})
+    refuses(compute.expert_combine_backward, [4, 2, 2, z(bf16), z(bf16), 8, z(i32), z(f32), z(bf16), z(f32)],
+            {3: (f32,), 4: (f32,), 6: (i64,), 7: (bf16,), 8: (f32,), 9: (bf16,)})
+    for src, dst, kw in (([z(f64)], [z(bf16)], {}), ([z(f32), z(bf16)], [z(bf16)] * 2, {}), ([z(f32)], [z(f32)], {}),
+                         ([z(bf16)], [z(bf16)], dict(src_type="fp32")), ([z(f32)], [z(bf16)], dict(src_type="bf16"))):
+        with pytest.raises(TypeError):
+            compute.orthogonalize(4, 2, src, dst, A, workspace_bytes=1 << 20, **kw)
+    assert not calls
