@@ -100,7 +100,8 @@ __device__ __forceinline__ float power_of(int e) { return __uint_as_float((uint3
 // The sum is q 4^h, q in [1, 4): its root is taken in 32 bits, as 64-bit
 // arithmetic would take longer than the kernel's loads.
 __device__ __forceinline__ Inverse inverse_of(double sum, float eps) {
-  if (!(sum < CUDART_INF)) return Inverse{sum == CUDART_INF ? 0.0f : CUDART_NAN_F, 1.0f, 1.0f};
+  // (a sum in 64 bits is infinite where an element is, and nowhere else)
+  if (!(sum < CUDART_INF)) return Inverse{CUDART_NAN_F, 1.0f, 1.0f};
   const uint64_t b = (uint64_t)__double_as_longlong(sum);
   const int e = (int)(b >> 52) - 1023, h = e >> 1;
   float root = 0.0f;

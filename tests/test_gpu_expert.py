@@ -452,6 +452,26 @@ def test_orthogonalize_not_finite_stays_with_its_matrix(compute):
     assert torch.equal(got[0], clean[0]) and torch.equal(got[3], clean[3])
 
 
+@pytest.mark.parametrize("steps", [0, 1, 2, 5])
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("rows,cols", [(3, 70), (130, 40)])
+def test_orthogonalize_not_finite_after_any_steps(compute, steps, kind, rows, cols):
+    """A matrix with an infinity or NaN becomes NaN all over, one without does not, however many steps."""
+    g = gen(15)
+    grads = [randn(g, rows, cols, dtype=TYPES[kind]) for _ in range(6)]
+    for m, v in zip(grads[1:], (math.nan, math.inf, -math.inf)):
+        m[rows // 2, cols // 3] = v
+    grads[4] *= 1e38 if kind == "fp32" else 2.0 ** 120  # (in fp32 a few of the larger matrix's are infinite then)
+    grads[5] *= 1e37  # its squares leave fp32, as may its norm
+    finite = [bool(torch.isfinite(m).all()) for m in grads]
+    assert finite[0] and finite[5] and not any(finite[1:4])
+    for got, grad, whole in zip(orthogonalized(compute, grads, kind, steps=steps), grads, finite):
+        if whole:
+            near(got, grad, steps=steps)
+        else:
+            assert bool(torch.isnan(got).all())
+
+
 def test_orthogonalize_many(compute):
     """More matrices than one launch takes, the same bits as one by one, every time."""
     grads = gradients(gen(8), 300, 24, 40, "bf16")
