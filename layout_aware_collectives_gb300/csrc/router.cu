@@ -234,14 +234,20 @@ __device__ __forceinline__ int pick(const Choice& c, int first, K (&key)[N]) {
 }
 
 // A lane's weight from its pick's logit, before the scale.  With
-// renormalisation a softmax goes by the picks alone; so do sigmoids of picks
-// that are all far below zero, where a sigmoid is exp(l) to fp32's last bit
-// and may itself be below what fp32 holds.
+// renormalisation a softmax goes by the picks alone; so do sigmoids where one of
+// the picks is far below zero, where a sigmoid is exp(l) to fp32's last bit and
+// may itself be below what fp32 holds, though its share is not: e^-top s for top
+// up to 0, as exp(l - top) / (1 + exp(l)).
 __device__ __forceinline__ float weight_of(float l, bool in, bool sigmoid, bool renormalize, float score) {
   if (!renormalize) return score;
   const float top = warp_max(in ? l : -CUDART_INF_F);
   float s = score;
-  if (!sigmoid || top < -60.0f) s = top == -CUDART_INF_F && l == top ? 0.0f : expf(l - top);
+  if (!sigmoid) {
+    s = top == -CUDART_INF_F && l == top ? 0.0f : expf(l - top);
+  } else if (__any_sync(0xffffffffu, in && l < -60.0f)) {
+    const float from = fminf(top, 0.0f);
+    if (l <= 0.0f) s = l == -CUDART_INF_F ? 0.0f : expf(l - from) / (1.0f + expf(l));
+  }
   if (!in) s = 0.0f;
   const float sum = warp_sum(s);
   return sum == 0.0f ? 0.0f : s / sum;

@@ -118,6 +118,29 @@ def test_route_borders_that_32_bits_do_not_tell(compute, score, levels, e):
     check_route(compute, dict(experts=e, topk=3, score=score, groups=4, top_groups=3), logits, bias, "fp32")
 
 
+@pytest.mark.parametrize("top", [40.0, 1.0, 0.0, -1.0, -30.0, -59.0, -61.0, -85.0, -200.0])
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+def test_route_shares_of_far_sigmoids(compute, top, kind):
+    """Sigmoids' shares down to where fp32 ends, though the sigmoids themselves do
+    not reach as far: forward and back."""
+    g = gen(16)
+    t, e, k = 100, 12, 6
+    logits = top - 70 * torch.rand(t, e, generator=g, device="cuda")
+    logits[:, 3] = top
+    logits[1, 5:] = -math.inf
+    logits[2, 4:], logits[2, :3] = -math.inf, -math.inf
+    logits[3] = -math.inf
+    logits = logits.to(TYPES[kind])
+    router = dict(experts=e, topk=k, score="sigmoid", scale=2.5)
+    check_route(compute, router, logits, None, kind)
+    check_route(compute, router, logits, torch.zeros(e, device="cuda"), kind)
+    ids = ref.route(logits, k, score="sigmoid")[0].int().contiguous()
+    dw, out = randn(g, t, k), Guarded(t, e, dtype=TYPES[kind])
+    compute.route_backward(tide.Router(**router), t, logits, ids, dw, out, logits_type=kind)
+    want, bound = ref.route_backward(logits, ids, dw, "sigmoid", True, 2.5)
+    close(out.view, want, bound + (ref.U_BF16 * (want.abs() + bound) if kind == "bf16" else 0))
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("experts,groups", [(256, 8), (100, 4), (64, 32)])
 @pytest.mark.parametrize("size", [4.0, 64.0, 1000.0, 1e6, 2e38])
