@@ -244,9 +244,10 @@ cudaError_t launch_route(const RouterArgs& a, cudaStream_t stream);
 cudaError_t launch_route_backward(const RouterArgs& a, cudaStream_t stream);
 int64_t slots_workspace_bytes(int64_t pairs, int64_t experts);
 cudaError_t launch_expert_slots(const SlotsArgs& a, cudaStream_t stream);
-cudaError_t launch_expert_gather(const RowsArgs& a, cudaStream_t stream);
-cudaError_t launch_expert_combine(const RowsArgs& a, cudaStream_t stream);
-cudaError_t launch_expert_combine_backward(const RowsArgs& a, cudaStream_t stream);
+// sms: of the handle's device.
+cudaError_t launch_expert_gather(const RowsArgs& a, int sms, cudaStream_t stream);
+cudaError_t launch_expert_combine(const RowsArgs& a, int sms, cudaStream_t stream);
+cudaError_t launch_expert_combine_backward(const RowsArgs& a, int sms, cudaStream_t stream);
 cudaError_t ortho_prepare(TcDevice* dev);
 int64_t ortho_workspace_bytes(int64_t count, int64_t rows, int64_t cols);
 // Whether singular values stay within what the kernels' scales hold.

@@ -148,7 +148,7 @@ tide_status_t tide_expert_gather(tide_compute_t c, int64_t tokens, int64_t hidde
   RowsArgs a{};
   a.tokens = tokens, a.hidden = hidden, a.num_rows = num_rows, a.topk = (int)topk, a.slots = slots;
   a.in = x, a.ld_in = ld_x, a.out = rows, a.ld_out = ld_rows;
-  return launched(launch_expert_gather(a, stream), "tide_expert_gather");
+  return launched(launch_expert_gather(a, launch_of(c).dev->sms, stream), "tide_expert_gather");
 }
 TIDE_CATCH
 
@@ -165,7 +165,7 @@ tide_status_t tide_expert_combine(tide_compute_t c, int64_t tokens, int64_t hidd
   RowsArgs a{};
   a.tokens = tokens, a.hidden = hidden, a.num_rows = num_rows, a.topk = (int)topk, a.slots = slots;
   a.weights = weights, a.in = rows, a.ld_in = ld_rows, a.out = y, a.ld_out = ld_y;
-  return launched(launch_expert_combine(a, stream), "tide_expert_combine");
+  return launched(launch_expert_combine(a, launch_of(c).dev->sms, stream), "tide_expert_combine");
 }
 TIDE_CATCH
 
@@ -189,7 +189,7 @@ tide_status_t tide_expert_combine_backward(tide_compute_t c, int64_t tokens, int
   a.tokens = tokens, a.hidden = hidden, a.num_rows = num_rows, a.topk = (int)topk, a.slots = slots;
   a.weights = weights, a.in = dy, a.ld_in = ld_dy, a.rows = rows, a.ld_rows = ld_rows;
   a.out = drows, a.ld_out = ld_drows, a.dweights = dweights;
-  return launched(launch_expert_combine_backward(a, stream), "tide_expert_combine_backward");
+  return launched(launch_expert_combine_backward(a, launch_of(c).dev->sms, stream), "tide_expert_combine_backward");
 }
 TIDE_CATCH
 

@@ -378,16 +378,15 @@ __global__ void __launch_bounds__(kThreads) combine_windows_kernel(RowsArgs a, S
 // 51 us with 256 to 768 threads, 57 with 1024, 79 with a CTA a token; results
 // of 4096 x 4096 x 2 back: 19.6, 21 and 32; 8191 x 2048 x 8 there: 53 with up
 // to 1024, 48.6 with 2048.)
-Shape shape_of(const RowsArgs& a, int64_t pieces, int64_t busy) {
-  constexpr int64_t kSms = 152;
+Shape shape_of(const RowsArgs& a, int64_t pieces, int64_t busy, int sms) {
   Shape s{1, 0, pieces};
-  while (s.lanes < kThreads && s.lanes < s.pieces && (s.lanes < 32 || s.lanes * a.tokens < kSms * busy)) s.lanes *= 2;
+  while (s.lanes < kThreads && s.lanes < s.pieces && (s.lanes < 32 || s.lanes * a.tokens < sms * busy)) s.lanes *= 2;
   s.tokens = kThreads / s.lanes;
   return s;
 }
 
-cudaError_t run(void (*kernel)(RowsArgs, Shape), const RowsArgs& a, int64_t pieces, int64_t busy, cudaStream_t stream) {
-  const Shape s = shape_of(a, pieces, busy);
+cudaError_t run(void (*kernel)(RowsArgs, Shape), const RowsArgs& a, int64_t pieces, int64_t busy, int sms, cudaStream_t stream) {
+  const Shape s = shape_of(a, pieces, busy, sms);
   return launch_early(kernel, dim3((unsigned)ceil_div(a.tokens, s.tokens)), kThreads, 0, 0, stream, a, s);
 }
 
@@ -400,29 +399,29 @@ int64_t windows(const RowsArgs& a) { return (a.hidden + 14) / 8; }
 
 }  // namespace
 
-cudaError_t launch_expert_gather(const RowsArgs& a, cudaStream_t stream) {
-  if (by8(a)) return run(a.topk <= 2 ? gather_kernel<8, 2> : gather_kernel<8, 8>, a, a.hidden / 8, 2048, stream);
+cudaError_t launch_expert_gather(const RowsArgs& a, int sms, cudaStream_t stream) {
+  if (by8(a)) return run(a.topk <= 2 ? gather_kernel<8, 2> : gather_kernel<8, 8>, a, a.hidden / 8, 2048, sms, stream);
   // a short row's ends, which are written by elements, cost more than the rest
   // saves (4000 tokens of 333, 8 choices, their order too: 22 us, 19 by
   // elements; 8000 of 1023, 10 choices: 69 and 101)
-  if (a.hidden < 512) return run(a.topk <= 2 ? gather_kernel<1, 2> : gather_kernel<1, 8>, a, a.hidden, 2048, stream);
-  return run(a.topk <= 2 ? gather_windows_kernel<2> : gather_windows_kernel<8>, a, windows(a), 2048, stream);
+  if (a.hidden < 512) return run(a.topk <= 2 ? gather_kernel<1, 2> : gather_kernel<1, 8>, a, a.hidden, 2048, sms, stream);
+  return run(a.topk <= 2 ? gather_windows_kernel<2> : gather_windows_kernel<8>, a, windows(a), 2048, sms, stream);
 }
 
-cudaError_t launch_expert_combine(const RowsArgs& a, cudaStream_t stream) {
+cudaError_t launch_expert_combine(const RowsArgs& a, int sms, cudaStream_t stream) {
   if (by8(a)) {
-    if (a.topk <= 4) return run(a.topk <= 2 ? combine_kernel<2, 4> : combine_kernel<4, 2>, a, a.hidden / 8, 512, stream);
-    return run(combine_kernel<8, 1>, a, a.hidden / 8, 2048, stream);
+    if (a.topk <= 4) return run(a.topk <= 2 ? combine_kernel<2, 4> : combine_kernel<4, 2>, a, a.hidden / 8, 512, sms, stream);
+    return run(combine_kernel<8, 1>, a, a.hidden / 8, 2048, sms, stream);
   }
   return run(a.topk <= 2   ? combine_windows_kernel<2>
              : a.topk <= 4 ? combine_windows_kernel<4>
                            : combine_windows_kernel<8>,
-             a, windows(a), 512, stream);
+             a, windows(a), 512, sms, stream);
 }
 
-cudaError_t launch_expert_combine_backward(const RowsArgs& a, cudaStream_t stream) {
-  if (by8(a)) return run(a.topk <= 2 ? combine_backward_kernel<8, 2, 1> : combine_backward_kernel<8, 8, 1>, a, a.hidden / 8, 512, stream);
-  return run(a.topk <= 2 ? combine_backward_kernel<1, 2, 8> : combine_backward_kernel<1, 8, 4>, a, a.hidden, 256, stream);
+cudaError_t launch_expert_combine_backward(const RowsArgs& a, int sms, cudaStream_t stream) {
+  if (by8(a)) return run(a.topk <= 2 ? combine_backward_kernel<8, 2, 1> : combine_backward_kernel<8, 8, 1>, a, a.hidden / 8, 512, sms, stream);
+  return run(a.topk <= 2 ? combine_backward_kernel<1, 2, 8> : combine_backward_kernel<1, 8, 4>, a, a.hidden, 256, sms, stream);
 }
 
 }  // namespace tide

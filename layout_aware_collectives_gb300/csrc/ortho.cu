@@ -12,7 +12,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxParts = 1216;  // eight CTAs an SM
+constexpr int kMaxParts = 1216;  // of all matrices, at most, whatever the device: the workspace holds as many
 
 struct Sources {
   const void* p[kOrthoTable];
@@ -203,7 +203,8 @@ OrthoPlan plan_of(int64_t count, int64_t rows, int64_t cols, char* base, int64_t
   p.tall = rows > cols;
   p.m = (int)(p.tall ? cols : rows), p.n = (int)(p.tall ? rows : cols);
   p.count = count, p.ld_x = line(p.n), p.ld_a = line(p.m);
-  // a row a warp, and no more CTAs than the device holds
+  // a row a warp, and no more CTAs than a device holds by and by (on 152 SMs
+  // eight each)
   const int64_t room = ceil_div(kMaxParts, count), parts = ceil_div(rows, kWarps);
   p.parts = (int)(parts < room ? parts : room);
   int64_t at = 0;

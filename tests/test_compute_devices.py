@@ -102,3 +102,28 @@ assert shapes(third) == want
 on(1)
 assert shapes(second) == other
 """)
+
+
+def test_rows_go_by_the_handle_s_device(runtime):
+    """How many threads a token's row takes goes by the SMs of the handle's own
+    device, whatever handle was bound since."""
+    child(runtime, """
+def shapes(c):
+    out = []
+    for call in (lambda: c.expert_gather(300, 2048, 8, A, A, A, 2400), lambda: c.expert_combine(700, 2048, 2, A, 1400, A, A, A),
+                 lambda: c.expert_gather(300, 2049, 8, A, A, A, 2400), lambda: c.expert_combine(900, 2049, 2, A, 1800, A, A, A),
+                 lambda: c.expert_combine_backward(900, 2048, 2, A, A, 1800, A, A, A, A)):
+        call()
+        out.append(fake.fake_grid(0))
+    return out
+
+first = bound(0)
+want = shapes(first)
+second = bound(1)
+other = shapes(second)
+assert all(a != b for a, b in zip(want, other)), (want, other)
+on(0)
+assert shapes(first) == want
+on(1)
+assert shapes(second) == other
+""")
