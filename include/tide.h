@@ -745,7 +745,7 @@ TIDE_API tide_status_t tide_expert_combine_backward(tide_compute_t compute, int6
                                                     int64_t ld_drows, float* dweights, cudaStream_t stream);
 
 /* Bytes of tide_orthogonalize's workspace for `count` matrices of up to 2^30
- * rows and columns, 2^38 elements in all. */
+ * rows and columns, of which one is at most 2^17, 2^38 elements in all. */
 TIDE_API tide_status_t tide_orthogonalize_workspace(int64_t count, int64_t rows, int64_t cols, int64_t* bytes);
 
 #define TIDE_MAX_ORTHOGONALIZE_STEPS 16

@@ -9,6 +9,7 @@ using namespace tide;
 namespace {
 
 constexpr int64_t kMaxSide = (int64_t)1 << 30;  // of a matrix to orthogonalise: tiles pass its end
+constexpr int64_t kMaxShort = (int64_t)1 << 17;  // of its short side: sums along it are not parted
 const float kCoefficients[3] = {3.4445f, -4.7750f, 2.0315f};
 
 // An array of `bytes`-sized elements, aligned to them.
@@ -197,7 +198,8 @@ tide_status_t tide_orthogonalize_workspace(int64_t count, int64_t rows, int64_t 
   if (!bytes) return invalid("bytes is NULL");
   *bytes = 0;
   TIDE_TRY(check_dims(rows, cols, "tide_orthogonalize"));
-  if (rows > kMaxSide || cols > kMaxSide) return invalid("tide_orthogonalize: sizes out of range");
+  if (rows > kMaxSide || cols > kMaxSide || (rows > kMaxShort && cols > kMaxShort))
+    return invalid("tide_orthogonalize: sizes out of range");
   const int64_t numel = rows * cols;
   if (count < 0 || count > kMaxDim || (numel != 0 && count > kMaxNumel / numel))
     return invalid("tide_orthogonalize: count out of range");

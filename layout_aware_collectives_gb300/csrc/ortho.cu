@@ -181,6 +181,31 @@ __global__ void __launch_bounds__(kThreads) first_kernel(OrthoPlan p, Sources s,
   }
 }
 
+// A's planes of all segments, added up in their order: two neighbours of a row a
+// thread, and its diagonal's element.  Each segment's rounding to fp16 is of its own
+// size, so that all of them leave as much as A's own, about.
+__global__ void __launch_bounds__(kThreads) join_kernel(OrthoPlan p, int out) {
+  after_previous();
+  const int64_t z = blockIdx.z, row = blockIdx.x, plane = (int64_t)p.m * p.ld_a;
+  const int c = blockIdx.y * kThreads + threadIdx.x, pairs = (p.m + 1) / 2;
+  if (c < pairs) {
+    const __half* from = p.part_t + z * p.segments * plane + row * p.ld_a + 2 * c;
+    float a = 0.0f, b = 0.0f;
+#pragma unroll 8
+    for (int s = 0; s < p.segments; ++s, from += plane) {
+      const float2 v = __half22float2(*(const __half2*)from);
+      a += v.x, b += v.y;
+    }
+    *(uint32_t*)(p.t[out] + z * plane + row * p.ld_a + 2 * c) = pack_half(a, b);
+  } else if (c == pairs) {
+    const float* from = p.part_d + z * p.segments * p.m + row;
+    double sum = 0.0;
+#pragma unroll 8
+    for (int s = 0; s < p.segments; ++s, from += p.m) sum += *from;
+    p.d[out][z * p.m + row] = (float)sum;
+  }
+}
+
 // No steps: the normalised matrix itself.
 template <class T>
 __global__ void __launch_bounds__(kThreads) normalised_kernel(OrthoPlan p, Sources s, OrthoTargets out, int64_t first,
@@ -217,6 +242,11 @@ OrthoPlan plan_of(int64_t count, int64_t rows, int64_t cols, char* base, int64_t
     for (auto& plane : turn) plane = (__half*)take(count * p.m * p.ld_x * 2);
   for (auto& plane : p.t) plane = (__half*)take(count * p.m * p.ld_a * 2);
   for (auto& diagonal : p.d) diagonal = (float*)take(count * p.m * 4);
+  p.segments = (int)ceil_div(p.n, kOrthoSegment);
+  if (p.segments > 1) {
+    p.part_t = (__half*)take(count * p.segments * p.m * p.ld_a * 2);
+    p.part_d = (float*)take(count * p.segments * p.m * 4);
+  }
   p.norms = (double*)take(count * p.parts * 8);
   *bytes = at;
   return p;
@@ -273,6 +303,19 @@ bool paired(const OrthoPlan& p, const OrthoArgs& a, int i) {
 }
 
 }  // namespace
+
+cudaError_t launch_ortho_join(const OrthoPlan& p, int out, cudaStream_t stream) {
+  const unsigned across = (unsigned)ceil_div((p.m + 1) / 2 + 1, kThreads);
+  OrthoPlan k = p;
+  for (int64_t z = 0; z < p.count; z += kOrthoTable) {
+    const unsigned some = (unsigned)(p.count - z < kOrthoTable ? p.count - z : kOrthoTable);
+    k.part_t = p.part_t + z * p.segments * p.m * p.ld_a, k.part_d = p.part_d + z * p.segments * p.m;
+    k.t[out] = p.t[out] + z * p.m * p.ld_a, k.d[out] = p.d[out] + z * p.m;
+    const cudaError_t e = launch_early(join_kernel, dim3((unsigned)p.m, across, some), kThreads, 0, 0, stream, k, out);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
 
 int64_t ortho_workspace_bytes(int64_t count, int64_t rows, int64_t cols) {
   int64_t bytes = 0;

@@ -23,6 +23,13 @@ namespace tide {
 
 enum OrthoForm { kGram = 0, kSym = 1, kUpdate = 2, kLast = 3 };
 
+// Columns of X that one of gram's sums takes.  The tensor cores' fp32 sums lose
+// some 2^-24 of themselves with every 16 products that are added, always downwards:
+// 3.7e-4 of A after 65536 columns, 1.5e-3 after four times as many, 8.5e-2 after
+// 2^24.  Longer rows are summed in segments of as many, each to a plane of its
+// own, which are added up afterwards.
+constexpr int64_t kOrthoSegment = 65536;
+
 constexpr int kOrthoTable = 128;  // matrices of a launch that goes by the caller's pointers
 
 // The workspace's parts.
@@ -33,6 +40,9 @@ struct OrthoPlan {
   __half* x[2][2];  // of two turns: hi, lo [count, m, ld_x]
   __half* t[3];     // symmetric matrices without their diagonals [count, m, ld_a]
   float* d[3];      // the diagonals [count, m]
+  int segments;     // of gram's sums; where there is more than one:
+  __half* part_t;   // [count, segments, m, ld_a]
+  float* part_d;    // [count, segments, m]
   double* norms;    // parts of the sums of squares [count, parts]
   int parts;
 };
@@ -51,6 +61,9 @@ struct OrthoProduct {
 struct OrthoTargets {
   uint16_t* p[kOrthoTable];
 };
+
+// A from its segments (ortho.cu).
+cudaError_t launch_ortho_join(const OrthoPlan& p, int out, cudaStream_t stream);
 
 // The products in order (ortho_tc.cu); the last form's results go to the
 // caller's matrices.

@@ -67,6 +67,7 @@ struct Phase {
   int width;                // columns of a tile
   TileGrid grid;            // update, last
   Divisor each;             // gram, sym: tiles of a matrix
+  Divisor segments;         // gram: sums of a matrix, a result each; in a chain 1
   int tiles;
   const float *left_d, *right_d;  // diagonals
   float* out_d;
@@ -483,17 +484,22 @@ __device__ __forceinline__ bool load_phase(const Phase& p, const CUtensorMap* ma
   bool more = first.more;
   for (int i = 1; more; more = work_at<FORM>(p, team, i++, at)) {
     const int row = (at.m * 2 + team.rank) * kHalf, col = at.n * p.width + (int)team.rank * (p.width / 2);
+    int z = at.z, from = 0;
+    if (FORM == kGram) {
+      z = p.segments.of(at.z);
+      from = (at.z - z * p.segments.d) * steps * kStep;
+    }
     for (int k = 0; k < steps; ++k, ++j) {
       if (j >= kStages && !bar_wait(bars.empty(s), parity, watch)) return false;
       if (expects) bar_expect(bars.full(s), bytes);
       const uint32_t bar = leaders + 8u * s;
       const uint32_t a = smem + s * kStage, b = a + kOperand;
       if (!left)
-        load_box3<true>(b, map, k * kStep, col, at.z, bar);
+        load_box3<true>(b, map, from + k * kStep, col, z, bar);
       else if (a_mn)
-        load_box4(a, map, 0, k * kStep, row / 64, at.z, bar);
+        load_box4(a, map, 0, k * kStep, row / 64, z, bar);
       else
-        load_box3<true>(a, map, k * kStep, row, at.z, bar);
+        load_box3<true>(a, map, from + k * kStep, row, z, bar);
       if (++s == kStages) s = 0, parity ^= 1;
     }
   }
@@ -762,12 +768,14 @@ Phase phase_of(const OrthoPlan& p, const OrthoProduct& q, const Widths& w, int64
   k.left = q.form == kGram ? kLeftX + q.turn : q.form == kSym ? kLeftT + q.left : kWideX + q.turn;
   k.right = q.form == kGram ? kRightX + q.turn : (update ? kUpdateT : kRightT) + q.right;
   k.m = update ? p.n : p.m, k.wide = p.m;
-  k.steps = (int)ceil_div(q.form == kGram ? p.n : p.m, kStep);
+  const bool parted = q.form == kGram && p.segments > 1;
+  k.steps = (int)ceil_div(parted ? kOrthoSegment : q.form == kGram ? p.n : p.m, kStep);
+  k.segments = Divisor(parted ? p.segments : 1);
   k.planes = q.form == kGram ? 0 : q.form == kSym && q.left == q.right ? 1 : 2;
   k.in[0] = update ? p.x[q.turn][0] : p.t[q.left], k.in[1] = update ? p.x[q.turn][1] : p.t[q.right];
-  k.out[0] = update ? p.x[q.turn ^ 1][0] : p.t[q.out], k.out[1] = p.x[q.turn ^ 1][1];
+  k.out[0] = update ? p.x[q.turn ^ 1][0] : parted ? p.part_t : p.t[q.out], k.out[1] = p.x[q.turn ^ 1][1];
   k.ld = update ? p.ld_x : p.ld_a;
-  k.left_d = p.d[q.left], k.right_d = p.d[q.right], k.out_d = p.d[q.out];
+  k.left_d = p.d[q.left], k.right_d = p.d[q.right], k.out_d = parted ? p.part_d : p.d[q.out];
   k.s2 = q.s2, k.s1 = q.s1, k.s0 = q.s0;
   k.sum_scale = 1.0f / (q.left_scale * q.right_scale);
   k.left_scale = 1.0f / q.left_scale, k.right_scale = 1.0f / q.right_scale;
@@ -788,13 +796,14 @@ cudaError_t launch_product(const OrthoPlan& p, const OrthoProduct& q, const Widt
   k.phase = phase_of(p, q, w, a.ld_dst);
   k.limits = limits_of(l);
   if (!map_of(&k.left, k.phase.left, p, w) || !map_of(&k.right, k.phase.right, p, w)) return cudaErrorInvalidValue;
-  // as many matrices as a launch counts tiles, and the last form's table holds
+  // as many matrices (or segments) as a launch counts tiles, and the last form's table holds
   const int64_t each = tiles_of(k.phase);
   int64_t most = INT32_MAX / 2 / each;
   if (most < 1) return cudaErrorInvalidValue;
   if (q.form == kLast && most > kOrthoTable) most = kOrthoTable;
-  for (k.first = 0; k.first < p.count; k.first += most) {
-    const int64_t some = p.count - k.first < most ? p.count - k.first : most;
+  const int64_t count = p.count * k.phase.segments.d;
+  for (k.first = 0; k.first < count; k.first += most) {
+    const int64_t some = count - k.first < most ? count - k.first : most;
     k.phase.tiles = (int)(some * each);
     if (q.form == kLast)
       for (int64_t i = 0; i < some; ++i) targets.p[i] = a.dst[k.first + i];
@@ -806,7 +815,7 @@ cudaError_t launch_product(const OrthoPlan& p, const OrthoProduct& q, const Widt
     const cudaError_t e = launch_early(kernel, dim3(2 * pairs), kThreads, kSmem, 2, stream, k, targets);
     if (e != cudaSuccess) return e;
   }
-  return cudaSuccess;
+  return k.phase.segments.d > 1 ? launch_ortho_join(p, q.out, stream) : cudaSuccess;
 }
 
 cudaError_t launch_chain(const OrthoPlan& p, const OrthoProduct* q, int products, const Widths& w, int pairs, const OrthoArgs& a,
@@ -856,14 +865,14 @@ Way way_of(const OrthoPlan& p, const OrthoProduct* q, int products, const TcDevi
   int number[3] = {};  // of products: gram, sym, update and last
   for (int i = 0; i < products; ++i) ++number[q[i].form == kGram ? 0 : q[i].form == kSym ? 1 : 2];
   const int64_t down = ceil_div(p.n, 2 * kHalf);
-  const int long_steps = (int)ceil_div(p.n, kStep), short_steps = (int)ceil_div(p.m, kStep);
+  const int long_steps = (int)ceil_div(p.n < kOrthoSegment ? p.n : kOrthoSegment, kStep), short_steps = (int)ceil_div(p.m, kStep);
   // the widths that take the least time with so many pairs for so many matrices
   const auto best_of = [&](int64_t matrices, int64_t pairs, bool chain, Widths* w) {
     double least[3] = {};
     for (int width = 64; width <= 256; width *= 2) {
       int* const at[3] = {&w->gram, &w->sym, &w->update};
       for (int f = 0; f < 3; ++f) {
-        const int64_t tiles = matrices * (f < 2 ? triangle(p.m, width) : down * ceil_div(p.m, width));
+        const int64_t tiles = matrices * (f < 2 ? triangle(p.m, width) : down * ceil_div(p.m, width)) * (f == 0 ? p.segments : 1);
         const double t = product_time(tiles, pairs, f == 0 ? long_steps : short_steps, width) +
                          (chain ? kMeet : 2 * tiles > pairs ? kLaunchFull : kLaunch);
         if (width == 64 || t <= least[f]) least[f] = t, *at[f] = width;
@@ -873,7 +882,7 @@ Way way_of(const OrthoPlan& p, const OrthoProduct* q, int products, const TcDevi
   };
   Way best{};
   double least = best_of(p.count, dev.pairs, false, &best.widths);
-  for (int pairs = 1; pairs <= kMaxTeam && products <= kMaxPhases; ++pairs) {
+  for (int pairs = 1; pairs <= kMaxTeam && products <= kMaxPhases && p.segments == 1; ++pairs) {
     const int held = pairs == 1 ? dev.pairs : dev.ortho[pairs];
     if (held < 1) continue;
     Way way{pairs, {}};

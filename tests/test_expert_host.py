@@ -269,3 +269,17 @@ def test_elements_of_other_types_are_refused(compute, calls):
         with pytest.raises(TypeError):
             compute.orthogonalize(4, 2, src, dst, A, workspace_bytes=1 << 20, **kw)
     assert not calls
+
+
+def test_orthogonalize_sizes_of_long_and_short_sides():
+    """Sides up to 2^30, of which one is up to 2^17; a workspace that holds what long sides' sums take."""
+    for ok in ((1, 1 << 17, 1 << 17), (1, 1 << 30, 3), (1, 3, 1 << 30), (1, 1 << 21, 1 << 17)):
+        assert tide.orthogonalize_workspace_bytes(*ok) > 0
+    for bad in ((1, (1 << 17) + 1, (1 << 17) + 1), (1, 1 << 18, 1 << 18)):
+        with pytest.raises(tide.TideError):
+            tide.orthogonalize_workspace_bytes(*bad)
+    m, n = 100, 65536
+    planes = 4 * m * n * 2 + 3 * m * 128 * 2 + 3 * m * 4
+    assert planes <= tide.orthogonalize_workspace_bytes(1, m, n) < planes + (1 << 16)
+    n += 64
+    assert tide.orthogonalize_workspace_bytes(1, m, n) >= 4 * m * n * 2 + (3 + 2) * m * 128 * 2 + (3 + 2) * m * 4

@@ -462,6 +462,31 @@ def test_orthogonalize_zeros_and_padding(compute):
         near(alone.T if t else alone, m[:190, :290])
 
 
+@pytest.mark.parametrize("count,rows,cols", [(1, 1, 65537), (3, 3, 70001), (1, 70001, 3), (2, 40, 131077), (1, 200003, 33), (1, 64, 1 << 20),
+                                             (2, 1 << 18, 300)])
+def test_orthogonalize_long_sides(compute, count, rows, cols):
+    """Sums along a long side are as near as others: what they leave stays below the result's own rounding."""
+    grads = [randn(gen(rows + i), rows, cols) for i in range(count)]
+    for got, grad in zip(orthogonalized(compute, grads), grads):
+        near(got, grad)
+        want = ref.orthogonalize(grad)
+        assert float((got.double() - want).norm()) <= math.sqrt(2) * float((want.bfloat16().double() - want).norm())
+
+
+def test_orthogonalize_the_longest_vector(compute):
+    """One row of 2^26 and some: its length goes through the polynomial, its direction stays."""
+    n = (1 << 26) + 3
+    grad = randn(gen(17), 1, n)
+    got = orthogonalized(compute, [grad])[0].double()
+    unit, length = grad.double() / grad.double().norm(), 1.0
+    for _ in range(5):
+        a, b, c = ref.step_of(ref.COEFFICIENTS, 0)
+        length = a * length + b * length ** 3 + c * length ** 5
+    # across the direction: the roundings of the elements; along it, where those average out, what the sums leave
+    assert float((got - length * unit).norm()) <= ref.U_BF16 * length
+    assert abs(float((got * unit).sum()) - length) <= 2.0 ** -9 * length
+
+
 def test_orthogonalize_not_finite_stays_with_its_matrix(compute):
     g = gen(7)
     grads = [randn(g, 130, 260) for _ in range(4)]
