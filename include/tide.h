@@ -765,7 +765,8 @@ TIDE_API tide_status_t tide_orthogonalize_workspace(int64_t count, int64_t rows,
  *   workspace     at least tide_orthogonalize_workspace bytes
  * Rows and columns of zeros stay zero, so a padded gradient may be passed
  * as it is.  A matrix with an infinity or NaN becomes NaN.
- * X is kept as two fp16 terms, A and the matrices made of it as one beside
+ * Matrices of up to 16 rows or columns take 32-bit arithmetic throughout.  Of
+ * others X is kept as two fp16 terms, A and the matrices made of it as one beside
  * their diagonals in fp32; products take the first terms, and where that is
  * less work two steps share a pass over X.  What all this leaves is below the
  * result's own rounding to bf16 (up to one and a half times it next to

@@ -1,4 +1,4 @@
-// Newton-Schulz orthogonalisation: norms, the first X, and the steps.
+// Newton-Schulz orthogonalisation: norms, the first X, short sides, and the steps.
 //
 // The first two kernels are passes over the matrices, bound by HBM: norms of
 // one 14336 x 4096 in fp32 46 us (5.1 TB/s), its first X 112 (4.2; turned, and
@@ -181,6 +181,120 @@ __global__ void __launch_bounds__(kThreads) first_kernel(OrthoPlan p, Sources s,
   }
 }
 
+// ------------------------------------------------------------ short sides
+
+// Short sides of up to 16 rows: one fp16 term of a product's operands would
+// leave 0.02 of the result next to rank one, and the products are too small for
+// the tensor cores to matter.  X is kept in fp32, a CTA has a span of its columns: it
+// adds up A from all spans' parts (in 64 bits, in order), makes C, takes its
+// columns to C X, and leaves its part of the next A.  So a step is one launch, bound
+// by what a launch and the parts' way take: one 8 x 4096 37 us (92 on the tensor
+// cores, by pairs of steps), 64 of them 131 (163), 1000 of 16 x 64 293 (464).
+constexpr int kShortTile = 64;  // columns at a time
+
+struct ShortStep {
+  bool from_source, apply, last;  // no `apply`: A's first parts
+  int turn;                       // of the parts that are written
+  float a, b, c;
+};
+
+// The e-th pair i <= j of rows.
+__device__ __forceinline__ void pair_of(int e, int m, int& i, int& j) {
+  for (i = 0; e >= m - i; ++i) e -= m - i;
+  j = i + e;
+}
+
+template <class T>
+__global__ void __launch_bounds__(kThreads) short_kernel(OrthoPlan p, Sources s, OrthoTargets out, int64_t first, int64_t ld,
+                                                         int64_t ld_out, float eps, ShortStep k) {
+  after_previous();
+  __shared__ float x[kShortSide][kShortTile + 1], y[kShortSide][kShortTile + 1];
+  __shared__ float a[kShortSide][kShortSide + 1], c[kShortSide][kShortSide + 1];
+  __shared__ double sums[kThreads];
+  const int m = p.m, entries = m * (m + 1) / 2, slices = min(kThreads / entries, 32);
+  const int64_t z = first + blockIdx.y;
+  // an entry of A and a slice of what it is summed over
+  const int entry = threadIdx.x % entries, slice = threadIdx.x / entries;
+  int ei, ej;
+  pair_of(entry, m, ei, ej);
+  const auto add_up = [&](double v) {  // an entry's slices, in order: a sum for each of the first threads
+    if (slice < slices) sums[threadIdx.x] = v;
+    __syncthreads();
+    double sum = 0.0;
+    if (threadIdx.x < entries)
+      for (int q = 0; q < slices; ++q) sum += sums[q * entries + entry];
+    __syncthreads();
+    return sum;
+  };
+  if (k.apply) {
+    const double* part = p.short_a[k.turn ^ 1] + z * p.spans * entries + entry;
+    double v = 0.0;
+    if (slice < slices)
+#pragma unroll 8
+      for (int q = slice; q < p.spans; q += slices) v += part[(int64_t)q * entries];
+    const double sum = add_up(v);
+    if (threadIdx.x < entries) a[ei][ej] = a[ej][ei] = (float)sum;
+    __syncthreads();
+    const int i = threadIdx.x / kShortSide, j = threadIdx.x % kShortSide;
+    if (i < m && j < m) {
+      float square = 0.0f;
+      for (int q = 0; q < m; ++q) square = fmaf(a[i][q], a[q][j], square);
+      c[i][j] = fmaf(k.c, square, fmaf(k.b, a[i][j], i == j ? k.a : 0.0f));
+    }
+    __syncthreads();
+  }
+  Inverse inv{};
+  const T* src = (const T*)s.p[blockIdx.y];
+  if (k.from_source) inv = inverse_norm(p, z, eps);
+  float* const mine = p.short_x + z * m * p.ld_x;
+  double all = 0.0;  // of this thread's entry and slice
+  for (int n = 0; n < p.span; ++n) {
+    const int64_t c0 = ((int64_t)blockIdx.x * p.span + n) * kShortTile;
+    if (c0 >= p.n) break;
+    for (int e = threadIdx.x; e < m * kShortTile; e += kThreads) {
+      const bool turned = k.from_source && p.tall;
+      const int i = turned ? e % m : e / kShortTile, q = turned ? e / m : e % kShortTile;
+      const int64_t at = c0 + q;
+      float v = 0.0f;
+      if (at < p.n) {
+        if (k.from_source)
+          v = element(src + (p.tall ? at * ld + i : i * ld + at)) * inv.i * inv.f * inv.j;
+        else
+          v = mine[i * p.ld_x + at];
+      }
+      x[i][q] = v;
+    }
+    __syncthreads();
+    if (k.apply) {
+      for (int e = threadIdx.x; e < m * kShortTile; e += kThreads) {
+        const int i = e / kShortTile, q = e % kShortTile;
+        float v = 0.0f;
+        for (int r = 0; r < m; ++r) v = fmaf(c[i][r], x[r][q], v);
+        y[i][q] = v;
+        if (!k.last && c0 + q < p.n) mine[i * p.ld_x + c0 + q] = v;
+      }
+      __syncthreads();
+    }
+    if (k.last) {
+      uint16_t* to = out.p[blockIdx.y];
+      for (int e = threadIdx.x; e < m * kShortTile; e += kThreads) {
+        const int i = p.tall ? e % m : e / kShortTile, q = p.tall ? e / m : e % kShortTile;
+        const int64_t at = c0 + q;
+        if (at < p.n) to[p.tall ? at * ld_out + i : i * ld_out + at] = to_bf16(y[i][q]);
+      }
+    } else if (slice < slices) {
+      const auto& t = k.apply ? y : x;
+      float sum = 0.0f;
+      for (int q = slice; q < kShortTile; q += slices) sum = fmaf(t[ei][q], t[ej][q], sum);
+      all += sum;
+    }
+    __syncthreads();
+  }
+  if (k.last) return;
+  const double sum = add_up(all);
+  if (threadIdx.x < entries) p.short_a[k.turn][(z * p.spans + blockIdx.x) * entries + entry] = sum;
+}
+
 // A's planes of all segments, added up in their order: two neighbours of a row a
 // thread, and its diagonal's element.  Each segment's rounding to fp16 is of its own
 // size, so that all of them leave as much as A's own, about.
@@ -238,6 +352,20 @@ OrthoPlan plan_of(int64_t count, int64_t rows, int64_t cols, char* base, int64_t
     at += round256(n);
     return r;
   };
+  p.norms = (double*)take(count * p.parts * 8);
+  if (p.m <= kShortSide) {
+    // as many spans as the device has CTAs at a time, or, as each reads all spans'
+    // parts, as those stay short
+    const int64_t tiles = ceil_div(p.n, kShortTile), entries = p.m * (p.m + 1) / 2;
+    int64_t most = 20000 / entries < kMaxParts ? 20000 / entries : kMaxParts;
+    if (most > room) most = room;
+    p.span = (int)ceil_div(tiles, most);
+    p.spans = (int)ceil_div(tiles, p.span);
+    p.short_x = (float*)take(count * p.m * p.ld_x * 4);
+    for (auto& turn : p.short_a) turn = (double*)take(count * p.spans * entries * 8);
+    *bytes = at;
+    return p;
+  }
   for (auto& turn : p.x)
     for (auto& plane : turn) plane = (__half*)take(count * p.m * p.ld_x * 2);
   for (auto& plane : p.t) plane = (__half*)take(count * p.m * p.ld_a * 2);
@@ -247,7 +375,6 @@ OrthoPlan plan_of(int64_t count, int64_t rows, int64_t cols, char* base, int64_t
     p.part_t = (__half*)take(count * p.segments * p.m * p.ld_a * 2);
     p.part_d = (float*)take(count * p.segments * p.m * 4);
   }
-  p.norms = (double*)take(count * p.parts * 8);
   *bytes = at;
   return p;
 }
@@ -348,7 +475,13 @@ cudaError_t launch_orthogonalize(const OrthoArgs& a, const TcLaunch& l, cudaStre
                                  : vec  ? norm_kernel<float, true>
                                         : norm_kernel<float, false>,
                                  dim3(p.parts, some), kThreads, 0, 0, stream, p, s, first, a.rows, a.cols, a.ld_src);
-    if (e == cudaSuccess && a.steps)
+    if (p.m <= kShortSide && a.steps) {
+      for (int i = -1; i < a.steps && e == cudaSuccess; ++i) {  // A's first parts, then the steps
+        const float* c = a.coefficients + 3 * (i < 0 ? 0 : i);
+        e = launch_early(a.bf16 ? short_kernel<uint16_t> : short_kernel<float>, dim3(p.spans, some), kThreads, 0, 0, stream, p, s, out,
+                         first, a.ld_src, a.ld_dst, a.eps, ShortStep{i <= 0, i >= 0, i == a.steps - 1, i & 1, c[0], c[1], c[2]});
+      }
+    } else if (e == cudaSuccess && a.steps)
       e = launch_early(a.bf16 ? vec ? first_kernel<uint16_t, true> : first_kernel<uint16_t, false>
                        : vec  ? first_kernel<float, true>
                               : first_kernel<float, false>,
@@ -360,7 +493,7 @@ cudaError_t launch_orthogonalize(const OrthoArgs& a, const TcLaunch& l, cudaStre
                        a.cols, a.ld_src, a.ld_dst, a.eps);
     if (e != cudaSuccess) return e;
   }
-  if (!a.steps) return cudaSuccess;
+  if (!a.steps || p.m <= kShortSide) return cudaSuccess;
   OrthoProduct q[4 * TIDE_MAX_ORTHOGONALIZE_STEPS];  // 3 a step, 7 for two that share a pass
   int products = 0, turn = 0;
   for (int i = 0; i < a.steps; turn ^= 1) {

@@ -30,6 +30,10 @@ enum OrthoForm { kGram = 0, kSym = 1, kUpdate = 2, kLast = 3 };
 // own, which are added up afterwards.
 constexpr int64_t kOrthoSegment = 65536;
 
+// Short sides of up to so many rows take no tensor cores, but 32-bit arithmetic
+// throughout (ortho.cu).
+constexpr int kShortSide = 16;
+
 constexpr int kOrthoTable = 128;  // matrices of a launch that goes by the caller's pointers
 
 // The workspace's parts.
@@ -43,6 +47,11 @@ struct OrthoPlan {
   int segments;     // of gram's sums; where there is more than one:
   __half* part_t;   // [count, segments, m, ld_a]
   float* part_d;    // [count, segments, m]
+  // short sides: X [count, m, ld_x], and A's parts of two turns [count, spans,
+  // m (m + 1) / 2]
+  float* short_x;
+  double* short_a[2];
+  int spans, span;  // of X's columns, 64 at a time: so many a span
   double* norms;    // parts of the sums of squares [count, parts]
   int parts;
 };

@@ -436,6 +436,50 @@ def test_orthogonalize_magnitudes(compute, scale):
     near(orthogonalized(compute, [grad])[0], grad)
 
 
+def spectra(g, rows, cols, kind):
+    """Noise, noise over rank one, spectra of e^-4 to e^-14, columns of very different sizes."""
+    m = min(rows, cols)
+    one = randn(g, rows, 1) @ randn(g, 1, cols)
+    out = [randn(g, rows, cols)] + [one + 10.0 ** -e * randn(g, rows, cols) for e in (1, 2, 3, 4, 5)]
+    u, v = (torch.linalg.qr(torch.randn(n, m, generator=g, device="cuda", dtype=torch.float64))[0] for n in (rows, cols))
+    for depth in (4, 8, 14):
+        s = torch.exp(-depth * torch.arange(m, device="cuda", dtype=torch.float64) / max(1, m - 1))
+        out.append((u * s) @ v.T)
+    out.append(randn(g, rows, cols) * torch.exp(3 * randn(g, 1, cols)))
+    return [v.to(TYPES[kind]).contiguous() for v in out]
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 1), (1, 7), (2, 3), (2, 50), (50, 3), (5, 5), (8, 8), (8, 5000), (15, 100), (16, 16), (16, 64), (3000, 16),
+                                       (16, 70001), (1 << 20, 4), (1, 300000)])
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("pad", [0, 3])
+def test_orthogonalize_short_sides(compute, rows, cols, kind, pad):
+    """Up to 16 rows or columns: 32-bit arithmetic, whatever the spectrum.  Five steps
+    stretch by 485 at most what roundings of 2^-24 and sums of 16 terms leave in each."""
+    grads = spectra(gen(rows + 3 * cols), rows, cols, kind)
+    for got, grad in zip(orthogonalized(compute, grads, kind, pad), grads):
+        want = ref.orthogonalize(grad)
+        size, own = float(want.norm()), float((want.bfloat16().double() - want).norm())
+        # 2^-24 * 485 * (a few roundings in each of five steps): 2^-12
+        assert float((got.double() - want).norm()) <= own + 2.0 ** -12 * size
+
+
+@pytest.mark.parametrize("count,rows,cols", [(300, 3, 40), (130, 70, 9), (2000, 16, 16), (1, 16, 1 << 18)])
+def test_orthogonalize_short_sides_of_many(compute, count, rows, cols):
+    """As many as several launches take, each as alone; in place too; the same bits every time."""
+    grads = gradients(gen(18), count, rows, cols, "bf16")
+    got = orthogonalized(compute, grads, "bf16")
+    for i in sorted({0, count // 2, count - 1}):
+        near(got[i], grads[i])
+        # (how columns are shared out, and with it the sums' order, goes by the number of matrices)
+        near(orthogonalized(compute, [grads[i]], "bf16")[0], grads[i])
+    assert all(torch.equal(a, b) for a, b in zip(orthogonalized(compute, grads, "bf16"), got))
+    ws = torch.empty(tide.orthogonalize_workspace_bytes(count, rows, cols), dtype=torch.uint8, device="cuda")
+    own = [v.clone() for v in grads]
+    compute.orthogonalize(rows, cols, own, own, ws)
+    assert all(torch.equal(a, b) for a, b in zip(own, got))
+
+
 def test_orthogonalize_structures(compute):
     """One large element, equal rows, one direction, an orthogonal matrix, columns of very different sizes."""
     g = gen(5)
