@@ -370,6 +370,7 @@ OrthoPlan plan_of(int64_t count, int64_t rows, int64_t cols, char* base, int64_t
     for (auto& plane : turn) plane = (__half*)take(count * p.m * p.ld_x * 2);
   for (auto& plane : p.t) plane = (__half*)take(count * p.m * p.ld_a * 2);
   for (auto& diagonal : p.d) diagonal = (float*)take(count * p.m * 4);
+  p.x_terms = p.m <= 64 ? 2 : 1;
   p.segments = (int)ceil_div(p.n, kOrthoSegment);
   if (p.segments > 1) {
     p.part_t = (__half*)take(count * p.segments * p.m * p.ld_a * 2);
@@ -423,10 +424,22 @@ bool bounds_of(int steps, const float* k, Bounds* out) {
 
 // Whether step i and the next share a pass over X: 5 products of m^3 / 2
 // operations and 3 of m m n / 2 instead of 2 and 6.  An error of A grows by up
-// to a^2 on its way to the second step's, which a moderate a only allows.
+// to a^2 on its way to the second step's, which a moderate a only allows; it
+// leaves less the more rows there are (ortho.cuh), and below 384 more than a
+// quarter above 2^-9 of the result.  That costs 27 of 3131 x 257 482 us instead of
+// 385, 64 of 256 x 704 239 instead of 217, 128 x 2048 94 instead of 84; 100 of 128 x 512
+// take 165 instead of 171.
+constexpr int kPairedSide = 384;
 bool paired(const OrthoPlan& p, const OrthoArgs& a, int i) {
   const float k = a.coefficients[3 * i];
-  return i + 1 < a.steps && 2 * (int64_t)p.n >= 3 * (int64_t)p.m && k * k <= 16.0f;
+  return i + 1 < a.steps && p.m >= kPairedSide && 2 * (int64_t)p.n >= 3 * (int64_t)p.m && k * k <= 16.0f;
+}
+
+// How far steps from i on may stretch what is small.
+float stretch_from(const OrthoArgs& a, int i) {
+  float r = 1.0f;
+  for (; i < a.steps; ++i) r *= std::fabs(a.coefficients[3 * i]);
+  return r;
 }
 
 }  // namespace
@@ -502,7 +515,7 @@ cudaError_t launch_orthogonalize(const OrthoArgs& a, const TcLaunch& l, cudaStre
     float t[3] = {};  // scales of what lies in the symmetric places
     const auto sym = [&](int left, int right, int out, double top, float s2, float s1, float s0) {
       const float scale = (float)scale_for(top);
-      q[products++] = OrthoProduct{kSym, turn, left, right, out, s2, s1, s0, t[left], t[right], scale};
+      q[products++] = OrthoProduct{kSym, turn, left, right, out, s2, s1, s0, t[left], t[right], scale, 0};
       t[out] = scale;
     };
     const auto square = [&](int from, int out, int step) {
@@ -510,7 +523,7 @@ cudaError_t launch_orthogonalize(const OrthoArgs& a, const TcLaunch& l, cudaStre
       sym(from, from, out, bound.c[step], k[2], k[1], k[0]);
     };
     t[0] = (float)scale_for(bound.x[i] * bound.x[i]);
-    q[products++] = OrthoProduct{kGram, turn, 0, 0, 0, 1, 0, 0, x, x, t[0]};
+    q[products++] = OrthoProduct{kGram, turn, 0, 0, 0, 1, 0, 0, x, x, t[0], 0};
     square(0, 1, i);  // C
     if (two) {
       sym(1, 0, 2, bound.c[i] * bound.x[i] * bound.x[i], 1, 0, 0);  // C A
@@ -518,9 +531,12 @@ cudaError_t launch_orthogonalize(const OrthoArgs& a, const TcLaunch& l, cudaStre
       square(0, 2, i + 1);                                          // C'
       sym(2, 1, 0, bound.c[i] * bound.c[i + 1], 1, 0, 0);           // C' C
     }
+    const float first = a.coefficients[3 * i] * (two ? a.coefficients[3 * i + 3] : 1.0f);  // L(0)
     i += two ? 2 : 1;
     const int by = two ? 0 : 1;
-    q[products++] = OrthoProduct{i < a.steps ? kUpdate : kLast, turn, 0, by, 0, 1, 0, 0, x, t[by], (float)scale_for(bound.x[i])};
+    const float rest = p.x_terms == 1 && stretch_from(a, i) > 8.0f ? first : 0.0f;
+    q[products++] =
+        OrthoProduct{i < a.steps ? kUpdate : kLast, turn, 0, by, 0, 1, 0, 0, x, t[by], (float)scale_for(bound.x[i]), rest};
   }
   return launch_ortho_products(p, q, products, a, l, stream);
 }

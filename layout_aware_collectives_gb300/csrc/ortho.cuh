@@ -1,8 +1,8 @@
 // Newton-Schulz orthogonalisation: what its kernels share.
 //
 // One step takes X [m, n], m <= n (the matrix, or its transpose where it has
-// more rows), to C X, C = a + b A + c A A, A = X X^T.  Two steps may share one
-// pass over X: the second's A is C A C, and X becomes C' C X.
+// more rows), to C X, C = a + b A + c A A, A = X X^T.  Where m is large two steps
+// may share one pass over X: the second's A is C A C, and X becomes C' C X.
 //
 // X is kept as two fp16 terms (hi + lo: 22 bits) of a power-of-two scale, the
 // symmetric matrices as one, all but their diagonals, which are kept in fp32
@@ -12,7 +12,30 @@
 // identity, and the diagonals carry most of a product.  With L = D + P, P's
 // diagonal 0,
 //   L L' = P P' + D P' + P D' + D D',   L X = P X + D X,
-// and the tensor cores see the first terms only.  That leaves 0.0002-0.0011.
+// and the tensor cores see the first terms only.
+//
+// Next to a low rank that is not enough: small singular values grow by a in every
+// step, by 485 in five, and with them whatever a step leaves in their directions.
+// There L is L(0), its value at A = 0 (a, or a a' of two steps), while D is less
+// by some 1 / m of what L takes from the large ones: P lo, which the products pass
+// over, has the difference, and so left 0.02 of the result of 8 rows, 0.01 of 33,
+// 0.005 of 128, for a floor of noise below rank one.  So while later steps may still
+// stretch things by more than 8, lo is multiplied by L(0): what that leaves, (L -
+// L(0)) lo, lies in directions with large singular values, which do not grow.  In
+// the last steps all are near 1, and lo is multiplied by D, which is nearer to L
+// on average.  Short sides of up to 64 have lo in the product itself, a second
+// term of its sums, which are a stage long.
+//
+// What all this leaves, in 2^-9 of the result's norm (rounding it to bf16 leaves
+// 0.85 of that), the largest of noise, noise of 1e-1 to 1e-5 over rank one, spectra
+// of e^-4 to e^-14 and columns of very different sizes:
+//   17 x 40  33 x 2500  64 x 200  128 x 1000  256 x 704  512 x 1024, steps apart
+//   0.6      0.4        0.4       0.4         0.4        0.35
+//   (7.9     5.0        2.6       2.1         1.2        1.0, in pairs, lo by D)
+//   384 x 1024  512 x 1024  768 x 2048  1024 x 1536, in pairs
+//   1.2         1.1         0.95        0.85
+// Pairs leave more, as A's rounding passes through C on both sides, a a of it; the
+// more rows, the less.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -44,6 +67,7 @@ struct OrthoPlan {
   __half* x[2][2];  // of two turns: hi, lo [count, m, ld_x]
   __half* t[3];     // symmetric matrices without their diagonals [count, m, ld_a]
   float* d[3];      // the diagonals [count, m]
+  int x_terms;      // of update's and last's sums: 1, or 2 with X's lo
   int segments;     // of gram's sums; where there is more than one:
   __half* part_t;   // [count, segments, m, ld_a]
   float* part_d;    // [count, segments, m]
@@ -64,6 +88,7 @@ struct OrthoProduct {
   int out;             // kGram, kSym: a t
   float s2, s1, s0;    // kSym: s2 (left right) + s1 left + s0
   float left_scale, right_scale, out_scale;
+  float rest;  // kUpdate, kLast: the factor of X's lo; 0: the right t's diagonal
 };
 
 // The caller's matrices of one launch.

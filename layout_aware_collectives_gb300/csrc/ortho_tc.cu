@@ -59,6 +59,8 @@ constexpr size_t kSmem = 1024 + kStages * kStage + kEpiWarps * kSlots * kSlot;
 struct Phase {
   int form;
   int left, right;          // maps of the operands
+  int left_lo;              // and of X's lo, where a sum has two terms
+  int term;                 // stages of a term
   const __half* in[2];      // planes that are added: sym: left, right; update, last: X, hi and lo
   __half* out[2];           // gram, sym: the one; update: the next X, hi and lo
   int64_t ld;               // of those
@@ -72,14 +74,16 @@ struct Phase {
   const float *left_d, *right_d;  // diagonals
   float* out_d;
   float s2, s1, s0;
+  float rest;               // update, last: the factor of X's lo; 0: as of its hi
   float sum_scale, left_scale, right_scale, out_scale;  // factors of the sums, of `in`, of what is kept
   bool tall;
   int64_t ld_out;
 };
 
 // The operands that products have: left ones of gram, sym and update, right
-// ones of the same.
-enum Map { kLeftX = 0, kLeftT = 2, kWideX = 5, kRightX = 7, kRightT = 9, kUpdateT = 12, kMaps = 14 };
+// ones of the same; those of X's lo last.
+enum Map { kLeftX = 0, kLeftT = 2, kWideX = 5, kRightX = 7, kRightT = 9, kUpdateT = 12, kWideLo = 14,
+           kMaps = 16 };
 
 struct Limits {
   int* err;
@@ -87,7 +91,7 @@ struct Limits {
 };
 
 struct Params {  // of one product of all matrices
-  CUtensorMap left, right;
+  CUtensorMap left, right, left_lo;
   Phase phase;
   int64_t first;  // matrix, of this launch
   Limits limits;
@@ -96,6 +100,7 @@ struct Params {  // of one product of all matrices
 constexpr int kMaxPhases = 24;
 struct ChainParams {  // of all products of each matrix
   CUtensorMap maps[kMaps];
+  int used;  // of those
   Phase phase[kMaxPhases];
   int phases;
   int64_t first;
@@ -332,16 +337,18 @@ __device__ __forceinline__ void finish(const Phase& p, uint16_t* dst, const Curs
   for (int i = 0; i < 8; ++i) b[0][i] = a[0][i], b[1][i] = a[1][i];
   if (p.planes == 2) get_box<kTurned>(slot + kBox, at, b);
   // What is kept is scale * (s2 (sum + di right + left dj) + s1 left), or
-  // scale * (sum + dj hi + dj lo): each factor with its scales taken together.
+  // scale * (sum + dj hi + dj or rest lo): each factor with its scales taken together.
   const float k0 = p.sum_scale * p.out_scale * p.s2;
   const uint64_t k2 = two(k0, k0);
   const float by_row = d.di * p.s2 * p.right_scale * p.out_scale;
-  uint64_t by_col[4];  // of the fragments' columns
+  uint64_t by_col[4], by_lo[4];  // of the fragments' columns
   if (form != kGram) {
-    const float own = fmaf(d.dj, p.s2, p.s1) * p.left_scale * p.out_scale;
+    const float own = fmaf(d.dj, p.s2, p.s1) * p.left_scale * p.out_scale, rest = p.rest * p.left_scale * p.out_scale;
 #pragma unroll
-    for (int g = 0; g < 4; ++g)
+    for (int g = 0; g < 4; ++g) {
       by_col[g] = two(__shfl_sync(0xffffffffu, own, g * 8 + (lane & 3) * 2), __shfl_sync(0xffffffffu, own, g * 8 + (lane & 3) * 2 + 1));
+      by_lo[g] = p.rest != 0.0f ? two(rest, rest) : by_col[g];
+    }
   }
   const bool upper = form < kUpdate && t.n * p.width / (2 * kHalf) != t.m;  // above the diagonal's tiles
   tmem_arrived(sums[0]);
@@ -362,7 +369,7 @@ __device__ __forceinline__ void finish(const Phase& p, uint16_t* dst, const Curs
       y[i] = mul2(two(sums[q][2 * i], sums[q][2 * i + 1]), k2);
       if (FORM == kGram) continue;
       y[i] = muladd2(two_halves(a[q][i]), by_col[i >> 1], y[i]);
-      y[i] = muladd2(two_halves(b[q][i]), form == kSym ? by[i & 1] : by_col[i >> 1], y[i]);
+      y[i] = muladd2(two_halves(b[q][i]), form == kSym ? by[i & 1] : by_lo[i >> 1], y[i]);
     }
     if (form == kLast) {
 #pragma unroll
@@ -472,8 +479,9 @@ __device__ __forceinline__ First first_of(const Phase& p, const Team& team) {
 // One thread loads the left operand, another the right one.  j: stages
 // filled so far.  `leader`: the pair's first CTA's rank in the cluster.
 template <int FORM>
-__device__ __forceinline__ bool load_phase(const Phase& p, const CUtensorMap* map, const Team& team, const First& first, bool left,
-                                           uint32_t smem, const Bars& bars, uint32_t leader, const Watch& watch, int& j) {
+__device__ __forceinline__ bool load_phase(const Phase& p, const CUtensorMap* map, const CUtensorMap* map_lo, const Team& team,
+                                           const First& first, bool left, uint32_t smem, const Bars& bars, uint32_t leader,
+                                           const Watch& watch, int& j) {
   const bool a_mn = form_of<FORM>(p) >= kUpdate;  // the left operand's major
   const uint32_t leaders = peer_addr(bars.full(0), leader);
   const uint32_t bytes = 2 * kOperand + p.width * (kStep * 2);
@@ -482,25 +490,28 @@ __device__ __forceinline__ bool load_phase(const Phase& p, const CUtensorMap* ma
   int s = j % kStages, parity = (j / kStages + 1) & 1;
   TileAt at = first.at;
   bool more = first.more;
-  for (int i = 1; more; more = work_at<FORM>(p, team, i++, at)) {
+  for (int next = 1; more; more = work_at<FORM>(p, team, next++, at)) {
     const int row = (at.m * 2 + team.rank) * kHalf, col = at.n * p.width + (int)team.rank * (p.width / 2);
     int z = at.z, from = 0;
     if (FORM == kGram) {
       z = p.segments.of(at.z);
-      from = (at.z - z * p.segments.d) * steps * kStep;
+      from = (at.z - z * p.segments.d) * p.term * kStep;
     }
-    for (int k = 0; k < steps; ++k, ++j) {
+    // X's lo before its hi: a sum loses of its own size with every product that is added
+    const CUtensorMap* now = steps > p.term ? map_lo : map;
+    for (int i = 0, k = 0; i < steps; ++i, ++j) {
       if (j >= kStages && !bar_wait(bars.empty(s), parity, watch)) return false;
       if (expects) bar_expect(bars.full(s), bytes);
       const uint32_t bar = leaders + 8u * s;
       const uint32_t a = smem + s * kStage, b = a + kOperand;
       if (!left)
-        load_box3<true>(b, map, from + k * kStep, col, z, bar);
+        load_box3<true>(b, now, from + k * kStep, col, z, bar);
       else if (a_mn)
-        load_box4(a, map, 0, k * kStep, row / 64, z, bar);
+        load_box4(a, now, 0, k * kStep, row / 64, z, bar);
       else
-        load_box3<true>(a, map, from + k * kStep, row, z, bar);
+        load_box3<true>(a, now, from + k * kStep, row, z, bar);
       if (++s == kStages) s = 0, parity ^= 1;
+      if (++k == p.term) k = 0, now = map;
     }
   }
   return true;
@@ -616,6 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Watch watch{&stop, p.limits.err, p.limits.limit_ns};
   const bool late = p.limits.late_ns && warp == 4;  // test: this warp waits for sums where nothing arrives
   if (threadIdx.x == 0) prefetch_map(&p.left), prefetch_map(&p.right);
+  if (threadIdx.x == 0 && p.phase.term < p.phase.steps) prefetch_map(&p.left_lo);
   const uint32_t tmem = set_up(bars, &stop, &tmem_at, warp);
   after_previous();
 
@@ -625,7 +637,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 0 || warp == 3) {
     if (elected()) {
       const bool left = warp == 0;
-      const bool go = load_phase<FORM>(p.phase, left ? &p.left : &p.right, team, first_of(p.phase, team), left, smem, bars, 0, watch, j);
+      const bool go = load_phase<FORM>(p.phase, left ? &p.left : &p.right, left ? &p.left_lo : &p.right, team,
+                                       first_of(p.phase, team), left, smem, bars, 0, watch, j);
       load_end(go, team, bars, watch, j);
     }
   } else if (warp == 1 && team.rank == 0) {
@@ -674,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   if (threadIdx.x == 0) ended_at = INT32_MAX;
   fetch(0, threadIdx.x, kThreads);
-  if (threadIdx.x < kMaps) prefetch_map(&p.maps[threadIdx.x]);
+  if (threadIdx.x < p.used) prefetch_map(&p.maps[threadIdx.x]);
   const uint32_t tmem = set_up(bars, &stop, &tmem_at, warp);
   after_previous();
 
@@ -690,8 +703,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0 || warp == 3) {
       if (elected()) {
         const bool left = warp == 0;
-        const CUtensorMap* map = &p.maps[left ? f.left : f.right];
-        go = load_phase<kAny>(f, map, team, first, left, smem, bars, leader, watch, j);
+        go = load_phase<kAny>(f, &p.maps[left ? f.left : f.right], &p.maps[left ? f.left_lo : f.right], team, first, left, smem,
+                              bars, leader, watch, j);
         if (!go || n == phases - 1)
           load_end(go, team, bars, watch, j);
         else
@@ -748,7 +761,8 @@ bool map_of(CUtensorMap* map, int which, const OrthoPlan& p, const Widths& w) {
   if (which < kRightX) return make_slab_stack_map(map, p.x[which - kWideX][0], p.m, p.count, p.ld_x, kStep, kHalf / 64);
   if (which < kRightT) return k(p.x[which - kRightX][0], p.n, p.ld_x, w.gram / 2);
   if (which < kUpdateT) return k(p.t[which - kRightT], p.m, p.ld_a, w.sym / 2);
-  return k(p.t[which - kUpdateT], p.m, p.ld_a, w.update / 2);
+  if (which < kWideLo) return k(p.t[which - kUpdateT], p.m, p.ld_a, w.update / 2);
+  return make_slab_stack_map(map, p.x[which - kWideLo][1], p.m, p.count, p.ld_x, kStep, kHalf / 64);
 }
 
 Limits limits_of(const TcLaunch& l) { return Limits{l.err, TIDE_BULK_TIMEOUT_NS, l.stall_ns, l.late_ns}; }
@@ -771,6 +785,10 @@ Phase phase_of(const OrthoPlan& p, const OrthoProduct& q, const Widths& w, int64
   const bool parted = q.form == kGram && p.segments > 1;
   k.steps = (int)ceil_div(parted ? kOrthoSegment : q.form == kGram ? p.n : p.m, kStep);
   k.segments = Divisor(parted ? p.segments : 1);
+  k.term = k.steps;
+  if (update) k.steps *= p.x_terms;
+  k.left_lo = update && p.x_terms > 1 ? kWideLo + q.turn : k.left;
+  k.rest = q.rest;
   k.planes = q.form == kGram ? 0 : q.form == kSym && q.left == q.right ? 1 : 2;
   k.in[0] = update ? p.x[q.turn][0] : p.t[q.left], k.in[1] = update ? p.x[q.turn][1] : p.t[q.right];
   k.out[0] = update ? p.x[q.turn ^ 1][0] : parted ? p.part_t : p.t[q.out], k.out[1] = p.x[q.turn ^ 1][1];
@@ -796,6 +814,7 @@ cudaError_t launch_product(const OrthoPlan& p, const OrthoProduct& q, const Widt
   k.phase = phase_of(p, q, w, a.ld_dst);
   k.limits = limits_of(l);
   if (!map_of(&k.left, k.phase.left, p, w) || !map_of(&k.right, k.phase.right, p, w)) return cudaErrorInvalidValue;
+  if (k.phase.term < k.phase.steps && !map_of(&k.left_lo, k.phase.left_lo, p, w)) return cudaErrorInvalidValue;
   // as many matrices (or segments) as a launch counts tiles, and the last form's table holds
   const int64_t each = tiles_of(k.phase);
   int64_t most = INT32_MAX / 2 / each;
@@ -828,7 +847,8 @@ cudaError_t launch_chain(const OrthoPlan& p, const OrthoProduct* q, int products
     k.phase[i] = phase_of(p, q[i], w, a.ld_dst);
     k.phase[i].tiles = (int)tiles_of(k.phase[i]);
   }
-  for (int i = 0; i < kMaps; ++i)
+  k.used = p.x_terms > 1 ? kMaps : kWideLo;
+  for (int i = 0; i < k.used; ++i)
     if (!map_of(&k.maps[i], i, p, w)) return cudaErrorInvalidValue;
   for (k.first = 0; k.first < p.count; k.first += kOrthoTable) {
     const int64_t some = p.count - k.first < kOrthoTable ? p.count - k.first : kOrthoTable;
@@ -873,7 +893,7 @@ Way way_of(const OrthoPlan& p, const OrthoProduct* q, int products, const TcDevi
       int* const at[3] = {&w->gram, &w->sym, &w->update};
       for (int f = 0; f < 3; ++f) {
         const int64_t tiles = matrices * (f < 2 ? triangle(p.m, width) : down * ceil_div(p.m, width)) * (f == 0 ? p.segments : 1);
-        const double t = product_time(tiles, pairs, f == 0 ? long_steps : short_steps, width) +
+        const double t = product_time(tiles, pairs, f == 0 ? long_steps : f == 1 ? short_steps : short_steps * p.x_terms, width) +
                          (chain ? kMeet : 2 * tiles > pairs ? kLaunchFull : kLaunch);
         if (width == 64 || t <= least[f]) least[f] = t, *at[f] = width;
       }

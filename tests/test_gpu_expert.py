@@ -480,6 +480,25 @@ def test_orthogonalize_short_sides_of_many(compute, count, rows, cols):
     assert all(torch.equal(a, b) for a, b in zip(own, got))
 
 
+@pytest.mark.parametrize("rows,cols", [(17, 40), (17, 17), (33, 2500), (32, 32), (64, 64), (64, 200), (200, 65), (65, 66), (128, 150), (128, 1000), (300, 256),
+                                       (256, 704), (383, 1000), (384, 1024), (512, 1024), (640, 960), (1100, 700), (768, 2048), (1024, 1536)])
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+def test_orthogonalize_leaves_what_is_documented(compute, rows, cols, kind):
+    """2^-9 of the result's norm, whatever the spectrum, a quarter more where steps
+    share a pass over X.  By the 64-bit result alone."""
+    m = min(rows, cols)
+    limit = 2.0 ** -9 * (1.25 if m >= 384 and 2 * max(rows, cols) >= 3 * m else 1)
+    grads = spectra(gen(rows + 3 * cols), rows, cols, kind)
+    worst = []
+    for got, grad in zip(orthogonalized(compute, grads, kind), grads):
+        want = ref.orthogonalize(grad)
+        size, own = float(want.norm()), float((want.bfloat16().double() - want).norm())
+        # the result's rounding comes on top, independent of it where there are many elements
+        most = math.hypot(own, limit * size) if want.numel() >= 1024 else own + limit * size
+        worst.append(float((got.double() - want).norm()) / most)
+    assert max(worst) <= 1, worst
+
+
 def test_orthogonalize_structures(compute):
     """One large element, equal rows, one direction, an orthogonal matrix, columns of very different sizes."""
     g = gen(5)
