@@ -188,9 +188,11 @@ __global__ void __launch_bounds__(kThreads) first_kernel(OrthoPlan p, Sources s,
 // the tensor cores to matter.  X is kept in fp32, a CTA has a span of its columns: it
 // adds up A from all spans' parts (in 64 bits, in order), makes C, takes its
 // columns to C X, and leaves its part of the next A.  So a step is one launch, bound
-// by what a launch and the parts' way take: one 8 x 4096 37 us (92 on the tensor
-// cores, by pairs of steps), 64 of them 131 (163), 1000 of 16 x 64 293 (464).
+// by what a launch and the parts' way take: one 8 x 4096 46 us (92 on the tensor
+// cores, by pairs of steps), 64 of them 148 (163), 1000 of 16 x 64 298 (464).
 constexpr int kShortTile = 64;  // columns at a time
+// Of those a CTA, at least (one: 37 us and 243 for 64 of 8 x 4096, four: 61 and 131).
+constexpr int kShortSpan = 2;
 
 struct ShortStep {
   bool from_source, apply, last;  // no `apply`: A's first parts
@@ -355,11 +357,12 @@ OrthoPlan plan_of(int64_t count, int64_t rows, int64_t cols, char* base, int64_t
   p.norms = (double*)take(count * p.parts * 8);
   if (p.m <= kShortSide) {
     // as many spans as the device has CTAs at a time, or, as each reads all spans'
-    // parts, as those stay short
+    // parts, as those stay short; by the sizes alone, so that a matrix's sums are the
+    // same among any number of others
     const int64_t tiles = ceil_div(p.n, kShortTile), entries = p.m * (p.m + 1) / 2;
-    int64_t most = 20000 / entries < kMaxParts ? 20000 / entries : kMaxParts;
-    if (most > room) most = room;
+    const int64_t most = 20000 / entries < kMaxParts ? 20000 / entries : kMaxParts;
     p.span = (int)ceil_div(tiles, most);
+    if (p.span < kShortSpan) p.span = kShortSpan;
     p.spans = (int)ceil_div(tiles, p.span);
     p.short_x = (float*)take(count * p.m * p.ld_x * 4);
     for (auto& turn : p.short_a) turn = (double*)take(count * p.spans * entries * 8);
