@@ -156,29 +156,39 @@ def _addr(x) -> int:
     return int(x.data_ptr())
 
 
-_KINDS: dict = {}  # names of the element types seen, by their dtype
+class _Kinds(dict):
+    """Whether a dtype is one of the named kinds of elements, by dtype (each is
+    looked at once: a call has a dozen arrays and takes a few microseconds)."""
+
+    def __init__(self, *names):
+        self.names = names
+
+    def __missing__(self, dtype):
+        ok = self[dtype] = dtype is None or _kind(dtype) in self.names
+        return ok
 
 
 def _kind(dtype) -> str:
     """'float32' of torch.float32."""
-    name = _KINDS.get(dtype)
-    if name is None:
-        name = _KINDS[dtype] = str(dtype).rpartition(".")[2]
-    return name
+    return str(dtype).rpartition(".")[2]
 
 
-_BF16 = ("bfloat16", "uint16", "int16")  # bf16, or its bits
-_FP32 = ("float32",)
-_I32 = ("int32", "uint32")
+_BF16 = _Kinds("bfloat16", "uint16", "int16")  # bf16, or its bits
+_FP32 = _Kinds("float32")
+_I32 = _Kinds("int32", "uint32")
 
 
 def _typed(x, kinds, what) -> int:
     """The address of x, which is one of `kinds` if it says what it is: an
     array's elements are read by the operator's type, whatever its own are."""
+    if x is None:
+        return 0
     dtype = getattr(x, "dtype", None)
-    if dtype is not None and _kind(dtype) not in kinds:
-        raise TypeError(f"{what}: {_kind(dtype)} elements, {kinds[0]} wanted")
-    return _addr(x)
+    if dtype is None:
+        return _addr(x)
+    if not kinds[dtype]:
+        raise TypeError(f"{what}: {_kind(dtype)} elements, {kinds.names[0]} wanted")
+    return x.data_ptr()
 
 
 def _stream(s) -> int:
@@ -520,23 +530,20 @@ def _named(names, v, what) -> int:
 
 
 _TYPES = {"bf16": TIDE_BF16, "fp32": TIDE_FP32}
-_TYPE_KINDS = {TIDE_BF16: _BF16, TIDE_FP32: _FP32}
 _SCORES = {"softmax": TIDE_SCORE_SOFTMAX, "sigmoid": TIDE_SCORE_SIGMOID}
 
 
-def _type(given, dtypes, what) -> int:
-    """The element type that is given, which arrays that know theirs agree with;
-    theirs where none is given, and fp32 of addresses."""
-    code = None if given is None else _named(_TYPES, given, f"{what}' type")
-    for dtype in dtypes:
-        if dtype is None:
-            continue
-        own = next((c for c, kinds in _TYPE_KINDS.items() if _kind(dtype) in kinds), None)
-        if code is None:
-            code = own
-        if own is None or own != code:
-            raise TypeError(f"{what}: {_kind(dtype)} elements, {'bf16 or fp32' if code is None else 'bf16' if code == TIDE_BF16 else 'fp32'} wanted")
-    return TIDE_FP32 if code is None else code
+def _type(given, dtype, what) -> int:
+    """The element type that is given, which an array that knows its own agrees
+    with; its own where none is given, and fp32 of an address (no dtype)."""
+    if given is None:
+        code = TIDE_BF16 if dtype is not None and _BF16[dtype] else TIDE_FP32
+    else:
+        code = _named(_TYPES, given, f"{what}' type")
+    if dtype is not None and not (_BF16 if code == TIDE_BF16 else _FP32)[dtype]:
+        raise TypeError(f"{what}: {_kind(dtype)} elements, "
+                        + ("bf16 or fp32" if given is None else "bf16" if code == TIDE_BF16 else "fp32") + " wanted")
+    return code
 
 
 def _router(r):
@@ -545,7 +552,7 @@ def _router(r):
 
 def tide_route(compute, tokens, router, type, logits, ld_logits, bias, ids, weights, stream=None) -> None:
     """ids and weights [tokens, topk] from logits [tokens, experts]; type: theirs, or None; see include/tide.h."""
-    _check(_lib.tide_route(compute, tokens, _router(router), _type(type, (getattr(logits, "dtype", None),), "logits"),
+    _check(_lib.tide_route(compute, tokens, _router(router), _type(type, getattr(logits, "dtype", None), "logits"),
                            _addr(logits), ld_logits, _typed(bias, _FP32, "bias"), _typed(ids, _I32, "ids"),
                            _typed(weights, _FP32, "weights"), _stream(stream)), "tide_route")
 
@@ -553,10 +560,11 @@ def tide_route(compute, tokens, router, type, logits, ld_logits, bias, ids, weig
 def tide_route_backward(compute, tokens, router, type, logits, ld_logits, ids, dweights, dlogits, ld_dlogits,
                         stream=None) -> None:
     """dlogits [tokens, experts] from dweights [tokens, topk]."""
-    dtypes = getattr(logits, "dtype", None), getattr(dlogits, "dtype", None)
-    _check(_lib.tide_route_backward(compute, tokens, _router(router), _type(type, dtypes, "logits"), _addr(logits),
-                                    ld_logits, _typed(ids, _I32, "ids"), _typed(dweights, _FP32, "dweights"),
-                                    _addr(dlogits), ld_dlogits, _stream(stream)), "tide_route_backward")
+    code = _type(type, getattr(logits, "dtype", None), "logits")
+    _check(_lib.tide_route_backward(compute, tokens, _router(router), code, _addr(logits), ld_logits,
+                                    _typed(ids, _I32, "ids"), _typed(dweights, _FP32, "dweights"),
+                                    _typed(dlogits, _BF16 if code == TIDE_BF16 else _FP32, "dlogits"), ld_dlogits,
+                                    _stream(stream)), "tide_route_backward")
 
 
 def expert_slots_workspace_bytes(tokens: int, topk: int, experts: int) -> int:
@@ -608,10 +616,12 @@ def tide_orthogonalize(compute, rows, cols, type, src, ld_src, dst, ld_dst, step
     s, d = _table(src), _table(dst)
     if s.n != d.n:
         raise ValueError(f"{s.n} sources, {d.n} destinations")
-    code = _type(type, s.dtypes, "gradients")
-    for dtype in d.dtypes:
-        if dtype is not None and _kind(dtype) not in _BF16:
-            raise TypeError(f"dst: {_kind(dtype)} elements, bfloat16 wanted")
+    known = s.dtypes - {None}
+    code = _type(type, next(iter(known), None), "gradients")
+    for kinds, dtypes, what in ((_BF16 if code == TIDE_BF16 else _FP32, known, "gradients"), (_BF16, d.dtypes, "dst")):
+        for dtype in dtypes:
+            if not kinds[dtype]:
+                raise TypeError(f"{what}: {_kind(dtype)} elements, {kinds.names[0]} wanted")
     c = None
     if coefficients is not None:
         c = np.ascontiguousarray(coefficients, dtype=np.float32).reshape(-1)
