@@ -1,7 +1,8 @@
 // Tokens' rows to their experts and back: one pass over the rows, bound by
 // HBM.  A thread takes 16 bytes of a token's row and the same of each of its
 // topk rows.  8191 tokens of 2048 there, 8 choices each: 48 us (6.3 TB/s); 4096
-// of them back 25 (6.0), backward 51 (5.6).  Rows that do not start on 16 bytes
+// of them back 25 (6.0), backward 51 (5.6); with 10 choices, which take two turns
+// of eight, 37, 38 and 73 (5.0 TB/s).  Rows that do not start on 16 bytes
 // take windows of as many, or single elements: 2000 of 2049 there 22 us, back 27,
 // backward 52.
 #include "compute_device.cuh"

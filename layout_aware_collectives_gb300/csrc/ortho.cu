@@ -430,8 +430,8 @@ bool bounds_of(int steps, const float* k, Bounds* out) {
 // to a^2 on its way to the second step's, which a moderate a only allows; it
 // leaves less the more rows there are (ortho.cuh), and below 384 more than a
 // quarter above 2^-9 of the result.  That costs 27 of 3131 x 257 482 us instead of
-// 385, 64 of 256 x 704 239 instead of 217, 128 x 2048 94 instead of 84; 100 of 128 x 512
-// take 165 instead of 171.
+// 385, 3457 x 63 121 instead of 100, 128 x 2048 94 instead of 84; 64 of 256 x 704 take
+// 205 to 240 us instead of 190 to 215, 100 of 128 x 512 165 instead of 171.
 constexpr int kPairedSide = 384;
 bool paired(const OrthoPlan& p, const OrthoArgs& a, int i) {
   const float k = a.coefficients[3 * i];

@@ -10,8 +10,8 @@
 // Update's and last's tiles are of X turned, X^T L (L is symmetric): the long
 // side lies along a tile's 256 rows, and the short one along its columns, of
 // which a tile may have 64.  With X as it is, a matrix of 33 rows left seven of
-// eight warps without results (25 of 3582 x 33: 204 us, 153 turned; level where
-// both sides are long).
+// eight warps without results (25 of 3582 x 33, in pairs of steps: 204 us, 153 turned;
+// level where both sides are long).
 //
 // As in the gated block, a pair of CTAs works on one tile of 256 rows and 256
 // columns (or 128 or 64, where there are few tiles): each loads 128 rows of the
@@ -869,11 +869,11 @@ struct Way {
 // results' way out, whichever is longer, as one hides behind the other but for the
 // last; and what a product costs besides, in a chain or alone, where half of the
 // device's SMs is free for the next one's CTAs to set up or is not.  Measured, in
-// us (all pairs; one, two, three, four, six, eight pairs a matrix): 704 x 256 88;
-// 158, 106, 95, 85, 75, 75.  128 x 2048 96; 163, 113, 103, 94, 92, 83.  64 of 256 x
-// 704 218; 189, 235, 300, 430, 595, 731.  16 of 300 x 300 130; 232, 140, 114, 196,
-// 151, 220.  100 of 128 x 512 171; 188, 211, 334, 433, 781, 897.  512 x 768 107; 375,
-// 248, 180, 175, 119, 119.
+// us (all pairs; one, two, three, four, six, eight pairs a matrix): 704 x 256 83;
+// 174, 116, 97, 92, 77, 76.  128 x 2048 97; 218, 144, 128, 111, 110, 94.  64 of 256 x
+// 704 229; 205, 255, 306, 456, 595, 726.  16 of 300 x 300 127; 224, 137, 111, 187,
+// 150, 218.  100 of 128 x 512 165; 190, 208, 329, 406, 732, 840.  512 x 768 109; 377,
+// 251, 180, 175, 122, 122.
 constexpr double kMeet = 12, kLaunch = 16, kLaunchFull = 18;
 double way_out(int width) { return 4.4 + width / 22.0; }
 double product_time(int64_t tiles, int64_t pairs, int steps, int width) {

@@ -3,8 +3,8 @@
 // A warp takes a token: each lane holds a run of neighbouring experts' logits
 // in registers, so nothing is read twice and, as the lowest lane holds the
 // lowest indices, equals go to the lowest index by going to the lowest lane.
-// Bound by instructions, some 1,300 a token of 256 experts in groups (8192 of
-// them 17 us, of 128 experts without 7, backward 5), and by the few tokens
+// Bound by instructions, some 1,400 a token of 256 experts in groups (8192 of
+// them 16 to 18 us, of 128 experts without 7, backward 5), and by the few tokens
 // whose borders take 64 bits (33 us with all of a token's scores in them).
 #include "compute_device.cuh"
 

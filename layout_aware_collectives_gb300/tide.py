@@ -183,12 +183,12 @@ def _typed(x, kinds, what) -> int:
     array's elements are read by the operator's type, whatever its own are."""
     if x is None:
         return 0
-    dtype = getattr(x, "dtype", None)
-    if dtype is None:
+    try:
+        if kinds[x.dtype]:
+            return x.data_ptr()
+    except AttributeError:  # an address, or something that has one
         return _addr(x)
-    if not kinds[dtype]:
-        raise TypeError(f"{what}: {_kind(dtype)} elements, {kinds.names[0]} wanted")
-    return x.data_ptr()
+    raise TypeError(f"{what}: {_kind(x.dtype)} elements, {kinds.names[0]} wanted")
 
 
 def _stream(s) -> int:
@@ -539,10 +539,10 @@ def _type(given, dtype, what) -> int:
     if given is None:
         code = TIDE_BF16 if dtype is not None and _BF16[dtype] else TIDE_FP32
     else:
-        code = _named(_TYPES, given, f"{what}' type")
-    if dtype is not None and not (_BF16 if code == TIDE_BF16 else _FP32)[dtype]:
+        code = _named(_TYPES, given, f"{what}' type") if given not in _TYPES else _TYPES[given]
+    if not (_FP32 if code else _BF16)[dtype]:
         raise TypeError(f"{what}: {_kind(dtype)} elements, "
-                        + ("bf16 or fp32" if given is None else "bf16" if code == TIDE_BF16 else "fp32") + " wanted")
+                        + ("bf16 or fp32" if given is None else "fp32" if code else "bf16") + " wanted")
     return code
 
 
