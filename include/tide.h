@@ -768,11 +768,13 @@ TIDE_API tide_status_t tide_orthogonalize_workspace(int64_t count, int64_t rows,
  * Matrices of up to 16 rows or columns take 32-bit arithmetic throughout.  Of
  * others X is kept as two fp16 terms, A and the matrices made of it as one beside
  * their diagonals in fp32; products take the first terms, and where that is
- * less work two steps share a pass over X (384 rows and columns or more, one of
- * them half as many again).  With the default coefficients what all this leaves is
- * below 2^-9 of the result's norm, about what its rounding to bf16 leaves, and at
- * most a quarter more where steps share a pass, whatever the singular values;
- * other coefficients leave more as their products of a's are larger.
+ * much less work two steps share a pass over X (384 rows and columns or more,
+ * two and a half times as many one way as the other).  With the default
+ * coefficients what all this leaves is as a rule below 2^-9 of the result's
+ * norm, about what its rounding to bf16 leaves (a quarter more where steps share
+ * a pass), and at most 2^-7, whatever the singular values; where a few elements
+ * make up a matrix (a permutation), so that no rounding averages out, at most
+ * 2^-5.  Other coefficients leave more as their products of a's are larger.
  * Sums are fp32.  What is below 2^-37 of the largest norm that X can
  * have in a step counts as nothing.
  */

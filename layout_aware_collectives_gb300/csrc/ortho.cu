@@ -428,14 +428,17 @@ bool bounds_of(int steps, const float* k, Bounds* out) {
 // Whether step i and the next share a pass over X: 5 products of m^3 / 2
 // operations and 3 of m m n / 2 instead of 2 and 6.  An error of A grows by up
 // to a^2 on its way to the second step's, which a moderate a only allows; it
-// leaves less the more rows there are (ortho.cuh), and below 384 more than a
-// quarter above 2^-9 of the result.  That costs 27 of 3131 x 257 482 us instead of
-// 385, 3457 x 63 121 instead of 100, 128 x 2048 94 instead of 84; 64 of 256 x 704 take
-// 205 to 240 us instead of 190 to 215, 100 of 128 x 512 165 instead of 171.
+// leaves less the more rows there are (ortho.cuh).  So steps share a pass where it
+// pays: 14336 x 4096 takes 2.18 ms instead of 2.79 by single steps, four of 2048 x
+// 8192 1.26 instead of 1.66, 128 of 768 x 2048 2.56 instead of 2.99, eight of 600 x
+// 2400 247 us instead of 286; of two sides that are nearer to one another or shorter
+// they save less than 5% (64 of 1024 x 1536 1.85 ms and 1.91, 384 x 1024 99 us and
+// 104, 512 x 2048 122 and 117), but for thin ones (27 of 3131 x 257 385 us and 482,
+// 3457 x 63 100 and 121, 128 x 2048 84 and 94).
 constexpr int kPairedSide = 384;
 bool paired(const OrthoPlan& p, const OrthoArgs& a, int i) {
   const float k = a.coefficients[3 * i];
-  return i + 1 < a.steps && p.m >= kPairedSide && 2 * (int64_t)p.n >= 3 * (int64_t)p.m && k * k <= 16.0f;
+  return i + 1 < a.steps && p.m >= kPairedSide && 2 * (int64_t)p.n >= 5 * (int64_t)p.m && k * k <= 16.0f;
 }
 
 // How far steps from i on may stretch what is small.

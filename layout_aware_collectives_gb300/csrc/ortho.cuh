@@ -23,8 +23,9 @@
 // stretch things by more than 8, lo is multiplied by L(0): what that leaves, (L -
 // L(0)) lo, lies in directions with large singular values, which do not grow.  In
 // the last steps all are near 1, and lo is multiplied by D, which is nearer to L
-// on average.  Short sides of up to 64 have lo in the product itself, a second
-// term of its sums, which are a stage long.
+// on average, as it is in rows whose diagonal is below 3/4 of L(0): such a row lies
+// in directions that do not grow.  Short sides of up to 64 have lo in the product
+// itself, a second term of its sums, which are a stage long.
 //
 // What all this leaves, in 2^-9 of the result's norm (rounding it to bf16 leaves
 // 0.85 of that), the largest of noise, noise of 1e-1 to 1e-5 over rank one, spectra
@@ -32,10 +33,13 @@
 //   17 x 40  33 x 2500  64 x 200  128 x 1000  256 x 704  512 x 1024, steps apart
 //   0.6      0.4        0.4       0.4         0.4        0.35
 //   (7.9     5.0        2.6       2.1         1.2        1.0, in pairs, lo by D)
-//   384 x 1024  512 x 1024  768 x 2048  1024 x 1536, in pairs
-//   1.2         1.1         0.95        0.85
+//   384 x 1024  768 x 2048, in pairs
+//   1.1         0.95
 // Pairs leave more, as A's rounding passes through C on both sides, a a of it; the
-// more rows, the less.
+// more rows, the less.  Of 200,000 matrices made to be hard, two or three levels of
+// singular values left up to 2.1 (in pairs 3.4).  Where a few elements make up a
+// matrix, roundings average out over nothing: permutations with up to 5.4, a dozen
+// elements with up to 7.8, A's diagonal itself being off by 2^-11.
 #pragma once
 
 #include <cuda_fp16.h>

@@ -74,7 +74,7 @@ struct Phase {
   const float *left_d, *right_d;  // diagonals
   float* out_d;
   float s2, s1, s0;
-  float rest;               // update, last: the factor of X's lo; 0: as of its hi
+  float rest;               // update, last: the factor of X's lo in rows whose diagonal is near it; 0: as of its hi
   float sum_scale, left_scale, right_scale, out_scale;  // factors of the sums, of `in`, of what is kept
   bool tall;
   int64_t ld_out;
@@ -343,12 +343,15 @@ __device__ __forceinline__ void finish(const Phase& p, uint16_t* dst, const Curs
   const float by_row = d.di * p.s2 * p.right_scale * p.out_scale;
   uint64_t by_col[4], by_lo[4];  // of the fragments' columns
   if (form != kGram) {
-    const float own = fmaf(d.dj, p.s2, p.s1) * p.left_scale * p.out_scale, rest = p.rest * p.left_scale * p.out_scale;
+    const float own = fmaf(d.dj, p.s2, p.s1) * p.left_scale * p.out_scale;
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
+    for (int g = 0; g < 4; ++g)
       by_col[g] = two(__shfl_sync(0xffffffffu, own, g * 8 + (lane & 3) * 2), __shfl_sync(0xffffffffu, own, g * 8 + (lane & 3) * 2 + 1));
-      by_lo[g] = p.rest != 0.0f ? two(rest, rest) : by_col[g];
-    }
+    // (a row whose diagonal is far from L(0) lies in directions that do not grow)
+    const float rest = p.rest * p.left_scale * p.out_scale, least = 0.75f * rest * rest;
+    const auto lo_by = [&](uint32_t v) { return __uint_as_float(v) * rest > least ? rest : __uint_as_float(v); };
+#pragma unroll
+    for (int g = 0; g < 4; ++g) by_lo[g] = two(lo_by((uint32_t)by_col[g]), lo_by((uint32_t)(by_col[g] >> 32)));
   }
   const bool upper = form < kUpdate && t.n * p.width / (2 * kHalf) != t.m;  // above the diagonal's tiles
   tmem_arrived(sums[0]);
